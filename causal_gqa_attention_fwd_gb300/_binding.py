@@ -24,7 +24,7 @@ STATUS = {
 }
 
 # name -> (restype, argtypes)
-_P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_P, _I, _F, _Z, _X = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_double
 SIGNATURES = {
     "attn_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
     "attn_fwd_rope_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
@@ -55,10 +55,22 @@ SIGNATURES = {
     "attn_decode_fwd": (_I, [_P] * 7 + [_Z, _I, _I, _I, _I, _I, _I, _F, _P, _I, _P]),
     "attn_decode_paged_fwd": (_I, [_P] * 8 + [_Z] + [_I] * 8 + [_F, _P, _I, _P]),
     "attn_decode_fp8_fwd": (_I, [_P, _P, _P, _F, _F] + [_P] * 4 + [_Z] + [_I] * 6 + [_F, _P, _I, _P]),
+    "attn_cache_plan": (_I, [_P] * 10 + [_I] * 5 + [_P]),
+    "attn_rope_table": (_I, [_P, _I, _I, _X, _X, _I, _X, _X, _X, _P]),
+    "attn_rope": (_I, [_P] * 5 + [_I, _P] + [_I] * 8 + [_P, _P]),
+    "attn_rope_bwd": (_I, [_P] * 5 + [_I, _P] + [_I] * 8 + [_P, _P]),
+    "attn_cache_append": (_I, [_P] * 5 + [_I] * 3 + [_P] * 2 + [_I] * 6 + [_P, _P]),
+    "attn_cache_append_fp8": (_I, [_P] * 5 + [_I] * 3 + [_P] * 2 + [_F] * 2 + [_I] * 6 + [_P, _P]),
+    "attn_cache_append_q4": (_I, [_P] * 5 + [_I] * 3 + [_P] * 4 + [_F] * 2 + [_I] * 6 + [_P, _P]),
+    "attn_cache_gather_q4": (_I, [_P] * 5 + [_F] * 2 + [_P] * 2 + [_I] * 5 + [_P]),
+    "attn_decode_q4_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
+    "attn_decode_q4_fwd": (_I, [_P] * 5 + [_F] * 2 + [_P] * 4 + [_Z] + [_I] * 6 + [_F, _P, _I, _P]),
+    "attn_decode_paged_q4_fwd": (_I, [_P] * 5 + [_F] * 2 + [_P] * 5 + [_Z] + [_I] * 8 + [_F, _P, _I, _P]),
     "attn_decode_paged_fp8_fwd": (_I, [_P, _P, _P, _F, _F] + [_P] * 5 + [_Z] + [_I] * 8 + [_F, _P, _I, _P]),
 }
 
-PROFILE_KINDS = {"attn_fwd": 0, "bwd_pre": 1, "bwd_dkdv": 2, "decode": 4, "decode_merge": 5, "bwd_dq": 6}
+PROFILE_KINDS = {"attn_fwd": 0, "bwd_pre": 1, "bwd_dkdv": 2, "decode": 4, "decode_merge": 5, "bwd_dq": 6,
+                 "cache_plan": 7, "rope": 8, "rope_table": 9, "cache_append": 10, "cache_gather": 11}
 
 _lib = None
 

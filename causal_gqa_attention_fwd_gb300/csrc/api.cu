@@ -7,6 +7,7 @@
 
 #include <vector>
 
+#include "api_util.h"
 #include "gqa_attn.h"
 #include "kernels.h"
 #include "rope.h"
@@ -264,6 +265,15 @@ __global__ void selftest_wait_timeout_kernel(int* status, uint64_t limit_ns) {
 }
 
 }  // namespace
+
+// ------------------------------------------- shared with the other entry points
+namespace gqa {
+int* api_status_word() { return status_word(); }
+int* api_check_line() { return check_line_word(); }
+int api_sm_count() { return sm_count(); }
+attn_status api_check_arch() { return check_arch(); }
+attn_status api_check_heads(int Hq, int Hkv, int D) { return check_heads(Hq, Hkv, D); }
+}  // namespace gqa
 
 // ------------------------------------------------------- kernel timing
 namespace gqa {

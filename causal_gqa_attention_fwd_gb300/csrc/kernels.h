@@ -144,7 +144,12 @@ enum ProfKind {
   kProfDecode = 4,
   kProfDecodeMerge = 5,
   kProfBwdDq = 6,
-  kProfKinds = 7
+  kProfPlan = 7,
+  kProfRope = 8,
+  kProfRopeTable = 9,
+  kProfAppend = 10,
+  kProfGather = 11,
+  kProfKinds = 12
 };
 // Launch with programmatic stream serialization (see griddep_wait in
 // sm103.cuh): the kernel's CTAs may be scheduled, and run their set-up, while

@@ -20,7 +20,7 @@
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers, 16-byte aligned, densely
- *     packed (no strides).  bf16 = IEEE bfloat16 stored as uint16.
+ *     packed (no strides, but for the token views below).  bf16 = IEEE bfloat16 stored as uint16.
  *   - Dense layout:  Q, O, dO, dQ  [B, Hq, T, D];  K, V, dK, dV  [B, Hkv, T, D];
  *                    LSE  [B, Hq, T] float32 (natural log).
  *   - Packed (varlen) layout, sequences s = 0..num_seqs-1 occupying token rows
@@ -307,6 +307,179 @@ GQA_ATTN_API attn_status attn_decode_paged_fp8_fwd(const void* q, const void* k8
                                                    int page_size, int num_pages, int max_pages, int D, float scale,
                                                    const float* rope_cos_sin, int rope_positions, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The KV cache of a serving step: where its tokens go (attn_cache_plan), rotary
+ * positions (attn_rope*), writing keys and values (attn_cache_append*), and
+ * attention over a cache held in 4 bits (attn_decode_q4_fwd and its paged
+ * form).  These belong to the paged KV-cache management of the RoseLLM README
+ * (section "Inference and serving") and the positions-aware RoPE and KV-cache
+ * decode of the microLLM-rocm README (section "Why this project exists").
+ *
+ * Cache slots.  A cache is [num_pages, Hkv, page_size, ...]: slot
+ * p * page_size + r is row r of page p, in every K/V head.  A contiguous
+ * cache [B, Hkv, S, ...] is the case num_pages = B, page_size = S, where
+ * position j of batch row b is slot b * S + j.
+ *
+ * Token views.  q, k and v here are [B, T, H, D] bf16 with strides of their
+ * own: element (b, t, h, d) lies at b*s_b + t*s_t + h*s_h + d (strides in
+ * elements, multiples of 8, none negative), so the views of one fused
+ * projection's output and both layouts above ([B,H,T,D] and [total,H,D] as
+ * B = 1, T = total) need no copy.  Strides are passed as HOST arrays of three
+ * (s_b, s_t, s_h) per tensor, read before the call returns.  Token (b, t) is
+ * number b*T + t of slots.  Outputs whose rows overlap give undefined values.
+ *
+ * Rotary positions.  rope_cos_sin is float32 [rope_positions, rotary_dim]
+ * (DEVICE, 16-byte aligned), row p holding the rotary_dim/2 cosines, then the
+ * sines.  The first rotary_dim features of each head are rotated (a multiple
+ * of 16, <= D), the others kept: pair i is features (i, i + rotary_dim/2), or
+ * with interleaved != 0 features (2i, 2i+1):
+ *   y_first = x_first c - x_second s,   y_second = x_second c + x_first s.
+ * positions: DEVICE int32.  A position outside the table is reported through
+ * the device status word (ATTN_ERR_SEQLENS). */
+
+/* Block table, slots and positions of a step's new tokens, from the request
+ * lengths, in one launch (graph-capturable: nothing depends on the lengths on
+ * the host).  Request b holds cache_lens[b] keys in the first
+ * ceil(cache_lens[b] / page_size) entries of block_table row b and adds
+ * new_lens[b] tokens.  It gets the pages it lacks from free_pages, in request
+ * order from index cursor[0] on (NULL: 0), and they are written into its
+ * block-table row (the only entries changed).  Written as well:
+ *   slots, positions  [total_tokens]  of the new tokens, packed in request
+ *                     order; entries past the last token are -1 and 0
+ *   cu_seqlens        [B + 1]  each request's first packed token
+ *   lens_out          [B]      cache_lens + new_lens
+ *   cursor_out        [1]      index of the first page still free
+ * (DEVICE int32; lens_out and cursor_out must not be the inputs' memory.)
+ * A request with a negative length, or whose new length exceeds
+ * max_pages * page_size, is refused: it gets no pages, its tokens (none if
+ * new_lens[b] < 0) get slot -1 and its length stays (ATTN_ERR_SEQLENS).  So
+ * are the first request whose tokens exceed total_tokens (ATTN_ERR_SEQLENS;
+ * cu_seqlens stops at total_tokens) or whose pages exceed free_pages
+ * (ATTN_ERR_PAGES) and every valid one after it.  A negative page in
+ * block_table or free_pages gives slot -1 (ATTN_ERR_PAGES).
+ * 0 <= B <= 8192; page_size >= 1; B * max_pages and max_pages * page_size
+ * below 2^31. */
+GQA_ATTN_API attn_status attn_cache_plan(const int* cache_lens, const int* new_lens, int* block_table,
+                                         const int* free_pages, const int* cursor, int* slots, int* positions,
+                                         int* cu_seqlens, int* lens_out, int* cursor_out, int B, int page_size,
+                                         int max_pages, int num_free, int total_tokens, void* stream);
+
+/* Rotary table of positions 0..n-1 (rope_cos_sin float32 [n, rotary_dim], as
+ * above), with frequencies theta_i = base^(-2i/rotary_dim) scaled for contexts
+ * longer than the trained one:
+ *   original_positions = 0: theta_i / factor (position interpolation; factor 1: none);
+ *   otherwise by parts: with t_i = original_positions * theta_i / (2 pi) turns
+ *   over the original context and g = clamp((t_i - low_turns) /
+ *   (high_turns - low_turns), 0, 1), theta_i g + (theta_i / factor) (1 - g).
+ * Cosines and sines are multiplied by mscale.  The angle of a position is
+ * taken in fixed point (64 bits of a turn), so that far positions lose
+ * nothing; entries are within 2^-22 |mscale| of the exact ones.  rotary_dim:
+ * a multiple of 16, at most 512.  base > 1, factor > 0, low_turns <
+ * high_turns, all finite. */
+GQA_ATTN_API attn_status attn_rope_table(float* rope_cos_sin, int n, int rotary_dim, double base, double factor,
+                                         int original_positions, double low_turns, double high_turns, double mscale,
+                                         void* stream);
+
+/* Rotates q [B,T,Hq,D] and k [B,T,Hkv,D] (k, k_out NULL with Hkv = 0: q alone)
+ * at positions[b * positions_stride + t] (positions_stride: T, or 0 for the
+ * same positions in every batch row), in f32, rounded once to bf16.
+ * strides: HOST, 12 entries: q, k, q_out, k_out, three each.  An output may be
+ * its input (same pointer and strides).  A row whose position is outside the
+ * table is written as zeros.  D: a multiple of 16, at most 512. */
+GQA_ATTN_API attn_status attn_rope(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                                   int positions_stride, const float* rope_cos_sin, int rope_positions, int B, int T,
+                                   int Hq, int Hkv, int D, int rotary_dim, int interleaved, const long long* strides,
+                                   void* stream);
+
+/* Backward of attn_rope: the gradients of its inputs from those of its outputs
+ * (the transposed rotation; with a table of mscale m, m^2 times the inverse's
+ * input).  Arguments as attn_rope. */
+GQA_ATTN_API attn_status attn_rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                       const int* positions, int positions_stride, const float* rope_cos_sin,
+                                       int rope_positions, int B, int T, int Hq, int Hkv, int D, int rotary_dim,
+                                       int interleaved, const long long* strides, void* stream);
+
+/* Writes k and v [B,T,Hkv,D] into the cache slots slots[b*T + t] (DEVICE
+ * int32).  Slot -1 writes nothing (padded tokens); any other slot outside
+ * [0, num_pages * page_size) is reported (ATTN_ERR_PAGES) and writes nothing.
+ * The slots of one call must differ from one another: a slot named twice
+ * holds a mixture of its tokens.  rope_cos_sin (NULL: none) rotates k in f32
+ * at positions[b*T + t] on the way; a token whose position is outside the
+ * table is reported and not written.  strides: HOST, 6 entries: k, v.
+ *   attn_cache_append      bf16 caches [num_pages, Hkv, page_size, D]
+ *   attn_cache_append_fp8  E4M3 caches: code = e4m3(x * (1 / scale)), nearest
+ *                          even, saturating at +-448 (infinities too), NaN
+ *                          kept; 1 / scale rounded to f32
+ *   attn_cache_append_q4   4-bit caches (below)
+ * D: 64 or 128. */
+GQA_ATTN_API attn_status attn_cache_append(const void* k, const void* v, const int* slots, const int* positions,
+                                           const float* rope_cos_sin, int rope_positions, int rotary_dim,
+                                           int interleaved, void* k_cache, void* v_cache, int B, int T, int Hkv,
+                                           int D, int page_size, int num_pages, const long long* strides,
+                                           void* stream);
+GQA_ATTN_API attn_status attn_cache_append_fp8(const void* k, const void* v, const int* slots, const int* positions,
+                                               const float* rope_cos_sin, int rope_positions, int rotary_dim,
+                                               int interleaved, void* k8, void* v8, float k_scale, float v_scale,
+                                               int B, int T, int Hkv, int D, int page_size, int num_pages,
+                                               const long long* strides, void* stream);
+
+/* The 4-bit cache format: E2M1 codes (sign, 2 exponent bits, 1 mantissa bit:
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6) with one E4M3 scale for 16 consecutive features
+ * and one f32 scale for the cache; 4.5 bits per element.
+ *   k4, v4        uint8 [num_pages, Hkv, page_size, D/2]: features 2i (low
+ *                 half) and 2i + 1 of a row in byte i
+ *   k4_sf, v4_sf  uint8 [num_pages, Hkv, page_size, D/16]: E4M3 codes
+ *   value = e2m1(code) * e4m3(sf) * k_scale (v_scale).
+ * Appending takes, in f32 and rounded as elementary operations are,
+ *   sf = e4m3(min(max_16 |x| * (1 / (6 scale)), 448)),
+ *   code = e2m1(x * (1 / (e4m3(sf) * scale))), nearest even, saturating at 6;
+ * a block with a NaN or an infinity stores the NaN scale and reads as NaN, one
+ * whose sf rounds to 0 stores zeros.  Scales: 1e-20 <= scale <= 1e20. */
+GQA_ATTN_API attn_status attn_cache_append_q4(const void* k, const void* v, const int* slots, const int* positions,
+                                              const float* rope_cos_sin, int rope_positions, int rotary_dim,
+                                              int interleaved, void* k4, void* k4_sf, void* v4, void* v4_sf,
+                                              float k_scale, float v_scale, int B, int T, int Hkv, int D,
+                                              int page_size, int num_pages, const long long* strides, void* stream);
+
+/* Reads cache slots back as values: k, v bf16 [tokens, Hkv, D] (dense), the
+ * 4-bit values above rounded to bf16 -- what a later prompt chunk or a shared
+ * prefix attends to through attn_fwd.  Slot -1 (and, reported as
+ * ATTN_ERR_PAGES, any other outside the cache) gives zeros. */
+GQA_ATTN_API attn_status attn_cache_gather_q4(const int* slots, const void* k4, const void* k4_sf, const void* v4,
+                                              const void* v4_sf, float k_scale, float v_scale, void* k, void* v,
+                                              int tokens, int Hkv, int D, int page_size, int num_pages, void* stream);
+
+/* Cached attention over 4-bit caches: the queries, mask, rotary table and
+ * outputs of attn_decode_fwd over k4, k4_sf, v4, v4_sf [B, Hkv, S, ...] as
+ * above.  Any 0 <= cache_lens[b] <= S is a valid length: a query at a
+ * negative position (cache_lens[b] < Tq) sees no key and gets O = 0, LSE =
+ * -infinity, so a batch slot without a request is a row of length 0.  A row
+ * outside that range is reported (ATTN_ERR_SEQLENS), its outputs unwritten.
+ * e2m1 * e4m3 is exact in f16; the query rows (after rotation, if any) are
+ * scaled by a power of two per row and carried in f16, value and remainder
+ * when rotated, so the scores' only roundings are the f32 accumulation's.  P
+ * is rounded to f16 for the P V product (f32 accumulation).
+ * workspace: attn_decode_q4_workspace_size() bytes, 256-byte aligned, no
+ * initialisation; calls in flight at once need one each.  Errors as
+ * attn_decode_fwd; the cache tensors must be 16-byte aligned. */
+GQA_ATTN_API size_t attn_decode_q4_workspace_size(int B, int Hq, int Hkv, int Tq, int S, int D);
+GQA_ATTN_API attn_status attn_decode_q4_fwd(const void* q, const void* k4, const void* k4_sf, const void* v4,
+                                            const void* v4_sf, float k_scale, float v_scale, const int* cache_lens,
+                                            void* o, float* lse, void* workspace, size_t workspace_bytes, int B,
+                                            int Hq, int Hkv, int Tq, int S, int D, float scale,
+                                            const float* rope_cos_sin, int rope_positions, void* stream);
+
+/* The same over paged 4-bit caches [num_pages, Hkv, page_size, ...] through a
+ * block table (both as attn_decode_paged_fwd; a table entry outside the pool
+ * is reported as ATTN_ERR_PAGES and its keys read as zeros). */
+GQA_ATTN_API attn_status attn_decode_paged_q4_fwd(const void* q, const void* k4_pages, const void* k4_sf_pages,
+                                                  const void* v4_pages, const void* v4_sf_pages, float k_scale,
+                                                  float v_scale, const int* block_table, const int* cache_lens,
+                                                  void* o, float* lse, void* workspace, size_t workspace_bytes, int B,
+                                                  int Hq, int Hkv, int Tq, int page_size, int num_pages, int max_pages,
+                                                  int D, float scale, const float* rope_cos_sin, int rope_positions,
+                                                  void* stream);
+
 /* Static description of a status code. */
 GQA_ATTN_API const char* attn_status_string(attn_status status);
 
@@ -356,9 +529,9 @@ GQA_ATTN_API attn_status attn_test_inject_timeout(int kernel, int limit_ms);
  * kernel launch is bracketed by a CUDA event pair recorded on the caller's
  * stream.  attn_profile_read synchronises those events and returns, for one
  * kernel kind (0 forward, 1 backward preprocess, 2 backward dK/dV kernel,
- * 3 unused, 4 decode partial, 5 decode split merge, 6 backward dQ kernel),
- * the
- * number of launches and their summed device
+ * 3 unused, 4 decode partial, 5 decode split merge, 6 backward dQ kernel,
+ * 7 cache plan, 8 rotary rows, 9 rotary table, 10 cache append, 11 cache
+ * gather), the number of launches and their summed device
  * time in milliseconds since the last attn_profile_reset.  At most 65536
  * launches are recorded between resets.  Off by default. */
 GQA_ATTN_API attn_status attn_profile_enable(int enable);
