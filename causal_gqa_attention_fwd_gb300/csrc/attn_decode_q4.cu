@@ -52,25 +52,26 @@ constexpr float kOff = 7.f;    // ... and P is scaled by 2^7, so P <= 2^15 and f
 
 template <int D, int NT>
 struct Q4Cfg {
-  static constexpr int kWarps = 8;
-  static constexpr int kStages = 4;
+  static constexpr int kWarps = NT == 2 ? 8 : D == 128 ? 12 : 16;
+  static constexpr int kStages = NT == 1 && D == 128 ? 3 : 4;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kMT = D / 16;                // 16-feature tiles of O^T
   static constexpr int kCodes = kTK * D / 2;        // bytes of a tile's K (or V) codes
   static constexpr int kSf = kTK * D / 16;          // bytes of its block scales
   static constexpr int kStage = 2 * kCodes + 2 * kSf;
   static constexpr int kRing = kStages * kStage;    // per warp
-  static constexpr int kRec = NT * (kMT * 4 + 4);   // f32 of a piece per lane: O^T fragment, maxima, sums
+  static constexpr int kRec = NT * (kMT * 4 + 4);   // f32 of a piece per lane: per 8 rows O^T's fragments, maxima, sums
   static constexpr int kSmem = kWarps * (kRing + kRec * 128);   // rings, then a piece per warp
   static_assert(kRec * 128 <= kRing, "a warp's last piece goes into its drained ring");
-  static_assert(kSmem <= 227 * 1024 - 2048, "shared memory");
+  static_assert(kSmem <= 227 * 1024 - 4096, "shared memory");
 };
 
 // A thread's part of a piece: O^T fragments and, for its two columns of each
 // 8-row tile, the maximum (log2 units, the same in all lanes of a column) and
-// its own keys' sum.
+// its own keys' sum.  Stored as f32 [register][lane].
 template <int D, int NT>
 struct Piece4 {
+  static constexpr int kPer = D / 16 * 4 + 4;   // registers per 8 rows
   float acc[NT][D / 16][4];
   float m[NT][2], l[NT][2];
 
@@ -85,44 +86,83 @@ struct Piece4 {
       l[n][0] = l[n][1] = 0.f;
     }
   }
-  // [register][lane] f32: coalesced in global memory, free of conflicts in shared memory
   __device__ __forceinline__ void store(float* p, int lane) const {
-    int r = 0;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      float* q = p + n * kPer * 32 + lane;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[32 * r++ + lane] = acc[n][i][j];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) p[32 * r++ + lane] = m[n][c];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) p[32 * r++ + lane] = l[n][c];
-    }
-  }
-  // combine with a stored piece of the same unit
-  __device__ __forceinline__ void add(const float* p, int lane) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float* q = p + n * (D / 16 * 4 + 4) * 32 + lane;
-      float a[2], b[2];
+        for (int j = 0; j < 4; ++j) q[32 * (4 * i + j)] = acc[n][i][j];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float m2 = q[(D / 16 * 4 + c) * 32], l2 = q[(D / 16 * 4 + 2 + c) * 32];
-        const float mn = fmaxf(m[n][c], m2);
-        a[c] = m[n][c] == -CUDART_INF_F ? 0.f : ex2_approx(m[n][c] - mn);
-        b[c] = m2 == -CUDART_INF_F ? 0.f : ex2_approx(m2 - mn);
-        // a NaN sum must survive a piece whose maximum is -infinity
-        l[n][c] = (m[n][c] == -CUDART_INF_F ? l[n][c] : l[n][c] * a[c]) + (m2 == -CUDART_INF_F ? l2 : l2 * b[c]);
-        if (m[n][c] == -CUDART_INF_F) a[c] = 1.f;
-        if (m2 == -CUDART_INF_F) b[c] = 1.f;
-        m[n][c] = mn;
+        q[32 * (D / 4 + c)] = m[n][c];
+        q[32 * (D / 4 + 2 + c)] = l[n][c];
+      }
+    }
+  }
+};
+
+// One 16-feature tile of 8 rows of a unit, combined from stored pieces:
+// at(i) is piece i's base, nullptr for none.
+template <int D>
+struct Combined {
+  float acc[4], m[2], l[2];
+  template <typename At>
+  __device__ __forceinline__ void from(At at, int first, int last, int n, int tile, int lane) {
+    constexpr int kPer = D / 16 * 4 + 4;
+    const int base = n * kPer * 32 + lane;
+    m[0] = m[1] = -CUDART_INF_F;
+#pragma unroll 8
+    for (int i = first; i <= last; ++i) {
+      const float* p = at(i);
+      if (!p) continue;
+      m[0] = fmaxf(m[0], p[base + 32 * (D / 4)]);
+      m[1] = fmaxf(m[1], p[base + 32 * (D / 4 + 1)]);
+    }
+    l[0] = l[1] = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+#pragma unroll 4
+    for (int i = first; i <= last; ++i) {
+      const float* p = at(i);
+      if (!p) continue;
+      float f[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float mp = p[base + 32 * (D / 4 + c)];
+        f[c] = mp == -CUDART_INF_F ? 1.f : ex2_approx(mp - m[c]);   // such a piece holds zeros (or NaN, kept)
+        l[c] = fmaf(p[base + 32 * (D / 4 + 2 + c)], f[c], l[c]);
       }
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[n][i][j] = acc[n][i][j] * a[j & 1] + q[(i * 4 + j) * 32] * b[j & 1];
+      for (int j = 0; j < 4; ++j) acc[j] = fmaf(p[base + 32 * (4 * tile + j)], f[j & 1], acc[j]);
     }
+  }
+};
+
+// Tiles of batch row b: a row without keys has one (all masked), a row with an
+// invalid length none.
+__device__ __forceinline__ int row_tiles(const DecodeQ4Args& a, int b, int& len) {
+  len = a.cache_lens[b];
+  return len < 0 || len > a.S ? 0 : len == 0 ? 1 : (len + kTK - 1) / kTK;
+}
+
+// The share of all C tiles (C < 2^31): warps 0..G-1 of the grid, warp w takes [wC/G, (w+1)C/G).
+__device__ __forceinline__ int share_begin(int w, int C, int G) { return (int)((long)w * C / G); }
+__device__ __forceinline__ int owner_of(int g, int C, int G) { return (int)((((long)g + 1) * G - 1) / C); }
+
+// A unit of the stream.
+struct Unit {
+  int Pu;          // stream index of its first tile
+  int nb;          // its tiles
+  int b, k;        // batch row, unit within it (hkv * nrb + row block)
+  int len;         // keys of the row
+  __device__ __forceinline__ void next(const DecodeQ4Args& a) {
+    Pu += nb;
+    if (++k < a.Hkv * a.nrb) return;
+    k = 0;
+    do {
+      if (++b >= a.B) return;     // past the last unit
+      nb = row_tiles(a, b, len);
+    } while (nb == 0);
   }
 };
 
@@ -135,42 +175,20 @@ __device__ __forceinline__ float* piece_at(uint8_t* smem, int s) {
                                         : smem + C::kWarps * C::kRing + (s >> 1) * C::kRec * 128);
 }
 
-// Tiles of batch row b: a row without keys has one (all masked), a row with an
-// invalid length none.
-__device__ __forceinline__ int row_tiles(const DecodeQ4Args& a, int b, int& len) {
-  len = a.cache_lens[b];
-  return len < 0 || len > a.S ? 0 : len == 0 ? 1 : (len + kTK - 1) / kTK;
-}
-
-// The share of all tiles: warps 0..G-1 of the grid, warp w takes [wC/G, (w+1)C/G).
-__device__ __forceinline__ int owner_of(long g, long C, int G) { return (int)(((g + 1) * G - 1) / C); }
-
-// A position in the stream.
-struct Walk {
-  long g;          // stream index of the tile
-  long Pu;         // stream index of its unit's first tile
-  int b, k;        // batch row, unit within it (hkv * nrb + row block)
-  int len, nb;     // keys of the row, tiles per unit
-  __device__ __forceinline__ int tile() const { return (int)(g - Pu); }
-  __device__ __forceinline__ void next(const DecodeQ4Args& a, long end) {
-    ++g;
-    if (g - Pu < nb || g >= end) return;
-    Pu += nb;
-    if (++k < a.Hkv * a.nrb) return;
-    k = 0;
-    do {
-      if (++b >= a.B) return;     // not reached before `end`
-      nb = row_tiles(a, b, len);
-    } while (nb == 0);
-  }
-};
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(ok ? N : 0) : "memory");
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -216,7 +234,7 @@ __device__ __forceinline__ int row_at(int k, int c) {
 // queries) the remainder; rows are scaled by a power of two so that their
 // largest element lies in [2^14, 2^15); fac undoes it and applies the softmax scale.
 template <int D, int NT, int PARTS>
-__device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Walk& w, int lane, uint32_t (*qf)[PARTS][D / 16][2],
+__device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& w, int lane, uint32_t (*qf)[PARTS][D / 16][2],
                                              float (*fac)[2]) {
   constexpr int F = D / 4;            // features of a thread
   const int g = lane >> 2, t = lane & 3;
@@ -278,43 +296,145 @@ __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Walk& 
   }
 }
 
-// O and LSE of a unit from its complete piece.
-template <int D, int NT>
-__device__ __forceinline__ void write_unit(const DecodeQ4Args& a, int b, int k, int len, Piece4<D, NT>& p, int lane) {
+// O and LSE of two rows (columns 2t, 2t+1 of 8-row tile n) from their sums and
+// a run of O^T's tiles: tile i holds features 2i, 2i+1 of the gD/8.. that a lane group has.
+template <int D, int TILES>
+__device__ __forceinline__ void write_rows(const DecodeQ4Args& a, int b, int k, int len, int rows_per, int n, int tile0,
+                                           const float (*acc)[4], const float* m, const float* lsum, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const int hkv = k / a.nrb, r0 = (k - hkv * a.nrb) * 8 * NT;
+  const int hkv = k / a.nrb, r0 = (k - hkv * a.nrb) * rows_per;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int c = 0; c < 2; ++c) {
+    float l = lsum[c];
+    l += __shfl_xor_sync(~0u, l, 4);
+    l += __shfl_xor_sync(~0u, l, 8);
+    l += __shfl_xor_sync(~0u, l, 16);
+    const int r = r0 + n * 8 + 2 * t + c;
+    if (r >= a.R) continue;
+    const long row = ((long)b * a.Hq + hkv * a.G) * a.Tq + r;
+    const bool empty = len - a.Tq + r % a.Tq < 0;      // the row sees no key
+    const float inv = a.v_scale / l;
+    if (!GQA_CHECK(row >= 0 && row < (long)a.B * a.Hq * a.Tq, a.status, a.dbg_line)) continue;
+    __nv_bfloat16* o = a.o + row * D + g * (D / 8) + 2 * tile0;
+    uint32_t w[TILES];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float l = p.l[n][c];
-      l += __shfl_xor_sync(~0u, l, 4);
-      l += __shfl_xor_sync(~0u, l, 8);
-      l += __shfl_xor_sync(~0u, l, 16);
-      const int r = r0 + n * 8 + 2 * t + c;
-      if (r >= a.R) continue;
-      const long row = ((long)b * a.Hq + hkv * a.G) * a.Tq + r;
-      const bool empty = len - a.Tq + r % a.Tq < 0;      // the row sees no key
-      const float inv = empty ? 0.f : a.v_scale / l;
-      if (!GQA_CHECK(row >= 0 && row < (long)a.B * a.Hq * a.Tq, a.status, a.dbg_line)) continue;
-      // features gD/8 ..: tile i holds features 2i, 2i+1 of them
-      __nv_bfloat16* o = a.o + row * D + g * (D / 8);
-      uint32_t w[D / 16];
+    for (int i = 0; i < TILES; ++i) w[i] = empty ? 0u : pack_bf16x2(acc[i][c] * inv, acc[i][2 + c] * inv);
+    if constexpr (TILES == 1) {
+      *reinterpret_cast<uint32_t*>(o) = w[0];
+    } else {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        w[i] = empty ? 0u : pack_bf16x2(p.acc[n][i][c] * inv, p.acc[n][i][2 + c] * inv);
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i)
+      for (int i = 0; i < TILES / 4; ++i)
         reinterpret_cast<uint4*>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      if (g == 0) a.lse[row] = empty ? -CUDART_INF_F : (p.m[n][c] - kOff + log2f(l)) * 0.69314718055994531f;
     }
+    if (g == 0 && tile0 == 0) a.lse[row] = empty ? -CUDART_INF_F : (m[c] - kOff + log2f(l)) * 0.69314718055994531f;
+  }
 }
 
-// Workspace: a header per CTA, then two pieces per CTA (kRec * 32 f32 each).
+// Workspace: a header per CTA, then two pieces per CTA (kRec * 32 f32 each):
+// 0 of the unit begun before the CTA's share, 1 of the one that goes on after it.
 struct Q4Head {
   int b, k, len;   // unit of the CTA's first piece
-  int first, last; // CTAs that hold pieces of it, -1: not cut before this CTA
+  int first, last; // CTAs that hold pieces of it, first = -1: not cut before this CTA
   int pad[3];
+};
+
+// Copies tiles of a share into a warp's ring.
+template <int D, int NT>
+struct Loader {
+  using C = Q4Cfg<D, NT>;
+  Unit u;
+  int left;            // tiles of the share not yet issued
+  int tiles;           // of the unit's tiles, those from the current one on
+  int keys;            // keys from the current tile on
+  int pidx, inpg;      // paged: block-table index and row in the page of the tile
+  int page[2];         // pages of its two 16-key halves
+  long base;           // contiguous: cache row of the tile
+
+  __device__ __forceinline__ void look_up(const DecodeQ4Args& a) {
+    const int* bt = a.block_table + (long)u.b * a.max_pages + pidx;
+    page[0] = keys > 0 ? __ldg(bt) : 0;
+    page[1] = a.page_size != 16 ? page[0] : keys > 16 ? __ldg(bt + 1) : 0;
+  }
+  __device__ __forceinline__ void enter(const DecodeQ4Args& a, int tile) {   // the unit's tile `tile`
+    const int j = tile * kTK;
+    tiles = u.nb - tile;
+    keys = u.len - j;
+    if (a.block_table) {
+      pidx = j / a.page_size;
+      inpg = j - pidx * a.page_size;
+      look_up(a);
+    } else {
+      base = ((long)u.b * a.Hkv + u.k / a.nrb) * a.S + j;
+    }
+  }
+  // lane_dst: the lane's byte in a stage's codes; lane = its 16-byte chunk of 512 bytes
+  __device__ __forceinline__ void issue(const DecodeQ4Args& a, uint32_t s, int lane, uint32_t lane_dst) {
+    if (left > 0) {
+      constexpr int CH = D / 32;            // 16-byte chunks of a key's codes; a copy covers 32 / CH keys
+      long row[2];                          // cache row of the tile's key 0, as seen from each half
+      bool ok[2] = {true, true};
+      if (a.block_table) {
+        const int hkv = u.k / a.nrb;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if ((unsigned)page[h] >= (unsigned)a.num_pages) {
+            if (lane == 0 && keys > 16 * h) atomicCAS(a.status, 0, kDevBadPage);
+            ok[h] = false;
+            page[h] = 0;
+          }
+          row[h] = ((long)page[h] * a.Hkv + hkv) * a.page_size + (a.page_size == 16 ? -16 * h : inpg);
+        }
+      } else {
+        row[0] = row[1] = base;
+      }
+      [[maybe_unused]] const long rows = a.block_table ? (long)a.num_pages * a.Hkv * a.page_size : (long)a.B * a.Hkv * a.S;
+      if (keys >= kTK && ok[0] && ok[1] && GQA_CHECK(row[0] >= 0 && row[0] + 15 < rows && row[1] + 31 < rows, a.status, a.dbg_line)) {
+        const long o0 = row[0] * (D / 2) + lane * 16, o1 = row[1] * (D / 2) + lane * 16;
+        const uint8_t *k0 = a.k4 + o0, *k1 = a.k4 + o1, *v0 = a.v4 + o0, *v1 = a.v4 + o1;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          cp_async16(s + lane_dst + i * 512, (i < CH / 2 ? k0 : k1) + i * 512);
+          cp_async16(s + lane_dst + C::kCodes + i * 512, (i < CH / 2 ? v0 : v1) + i * 512);
+        }
+        const long f = (lane < 16 ? row[0] : row[1]) * (D / 16) + lane * (D / 16);
+        cp_async_small<D / 16>(s + 2 * C::kCodes + lane * (D / 16), a.ksf + f);
+        cp_async_small<D / 16>(s + 2 * C::kCodes + C::kSf + lane * (D / 16), a.vsf + f);
+      } else {                              // the row's last tile, or a page outside the pool: zeros for what is not there
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int key = i * (32 / CH) + lane / CH, h = i < CH / 2 ? 0 : 1;
+          const bool valid = key < keys && ok[h] && GQA_CHECK(row[h] + key >= 0 && row[h] + key < rows, a.status, a.dbg_line);
+          const long o = valid ? row[h] * (D / 2) + lane * 16 + i * 512 : 0;
+          cp_async16(s + lane_dst + i * 512, a.k4 + o, valid);
+          cp_async16(s + lane_dst + C::kCodes + i * 512, a.v4 + o, valid);
+        }
+        const long r = (lane < 16 ? row[0] : row[1]) + lane;
+        const bool valid = lane < keys && (lane < 16 ? ok[0] : ok[1]) && GQA_CHECK(r >= 0 && r < rows, a.status, a.dbg_line);
+        const long f = valid ? r * (D / 16) : 0;
+        cp_async_small<D / 16>(s + 2 * C::kCodes + lane * (D / 16), a.ksf + f, valid);
+        cp_async_small<D / 16>(s + 2 * C::kCodes + C::kSf + lane * (D / 16), a.vsf + f, valid);
+      }
+      if (--left > 0) {
+        if (--tiles > 0) {
+          keys -= kTK;
+          if (a.block_table) {
+            inpg += kTK;
+            if (inpg >= a.page_size) {
+              pidx += a.page_size == 16 ? 2 : 1;
+              inpg = 0;
+              look_up(a);
+            }
+          } else {
+            base += kTK;
+          }
+        } else {
+          u.next(a);
+          enter(a, 0);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
 };
 
 template <int D, int NT, int PARTS>
@@ -323,14 +443,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long sums[C::kWarps];
   __shared__ int prefix[C::kThreads];
-  __shared__ Walk rec_walk[2 * C::kWarps];   // unit of each stored piece, its first and last tile
-  __shared__ long rec_end[2 * C::kWarps];    // stream index after the piece; 0: none
+  __shared__ Unit rec_unit[2 * C::kWarps];   // unit of each stored piece
+  __shared__ int rec_end[2 * C::kWarps];     // stream index after the piece; 0: none
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int upb = a.Hkv * a.nrb;
 
   if (tid < 2 * C::kWarps) rec_end[tid] = 0;
-  // C: tiles of all units
+  // tiles of all units
   long mine = 0;
   for (int b = tid; b < a.B; b += C::kThreads) {
     int len;
@@ -342,20 +462,19 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(~0u, mine, d);
   if (lane == 0) sums[warp] = mine;
   __syncthreads();
-  long total = 0;
+  int total = 0;
 #pragma unroll
-  for (int w = 0; w < C::kWarps; ++w) total += sums[w];
+  for (int w = 0; w < C::kWarps; ++w) total += (int)sums[w];
   total *= upb;
-  const int Wn = (int)(total < (long)gridDim.x * C::kWarps ? total : (long)gridDim.x * C::kWarps);
+  const int Wn = min(total, (int)gridDim.x * C::kWarps);
   const int gw = blockIdx.x * C::kWarps + warp;
-  const long g0 = Wn == 0 || gw >= Wn ? 0 : gw * total / Wn, g1 = Wn == 0 || gw >= Wn ? 0 : (gw + 1) * total / Wn;
+  const int g0 = gw < Wn ? share_begin(gw, total, Wn) : 0, g1 = gw < Wn ? share_begin(gw + 1, total, Wn) : 0;
 
   // the batch row that holds tile g0: inclusive sums of the rows' tiles, kThreads rows at a time
-  Walk cw{g0, 0, -1, 0, 0, 0};
-  long before = 0;
+  Unit cu{0, 0, -1, 0, 0};
+  int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
-    int len = 0, nb = b0 + tid < a.B ? row_tiles(a, b0 + tid, len) : 0;
-    int inc = nb;
+    int len = 0, inc = b0 + tid < a.B ? row_tiles(a, b0 + tid, len) : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int x = __shfl_up_sync(~0u, inc, d);
@@ -364,352 +483,317 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     __syncthreads();
     if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    long all = 0;
+    int all = 0;
     for (int w = 0; w < C::kWarps; ++w) {
       if (w < warp) inc += (int)sums[w];
-      all += sums[w];
+      all += (int)sums[w];
     }
     prefix[tid] = inc;
     __syncthreads();
-    if (g0 < g1 && cw.b < 0 && g0 < (before + all) * upb) {
-      const long x = g0 - before * upb;   // row i of these: prefix[i - 1] * upb <= x < prefix[i] * upb
+    if (g0 < g1 && cu.b < 0 && g0 < (before + all) * upb) {
+      const int x = g0 - before * upb;   // row i of these: prefix[i - 1] * upb <= x < prefix[i] * upb
       int lo = 0, hi = C::kThreads - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if ((long)prefix[mid] * upb > x) hi = mid;
+        if (prefix[mid] * upb > x) hi = mid;
         else lo = mid + 1;
       }
-      cw.b = b0 + lo;
-      cw.nb = row_tiles(a, cw.b, cw.len);
-      const long P = (before + (lo ? prefix[lo - 1] : 0)) * upb;
-      cw.k = (int)((g0 - P) / cw.nb);
-      cw.Pu = P + (long)cw.k * cw.nb;
+      cu.b = b0 + lo;
+      cu.nb = row_tiles(a, cu.b, cu.len);
+      const int P = (before + (lo ? prefix[lo - 1] : 0)) * upb;
+      cu.k = (g0 - P) / cu.nb;
+      cu.Pu = P + cu.k * cu.nb;
     }
     before += all;
   }
 
   if (g0 < g1) {
-    uint8_t* ring = smem + warp * C::kRing;
-    const uint32_t ring_s = smem_u32(ring);
-    Walk lw = cw;
-    int page[2] = {0, 0};
-    auto look_up = [&]() {   // pages of the two halves of the tile at lw
-      if (a.block_table && lw.g < g1) {
-        const int j = lw.tile() * kTK;
-        const int* bt = a.block_table + (long)lw.b * a.max_pages;
-        const int p = j / a.page_size;
-        page[0] = j < lw.len ? __ldg(bt + p) : 0;
-        page[1] = a.page_size == 16 ? (j + 16 < lw.len ? __ldg(bt + p + 1) : 0) : page[0];
-      }
-    };
-    auto issue = [&](int stage) {
-      if (lw.g < g1) {
-        const int j = lw.tile() * kTK, n = lw.len - j;   // keys of the tile
-        const int hkv = lw.k / a.nrb;
-        long row[2];
-        bool ok[2] = {true, true};
-        if (a.block_table) {
+    const uint32_t ring = smem_u32(smem + warp * C::kRing);
+    Loader<D, NT> ld;
+    ld.u = cu;
+    ld.left = g1 - g0;
+    ld.enter(a, g0 - cu.Pu);
+    const uint32_t lane_dst = row_at<D>(lane / (D / 32), lane % (D / 32));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (page[h] < 0 || page[h] >= a.num_pages) {
-              if (lane == 0 && j + 16 * h < lw.len) atomicCAS(a.status, 0, kDevBadPage);
-              ok[h] = false;
-              page[h] = 0;
-            }
-            const int off = a.page_size == 16 ? -16 * h : j % a.page_size;   // so that row + key is the key's row
-            row[h] = ((long)page[h] * a.Hkv + hkv) * a.page_size + off;
-          }
-        } else {
-          row[0] = row[1] = ((long)lw.b * a.Hkv + hkv) * a.S + j;
-        }
-        [[maybe_unused]] const long rows = a.block_table ? (long)a.num_pages * a.Hkv * a.page_size : (long)a.B * a.Hkv * a.S;
-        const uint32_t s = ring_s + stage * C::kStage;
-        constexpr int CH = D / 32;    // 16-byte chunks of a key's codes
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int key = (i * 32 + lane) / CH, c = lane % CH, h = key >> 4;
-          const bool valid = key < n && ok[h] && GQA_CHECK(row[h] + key < rows, a.status, a.dbg_line);
-          const long at = valid ? (row[h] + key) * (D / 2) + c * 16 : 0;
-          const uint32_t d = s + row_at<D>(key, c);
-          cp_async16(d, a.k4 + at, valid);
-          cp_async16(d + C::kCodes, a.v4 + at, valid);
-        }
-        const int h = lane >> 4;
-        const bool valid = lane < n && ok[h] && GQA_CHECK(row[h] + lane < rows, a.status, a.dbg_line);
-        const long at = valid ? (row[h] + lane) * (D / 16) : 0;
-        const uint32_t d = s + 2 * C::kCodes + lane * (D / 16);
-        cp_async_small<D / 16>(d, a.ksf + at, valid);
-        cp_async_small<D / 16>(d + C::kSf, a.vsf + at, valid);
-        lw.next(a, g1);
-        look_up();
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    look_up();
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+    for (int i = 0; i < C::kStages - 1; ++i) ld.issue(a, ring + i * C::kStage, lane, lane_dst);
 
     Piece4<D, NT> p;
     uint32_t qf[NT][PARTS][D / 16][2];
-    float fac[NT][2];
-    int lim[NT][2];               // last key each of the thread's rows sees
-    bool fresh = true;
-    int stage = 0;
-    while (cw.g < g1) {
-      if (fresh) {
-        load_queries<D, NT, PARTS>(a, cw, lane, qf, fac);
-        p.clear();
-        const int r0 = (cw.k % a.nrb) * 8 * NT;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) lim[n][c] = cw.len - a.Tq + (r0 + n * 8 + 2 * t + c) % a.Tq;
-        fresh = false;
-      }
-      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-      __syncwarp();               // every lane's copies have landed; the stage before is read
-      issue(stage == 0 ? C::kStages - 1 : stage - 1);
-      const uint32_t s = ring_s + stage * C::kStage;
-      const int j0 = cw.tile() * kTK;
-
-      // S^T of both 16-key groups
-      float sc[2][NT][4];
-#pragma unroll
-      for (int G = 0; G < 2; ++G) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) sc[G][n][0] = sc[G][n][1] = sc[G][n][2] = sc[G][n][3] = 0.f;
-        const int ka = 16 * G + key_of(g), kb = ka + 8;
-        uint32_t wa[D / 32], wb[D / 32];
-        uint32_t sa, sb;             // block scales as f16 pairs: (first, second) 16 features, D = 64: one
-        if constexpr (D == 128) {
-          const uint4 u = ld_shared_v4(s + row_at<D>(ka, t)), v = ld_shared_v4(s + row_at<D>(kb, t));
-          wa[0] = u.x, wa[1] = u.y, wa[2] = u.z, wa[3] = u.w;
-          wb[0] = v.x, wb[1] = v.y, wb[2] = v.z, wb[3] = v.w;
-          sa = e4m3x2_to_f16(lds<2>(s + 2 * C::kCodes + ka * 8 + 2 * t));
-          sb = e4m3x2_to_f16(lds<2>(s + 2 * C::kCodes + kb * 8 + 2 * t));
-        } else {
-          lds64(s + row_at<D>(ka, 0) + 8 * t, wa);
-          lds64(s + row_at<D>(kb, 0) + 8 * t, wb);
-          sa = e4m3x2_to_f16(lds<1>(s + 2 * C::kCodes + ka * 4 + t));
-          sb = e4m3x2_to_f16(lds<1>(s + 2 * C::kCodes + kb * 4 + t));
-        }
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {     // 8 features: two MMAs
-          uint32_t ra[4], rb[4];
-          e2m1x8_to_f16(wa[w], ra);
-          e2m1x8_to_f16(wb[w], rb);
-          const uint32_t sel = D == 128 && w >= 2 ? 0x3232u : 0x1010u;
-          const uint32_t fa = __byte_perm(sa, 0, sel), fb = __byte_perm(sb, 0, sel);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ra[i] = hmul2_u(ra[i], fa), rb[i] = hmul2_u(rb[i], fb);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int q = 0; q < PARTS; ++q)
-                mma_f16(sc[G][n], ra[2 * i], rb[2 * i], ra[2 * i + 1], rb[2 * i + 1], qf[n][q][2 * w + i][0],
-                        qf[n][q][2 * w + i][1]);
-        }
-      }
-      // scale, mask, running maximum
-      const bool edge = j0 + kTK > cw.len - a.Tq + 1;   // some key of the tile is hidden from some row
-      bool grow = false;
+    float fac[NT][2], bias[NT][2];
+    int lim[NT][2];                      // last key each of the thread's rows sees
+    uint32_t s = ring;                   // stage of the current tile, and the one before
+    uint32_t prev = ring + (C::kStages - 1) * C::kStage;
+    for (int at = g0;;) {                // a piece of unit cu, from tile `at` on
+      load_queries<D, NT, PARTS>(a, cu, lane, qf, fac);
+      p.clear();
+      const int r0 = (cu.k % a.nrb) * 8 * NT;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = -CUDART_INF_F;
-#pragma unroll
-          for (int G = 0; G < 2; ++G)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float& x = sc[G][n][2 * h + c];
-              x *= fac[n][c];
-              if (edge && j0 + 16 * G + 8 * h + key_of(g) > lim[n][c]) x = -CUDART_INF_F;
-              mx = fmaxf(mx, x);
-            }
-          grow |= mx > p.m[n][c] + kLazy;
+          lim[n][c] = cu.len - a.Tq + (r0 + n * 8 + 2 * t + c) % a.Tq;
+          bias[n][c] = CUDART_INF_F;     // kOff - m: any visible score makes the maximum move
         }
-      if (__any_sync(~0u, grow)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c]));
-            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-            mx = fmaxf(mx, p.m[n][c]);
-            const float f = p.m[n][c] == -CUDART_INF_F ? 1.f : ex2_approx(p.m[n][c] - mx);
-            p.m[n][c] = mx;
-            p.l[n][c] *= f;
-#pragma unroll
-            for (int i = 0; i < C::kMT; ++i) p.acc[n][i][c] *= f, p.acc[n][i][2 + c] *= f;
-          }
-      }
-      // P, its sums, and its fragments
-      uint32_t pf[2][NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float bias[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) bias[c] = p.m[n][c] == -CUDART_INF_F ? 0.f : kOff - p.m[n][c];
+      const int end = min(cu.Pu + cu.nb, g1);
+      for (int j0 = (at - cu.Pu) * kTK, je = (end - cu.Pu) * kTK; j0 < je; j0 += kTK) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+        __syncwarp();                    // every lane's copies have landed; the stage before is read
+        ld.issue(a, prev, lane, lane_dst);
+
+        // S^T of both 16-key groups
+        float sc[2][NT][4];
 #pragma unroll
         for (int G = 0; G < 2; ++G) {
-          float x[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = ex2_approx(sc[G][n][i] + bias[i & 1]);
-            p.l[n][i & 1] += x[i];
+          for (int n = 0; n < NT; ++n) sc[G][n][0] = sc[G][n][1] = sc[G][n][2] = sc[G][n][3] = 0.f;
+          const int ka = 16 * G + key_of(g), kb = ka + 8;
+          uint32_t wa[D / 32], wb[D / 32];
+          uint32_t sa, sb;               // block scales as f16 pairs: (first, second) 16 features, D = 64: one
+          if constexpr (D == 128) {
+            const uint4 u = ld_shared_v4(s + row_at<D>(ka, t)), v = ld_shared_v4(s + row_at<D>(kb, t));
+            wa[0] = u.x, wa[1] = u.y, wa[2] = u.z, wa[3] = u.w;
+            wb[0] = v.x, wb[1] = v.y, wb[2] = v.z, wb[3] = v.w;
+            sa = e4m3x2_to_f16(lds<2>(s + 2 * C::kCodes + ka * 8 + 2 * t));
+            sb = e4m3x2_to_f16(lds<2>(s + 2 * C::kCodes + kb * 8 + 2 * t));
+          } else {
+            lds64(s + row_at<D>(ka, 0) + 8 * t, wa);
+            lds64(s + row_at<D>(kb, 0) + 8 * t, wb);
+            sa = e4m3x2_to_f16(lds<1>(s + 2 * C::kCodes + ka * 4 + t));
+            sb = e4m3x2_to_f16(lds<1>(s + 2 * C::kCodes + kb * 4 + t));
           }
-          pf[G][n][0] = transpose8x8(pack_f16x2(x[0], x[1]));
-          pf[G][n][1] = transpose8x8(pack_f16x2(x[2], x[3]));
-        }
-      }
-      // O^T
 #pragma unroll
-      for (int G = 0; G < 2; ++G) {
-        uint32_t sb[4];
-        constexpr int VW = D / 64;                 // words of a thread's features of one key
-        uint32_t w[4][VW];
+          for (int w = 0; w < D / 32; ++w) {     // 8 features: two MMAs
+            uint32_t ra[4], rb[4];
+            e2m1x8_to_f16(wa[w], ra);
+            e2m1x8_to_f16(wb[w], rb);
+            const uint32_t sel = D == 128 && w >= 2 ? 0x3232u : 0x1010u;
+            const uint32_t fa = __byte_perm(sa, 0, sel), fb = __byte_perm(sb, 0, sel);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {              // keys pi(2t), pi(2t+1), pi(2t+8), pi(2t+9)
-          const int key = 16 * G + 8 * (i >> 1) + key_of(2 * t + (i & 1));
-          if constexpr (D == 128) lds64(s + C::kCodes + row_at<D>(key, g >> 1) + 8 * (g & 1), w[i]);
-          else w[i][0] = lds<4>(s + C::kCodes + row_at<D>(key, 0) + 4 * g);
-          sb[i] = lds<1>(s + 2 * C::kCodes + C::kSf + key * (D / 16) + (D == 128 ? g : g >> 1));
-        }
-        if (edge && a.Tq > 1) {
-          // a NaN block at a key that some rows do not see: 0 * NaN would reach them through the MMA, so it is
-          // taken out here and put into the rows that do see it
-          bool bad = false;
+            for (int i = 0; i < 4; ++i) ra[i] = hmul2_u(ra[i], fa), rb[i] = hmul2_u(rb[i], fb);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if ((sb[i] & 0x7f) == 0x7f) bad = true, sb[i] = 0;
-          }
-          if (__any_sync(~0u, bad)) {
-            for (int k = 0; k < 16; ++k) {
-              const uint32_t v = lds<1>(s + 2 * C::kCodes + C::kSf + (16 * G + k) * (D / 16) + (D == 128 ? g : g >> 1));
-              if ((v & 0x7f) != 0x7f) continue;
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                  if (j0 + 16 * G + k <= lim[n][c]) {
+                for (int q = 0; q < PARTS; ++q)
+                  mma_f16(sc[G][n], ra[2 * i], rb[2 * i], ra[2 * i + 1], rb[2 * i + 1], qf[n][q][2 * w + i][0],
+                          qf[n][q][2 * w + i][1]);
+          }
+        }
+        // y = s - m + kOff in log2 units, hidden keys out; the maximum moves when some y is above kOff + kLazy
+        const bool edge = j0 + kTK > cu.len - a.Tq + 1;   // some key of the tile is hidden from some row
+        float y[2][NT][4];
+        float top = -CUDART_INF_F;
 #pragma unroll
-                    for (int i = 0; i < C::kMT; ++i) p.acc[n][i][c] = p.acc[n][i][2 + c] = CUDART_NAN_F;
-                  }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int G = 0; G < 2; ++G) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[G][n][i] = fmaf(sc[G][n][i], fac[n][i & 1], bias[n][i & 1]);
+            if (edge) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (j0 + 16 * G + 8 * (i >> 1) + key_of(g) > lim[n][i & 1]) y[G][n][i] = sc[G][n][i] = -CUDART_INF_F;
+            }
+            top = max3f(max3f(top, y[G][n][0], y[G][n][1]), y[G][n][2], y[G][n][3]);
+          }
+        if (__any_sync(~0u, top > kOff + kLazy)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float mx = -CUDART_INF_F;
+#pragma unroll
+              for (int G = 0; G < 2; ++G)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {   // a hidden key's score is -infinity whatever the factor's sign
+                  const float x = sc[G][n][2 * h + c];
+                  mx = fmaxf(mx, x == -CUDART_INF_F ? x : x * fac[n][c]);
+                }
+              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+              mx = fmaxf(mx, p.m[n][c]);
+              const float f = p.m[n][c] == -CUDART_INF_F ? 1.f : ex2_approx(p.m[n][c] - mx);
+              p.m[n][c] = mx;
+              bias[n][c] = kOff - mx;
+              p.l[n][c] *= f;
+#pragma unroll
+              for (int i = 0; i < C::kMT; ++i) p.acc[n][i][c] *= f, p.acc[n][i][2 + c] *= f;
+#pragma unroll
+              for (int G = 0; G < 2; ++G)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float x = sc[G][n][2 * h + c];
+                  y[G][n][2 * h + c] = x == -CUDART_INF_F ? x : fmaf(x, fac[n][c], bias[n][c]);
+                }
+            }
+        }
+        // P, its sums, and its fragments
+        uint32_t pf[2][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int G = 0; G < 2; ++G) {
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] = ex2_approx(y[G][n][i]);
+              p.l[n][i & 1] += x[i];
+            }
+            pf[G][n][0] = transpose8x8(pack_f16x2(x[0], x[1]));
+            pf[G][n][1] = transpose8x8(pack_f16x2(x[2], x[3]));
+          }
+        // O^T
+#pragma unroll
+        for (int G = 0; G < 2; ++G) {
+          uint32_t sb[4];
+          constexpr int VW = D / 64;                 // words of a thread's features of one key
+          uint32_t w[4][VW];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {              // keys pi(2t), pi(2t+1), pi(2t+8), pi(2t+9)
+            const int key = 16 * G + 8 * (i >> 1) + key_of(2 * t + (i & 1));
+            if constexpr (D == 128) lds64(s + C::kCodes + row_at<D>(key, g >> 1) + 8 * (g & 1), w[i]);
+            else w[i][0] = lds<4>(s + C::kCodes + row_at<D>(key, 0) + 4 * g);
+            sb[i] = lds<1>(s + 2 * C::kCodes + C::kSf + key * (D / 16) + (D == 128 ? g : g >> 1));
+          }
+          if (edge && a.Tq > 1) {
+            // a NaN block at a key that some rows do not see: 0 * NaN would reach them through the MMA, so it is
+            // taken out here and put into the rows that do see it
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if ((sb[i] & 0x7f) == 0x7f) bad = true, sb[i] = 0;
+            }
+            if (__any_sync(~0u, bad)) {
+              for (int k = 0; k < 16; ++k) {
+                const uint32_t v = lds<1>(s + 2 * C::kCodes + C::kSf + (16 * G + k) * (D / 16) + (D == 128 ? g : g >> 1));
+                if ((v & 0x7f) != 0x7f) continue;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c)
+                    if (j0 + 16 * G + k <= lim[n][c]) {
+#pragma unroll
+                      for (int i = 0; i < C::kMT; ++i) p.acc[n][i][c] = p.acc[n][i][2 + c] = CUDART_NAN_F;
+                    }
+              }
+            }
+          }
+          const uint32_t f01 = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x0040)), f23 = e4m3x2_to_f16(__byte_perm(sb[2], sb[3], 0x0040));
+#pragma unroll
+          for (int v = 0; v < VW; ++v) {
+            // half bytes of two keys side by side: byte i of e.. is feature 2i of both, of o.. feature 2i+1
+            uint32_t e01[4], o01[4], e23[4], o23[4];
+            e2m1x8_to_f16((w[0][v] & 0x0F0F0F0Fu) | ((w[1][v] << 4) & 0xF0F0F0F0u), e01);
+            e2m1x8_to_f16(((w[0][v] >> 4) & 0x0F0F0F0Fu) | (w[1][v] & 0xF0F0F0F0u), o01);
+            e2m1x8_to_f16((w[2][v] & 0x0F0F0F0Fu) | ((w[3][v] << 4) & 0xF0F0F0F0u), e23);
+            e2m1x8_to_f16(((w[2][v] >> 4) & 0x0F0F0F0Fu) | (w[3][v] & 0xF0F0F0F0u), o23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a0 = hmul2_u(e01[i], f01), a1 = hmul2_u(o01[i], f01);
+              const uint32_t a2 = hmul2_u(e23[i], f23), a3 = hmul2_u(o23[i], f23);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_f16(p.acc[n][4 * v + i], a0, a1, a2, a3, pf[G][n][0], pf[G][n][1]);
             }
           }
         }
-        const uint32_t f01 = e4m3x2_to_f16(sb[0] | sb[1] << 8), f23 = e4m3x2_to_f16(sb[2] | sb[3] << 8);
-#pragma unroll
-        for (int v = 0; v < VW; ++v) {
-          // half bytes of two keys side by side: byte i of `even` is feature 2i of both, of `odd` feature 2i+1
-          uint32_t e01[4], o01[4], e23[4], o23[4];
-          e2m1x8_to_f16((w[0][v] & 0x0F0F0F0Fu) | ((w[1][v] << 4) & 0xF0F0F0F0u), e01);
-          e2m1x8_to_f16(((w[0][v] >> 4) & 0x0F0F0F0Fu) | (w[1][v] & 0xF0F0F0F0u), o01);
-          e2m1x8_to_f16((w[2][v] & 0x0F0F0F0Fu) | ((w[3][v] << 4) & 0xF0F0F0F0u), e23);
-          e2m1x8_to_f16(((w[2][v] >> 4) & 0x0F0F0F0Fu) | (w[3][v] & 0xF0F0F0F0u), o23);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t a0 = hmul2_u(e01[i], f01), a1 = hmul2_u(o01[i], f01);
-            const uint32_t a2 = hmul2_u(e23[i], f23), a3 = hmul2_u(o23[i], f23);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(p.acc[n][4 * v + i], a0, a1, a2, a3, pf[G][n][0], pf[G][n][1]);
-          }
-        }
+        prev = s;
+        s = s == ring + (C::kStages - 1) * C::kStage ? ring : s + C::kStage;
       }
-      stage = stage == C::kStages - 1 ? 0 : stage + 1;
 
-      // end of the unit, or of the share
-      const long at = cw.g;
-      const bool unit_end = cw.tile() == cw.nb - 1;
-      if (unit_end || at == g1 - 1) {
-        if (unit_end && cw.Pu >= g0) {
-          write_unit<D, NT>(a, cw.b, cw.k, cw.len, p, lane);
-        } else {
-          const int slot = 2 * warp + (cw.Pu < g0 ? 0 : 1);   // a unit begun before the share, or continued after it
-          if (slot & 1) {   // the share ends here: no copy is in flight, and every lane has read the last tile
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            __syncwarp();
-          }
-          p.store(piece_at<D, NT>(smem, slot), lane);
-          if (lane == 0) {
-            rec_walk[slot] = cw;
-            rec_end[slot] = at + 1;
-          }
+      // the piece is done: written if it is its whole unit, else stored
+      if (end == cu.Pu + cu.nb && cu.Pu >= g0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          write_rows<D, C::kMT>(a, cu.b, cu.k, cu.len, 8 * NT, n, 0, p.acc[n], p.m[n], p.l[n], lane);
+      } else {
+        const int slot = 2 * warp + (cu.Pu < g0 ? 0 : 1);   // a unit begun before the share, or continued after it
+        if (slot & 1) {   // the share ends here: no copy is in flight, and every lane has read the last tile
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          __syncwarp();
         }
-        fresh = true;
+        p.store(piece_at<D, NT>(smem, slot), lane);
+        if (lane == 0) {
+          rec_unit[slot] = cu;
+          rec_end[slot] = end;
+        }
       }
-      cw.next(a, g1);
+      if (end == g1) break;
+      at = end;
+      cu.next(a);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   __syncthreads();
   griddep_launch();
 
-  // combine the stored pieces of each unit, in stream order; a warp takes the
-  // units whose first piece here is its own
-  const long c0 = Wn == 0 ? 0 : (long)min((int)blockIdx.x * C::kWarps, Wn) * total / Wn;   // the CTA's share
+  // Combine the stored pieces of each unit, in stream order; the warps share the unit's 16-feature tiles.
+  const int c0 = share_begin(min((int)blockIdx.x * C::kWarps, Wn), total, max(Wn, 1));   // the CTA's share
   Q4Head* heads = static_cast<Q4Head*>(a.ws);
   float* parts = reinterpret_cast<float*>(heads + kMaxCtas);
-  bool cut_before = false;
-  for (int s = 2 * warp; s < 2 * warp + 2; ++s) {
-    if (rec_end[s] == 0) continue;
-    const Walk w = rec_walk[s];
-    int prev = s - 1;
-    while (prev >= 0 && rec_end[prev] == 0) --prev;
-    if (prev >= 0 && rec_walk[prev].Pu == w.Pu) continue;   // not the unit's first piece here
-    Piece4<D, NT> p;
-    p.clear();
-    long end = 0;
-    for (int i = s; i < 2 * C::kWarps; ++i) {
-      if (rec_end[i] == 0) continue;
-      if (rec_walk[i].Pu != w.Pu) break;
-      p.add(piece_at<D, NT>(smem, i), lane);
-      end = rec_end[i];
-    }
-    if (w.Pu >= c0 && end == w.Pu + w.nb) {
-      write_unit<D, NT>(a, w.b, w.k, w.len, p, lane);
+  Q4Head head{};
+  head.first = -1;
+  auto at = [&](int i) -> const float* { return rec_end[i] ? piece_at<D, NT>(smem, i) : nullptr; };
+  for (int s0 = 0; s0 < 2 * C::kWarps;) {
+    if (rec_end[s0] == 0) {
+      ++s0;
       continue;
     }
-    const int slot = w.Pu < c0 ? 0 : 1;   // begun before the CTA's share, or in it
-    p.store(parts + ((long)blockIdx.x * 2 + slot) * C::kRec * 32, lane);
-    if (slot == 0) {
-      cut_before = true;
-      if (lane == 0) {
-        Q4Head h{};
-        h.b = w.b;
-        h.k = w.k;
-        h.len = w.len;
-        h.first = owner_of(w.Pu, total, Wn) / C::kWarps;
-        h.last = owner_of(w.Pu + w.nb - 1, total, Wn) / C::kWarps;
-        heads[blockIdx.x] = h;
+    const Unit u = rec_unit[s0];
+    int last = s0, next = s0 + 1;
+    while (next < 2 * C::kWarps && (rec_end[next] == 0 || rec_unit[next].Pu == u.Pu)) {
+      if (rec_end[next]) last = next;
+      ++next;
+    }
+    const bool whole = u.Pu >= c0 && rec_end[last] == u.Pu + u.nb;
+    const int slot = u.Pu < c0 ? 0 : 1;   // begun before the CTA's share, or in it
+    for (int tt = warp; tt < NT * C::kMT; tt += C::kWarps) {
+      const int n = tt / C::kMT, i = tt % C::kMT;
+      Combined<D> x;
+      x.from(at, s0, last, n, i, lane);
+      if (whole) {
+        write_rows<D, 1>(a, u.b, u.k, u.len, 8 * NT, n, i, &x.acc, x.m, x.l, lane);
+      } else {
+        float* q = parts + ((long)blockIdx.x * 2 + slot) * C::kRec * 32 + n * Piece4<D, NT>::kPer * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[32 * (4 * i + j)] = x.acc[j];
+        if (i == 0) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            q[32 * (D / 4 + c)] = x.m[c];
+            q[32 * (D / 4 + 2 + c)] = x.l[c];
+          }
+        }
       }
     }
+    if (!whole && slot == 0) {
+      head.b = u.b;
+      head.k = u.k;
+      head.len = u.len;
+      head.first = owner_of(u.Pu, total, Wn) / C::kWarps;
+      head.last = owner_of(u.Pu + u.nb - 1, total, Wn) / C::kWarps;
+    }
+    s0 = next;
   }
-  // slot 0 belongs to the warp with the CTA's first tile: warp 0
-  if (warp == 0 && lane == 0 && !cut_before) heads[blockIdx.x].first = -1;
+  if (tid == 0) heads[blockIdx.x] = head;
 }
 
 // Units cut between CTAs: the block of the second CTA that holds a piece of a
-// unit combines all of them.
+// unit combines all of them, a warp per 16-feature tile.
 template <int D, int NT>
-__global__ void __launch_bounds__(32) decode_q4_merge(const DecodeQ4Args a) {
+__global__ void __launch_bounds__(32 * NT * D / 16) decode_q4_merge(const DecodeQ4Args a) {
   using C = Q4Cfg<D, NT>;
   griddep_wait();
   const Q4Head* heads = static_cast<const Q4Head*>(a.ws);
   const float* parts = reinterpret_cast<const float*>(heads + kMaxCtas);
   const Q4Head h = heads[blockIdx.x];
   if (h.first < 0 || (int)blockIdx.x != h.first + 1) return;
-  const int lane = threadIdx.x;
-  Piece4<D, NT> p;
-  p.clear();
-  p.add(parts + ((long)h.first * 2 + 1) * C::kRec * 32, lane);
-  for (int c = h.first + 1; c <= h.last; ++c) p.add(parts + (long)c * 2 * C::kRec * 32, lane);
-  write_unit<D, NT>(a, h.b, h.k, h.len, p, lane);
+  const int lane = threadIdx.x & 31, tt = threadIdx.x >> 5;
+  auto at = [&](int c) -> const float* { return parts + ((long)c * 2 + (c == h.first)) * C::kRec * 32; };
+  Combined<D> x;
+  x.from(at, h.first, h.last, tt / C::kMT, tt % C::kMT, lane);
+  write_rows<D, 1>(a, h.b, h.k, h.len, 8 * NT, tt / C::kMT, tt % C::kMT, &x.acc, x.m, x.l, lane);
 }
 
 template <int D, int NT, int PARTS>
@@ -722,7 +806,7 @@ cudaError_t run(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
   prof_end(stream);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   prof_begin(kProfDecodeMerge, stream);
-  e = launch_programmatic(decode_q4_merge<D, NT>, dim3(ctas), dim3(32), 0, stream, a);
+  e = launch_programmatic(decode_q4_merge<D, NT>, dim3(ctas), dim3(32 * NT * D / 16), 0, stream, a);
   prof_end(stream);
   return e;
 }
