@@ -103,37 +103,49 @@ struct Piece4 {
   }
 };
 
-// One 16-feature tile of 8 rows of a unit, combined from stored pieces:
-// at(i) is piece i's base, nullptr for none.
+// One 16-feature tile of 8 rows of a unit, combined from `count` stored pieces;
+// at(i) is piece i's base.  Several pieces' loads are in flight at a time.
 template <int D>
 struct Combined {
   float acc[4], m[2], l[2];
   template <typename At>
-  __device__ __forceinline__ void from(At at, int first, int last, int n, int tile, int lane) {
-    constexpr int kPer = D / 16 * 4 + 4;
+  __device__ __forceinline__ void from(At at, int count, int n, int tile, int lane) {
+    constexpr int kPer = D / 16 * 4 + 4, kBatch = 4;
     const int base = n * kPer * 32 + lane;
     m[0] = m[1] = -CUDART_INF_F;
-#pragma unroll 8
-    for (int i = first; i <= last; ++i) {
-      const float* p = at(i);
-      if (!p) continue;
-      m[0] = fmaxf(m[0], p[base + 32 * (D / 4)]);
-      m[1] = fmaxf(m[1], p[base + 32 * (D / 4 + 1)]);
-    }
-    l[0] = l[1] = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-#pragma unroll 4
-    for (int i = first; i <= last; ++i) {
-      const float* p = at(i);
-      if (!p) continue;
-      float f[2];
+    for (int i = 0; i < count; i += kBatch) {
+      float x[kBatch][2];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float mp = p[base + 32 * (D / 4 + c)];
-        f[c] = mp == -CUDART_INF_F ? 1.f : ex2_approx(mp - m[c]);   // such a piece holds zeros (or NaN, kept)
-        l[c] = fmaf(p[base + 32 * (D / 4 + 2 + c)], f[c], l[c]);
+      for (int u = 0; u < kBatch; ++u) {
+        const float* p = at(min(i + u, count - 1)) + base;
+        x[u][0] = p[32 * (D / 4)], x[u][1] = p[32 * (D / 4 + 1)];
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = fmaf(p[base + 32 * (4 * tile + j)], f[j & 1], acc[j]);
+      for (int u = 0; u < kBatch; ++u) m[0] = fmaxf(m[0], x[u][0]), m[1] = fmaxf(m[1], x[u][1]);
+    }
+    l[0] = l[1] = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+    for (int i = 0; i < count; i += kBatch) {
+      float x[kBatch][8];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float* p = at(min(i + u, count - 1)) + base;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[u][j] = p[32 * (4 * tile + j)];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[u][4 + j] = p[32 * (D / 4 + j)];
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (i + u >= count) break;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          // a piece whose maximum is -infinity holds zeros (or NaN, which is kept)
+          const float f = x[u][4 + c] == -CUDART_INF_F ? 1.f : ex2_approx(x[u][4 + c] - m[c]);
+          l[c] = fmaf(x[u][6 + c], f, l[c]);
+          acc[c] = fmaf(x[u][c], f, acc[c]);
+          acc[2 + c] = fmaf(x[u][2 + c], f, acc[2 + c]);
+        }
+      }
     }
   }
 };
@@ -441,7 +453,7 @@ template <int D, int NT, int PARTS>
 __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(const DecodeQ4Args a) {
   using C = Q4Cfg<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long sums[C::kWarps];
+  __shared__ int sums[C::kWarps];
   __shared__ int prefix[C::kThreads];
   __shared__ Unit rec_unit[2 * C::kWarps];   // unit of each stored piece
   __shared__ int rec_end[2 * C::kWarps];     // stream index after the piece; 0: none
@@ -450,49 +462,56 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   const int upb = a.Hkv * a.nrb;
 
   if (tid < 2 * C::kWarps) rec_end[tid] = 0;
-  // tiles of all units
-  long mine = 0;
-  for (int b = tid; b < a.B; b += C::kThreads) {
-    int len;
-    const int nb = row_tiles(a, b, len);
-    if (nb == 0 && blockIdx.x == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
-    mine += nb;
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(~0u, mine, d);
-  if (lane == 0) sums[warp] = mine;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < C::kWarps; ++w) total += (int)sums[w];
-  total *= upb;
-  const int Wn = min(total, (int)gridDim.x * C::kWarps);
+  // The tiles of all units, and the batch row that holds tile g0: inclusive
+  // sums of the rows' tiles, kThreads rows at a time (more rows: a pass for the total first).
+  int total = 0, Wn = 0, g0 = 0, g1 = 0, before = 0;
   const int gw = blockIdx.x * C::kWarps + warp;
-  const int g0 = gw < Wn ? share_begin(gw, total, Wn) : 0, g1 = gw < Wn ? share_begin(gw + 1, total, Wn) : 0;
-
-  // the batch row that holds tile g0: inclusive sums of the rows' tiles, kThreads rows at a time
   Unit cu{0, 0, -1, 0, 0};
-  int before = 0;
+  auto take_share = [&](int tiles) {
+    total = tiles * upb;
+    Wn = min(total, (int)gridDim.x * C::kWarps);
+    if (gw < Wn) g0 = share_begin(gw, total, Wn), g1 = share_begin(gw + 1, total, Wn);
+  };
+  if (a.B > C::kThreads) {
+    int mine = 0;
+    for (int b = tid; b < a.B; b += C::kThreads) {
+      int len;
+      mine += row_tiles(a, b, len);
+    }
+    mine = __reduce_add_sync(~0u, mine);
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) all += sums[w];
+    take_share(all);
+  }
   for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
-    int len = 0, inc = b0 + tid < a.B ? row_tiles(a, b0 + tid, len) : 0;
+    int len = 0, inc = 0;
+    if (b0 + tid < a.B) {
+      inc = row_tiles(a, b0 + tid, len);
+      if (inc == 0 && blockIdx.x == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+    }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int x = __shfl_up_sync(~0u, inc, d);
       if (lane >= d) inc += x;
     }
-    __syncthreads();
+    if (b0 > 0 || a.B > C::kThreads) __syncthreads();   // the sums before are read
     if (lane == 31) sums[warp] = inc;
     __syncthreads();
     int all = 0;
+#pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-      if (w < warp) inc += (int)sums[w];
-      all += (int)sums[w];
+      if (w < warp) inc += sums[w];
+      all += sums[w];
     }
     prefix[tid] = inc;
     __syncthreads();
+    if (a.B <= C::kThreads) take_share(all);
     if (g0 < g1 && cu.b < 0 && g0 < (before + all) * upb) {
       const int x = g0 - before * upb;   // row i of these: prefix[i - 1] * upb <= x < prefix[i] * upb
-      int lo = 0, hi = C::kThreads - 1;
+      int lo = 0, hi = min(C::kThreads, a.B - b0) - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (prefix[mid] * upb > x) hi = mid;
@@ -734,24 +753,30 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   float* parts = reinterpret_cast<float*>(heads + kMaxCtas);
   Q4Head head{};
   head.first = -1;
-  auto at = [&](int i) -> const float* { return rec_end[i] ? piece_at<D, NT>(smem, i) : nullptr; };
-  for (int s0 = 0; s0 < 2 * C::kWarps;) {
-    if (rec_end[s0] == 0) {
-      ++s0;
-      continue;
-    }
+  // Lane s looks after slot s: which are taken, and which of them begin a unit.
+  static_assert(2 * C::kWarps <= 32, "a lane per slot");
+  const int my_end = lane < 2 * C::kWarps ? rec_end[lane] : 0;
+  const int my_Pu = my_end ? rec_unit[lane].Pu : -1;
+  const unsigned taken = __ballot_sync(~0u, my_end > 0);
+  const unsigned earlier = taken & ((1u << lane) - 1);
+  const int prev_Pu = __shfl_sync(~0u, my_Pu, earlier ? 31 - __clz(earlier) : lane);
+  const unsigned begins = __ballot_sync(~0u, my_end > 0 && (!earlier || prev_Pu != my_Pu));
+  unsigned rest = taken;
+  for (int i = 0; i < lane; ++i) rest &= rest - 1;
+  const int nth = __ffs(rest) - 1;          // lane i: the i-th slot taken
+  for (unsigned todo = begins; todo;) {
+    const int s0 = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const unsigned slots = taken & ~((1u << s0) - 1) & (todo ? (todo & -todo) - 1 : ~0u);   // up to the next unit's
     const Unit u = rec_unit[s0];
-    int last = s0, next = s0 + 1;
-    while (next < 2 * C::kWarps && (rec_end[next] == 0 || rec_unit[next].Pu == u.Pu)) {
-      if (rec_end[next]) last = next;
-      ++next;
-    }
-    const bool whole = u.Pu >= c0 && rec_end[last] == u.Pu + u.nb;
+    const bool whole = u.Pu >= c0 && rec_end[31 - __clz(slots)] == u.Pu + u.nb;
     const int slot = u.Pu < c0 ? 0 : 1;   // begun before the CTA's share, or in it
+    const int rank = __popc(taken & ((1u << s0) - 1));
     for (int tt = warp; tt < NT * C::kMT; tt += C::kWarps) {
       const int n = tt / C::kMT, i = tt % C::kMT;
       Combined<D> x;
-      x.from(at, s0, last, n, i, lane);
+      x.from([&](int j) -> const float* { return piece_at<D, NT>(smem, __shfl_sync(~0u, nth, rank + j)); }, __popc(slots), n,
+             i, lane);
       if (whole) {
         write_rows<D, 1>(a, u.b, u.k, u.len, 8 * NT, n, i, &x.acc, x.m, x.l, lane);
       } else {
@@ -774,7 +799,6 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
       head.first = owner_of(u.Pu, total, Wn) / C::kWarps;
       head.last = owner_of(u.Pu + u.nb - 1, total, Wn) / C::kWarps;
     }
-    s0 = next;
   }
   if (tid == 0) heads[blockIdx.x] = head;
 }
@@ -790,9 +814,9 @@ __global__ void __launch_bounds__(32 * NT * D / 16) decode_q4_merge(const Decode
   const Q4Head h = heads[blockIdx.x];
   if (h.first < 0 || (int)blockIdx.x != h.first + 1) return;
   const int lane = threadIdx.x & 31, tt = threadIdx.x >> 5;
-  auto at = [&](int c) -> const float* { return parts + ((long)c * 2 + (c == h.first)) * C::kRec * 32; };
+  auto at = [&](int i) -> const float* { return parts + ((long)(h.first + i) * 2 + (i == 0)) * C::kRec * 32; };
   Combined<D> x;
-  x.from(at, h.first, h.last, tt / C::kMT, tt % C::kMT, lane);
+  x.from(at, h.last - h.first + 1, tt / C::kMT, tt % C::kMT, lane);
   write_rows<D, 1>(a, h.b, h.k, h.len, 8 * NT, tt / C::kMT, tt % C::kMT, &x.acc, x.m, x.l, lane);
 }
 
