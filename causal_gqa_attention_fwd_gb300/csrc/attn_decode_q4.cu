@@ -157,9 +157,16 @@ __device__ __forceinline__ int row_tiles(const DecodeQ4Args& a, int b, int& len)
   return len < 0 || len > a.S ? 0 : len == 0 ? 1 : (len + kTK - 1) / kTK;
 }
 
-// The share of all C tiles (C < 2^31): warps 0..G-1 of the grid, warp w takes [wC/G, (w+1)C/G).
-__device__ __forceinline__ int share_begin(int w, int C, int G) { return (int)((long)w * C / G); }
-__device__ __forceinline__ int owner_of(int g, int C, int G) { return (int)((((long)g + 1) * G - 1) / C); }
+// The shares of all C tiles (C < 2^31): warps 0..G-1 of the grid take C / G tiles each, the first C % G one more.
+struct Shares {
+  int q, r;
+  __device__ __forceinline__ Shares(int C, int G) : q(C / G), r(C - C / G * G) {}
+  __device__ __forceinline__ int begin(int w) const { return w * q + min(w, r); }
+  __device__ __forceinline__ int owner(int g) const {
+    const int cut = r * (q + 1);
+    return g < cut ? g / (q + 1) : r + (g - cut) / q;
+  }
+};
 
 // A unit of the stream.
 struct Unit {
@@ -242,7 +249,15 @@ __device__ __forceinline__ int row_at(int k, int c) {
   return D == 128 ? k * 64 + ((c ^ (2 * s)) * 16) : (k ^ s) * 32 + c * 16;
 }
 
-// One piece's query rows as B fragments: part 0 the f16 value, part 1 (rotary
+// The last key that rows r0 + 8n + 2t (+ 1) of a unit see, for a thread's columns of 8-row tile n: key
+// len - Tq + (row % Tq); below 0: none.
+__device__ __forceinline__ void row_limits(const DecodeQ4Args& a, int len, int r, int* lim) {
+  const int q = r % a.Tq;
+  lim[0] = len - a.Tq + q;
+  lim[1] = q + 1 == a.Tq ? len - a.Tq : lim[0] + 1;
+}
+
+// A unit's query rows as B fragments: part 0 the f16 value, part 1 (rotary
 // queries) the remainder; rows are scaled by a power of two so that their
 // largest element lies in [2^14, 2^15); fac undoes it and applies the softmax scale.
 template <int D, int NT, int PARTS>
@@ -255,33 +270,40 @@ __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& 
   for (int n = 0; n < NT; ++n) {
     const int r = r0 + n * 8 + g;
     const long row = ((long)w.b * a.Hq + hkv * a.G) * a.Tq + r;
-    const int pos = w.len - a.Tq + r % a.Tq;
     float x[F];
-    float amax = 0.f;
     const bool live = r < a.R;
+    uint32_t u[F / 2];
 #pragma unroll
     for (int c = 0; c < F / 8; ++c) {
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (live) u = __ldg(reinterpret_cast<const uint4*>(a.q + row * D + t * F) + c);
-      bf16x8_to_f32(u, x + 8 * c);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (live) v = __ldg(reinterpret_cast<const uint4*>(a.q + row * D + t * F) + c);
+      u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
     }
     if constexpr (PARTS == 2) {
-      if (live && pos >= 0) {
-        const bool second = t >= 2;   // features D/2.. pair with features 0..
-        const int f0 = t * F;
-        const float* cs = a.rope_cs + (long)pos * D + (second ? f0 - D / 2 : f0);
+      // features t F.. pair with those of lane t ^ 2; a row at a negative position sees no key: any angle will do
+      const int pos = max(w.len - a.Tq + r % a.Tq, 0);
+      const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (long)pos * D + (t & 1) * F);
+      const float sign = t < 2 ? -1.f : 1.f;
 #pragma unroll
-        for (int c = 0; c < F / 8; ++c) {
-          float y[8];
-          bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(a.q + row * D + (second ? f0 - D / 2 : f0 + D / 2)) + c), y);
+      for (int c = 0; c < F / 4; ++c) {
+        const float4 co = __ldg(cs + c), si = __ldg(cs + D / 8 + c);
+        const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float co = __ldg(cs + 8 * c + i), si = __ldg(cs + D / 2 + 8 * c + i);
-            x[8 * c + i] = second ? fmaf(x[8 * c + i], co, y[i] * si) : fmaf(x[8 * c + i], co, -y[i] * si);
-          }
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t y = __shfl_xor_sync(~0u, u[2 * c + i], 2);
+          x[4 * c + 2 * i] = fmaf(__uint_as_float(u[2 * c + i] << 16), cc[2 * i], sign * ss[2 * i] * __uint_as_float(y << 16));
+          x[4 * c + 2 * i + 1] = fmaf(__uint_as_float(u[2 * c + i] & 0xFFFF0000u), cc[2 * i + 1],
+                                      sign * ss[2 * i + 1] * __uint_as_float(y & 0xFFFF0000u));
         }
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < F / 2; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      }
     }
+    float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < F; ++i) amax = fmaxf(amax, fabsf(x[i]));
     amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
@@ -289,6 +311,7 @@ __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& 
     const int ex = (int)(__float_as_uint(amax) >> 23);          // biased exponent: 0 zero, 255 not finite
     const int sh = ex == 0 || ex == 255 ? 0 : 14 - (ex - 127);  // x * 2^sh, in two steps within f32's range
     const float s1 = __uint_as_float((uint32_t)(127 + sh / 2) << 23), s2 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
+    const float i1 = __uint_as_float((uint32_t)(127 - sh / 2) << 23), i2 = __uint_as_float((uint32_t)(127 - sh + sh / 2) << 23);
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -302,29 +325,28 @@ __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& 
         }
       }
     // the columns of S^T are rows 2t and 2t+1: their factors come from the lanes that hold those rows
-    const float mine = a.scale_log2 * (1.f / s1) * (1.f / s2);
+    const float mine = a.scale_log2 * i1 * i2;
     fac[n][0] = __shfl_sync(~0u, mine, 8 * t);
     fac[n][1] = __shfl_sync(~0u, mine, 8 * t + 4);
   }
 }
 
-// O and LSE of two rows (columns 2t, 2t+1 of 8-row tile n) from their sums and
+// O and LSE of two rows (2t, 2t+1 of the 8 from r0 on) from their sums and
 // a run of O^T's tiles: tile i holds features 2i, 2i+1 of the gD/8.. that a lane group has.
 template <int D, int TILES>
-__device__ __forceinline__ void write_rows(const DecodeQ4Args& a, int b, int k, int len, int rows_per, int n, int tile0,
+__device__ __forceinline__ void write_rows(const DecodeQ4Args& a, int b, int hkv, int r0, const int* lim, int tile0,
                                            const float (*acc)[4], const float* m, const float* lsum, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const int hkv = k / a.nrb, r0 = (k - hkv * a.nrb) * rows_per;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     float l = lsum[c];
     l += __shfl_xor_sync(~0u, l, 4);
     l += __shfl_xor_sync(~0u, l, 8);
     l += __shfl_xor_sync(~0u, l, 16);
-    const int r = r0 + n * 8 + 2 * t + c;
+    const int r = r0 + 2 * t + c;
     if (r >= a.R) continue;
     const long row = ((long)b * a.Hq + hkv * a.G) * a.Tq + r;
-    const bool empty = len - a.Tq + r % a.Tq < 0;      // the row sees no key
+    const bool empty = lim[c] < 0;      // the row sees no key
     const float inv = a.v_scale / l;
     if (!GQA_CHECK(row >= 0 && row < (long)a.B * a.Hq * a.Tq, a.status, a.dbg_line)) continue;
     __nv_bfloat16* o = a.o + row * D + g * (D / 8) + 2 * tile0;
@@ -340,6 +362,15 @@ __device__ __forceinline__ void write_rows(const DecodeQ4Args& a, int b, int k, 
     }
     if (g == 0 && tile0 == 0) a.lse[row] = empty ? -CUDART_INF_F : (m[c] - kOff + log2f(l)) * 0.69314718055994531f;
   }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void write_tile(const DecodeQ4Args& a, int b, int k, int len, int n, int tile,
+                                           const Combined<D>& x, int lane) {
+  const int hkv = k / a.nrb, r0 = (k - hkv * a.nrb) * 8 * NT + n * 8;
+  int lim[2];
+  row_limits(a, len, r0 + 2 * (lane & 3), lim);
+  write_rows<D, 1>(a, b, hkv, r0, lim, tile, &x.acc, x.m, x.l, lane);
 }
 
 // Workspace: a header per CTA, then two pieces per CTA (kRec * 32 f32 each):
@@ -470,7 +501,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   auto take_share = [&](int tiles) {
     total = tiles * upb;
     Wn = min(total, (int)gridDim.x * C::kWarps);
-    if (gw < Wn) g0 = share_begin(gw, total, Wn), g1 = share_begin(gw + 1, total, Wn);
+    if (gw < Wn) {
+      const Shares sh(total, Wn);
+      g0 = sh.begin(gw), g1 = sh.begin(gw + 1);
+    }
   };
   if (a.B > C::kThreads) {
     int mine = 0;
@@ -533,32 +567,35 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     ld.left = g1 - g0;
     ld.enter(a, g0 - cu.Pu);
     const uint32_t lane_dst = row_at<D>(lane / (D / 32), lane % (D / 32));
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) ld.issue(a, ring + i * C::kStage, lane, lane_dst);
-
     Piece4<D, NT> p;
     uint32_t qf[NT][PARTS][D / 16][2];
     float fac[NT][2], bias[NT][2];
     int lim[NT][2];                      // last key each of the thread's rows sees
-    uint32_t s = ring;                   // stage of the current tile, and the one before
-    uint32_t prev = ring + (C::kStages - 1) * C::kStage;
-    for (int at = g0;;) {                // a piece of unit cu, from tile `at` on
-      load_queries<D, NT, PARTS>(a, cu, lane, qf, fac);
-      p.clear();
-      const int r0 = (cu.k % a.nrb) * 8 * NT;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          lim[n][c] = cu.len - a.Tq + (r0 + n * 8 + 2 * t + c) % a.Tq;
-          bias[n][c] = CUDART_INF_F;     // kOff - m: any visible score makes the maximum move
-        }
-      const int end = min(cu.Pu + cu.nb, g1);
-      for (int j0 = (at - cu.Pu) * kTK, je = (end - cu.Pu) * kTK; j0 < je; j0 += kTK) {
+    int r0 = 0;
+    uint32_t s = ring;                   // stage of the current tile, and the one to fill
+    uint32_t fill = ring;
+    int at = g0;                         // the current piece: unit cu's tiles from stream index `at` on
+    // tile i of the share is consumed kStages - 1 rounds after its copies were issued
+    for (int i = g0 - (C::kStages - 1); i < g1; ++i) {
+      if (i >= g0) {
         asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-        __syncwarp();                    // every lane's copies have landed; the stage before is read
-        ld.issue(a, prev, lane, lane_dst);
-
+        __syncwarp();                    // every lane's copies have landed; the stage to fill is read
+      }
+      ld.issue(a, fill, lane, lane_dst);
+      fill = fill == ring + (C::kStages - 1) * C::kStage ? ring : fill + C::kStage;
+      if (i < g0) continue;
+      if (i == at) {
+        load_queries<D, NT, PARTS>(a, cu, lane, qf, fac);
+        p.clear();
+        r0 = (cu.k % a.nrb) * 8 * NT;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          row_limits(a, cu.len, r0 + n * 8 + 2 * t, lim[n]);
+          bias[n][0] = bias[n][1] = CUDART_INF_F;     // kOff - m: any visible score makes the maximum move
+        }
+      }
+      const int j0 = (i - cu.Pu) * kTK;
+      {
         // S^T of both 16-key groups
         float sc[2][NT][4];
 #pragma unroll
@@ -685,6 +722,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
               if ((sb[i] & 0x7f) == 0x7f) bad = true, sb[i] = 0;
             }
             if (__any_sync(~0u, bad)) {
+#pragma unroll 1
               for (int k = 0; k < 16; ++k) {
                 const uint32_t v = lds<1>(s + 2 * C::kCodes + C::kSf + (16 * G + k) * (D / 16) + (D == 128 ? g : g >> 1));
                 if ((v & 0x7f) != 0x7f) continue;
@@ -717,15 +755,16 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
             }
           }
         }
-        prev = s;
         s = s == ring + (C::kStages - 1) * C::kStage ? ring : s + C::kStage;
       }
+      const bool unit_end = i + 1 == cu.Pu + cu.nb;
+      if (!unit_end && i + 1 < g1) continue;
 
       // the piece is done: written if it is its whole unit, else stored
-      if (end == cu.Pu + cu.nb && cu.Pu >= g0) {
+      if (unit_end && cu.Pu >= g0) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          write_rows<D, C::kMT>(a, cu.b, cu.k, cu.len, 8 * NT, n, 0, p.acc[n], p.m[n], p.l[n], lane);
+          write_rows<D, C::kMT>(a, cu.b, cu.k / a.nrb, r0 + 8 * n, lim[n], 0, p.acc[n], p.m[n], p.l[n], lane);
       } else {
         const int slot = 2 * warp + (cu.Pu < g0 ? 0 : 1);   // a unit begun before the share, or continued after it
         if (slot & 1) {   // the share ends here: no copy is in flight, and every lane has read the last tile
@@ -735,12 +774,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
         p.store(piece_at<D, NT>(smem, slot), lane);
         if (lane == 0) {
           rec_unit[slot] = cu;
-          rec_end[slot] = end;
+          rec_end[slot] = i + 1;
         }
       }
-      if (end == g1) break;
-      at = end;
-      cu.next(a);
+      at = i + 1;
+      if (at < g1) cu.next(a);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
@@ -748,7 +786,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   griddep_launch();
 
   // Combine the stored pieces of each unit, in stream order; the warps share the unit's 16-feature tiles.
-  const int c0 = share_begin(min((int)blockIdx.x * C::kWarps, Wn), total, max(Wn, 1));   // the CTA's share
+  const Shares sh(total, max(Wn, 1));
+  const int c0 = sh.begin(min((int)blockIdx.x * C::kWarps, Wn));   // first tile of the CTA's share
   Q4Head* heads = static_cast<Q4Head*>(a.ws);
   float* parts = reinterpret_cast<float*>(heads + kMaxCtas);
   Q4Head head{};
@@ -778,7 +817,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
       x.from([&](int j) -> const float* { return piece_at<D, NT>(smem, __shfl_sync(~0u, nth, rank + j)); }, __popc(slots), n,
              i, lane);
       if (whole) {
-        write_rows<D, 1>(a, u.b, u.k, u.len, 8 * NT, n, i, &x.acc, x.m, x.l, lane);
+        write_tile<D, NT>(a, u.b, u.k, u.len, n, i, x, lane);
       } else {
         float* q = parts + ((long)blockIdx.x * 2 + slot) * C::kRec * 32 + n * Piece4<D, NT>::kPer * 32 + lane;
 #pragma unroll
@@ -796,8 +835,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
       head.b = u.b;
       head.k = u.k;
       head.len = u.len;
-      head.first = owner_of(u.Pu, total, Wn) / C::kWarps;
-      head.last = owner_of(u.Pu + u.nb - 1, total, Wn) / C::kWarps;
+      head.first = sh.owner(u.Pu) / C::kWarps;
+      head.last = sh.owner(u.Pu + u.nb - 1) / C::kWarps;
     }
   }
   if (tid == 0) heads[blockIdx.x] = head;
@@ -817,7 +856,7 @@ __global__ void __launch_bounds__(32 * NT * D / 16) decode_q4_merge(const Decode
   auto at = [&](int i) -> const float* { return parts + ((long)(h.first + i) * 2 + (i == 0)) * C::kRec * 32; };
   Combined<D> x;
   x.from(at, h.last - h.first + 1, tt / C::kMT, tt % C::kMT, lane);
-  write_rows<D, 1>(a, h.b, h.k, h.len, 8 * NT, tt / C::kMT, tt % C::kMT, &x.acc, x.m, x.l, lane);
+  write_tile<D, NT>(a, h.b, h.k, h.len, tt / C::kMT, tt % C::kMT, x, lane);
 }
 
 template <int D, int NT, int PARTS>
