@@ -488,6 +488,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   __shared__ int prefix[C::kThreads];
   __shared__ Unit rec_unit[2 * C::kWarps];   // unit of each stored piece
   __shared__ int rec_end[2 * C::kWarps];     // stream index after the piece; 0: none
+  __shared__ uint8_t order[C::kWarps][2 * C::kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int upb = a.Hkv * a.nrb;
@@ -567,6 +568,16 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     ld.left = g1 - g0;
     ld.enter(a, g0 - cu.Pu);
     const uint32_t lane_dst = row_at<D>(lane / (D / 32), lane % (D / 32));
+    // the lane's bytes in a stage: of K rows pi(g) (+ 8, 16, 24) and of V rows pi(2t), pi(2t + 1)
+    const uint32_t k_at = row_at<D>(key_of(g), D == 128 ? t : 0) + (D == 128 ? 0 : 8 * t);
+    const uint32_t ks_at = 2 * C::kCodes + key_of(g) * (D / 16) + (D == 128 ? 2 * t : t);
+    uint32_t v_at[2], vs_at[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int key = key_of(2 * t + e);
+      v_at[e] = C::kCodes + row_at<D>(key, D == 128 ? g >> 1 : 0) + (D == 128 ? 8 * (g & 1) : 4 * g);
+      vs_at[e] = 2 * C::kCodes + C::kSf + key * (D / 16) + (D == 128 ? g : g >> 1);
+    }
     Piece4<D, NT> p;
     uint32_t qf[NT][PARTS][D / 16][2];
     float fac[NT][2], bias[NT][2];
@@ -575,16 +586,13 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     uint32_t s = ring;                   // stage of the current tile, and the one to fill
     uint32_t fill = ring;
     int at = g0;                         // the current piece: unit cu's tiles from stream index `at` on
-    // tile i of the share is consumed kStages - 1 rounds after its copies were issued
+    // a round issues the copies of the tile kStages - 1 ahead, then takes tile i
     for (int i = g0 - (C::kStages - 1); i < g1; ++i) {
-      if (i >= g0) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-        __syncwarp();                    // every lane's copies have landed; the stage to fill is read
-      }
+      __syncwarp();                      // the stage to fill is read
       ld.issue(a, fill, lane, lane_dst);
       fill = fill == ring + (C::kStages - 1) * C::kStage ? ring : fill + C::kStage;
       if (i < g0) continue;
-      if (i == at) {
+      if (i == at) {                     // while the copies are in flight
         load_queries<D, NT, PARTS>(a, cu, lane, qf, fac);
         p.clear();
         r0 = (cu.k % a.nrb) * 8 * NT;
@@ -594,6 +602,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
           bias[n][0] = bias[n][1] = CUDART_INF_F;     // kOff - m: any visible score makes the maximum move
         }
       }
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
+      __syncwarp();                      // every lane's copies of tile i have landed
       const int j0 = (i - cu.Pu) * kTK;
       {
         // S^T of both 16-key groups
@@ -602,20 +612,22 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
         for (int G = 0; G < 2; ++G) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) sc[G][n][0] = sc[G][n][1] = sc[G][n][2] = sc[G][n][3] = 0.f;
-          const int ka = 16 * G + key_of(g), kb = ka + 8;
+          // row_at's swizzle repeats every 8 keys: the rows 8 and 16 further on are at fixed distances
+          const uint32_t ka = s + k_at + G * 16 * (D / 2), kb = ka + 8 * (D / 2);
+          const uint32_t fa_at = s + ks_at + G * D, fb_at = fa_at + D / 2;
           uint32_t wa[D / 32], wb[D / 32];
           uint32_t sa, sb;               // block scales as f16 pairs: (first, second) 16 features, D = 64: one
           if constexpr (D == 128) {
-            const uint4 u = ld_shared_v4(s + row_at<D>(ka, t)), v = ld_shared_v4(s + row_at<D>(kb, t));
+            const uint4 u = ld_shared_v4(ka), v = ld_shared_v4(kb);
             wa[0] = u.x, wa[1] = u.y, wa[2] = u.z, wa[3] = u.w;
             wb[0] = v.x, wb[1] = v.y, wb[2] = v.z, wb[3] = v.w;
-            sa = e4m3x2_to_f16(lds<2>(s + 2 * C::kCodes + ka * 8 + 2 * t));
-            sb = e4m3x2_to_f16(lds<2>(s + 2 * C::kCodes + kb * 8 + 2 * t));
+            sa = e4m3x2_to_f16(lds<2>(fa_at));
+            sb = e4m3x2_to_f16(lds<2>(fb_at));
           } else {
-            lds64(s + row_at<D>(ka, 0) + 8 * t, wa);
-            lds64(s + row_at<D>(kb, 0) + 8 * t, wb);
-            sa = e4m3x2_to_f16(lds<1>(s + 2 * C::kCodes + ka * 4 + t));
-            sb = e4m3x2_to_f16(lds<1>(s + 2 * C::kCodes + kb * 4 + t));
+            lds64(ka, wa);
+            lds64(kb, wb);
+            sa = e4m3x2_to_f16(lds<1>(fa_at));
+            sb = e4m3x2_to_f16(lds<1>(fb_at));
           }
 #pragma unroll
           for (int w = 0; w < D / 32; ++w) {     // 8 features: two MMAs
@@ -708,10 +720,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
           uint32_t w[4][VW];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {              // keys pi(2t), pi(2t+1), pi(2t+8), pi(2t+9)
-            const int key = 16 * G + 8 * (i >> 1) + key_of(2 * t + (i & 1));
-            if constexpr (D == 128) lds64(s + C::kCodes + row_at<D>(key, g >> 1) + 8 * (g & 1), w[i]);
-            else w[i][0] = lds<4>(s + C::kCodes + row_at<D>(key, 0) + 4 * g);
-            sb[i] = lds<1>(s + 2 * C::kCodes + C::kSf + key * (D / 16) + (D == 128 ? g : g >> 1));
+            const uint32_t at_v = s + v_at[i & 1] + (16 * G + 8 * (i >> 1)) * (D / 2);
+            if constexpr (D == 128) lds64(at_v, w[i]);
+            else w[i][0] = lds<4>(at_v);
+            sb[i] = lds<1>(s + vs_at[i & 1] + (16 * G + 8 * (i >> 1)) * (D / 16));
           }
           if (edge && a.Tq > 1) {
             // a NaN block at a key that some rows do not see: 0 * NaN would reach them through the MMA, so it is
@@ -800,9 +812,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   const unsigned earlier = taken & ((1u << lane) - 1);
   const int prev_Pu = __shfl_sync(~0u, my_Pu, earlier ? 31 - __clz(earlier) : lane);
   const unsigned begins = __ballot_sync(~0u, my_end > 0 && (!earlier || prev_Pu != my_Pu));
-  unsigned rest = taken;
-  for (int i = 0; i < lane; ++i) rest &= rest - 1;
-  const int nth = __ffs(rest) - 1;          // lane i: the i-th slot taken
+  if (my_end > 0) order[warp][__popc(earlier)] = (uint8_t)lane;   // the slots taken, in stream order
+  __syncwarp();
   for (unsigned todo = begins; todo;) {
     const int s0 = __ffs(todo) - 1;
     todo &= todo - 1;
@@ -814,8 +825,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     for (int tt = warp; tt < NT * C::kMT; tt += C::kWarps) {
       const int n = tt / C::kMT, i = tt % C::kMT;
       Combined<D> x;
-      x.from([&](int j) -> const float* { return piece_at<D, NT>(smem, __shfl_sync(~0u, nth, rank + j)); }, __popc(slots), n,
-             i, lane);
+      x.from([&](int j) -> const float* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, __popc(slots), n, i, lane);
       if (whole) {
         write_tile<D, NT>(a, u.b, u.k, u.len, n, i, x, lane);
       } else {
