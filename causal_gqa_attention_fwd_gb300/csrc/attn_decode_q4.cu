@@ -29,12 +29,14 @@
 // the second product's by two 8x8 transpositions (movmatrix).
 //
 // Work: units (batch row, K/V head, block of 8*NT query rows) of 32-key tiles
-// form one stream; warp w of all W takes tiles [wC/W, (w+1)C/W), each with a
-// ring of its own in shared memory that it fills by cp.async, kStages - 1
-// tiles ahead, across units.  No warp waits for another until the end: a unit
-// inside one warp's share is written directly; pieces of a unit cut between
-// warps of a CTA are combined through shared memory, those of a unit cut
-// between CTAs through the workspace by decode_q4_merge.
+// form one stream that is shared out evenly over the grid's warps, each unit
+// counting kUnitCost tiles more than it has (its queries have to be loaded,
+// its output written).  Each warp has a ring of its own in shared memory that
+// it fills by cp.async, kStages - 1 tiles ahead, across units.  No warp waits
+// for another until the end: a unit inside one warp's share is written
+// directly; pieces of a unit cut between warps of a CTA are combined through
+// shared memory, those of a unit cut between CTAs through the workspace by
+// decode_q4_merge.
 #include <math_constants.h>
 
 #include "cache_ops.h"
@@ -47,6 +49,8 @@ namespace {
 
 constexpr int kTK = 32;        // keys per tile
 constexpr int kMaxCtas = 160;  // CTAs the workspace holds pieces for
+constexpr int kUnitCost = 2;   // what a unit costs beside its tiles, in tiles
+constexpr int kMinWarps = 4;   // warps a CTA uses before the work goes to another SM
 constexpr float kLazy = 8.f;   // the maximum moves when it would grow by more than 2^8 ...
 constexpr float kOff = 7.f;    // ... and P is scaled by 2^7, so P <= 2^15 and f16's smallest step is 2^-31 of a row's largest P
 
@@ -103,50 +107,56 @@ struct Piece4 {
   }
 };
 
-// One 16-feature tile of 8 rows of a unit, combined from `count` stored pieces;
-// at(i) is piece i's base.  Several pieces' loads are in flight at a time.
+// One 16-feature tile of 8 rows of a unit, combined from stored pieces with a
+// running maximum; the loads of kBatch pieces are in flight at a time.
 template <int D>
 struct Combined {
   float acc[4], m[2], l[2];
+  __device__ __forceinline__ void clear() {
+    m[0] = m[1] = -CUDART_INF_F;
+    l[0] = l[1] = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+  }
+  // pieces first, first + step, ... below count; at(i) is piece i's base
   template <typename At>
-  __device__ __forceinline__ void from(At at, int count, int n, int tile, int lane) {
+  __device__ __forceinline__ void add(At at, int first, int step, int count, int n, int tile, int lane) {
     constexpr int kPer = D / 16 * 4 + 4, kBatch = 4;
     const int base = n * kPer * 32 + lane;
-    m[0] = m[1] = -CUDART_INF_F;
-    for (int i = 0; i < count; i += kBatch) {
-      float x[kBatch][2];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const float* p = at(min(i + u, count - 1)) + base;
-        x[u][0] = p[32 * (D / 4)], x[u][1] = p[32 * (D / 4 + 1)];
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) m[0] = fmaxf(m[0], x[u][0]), m[1] = fmaxf(m[1], x[u][1]);
-    }
-    l[0] = l[1] = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-    for (int i = 0; i < count; i += kBatch) {
+    for (int i = first; i < count; i += kBatch * step) {
       float x[kBatch][8];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const float* p = at(min(i + u, count - 1)) + base;
+        const float* p = at(min(i + u * step, count - 1)) + base;
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[u][j] = p[32 * (4 * tile + j)];
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[u][4 + j] = p[32 * (D / 4 + j)];
       }
+      float top[2] = {m[0], m[1]};
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (i + u >= count) break;
+      for (int u = 0; u < kBatch; ++u)
+        if (i + u * step < count) top[0] = fmaxf(top[0], x[u][4]), top[1] = fmaxf(top[1], x[u][5]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          // a piece whose maximum is -infinity holds zeros (or NaN, which is kept)
-          const float f = x[u][4 + c] == -CUDART_INF_F ? 1.f : ex2_approx(x[u][4 + c] - m[c]);
-          l[c] = fmaf(x[u][6 + c], f, l[c]);
-          acc[c] = fmaf(x[u][c], f, acc[c]);
-          acc[2 + c] = fmaf(x[u][2 + c], f, acc[2 + c]);
+      for (int c = 0; c < 2; ++c) scale_to(c, top[c]);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i + u * step < count) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) accumulate(c, x[u][4 + c], x[u][6 + c], x[u][c], x[u][2 + c]);
         }
-      }
     }
+  }
+  __device__ __forceinline__ void scale_to(int c, float top) {
+    const float f = m[c] == -CUDART_INF_F ? 1.f : ex2_approx(m[c] - top);   // zeros so far (or NaN, which is kept)
+    m[c] = top;
+    l[c] *= f;
+    acc[c] *= f;
+    acc[2 + c] *= f;
+  }
+  __device__ __forceinline__ void accumulate(int c, float mp, float lp, float x0, float x1) {   // mp <= m[c]
+    const float f = mp == -CUDART_INF_F ? 1.f : ex2_approx(mp - m[c]);
+    l[c] = fmaf(lp, f, l[c]);
+    acc[c] = fmaf(x0, f, acc[c]);
+    acc[2 + c] = fmaf(x1, f, acc[2 + c]);
   }
 };
 
@@ -157,7 +167,9 @@ __device__ __forceinline__ int row_tiles(const DecodeQ4Args& a, int b, int& len)
   return len < 0 || len > a.S ? 0 : len == 0 ? 1 : (len + kTK - 1) / kTK;
 }
 
-// The shares of all C tiles (C < 2^31): warps 0..G-1 of the grid take C / G tiles each, the first C % G one more.
+// The stream's positions: each unit has kUnitCost that stand for no tile, then
+// one a tile.  All C of them (C < 2^31) are shared out: warps 0..G-1 take C / G
+// each, the first C % G one more.
 struct Shares {
   int q, r;
   __device__ __forceinline__ Shares(int C, int G) : q(C / G), r(C - C / G * G) {}
@@ -170,16 +182,19 @@ struct Shares {
 
 // A unit of the stream.
 struct Unit {
-  int Pu;          // stream index of its first tile
+  int P;           // position of its first tile
   int nb;          // its tiles
   int b, k;        // batch row, unit within it (hkv * nrb + row block)
   int len;         // keys of the row
   __device__ __forceinline__ void next(const DecodeQ4Args& a) {
-    Pu += nb;
+    P += nb + kUnitCost;
     if (++k < a.Hkv * a.nrb) return;
     k = 0;
     do {
-      if (++b >= a.B) return;     // past the last unit
+      if (++b >= a.B) {             // past the last unit
+        P = 0x7fffffff;
+        return;
+      }
       nb = row_tiles(a, b, len);
     } while (nb == 0);
   }
@@ -373,11 +388,11 @@ __device__ __forceinline__ void write_tile(const DecodeQ4Args& a, int b, int k, 
   write_rows<D, 1>(a, b, hkv, r0, lim, tile, &x.acc, x.m, x.l, lane);
 }
 
-// Workspace: a header per CTA, then two pieces per CTA (kRec * 32 f32 each):
-// 0 of the unit begun before the CTA's share, 1 of the one that goes on after it.
+// Workspace: a header per CTA, then two pieces a CTA (kRec * 32 f32 each): 0 of
+// the unit begun before the CTA's share, 1 of the one that goes on after it.
 struct Q4Head {
-  int b, k, len;   // unit of the CTA's first piece
-  int first, last; // CTAs that hold pieces of it, first = -1: not cut before this CTA
+  int b, k, len;   // the unit begun before the CTA's share
+  int first, last; // CTAs that hold pieces of it; first = -1: there is none
   int pad[3];
 };
 
@@ -386,46 +401,58 @@ template <int D, int NT>
 struct Loader {
   using C = Q4Cfg<D, NT>;
   Unit u;
-  int left;            // tiles of the share not yet issued
-  int tiles;           // of the unit's tiles, those from the current one on
+  int end;             // end of the share
+  bool more;           // tiles left to issue
+  int tiles;           // of the unit's tiles in the share, those from the current one on
   int keys;            // keys from the current tile on
   int pidx, inpg;      // paged: block-table index and row in the page of the tile
-  int page[2];         // pages of its two 16-key halves
+  int pbase;           // lane i holds block-table entries pbase + i and pbase + 32 + i
+  int entry[2];
   long base;           // contiguous: cache row of the tile
 
-  __device__ __forceinline__ void look_up(const DecodeQ4Args& a) {
-    const int* bt = a.block_table + (long)u.b * a.max_pages + pidx;
-    page[0] = keys > 0 ? __ldg(bt) : 0;
-    page[1] = a.page_size != 16 ? page[0] : keys > 16 ? __ldg(bt + 1) : 0;
+  __device__ __forceinline__ int load_entry(const DecodeQ4Args& a, int e) const {   // only pages that hold keys are looked up
+    return (long)e * a.page_size < u.len ? __ldg(a.block_table + (long)u.b * a.max_pages + e) : 0;
   }
-  __device__ __forceinline__ void enter(const DecodeQ4Args& a, int tile) {   // the unit's tile `tile`
+  // the unit's tile `tile`, if the share reaches it
+  __device__ __forceinline__ void enter(const DecodeQ4Args& a, int tile, int lane) {
+    tiles = min(u.nb, end - u.P) - tile;
+    more = tiles > 0;
+    if (!more) return;
     const int j = tile * kTK;
-    tiles = u.nb - tile;
     keys = u.len - j;
+    const int hkv = u.k / a.nrb;
     if (a.block_table) {
-      pidx = j / a.page_size;
+      pidx = pbase = j / a.page_size;
       inpg = j - pidx * a.page_size;
-      look_up(a);
+      entry[0] = load_entry(a, pbase + lane);
+      entry[1] = load_entry(a, pbase + 32 + lane);
     } else {
-      base = ((long)u.b * a.Hkv + u.k / a.nrb) * a.S + j;
+      base = ((long)u.b * a.Hkv + hkv) * a.S + j;
     }
+    // its queries, and the rotary rows of their positions, towards L2
+    const int r0 = (u.k - hkv * a.nrb) * 8 * NT, n = min(8 * NT, a.R - r0) * D * 2;
+    const char* q = reinterpret_cast<const char*>(a.q + (((long)u.b * a.Hq + hkv * a.G) * a.Tq + r0) * D);
+    if (lane * 128 < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
+    const int pos = u.len - a.Tq + (lane >> 2);
+    if (a.rope_cs && (lane >> 2) < a.Tq && pos >= 0 && (lane & 3) < D / 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope_cs + (long)pos * D + (lane & 3) * 32));
   }
   // lane_dst: the lane's byte in a stage's codes; lane = its 16-byte chunk of 512 bytes
   __device__ __forceinline__ void issue(const DecodeQ4Args& a, uint32_t s, int lane, uint32_t lane_dst) {
-    if (left > 0) {
+    if (more) {
       constexpr int CH = D / 32;            // 16-byte chunks of a key's codes; a copy covers 32 / CH keys
       long row[2];                          // cache row of the tile's key 0, as seen from each half
       bool ok[2] = {true, true};
       if (a.block_table) {
         const int hkv = u.k / a.nrb;
+        const int page[2] = {__shfl_sync(~0u, entry[0], pidx - pbase), __shfl_sync(~0u, entry[0], (pidx - pbase + 1) & 31)};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if ((unsigned)page[h] >= (unsigned)a.num_pages) {
-            if (lane == 0 && keys > 16 * h) atomicCAS(a.status, 0, kDevBadPage);
-            ok[h] = false;
-            page[h] = 0;
-          }
-          row[h] = ((long)page[h] * a.Hkv + hkv) * a.page_size + (a.page_size == 16 ? -16 * h : inpg);
+          const bool wide = a.page_size != 16;        // both halves in one page
+          const int pg = wide ? page[0] : page[h];
+          ok[h] = (unsigned)pg < (unsigned)a.num_pages || keys <= 16 * h;
+          if (!ok[h] && lane == 0) atomicCAS(a.status, 0, kDevBadPage);
+          row[h] = ((long)(ok[h] ? pg : 0) * a.Hkv + hkv) * a.page_size + (wide ? inpg : -16 * h);
         }
       } else {
         row[0] = row[1] = base;
@@ -457,28 +484,32 @@ struct Loader {
         cp_async_small<D / 16>(s + 2 * C::kCodes + lane * (D / 16), a.ksf + f, valid);
         cp_async_small<D / 16>(s + 2 * C::kCodes + C::kSf + lane * (D / 16), a.vsf + f, valid);
       }
-      if (--left > 0) {
-        if (--tiles > 0) {
-          keys -= kTK;
-          if (a.block_table) {
-            inpg += kTK;
-            if (inpg >= a.page_size) {
-              pidx += a.page_size == 16 ? 2 : 1;
-              inpg = 0;
-              look_up(a);
+      if (--tiles > 0) {
+        keys -= kTK;
+        if (a.block_table) {
+          inpg += kTK;
+          if (inpg >= a.page_size) {
+            pidx += a.page_size == 16 ? 2 : 1;
+            inpg = 0;
+            if (pidx >= pbase + 32) {
+              pbase += 32;
+              entry[0] = entry[1];
+              entry[1] = load_entry(a, pbase + 32 + lane);
             }
-          } else {
-            base += kTK;
           }
         } else {
-          u.next(a);
-          enter(a, 0);
+          base += kTK;
         }
+      } else {
+        u.next(a);
+        enter(a, 0, lane);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
 };
+
+constexpr int kStored = 1, kFirst = 2, kLast = 4;
 
 template <int D, int NT, int PARTS>
 __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(const DecodeQ4Args a) {
@@ -487,32 +518,36 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   __shared__ int sums[C::kWarps];
   __shared__ int prefix[C::kThreads];
   __shared__ Unit rec_unit[2 * C::kWarps];   // unit of each stored piece
-  __shared__ int rec_end[2 * C::kWarps];     // stream index after the piece; 0: none
+  __shared__ int rec_kind[2 * C::kWarps];    // kStored, with kFirst / kLast if it has the unit's first / last tile; 0: none
   __shared__ uint8_t order[C::kWarps][2 * C::kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int upb = a.Hkv * a.nrb;
 
-  if (tid < 2 * C::kWarps) rec_end[tid] = 0;
-  // The tiles of all units, and the batch row that holds tile g0: inclusive
-  // sums of the rows' tiles, kThreads rows at a time (more rows: a pass for the total first).
-  int total = 0, Wn = 0, g0 = 0, g1 = 0, before = 0;
-  const int gw = blockIdx.x * C::kWarps + warp;
+  griddep_launch();                          // the merge waits for this grid's end in any case
+  if (tid < 2 * C::kWarps) rec_kind[tid] = 0;
+  // The positions of all units, and the batch row that holds the share's first:
+  // inclusive sums over the rows, kThreads rows at a time (more rows: a pass for the total first).
+  int total = 0, Wn = 0, wpc = 1, v0 = 0, v1 = 0, before = 0;
   Unit cu{0, 0, -1, 0, 0};
-  auto take_share = [&](int tiles) {
-    total = tiles * upb;
-    Wn = min(total, (int)gridDim.x * C::kWarps);
-    if (gw < Wn) {
+  auto positions = [&](int b) {
+    int len;
+    const int nb = row_tiles(a, b, len);
+    return nb ? nb + kUnitCost : 0;
+  };
+  auto take_share = [&](int sum) {
+    total = sum * upb;
+    wpc = min(max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinWarps), C::kWarps);
+    Wn = min(total, (int)gridDim.x * wpc);
+    const int gw = blockIdx.x * wpc + warp;
+    if (warp < wpc && gw < Wn) {
       const Shares sh(total, Wn);
-      g0 = sh.begin(gw), g1 = sh.begin(gw + 1);
+      v0 = sh.begin(gw), v1 = sh.begin(gw + 1);
     }
   };
   if (a.B > C::kThreads) {
     int mine = 0;
-    for (int b = tid; b < a.B; b += C::kThreads) {
-      int len;
-      mine += row_tiles(a, b, len);
-    }
+    for (int b = tid; b < a.B; b += C::kThreads) mine += positions(b);
     mine = __reduce_add_sync(~0u, mine);
     if (lane == 0) sums[warp] = mine;
     __syncthreads();
@@ -522,9 +557,9 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     take_share(all);
   }
   for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
-    int len = 0, inc = 0;
+    int inc = 0;
     if (b0 + tid < a.B) {
-      inc = row_tiles(a, b0 + tid, len);
+      inc = positions(b0 + tid);
       if (inc == 0 && blockIdx.x == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
     }
 #pragma unroll
@@ -544,8 +579,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     prefix[tid] = inc;
     __syncthreads();
     if (a.B <= C::kThreads) take_share(all);
-    if (g0 < g1 && cu.b < 0 && g0 < (before + all) * upb) {
-      const int x = g0 - before * upb;   // row i of these: prefix[i - 1] * upb <= x < prefix[i] * upb
+    if (v0 < v1 && cu.b < 0 && v0 < (before + all) * upb) {
+      const int x = v0 - before * upb;   // row i of these: prefix[i - 1] * upb <= x < prefix[i] * upb
       int lo = 0, hi = min(C::kThreads, a.B - b0) - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -555,18 +590,20 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
       cu.b = b0 + lo;
       cu.nb = row_tiles(a, cu.b, cu.len);
       const int P = (before + (lo ? prefix[lo - 1] : 0)) * upb;
-      cu.k = (g0 - P) / cu.nb;
-      cu.Pu = P + cu.k * cu.nb;
+      cu.k = (v0 - P) / (cu.nb + kUnitCost);
+      cu.P = P + cu.k * (cu.nb + kUnitCost) + kUnitCost;
     }
     before += all;
   }
 
-  if (g0 < g1) {
+  // the share's tiles [ct, te) of its first unit
+  int ct = max(v0 - cu.P, 0), te = min(cu.nb, v1 - cu.P);
+  if (v0 < v1 && ct < te) {
     const uint32_t ring = smem_u32(smem + warp * C::kRing);
     Loader<D, NT> ld;
     ld.u = cu;
-    ld.left = g1 - g0;
-    ld.enter(a, g0 - cu.Pu);
+    ld.end = v1;
+    ld.enter(a, ct, lane);
     const uint32_t lane_dst = row_at<D>(lane / (D / 32), lane % (D / 32));
     // the lane's bytes in a stage: of K rows pi(g) (+ 8, 16, 24) and of V rows pi(2t), pi(2t + 1)
     const uint32_t k_at = row_at<D>(key_of(g), D == 128 ? t : 0) + (D == 128 ? 0 : 8 * t);
@@ -585,14 +622,17 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     int r0 = 0;
     uint32_t s = ring;                   // stage of the current tile, and the one to fill
     uint32_t fill = ring;
-    int at = g0;                         // the current piece: unit cu's tiles from stream index `at` on
-    // a round issues the copies of the tile kStages - 1 ahead, then takes tile i
-    for (int i = g0 - (C::kStages - 1); i < g1; ++i) {
+    int ta = ct;                         // the current piece: unit cu's tiles [ta, te)
+    // a round issues the copies of the tile kStages - 1 ahead, then takes a tile
+    for (int lead = C::kStages - 1;;) {
       __syncwarp();                      // the stage to fill is read
       ld.issue(a, fill, lane, lane_dst);
       fill = fill == ring + (C::kStages - 1) * C::kStage ? ring : fill + C::kStage;
-      if (i < g0) continue;
-      if (i == at) {                     // while the copies are in flight
+      if (lead > 0) {
+        --lead;
+        continue;
+      }
+      if (ct == ta) {                    // while the copies are in flight
         load_queries<D, NT, PARTS>(a, cu, lane, qf, fac);
         p.clear();
         r0 = (cu.k % a.nrb) * 8 * NT;
@@ -604,7 +644,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
       }
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
       __syncwarp();                      // every lane's copies of tile i have landed
-      const int j0 = (i - cu.Pu) * kTK;
+      const int j0 = ct * kTK;
       {
         // S^T of both 16-key groups
         float sc[2][NT][4];
@@ -769,16 +809,15 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
         }
         s = s == ring + (C::kStages - 1) * C::kStage ? ring : s + C::kStage;
       }
-      const bool unit_end = i + 1 == cu.Pu + cu.nb;
-      if (!unit_end && i + 1 < g1) continue;
+      if (++ct < te) continue;
 
       // the piece is done: written if it is its whole unit, else stored
-      if (unit_end && cu.Pu >= g0) {
+      if (ta == 0 && te == cu.nb) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           write_rows<D, C::kMT>(a, cu.b, cu.k / a.nrb, r0 + 8 * n, lim[n], 0, p.acc[n], p.m[n], p.l[n], lane);
       } else {
-        const int slot = 2 * warp + (cu.Pu < g0 ? 0 : 1);   // a unit begun before the share, or continued after it
+        const int slot = 2 * warp + (ta == 0);   // a unit begun before the share, or continued after it
         if (slot & 1) {   // the share ends here: no copy is in flight, and every lane has read the last tile
           asm volatile("cp.async.wait_group 0;" ::: "memory");
           __syncwarp();
@@ -786,50 +825,49 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
         p.store(piece_at<D, NT>(smem, slot), lane);
         if (lane == 0) {
           rec_unit[slot] = cu;
-          rec_end[slot] = i + 1;
+          rec_kind[slot] = kStored | (ta == 0 ? kFirst : 0) | (te == cu.nb ? kLast : 0);
         }
       }
-      at = i + 1;
-      if (at < g1) cu.next(a);
+      cu.next(a);
+      ct = ta = 0;
+      te = min(cu.nb, v1 - cu.P);
+      if (te <= 0) break;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   __syncthreads();
-  griddep_launch();
 
   // Combine the stored pieces of each unit, in stream order; the warps share the unit's 16-feature tiles.
-  const Shares sh(total, max(Wn, 1));
-  const int c0 = sh.begin(min((int)blockIdx.x * C::kWarps, Wn));   // first tile of the CTA's share
+  static_assert(2 * C::kWarps <= 32, "a lane per slot");   // lane s looks after slot s
+  const int kind = lane < 2 * C::kWarps ? rec_kind[lane] : 0;
+  const unsigned taken = __ballot_sync(~0u, kind);
+  const unsigned earlier = taken & ((1u << lane) - 1);
+  const int my_P = kind ? rec_unit[lane].P : -1;
+  const int prev_P = __shfl_sync(~0u, my_P, earlier ? 31 - __clz(earlier) : lane);
+  const unsigned begins = __ballot_sync(~0u, kind && (!earlier || prev_P != my_P));
+  if (kind) order[warp][__popc(earlier)] = (uint8_t)lane;   // the slots taken, in stream order
+  __syncwarp();
   Q4Head* heads = static_cast<Q4Head*>(a.ws);
-  float* parts = reinterpret_cast<float*>(heads + kMaxCtas);
+  float* pieces = reinterpret_cast<float*>(heads + kMaxCtas);
   Q4Head head{};
   head.first = -1;
-  // Lane s looks after slot s: which are taken, and which of them begin a unit.
-  static_assert(2 * C::kWarps <= 32, "a lane per slot");
-  const int my_end = lane < 2 * C::kWarps ? rec_end[lane] : 0;
-  const int my_Pu = my_end ? rec_unit[lane].Pu : -1;
-  const unsigned taken = __ballot_sync(~0u, my_end > 0);
-  const unsigned earlier = taken & ((1u << lane) - 1);
-  const int prev_Pu = __shfl_sync(~0u, my_Pu, earlier ? 31 - __clz(earlier) : lane);
-  const unsigned begins = __ballot_sync(~0u, my_end > 0 && (!earlier || prev_Pu != my_Pu));
-  if (my_end > 0) order[warp][__popc(earlier)] = (uint8_t)lane;   // the slots taken, in stream order
-  __syncwarp();
   for (unsigned todo = begins; todo;) {
     const int s0 = __ffs(todo) - 1;
     todo &= todo - 1;
     const unsigned slots = taken & ~((1u << s0) - 1) & (todo ? (todo & -todo) - 1 : ~0u);   // up to the next unit's
     const Unit u = rec_unit[s0];
-    const bool whole = u.Pu >= c0 && rec_end[31 - __clz(slots)] == u.Pu + u.nb;
-    const int slot = u.Pu < c0 ? 0 : 1;   // begun before the CTA's share, or in it
+    const bool first = rec_kind[s0] & kFirst, last = rec_kind[31 - __clz(slots)] & kLast;
     const int rank = __popc(taken & ((1u << s0) - 1));
     for (int tt = warp; tt < NT * C::kMT; tt += C::kWarps) {
       const int n = tt / C::kMT, i = tt % C::kMT;
       Combined<D> x;
-      x.from([&](int j) -> const float* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, __popc(slots), n, i, lane);
-      if (whole) {
+      x.clear();
+      x.add([&](int j) -> const float* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, 0, 1, __popc(slots), n, i,
+            lane);
+      if (first && last) {
         write_tile<D, NT>(a, u.b, u.k, u.len, n, i, x, lane);
       } else {
-        float* q = parts + ((long)blockIdx.x * 2 + slot) * C::kRec * 32 + n * Piece4<D, NT>::kPer * 32 + lane;
+        float* q = pieces + ((long)blockIdx.x * 2 + first) * C::kRec * 32 + n * Piece4<D, NT>::kPer * 32 + lane;
 #pragma unroll
         for (int j = 0; j < 4; ++j) q[32 * (4 * i + j)] = x.acc[j];
         if (i == 0) {
@@ -841,32 +879,61 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
         }
       }
     }
-    if (!whole && slot == 0) {
-      head.b = u.b;
-      head.k = u.k;
-      head.len = u.len;
-      head.first = sh.owner(u.Pu) / C::kWarps;
-      head.last = sh.owner(u.Pu + u.nb - 1) / C::kWarps;
+    if (!first) {
+      const Shares sh(total, Wn);
+      head = Q4Head{u.b, u.k, u.len, sh.owner(u.P) / wpc, sh.owner(u.P + u.nb - 1) / wpc, {}};
     }
   }
   if (tid == 0) heads[blockIdx.x] = head;
 }
 
 // Units cut between CTAs: the block of the second CTA that holds a piece of a
-// unit combines all of them, a warp per 16-feature tile.
+// unit combines all of them.  A warp takes every kGroups-th piece of a
+// 16-feature tile; the groups meet in shared memory.
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * NT * D / 16) decode_q4_merge(const DecodeQ4Args a) {
+struct MergeCfg {
+  static constexpr int kTiles = NT * D / 16;
+  static constexpr int kGroups = 16 / kTiles;
+  static constexpr int kThreads = 512;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(512) decode_q4_merge(const DecodeQ4Args a) {
   using C = Q4Cfg<D, NT>;
+  using M = MergeCfg<D, NT>;
+  __shared__ float part[16][8][32];
   griddep_wait();
   const Q4Head* heads = static_cast<const Q4Head*>(a.ws);
-  const float* parts = reinterpret_cast<const float*>(heads + kMaxCtas);
+  const float* pieces = reinterpret_cast<const float*>(heads + kMaxCtas);
   const Q4Head h = heads[blockIdx.x];
   if (h.first < 0 || (int)blockIdx.x != h.first + 1) return;
-  const int lane = threadIdx.x & 31, tt = threadIdx.x >> 5;
-  auto at = [&](int i) -> const float* { return parts + ((long)(h.first + i) * 2 + (i == 0)) * C::kRec * 32; };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tt = warp % M::kTiles, group = warp / M::kTiles;
+  const int n = tt / C::kMT, i = tt % C::kMT;
   Combined<D> x;
-  x.from(at, h.last - h.first + 1, tt / C::kMT, tt % C::kMT, lane);
-  write_tile<D, NT>(a, h.b, h.k, h.len, tt / C::kMT, tt % C::kMT, x, lane);
+  x.clear();
+  x.add([&](int j) -> const float* { return pieces + ((long)(h.first + j) * 2 + (j == 0)) * C::kRec * 32; }, group, M::kGroups,
+        h.last - h.first + 1, n, i, lane);
+  if constexpr (M::kGroups > 1) {
+    if (group > 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[warp][j][lane] = x.acc[j];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) part[warp][4 + c][lane] = x.m[c], part[warp][6 + c][lane] = x.l[c];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int q = 1; q < M::kGroups; ++q) {
+      const int w = q * M::kTiles + tt;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float mp = part[w][4 + c][lane];
+        x.scale_to(c, fmaxf(x.m[c], mp));
+        x.accumulate(c, mp, part[w][6 + c][lane], part[w][c][lane], part[w][2 + c][lane]);
+      }
+    }
+  }
+  write_tile<D, NT>(a, h.b, h.k, h.len, n, i, x, lane);
 }
 
 template <int D, int NT, int PARTS>
@@ -879,7 +946,7 @@ cudaError_t run(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
   prof_end(stream);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   prof_begin(kProfDecodeMerge, stream);
-  e = launch_programmatic(decode_q4_merge<D, NT>, dim3(ctas), dim3(32 * NT * D / 16), 0, stream, a);
+  e = launch_programmatic(decode_q4_merge<D, NT>, dim3(ctas), dim3(MergeCfg<D, NT>::kThreads), 0, stream, a);
   prof_end(stream);
   return e;
 }

@@ -119,9 +119,9 @@ attn_status decode_q4_check(int B, int Hq, int Hkv, int Tq, int S, int D) {
   if (B == 0 || Tq == 0) return ATTN_OK;
   if (Tq > S) return ATTN_ERR_SHAPE;
   if ((long)B * Hq * Tq > 0x7fffffffL) return ATTN_ERR_SHAPE;
-  // the kernel numbers the 32-key tiles of all (row, K/V head, block of 8 or 16 query rows) units
+  // the kernel numbers the 32-key tiles (and three more) of all (row, K/V head, block of 8 or 16 query rows) units
   const long blocks = ((long)Hq / Hkv * Tq + 7) / 8;
-  if ((long)B * Hkv * blocks > 0x7fffffffL / (S / 32 + 1L)) return ATTN_ERR_SHAPE;
+  if ((long)B * Hkv * blocks > 0x7fffffffL / (S / 32 + 4L)) return ATTN_ERR_SHAPE;
   return ATTN_OK;
 }
 
