@@ -107,41 +107,43 @@ struct Piece4 {
   }
 };
 
-// One 16-feature tile of 8 rows of a unit, combined from stored pieces with a
-// running maximum; the loads of kBatch pieces are in flight at a time.
-template <int D>
+// TILES 16-feature tiles of 8 rows of a unit, combined from stored pieces with
+// a running maximum; the loads of kBatch pieces are in flight at a time.
+template <int D, int TILES>
 struct Combined {
-  float acc[4], m[2], l[2];
+  float acc[TILES][4], m[2], l[2];
   __device__ __forceinline__ void clear() {
     m[0] = m[1] = -CUDART_INF_F;
-    l[0] = l[1] = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   }
   // pieces first, first + step, ... below count; at(i) is piece i's base
   template <typename At>
   __device__ __forceinline__ void add(At at, int first, int step, int count, int n, int tile, int lane) {
-    constexpr int kPer = D / 16 * 4 + 4, kBatch = 4;
+    constexpr int kPer = D / 16 * 4 + 4, kBatch = TILES == 1 ? 4 : 2;
     const int base = n * kPer * 32 + lane;
     for (int i = first; i < count; i += kBatch * step) {
-      float x[kBatch][8];
+      float x[kBatch][TILES * 4], ml[kBatch][4];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const float* p = at(min(i + u * step, count - 1)) + base;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[u][j] = p[32 * (4 * tile + j)];
+        for (int j = 0; j < 4 * TILES; ++j) x[u][j] = p[32 * (4 * tile + j)];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[u][4 + j] = p[32 * (D / 4 + j)];
+        for (int j = 0; j < 4; ++j) ml[u][j] = p[32 * (D / 4 + j)];
       }
       float top[2] = {m[0], m[1]};
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        if (i + u * step < count) top[0] = fmaxf(top[0], x[u][4]), top[1] = fmaxf(top[1], x[u][5]);
+        if (i + u * step < count) top[0] = fmaxf(top[0], ml[u][0]), top[1] = fmaxf(top[1], ml[u][1]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) scale_to(c, top[c]);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
         if (i + u * step < count) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) accumulate(c, x[u][4 + c], x[u][6 + c], x[u][c], x[u][2 + c]);
+          for (int c = 0; c < 2; ++c) accumulate(c, ml[u][c], ml[u][2 + c], x[u]);
         }
     }
   }
@@ -149,14 +151,17 @@ struct Combined {
     const float f = m[c] == -CUDART_INF_F ? 1.f : ex2_approx(m[c] - top);   // zeros so far (or NaN, which is kept)
     m[c] = top;
     l[c] *= f;
-    acc[c] *= f;
-    acc[2 + c] *= f;
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) acc[i][c] *= f, acc[i][2 + c] *= f;
   }
-  __device__ __forceinline__ void accumulate(int c, float mp, float lp, float x0, float x1) {   // mp <= m[c]
+  __device__ __forceinline__ void accumulate(int c, float mp, float lp, const float* x) {   // mp <= m[c]
     const float f = mp == -CUDART_INF_F ? 1.f : ex2_approx(mp - m[c]);
     l[c] = fmaf(lp, f, l[c]);
-    acc[c] = fmaf(x0, f, acc[c]);
-    acc[2 + c] = fmaf(x1, f, acc[2 + c]);
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+      acc[i][c] = fmaf(x[4 * i + c], f, acc[i][c]);
+      acc[i][2 + c] = fmaf(x[4 * i + 2 + c], f, acc[i][2 + c]);
+    }
   }
 };
 
@@ -379,13 +384,13 @@ __device__ __forceinline__ void write_rows(const DecodeQ4Args& a, int b, int hkv
   }
 }
 
-template <int D, int NT>
-__device__ __forceinline__ void write_tile(const DecodeQ4Args& a, int b, int k, int len, int n, int tile,
-                                           const Combined<D>& x, int lane) {
+template <int D, int NT, int TILES>
+__device__ __forceinline__ void write_tiles(const DecodeQ4Args& a, int b, int k, int len, int n, int tile,
+                                            const Combined<D, TILES>& x, int lane) {
   const int hkv = k / a.nrb, r0 = (k - hkv * a.nrb) * 8 * NT + n * 8;
   int lim[2];
   row_limits(a, len, r0 + 2 * (lane & 3), lim);
-  write_rows<D, 1>(a, b, hkv, r0, lim, tile, &x.acc, x.m, x.l, lane);
+  write_rows<D, TILES>(a, b, hkv, r0, lim, tile, x.acc, x.m, x.l, lane);
 }
 
 // Workspace: a header per CTA, then two pieces a CTA (kRec * 32 f32 each): 0 of
@@ -400,6 +405,7 @@ struct Q4Head {
 template <int D, int NT>
 struct Loader {
   using C = Q4Cfg<D, NT>;
+  static constexpr int kHalf = 16 * D / 2;   // bytes of 16 keys' codes
   Unit u;
   int end;             // end of the share
   bool more;           // tiles left to issue
@@ -408,8 +414,15 @@ struct Loader {
   int pidx, inpg;      // paged: block-table index and row in the page of the tile
   int pbase;           // lane i holds block-table entries pbase + i and pbase + 32 + i
   int entry[2];
-  long base;           // contiguous: cache row of the tile
+  long base;           // contiguous: offset of the tile's codes; paged: of the K/V head in a page
+  const uint8_t *kb, *vb, *ksb, *vsb;   // the lane's 16 bytes of a half tile at offset 0; its key's scales
 
+  __device__ __forceinline__ void begin(const DecodeQ4Args& a, int lane) {
+    kb = a.k4 + lane * 16;
+    vb = a.v4 + lane * 16;
+    ksb = a.ksf + (lane & 15) * (D / 16);
+    vsb = a.vsf + (lane & 15) * (D / 16);
+  }
   __device__ __forceinline__ int load_entry(const DecodeQ4Args& a, int e) const {   // only pages that hold keys are looked up
     return (long)e * a.page_size < u.len ? __ldg(a.block_table + (long)u.b * a.max_pages + e) : 0;
   }
@@ -426,8 +439,9 @@ struct Loader {
       inpg = j - pidx * a.page_size;
       entry[0] = load_entry(a, pbase + lane);
       entry[1] = load_entry(a, pbase + 32 + lane);
+      base = (long)hkv * a.page_size * (D / 2);
     } else {
-      base = ((long)u.b * a.Hkv + hkv) * a.S + j;
+      base = (((long)u.b * a.Hkv + hkv) * a.S + j) * (D / 2);
     }
     // its queries, and the rotary rows of their positions, towards L2
     const int r0 = (u.k - hkv * a.nrb) * 8 * NT, n = min(8 * NT, a.R - r0) * D * 2;
@@ -437,52 +451,68 @@ struct Loader {
     if (a.rope_cs && (lane >> 2) < a.Tq && pos >= 0 && (lane & 3) < D / 32)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope_cs + (long)pos * D + (lane & 3) * 32));
   }
-  // lane_dst: the lane's byte in a stage's codes; lane = its 16-byte chunk of 512 bytes
+  // Copies the current tile to stage s.  lane_dst: where the lane's 16 bytes of a half tile go.
   __device__ __forceinline__ void issue(const DecodeQ4Args& a, uint32_t s, int lane, uint32_t lane_dst) {
     if (more) {
-      constexpr int CH = D / 32;            // 16-byte chunks of a key's codes; a copy covers 32 / CH keys
-      long row[2];                          // cache row of the tile's key 0, as seen from each half
+      long off[2];                          // of the codes of keys 0 and 16
+      bool there = keys >= kTK;
       bool ok[2] = {true, true};
       if (a.block_table) {
-        const int hkv = u.k / a.nrb;
-        const int page[2] = {__shfl_sync(~0u, entry[0], pidx - pbase), __shfl_sync(~0u, entry[0], (pidx - pbase + 1) & 31)};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool wide = a.page_size != 16;        // both halves in one page
-          const int pg = wide ? page[0] : page[h];
-          ok[h] = (unsigned)pg < (unsigned)a.num_pages || keys <= 16 * h;
-          if (!ok[h] && lane == 0) atomicCAS(a.status, 0, kDevBadPage);
-          row[h] = ((long)(ok[h] ? pg : 0) * a.Hkv + hkv) * a.page_size + (wide ? inpg : -16 * h);
+        const int at = pidx - pbase;
+        const int p0 = __shfl_sync(~0u, entry[0], at);
+        const long page_bytes = (long)a.Hkv * a.page_size * (D / 2);
+        ok[0] = ok[1] = (unsigned)p0 < (unsigned)a.num_pages;
+        off[0] = (ok[0] ? p0 : 0) * page_bytes + base + inpg * (D / 2);
+        off[1] = off[0] + kHalf;
+        if (a.page_size == 16) {
+          const int p1 = __shfl_sync(~0u, entry[0], at + 1);
+          ok[1] = (unsigned)p1 < (unsigned)a.num_pages || keys <= 16;
+          off[1] = (ok[1] ? p1 : 0) * page_bytes + base;
+        }
+        if (!(ok[0] && ok[1])) {
+          if (keys > 0 && lane == 0) atomicCAS(a.status, 0, kDevBadPage);
+          there = false;
         }
       } else {
-        row[0] = row[1] = base;
+        off[0] = base;
+        off[1] = base + kHalf;
       }
-      [[maybe_unused]] const long rows = a.block_table ? (long)a.num_pages * a.Hkv * a.page_size : (long)a.B * a.Hkv * a.S;
-      if (keys >= kTK && ok[0] && ok[1] && GQA_CHECK(row[0] >= 0 && row[0] + 15 < rows && row[1] + 31 < rows, a.status, a.dbg_line)) {
-        const long o0 = row[0] * (D / 2) + lane * 16, o1 = row[1] * (D / 2) + lane * 16;
-        const uint8_t *k0 = a.k4 + o0, *k1 = a.k4 + o1, *v0 = a.v4 + o0, *v1 = a.v4 + o1;
+      // the scales' offset is an eighth of the codes': 1 byte to 8
+      const long f = (lane < 16 ? off[0] : off[1]) >> 3;
+      const uint32_t d = s + lane_dst, ds = s + 2 * C::kCodes + lane * (D / 16);
+#ifdef GQA_DEBUG
+      const long bytes = (a.block_table ? (long)a.num_pages * a.Hkv * a.page_size : (long)a.B * a.Hkv * a.S) * (D / 2);
+      for (int h = 0; h < 2; ++h)
+        if (min(keys - 16 * h, 16) > 0 && ok[h] &&
+            !GQA_CHECK(off[h] >= 0 && off[h] + min(keys - 16 * h, 16) * (D / 2) <= bytes, a.status, a.dbg_line))
+          there = ok[h] = false;
+#endif
+      if (there) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          cp_async16(s + lane_dst + i * 512, (i < CH / 2 ? k0 : k1) + i * 512);
-          cp_async16(s + lane_dst + C::kCodes + i * 512, (i < CH / 2 ? v0 : v1) + i * 512);
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t *k = kb + off[h], *v = vb + off[h];
+#pragma unroll
+          for (int i = 0; i < kHalf; i += 512) {
+            cp_async16(d + h * kHalf + i, k + i);
+            cp_async16(d + C::kCodes + h * kHalf + i, v + i);
+          }
         }
-        const long f = (lane < 16 ? row[0] : row[1]) * (D / 16) + lane * (D / 16);
-        cp_async_small<D / 16>(s + 2 * C::kCodes + lane * (D / 16), a.ksf + f);
-        cp_async_small<D / 16>(s + 2 * C::kCodes + C::kSf + lane * (D / 16), a.vsf + f);
+        cp_async_small<D / 16>(ds, ksb + f);
+        cp_async_small<D / 16>(ds + C::kSf, vsb + f);
       } else {                              // the row's last tile, or a page outside the pool: zeros for what is not there
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int key = i * (32 / CH) + lane / CH, h = i < CH / 2 ? 0 : 1;
-          const bool valid = key < keys && ok[h] && GQA_CHECK(row[h] + key >= 0 && row[h] + key < rows, a.status, a.dbg_line);
-          const long o = valid ? row[h] * (D / 2) + lane * 16 + i * 512 : 0;
-          cp_async16(s + lane_dst + i * 512, a.k4 + o, valid);
-          cp_async16(s + lane_dst + C::kCodes + i * 512, a.v4 + o, valid);
-        }
-        const long r = (lane < 16 ? row[0] : row[1]) + lane;
-        const bool valid = lane < keys && (lane < 16 ? ok[0] : ok[1]) && GQA_CHECK(r >= 0 && r < rows, a.status, a.dbg_line);
-        const long f = valid ? r * (D / 16) : 0;
-        cp_async_small<D / 16>(s + 2 * C::kCodes + lane * (D / 16), a.ksf + f, valid);
-        cp_async_small<D / 16>(s + 2 * C::kCodes + C::kSf + lane * (D / 16), a.vsf + f, valid);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < kHalf; i += 512) {
+            const bool valid = ok[h] && 16 * h + (i + lane * 16) / (D / 2) < keys;
+            const long o = valid ? off[h] + i : -(long)lane * 16;
+            cp_async16(d + h * kHalf + i, kb + o, valid);
+            cp_async16(d + C::kCodes + h * kHalf + i, vb + o, valid);
+          }
+        const bool valid = lane < keys && (lane < 16 ? ok[0] : ok[1]);
+        const long o = valid ? f : -(long)(lane & 15) * (D / 16);
+        cp_async_small<D / 16>(ds, ksb + o, valid);
+        cp_async_small<D / 16>(ds + C::kSf, vsb + o, valid);
       }
       if (--tiles > 0) {
         keys -= kTK;
@@ -498,7 +528,7 @@ struct Loader {
             }
           }
         } else {
-          base += kTK;
+          base += 2 * kHalf;
         }
       } else {
         u.next(a);
@@ -520,7 +550,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   __shared__ Unit rec_unit[2 * C::kWarps];   // unit of each stored piece
   __shared__ int rec_kind[2 * C::kWarps];    // kStored, with kFirst / kLast if it has the unit's first / last tile; 0: none
   __shared__ uint8_t order[C::kWarps][2 * C::kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);   // the same in a warp, told so
   const int g = lane >> 2, t = lane & 3;
   const int upb = a.Hkv * a.nrb;
 
@@ -603,6 +633,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     Loader<D, NT> ld;
     ld.u = cu;
     ld.end = v1;
+    ld.begin(a, lane);
     ld.enter(a, ct, lane);
     const uint32_t lane_dst = row_at<D>(lane / (D / 32), lane % (D / 32));
     // the lane's bytes in a stage: of K rows pi(g) (+ 8, 16, 24) and of V rows pi(2t), pi(2t + 1)
@@ -851,25 +882,34 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   float* pieces = reinterpret_cast<float*>(heads + kMaxCtas);
   Q4Head head{};
   head.first = -1;
+  constexpr int kQuads = NT * C::kMT / 4;   // a warp takes four tiles of a unit at a time, units and quads in turn
+  int item = 0;
   for (unsigned todo = begins; todo;) {
     const int s0 = __ffs(todo) - 1;
     todo &= todo - 1;
     const unsigned slots = taken & ~((1u << s0) - 1) & (todo ? (todo & -todo) - 1 : ~0u);   // up to the next unit's
-    const Unit u = rec_unit[s0];
     const bool first = rec_kind[s0] & kFirst, last = rec_kind[31 - __clz(slots)] & kLast;
-    const int rank = __popc(taken & ((1u << s0) - 1));
-    for (int tt = warp; tt < NT * C::kMT; tt += C::kWarps) {
-      const int n = tt / C::kMT, i = tt % C::kMT;
-      Combined<D> x;
+    if (!first && warp == 0) {
+      const Unit u = rec_unit[s0];
+      const Shares sh(total, Wn);
+      head = Q4Head{u.b, u.k, u.len, sh.owner(u.P) / wpc, sh.owner(u.P + u.nb - 1) / wpc, {}};
+    }
+#pragma unroll 1
+    for (int qd = 0; qd < kQuads; ++qd, ++item) {
+      if (item >= C::kWarps) item = 0;
+      if (item != warp) continue;
+      const int n = qd * 4 / C::kMT, i = qd * 4 % C::kMT, rank = __popc(taken & ((1u << s0) - 1));
+      Combined<D, 4> x;
       x.clear();
       x.add([&](int j) -> const float* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, 0, 1, __popc(slots), n, i,
             lane);
       if (first && last) {
-        write_tile<D, NT>(a, u.b, u.k, u.len, n, i, x, lane);
+        const Unit u = rec_unit[s0];
+        write_tiles<D, NT>(a, u.b, u.k, u.len, n, i, x, lane);
       } else {
         float* q = pieces + ((long)blockIdx.x * 2 + first) * C::kRec * 32 + n * Piece4<D, NT>::kPer * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q[32 * (4 * i + j)] = x.acc[j];
+        for (int j = 0; j < 16; ++j) q[32 * (4 * i + j)] = x.acc[j >> 2][j & 3];
         if (i == 0) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -878,10 +918,6 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
           }
         }
       }
-    }
-    if (!first) {
-      const Shares sh(total, Wn);
-      head = Q4Head{u.b, u.k, u.len, sh.owner(u.P) / wpc, sh.owner(u.P + u.nb - 1) / wpc, {}};
     }
   }
   if (tid == 0) heads[blockIdx.x] = head;
@@ -909,14 +945,14 @@ __global__ void __launch_bounds__(512) decode_q4_merge(const DecodeQ4Args a) {
   if (h.first < 0 || (int)blockIdx.x != h.first + 1) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tt = warp % M::kTiles, group = warp / M::kTiles;
   const int n = tt / C::kMT, i = tt % C::kMT;
-  Combined<D> x;
+  Combined<D, 1> x;
   x.clear();
   x.add([&](int j) -> const float* { return pieces + ((long)(h.first + j) * 2 + (j == 0)) * C::kRec * 32; }, group, M::kGroups,
         h.last - h.first + 1, n, i, lane);
   if constexpr (M::kGroups > 1) {
     if (group > 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) part[warp][j][lane] = x.acc[j];
+      for (int j = 0; j < 4; ++j) part[warp][j][lane] = x.acc[0][j];
 #pragma unroll
       for (int c = 0; c < 2; ++c) part[warp][4 + c][lane] = x.m[c], part[warp][6 + c][lane] = x.l[c];
     }
@@ -925,15 +961,18 @@ __global__ void __launch_bounds__(512) decode_q4_merge(const DecodeQ4Args a) {
 #pragma unroll
     for (int q = 1; q < M::kGroups; ++q) {
       const int w = q * M::kTiles + tt;
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = part[w][j][lane];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float mp = part[w][4 + c][lane];
         x.scale_to(c, fmaxf(x.m[c], mp));
-        x.accumulate(c, mp, part[w][6 + c][lane], part[w][c][lane], part[w][2 + c][lane]);
+        x.accumulate(c, mp, part[w][6 + c][lane], y);
       }
     }
   }
-  write_tile<D, NT>(a, h.b, h.k, h.len, n, i, x, lane);
+  write_tiles<D, NT>(a, h.b, h.k, h.len, n, i, x, lane);
 }
 
 template <int D, int NT, int PARTS>
