@@ -626,6 +626,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     before += all;
   }
 
+  // all of a warp's lanes found the same: told so, the loops below need no divergence handling
+  v0 = __shfl_sync(~0u, v0, 0), v1 = __shfl_sync(~0u, v1, 0);
+  cu.P = __shfl_sync(~0u, cu.P, 0), cu.nb = __shfl_sync(~0u, cu.nb, 0), cu.b = __shfl_sync(~0u, cu.b, 0);
+  cu.k = __shfl_sync(~0u, cu.k, 0), cu.len = __shfl_sync(~0u, cu.len, 0);
   // the share's tiles [ct, te) of its first unit
   int ct = max(v0 - cu.P, 0), te = min(cu.nb, v1 - cu.P);
   if (v0 < v1 && ct < te) {
@@ -722,20 +726,27 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
         // y = s - m + kOff in log2 units, hidden keys out; the maximum moves when some y is above kOff + kLazy
         const bool edge = j0 + kTK > cu.len - a.Tq + 1;   // some key of the tile is hidden from some row
         float y[2][NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int G = 0; G < 2; ++G)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[G][n][i] = fmaf(sc[G][n][i], fac[n][i & 1], bias[n][i & 1]);
+        if (edge) {
+          const int key = j0 + key_of(g);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int G = 0; G < 2; ++G)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (key + 16 * G + 8 * (i >> 1) > lim[n][i & 1]) y[G][n][i] = sc[G][n][i] = -CUDART_INF_F;
+        }
         float top = -CUDART_INF_F;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int G = 0; G < 2; ++G) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[G][n][i] = fmaf(sc[G][n][i], fac[n][i & 1], bias[n][i & 1]);
-            if (edge) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (j0 + 16 * G + 8 * (i >> 1) + key_of(g) > lim[n][i & 1]) y[G][n][i] = sc[G][n][i] = -CUDART_INF_F;
-            }
-            top = max3f(max3f(top, y[G][n][0], y[G][n][1]), y[G][n][2], y[G][n][3]);
-          }
+          for (int G = 0; G < 2; ++G) top = max3f(max3f(top, y[G][n][0], y[G][n][1]), y[G][n][2], y[G][n][3]);
         if (__any_sync(~0u, top > kOff + kLazy)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -783,43 +794,48 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
             pf[G][n][0] = transpose8x8(pack_f16x2(x[0], x[1]));
             pf[G][n][1] = transpose8x8(pack_f16x2(x[2], x[3]));
           }
-        // O^T
+        // O^T: the block scales of the thread's keys pi(2t), pi(2t+1), pi(2t+8), pi(2t+9) of each group
+        uint32_t vsf[2][4];
+#pragma unroll
+        for (int G = 0; G < 2; ++G)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vsf[G][i] = lds<1>(s + vs_at[i & 1] + (16 * G + 8 * (i >> 1)) * (D / 16));
+        if (edge && a.Tq > 1) {
+          // a NaN block at a key that some rows do not see: 0 * NaN would reach them through the MMA, so it is
+          // taken out here and put into the rows that do see it
+          bool bad = false;
+#pragma unroll
+          for (int G = 0; G < 2; ++G)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((vsf[G][i] & 0x7f) == 0x7f) bad = true, vsf[G][i] = 0;
+          if (__any_sync(~0u, bad)) {
+#pragma unroll 1
+            for (int k = 0; k < kTK; ++k) {
+              const uint32_t v = lds<1>(s + 2 * C::kCodes + C::kSf + k * (D / 16) + (D == 128 ? g : g >> 1));
+              if ((v & 0x7f) != 0x7f) continue;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  if (j0 + k <= lim[n][c]) {
+#pragma unroll
+                    for (int i = 0; i < C::kMT; ++i) p.acc[n][i][c] = p.acc[n][i][2 + c] = CUDART_NAN_F;
+                  }
+            }
+          }
+        }
 #pragma unroll
         for (int G = 0; G < 2; ++G) {
-          uint32_t sb[4];
           constexpr int VW = D / 64;                 // words of a thread's features of one key
           uint32_t w[4][VW];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {              // keys pi(2t), pi(2t+1), pi(2t+8), pi(2t+9)
+          for (int i = 0; i < 4; ++i) {
             const uint32_t at_v = s + v_at[i & 1] + (16 * G + 8 * (i >> 1)) * (D / 2);
             if constexpr (D == 128) lds64(at_v, w[i]);
             else w[i][0] = lds<4>(at_v);
-            sb[i] = lds<1>(s + vs_at[i & 1] + (16 * G + 8 * (i >> 1)) * (D / 16));
           }
-          if (edge && a.Tq > 1) {
-            // a NaN block at a key that some rows do not see: 0 * NaN would reach them through the MMA, so it is
-            // taken out here and put into the rows that do see it
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if ((sb[i] & 0x7f) == 0x7f) bad = true, sb[i] = 0;
-            }
-            if (__any_sync(~0u, bad)) {
-#pragma unroll 1
-              for (int k = 0; k < 16; ++k) {
-                const uint32_t v = lds<1>(s + 2 * C::kCodes + C::kSf + (16 * G + k) * (D / 16) + (D == 128 ? g : g >> 1));
-                if ((v & 0x7f) != 0x7f) continue;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                  for (int c = 0; c < 2; ++c)
-                    if (j0 + 16 * G + k <= lim[n][c]) {
-#pragma unroll
-                      for (int i = 0; i < C::kMT; ++i) p.acc[n][i][c] = p.acc[n][i][2 + c] = CUDART_NAN_F;
-                    }
-              }
-            }
-          }
+          const uint32_t* sb = vsf[G];
           const uint32_t f01 = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x0040)), f23 = e4m3x2_to_f16(__byte_perm(sb[2], sb[3], 0x0040));
 #pragma unroll
           for (int v = 0; v < VW; ++v) {
