@@ -658,16 +658,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     uint32_t s = ring;                   // stage of the current tile, and the one to fill
     uint32_t fill = ring;
     int ta = ct;                         // the current piece: unit cu's tiles [ta, te)
+    bool fresh = true;
     // a round issues the copies of the tile kStages - 1 ahead, then takes a tile
     for (int lead = C::kStages - 1;;) {
-      __syncwarp();                      // the stage to fill is read
-      ld.issue(a, fill, lane, lane_dst);
-      fill = fill == ring + (C::kStages - 1) * C::kStage ? ring : fill + C::kStage;
-      if (lead > 0) {
-        --lead;
-        continue;
-      }
-      if (ct == ta) {                    // while the copies are in flight
+      if (fresh) {                       // before the copies: these loads would queue behind them
         load_queries<D, NT, PARTS>(a, cu, lane, qf, fac);
         p.clear();
         r0 = (cu.k % a.nrb) * 8 * NT;
@@ -676,6 +670,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
           row_limits(a, cu.len, r0 + n * 8 + 2 * t, lim[n]);
           bias[n][0] = bias[n][1] = CUDART_INF_F;     // kOff - m: any visible score makes the maximum move
         }
+        fresh = false;
+      }
+      __syncwarp();                      // the stage to fill is read
+      ld.issue(a, fill, lane, lane_dst);
+      fill = fill == ring + (C::kStages - 1) * C::kStage ? ring : fill + C::kStage;
+      if (lead > 0) {
+        --lead;
+        continue;
       }
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
       __syncwarp();                      // every lane's copies of tile i have landed
@@ -876,6 +878,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
         }
       }
       cu.next(a);
+      fresh = true;
       ct = ta = 0;
       te = min(cu.nb, v1 - cu.P);
       if (te <= 0) break;
