@@ -39,6 +39,8 @@
 // decode_q4_merge.
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "cache_ops.h"
 #include "fp4.cuh"
 #include "kernels.h"
@@ -997,8 +999,17 @@ __global__ void __launch_bounds__(512) decode_q4_merge(const DecodeQ4Args a) {
 template <int D, int NT, int PARTS>
 cudaError_t run(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
   using C = Q4Cfg<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  // once per device: the call costs a microsecond
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!bit || !(done.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
   prof_begin(kProfDecode, stream);
   decode_q4_kernel<D, NT, PARTS><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
   prof_end(stream);
