@@ -60,7 +60,6 @@ attn_status rope(const void* q, const void* k, void* qo, void* ko, const int* po
   a.Hkv = Hkv;
   a.D = D;
   a.status = gqa::api_status_word();
-  a.dbg_line = gqa::api_check_line();
   const int sms = gqa::api_sm_count();
   if (!a.status || sms < 1) return ATTN_ERR_CUDA;
   return status_of(gqa::launch_rope(a, sms, st_of(stream)));
@@ -100,6 +99,8 @@ attn_status append(const void* k, const void* v, const int* slots, const int* po
   a.vsf = static_cast<uint8_t*>(vsf);
   a.k_scale = k_scale;
   a.v_scale = v_scale;
+  a.k_inv = 1.f / (fmt == gqa::kCacheQ4 ? 6.f * k_scale : k_scale);
+  a.v_inv = 1.f / (fmt == gqa::kCacheQ4 ? 6.f * v_scale : v_scale);
   a.B = B;
   a.T = T;
   a.H = H;
@@ -108,8 +109,9 @@ attn_status append(const void* k, const void* v, const int* slots, const int* po
   a.num_pages = num_pages;
   a.status = gqa::api_status_word();
   a.dbg_line = gqa::api_check_line();
-  if (!a.status) return ATTN_ERR_CUDA;
-  return status_of(gqa::launch_cache_append(a, fmt, st_of(stream)));
+  const int sms = gqa::api_sm_count();
+  if (!a.status || sms < 1) return ATTN_ERR_CUDA;
+  return status_of(gqa::launch_cache_append(a, fmt, sms, st_of(stream)));
 }
 
 attn_status decode_q4_check(int B, int Hq, int Hkv, int Tq, int S, int D) {
@@ -300,8 +302,9 @@ attn_status attn_cache_gather_q4(const int* slots, const void* k4, const void* k
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.status = gqa::api_status_word();
-  if (!a.status) return ATTN_ERR_CUDA;
-  return status_of(gqa::launch_cache_gather(a, st_of(stream)));
+  const int sms = gqa::api_sm_count();
+  if (!a.status || sms < 1) return ATTN_ERR_CUDA;
+  return status_of(gqa::launch_cache_gather(a, sms, st_of(stream)));
 }
 
 size_t attn_decode_q4_workspace_size(int B, int Hq, int Hkv, int Tq, int S, int D) {

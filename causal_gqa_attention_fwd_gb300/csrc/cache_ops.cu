@@ -32,8 +32,14 @@ __device__ __forceinline__ PlanReq plan_req(const PlanArgs& a, int b) {
   return r;
 }
 
-__device__ __forceinline__ long pages_of(long keys, int page_size) { return (keys + page_size - 1) / page_size; }
+// Pages of the keys of a valid request (below 2^31, as page_size is).
+__device__ __forceinline__ int pages_of(long keys, int page_size) {
+  return (int)(((unsigned)keys + (unsigned)page_size - 1u) / (unsigned)page_size);
+}
 
+// kPer: tokens a thread takes, kPlanThreads apart, so that their searches and
+// look-ups overlap.
+template <int kPer>
 __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanArgs a) {
   extern __shared__ int plan_smem[];
   int* cu = plan_smem;              // [B + 1] first token of each request
@@ -99,50 +105,61 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanArgs
     const int f = first[b];
     if (f < 0) continue;
     const PlanReq r = plan_req(a, b);
-    const int have = (int)pages_of(r.len, a.page_size), want = (int)pages_of(r.len + r.add, a.page_size);
+    const int have = pages_of(r.len, a.page_size), want = pages_of(r.len + r.add, a.page_size);
     for (int p = have + lane; p < want; p += 32) a.block_table[(long)b * a.max_pages + p] = a.free_pages[f + p - have];
   }
   // tokens
+  const int live = cu[a.B];
   bool bad_page = false;
-  for (int n = blockIdx.x * kPlanThreads + tid; n < a.total; n += gridDim.x * kPlanThreads) {
-    int slot = -1, pos = 0;
-    if (n < cu[a.B]) {
+  for (long n0 = (long)blockIdx.x * kPlanThreads * kPer + tid; n0 < a.total; n0 += (long)gridDim.x * kPlanThreads * kPer) {
+    int slot[kPer], pos[kPer], req[kPer], page[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const long n = n0 + i * kPlanThreads;
       int lo = 0, hi = a.B - 1;   // the last request that starts at or before n
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (cu[mid] <= n) lo = mid;
         else hi = mid - 1;
       }
-      const int f = first[lo];
-      if (f >= 0) {
-        const int len = a.cache_lens[lo];
-        pos = len + (n - cu[lo]);
-        const int p = pos / a.page_size, have = (int)pages_of(len, a.page_size);
-        const int page = p < have ? a.block_table[(long)lo * a.max_pages + p] : a.free_pages[f + p - have];
-        const long s = (long)page * a.page_size + (pos - p * a.page_size);
-        if (page >= 0 && s <= 0x7fffffffL) slot = (int)s;
-        else bad_page = true;
-      }
+      req[i] = n < live && first[lo] >= 0 ? lo : -1;
+      slot[i] = -1;
+      pos[i] = page[i] = 0;
     }
-    a.slots[n] = slot;
-    a.positions[n] = pos;
-    if (n > 0x7fffffff - (int)(gridDim.x * kPlanThreads)) break;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (req[i] >= 0) {
+        const int len = a.cache_lens[req[i]];
+        pos[i] = len + (int)(n0 + i * kPlanThreads - cu[req[i]]);
+        const int p = (int)((unsigned)pos[i] / (unsigned)a.page_size), have = pages_of(len, a.page_size);
+        page[i] = p < have ? a.block_table[(long)req[i] * a.max_pages + p] : a.free_pages[first[req[i]] + p - have];
+        slot[i] = pos[i] - p * a.page_size;
+      }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const long n = n0 + i * kPlanThreads;
+      if (n >= a.total) break;
+      if (req[i] >= 0) {
+        const long s = (long)page[i] * a.page_size + slot[i];
+        const bool ok = page[i] >= 0 && s <= 0x7fffffffL;
+        slot[i] = ok ? (int)s : -1;
+        bad_page |= !ok;
+      }
+      a.slots[n] = slot[i];
+      a.positions[n] = pos[i];
+    }
   }
   if (bad_page) atomicCAS(a.status, 0, kDevBadPage);
 }
 
 // ------------------------------------------------------------ rotary rows
-// A thread takes 16 features of a token: 8 rotated pairs (both layouts use
-// the same 8 cosines and sines) or 16 features past rotary_dim, for HC heads,
-// so the table row is read once per HC heads.  Products and sums are rounded
-// one by one (no fused multiply-add): the values are the elementary ones.
-__device__ __forceinline__ void rotate8(const float* x, const float* y, const float* c, const float* s, float* xo,
-                                        float* yo) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    xo[i] = __fsub_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y[i], s[i]));
-    yo[i] = __fadd_rn(__fmul_rn(y[i], c[i]), __fmul_rn(x[i], s[i]));
-  }
+// Products and sums are rounded one by one (no fused multiply-add): the values
+// are the elementary ones, whoever computes them.
+__device__ __forceinline__ float rot_first(float x, float y, float c, float s) {
+  return __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+}
+__device__ __forceinline__ float rot_second(float x, float y, float c, float s) {   // x: the pair's second
+  return __fadd_rn(__fmul_rn(x, c), __fmul_rn(y, s));
 }
 
 __device__ __forceinline__ void load8f(const float* p, float* x) {
@@ -151,65 +168,86 @@ __device__ __forceinline__ void load8f(const float* p, float* x) {
   x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-template <int HC>
+// Bound by memory: each row is read and written once.  A thread takes one part
+// of a token's heads, HC of them: 8 features (4 neighbouring pairs, or features
+// past rotary_dim), or in the half layout the two groups of 8 that are paired.
+// Neighbouring threads take neighbouring 16 bytes, the table row is read once
+// for HC heads, and all HC heads' loads are in flight together (8 heads at
+// T = 4096, 32 + 8 heads: 29 us with the loads one head after another).
+template <int HC, bool INTER>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
-  const int U = a.D / 16;
+  const int rotated = a.R / (INTER ? 8 : 16), U = rotated + (a.D - a.R) / 8;
   const long idx = (long)blockIdx.x * 256 + threadIdx.x;
   const long n = idx / U;
   if (n >= (long)a.B * a.T) return;
   const int u = (int)(idx - n * U);
-  const long b = n / a.T, t = n - b * a.T;
+  const long b = a.B == 1 ? 0 : n / a.T, t = n - b * a.T;
   const int pos = a.positions[b * a.pos_stride + t];
   const bool ok = pos >= 0 && pos < a.n_table;
-  if (!ok && u == 0 && blockIdx.y == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
-  const bool rot = u < a.R / 16;
-  // features of the thread: [fa, fa + 8) and [fb, fb + 8)
-  const int fa = rot && !a.interleaved ? 8 * u : 16 * u;
-  const int fb = rot && !a.interleaved ? a.R / 2 + 8 * u : 16 * u + 8;
-  float c[8], s[8];
-  if (rot && ok) {
-    const float* cs = a.cs + (long)pos * a.R + 8 * u;
-    load8f(cs, c);
-    load8f(cs + a.R / 2, s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] *= a.sign;
-  }
+  const bool rot = u < rotated, two = rot && !INTER;   // two: features fa.. are paired with fb..
+  const int fa = rot ? 8 * u : a.R + 8 * (u - rotated), fb = a.R / 2 + 8 * u;
   const int h0 = blockIdx.y * HC;
+  const int H = a.Hq + a.Hkv;
+  uint4 wa[HC], wb[HC];
 #pragma unroll
   for (int i = 0; i < HC; ++i) {
     const int hh = h0 + i;
-    if (hh >= a.Hq + a.Hkv) break;
     const bool is_q = hh < a.Hq;
-    const RowView& in = is_q ? a.q : a.k;
-    const RowView& out = is_q ? a.qo : a.ko;
-    const int h = is_q ? hh : hh - a.Hq;
-    const __nv_bfloat16* x = in.p + b * in.sb + t * in.st + h * in.sh;
-    __nv_bfloat16* y = const_cast<__nv_bfloat16*>(out.p) + b * out.sb + t * out.st + h * out.sh;
-    uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
-    if (ok) {
-      wa = *reinterpret_cast<const uint4*>(x + fa);
-      wb = *reinterpret_cast<const uint4*>(x + fb);
-      if (rot) {
-        float va[8], vb[8], oa[8], ob[8];
-        bf16x8_to_f32(wa, va);
-        bf16x8_to_f32(wb, vb);
-        if (a.interleaved) {   // pairs (0,1), (2,3), ...: split, rotate, put back
-          float e[8], o[8];
+    const __nv_bfloat16* x = is_q ? a.q.p + b * a.q.sb + t * a.q.st + hh * a.q.sh
+                                  : a.k.p + b * a.k.sb + t * a.k.st + (hh - a.Hq) * a.k.sh;
+    wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
+    if (ok && hh < H) {
+      wa[i] = *reinterpret_cast<const uint4*>(x + fa);
+      if (two) wb[i] = *reinterpret_cast<const uint4*>(x + fb);
+    }
+  }
+  if (!ok && u == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+  float c[8], s[8];
+  if (rot && ok) {
+    const float* cs = a.cs + (long)pos * a.R + (INTER ? 4 * u : 8 * u);
+    if constexpr (INTER) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(cs)), y = __ldg(reinterpret_cast<const float4*>(cs + a.R / 2));
+      c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
+      s[0] = y.x, s[1] = y.y, s[2] = y.z, s[3] = y.w;
+    } else {
+      load8f(cs, c);
+      load8f(cs + a.R / 2, s);
+    }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) e[j] = va[2 * j], o[j] = va[2 * j + 1], e[4 + j] = vb[2 * j], o[4 + j] = vb[2 * j + 1];
-          float re[8], ro[8];
-          rotate8(e, o, c, s, re, ro);
+    for (int i = 0; i < (INTER ? 4 : 8); ++i) s[i] *= a.sign;
+  }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) oa[2 * j] = re[j], oa[2 * j + 1] = ro[j], ob[2 * j] = re[4 + j], ob[2 * j + 1] = ro[4 + j];
-        } else {
-          rotate8(va, vb, c, s, oa, ob);
+  for (int i = 0; i < HC; ++i) {
+    const int hh = h0 + i;
+    if (hh >= H) break;
+    if (rot && ok) {
+      float x[8];
+      bf16x8_to_f32(wa[i], x);
+      if constexpr (INTER) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[2 * j] = rot_first(x[2 * j], x[2 * j + 1], c[j], s[j]);
+          y[2 * j + 1] = rot_second(x[2 * j + 1], x[2 * j], c[j], s[j]);
         }
-        wa = f32_to_bf16x8(oa);
-        wb = f32_to_bf16x8(ob);
+        wa[i] = f32_to_bf16x8(y);
+      } else {
+        float y[8], x2[8], y2[8];
+        bf16x8_to_f32(wb[i], x2);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          y[j] = rot_first(x[j], x2[j], c[j], s[j]);
+          y2[j] = rot_second(x2[j], x[j], c[j], s[j]);
+        }
+        wa[i] = f32_to_bf16x8(y);
+        wb[i] = f32_to_bf16x8(y2);
       }
     }
-    *reinterpret_cast<uint4*>(y + fa) = wa;
-    *reinterpret_cast<uint4*>(y + fb) = wb;
+    const bool is_q = hh < a.Hq;
+    __nv_bfloat16* y = const_cast<__nv_bfloat16*>(is_q ? a.qo.p + b * a.qo.sb + t * a.qo.st + hh * a.qo.sh
+                                                       : a.ko.p + b * a.ko.sb + t * a.ko.st + (hh - a.Hq) * a.ko.sh);
+    *reinterpret_cast<uint4*>(y + fa) = wa[i];
+    if (two) *reinterpret_cast<uint4*>(y + fb) = wb[i];
   }
 }
 
@@ -224,185 +262,193 @@ struct TurnsTable {
   unsigned long long w[kMaxPairs];
 };
 
+// A thread keeps one pair: its w is read once (a constant indexed by the lane
+// is fetched once per lane), its phase advances by an addition.
 __global__ void __launch_bounds__(256) rope_table_kernel(float* out, int n, int R, float mscale, const TurnsTable tt) {
-  const int H = R / 2;
-  const long total = (long)n * H, step = (long)gridDim.x * 256;
-  for (long e = (long)blockIdx.x * 256 + threadIdx.x; e < total; e += step) {
-    const int p = (int)(e / H), i = (int)(e - (long)p * H);
-    const unsigned long long ph = (unsigned long long)p * tt.w[i];
-    const float half_turns = (float)(int)((long long)ph >> 40) * 0x1p-23f;
-    const float d = (float)(unsigned)((ph >> 16) & 0xFFFFFFull) * (0x1p-47f * 3.14159265358979f);
+  const int H = R / 2, rows = blockDim.x / H, i = threadIdx.x % H, step = rows * gridDim.x;
+  const int p0 = blockIdx.x * rows + threadIdx.x / H;
+  const unsigned long long w = tt.w[i], dw = w * step;
+  unsigned long long ph = w * p0;
+  float* o = out + (long)p0 * R + i;
+  const long stride = (long)step * R;
+#pragma unroll 2
+  for (long p = p0; p < n; p += step, ph += dw, o += stride) {
+    const float half_turns = (float)((int)(ph >> 32) >> 8) * 0x1p-23f;
+    const float d = (float)((unsigned)(ph >> 16) & 0xFFFFFFu) * (0x1p-47f * 3.14159265358979f);
     float s, c;
     sincospif(half_turns, &s, &c);
-    out[(long)p * R + i] = fmaf(-s, d, c) * mscale;
-    out[(long)p * R + H + i] = fmaf(c, d, s) * mscale;
+    o[0] = fmaf(-s, d, c) * mscale;
+    o[H] = fmaf(c, d, s) * mscale;
   }
 }
 
 // ------------------------------------------------------------------ append
-// A thread takes one 16-feature block of one head of one token, of k and of
-// v: the unit that shares a 4-bit scale, so nothing crosses threads.  With
-// half-layout rotation it also loads the 16 features its own are paired with
-// (they come from L1: a neighbouring thread's own block).
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* x) {
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), x);
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(p + 8), x + 8);
-}
-
-// Features [f0, f0 + 16) of one k row, rotated by table row cs.
-__device__ __forceinline__ void rotate_block(const AppendArgs& a, const __nv_bfloat16* row, const float* cs, int f0,
-                                             float* x) {
-  const int H = a.R / 2;
-  if (a.interleaved) {
-    float c[8], s[8];
-    load8f(cs + f0 / 2, c);
-    load8f(cs + H + f0 / 2, s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float e = x[2 * i], o = x[2 * i + 1];
-      x[2 * i] = __fsub_rn(__fmul_rn(e, c[i]), __fmul_rn(o, s[i]));
-      x[2 * i + 1] = __fadd_rn(__fmul_rn(o, c[i]), __fmul_rn(e, s[i]));
-    }
-    return;
-  }
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {   // 8 features at a time: H is a multiple of 8
-    const int f = f0 + 8 * g;
-    const bool second = f >= H;
-    const int i0 = second ? f - H : f;
-    float c[8], s[8], y[8];
-    load8f(cs + i0, c);
-    load8f(cs + H + i0, s);
-    bf16x8_to_f32(*reinterpret_cast<const uint4*>(row + (second ? f - H : f + H)), y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = __fmul_rn(x[8 * g + i], c[i]), q = __fmul_rn(y[i], s[i]);
-      x[8 * g + i] = second ? __fadd_rn(p, q) : __fsub_rn(p, q);
-    }
-  }
-}
-
+// A thread takes 8 features of a token, of k and of v, in HC heads: neighbouring
+// threads write neighbouring bytes, the table row is read once for HC heads and
+// all their loads are in flight together.  Two neighbouring lanes share a block
+// of 16 features and its 4-bit scale.  In the half layout a thread also loads
+// the 8 features its own are paired with (from L1: another lane's own).
 __device__ __forceinline__ uint32_t e4m3_of(float x) { return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3); }
 
-// One 16-feature block into a 4-bit cache: its codes and its scale byte.
-__device__ __forceinline__ void quantise_block(const float* x, float scale, uint2& codes, uint8_t& sf8) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-  if (m >= 0x7f800000u) {   // a NaN or an infinity: the whole block reads as NaN
-    sf8 = 0x7f;
-    codes = make_uint2(0, 0);
-    return;
-  }
-  const float rc = __fdiv_rn(1.f, __fmul_rn(6.f, scale));
-  sf8 = (uint8_t)e4m3_of(fminf(__fmul_rn(__uint_as_float(m), rc), 448.f));
-  const float sf = f16x2_to_f32(e4m3x2_to_f16(sf8)).x;
-  const float inv = sf > 0.f ? __fdiv_rn(1.f, __fmul_rn(sf, scale)) : 0.f;
-  float y[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(x[i], inv);
-  codes = make_uint2(f32x8_to_e2m1(y), f32x8_to_e2m1(y + 8));
-}
-
+// 8 features into row `row` of a cache; for 4 bits the lane pair (lane, lane ^ 1)
+// calls it together with the two halves of a block.
 template <int FMT>
-__device__ __forceinline__ void store_block(const AppendArgs& a, bool is_k, long row, int f0, const float* x) {
+__device__ __forceinline__ void store8(const AppendArgs& a, bool is_k, bool live, long row, int f0, const float* x) {
   void* cache = is_k ? a.kc : a.vc;
-  const float scale = is_k ? a.k_scale : a.v_scale;
+  [[maybe_unused]] const float scale = is_k ? a.k_scale : a.v_scale;
   if constexpr (FMT == kCacheBf16) {
-    uint4* y = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + row * a.D + f0);
-    y[0] = f32_to_bf16x8(x);
-    y[1] = f32_to_bf16x8(x + 8);
+    if (live) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + row * a.D + f0) = f32_to_bf16x8(x);
   } else if constexpr (FMT == kCacheE4m3) {
-    const float r = __fdiv_rn(1.f, scale);
-    uint32_t w[4];
+    const float r = is_k ? a.k_inv : a.v_inv;
+    uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
       w[i] = e4m3_of(__fmul_rn(x[4 * i], r)) | e4m3_of(__fmul_rn(x[4 * i + 1], r)) << 8 |
              e4m3_of(__fmul_rn(x[4 * i + 2], r)) << 16 | e4m3_of(__fmul_rn(x[4 * i + 3], r)) << 24;
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(cache) + row * a.D + f0) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (live) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * a.D + f0) = make_uint2(w[0], w[1]);
   } else {
-    uint2 codes;
-    uint8_t sf;
-    quantise_block(x, scale, codes, sf);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * (a.D / 2) + f0 / 2) = codes;
-    (is_k ? a.ksf : a.vsf)[row * (a.D / 16) + f0 / 16] = sf;
+    uint32_t m = 0;   // the largest magnitude's bits; NaN and infinity are the largest of all
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      m = __vimax3_u32(m, __float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(x[i + 1]) & 0x7fffffffu);
+    m = max(m, __shfl_xor_sync(~0u, m, 1));
+    uint32_t sf8 = 0x7f, codes = 0;   // a NaN or an infinity: the whole block reads as NaN
+    if (m < 0x7f800000u) {
+      sf8 = e4m3_of(fminf(__fmul_rn(__uint_as_float(m), is_k ? a.k_inv : a.v_inv), 448.f));
+      const float sf = f16x2_to_f32(e4m3x2_to_f16(sf8)).x;
+      const float inv = sf > 0.f ? __frcp_rn(__fmul_rn(sf, scale)) : 0.f;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
+      codes = f32x8_to_e2m1(y);
+    }
+    if (live) {
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(cache) + row * (a.D / 2) + f0 / 2) = codes;
+      if (f0 % 16 == 0) (is_k ? a.ksf : a.vsf)[row * (a.D / 16) + f0 / 16] = (uint8_t)sf8;
+    }
   }
 }
 
-template <int FMT>
+template <int FMT, int HC>
 __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
-  const int NB = a.D / 16;
+  const int U = a.D / 8, u_log = a.D == 128 ? 4 : 3;
+  const long total = (long)a.B * a.T * U;
   const long idx = (long)blockIdx.x * 256 + threadIdx.x;
-  const long rowi = idx / NB, n = rowi / a.H;
-  if (n >= (long)a.B * a.T) return;
-  const int f0 = (int)(idx - rowi * NB) * 16, h = (int)(rowi - n * a.H);
-  const int slot = a.slots[n];
-  if (slot < 0 || slot >= (long)a.num_pages * a.page_size) {
-    if (slot != -1 && f0 == 0 && h == 0) atomicCAS(a.status, 0, kDevBadPage);
-    return;
+  const bool inside = idx < total;                   // lanes outside go along: lanes work in pairs
+  const long n = (inside ? idx : total - 1) >> u_log;
+  const int f0 = (int)(idx & (U - 1)) * 8, h0 = blockIdx.y * HC;
+  const long b = a.B == 1 ? 0 : n / a.T, t = n - b * a.T;
+  const bool rot = a.cs && f0 < a.R, half = rot && !a.interleaved, second = f0 >= a.R / 2;
+  const __nv_bfloat16* kr = a.k.p + b * a.k.sb + t * a.k.st + h0 * a.k.sh;
+  const __nv_bfloat16* vr = a.v.p + b * a.v.sb + t * a.v.st + h0 * a.v.sh;
+  uint4 wk[HC], wp[HC], wv[HC];
+#pragma unroll
+  for (int i = 0; i < HC; ++i) {
+    wk[i] = wp[i] = wv[i] = make_uint4(0, 0, 0, 0);
+    if (h0 + i < a.H) {
+      wk[i] = __ldg(reinterpret_cast<const uint4*>(kr + i * a.k.sh + f0));
+      if (half) wp[i] = __ldg(reinterpret_cast<const uint4*>(kr + i * a.k.sh + (second ? f0 - a.R / 2 : f0 + a.R / 2)));
+      wv[i] = __ldg(reinterpret_cast<const uint4*>(vr + i * a.v.sh + f0));
+    }
   }
-  const float* cs = nullptr;
-  if (a.cs) {
+  const int slot = a.slots[n];
+  bool live = inside && slot >= 0 && slot < (long)a.num_pages * a.page_size;
+  if (inside && !live && slot != -1 && f0 == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadPage);
+  float c[8], s[8];
+  if (a.cs && live) {
     const int pos = a.positions[n];
     if (pos < 0 || pos >= a.n_table) {
-      if (f0 == 0 && h == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
-      return;
+      if (f0 == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+      live = false;
+    } else if (rot) {
+      const float* cs = a.cs + (long)pos * a.R + (half ? (second ? f0 - a.R / 2 : f0) : f0 / 2);
+      if (half) {
+        load8f(cs, c);
+        load8f(cs + a.R / 2, s);
+      } else {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(cs)), y = __ldg(reinterpret_cast<const float4*>(cs + a.R / 2));
+        c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
+        s[0] = y.x, s[1] = y.y, s[2] = y.z, s[3] = y.w;
+      }
     }
-    cs = a.cs + (long)pos * a.R;
   }
-  const long b = n / a.T, t = n - b * a.T;
-  const int page = slot / a.page_size;
-  const long row = ((long)page * a.H + h) * a.page_size + (slot - page * a.page_size);
-  const __nv_bfloat16* kr = a.k.p + b * a.k.sb + t * a.k.st + h * a.k.sh;
-  const __nv_bfloat16* vr = a.v.p + b * a.v.sb + t * a.v.st + h * a.v.sh;
-  if (!GQA_CHECK(row >= 0 && row < (long)a.num_pages * a.H * a.page_size, a.status, a.dbg_line)) return;
-  float x[16];
-  load16(kr + f0, x);
-  if (cs && f0 < a.R) rotate_block(a, kr, cs, f0, x);
-  store_block<FMT>(a, true, row, f0, x);
-  load16(vr + f0, x);
-  store_block<FMT>(a, false, row, f0, x);
+  if (!live) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = s[i] = 0.f;
+  }
+  const int page = live ? slot / a.page_size : 0;
+  const long row0 = (long)page * a.H * a.page_size + (live ? slot - page * a.page_size : 0);
+#pragma unroll
+  for (int i = 0; i < HC; ++i) {
+    if (h0 + i >= a.H) break;                        // the same in all lanes
+    const long row = row0 + (long)(h0 + i) * a.page_size;
+    const bool ok = live && GQA_CHECK(row >= 0 && row < (long)a.num_pages * a.H * a.page_size, a.status, a.dbg_line);
+    float x[8], y[8];
+    bf16x8_to_f32(wk[i], x);
+    if (half) {
+      bf16x8_to_f32(wp[i], y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = second ? rot_second(x[j], y[j], c[j], s[j]) : rot_first(x[j], y[j], c[j], s[j]);
+    } else if (rot) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = x[2 * j], o = x[2 * j + 1];
+        x[2 * j] = rot_first(e, o, c[j], s[j]);
+        x[2 * j + 1] = rot_second(o, e, c[j], s[j]);
+      }
+    }
+    store8<FMT>(a, true, ok, row, f0, x);
+    bf16x8_to_f32(wv[i], x);
+    store8<FMT>(a, false, ok, row, f0, x);
+  }
 }
 
 // ------------------------------------------------------------------ gather
-__device__ __forceinline__ void block_values(const uint8_t* c4, const uint8_t* sf8, float scale, float* x) {
-  const uint2 w = *reinterpret_cast<const uint2*>(c4);
-  const uint32_t s = e4m3x2_to_f16(*sf8 | (uint32_t)*sf8 << 8);
-  uint32_t r[8];
-  e2m1x8_to_f16(w.x, r);
-  e2m1x8_to_f16(w.y, r + 4);
+// A thread takes 8 features of HC heads of a token.
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t sf8, float scale) {
+  const uint32_t s = e4m3x2_to_f16(sf8 | sf8 << 8);
+  uint32_t r[4];
+  e2m1x8_to_f16(codes, r);
+  float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const float2 v = f16x2_to_f32(hmul2_u(r[i], s));   // exact: 6 significant bits within f16's range
     x[2 * i] = v.x * scale;
     x[2 * i + 1] = v.y * scale;
   }
+  return f32_to_bf16x8(x);
 }
 
+template <int HC>
 __global__ void __launch_bounds__(256) cache_gather_kernel(const GatherArgs a) {
-  const int NB = a.D / 16;
-  const long idx = (long)blockIdx.x * 256 + threadIdx.x;
-  const long rowi = idx / NB, n = rowi / a.H;
+  const int U = a.D / 8, u_log = a.D == 128 ? 4 : 3;
+  const long idx = (long)blockIdx.x * 256 + threadIdx.x, n = idx >> u_log;
   if (n >= a.tokens) return;
-  const int blk = (int)(idx - rowi * NB), h = (int)(rowi - n * a.H);
+  const int u = (int)(idx & (U - 1)), h0 = blockIdx.y * HC;
   const int slot = a.slots[n];
-  uint4* ko = reinterpret_cast<uint4*>(a.k + rowi * a.D + blk * 16);
-  uint4* vo = reinterpret_cast<uint4*>(a.v + rowi * a.D + blk * 16);
-  if (slot < 0 || slot >= (long)a.num_pages * a.page_size) {
-    if (slot != -1 && blk == 0 && h == 0) atomicCAS(a.status, 0, kDevBadPage);
-    ko[0] = ko[1] = vo[0] = vo[1] = make_uint4(0, 0, 0, 0);
-    return;
+  const bool live = slot >= 0 && slot < (long)a.num_pages * a.page_size;
+  if (!live && slot != -1 && u == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadPage);
+  const int page = live ? slot / a.page_size : 0;
+  const long row0 = ((long)page * a.H + h0) * a.page_size + (live ? slot - page * a.page_size : 0);
+  uint32_t kc[HC], vc[HC], ks[HC], vs[HC];
+#pragma unroll
+  for (int i = 0; i < HC; ++i) {
+    kc[i] = vc[i] = ks[i] = vs[i] = 0;
+    if (live && h0 + i < a.H) {
+      const long row = row0 + (long)i * a.page_size;
+      kc[i] = __ldg(reinterpret_cast<const uint32_t*>(a.k4 + row * (a.D / 2)) + u);
+      vc[i] = __ldg(reinterpret_cast<const uint32_t*>(a.v4 + row * (a.D / 2)) + u);
+      ks[i] = __ldg(a.ksf + row * (a.D / 16) + u / 2);
+      vs[i] = __ldg(a.vsf + row * (a.D / 16) + u / 2);
+    }
   }
-  const int page = slot / a.page_size;
-  const long row = ((long)page * a.H + h) * a.page_size + (slot - page * a.page_size);
-  const long c = row * (a.D / 2) + blk * 8, s = row * NB + blk;
-  float x[16];
-  block_values(a.k4 + c, a.ksf + s, a.k_scale, x);
-  ko[0] = f32_to_bf16x8(x);
-  ko[1] = f32_to_bf16x8(x + 8);
-  block_values(a.v4 + c, a.vsf + s, a.v_scale, x);
-  vo[0] = f32_to_bf16x8(x);
-  vo[1] = f32_to_bf16x8(x + 8);
+#pragma unroll
+  for (int i = 0; i < HC; ++i) {
+    if (h0 + i >= a.H) break;
+    const long out = (n * a.H + h0 + i) * U + u;
+    reinterpret_cast<uint4*>(a.k)[out] = values8(kc[i], ks[i], a.k_scale);
+    reinterpret_cast<uint4*>(a.v)[out] = values8(vc[i], vs[i], a.v_scale);
+  }
 }
 
 bool grid_of(long threads, unsigned* blocks) {
@@ -413,35 +459,51 @@ bool grid_of(long threads, unsigned* blocks) {
 
 }  // namespace
 
-cudaError_t launch_cache_plan(const PlanArgs& a, int sms, cudaStream_t stream) {
+template <int kPer>
+static cudaError_t launch_plan_as(const PlanArgs& a, long grid, cudaStream_t stream) {
   const size_t smem = (size_t)(2 * a.B + 1) * sizeof(int);
   if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * kPlanMaxB + 1) * 4);
+    const cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel<kPer>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (2 * kPlanMaxB + 1) * 4);
     if (e != cudaSuccess) return e;
   }
-  long g = ((long)a.total + 2 * kPlanThreads - 1) / (2 * kPlanThreads);
-  if (g > sms) g = sms;
-  if (g < 1) g = 1;
   prof_begin(kProfPlan, stream);
-  cache_plan_kernel<<<(unsigned)g, kPlanThreads, smem, stream>>>(a);
+  cache_plan_kernel<kPer><<<(unsigned)grid, kPlanThreads, smem, stream>>>(a);
+  prof_end(stream);
+  return cudaGetLastError();
+}
+
+// One token a thread while that needs no more blocks than there are SMs (each
+// scans all requests anew), else four.
+cudaError_t launch_cache_plan(const PlanArgs& a, int sms, cudaStream_t stream) {
+  const long one = ((long)a.total + kPlanThreads - 1) / kPlanThreads;
+  if (one <= sms) return launch_plan_as<1>(a, one < 1 ? 1 : one, stream);
+  const long four = (one + 3) / 4;
+  return launch_plan_as<4>(a, four < sms ? four : sms, stream);
+}
+
+// Heads a thread takes: `most` if that leaves every SM two blocks or more, else
+// one, so that few tokens still spread over the SMs (one token of 40 heads: 16
+// threads a head group).
+static bool many_heads(unsigned gx, int H, int most, int sms) { return (long)gx * ((H + most - 1) / most) >= 2L * sms; }
+
+template <bool INTER>
+static cudaError_t launch_rope_as(const RopeArgs& a, int sms, cudaStream_t stream) {
+  constexpr int kHeads = 8;
+  const int H = a.Hq + a.Hkv, U = a.R / (INTER ? 8 : 16) + (a.D - a.R) / 8;
+  unsigned gx;
+  if (!grid_of((long)a.B * a.T * U, &gx)) return cudaErrorInvalidValue;
+  const bool wide = many_heads(gx, H, kHeads, sms);
+  const dim3 grid(gx, (unsigned)(wide ? (H + kHeads - 1) / kHeads : H));
+  prof_begin(kProfRope, stream);
+  if (wide) rope_kernel<kHeads, INTER><<<grid, 256, 0, stream>>>(a);
+  else rope_kernel<1, INTER><<<grid, 256, 0, stream>>>(a);
   prof_end(stream);
   return cudaGetLastError();
 }
 
 cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t stream) {
-  const int H = a.Hq + a.Hkv;
-  unsigned gx;
-  if (!grid_of((long)a.B * a.T * (a.D / 16), &gx)) return cudaErrorInvalidValue;
-  // 8 heads a thread when that still leaves every SM several blocks, else one
-  const bool wide = (long)gx * ((H + 7) / 8) >= 4L * sms;
-  const unsigned gy = (unsigned)(wide ? (H + 7) / 8 : H);
-  if (gy > 65535u) return cudaErrorInvalidValue;
-  prof_begin(kProfRope, stream);
-  if (wide) rope_kernel<8><<<dim3(gx, gy), 256, 0, stream>>>(a);
-  else rope_kernel<1><<<dim3(gx, gy), 256, 0, stream>>>(a);
-  prof_end(stream);
-  return cudaGetLastError();
+  return a.interleaved ? launch_rope_as<true>(a, sms, stream) : launch_rope_as<false>(a, sms, stream);
 }
 
 cudaError_t launch_rope_table(const RopeTableArgs& a, int sms, cudaStream_t stream) {
@@ -459,32 +521,44 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, int sms, cudaStream_t stre
     f -= floor(f);
     tt.w[i] = f < 1.0 ? (unsigned long long)ldexp(f, 64) : 0ull;
   }
-  const long total = (long)a.n * (a.R / 2);
-  long g = (total + 1023) / 1024;
+  const int H = a.R / 2, rows = 256 / H;   // positions a block takes at a time
+  long g = ((long)a.n + rows - 1) / rows;
   if (g > 8L * sms) g = 8L * sms;
-  if (g < 1) g = 1;
   prof_begin(kProfRopeTable, stream);
-  rope_table_kernel<<<(unsigned)g, 256, 0, stream>>>(a.out, a.n, a.R, a.mscale, tt);
+  rope_table_kernel<<<(unsigned)g, rows * H, 0, stream>>>(a.out, a.n, a.R, a.mscale, tt);
   prof_end(stream);
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_append(const AppendArgs& a, CacheFmt fmt, cudaStream_t stream) {
-  unsigned g;
-  if (!grid_of((long)a.B * a.T * a.H * (a.D / 16), &g)) return cudaErrorInvalidValue;
+template <int FMT>
+static cudaError_t launch_append_as(const AppendArgs& a, int sms, cudaStream_t stream) {
+  constexpr int kHeads = 4;
+  unsigned gx;
+  if (!grid_of((long)a.B * a.T * (a.D / 8), &gx)) return cudaErrorInvalidValue;
+  const bool wide = many_heads(gx, a.H, kHeads, sms);
+  const dim3 grid(gx, (unsigned)(wide ? (a.H + kHeads - 1) / kHeads : a.H));
   prof_begin(kProfAppend, stream);
-  if (fmt == kCacheBf16) cache_append_kernel<kCacheBf16><<<g, 256, 0, stream>>>(a);
-  else if (fmt == kCacheE4m3) cache_append_kernel<kCacheE4m3><<<g, 256, 0, stream>>>(a);
-  else cache_append_kernel<kCacheQ4><<<g, 256, 0, stream>>>(a);
+  if (wide) cache_append_kernel<FMT, kHeads><<<grid, 256, 0, stream>>>(a);
+  else cache_append_kernel<FMT, 1><<<grid, 256, 0, stream>>>(a);
   prof_end(stream);
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_gather(const GatherArgs& a, cudaStream_t stream) {
-  unsigned g;
-  if (!grid_of((long)a.tokens * a.H * (a.D / 16), &g)) return cudaErrorInvalidValue;
+cudaError_t launch_cache_append(const AppendArgs& a, CacheFmt fmt, int sms, cudaStream_t stream) {
+  if (fmt == kCacheBf16) return launch_append_as<kCacheBf16>(a, sms, stream);
+  if (fmt == kCacheE4m3) return launch_append_as<kCacheE4m3>(a, sms, stream);
+  return launch_append_as<kCacheQ4>(a, sms, stream);
+}
+
+cudaError_t launch_cache_gather(const GatherArgs& a, int sms, cudaStream_t stream) {
+  constexpr int kHeads = 4;
+  unsigned gx;
+  if (!grid_of((long)a.tokens * (a.D / 8), &gx)) return cudaErrorInvalidValue;
+  const bool wide = many_heads(gx, a.H, kHeads, sms);
+  const dim3 grid(gx, (unsigned)(wide ? (a.H + kHeads - 1) / kHeads : a.H));
   prof_begin(kProfGather, stream);
-  cache_gather_kernel<<<g, 256, 0, stream>>>(a);
+  if (wide) cache_gather_kernel<kHeads><<<grid, 256, 0, stream>>>(a);
+  else cache_gather_kernel<1><<<grid, 256, 0, stream>>>(a);
   prof_end(stream);
   return cudaGetLastError();
 }

@@ -34,7 +34,6 @@ struct RopeArgs {
   float sign;
   int B, T, Hq, Hkv, D;
   int* status;
-  int* dbg_line;
 };
 cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t stream);
 
@@ -58,11 +57,12 @@ struct AppendArgs {
   void *kc, *vc;             // caches; 4-bit: codes
   uint8_t *ksf, *vsf;        // 4-bit: block scales
   float k_scale, v_scale;
+  float k_inv, v_inv;        // E4M3: 1 / scale; 4-bit: 1 / (6 scale), in f32
   int B, T, H, D, page_size, num_pages;
   int* status;
   int* dbg_line;
 };
-cudaError_t launch_cache_append(const AppendArgs& a, CacheFmt fmt, cudaStream_t stream);
+cudaError_t launch_cache_append(const AppendArgs& a, CacheFmt fmt, int sms, cudaStream_t stream);
 
 struct GatherArgs {
   const int* slots;
@@ -72,7 +72,7 @@ struct GatherArgs {
   int tokens, H, D, page_size, num_pages;
   int* status;
 };
-cudaError_t launch_cache_gather(const GatherArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_gather(const GatherArgs& a, int sms, cudaStream_t stream);
 
 // 4-bit cached attention.  Codes [N, Hkv, P, D/2], block scales
 // [N, Hkv, P, D/16]; contiguous caches: N = B, P = S, no block table.
