@@ -283,123 +283,150 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* out, int n, int 
 }
 
 // ------------------------------------------------------------------ append
-// A thread takes 8 features of a token, of k and of v, in HC heads: neighbouring
-// threads write neighbouring bytes, the table row is read once for HC heads and
-// all their loads are in flight together.  Two neighbouring lanes share a block
-// of 16 features and its 4-bit scale.  In the half layout a thread also loads
-// the 8 features its own are paired with (from L1: another lane's own).
+// Bound by instructions, then by memory: 8 features are one 16-byte load, but
+// some 100 instructions to scale, round and pack.  A thread takes a part of a
+// token's row, of k and of v, in HC heads one after another, the next head's
+// loads in flight: what depends on the token alone (its place in the cache, its
+// cosines and sines) is found once.  The part is 8 features, so that
+// neighbouring threads write neighbouring 16 (8) bytes, or for 4-bit caches a
+// whole block of 16: its scale then stays in the thread.  In the half layout the
+// features paired with them are loaded too (from L1: another thread's own).
 __device__ __forceinline__ uint32_t e4m3_of(float x) { return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3); }
 
-// 8 features into row `row` of a cache; for 4 bits the lane pair (lane, lane ^ 1)
-// calls it together with the two halves of a block.
+// A part at p (of a 4-bit row: codes at p, the block's scale at sf).  to_scale:
+// E4M3 1 / scale, 4 bits 1 / (6 scale); inv: of each E4M3 code, 1 / (its value * scale).
 template <int FMT>
-__device__ __forceinline__ void store8(const AppendArgs& a, bool is_k, bool live, long row, int f0, const float* x) {
-  void* cache = is_k ? a.kc : a.vc;
-  [[maybe_unused]] const float scale = is_k ? a.k_scale : a.v_scale;
+__device__ __forceinline__ void store_part(uint8_t* p, uint8_t* sf, const float* x, float to_scale, const float* inv) {
   if constexpr (FMT == kCacheBf16) {
-    if (live) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + row * a.D + f0) = f32_to_bf16x8(x);
+    *reinterpret_cast<uint4*>(p) = f32_to_bf16x8(x);
   } else if constexpr (FMT == kCacheE4m3) {
-    const float r = is_k ? a.k_inv : a.v_inv;
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      w[i] = e4m3_of(__fmul_rn(x[4 * i], r)) | e4m3_of(__fmul_rn(x[4 * i + 1], r)) << 8 |
-             e4m3_of(__fmul_rn(x[4 * i + 2], r)) << 16 | e4m3_of(__fmul_rn(x[4 * i + 3], r)) << 24;
-    if (live) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * a.D + f0) = make_uint2(w[0], w[1]);
+      w[i] = e4m3_of(__fmul_rn(x[4 * i], to_scale)) | e4m3_of(__fmul_rn(x[4 * i + 1], to_scale)) << 8 |
+             e4m3_of(__fmul_rn(x[4 * i + 2], to_scale)) << 16 | e4m3_of(__fmul_rn(x[4 * i + 3], to_scale)) << 24;
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   } else {
     uint32_t m = 0;   // the largest magnitude's bits; NaN and infinity are the largest of all
 #pragma unroll
-    for (int i = 0; i < 8; i += 2)
+    for (int i = 0; i < 16; i += 2)
       m = __vimax3_u32(m, __float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(x[i + 1]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(~0u, m, 1));
-    uint32_t sf8 = 0x7f, codes = 0;   // a NaN or an infinity: the whole block reads as NaN
-    if (m < 0x7f800000u) {
-      sf8 = e4m3_of(fminf(__fmul_rn(__uint_as_float(m), is_k ? a.k_inv : a.v_inv), 448.f));
-      const float sf = f16x2_to_f32(e4m3x2_to_f16(sf8)).x;
-      const float inv = sf > 0.f ? __frcp_rn(__fmul_rn(sf, scale)) : 0.f;
-      float y[8];
+    // not finite: the NaN code, and codes 0
+    const bool fin = m < 0x7f800000u;
+    const uint32_t sf8 = fin ? e4m3_of(fminf(__fmul_rn(__uint_as_float(m), to_scale), 448.f)) : 0x7fu;
+    const float r = inv[sf8];
+    float y[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
-      codes = f32x8_to_e2m1(y);
-    }
-    if (live) {
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(cache) + row * (a.D / 2) + f0 / 2) = codes;
-      if (f0 % 16 == 0) (is_k ? a.ksf : a.vsf)[row * (a.D / 16) + f0 / 16] = (uint8_t)sf8;
-    }
+    for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(x[i], r);
+    const uint32_t lo = f32x8_to_e2m1(y), hi = f32x8_to_e2m1(y + 8);
+    *reinterpret_cast<uint2*>(p) = make_uint2(fin ? lo : 0u, fin ? hi : 0u);
+    *sf = (uint8_t)sf8;
   }
 }
 
-template <int FMT, int HC>
+enum { kNoRope = 0, kHalf = 1, kInter = 2 };
+
+template <int FMT, int HC, int ROT>
 __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
-  const int U = a.D / 8, u_log = a.D == 128 ? 4 : 3;
-  const long total = (long)a.B * a.T * U;
-  const long idx = (long)blockIdx.x * 256 + threadIdx.x;
-  const bool inside = idx < total;                   // lanes outside go along: lanes work in pairs
-  const long n = (inside ? idx : total - 1) >> u_log;
-  const int f0 = (int)(idx & (U - 1)) * 8, h0 = blockIdx.y * HC;
-  const long b = a.B == 1 ? 0 : n / a.T, t = n - b * a.T;
-  const bool rot = a.cs && f0 < a.R, half = rot && !a.interleaved, second = f0 >= a.R / 2;
-  const __nv_bfloat16* kr = a.k.p + b * a.k.sb + t * a.k.st + h0 * a.k.sh;
-  const __nv_bfloat16* vr = a.v.p + b * a.v.sb + t * a.v.st + h0 * a.v.sh;
-  uint4 wk[HC], wp[HC], wv[HC];
-#pragma unroll
-  for (int i = 0; i < HC; ++i) {
-    wk[i] = wp[i] = wv[i] = make_uint4(0, 0, 0, 0);
-    if (h0 + i < a.H) {
-      wk[i] = __ldg(reinterpret_cast<const uint4*>(kr + i * a.k.sh + f0));
-      if (half) wp[i] = __ldg(reinterpret_cast<const uint4*>(kr + i * a.k.sh + (second ? f0 - a.R / 2 : f0 + a.R / 2)));
-      wv[i] = __ldg(reinterpret_cast<const uint4*>(vr + i * a.v.sh + f0));
-    }
+  constexpr int G = FMT == kCacheQ4 ? 2 : 1;         // groups of 8 features of a part
+  // 1 / (sf * scale) for every block scale: rounded reciprocals, one a thread instead of one a block of features
+  __shared__ float inv[2][128];
+  if constexpr (FMT == kCacheQ4) {
+    const uint32_t code = threadIdx.x & 127;
+    const float sf = f16x2_to_f32(e4m3x2_to_f16(code)).x;
+    inv[threadIdx.x >> 7][code] = code == 0 || code == 127 ? 0.f : __frcp_rn(__fmul_rn(sf, threadIdx.x < 128 ? a.k_scale : a.v_scale));
+    __syncthreads();
   }
+  const int u_log = (a.D == 128 ? 4 : 3) - (G - 1);  // parts of a row, as a power of two
+  const long idx = (long)blockIdx.x * 256 + threadIdx.x, n = idx >> u_log;
+  if (n >= (long)a.B * a.T) return;
+  const int f0 = ((int)idx & ((1 << u_log) - 1)) * 8 * G, h0 = blockIdx.y * HC;
   const int slot = a.slots[n];
-  bool live = inside && slot >= 0 && slot < (long)a.num_pages * a.page_size;
-  if (inside && !live && slot != -1 && f0 == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadPage);
-  float c[8], s[8];
-  if (a.cs && live) {
-    const int pos = a.positions[n];
+  int pos = 0;
+  if constexpr (ROT != kNoRope) pos = a.positions[n];
+  const int heads = min(HC, a.H - h0), R2 = a.R / 2;
+  const long b = a.B == 1 ? 0 : n / a.T, t = n - b * a.T;
+  const __nv_bfloat16* kr = a.k.p + b * a.k.sb + t * a.k.st + h0 * a.k.sh + f0;
+  const __nv_bfloat16* vr = a.v.p + b * a.v.sb + t * a.v.st + h0 * a.v.sh + f0;
+  bool rot[G], second[G];                            // per group: rotated, and the second of its pairs
+#pragma unroll
+  for (int g = 0; g < G; ++g) rot[g] = ROT != kNoRope && f0 + 8 * g < a.R, second[g] = f0 + 8 * g >= R2;
+  uint4 wk[2][G], wp[2][G], wv[2][G];                // a head's rows, and the next one's
+  auto load = [&](int i, int to) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const __nv_bfloat16 *k = kr + i * a.k.sh + 8 * g, *v = vr + i * a.v.sh + 8 * g;
+      wk[to][g] = __ldg(reinterpret_cast<const uint4*>(k));
+      if (ROT == kHalf && rot[g]) wp[to][g] = __ldg(reinterpret_cast<const uint4*>(k + (second[g] ? -R2 : R2)));
+      wv[to][g] = __ldg(reinterpret_cast<const uint4*>(v));
+    }
+  };
+  load(0, 0);
+  if (slot < 0 || slot >= (long)a.num_pages * a.page_size) {
+    if (slot != -1 && f0 == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadPage);
+    return;
+  }
+  float c[G][8], s[G][8];
+  if constexpr (ROT != kNoRope) {
     if (pos < 0 || pos >= a.n_table) {
       if (f0 == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
-      live = false;
-    } else if (rot) {
-      const float* cs = a.cs + (long)pos * a.R + (half ? (second ? f0 - a.R / 2 : f0) : f0 / 2);
-      if (half) {
-        load8f(cs, c);
-        load8f(cs + a.R / 2, s);
+      return;
+    }
+    const float* cs = a.cs + (long)pos * a.R;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (!rot[g]) continue;
+      const int f = f0 + 8 * g;
+      if constexpr (ROT == kHalf) {
+        load8f(cs + (second[g] ? f - R2 : f), c[g]);
+        load8f(cs + R2 + (second[g] ? f - R2 : f), s[g]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[g][j] = second[g] ? -s[g][j] : s[g][j];   // x c + y s as x c - y (-s): the same rounding
       } else {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(cs)), y = __ldg(reinterpret_cast<const float4*>(cs + a.R / 2));
-        c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
-        s[0] = y.x, s[1] = y.y, s[2] = y.z, s[3] = y.w;
+        const float4 x = __ldg(reinterpret_cast<const float4*>(cs + f / 2)), y = __ldg(reinterpret_cast<const float4*>(cs + R2 + f / 2));
+        c[g][0] = x.x, c[g][1] = x.y, c[g][2] = x.z, c[g][3] = x.w;
+        s[g][0] = y.x, s[g][1] = y.y, s[g][2] = y.z, s[g][3] = y.w;
       }
     }
   }
-  if (!live) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = s[i] = 0.f;
-  }
-  const int page = live ? slot / a.page_size : 0;
-  const long row0 = (long)page * a.H * a.page_size + (live ? slot - page * a.page_size : 0);
+  // the part's place in the first head's row; the heads of a page are page_size rows apart
+  constexpr int kNum = FMT == kCacheBf16 ? 4 : FMT == kCacheE4m3 ? 2 : 1;   // half bytes a feature
+  const int page = slot / a.page_size, width = a.D * kNum / 2;
+  const long row = ((long)page * a.H + h0) * a.page_size + (slot - page * a.page_size);
+  if (!GQA_CHECK(row >= 0 && row + (long)(heads - 1) * a.page_size < (long)a.num_pages * a.H * a.page_size, a.status, a.dbg_line))
+    return;
+  const long at = row * width + f0 * kNum / 2, sf_at = row * (a.D / 16) + f0 / 16;
+  uint8_t *kp = static_cast<uint8_t*>(a.kc) + at, *vp = static_cast<uint8_t*>(a.vc) + at;
+  uint8_t *kf = a.ksf + sf_at, *vf = a.vsf + sf_at;
+  const long step = (long)a.page_size * width, sf_step = (long)a.page_size * (a.D / 16);
 #pragma unroll
   for (int i = 0; i < HC; ++i) {
-    if (h0 + i >= a.H) break;                        // the same in all lanes
-    const long row = row0 + (long)(h0 + i) * a.page_size;
-    const bool ok = live && GQA_CHECK(row >= 0 && row < (long)a.num_pages * a.H * a.page_size, a.status, a.dbg_line);
-    float x[8], y[8];
-    bf16x8_to_f32(wk[i], x);
-    if (half) {
-      bf16x8_to_f32(wp[i], y);
+    if (i >= heads) break;
+    if (i + 1 < HC && i + 1 < heads) load(i + 1, (i + 1) & 1);
+    float x[8 * G];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = second ? rot_second(x[j], y[j], c[j], s[j]) : rot_first(x[j], y[j], c[j], s[j]);
-    } else if (rot) {
+    for (int g = 0; g < G; ++g) {
+      bf16x8_to_f32(wk[i & 1][g], x + 8 * g);
+      if (ROT == kHalf && rot[g]) {
+        float y[8];
+        bf16x8_to_f32(wp[i & 1][g], y);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float e = x[2 * j], o = x[2 * j + 1];
-        x[2 * j] = rot_first(e, o, c[j], s[j]);
-        x[2 * j + 1] = rot_second(o, e, c[j], s[j]);
+        for (int j = 0; j < 8; ++j) x[8 * g + j] = rot_first(x[8 * g + j], y[j], c[g][j], s[g][j]);
+      }
+      if (ROT == kInter && rot[g]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = x[8 * g + 2 * j], o = x[8 * g + 2 * j + 1];
+          x[8 * g + 2 * j] = rot_first(e, o, c[g][j], s[g][j]);
+          x[8 * g + 2 * j + 1] = rot_second(o, e, c[g][j], s[g][j]);
+        }
       }
     }
-    store8<FMT>(a, true, ok, row, f0, x);
-    bf16x8_to_f32(wv[i], x);
-    store8<FMT>(a, false, ok, row, f0, x);
+    store_part<FMT>(kp, kf, x, a.k_inv, inv[0]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) bf16x8_to_f32(wv[i & 1][g], x + 8 * g);
+    store_part<FMT>(vp, vf, x, a.v_inv, inv[1]);
+    kp += step, vp += step, kf += sf_step, vf += sf_step;
   }
 }
 
@@ -530,24 +557,30 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, int sms, cudaStream_t stre
   return cudaGetLastError();
 }
 
-template <int FMT>
+template <int FMT, int ROT>
 static cudaError_t launch_append_as(const AppendArgs& a, int sms, cudaStream_t stream) {
   constexpr int kHeads = 4;
   unsigned gx;
-  if (!grid_of((long)a.B * a.T * (a.D / 8), &gx)) return cudaErrorInvalidValue;
+  if (!grid_of((long)a.B * a.T * (a.D / (FMT == kCacheQ4 ? 16 : 8)), &gx)) return cudaErrorInvalidValue;
   const bool wide = many_heads(gx, a.H, kHeads, sms);
   const dim3 grid(gx, (unsigned)(wide ? (a.H + kHeads - 1) / kHeads : a.H));
   prof_begin(kProfAppend, stream);
-  if (wide) cache_append_kernel<FMT, kHeads><<<grid, 256, 0, stream>>>(a);
-  else cache_append_kernel<FMT, 1><<<grid, 256, 0, stream>>>(a);
+  if (wide) cache_append_kernel<FMT, kHeads, ROT><<<grid, 256, 0, stream>>>(a);
+  else cache_append_kernel<FMT, 1, ROT><<<grid, 256, 0, stream>>>(a);
   prof_end(stream);
   return cudaGetLastError();
 }
 
+template <int FMT>
+static cudaError_t launch_append_rot(const AppendArgs& a, int sms, cudaStream_t stream) {
+  if (!a.cs) return launch_append_as<FMT, kNoRope>(a, sms, stream);
+  return a.interleaved ? launch_append_as<FMT, kInter>(a, sms, stream) : launch_append_as<FMT, kHalf>(a, sms, stream);
+}
+
 cudaError_t launch_cache_append(const AppendArgs& a, CacheFmt fmt, int sms, cudaStream_t stream) {
-  if (fmt == kCacheBf16) return launch_append_as<kCacheBf16>(a, sms, stream);
-  if (fmt == kCacheE4m3) return launch_append_as<kCacheE4m3>(a, sms, stream);
-  return launch_append_as<kCacheQ4>(a, sms, stream);
+  if (fmt == kCacheBf16) return launch_append_rot<kCacheBf16>(a, sms, stream);
+  if (fmt == kCacheE4m3) return launch_append_rot<kCacheE4m3>(a, sms, stream);
+  return launch_append_rot<kCacheQ4>(a, sms, stream);
 }
 
 cudaError_t launch_cache_gather(const GatherArgs& a, int sms, cudaStream_t stream) {
