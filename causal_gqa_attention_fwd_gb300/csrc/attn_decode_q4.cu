@@ -123,7 +123,7 @@ struct Combined {
   // pieces first, first + step, ... below count; at(i) is piece i's base
   template <typename At>
   __device__ __forceinline__ void add(At at, int first, int step, int count, int n, int tile, int lane) {
-    constexpr int kPer = D / 16 * 4 + 4, kBatch = TILES == 1 ? 4 : 2;
+    constexpr int kPer = D / 16 * 4 + 4, kBatch = TILES == 1 ? 8 : 2;
     const int base = n * kPer * 32 + lane;
     for (int i = first; i < count; i += kBatch * step) {
       float x[kBatch][TILES * 4], ml[kBatch][4];
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     bool fresh = true;
     // a round issues the copies of the tile kStages - 1 ahead, then takes a tile
     for (int lead = C::kStages - 1;;) {
-      if (fresh) {                       // before the copies: these loads would queue behind them
+      if (fresh && lead < C::kStages - 1) {   // before all copies but the first tile's: these loads would queue behind them
         load_queries<D, NT, PARTS>(a, cu, lane, qf, fac);
         p.clear();
         r0 = (cu.k % a.nrb) * 8 * NT;
