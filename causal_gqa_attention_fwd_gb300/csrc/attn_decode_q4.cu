@@ -556,6 +556,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   const int g = lane >> 2, t = lane & 3;
   const int upb = a.Hkv * a.nrb;
 
+  griddep_wait();                            // launched while the kernel before drains
   griddep_launch();                          // the merge waits for this grid's end in any case
   if (tid < 2 * C::kWarps) rec_kind[tid] = 0;
   // The positions of all units, and the batch row that holds the share's first:
@@ -960,6 +961,7 @@ __global__ void __launch_bounds__(512) decode_q4_merge(const DecodeQ4Args a) {
   using M = MergeCfg<D, NT>;
   __shared__ float part[16][8][32];
   griddep_wait();
+  griddep_launch();
   const Q4Head* heads = static_cast<const Q4Head*>(a.ws);
   const float* pieces = reinterpret_cast<const float*>(heads + kMaxCtas);
   const Q4Head h = heads[blockIdx.x];
@@ -1011,9 +1013,9 @@ cudaError_t run(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
     done.fetch_or(bit, std::memory_order_relaxed);
   }
   prof_begin(kProfDecode, stream);
-  decode_q4_kernel<D, NT, PARTS><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
+  e = launch_programmatic(decode_q4_kernel<D, NT, PARTS>, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, a);
   prof_end(stream);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (e != cudaSuccess) return e;
   prof_begin(kProfDecodeMerge, stream);
   e = launch_programmatic(decode_q4_merge<D, NT>, dim3(ctas), dim3(MergeCfg<D, NT>::kThreads), 0, stream, a);
   prof_end(stream);

@@ -46,6 +46,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanArgs
   int* first = plan_smem + a.B + 1; // [B] its first page's index in free_pages, -1: refused
   __shared__ long warp_need[kPlanThreads / 32], warp_add[kPlanThreads / 32];
   __shared__ int end_cursor;
+  griddep_wait();     // launched while the kernel before drains, as all kernels here
+  griddep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cursor = a.cursor ? *a.cursor : 0;
   const bool cursor_ok = cursor >= 0 && cursor <= a.num_free;
@@ -176,6 +178,8 @@ __device__ __forceinline__ void load8f(const float* p, float* x) {
 // T = 4096, 32 + 8 heads: 29 us with the loads one head after another).
 template <int HC, bool INTER>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
+  griddep_wait();
+  griddep_launch();
   const int rotated = a.R / (INTER ? 8 : 16), U = rotated + (a.D - a.R) / 8;
   const long idx = (long)blockIdx.x * 256 + threadIdx.x;
   const long n = idx / U;
@@ -268,6 +272,8 @@ struct TurnsTable {
 };
 
 __global__ void __launch_bounds__(256) rope_table_kernel(float* out, int n, int R, float mscale, const TurnsTable tt) {
+  griddep_wait();
+  griddep_launch();
   const int H = R / 2, rows = blockDim.x / H, i = threadIdx.x % H, step = rows * gridDim.x;
   const int p0 = blockIdx.x * rows + threadIdx.x / H;
   const unsigned long long w = tt.w[i], dw = w * step;
@@ -350,6 +356,8 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
     inv[threadIdx.x >> 7][code] = code == 0 || code == 127 ? 0.f : __frcp_rn(__fmul_rn(sf, threadIdx.x < 128 ? a.k_scale : a.v_scale));
     __syncthreads();
   }
+  griddep_wait();
+  griddep_launch();
   const int u_log = (a.D == 128 ? 4 : 3) - (G - 1);  // parts of a row, as a power of two
   const long idx = (long)blockIdx.x * 256 + threadIdx.x, n = idx >> u_log;
   if (n >= (long)a.B * a.T) return;
@@ -461,6 +469,8 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t sf8, float sca
 
 template <int HC>
 __global__ void __launch_bounds__(256) cache_gather_kernel(const GatherArgs a) {
+  griddep_wait();
+  griddep_launch();
   const int U = a.D / 8, u_log = a.D == 128 ? 4 : 3;
   const long idx = (long)blockIdx.x * 256 + threadIdx.x, n = idx >> u_log;
   if (n >= a.tokens) return;
@@ -508,9 +518,9 @@ static cudaError_t launch_plan_as(const PlanArgs& a, long grid, cudaStream_t str
     if (e != cudaSuccess) return e;
   }
   prof_begin(kProfPlan, stream);
-  cache_plan_kernel<kPer><<<(unsigned)grid, kPlanThreads, smem, stream>>>(a);
+  const cudaError_t e = launch_programmatic(cache_plan_kernel<kPer>, dim3((unsigned)grid), dim3(kPlanThreads), smem, stream, a);
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 // One token a thread while that needs no more blocks than there are SMs (each
@@ -536,10 +546,10 @@ static cudaError_t launch_rope_as(const RopeArgs& a, int sms, cudaStream_t strea
   const bool wide = many_heads(gx, H, kHeads, sms);
   const dim3 grid(gx, (unsigned)(wide ? (H + kHeads - 1) / kHeads : H));
   prof_begin(kProfRope, stream);
-  if (wide) rope_kernel<kHeads, INTER><<<grid, 256, 0, stream>>>(a);
-  else rope_kernel<1, INTER><<<grid, 256, 0, stream>>>(a);
+  const cudaError_t e = wide ? launch_programmatic(rope_kernel<kHeads, INTER>, grid, dim3(256), 0, stream, a)
+                             : launch_programmatic(rope_kernel<1, INTER>, grid, dim3(256), 0, stream, a);
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t stream) {
@@ -565,9 +575,10 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, int sms, cudaStream_t stre
   long g = ((long)a.n + rows - 1) / rows;
   if (g > 8L * sms) g = 8L * sms;
   prof_begin(kProfRopeTable, stream);
-  rope_table_kernel<<<(unsigned)g, rows * H, 0, stream>>>(a.out, a.n, a.R, a.mscale, tt);
+  const cudaError_t e = launch_programmatic(rope_table_kernel, dim3((unsigned)g), dim3(rows * H), 0, stream, a.out, a.n, a.R,
+                                            a.mscale, tt);
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 template <int FMT, int ROT>
@@ -578,10 +589,10 @@ static cudaError_t launch_append_as(const AppendArgs& a, int sms, cudaStream_t s
   const bool wide = many_heads(gx, a.H, kHeads, sms);
   const dim3 grid(gx, (unsigned)(wide ? (a.H + kHeads - 1) / kHeads : a.H));
   prof_begin(kProfAppend, stream);
-  if (wide) cache_append_kernel<FMT, kHeads, ROT><<<grid, 256, 0, stream>>>(a);
-  else cache_append_kernel<FMT, 1, ROT><<<grid, 256, 0, stream>>>(a);
+  const cudaError_t e = wide ? launch_programmatic(cache_append_kernel<FMT, kHeads, ROT>, grid, dim3(256), 0, stream, a)
+                             : launch_programmatic(cache_append_kernel<FMT, 1, ROT>, grid, dim3(256), 0, stream, a);
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 template <int FMT>
@@ -603,10 +614,10 @@ cudaError_t launch_cache_gather(const GatherArgs& a, int sms, cudaStream_t strea
   const bool wide = many_heads(gx, a.H, kHeads, sms);
   const dim3 grid(gx, (unsigned)(wide ? (a.H + kHeads - 1) / kHeads : a.H));
   prof_begin(kProfGather, stream);
-  if (wide) cache_gather_kernel<kHeads><<<grid, 256, 0, stream>>>(a);
-  else cache_gather_kernel<1><<<grid, 256, 0, stream>>>(a);
+  const cudaError_t e = wide ? launch_programmatic(cache_gather_kernel<kHeads>, grid, dim3(256), 0, stream, a)
+                             : launch_programmatic(cache_gather_kernel<1>, grid, dim3(256), 0, stream, a);
   prof_end(stream);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace gqa
