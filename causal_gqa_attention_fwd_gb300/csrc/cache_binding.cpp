@@ -48,7 +48,6 @@ struct Fns {
 } g_fn{};
 PyObject* g_check = nullptr;    // _binding._check(status, name)
 PyObject* g_stream = nullptr;   // the device's current stream's handle
-PyObject* g_scratch = nullptr;  // _scratch(bytes, device, stream)
 
 const char* dtype_name(at::ScalarType t) {
   switch (t) {
@@ -108,18 +107,12 @@ int bool_arg(PyObject* o) {
 }
 int dim(const at::Tensor& t, int i, const char* name) { return to_int(t.size(i), name); }
 
-void* stream_arg(PyObject* o, int dev) {
-  PyObject* h;
-  if (o == Py_None) {
-    PyObject* d = PyLong_FromLong(dev);
-    h = d ? PyObject_CallOneArg(g_stream, d) : nullptr;
-    Py_XDECREF(d);
-  } else if (PyLong_Check(o)) {
-    Py_INCREF(o);
-    h = o;
-  } else {
-    h = PyObject_GetAttrString(o, "cuda_stream");
-  }
+// The device's current stream (a call on another one makes it current first, so
+// that what it allocates is that stream's).
+void* stream_of(int dev) {
+  PyObject* d = PyLong_FromLong(dev);
+  PyObject* h = d ? PyObject_CallOneArg(g_stream, d) : nullptr;
+  Py_XDECREF(d);
   if (!h) throw Raised{};
   void* p = PyLong_AsVoidPtr(h);
   Py_DECREF(h);
@@ -190,9 +183,9 @@ PyObject* wrap2(at::Tensor a, at::Tensor b) {
 }
 
 // (cache_lens, new_lens, block_table, page_size, free_pages, cursor, total_tokens, slots, positions, cu_seqlens,
-//  lens_out, cursor_out, stream)
+//  lens_out, cursor_out)
 PyObject* plan(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 13);
+  need_args(n, 12);
   const at::Tensor &lens = tensor(a[0], "cache_lens"), &add = tensor(a[1], "new_lens"), &bt = tensor(a[2], "block_table"),
                    &pages = tensor(a[4], "free_pages");
   const int dev = device_of(lens, "cache_lens");
@@ -242,7 +235,7 @@ PyObject* plan(PyObject* const* a, Py_ssize_t n) {
                   address_of<const int>(pages, "free_pages", at::kInt, dev),
                   cursor.defined() ? address_of<const int>(cursor, "cursor", at::kInt, dev) : nullptr, p[0], p[1], p[2],
                   p[3], p[4], B, int_arg(a[3], "page_size"), dim(bt, 1, "block_table"), to_int(pages.numel(), "free_pages"),
-                  total, stream_arg(a[12], dev)),
+                  total, stream_of(dev)),
         "attn_cache_plan");
   PyObject* r = PyTuple_New(5);
   if (!r) throw Raised{};
@@ -250,9 +243,9 @@ PyObject* plan(PyObject* const* a, Py_ssize_t n) {
   return r;
 }
 
-// (out, n, rotary_dim, base, factor, original_positions, low_turns, high_turns, mscale, stream)
+// (out, n, rotary_dim, base, factor, original_positions, low_turns, high_turns, mscale)
 PyObject* rope_table(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 10);
+  need_args(n, 9);
   const at::Tensor& out = tensor(a[0], "out");
   const int dev = device_of(out, "out"), rows = int_arg(a[1], "n"), R = int_arg(a[2], "rotary_dim");
   if (out.dim() != 2 || out.size(0) != rows || out.size(1) != R)
@@ -260,15 +253,15 @@ PyObject* rope_table(PyObject* const* a, Py_ssize_t n) {
   float* p = address_of<float>(out, "out", at::kFloat, dev);
   const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
   check(g_fn.rope_table(p, rows, R, float_arg(a[3]), float_arg(a[4]), int_arg(a[5], "original_positions"), float_arg(a[6]),
-                        float_arg(a[7]), float_arg(a[8]), stream_arg(a[9], dev)),
+                        float_arg(a[7]), float_arg(a[8]), stream_of(dev)),
         "attn_rope_table");
   Py_INCREF(a[0]);
   return a[0];
 }
 
-// (backward, q, k, positions, rope_cos_sin, interleaved, q_out, k_out, stream)
+// (backward, q, k, positions, rope_cos_sin, interleaved, q_out, k_out)
 PyObject* rope(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 9);
+  need_args(n, 8);
   const bool bwd = bool_arg(a[0]);
   const at::Tensor& q = tensor(a[1], "q");
   const int dev = device_of(q, "q");
@@ -306,15 +299,15 @@ PyObject* rope(PyObject* const* a, Py_ssize_t n) {
             address(q, "q", bf, dev, false), Hkv ? address(k, "k", bf, dev, false) : nullptr,
             address(qo, "q_out", bf, dev, false), Hkv ? address(ko, "k_out", bf, dev, false) : nullptr,
             address_of<const int>(pos, "positions", at::kInt, dev), pos_stride, tab.p, tab.n, t.B, t.T, t.H, Hkv, t.D, tab.R,
-            bool_arg(a[5]), s, stream_arg(a[8], dev)),
+            bool_arg(a[5]), s, stream_of(dev)),
         bwd ? "attn_rope_bwd" : "attn_rope");
   return wrap2(std::move(qo), std::move(ko));
 }
 
-// (k, v, slots, caches, scales, positions, rope_cos_sin, interleaved, stream): two caches for bf16 (no scales) and
+// (k, v, slots, caches, scales, positions, rope_cos_sin, interleaved): two caches for bf16 (no scales) and
 // E4M3, four for 4 bits
 PyObject* append(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 9);
+  need_args(n, 8);
   const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &slots = tensor(a[2], "slots");
   const int dev = device_of(k, "k");
   const Tokens t = tokens_of(k, "k");
@@ -354,7 +347,7 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
   float ks = 1.f, vs = 1.f;
   if (!bf16) ks = (float)float_arg(PyTuple_GET_ITEM(a[4], 0)), vs = (float)float_arg(PyTuple_GET_ITEM(a[4], 1));
   const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
-  void* st = stream_arg(a[8], dev);
+  void* st = stream_of(dev);
   if (q4)
     check(g_fn.append_q4(kp, vp, sl, pos, tab.p, tab.n, tab.R, inter, c[0], c[1], c[2], c[3], ks, vs, t.B, t.T, t.H, t.D,
                          page_size, pages, s, st),
@@ -394,9 +387,9 @@ Q4Cache q4_cache(PyObject* const* a, int dev, bool paged) {
   return c;
 }
 
-// (slots, k4, k4_sf, v4, v4_sf, k_scale, v_scale, k, v, stream)
+// (slots, k4, k4_sf, v4, v4_sf, k_scale, v_scale, k, v)
 PyObject* gather(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 10);
+  need_args(n, 9);
   const at::Tensor& slots = tensor(a[0], "slots");
   const int dev = device_of(slots, "slots");
   const Q4Cache c = q4_cache(a + 1, dev, false);
@@ -411,15 +404,15 @@ PyObject* gather(PyObject* const* a, Py_ssize_t n) {
   check(g_fn.gather_q4(address_of<const int>(slots, "slots", at::kInt, dev), c.p[0], c.p[1], c.p[2], c.p[3],
                        (float)float_arg(a[5]), (float)float_arg(a[6]), address(out[0], "k", at::kBFloat16, dev),
                        address(out[1], "v", at::kBFloat16, dev), tokens, c.H, c.D, c.page_size, c.pages,
-                       stream_arg(a[9], dev)),
+                       stream_of(dev)),
         "attn_cache_gather_q4");
   return wrap2(std::move(out[0]), std::move(out[1]));
 }
 
-// (q, k4, k4_sf, v4, v4_sf, k_scale, v_scale, block_table, cache_lens, scale, o, lse, workspace, stream, rope_cos_sin);
+// (q, k4, k4_sf, v4, v4_sf, k_scale, v_scale, block_table, cache_lens, scale, o, lse, workspace, rope_cos_sin);
 // block_table None: contiguous caches
 PyObject* decode(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 15);
+  need_args(n, 14);
   const at::Tensor &q = tensor(a[0], "q"), &lens = tensor(a[8], "cache_lens");
   const at::Tensor bt = optional(a[7], "block_table");
   const int dev = device_of(q, "q");
@@ -442,19 +435,12 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   if (!lse.defined()) lse = at::empty(q.sizes().slice(0, 3), on(q, at::kFloat));
   if (o.sizes() != q.sizes() || lse.sizes() != q.sizes().slice(0, 3))
     value_error("o must be [B, Hq, Tq, D], lse [B, Hq, Tq]");
-  const Table tab = table_arg(a[14], dev);
-  if (a[14] != Py_None && tab.R != D) value_error("rope_cos_sin must be [positions, D]");
+  const Table tab = table_arg(a[13], dev);
+  if (a[13] != Py_None && tab.R != D) value_error("rope_cos_sin must be [positions, D]");
   at::Tensor ws = optional(a[12], "workspace");
   if (!ws.defined()) {
     const int64_t bytes = (int64_t)g_fn.decode_ws(B, Hq, c.H, Tq, S, D);
-    if (bytes > 0 && a[13] == Py_None) {
-      ws = at::empty({bytes}, on(q, at::kByte));
-    } else if (bytes > 0) {     // owned by the stream that uses it
-      PyObject* t = PyObject_CallFunction(g_scratch, "LiO", (long long)bytes, dev, a[13]);
-      if (!t) throw Raised{};
-      ws = THPVariable_Unpack(t);
-      Py_DECREF(t);
-    }
+    if (bytes > 0) ws = at::empty({bytes}, on(q, at::kByte));
   }
   void* wp = ws.defined() ? address(ws, "workspace", at::kByte, dev) : nullptr;
   const size_t wn = ws.defined() ? (size_t)ws.numel() : 0;
@@ -465,7 +451,7 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   const float ks = (float)float_arg(a[5]), vs = (float)float_arg(a[6]);
   const float scale = a[9] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)float_arg(a[9]);
   const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
-  void* st = stream_arg(a[13], dev);
+  void* st = stream_of(dev);
   if (paged)
     check(g_fn.decode_paged(qp, c.p[0], c.p[1], c.p[2], c.p[3], ks, vs,
                             address_of<const int>(bt, "block_table", at::kInt, dev), ln, op, lp, wp, wn, B, Hq, c.H, Tq,
@@ -478,9 +464,9 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   return wrap2(std::move(o), std::move(lse));
 }
 
-// (addresses of the C functions by name, _check, current raw stream of a device, _scratch)
+// (addresses of the C functions by name, _check, current raw stream of a device)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 4);
+  need_args(n, 3);
   auto of = [&](const char* name) {
     PyObject* v = PyDict_GetItemString(a[0], name);
     if (!v) value_error(std::string("no address of ") + name);
@@ -501,8 +487,8 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   BIND(decode, attn_decode_q4_fwd);
   BIND(decode_paged, attn_decode_paged_q4_fwd);
 #undef BIND
-  PyObject** keep[3] = {&g_check, &g_stream, &g_scratch};
-  for (int i = 0; i < 3; ++i) {
+  PyObject** keep[2] = {&g_check, &g_stream};
+  for (int i = 0; i < 2; ++i) {
     Py_INCREF(a[1 + i]);
     Py_XSETREF(*keep[i], a[1 + i]);
   }

@@ -403,7 +403,7 @@ GQA_ATTN_API attn_status attn_rope_bwd(const void* dq_out, const void* dk_out, v
  * int32).  Slot -1 writes nothing (padded tokens); any other slot outside
  * [0, num_pages * page_size) is reported (ATTN_ERR_PAGES) and writes nothing.
  * The slots of one call must differ from one another: a slot named twice
- * holds a mixture of its tokens.  rope_cos_sin (NULL: none) rotates k in f32
+ * holds a mixture of its tokens.  k and v must not overlap the caches.  rope_cos_sin (NULL: none) rotates k in f32
  * at positions[b*T + t] on the way; a token whose position is outside the
  * table is reported and not written.  strides: HOST, 6 entries: k, v.
  *   attn_cache_append      bf16 caches [num_pages, Hkv, page_size, D]

@@ -131,6 +131,24 @@ def test_binding_refuses_cpu_tensors():
         g.attn_cache_gather_q4([1], x, x, x, x, 1.0, 1.0)
 
 
+def test_workspace_size_is_the_c_functions():
+    import causal_gqa_attention_fwd_gb300 as g
+    for args in ((2, 8, 2, 1, 4096, 128), (1, 16, 1, 1, 64, 64), (3, 6, 2, 7, 100, 128)):
+        assert g.attn_decode_q4_workspace_size(*args) == int(g.lib().attn_decode_q4_workspace_size(*args)) > 0
+
+
+def test_native_module_fails_loudly_when_missing(monkeypatch):
+    import sys
+
+    from causal_gqa_attention_fwd_gb300 import _cache
+    monkeypatch.setattr(_cache, "_bound", None)
+    monkeypatch.setattr(_cache, "_mod", None)
+    monkeypatch.setitem(sys.modules, "causal_gqa_attention_fwd_gb300._cache_ext", None)
+    monkeypatch.delattr("causal_gqa_attention_fwd_gb300._cache_ext", raising=False)
+    with pytest.raises(RuntimeError, match="no fallback"):
+        _cache._ext()
+
+
 # ------------------------------------------------------------ the references
 def test_reference_quantisation_by_hand():
     """One block whose scale is exactly 1: amax 6; ties go to the even code; the sign is the top bit."""
