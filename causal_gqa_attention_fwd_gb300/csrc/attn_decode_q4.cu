@@ -246,6 +246,20 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// The low half bytes of a and the high ones of b: one three-input operation
+// (two, written with masks).
+__device__ __forceinline__ uint32_t half_bytes(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(a), "r"(b), "n"(0x0F0F0F0F));
+  return r;
+}
+// Both halves of a times one half of s.
+__device__ __forceinline__ uint32_t hmul2_half(uint32_t a, uint32_t s, bool high) {
+  const __half2 h = *reinterpret_cast<const __half2*>(&s);
+  const __half2 r = __hmul2_rn(*reinterpret_cast<const __half2*>(&a), high ? __high2half2(h) : __low2half2(h));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 template <int N>
 __device__ __forceinline__ uint32_t lds(uint32_t addr) {
   uint32_t v;
@@ -413,10 +427,12 @@ struct Loader {
   bool more;           // tiles left to issue
   int tiles;           // of the unit's tiles in the share, those from the current one on
   int keys;            // keys from the current tile on
-  int pidx, inpg;      // paged: block-table index and row in the page of the tile
-  int pbase;           // lane i holds block-table entries pbase + i and pbase + 32 + i
+  int inpg;            // row of the tile in its page (contiguous caches: a page of S rows)
+  int pidx, pbase;     // its page's block-table index; lane i holds entries pbase + i and pbase + 32 + i
   int entry[2];
-  long base;           // contiguous: offset of the tile's codes; paged: of the K/V head in a page
+  bool ok[2];          // the pages of its two 16-key halves are pages of the pool
+  long off[2];         // offsets of their codes
+  long head;           // offset of the K/V head in a page
   const uint8_t *kb, *vb, *ksb, *vsb;   // the lane's 16 bytes of a half tile at offset 0; its key's scales
 
   __device__ __forceinline__ void begin(const DecodeQ4Args& a, int lane) {
@@ -428,6 +444,19 @@ struct Loader {
   __device__ __forceinline__ int load_entry(const DecodeQ4Args& a, int e) const {   // only pages that hold keys are looked up
     return (long)e * a.page_size < u.len ? __ldg(a.block_table + (long)u.b * a.max_pages + e) : 0;
   }
+  // the halves of a tile that begins at row inpg of block-table entry pidx (pages of 16: the second half in the next)
+  __device__ __forceinline__ void to_page(const DecodeQ4Args& a) {
+    const long page_bytes = (long)a.Hkv * a.page_size * (D / 2);
+    const int p0 = __shfl_sync(~0u, entry[0], pidx - pbase);
+    ok[0] = ok[1] = (unsigned)p0 < (unsigned)a.num_pages;
+    off[0] = (ok[0] ? p0 : 0) * page_bytes + head + inpg * (D / 2);
+    off[1] = off[0] + kHalf;
+    if (a.page_size == 16) {
+      const int p1 = __shfl_sync(~0u, entry[0], pidx - pbase + 1);
+      ok[1] = (unsigned)p1 < (unsigned)a.num_pages || keys <= 16;
+      off[1] = (ok[1] ? p1 : 0) * page_bytes + head;
+    }
+  }
   // the unit's tile `tile`, if the share reaches it
   __device__ __forceinline__ void enter(const DecodeQ4Args& a, int tile, int lane) {
     tiles = min(u.nb, end - u.P) - tile;
@@ -436,14 +465,18 @@ struct Loader {
     const int j = tile * kTK;
     keys = u.len - j;
     const int hkv = u.k / a.nrb;
+    head = (long)hkv * a.page_size * (D / 2);
     if (a.block_table) {
       pidx = pbase = j / a.page_size;
       inpg = j - pidx * a.page_size;
       entry[0] = load_entry(a, pbase + lane);
       entry[1] = load_entry(a, pbase + 32 + lane);
-      base = (long)hkv * a.page_size * (D / 2);
+      to_page(a);
     } else {
-      base = (((long)u.b * a.Hkv + hkv) * a.S + j) * (D / 2);
+      inpg = j;
+      off[0] = (long)u.b * a.Hkv * a.S * (D / 2) + head + (long)j * (D / 2);
+      off[1] = off[0] + kHalf;
+      ok[0] = ok[1] = true;
     }
     // its queries, and the rotary rows of their positions, towards L2
     const int r0 = (u.k - hkv * a.nrb) * 8 * NT, n = min(8 * NT, a.R - r0) * D * 2;
@@ -456,28 +489,10 @@ struct Loader {
   // Copies the current tile to stage s.  lane_dst: where the lane's 16 bytes of a half tile go.
   __device__ __forceinline__ void issue(const DecodeQ4Args& a, uint32_t s, int lane, uint32_t lane_dst) {
     if (more) {
-      long off[2];                          // of the codes of keys 0 and 16
       bool there = keys >= kTK;
-      bool ok[2] = {true, true};
-      if (a.block_table) {
-        const int at = pidx - pbase;
-        const int p0 = __shfl_sync(~0u, entry[0], at);
-        const long page_bytes = (long)a.Hkv * a.page_size * (D / 2);
-        ok[0] = ok[1] = (unsigned)p0 < (unsigned)a.num_pages;
-        off[0] = (ok[0] ? p0 : 0) * page_bytes + base + inpg * (D / 2);
-        off[1] = off[0] + kHalf;
-        if (a.page_size == 16) {
-          const int p1 = __shfl_sync(~0u, entry[0], at + 1);
-          ok[1] = (unsigned)p1 < (unsigned)a.num_pages || keys <= 16;
-          off[1] = (ok[1] ? p1 : 0) * page_bytes + base;
-        }
-        if (!(ok[0] && ok[1])) {
-          if (keys > 0 && lane == 0) atomicCAS(a.status, 0, kDevBadPage);
-          there = false;
-        }
-      } else {
-        off[0] = base;
-        off[1] = base + kHalf;
+      if (!(ok[0] && ok[1])) {
+        if (keys > 0 && (threadIdx.x & 31) == 0) atomicCAS(a.status, 0, kDevBadPage);
+        there = false;
       }
       // the scales' offset is an eighth of the codes': 1 byte to 8
       const long f = (lane < 16 ? off[0] : off[1]) >> 3;
@@ -518,19 +533,18 @@ struct Loader {
       }
       if (--tiles > 0) {
         keys -= kTK;
-        if (a.block_table) {
-          inpg += kTK;
-          if (inpg >= a.page_size) {
-            pidx += a.page_size == 16 ? 2 : 1;
-            inpg = 0;
-            if (pidx >= pbase + 32) {
-              pbase += 32;
-              entry[0] = entry[1];
-              entry[1] = load_entry(a, pbase + 32 + lane);
-            }
+        inpg += kTK;
+        off[0] += 2 * kHalf;
+        off[1] += 2 * kHalf;
+        if (inpg >= a.page_size) {          // not in contiguous caches: the row goes on
+          pidx += a.page_size == 16 ? 2 : 1;
+          inpg = 0;
+          if (pidx >= pbase + 32) {
+            pbase += 32;
+            entry[0] = entry[1];
+            entry[1] = load_entry(a, pbase + 32 + lane);
           }
-        } else {
-          base += 2 * kHalf;
+          to_page(a);
         }
       } else {
         u.next(a);
@@ -714,10 +728,9 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
             uint32_t ra[4], rb[4];
             e2m1x8_to_f16(wa[w], ra);
             e2m1x8_to_f16(wb[w], rb);
-            const uint32_t sel = D == 128 && w >= 2 ? 0x3232u : 0x1010u;
-            const uint32_t fa = __byte_perm(sa, 0, sel), fb = __byte_perm(sb, 0, sel);
+            const bool high = D == 128 && w >= 2;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ra[i] = hmul2_u(ra[i], fa), rb[i] = hmul2_u(rb[i], fb);
+            for (int i = 0; i < 4; ++i) ra[i] = hmul2_half(ra[i], sa, high), rb[i] = hmul2_half(rb[i], sb, high);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -846,10 +859,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
           for (int v = 0; v < VW; ++v) {
             // half bytes of two keys side by side: byte i of e.. is feature 2i of both, of o.. feature 2i+1
             uint32_t e01[4], o01[4], e23[4], o23[4];
-            e2m1x8_to_f16((w[0][v] & 0x0F0F0F0Fu) | ((w[1][v] << 4) & 0xF0F0F0F0u), e01);
-            e2m1x8_to_f16(((w[0][v] >> 4) & 0x0F0F0F0Fu) | (w[1][v] & 0xF0F0F0F0u), o01);
-            e2m1x8_to_f16((w[2][v] & 0x0F0F0F0Fu) | ((w[3][v] << 4) & 0xF0F0F0F0u), e23);
-            e2m1x8_to_f16(((w[2][v] >> 4) & 0x0F0F0F0Fu) | (w[3][v] & 0xF0F0F0F0u), o23);
+            e2m1x8_to_f16(half_bytes(w[0][v], w[1][v] << 4), e01);
+            e2m1x8_to_f16(half_bytes(w[0][v] >> 4, w[1][v]), o01);
+            e2m1x8_to_f16(half_bytes(w[2][v], w[3][v] << 4), e23);
+            e2m1x8_to_f16(half_bytes(w[2][v] >> 4, w[3][v]), o23);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t a0 = hmul2_u(e01[i], f01), a1 = hmul2_u(o01[i], f01);
