@@ -293,10 +293,17 @@ __device__ __forceinline__ void row_limits(const DecodeQ4Args& a, int len, int r
   lim[1] = q + 1 == a.Tq ? len - a.Tq : lim[0] + 1;
 }
 
-// A unit's query rows as B fragments: part 0 the f16 value, part 1 (rotary
-// queries) the remainder; rows are scaled by a power of two so that their
-// largest element lies in [2^14, 2^15); fac undoes it and applies the softmax scale.
-template <int D, int NT, int PARTS>
+// How the queries reach the score MMA, whose columns are 8 query rows: their
+// bf16 values (exact in f16 after scaling); rotated, the f16 value and the f16
+// remainder, each an MMA of its own; or rotated and at most 4 rows, the values
+// in columns 0-3 and the remainders in columns 4-7 of the same MMA, added after
+// it (the 32k paged case: 50.6 us with two MMAs).
+enum { kPlain = 0, kRotated = 1, kStacked = 2 };
+
+// A unit's query rows as B fragments; rows are scaled by a power of two so that
+// their largest element lies in [2^14, 2^15); fac undoes it and applies the
+// softmax scale.
+template <int D, int NT, int MODE, int PARTS>
 __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& w, int lane, uint32_t (*qf)[PARTS][D / 16][2],
                                              float (*fac)[2]) {
   constexpr int F = D / 4;            // features of a thread
@@ -304,7 +311,7 @@ __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& 
   const int hkv = w.k / a.nrb, r0 = (w.k - hkv * a.nrb) * 8 * NT;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = r0 + n * 8 + g;
+    const int r = r0 + n * 8 + (MODE == kStacked ? g & 3 : g);
     const long row = ((long)w.b * a.Hq + hkv * a.G) * a.Tq + r;
     float x[F];
     const bool live = r < a.R;
@@ -315,7 +322,7 @@ __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& 
       if (live) v = __ldg(reinterpret_cast<const uint4*>(a.q + row * D + t * F) + c);
       u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
     }
-    if constexpr (PARTS == 2) {
+    if constexpr (MODE != kPlain) {
       // features t F.. pair with those of lane t ^ 2; a row at a negative position sees no key: any angle will do
       const int pos = max(w.len - a.Tq + r % a.Tq, 0);
       const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (long)pos * D + (t & 1) * F);
@@ -355,9 +362,11 @@ __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& 
         const float lo = x[4 * j + 2 * h] * s1 * s2, hi = x[4 * j + 2 * h + 1] * s1 * s2;
         const uint32_t v = pack_f16x2(lo, hi);
         qf[n][0][j][h] = v;
-        if constexpr (PARTS == 2) {
+        if constexpr (MODE != kPlain) {
           const float2 b = f16x2_to_f32(v);
-          qf[n][1][j][h] = pack_f16x2(lo - b.x, hi - b.y);
+          const uint32_t rest = pack_f16x2(lo - b.x, hi - b.y);
+          if constexpr (MODE == kRotated) qf[n][PARTS - 1][j][h] = rest;
+          else qf[n][0][j][h] = g < 4 ? v : rest;
         }
       }
     // the columns of S^T are rows 2t and 2t+1: their factors come from the lanes that hold those rows
@@ -557,9 +566,10 @@ struct Loader {
 
 constexpr int kStored = 1, kFirst = 2, kLast = 4;
 
-template <int D, int NT, int PARTS>
+template <int D, int NT, int MODE>
 __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(const DecodeQ4Args a) {
   using C = Q4Cfg<D, NT>;
+  constexpr int PARTS = MODE == kRotated ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int sums[C::kWarps];
   __shared__ int prefix[C::kThreads];
@@ -679,7 +689,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     // a round issues the copies of the tile kStages - 1 ahead, then takes a tile
     for (int lead = C::kStages - 1;;) {
       if (fresh && lead < C::kStages - 1) {   // before all copies but the first tile's: these loads would queue behind them
-        load_queries<D, NT, PARTS>(a, cu, lane, qf, fac);
+        load_queries<D, NT, MODE, PARTS>(a, cu, lane, qf, fac);
         p.clear();
         r0 = (cu.k % a.nrb) * 8 * NT;
 #pragma unroll
@@ -740,6 +750,12 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
                   mma_f16(sc[G][n], ra[2 * i], rb[2 * i], ra[2 * i + 1], rb[2 * i + 1], qf[n][q][2 * w + i][0],
                           qf[n][q][2 * w + i][1]);
           }
+        }
+        if constexpr (MODE == kStacked) {   // rows' values and remainders: columns c and c + 4 are lanes t and t ^ 2
+#pragma unroll
+          for (int G = 0; G < 2; ++G)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[G][0][i] += __shfl_xor_sync(~0u, sc[G][0][i], 2);
         }
         // y = s - m + kOff in log2 units, hidden keys out; the maximum moves when some y is above kOff + kLazy
         const bool edge = j0 + kTK > cu.len - a.Tq + 1;   // some key of the tile is hidden from some row
@@ -1011,7 +1027,7 @@ __global__ void __launch_bounds__(512) decode_q4_merge(const DecodeQ4Args a) {
   write_tiles<D, NT>(a, h.b, h.k, h.len, n, i, x, lane);
 }
 
-template <int D, int NT, int PARTS>
+template <int D, int NT, int MODE>
 cudaError_t run(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
   using C = Q4Cfg<D, NT>;
   // once per device: the call costs a microsecond
@@ -1021,12 +1037,12 @@ cudaError_t run(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (!bit || !(done.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
   prof_begin(kProfDecode, stream);
-  e = launch_programmatic(decode_q4_kernel<D, NT, PARTS>, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, a);
+  e = launch_programmatic(decode_q4_kernel<D, NT, MODE>, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, a);
   prof_end(stream);
   if (e != cudaSuccess) return e;
   prof_begin(kProfDecodeMerge, stream);
@@ -1046,18 +1062,20 @@ size_t decode_q4_ws_bytes(int, int Hq, int Hkv, int Tq, int, int D) {
   return sizeof(Q4Head) * kMaxCtas + (size_t)kMaxCtas * 2 * nt * (D / 16 * 4 + 4) * 128;
 }
 
+template <int D>
+static cudaError_t run_as(const DecodeQ4Args& a, int nt, int mode, int ctas, cudaStream_t stream) {
+  if (mode == kStacked) return run<D, 1, kStacked>(a, ctas, stream);
+  if (nt == 1) return mode ? run<D, 1, kRotated>(a, ctas, stream) : run<D, 1, kPlain>(a, ctas, stream);
+  return mode ? run<D, 2, kRotated>(a, ctas, stream) : run<D, 2, kPlain>(a, ctas, stream);
+}
+
 cudaError_t launch_decode_q4(const DecodeQ4Args& args, int sms, cudaStream_t stream) {
   DecodeQ4Args a = args;
   const int nt = row_tiles_of(a.R);
   a.nrb = (a.R + 8 * nt - 1) / (8 * nt);
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  const bool rope = a.rope_cs != nullptr;
-  if (a.D == 128) {
-    if (nt == 1) return rope ? run<128, 1, 2>(a, ctas, stream) : run<128, 1, 1>(a, ctas, stream);
-    return rope ? run<128, 2, 2>(a, ctas, stream) : run<128, 2, 1>(a, ctas, stream);
-  }
-  if (nt == 1) return rope ? run<64, 1, 2>(a, ctas, stream) : run<64, 1, 1>(a, ctas, stream);
-  return rope ? run<64, 2, 2>(a, ctas, stream) : run<64, 2, 1>(a, ctas, stream);
+  const int mode = !a.rope_cs ? kPlain : a.R <= 4 ? kStacked : kRotated;
+  return a.D == 128 ? run_as<128>(a, nt, mode, ctas, stream) : run_as<64>(a, nt, mode, ctas, stream);
 }
 
 }  // namespace gqa

@@ -112,6 +112,18 @@ def test_decode_q4_rope(gq, D, Tq):
     close(o, lse, reference(q, cache, lens, 0.09, tab=tab))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,Tq", [(3, 1, 1), (2, 2, 3), (6, 1, 1), (4, 2, 4), (20, 1, 1), (3, 1, 9)])
+def test_decode_q4_rope_row_counts(gq, Hq, Hkv, Tq, D):
+    """1 to 27 rotated query rows a K/V head: value and remainder in one score product (to 4 rows), in two, in blocks."""
+    B, S = 2, 517
+    lens, tab = lens_of([517, 64]), W.rope_cos_sin_table(S, D)
+    q, cache = queries(B, Hq, Tq, D, 30, 3.0), cache_of(B, Hkv, S, D, 31)
+    o, lse = run(gq, q, cache, lens, 0.08, tab=tab)
+    assert gq.get_device_status() == 0
+    close(o, lse, reference(q, cache, lens, 0.08, tab=tab))
+
+
 def paged(B, Hkv, page, mp, D, lens, seed, spare=2):
     n = B * mp + spare
     table = torch.randperm(n, generator=torch.Generator().manual_seed(seed))[:B * mp].reshape(B, mp).to(torch.int32)
