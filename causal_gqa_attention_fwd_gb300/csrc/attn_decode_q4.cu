@@ -26,7 +26,9 @@
 //      conversion gives a pair along the keys.
 // S^T's fragment has rows 2t, 2t+1 as columns, and so has O^T's: the running
 // maximum and the rescaling stay in the thread.  P goes from S^T's fragment to
-// the second product's by two 8x8 transpositions (movmatrix).
+// the second product's by two 8x8 transpositions (movmatrix).  It is rounded to
+// f16: its weights are at most 2^15, so an error is 2^-11 of the weight, and
+// 2^-24 below 2^-14, 2^-31 of the row's largest.  Scores, sums and O stay f32.
 //
 // Work: units (batch row, K/V head, block of 8*NT query rows) of 32-key tiles
 // form one stream that is shared out evenly over the grid's warps, each unit
@@ -37,6 +39,14 @@
 // directly; pieces of a unit cut between warps of a CTA are combined through
 // shared memory, those of a unit cut between CTAs through the workspace by
 // decode_q4_merge.
+//
+// Bound: long rows by the instructions that turn codes into operands.  A tile
+// of 32 keys and 128 features takes a warp some 600, and per SM sub-partition a
+// conversion (F2FP) or byte operation takes 2 cycles, an f16 multiplication 2,
+// an MMA 8, which overlap only in part: 226.6 MB of cache, queries, outputs and
+// tables take 47 us, 4.8 TB/s, 71% of a copy's rate.  Short rows by latency: 8
+// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 9.3 us, of which 3 lie
+// between the last warp's end and the end of decode_q4_merge.
 #include <math_constants.h>
 
 #include <atomic>
@@ -51,8 +61,11 @@ namespace {
 
 constexpr int kTK = 32;        // keys per tile
 constexpr int kMaxCtas = 160;  // CTAs the workspace holds pieces for
-constexpr int kUnitCost = 2;   // what a unit costs beside its tiles, in tiles
-constexpr int kMinWarps = 4;   // warps a CTA uses before the work goes to another SM
+constexpr int kUnitCost = 2;   // what a unit costs beside its tiles, in tiles (1 and 4 measure within 0.3 us of it)
+// Warps a CTA uses before work goes to another SM: pieces met in a CTA cost less than those that go through the
+// workspace, but a few warps on every SM convert faster than many on a few.  One row of 2048 keys, 2 K/V heads of
+// 128: 1 warp 9.7 us, 4 9.0, 8 9.6; 8192 keys: 10.3, 10.2, 10.4.
+constexpr int kMinWarps = 4;
 constexpr float kLazy = 8.f;   // the maximum moves when it would grow by more than 2^8 ...
 constexpr float kOff = 7.f;    // ... and P is scaled by 2^7, so P <= 2^15 and f16's smallest step is 2^-31 of a row's largest P
 
@@ -120,20 +133,22 @@ struct Combined {
 #pragma unroll
     for (int i = 0; i < TILES; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   }
-  // pieces first, first + step, ... below count; at(i) is piece i's base
+  // pieces first, first + step, ... below count; at(i) is piece i's base, its fragments' first tile and its maxima
+  // and sums lie at registers `frag` and `stat`
   template <typename At>
-  __device__ __forceinline__ void add(At at, int first, int step, int count, int n, int tile, int lane) {
-    constexpr int kPer = D / 16 * 4 + 4, kBatch = TILES == 1 ? 8 : 2;
-    const int base = n * kPer * 32 + lane;
+  __device__ __forceinline__ void add(At at, int first, int step, int count, int frag, int stat, int lane) {
+    constexpr int kBatch = TILES == 1 ? 8 : 2;
     for (int i = first; i < count; i += kBatch * step) {
       float x[kBatch][TILES * 4], ml[kBatch][4];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const float* p = at(min(i + u * step, count - 1)) + base;
+        if (TILES > 1 || i + u * step < count) {   // in shared memory a load more costs less than the guard
+          const float* p = at(min(i + u * step, count - 1)) + lane;
 #pragma unroll
-        for (int j = 0; j < 4 * TILES; ++j) x[u][j] = p[32 * (4 * tile + j)];
+          for (int j = 0; j < 4 * TILES; ++j) x[u][j] = p[32 * (frag + j)];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ml[u][j] = p[32 * (D / 4 + j)];
+          for (int j = 0; j < 4; ++j) ml[u][j] = p[32 * (stat + j)];
+        }
       }
       float top[2] = {m[0], m[1]};
 #pragma unroll
@@ -297,7 +312,7 @@ __device__ __forceinline__ void row_limits(const DecodeQ4Args& a, int len, int r
 // bf16 values (exact in f16 after scaling); rotated, the f16 value and the f16
 // remainder, each an MMA of its own; or rotated and at most 4 rows, the values
 // in columns 0-3 and the remainders in columns 4-7 of the same MMA, added after
-// it (the 32k paged case: 50.6 us with two MMAs).
+// it (8 rows of 24k keys on average, 8 K/V heads, 4 queries each: 47 us, 51 with two MMAs).
 enum { kPlain = 0, kRotated = 1, kStacked = 2 };
 
 // A unit's query rows as B fragments; rows are scaled by a power of two so that
@@ -952,8 +967,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
       const int n = qd * 4 / C::kMT, i = qd * 4 % C::kMT, rank = __popc(taken & ((1u << s0) - 1));
       Combined<D, 4> x;
       x.clear();
-      x.add([&](int j) -> const float* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, 0, 1, __popc(slots), n, i,
-            lane);
+      x.add([&](int j) -> const float* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, 0, 1, __popc(slots),
+            n * Piece4<D, NT>::kPer + 4 * i, n * Piece4<D, NT>::kPer + D / 4, lane);
       if (first && last) {
         const Unit u = rec_unit[s0];
         write_tiles<D, NT>(a, u.b, u.k, u.len, n, i, x, lane);
@@ -974,54 +989,55 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   if (tid == 0) heads[blockIdx.x] = head;
 }
 
-// Units cut between CTAs: the block of the second CTA that holds a piece of a
-// unit combines all of them.  A warp takes every kGroups-th piece of a
-// 16-feature tile; the groups meet in shared memory.
-template <int D, int NT>
-struct MergeCfg {
-  static constexpr int kTiles = NT * D / 16;
-  static constexpr int kGroups = 16 / kTiles;
-  static constexpr int kThreads = 512;
-};
+// Units cut between CTAs.  A warp combines a 16-feature tile of up to
+// kMergePieces pieces (their loads in flight together); with more pieces, 2, 4,
+// 8 or 16 groups of warps share them and meet in shared memory, and the tiles
+// go to several blocks: those of the CTAs from the second on that hold a piece
+// (there are more of them than blocks needed).  One row of 8192 keys, 2 K/V
+// heads of 128: 10.0 us, and 14.7 with one block for a unit.
+constexpr int kMergeLog = 4, kMergeWarps = 1 << kMergeLog;
+constexpr int kMergePieces = 4;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(512) decode_q4_merge(const DecodeQ4Args a) {
+__global__ void __launch_bounds__(kMergeWarps * 32) decode_q4_merge(const DecodeQ4Args a) {
   using C = Q4Cfg<D, NT>;
-  using M = MergeCfg<D, NT>;
-  __shared__ float part[16][8][32];
+  constexpr int kTilesLog = NT * C::kMT == 16 ? 4 : NT * C::kMT == 8 ? 3 : 2, kPer = Piece4<D, NT>::kPer;
+  __shared__ float part[kMergeWarps][8 * 32];   // per warp: a tile's fragment, maxima, sums
   griddep_wait();
   griddep_launch();
   const Q4Head* heads = static_cast<const Q4Head*>(a.ws);
   const float* pieces = reinterpret_cast<const float*>(heads + kMaxCtas);
   const Q4Head h = heads[blockIdx.x];
-  if (h.first < 0 || (int)blockIdx.x != h.first + 1) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tt = warp % M::kTiles, group = warp / M::kTiles;
-  const int n = tt / C::kMT, i = tt % C::kMT;
+  if (h.first < 0) return;
+  const int count = h.last - h.first + 1;
+  const int groups_log = min(count <= kMergePieces ? 0 : 32 - __clz((count - 1) / kMergePieces), kMergeLog);
+  const int tiles_log = min(kMergeLog - groups_log, kTilesLog), groups = 1 << groups_log;
+  const int block = blockIdx.x - h.first - 1;
+  if (block >> (kTilesLog - tiles_log)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tt = warp & ((1 << tiles_log) - 1), group = warp >> tiles_log;
+  const int tile = (block << tiles_log) + tt, n = tile / C::kMT, i = tile % C::kMT;
   Combined<D, 1> x;
   x.clear();
-  x.add([&](int j) -> const float* { return pieces + ((long)(h.first + j) * 2 + (j == 0)) * C::kRec * 32; }, group, M::kGroups,
-        h.last - h.first + 1, n, i, lane);
-  if constexpr (M::kGroups > 1) {
-    if (group > 0) {
+  if (group < groups)
+    x.add([&](int j) -> const float* { return pieces + ((long)(h.first + j) * 2 + (j == 0)) * C::kRec * 32; }, group, groups,
+          count, n * kPer + 4 * i, n * kPer + D / 4, lane);
+  if (groups > 1) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) part[warp][j][lane] = x.acc[0][j];
+    for (int j = 0; j < 4; ++j) part[warp][32 * j + lane] = x.acc[0][j];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) part[warp][4 + c][lane] = x.m[c], part[warp][6 + c][lane] = x.l[c];
-    }
+    for (int c = 0; c < 2; ++c) part[warp][32 * (4 + c) + lane] = x.m[c], part[warp][32 * (6 + c) + lane] = x.l[c];
     __syncthreads();
-    if (group > 0) return;
+  }
+  if (group > 0) return;
+#pragma unroll 3
+  for (int q = 1; q < groups; ++q) {
+    const float* p = part[(q << tiles_log) + tt] + lane;
+    const float y[4] = {p[0], p[32], p[64], p[96]};
 #pragma unroll
-    for (int q = 1; q < M::kGroups; ++q) {
-      const int w = q * M::kTiles + tt;
-      float y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = part[w][j][lane];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float mp = part[w][4 + c][lane];
-        x.scale_to(c, fmaxf(x.m[c], mp));
-        x.accumulate(c, mp, part[w][6 + c][lane], y);
-      }
+    for (int c = 0; c < 2; ++c) {
+      const float mp = p[32 * (4 + c)], lp = p[32 * (6 + c)];
+      x.scale_to(c, fmaxf(x.m[c], mp));
+      x.accumulate(c, mp, lp, y);
     }
   }
   write_tiles<D, NT>(a, h.b, h.k, h.len, n, i, x, lane);
@@ -1046,7 +1062,7 @@ cudaError_t run(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
   prof_end(stream);
   if (e != cudaSuccess) return e;
   prof_begin(kProfDecodeMerge, stream);
-  e = launch_programmatic(decode_q4_merge<D, NT>, dim3(ctas), dim3(MergeCfg<D, NT>::kThreads), 0, stream, a);
+  e = launch_programmatic(decode_q4_merge<D, NT>, dim3(ctas), dim3(kMergeWarps * 32), 0, stream, a);
   prof_end(stream);
   return e;
 }
@@ -1054,7 +1070,9 @@ cudaError_t run(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
 }  // namespace
 
 // Rows go in blocks of 16 (two 8-row tiles, one conversion of the cache for
-// both) unless one tile of 8 holds them all.
+// both) unless one tile of 8 holds them all: 8 rows of 8192 keys, 8 K/V heads,
+// blocks of 16 against 8: 16 query rows a head 27.8 us against 34.4 (D = 64:
+// 21.2, 24.3), 8 query rows 27.7 against 23.4 (21.1, 17.5).
 static int row_tiles_of(int R) { return R <= 8 ? 1 : 2; }
 
 size_t decode_q4_ws_bytes(int, int Hq, int Hkv, int Tq, int, int D) {
