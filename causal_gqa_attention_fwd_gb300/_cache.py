@@ -5,8 +5,9 @@ over 4-bit caches.
 All tensors of a call are on one device, which need not be the current one; the
 kernels run on ``stream`` (a torch.cuda.Stream or a handle), or on that device's
 current stream, and so is allocated what the call allocates: an output used on
-another stream afterwards needs Tensor.record_stream, as ever.  Checks, output allocation and the C calls are native
-(csrc/cache_binding.cpp): a decode step's calls take a few microseconds each.
+another stream afterwards needs Tensor.record_stream, as ever.  Checks, output
+allocation and the C calls are native (csrc/cache_binding.cpp): a decode step's
+calls take a few microseconds each.
 """
 from __future__ import annotations
 
@@ -71,7 +72,7 @@ def attn_rope_table(n: int, rotary_dim: int, base: float = 10000.0, factor: floa
     original context (all below low_turns, none above high_turns, in between blended); entries times mscale."""
     def make(out):
         if out is None:
-            out = torch.empty(n, rotary_dim, dtype=torch.float32, device=device or "cuda")
+            out = torch.empty(n, rotary_dim, dtype=torch.float32, device="cuda" if device is None else device)
         return _ext().rope_table(out, n, rotary_dim, base, factor, original_positions, low_turns, high_turns, mscale)
     return _run(stream, make, out)
 

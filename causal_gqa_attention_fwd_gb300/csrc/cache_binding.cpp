@@ -8,6 +8,7 @@
 // functions are not linked: bind() gets their addresses from the ctypes handle
 // of the library that _binding has loaded.
 #include <Python.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
@@ -164,6 +165,7 @@ Table table_arg(PyObject* o, int dev) {
   t.p = address_of<const float>(x, "rope_cos_sin", at::kFloat, dev);
   t.n = dim(x, 0, "rope_cos_sin");
   t.R = dim(x, 1, "rope_cos_sin");
+  if (t.n == 0) value_error("rope_cos_sin holds no position");   // its NULL would mean: no rotation
   return t;
 }
 
@@ -203,7 +205,7 @@ PyObject* plan(PyObject* const* a, Py_ssize_t n) {
   }
   if (total < 0) value_error("total_tokens must not be negative");
   static const char* names[5] = {"slots", "positions", "cu_seqlens", "lens_out", "cursor_out"};
-  const int64_t sizes[5] = {total, total, B + 1, B, 1};
+  const int64_t sizes[5] = {total, total, (int64_t)B + 1, B, 1};
   at::Tensor out[5];
   int* p[5];
   bool missing = false;
@@ -213,7 +215,7 @@ PyObject* plan(PyObject* const* a, Py_ssize_t n) {
   }
   if (missing) {
     // one allocation, and parts of it that do not go through the dispatcher (five of them took 6 us)
-    const at::Tensor all = at::empty({2 * (int64_t)total + 2 * B + 2}, on(lens, at::kInt));
+    const at::Tensor all = at::empty({2 * (int64_t)total + 2 * (int64_t)B + 2}, on(lens, at::kInt));
     int64_t at_entry = 0;
     for (int i = 0; i < 5; at_entry += sizes[i++]) {
       if (out[i].defined()) continue;
@@ -503,8 +505,8 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
   } catch (const Raised&) {
   } catch (const Refused& e) {
     PyErr_SetString(e.type, e.what());
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception&) {
+    torch::translate_exception_to_python(std::current_exception());   // torch.OutOfMemoryError and the like
   }
   return nullptr;
 }

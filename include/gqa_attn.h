@@ -372,9 +372,9 @@ GQA_ATTN_API attn_status attn_cache_plan(const int* cache_lens, const int* new_l
  *   over the original context and g = clamp((t_i - low_turns) /
  *   (high_turns - low_turns), 0, 1), theta_i g + (theta_i / factor) (1 - g).
  * Cosines and sines are multiplied by mscale.  The angle of a position is
- * taken in fixed point (64 bits of a turn), so that far positions lose
- * nothing; entries are within 2^-22 |mscale| of the exact ones.  rotary_dim:
- * a multiple of 16, at most 512.  base > 1, factor > 0, low_turns <
+ * taken in fixed point (64 bits of a turn from a frequency in double), so that
+ * far positions lose little: entries whose angle is below 2^24 are within
+ * 2^-22 |mscale| of the exact ones.  rotary_dim: a multiple of 16, at most 512.  base > 1, factor > 0, low_turns <
  * high_turns, all finite. */
 GQA_ATTN_API attn_status attn_rope_table(float* rope_cos_sin, int n, int rotary_dim, double base, double factor,
                                          int original_positions, double low_turns, double high_turns, double mscale,
