@@ -1,6 +1,6 @@
-// fp4.cuh -- the 4-bit cache format: E2M1 codes, an E4M3 scale for 16
-// features, and token views of bf16 tensors; shared by the kernels that write
-// and read the cache.
+// fp4.cuh -- conversions of the 4-bit cache format (E2M1 codes, an E4M3 scale
+// for 16 features) and of 8 bf16 at a time, for the kernels that write and
+// read caches.
 #pragma once
 
 #include <cuda_fp16.h>

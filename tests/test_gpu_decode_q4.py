@@ -124,6 +124,18 @@ def test_decode_q4_rope_row_counts(gq, Hq, Hkv, Tq, D):
     close(o, lse, reference(q, cache, lens, 0.08, tab=tab))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,S", [(4, 1, 20001), (16, 1, 20001), (40, 1, 9000), (16, 2, 12345), (6, 3, 9000), (80, 5, 6000),
+                                      (24, 12, 2500), (16, 16, 1300)])
+def test_decode_q4_units_cut_between_many_ctas(gq, Hq, Hkv, S, D):
+    """From a row whose only unit every CTA has a piece of, to units of a few pieces: each number of merging groups."""
+    lens = lens_of([S])
+    q, cache = queries(1, Hq, 1, D, 50), cache_of(1, Hkv, S, D, 51)
+    o, lse = run(gq, q, cache, lens, 1 / math.sqrt(D))
+    assert gq.get_device_status() == 0
+    close(o, lse, reference(q, cache, lens, 1 / math.sqrt(D)))
+
+
 def paged(B, Hkv, page, mp, D, lens, seed, spare=2):
     n = B * mp + spare
     table = torch.randperm(n, generator=torch.Generator().manual_seed(seed))[:B * mp].reshape(B, mp).to(torch.int32)
