@@ -44,8 +44,8 @@
 // of 32 keys and 128 features takes a warp some 600, and per SM sub-partition a
 // conversion (F2FP) or byte operation takes 2 cycles, an f16 multiplication 2,
 // an MMA 8, which overlap only in part: 226.6 MB of cache, queries, outputs and
-// tables take 47 us, 4.8 TB/s, 71% of a copy's rate.  Short rows by latency: 8
-// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 9.3 us, of which 3 lie
+// tables take 46 us, 4.9 TB/s, 72% of a copy's rate.  Short rows by latency: 8
+// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 9.2 us, of which 3 lie
 // between the last warp's end and the end of decode_q4_merge.
 #include <math_constants.h>
 
@@ -79,18 +79,19 @@ struct Q4Cfg {
   static constexpr int kSf = kTK * D / 16;          // bytes of its block scales
   static constexpr int kStage = 2 * kCodes + 2 * kSf;
   static constexpr int kRing = kStages * kStage;    // per warp
-  static constexpr int kRec = NT * (kMT * 4 + 4);   // f32 of a piece per lane: per 8 rows O^T's fragments, maxima, sums
-  static constexpr int kSmem = kWarps * (kRing + kRec * 128);   // rings, then a piece per warp
-  static_assert(kRec * 128 <= kRing, "a warp's last piece goes into its drained ring");
+  static constexpr int kRec = NT * (kMT + 1);       // float4 of a piece per lane: per 8 rows O^T's fragments, maxima and sums
+  static constexpr int kSmem = kWarps * (kRing + kRec * 512);   // rings, then a piece per warp
+  static_assert(kRec * 512 <= kRing, "a warp's last piece goes into its drained ring");
   static_assert(kSmem <= 227 * 1024 - 4096, "shared memory");
 };
 
 // A thread's part of a piece: O^T fragments and, for its two columns of each
 // 8-row tile, the maximum (log2 units, the same in all lanes of a column) and
-// its own keys' sum.  Stored as f32 [register][lane].
+// its own keys' sum.  Stored per 8 rows as kPer float4 a lane: a tile's
+// fragment each, then both maxima and sums.
 template <int D, int NT>
 struct Piece4 {
-  static constexpr int kPer = D / 16 * 4 + 4;   // registers per 8 rows
+  static constexpr int kPer = D / 16 + 1;
   float acc[NT][D / 16][4];
   float m[NT][2], l[NT][2];
 
@@ -105,19 +106,13 @@ struct Piece4 {
       l[n][0] = l[n][1] = 0.f;
     }
   }
-  __device__ __forceinline__ void store(float* p, int lane) const {
+  __device__ __forceinline__ void store(float4* p, int lane) const {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float* q = p + n * kPer * 32 + lane;
+      float4* q = p + n * kPer * 32 + lane;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[32 * (4 * i + j)] = acc[n][i][j];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        q[32 * (D / 4 + c)] = m[n][c];
-        q[32 * (D / 4 + 2 + c)] = l[n][c];
-      }
+      for (int i = 0; i < D / 16; ++i) q[32 * i] = make_float4(acc[n][i][0], acc[n][i][1], acc[n][i][2], acc[n][i][3]);
+      q[32 * (D / 16)] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
     }
   }
 };
@@ -133,35 +128,31 @@ struct Combined {
 #pragma unroll
     for (int i = 0; i < TILES; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   }
-  // pieces first, first + step, ... below count; at(i) is piece i's base, its fragments' first tile and its maxima
-  // and sums lie at registers `frag` and `stat`
+  // pieces first, first + step, ... below count; at(i) is piece i's base, where its fragments' first tile is float4
+  // `frag`, its maxima and sums `stat`
   template <typename At>
   __device__ __forceinline__ void add(At at, int first, int step, int count, int frag, int stat, int lane) {
     constexpr int kBatch = TILES == 1 ? 8 : 2;
     for (int i = first; i < count; i += kBatch * step) {
-      float x[kBatch][TILES * 4], ml[kBatch][4];
+      float4 x[kBatch][TILES], ml[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         if (TILES > 1 || i + u * step < count) {   // in shared memory a load more costs less than the guard
-          const float* p = at(min(i + u * step, count - 1)) + lane;
+          const float4* p = at(min(i + u * step, count - 1)) + lane;
 #pragma unroll
-          for (int j = 0; j < 4 * TILES; ++j) x[u][j] = p[32 * (frag + j)];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) ml[u][j] = p[32 * (stat + j)];
+          for (int j = 0; j < TILES; ++j) x[u][j] = p[32 * (frag + j)];
+          ml[u] = p[32 * stat];
         }
       }
       float top[2] = {m[0], m[1]};
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        if (i + u * step < count) top[0] = fmaxf(top[0], ml[u][0]), top[1] = fmaxf(top[1], ml[u][1]);
+        if (i + u * step < count) top[0] = fmaxf(top[0], ml[u].x), top[1] = fmaxf(top[1], ml[u].y);
 #pragma unroll
       for (int c = 0; c < 2; ++c) scale_to(c, top[c]);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        if (i + u * step < count) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) accumulate(c, ml[u][c], ml[u][2 + c], x[u]);
-        }
+        if (i + u * step < count) accumulate(ml[u], x[u]);
     }
   }
   __device__ __forceinline__ void scale_to(int c, float top) {
@@ -171,13 +162,17 @@ struct Combined {
 #pragma unroll
     for (int i = 0; i < TILES; ++i) acc[i][c] *= f, acc[i][2 + c] *= f;
   }
-  __device__ __forceinline__ void accumulate(int c, float mp, float lp, const float* x) {   // mp <= m[c]
-    const float f = mp == -CUDART_INF_F ? 1.f : ex2_approx(mp - m[c]);
-    l[c] = fmaf(lp, f, l[c]);
+  __device__ __forceinline__ void accumulate(const float4& ml, const float4* x) {   // ml's maxima <= m
+    const float f0 = ml.x == -CUDART_INF_F ? 1.f : ex2_approx(ml.x - m[0]);
+    const float f1 = ml.y == -CUDART_INF_F ? 1.f : ex2_approx(ml.y - m[1]);
+    l[0] = fmaf(ml.z, f0, l[0]);
+    l[1] = fmaf(ml.w, f1, l[1]);
 #pragma unroll
     for (int i = 0; i < TILES; ++i) {
-      acc[i][c] = fmaf(x[4 * i + c], f, acc[i][c]);
-      acc[i][2 + c] = fmaf(x[4 * i + 2 + c], f, acc[i][2 + c]);
+      acc[i][0] = fmaf(x[i].x, f0, acc[i][0]);
+      acc[i][1] = fmaf(x[i].y, f1, acc[i][1]);
+      acc[i][2] = fmaf(x[i].z, f0, acc[i][2]);
+      acc[i][3] = fmaf(x[i].w, f1, acc[i][3]);
     }
   }
 };
@@ -225,10 +220,10 @@ struct Unit {
 // Where slot s of a CTA's 2 * kWarps stored pieces lies: 2w is warp w's first
 // piece, 2w + 1 its last, which replaces the ring.
 template <int D, int NT>
-__device__ __forceinline__ float* piece_at(uint8_t* smem, int s) {
+__device__ __forceinline__ float4* piece_at(uint8_t* smem, int s) {
   using C = Q4Cfg<D, NT>;
-  return reinterpret_cast<float*>(s & 1 ? smem + (s >> 1) * C::kRing
-                                        : smem + C::kWarps * C::kRing + (s >> 1) * C::kRec * 128);
+  return reinterpret_cast<float4*>(s & 1 ? smem + (s >> 1) * C::kRing
+                                         : smem + C::kWarps * C::kRing + (s >> 1) * C::kRec * 512);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
@@ -433,7 +428,7 @@ __device__ __forceinline__ void write_tiles(const DecodeQ4Args& a, int b, int k,
   write_rows<D, TILES>(a, b, hkv, r0, lim, tile, x.acc, x.m, x.l, lane);
 }
 
-// Workspace: a header per CTA, then two pieces a CTA (kRec * 32 f32 each): 0 of
+// Workspace: a header per CTA, then two pieces a CTA (kRec * 32 float4 each): 0 of
 // the unit begun before the CTA's share, 1 of the one that goes on after it.
 struct Q4Head {
   int b, k, len;   // the unit begun before the CTA's share
@@ -490,6 +485,13 @@ struct Loader {
     keys = u.len - j;
     const int hkv = u.k / a.nrb;
     head = (long)hkv * a.page_size * (D / 2);
+    // its queries, and the rotary rows of their positions, towards L2 (before the wait for the block table)
+    const int r0 = (u.k - hkv * a.nrb) * 8 * NT, n = min(8 * NT, a.R - r0) * D * 2;
+    const char* q = reinterpret_cast<const char*>(a.q + (((long)u.b * a.Hq + hkv * a.G) * a.Tq + r0) * D);
+    if (lane * 128 < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
+    const int pos = u.len - a.Tq + (lane >> 2);
+    if (a.rope_cs && (lane >> 2) < a.Tq && pos >= 0 && (lane & 3) < D / 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope_cs + (long)pos * D + (lane & 3) * 32));
     if (a.block_table) {
       pidx = pbase = j / a.page_size;
       inpg = j - pidx * a.page_size;
@@ -502,13 +504,6 @@ struct Loader {
       off[1] = off[0] + kHalf;
       ok[0] = ok[1] = true;
     }
-    // its queries, and the rotary rows of their positions, towards L2
-    const int r0 = (u.k - hkv * a.nrb) * 8 * NT, n = min(8 * NT, a.R - r0) * D * 2;
-    const char* q = reinterpret_cast<const char*>(a.q + (((long)u.b * a.Hq + hkv * a.G) * a.Tq + r0) * D);
-    if (lane * 128 < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
-    const int pos = u.len - a.Tq + (lane >> 2);
-    if (a.rope_cs && (lane >> 2) < a.Tq && pos >= 0 && (lane & 3) < D / 32)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope_cs + (long)pos * D + (lane & 3) * 32));
   }
   // Copies the current tile to stage s.  lane_dst: where the lane's 16 bytes of a half tile go.
   __device__ __forceinline__ void issue(const DecodeQ4Args& a, uint32_t s, int lane, uint32_t lane_dst) {
@@ -945,7 +940,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   if (kind) order[warp][__popc(earlier)] = (uint8_t)lane;   // the slots taken, in stream order
   __syncwarp();
   Q4Head* heads = static_cast<Q4Head*>(a.ws);
-  float* pieces = reinterpret_cast<float*>(heads + kMaxCtas);
+  float4* pieces = reinterpret_cast<float4*>(heads + kMaxCtas);
   Q4Head head{};
   head.first = -1;
   constexpr int kQuads = NT * C::kMT / 4;   // a warp takes four tiles of a unit at a time, units and quads in turn
@@ -967,22 +962,16 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
       const int n = qd * 4 / C::kMT, i = qd * 4 % C::kMT, rank = __popc(taken & ((1u << s0) - 1));
       Combined<D, 4> x;
       x.clear();
-      x.add([&](int j) -> const float* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, 0, 1, __popc(slots),
-            n * Piece4<D, NT>::kPer + 4 * i, n * Piece4<D, NT>::kPer + D / 4, lane);
+      x.add([&](int j) -> const float4* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, 0, 1, __popc(slots),
+            n * Piece4<D, NT>::kPer + i, n * Piece4<D, NT>::kPer + C::kMT, lane);
       if (first && last) {
         const Unit u = rec_unit[s0];
         write_tiles<D, NT>(a, u.b, u.k, u.len, n, i, x, lane);
       } else {
-        float* q = pieces + ((long)blockIdx.x * 2 + first) * C::kRec * 32 + n * Piece4<D, NT>::kPer * 32 + lane;
+        float4* q = pieces + ((long)blockIdx.x * 2 + first) * C::kRec * 32 + n * Piece4<D, NT>::kPer * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) q[32 * (4 * i + j)] = x.acc[j >> 2][j & 3];
-        if (i == 0) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            q[32 * (D / 4 + c)] = x.m[c];
-            q[32 * (D / 4 + 2 + c)] = x.l[c];
-          }
-        }
+        for (int j = 0; j < 4; ++j) q[32 * (i + j)] = make_float4(x.acc[j][0], x.acc[j][1], x.acc[j][2], x.acc[j][3]);
+        if (i == 0) q[32 * C::kMT] = make_float4(x.m[0], x.m[1], x.l[0], x.l[1]);
       }
     }
   }
@@ -994,7 +983,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
 // 8 or 16 groups of warps share them and meet in shared memory, and the tiles
 // go to several blocks: those of the CTAs from the second on that hold a piece
 // (there are more of them than blocks needed).  One row of 8192 keys, 2 K/V
-// heads of 128: 10.0 us, and 14.7 with one block for a unit.
+// heads of 128: 9.9 us, and 14.7 with one block for a unit.
 constexpr int kMergeLog = 4, kMergeWarps = 1 << kMergeLog;
 constexpr int kMergePieces = 4;
 
@@ -1002,11 +991,11 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kMergeWarps * 32) decode_q4_merge(const DecodeQ4Args a) {
   using C = Q4Cfg<D, NT>;
   constexpr int kTilesLog = NT * C::kMT == 16 ? 4 : NT * C::kMT == 8 ? 3 : 2, kPer = Piece4<D, NT>::kPer;
-  __shared__ float part[kMergeWarps][8 * 32];   // per warp: a tile's fragment, maxima, sums
+  __shared__ float4 part[kMergeWarps][2][32];   // per warp: a tile's fragment, maxima and sums
   griddep_wait();
   griddep_launch();
   const Q4Head* heads = static_cast<const Q4Head*>(a.ws);
-  const float* pieces = reinterpret_cast<const float*>(heads + kMaxCtas);
+  const float4* pieces = reinterpret_cast<const float4*>(heads + kMaxCtas);
   const Q4Head h = heads[blockIdx.x];
   if (h.first < 0) return;
   const int count = h.last - h.first + 1;
@@ -1019,26 +1008,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_q4_merge(const Decode
   Combined<D, 1> x;
   x.clear();
   if (group < groups)
-    x.add([&](int j) -> const float* { return pieces + ((long)(h.first + j) * 2 + (j == 0)) * C::kRec * 32; }, group, groups,
-          count, n * kPer + 4 * i, n * kPer + D / 4, lane);
+    x.add([&](int j) -> const float4* { return pieces + ((long)(h.first + j) * 2 + (j == 0)) * C::kRec * 32; }, group, groups,
+          count, n * kPer + i, n * kPer + C::kMT, lane);
   if (groups > 1) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) part[warp][32 * j + lane] = x.acc[0][j];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) part[warp][32 * (4 + c) + lane] = x.m[c], part[warp][32 * (6 + c) + lane] = x.l[c];
+    part[warp][0][lane] = make_float4(x.acc[0][0], x.acc[0][1], x.acc[0][2], x.acc[0][3]);
+    part[warp][1][lane] = make_float4(x.m[0], x.m[1], x.l[0], x.l[1]);
     __syncthreads();
   }
   if (group > 0) return;
 #pragma unroll 3
   for (int q = 1; q < groups; ++q) {
-    const float* p = part[(q << tiles_log) + tt] + lane;
-    const float y[4] = {p[0], p[32], p[64], p[96]};
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float mp = p[32 * (4 + c)], lp = p[32 * (6 + c)];
-      x.scale_to(c, fmaxf(x.m[c], mp));
-      x.accumulate(c, mp, lp, y);
-    }
+    const float4(*p)[32] = part[(q << tiles_log) + tt];
+    const float4 y = p[0][lane], ml = p[1][lane];
+    x.scale_to(0, fmaxf(x.m[0], ml.x));
+    x.scale_to(1, fmaxf(x.m[1], ml.y));
+    x.accumulate(ml, &y);
   }
   write_tiles<D, NT>(a, h.b, h.k, h.len, n, i, x, lane);
 }
@@ -1077,7 +1061,7 @@ static int row_tiles_of(int R) { return R <= 8 ? 1 : 2; }
 
 size_t decode_q4_ws_bytes(int, int Hq, int Hkv, int Tq, int, int D) {
   const int nt = row_tiles_of(Hq / Hkv * Tq);
-  return sizeof(Q4Head) * kMaxCtas + (size_t)kMaxCtas * 2 * nt * (D / 16 * 4 + 4) * 128;
+  return sizeof(Q4Head) * kMaxCtas + (size_t)kMaxCtas * 2 * nt * (D / 16 + 1) * 512;
 }
 
 template <int D>
