@@ -309,17 +309,21 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* out, int n, int 
 }
 
 // ------------------------------------------------------------------ append
-// Bound by instructions, then by memory: 8 features are one 16-byte load, but
-// some 100 instructions to scale, round and pack.  A thread takes a part of a
-// token's row, of k and of v, in HC heads one after another, the next head's
-// loads in flight: what depends on the token alone (its place in the cache, its
-// cosines and sines) is found once.  The part is 8 features, so that
-// neighbouring threads write neighbouring 16 (8) bytes, or for 4-bit caches a
-// whole block of 16: its scale then stays in the thread.  In the half layout the
-// features paired with them are loaded too (from L1: another thread's own).
-// 4 bits, 16411 tokens of 8 heads of 128 and their gather (173 MB): 34.0 us, 5.1
-// TB/s, 75% of a copy's rate; 64 tokens: 4.1 us, two launches.  All arithmetic
-// is f32, each element rounded once to the cache's type.
+// Bound by instructions (4 bits), or by memory: 8 features are one 16-byte load,
+// but some 100 instructions to scale, round and pack.  A thread takes one part of
+// a token's row, or two paired ones, of k and of v, in HC heads one after
+// another: what depends on the token alone (its place in the cache) is found
+// once.  A part is 8 features, so that neighbouring threads write neighbouring
+// 16 (8) bytes, or for 4-bit caches a whole block of 16: its scale then stays in
+// the thread.  The cosines and sines are loaded anew for each head: a thread then
+// fits 64 registers, and the 8 warps a scheduler that this allows hide more
+// latency than the table's row and the next head's loads kept in registers did
+// (105 of them; 4 bits, 16411 tokens of 8 heads of 128, 64 features rotated:
+// 20.4 us against 18.2, 73% of a copy's rate).  All 128 rotated in halves, 16384
+// tokens: bf16 24.1 us (87%; one part a thread 28.5), E4M3 20.4 (79%; 24.4), 4
+// bits 24 (two parts a thread 23 to 26, but 2.9 against 2.5 for 1000 tokens).  64
+// tokens and their gather: 4.0 us, two launches.  All arithmetic is f32, each
+// element rounded once to the cache's type.
 __device__ __forceinline__ uint32_t e4m3_of(float x) { return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3); }
 
 // A part at p (of a 4-bit row: codes at p, the block's scale at sf).  to_scale:
@@ -353,11 +357,22 @@ __device__ __forceinline__ void store_part(uint8_t* p, uint8_t* sf, const float*
   }
 }
 
+// Loaded where it stands: a plain load would be moved out of the loop over the heads, into registers.
+__device__ __forceinline__ void load4_here(const float* p, float* x) {
+  asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "l"(p));
+}
+
 enum { kNoRope = 0, kHalf = 1, kInter = 2 };
 
+// Parts a thread takes: in the half layout the two that are paired, but for 4 bits (two blocks' values at once do not
+// fit its registers), where the paired features are loaded beside its own.
+template <int FMT, int ROT>
+constexpr int kParts = ROT == kHalf && FMT != kCacheQ4 ? 2 : 1;
+
 template <int FMT, int HC, int ROT>
-__global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(256, 4) cache_append_kernel(const AppendArgs a) {
   constexpr int G = FMT == kCacheQ4 ? 2 : 1;         // groups of 8 features of a part
+  constexpr int P = kParts<FMT, ROT>;
   // 1 / (sf * scale) for every block scale: rounded reciprocals, one a thread instead of one a block of features
   __shared__ float inv[2][128];
   if constexpr (FMT == kCacheQ4) {
@@ -368,58 +383,47 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
   }
   griddep_wait();
   griddep_launch();
-  const int u_log = (a.D == 128 ? 4 : 3) - (G - 1);  // parts of a row, as a power of two
+  const int u_log = (a.D == 128 ? 4 : 3) - (G - 1) - (P - 1);  // threads of a row, as a power of two
   const long idx = (long)blockIdx.x * 256 + threadIdx.x, n = idx >> u_log;
   if (n >= (long)a.B * a.T) return;
-  const int f0 = ((int)idx & ((1 << u_log) - 1)) * 8 * G, h0 = blockIdx.y * HC;
+  const int u = (int)idx & ((1 << u_log) - 1), h0 = blockIdx.y * HC, R2 = a.R / 2;
+  const bool rotated = ROT != kNoRope && 8 * G * P * u < a.R;
+  // the part's first feature; with two parts, the pairs' first and second ones, or neighbours past rotary_dim
+  const int f0 = 8 * G * u * (P == 1 || rotated ? 1 : 2), f1 = rotated ? f0 + R2 : f0 + 8 * G;
   const int slot = a.slots[n];
   int pos = 0;
   if constexpr (ROT != kNoRope) pos = a.positions[n];
-  const int heads = min(HC, a.H - h0), R2 = a.R / 2;
+  const int heads = min(HC, a.H - h0);
   const long b = a.B == 1 ? 0 : n / a.T, t = n - b * a.T;
   const __nv_bfloat16* kr = a.k.p + b * a.k.sb + t * a.k.st + h0 * a.k.sh + f0;
   const __nv_bfloat16* vr = a.v.p + b * a.v.sb + t * a.v.st + h0 * a.v.sh + f0;
-  bool rot[G], second[G];                            // per group: rotated, and the second of its pairs
+  bool second[G];                                    // a group of 8 is the second of its pairs
 #pragma unroll
-  for (int g = 0; g < G; ++g) rot[g] = ROT != kNoRope && f0 + 8 * g < a.R, second[g] = f0 + 8 * g >= R2;
-  uint4 wk[2][G], wp[2][G], wv[2][G];                // a head's rows, and the next one's
-  auto load = [&](int i, int to) {
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const __nv_bfloat16 *k = kr + i * a.k.sh + 8 * g, *v = vr + i * a.v.sh + 8 * g;
-      wk[to][g] = __ldg(reinterpret_cast<const uint4*>(k));
-      if (ROT == kHalf && rot[g]) wp[to][g] = __ldg(reinterpret_cast<const uint4*>(k + (second[g] ? -R2 : R2)));
-      wv[to][g] = __ldg(reinterpret_cast<const uint4*>(v));
-    }
-  };
-  load(0, 0);
+  for (int g = 0; g < G; ++g) second[g] = P == 1 && ROT == kHalf && f0 + 8 * g >= R2;
   if (slot < 0 || slot >= (long)a.num_pages * a.page_size) {
-    if (slot != -1 && f0 == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadPage);
+    if (slot != -1 && u == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadPage);
     return;
   }
-  float c[G][8], s[G][8];
-  if constexpr (ROT != kNoRope) {
+  if constexpr (ROT != kNoRope)
     if (pos < 0 || pos >= a.n_table) {
-      if (f0 == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+      if (u == 0 && h0 == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
       return;
     }
-    const float* cs = a.cs + (long)pos * a.R;
+  const float* cs = a.cs + (long)pos * a.R;
+  auto rotation = [&](int g, float* c, float* s) {   // of group g's features
+    const int f = f0 + 8 * g;
+    if constexpr (ROT == kHalf) {
+      const int p = second[g] ? f - R2 : f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      if (!rot[g]) continue;
-      const int f = f0 + 8 * g;
-      if constexpr (ROT == kHalf) {
-        load8f(cs + (second[g] ? f - R2 : f), c[g]);
-        load8f(cs + R2 + (second[g] ? f - R2 : f), s[g]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[g][j] = second[g] ? -s[g][j] : s[g][j];   // x c + y s as x c - y (-s): the same rounding
-      } else {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(cs + f / 2)), y = __ldg(reinterpret_cast<const float4*>(cs + R2 + f / 2));
-        c[g][0] = x.x, c[g][1] = x.y, c[g][2] = x.z, c[g][3] = x.w;
-        s[g][0] = y.x, s[g][1] = y.y, s[g][2] = y.z, s[g][3] = y.w;
+      for (int j = 0; j < 8; j += 4) {
+        load4_here(cs + p + j, c + j);
+        load4_here(cs + R2 + p + j, s + j);
       }
+    } else {
+      load4_here(cs + f / 2, c);
+      load4_here(cs + R2 + f / 2, s);
     }
-  }
+  };
   // the part's place in the first head's row; the heads of a page are page_size rows apart
   constexpr int kNum = FMT == kCacheBf16 ? 4 : FMT == kCacheE4m3 ? 2 : 1;   // half bytes a feature
   const int page = slot / a.page_size, width = a.D * kNum / 2;
@@ -429,34 +433,62 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
   const long at = row * width + f0 * kNum / 2, sf_at = row * (a.D / 16) + f0 / 16;
   uint8_t *kp = static_cast<uint8_t*>(a.kc) + at, *vp = static_cast<uint8_t*>(a.vc) + at;
   uint8_t *kf = a.ksf + sf_at, *vf = a.vsf + sf_at;
+  const int to1 = (f1 - f0) * kNum / 2, sf_to1 = (f1 - f0) / 16;
   const long step = (long)a.page_size * width, sf_step = (long)a.page_size * (a.D / 16);
 #pragma unroll
   for (int i = 0; i < HC; ++i) {
     if (i >= heads) break;
-    if (i + 1 < HC && i + 1 < heads) load(i + 1, (i + 1) & 1);
-    float x[8 * G];
+    uint4 wk[P][G], wp[G], wv[P][G];                 // the row's parts, and with one part the one paired with k's
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      bf16x8_to_f32(wk[i & 1][g], x + 8 * g);
-      if (ROT == kHalf && rot[g]) {
-        float y[8];
-        bf16x8_to_f32(wp[i & 1][g], y);
+      const __nv_bfloat16 *k = kr + i * a.k.sh + 8 * g, *v = vr + i * a.v.sh + 8 * g;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[8 * g + j] = rot_first(x[8 * g + j], y[j], c[g][j], s[g][j]);
+      for (int p = 0; p < P; ++p) {
+        wk[p][g] = __ldg(reinterpret_cast<const uint4*>(k + (p ? f1 - f0 : 0)));
+        wv[p][g] = __ldg(reinterpret_cast<const uint4*>(v + (p ? f1 - f0 : 0)));
       }
-      if (ROT == kInter && rot[g]) {
+      if (P == 1 && ROT == kHalf && rotated) wp[g] = __ldg(reinterpret_cast<const uint4*>(k + (second[g] ? -R2 : R2)));
+    }
+    float x[P][8 * G];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float e = x[8 * g + 2 * j], o = x[8 * g + 2 * j + 1];
-          x[8 * g + 2 * j] = rot_first(e, o, c[g][j], s[g][j]);
-          x[8 * g + 2 * j + 1] = rot_second(o, e, c[g][j], s[g][j]);
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) bf16x8_to_f32(wk[p][g], x[p] + 8 * g);
+      if constexpr (ROT != kNoRope) {
+        if (!rotated) continue;
+        float c[8], s[8];
+        rotation(g, c, s);
+        if constexpr (P == 2) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float y = x[0][8 * g + j], z = x[1][8 * g + j];
+            x[0][8 * g + j] = rot_first(y, z, c[j], s[j]);
+            x[1][8 * g + j] = rot_second(z, y, c[j], s[j]);
+          }
+        } else if constexpr (ROT == kHalf) {
+          const uint32_t sign = second[g] ? 0x80008000u : 0u;   // x c + y s as x c - (-y) s: the same rounding
+          float y[8];
+          bf16x8_to_f32(make_uint4(wp[g].x ^ sign, wp[g].y ^ sign, wp[g].z ^ sign, wp[g].w ^ sign), y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[0][8 * g + j] = rot_first(x[0][8 * g + j], y[j], c[j], s[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float e = x[0][8 * g + 2 * j], o = x[0][8 * g + 2 * j + 1];
+            x[0][8 * g + 2 * j] = rot_first(e, o, c[j], s[j]);
+            x[0][8 * g + 2 * j + 1] = rot_second(o, e, c[j], s[j]);
+          }
         }
       }
     }
-    store_part<FMT>(kp, kf, x, a.k_inv, inv[0]);
 #pragma unroll
-    for (int g = 0; g < G; ++g) bf16x8_to_f32(wv[i & 1][g], x + 8 * g);
-    store_part<FMT>(vp, vf, x, a.v_inv, inv[1]);
+    for (int p = 0; p < P; ++p) store_part<FMT>(kp + p * to1, kf + p * sf_to1, x[p], a.k_inv, inv[0]);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) bf16x8_to_f32(wv[p][g], x[p] + 8 * g);
+      store_part<FMT>(vp + p * to1, vf + p * sf_to1, x[p], a.v_inv, inv[1]);
+    }
     kp += step, vp += step, kf += sf_step, vf += sf_step;
   }
 }
@@ -547,7 +579,7 @@ cudaError_t launch_cache_plan(const PlanArgs& a, int sms, cudaStream_t stream) {
 // one, so that few tokens still spread over the SMs.  Rotary rows of 40 heads of
 // 128: 256 tokens 3.4 us with 8 heads a thread, 2.6 with one; 1024: 4.9, 4.8;
 // 8192: 28.4, 31.9.  Append (and gather, 4 bits, 8 heads of 128) of 1024 tokens:
-// 6.8, 5.5; 4096: 12.2, 12.7; 16384: 38.6, 49.2.
+// 8.7 with 4, 5.5 with one; 4096: 12.7, 11.6; 16384: 38.5, 43.7.
 static bool many_heads(unsigned gx, int H, int most, int sms) { return (long)gx * ((H + most - 1) / most) >= 2L * sms; }
 
 template <bool INTER>
@@ -596,9 +628,10 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, int sms, cudaStream_t stre
 
 template <int FMT, int ROT>
 static cudaError_t launch_append_as(const AppendArgs& a, int sms, cudaStream_t stream) {
-  constexpr int kHeads = 4;
+  constexpr int kHeads = 4 / kParts<FMT, ROT>;
   unsigned gx;
-  if (!grid_of((long)a.B * a.T * (a.D / (FMT == kCacheQ4 ? 16 : 8)), &gx)) return cudaErrorInvalidValue;
+  if (!grid_of((long)a.B * a.T * (a.D / ((FMT == kCacheQ4 ? 16 : 8) * kParts<FMT, ROT>)), &gx))
+    return cudaErrorInvalidValue;
   const bool wide = many_heads(gx, a.H, kHeads, sms);
   const dim3 grid(gx, (unsigned)(wide ? (a.H + kHeads - 1) / kHeads : a.H));
   prof_begin(kProfAppend, stream);
