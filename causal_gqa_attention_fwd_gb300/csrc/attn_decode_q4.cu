@@ -316,29 +316,33 @@ enum { kPlain = 0, kRotated = 1, kStacked = 2 };
 template <int D, int NT, int MODE, int PARTS>
 __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& w, int lane, uint32_t (*qf)[PARTS][D / 16][2],
                                              float (*fac)[2]) {
-  constexpr int F = D / 4;            // features of a thread
+  // A thread's features of its row: [tD/4, (t+1)D/4); stacked, where lanes g and g + 4 have the same row, half of
+  // them each, and then one exchanges its remainders for the other's values.
+  constexpr int F = D / 4, N = MODE == kStacked ? F / 2 : F;
   const int g = lane >> 2, t = lane & 3;
+  const bool upper = MODE == kStacked && g >= 4;
+  const int f0 = upper ? N : 0;
   const int hkv = w.k / a.nrb, r0 = (w.k - hkv * a.nrb) * 8 * NT;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = r0 + n * 8 + (MODE == kStacked ? g & 3 : g);
     const long row = ((long)w.b * a.Hq + hkv * a.G) * a.Tq + r;
-    float x[F];
+    float x[N];
     const bool live = r < a.R;
-    uint32_t u[F / 2];
+    uint32_t u[N / 2];
 #pragma unroll
-    for (int c = 0; c < F / 8; ++c) {
+    for (int c = 0; c < N / 8; ++c) {
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (live) v = __ldg(reinterpret_cast<const uint4*>(a.q + row * D + t * F) + c);
+      if (live) v = __ldg(reinterpret_cast<const uint4*>(a.q + row * D + t * F + f0) + c);
       u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
     }
     if constexpr (MODE != kPlain) {
       // features t F.. pair with those of lane t ^ 2; a row at a negative position sees no key: any angle will do
       const int pos = max(w.len - a.Tq + r % a.Tq, 0);
-      const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (long)pos * D + (t & 1) * F);
+      const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (long)pos * D + (t & 1) * F + f0);
       const float sign = t < 2 ? -1.f : 1.f;
 #pragma unroll
-      for (int c = 0; c < F / 4; ++c) {
+      for (int c = 0; c < N / 4; ++c) {
         const float4 co = __ldg(cs + c), si = __ldg(cs + D / 8 + c);
         const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
@@ -351,32 +355,39 @@ __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& 
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < F / 2; ++i) {
+      for (int i = 0; i < N / 2; ++i) {
         x[2 * i] = __uint_as_float(u[i] << 16);
         x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
       }
     }
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < F; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(x[i]));
     amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+    if constexpr (MODE == kStacked) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 16));
     const int ex = (int)(__float_as_uint(amax) >> 23);          // biased exponent: 0 zero, 255 not finite
     const int sh = ex == 0 || ex == 255 ? 0 : 14 - (ex - 127);  // x * 2^sh, in two steps within f32's range
     const float s1 = __uint_as_float((uint32_t)(127 + sh / 2) << 23), s2 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
     const float i1 = __uint_as_float((uint32_t)(127 - sh / 2) << 23), i2 = __uint_as_float((uint32_t)(127 - sh + sh / 2) << 23);
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j)
+    for (int j = 0; j < N / 4; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float lo = x[4 * j + 2 * h] * s1 * s2, hi = x[4 * j + 2 * h + 1] * s1 * s2;
         const uint32_t v = pack_f16x2(lo, hi);
-        qf[n][0][j][h] = v;
+        uint32_t rest = 0;
         if constexpr (MODE != kPlain) {
           const float2 b = f16x2_to_f32(v);
-          const uint32_t rest = pack_f16x2(lo - b.x, hi - b.y);
+          rest = pack_f16x2(lo - b.x, hi - b.y);
+        }
+        if constexpr (MODE == kStacked) {
+          const uint32_t mine = upper ? rest : v, other = __shfl_xor_sync(~0u, upper ? v : rest, 16);
+          qf[n][0][j][h] = upper ? other : mine;
+          qf[n][0][j + N / 4][h] = upper ? mine : other;
+        } else {
+          qf[n][0][j][h] = v;
           if constexpr (MODE == kRotated) qf[n][PARTS - 1][j][h] = rest;
-          else qf[n][0][j][h] = g < 4 ? v : rest;
         }
       }
     // the columns of S^T are rows 2t and 2t+1: their factors come from the lanes that hold those rows
