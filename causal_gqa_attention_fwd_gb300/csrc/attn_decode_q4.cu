@@ -118,7 +118,8 @@ struct Piece4 {
 };
 
 // TILES 16-feature tiles of 8 rows of a unit, combined from stored pieces with
-// a running maximum; the loads of kBatch pieces are in flight at a time.
+// a running maximum; the loads of kBatch pieces are in flight at a time (more
+// in shared memory cost more than they hide).
 template <int D, int TILES>
 struct Combined {
   float acc[TILES][4], m[2], l[2];
@@ -132,13 +133,13 @@ struct Combined {
   // `frag`, its maxima and sums `stat`
   template <typename At>
   __device__ __forceinline__ void add(At at, int first, int step, int count, int frag, int stat, int lane) {
-    constexpr int kBatch = TILES == 1 ? 8 : 2;
+    constexpr int kBatch = TILES == 1 ? 8 : 1;
     for (int i = first; i < count; i += kBatch * step) {
       float4 x[kBatch][TILES], ml[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        if (TILES > 1 || i + u * step < count) {   // in shared memory a load more costs less than the guard
-          const float4* p = at(min(i + u * step, count - 1)) + lane;
+        if (i + u * step < count) {
+          const float4* p = at(i + u * step) + lane;
 #pragma unroll
           for (int j = 0; j < TILES; ++j) x[u][j] = p[32 * (frag + j)];
           ml[u] = p[32 * stat];
@@ -940,7 +941,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   }
   __syncthreads();
 
-  // Combine the stored pieces of each unit, in stream order; the warps share the unit's 16-feature tiles.
+  // Combine the stored pieces of each unit, in stream order: a warp per 8 rows of a unit (shared out by its feature
+  // tiles among more warps, a unit's chain of dependent steps is as long, and there are more of them)
   static_assert(2 * C::kWarps <= 32, "a lane per slot");   // lane s looks after slot s
   const int kind = lane < 2 * C::kWarps ? rec_kind[lane] : 0;
   const unsigned taken = __ballot_sync(~0u, kind);
@@ -954,7 +956,6 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   float4* pieces = reinterpret_cast<float4*>(heads + kMaxCtas);
   Q4Head head{};
   head.first = -1;
-  constexpr int kQuads = NT * C::kMT / 4;   // a warp takes four tiles of a unit at a time, units and quads in turn
   int item = 0;
   for (unsigned todo = begins; todo;) {
     const int s0 = __ffs(todo) - 1;
@@ -967,22 +968,22 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
       head = Q4Head{u.b, u.k, u.len, sh.owner(u.P) / wpc, sh.owner(u.P + u.nb - 1) / wpc, {}};
     }
 #pragma unroll 1
-    for (int qd = 0; qd < kQuads; ++qd, ++item) {
+    for (int n = 0; n < NT; ++n, ++item) {   // 8 rows of a unit a warp, in turn
       if (item >= C::kWarps) item = 0;
       if (item != warp) continue;
-      const int n = qd * 4 / C::kMT, i = qd * 4 % C::kMT, rank = __popc(taken & ((1u << s0) - 1));
-      Combined<D, 4> x;
+      const int rank = __popc(taken & ((1u << s0) - 1));
+      Combined<D, C::kMT> x;
       x.clear();
       x.add([&](int j) -> const float4* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, 0, 1, __popc(slots),
-            n * Piece4<D, NT>::kPer + i, n * Piece4<D, NT>::kPer + C::kMT, lane);
+            n * Piece4<D, NT>::kPer, n * Piece4<D, NT>::kPer + C::kMT, lane);
       if (first && last) {
         const Unit u = rec_unit[s0];
-        write_tiles<D, NT>(a, u.b, u.k, u.len, n, i, x, lane);
+        write_tiles<D, NT>(a, u.b, u.k, u.len, n, 0, x, lane);
       } else {
         float4* q = pieces + ((long)blockIdx.x * 2 + first) * C::kRec * 32 + n * Piece4<D, NT>::kPer * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q[32 * (i + j)] = make_float4(x.acc[j][0], x.acc[j][1], x.acc[j][2], x.acc[j][3]);
-        if (i == 0) q[32 * C::kMT] = make_float4(x.m[0], x.m[1], x.l[0], x.l[1]);
+        for (int j = 0; j < C::kMT; ++j) q[32 * j] = make_float4(x.acc[j][0], x.acc[j][1], x.acc[j][2], x.acc[j][3]);
+        q[32 * C::kMT] = make_float4(x.m[0], x.m[1], x.l[0], x.l[1]);
       }
     }
   }
