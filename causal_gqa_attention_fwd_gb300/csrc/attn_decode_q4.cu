@@ -954,40 +954,39 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   __syncwarp();
   Q4Head* heads = static_cast<Q4Head*>(a.ws);
   float4* pieces = reinterpret_cast<float4*>(heads + kMaxCtas);
-  Q4Head head{};
-  head.first = -1;
-  int item = 0;
-  for (unsigned todo = begins; todo;) {
-    const int s0 = __ffs(todo) - 1;
-    todo &= todo - 1;
-    const unsigned slots = taken & ~((1u << s0) - 1) & (todo ? (todo & -todo) - 1 : ~0u);   // up to the next unit's
-    const bool first = rec_kind[s0] & kFirst, last = rec_kind[31 - __clz(slots)] & kLast;
-    if (!first && warp == 0) {
+  const int unit_of = begins >> lane & 1 ? __popc(begins & ((1u << lane) - 1)) : -1;   // the unit that begins with the lane's slot
+#pragma unroll 1
+  for (int item = warp; item < __popc(begins) * NT; item += C::kWarps) {
+    const int n = item % NT, s0 = __ffs(__ballot_sync(~0u, unit_of == item / NT)) - 1;
+    const unsigned later = begins & ~((2u << s0) - 1);
+    const unsigned slots = taken & ~((1u << s0) - 1) & (later ? (later & -later) - 1 : ~0u);   // up to the next unit's
+    const bool first = __shfl_sync(~0u, kind, s0) & kFirst, last = __shfl_sync(~0u, kind, 31 - __clz(slots)) & kLast;
+    const int rank = __popc(taken & ((1u << s0) - 1));
+    Combined<D, C::kMT> x;
+    x.clear();
+    x.add([&](int j) -> const float4* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, 0, 1, __popc(slots),
+          n * Piece4<D, NT>::kPer, n * Piece4<D, NT>::kPer + C::kMT, lane);
+    if (first && last) {
+      const Unit u = rec_unit[s0];
+      write_tiles<D, NT>(a, u.b, u.k, u.len, n, 0, x, lane);
+    } else {
+      float4* q = pieces + ((long)blockIdx.x * 2 + first) * C::kRec * 32 + n * Piece4<D, NT>::kPer * 32 + lane;
+#pragma unroll
+      for (int j = 0; j < C::kMT; ++j) q[32 * j] = make_float4(x.acc[j][0], x.acc[j][1], x.acc[j][2], x.acc[j][3]);
+      q[32 * C::kMT] = make_float4(x.m[0], x.m[1], x.l[0], x.l[1]);
+    }
+  }
+  if (tid == C::kThreads - 32) {   // of the warp that gets an item last
+    Q4Head head{};
+    head.first = -1;
+    const int s0 = __ffs(begins) - 1;
+    if (begins && !(rec_kind[s0] & kFirst)) {
       const Unit u = rec_unit[s0];
       const Shares sh(total, Wn);
       head = Q4Head{u.b, u.k, u.len, sh.owner(u.P) / wpc, sh.owner(u.P + u.nb - 1) / wpc, {}};
     }
-#pragma unroll 1
-    for (int n = 0; n < NT; ++n, ++item) {   // 8 rows of a unit a warp, in turn
-      if (item >= C::kWarps) item = 0;
-      if (item != warp) continue;
-      const int rank = __popc(taken & ((1u << s0) - 1));
-      Combined<D, C::kMT> x;
-      x.clear();
-      x.add([&](int j) -> const float4* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, 0, 1, __popc(slots),
-            n * Piece4<D, NT>::kPer, n * Piece4<D, NT>::kPer + C::kMT, lane);
-      if (first && last) {
-        const Unit u = rec_unit[s0];
-        write_tiles<D, NT>(a, u.b, u.k, u.len, n, 0, x, lane);
-      } else {
-        float4* q = pieces + ((long)blockIdx.x * 2 + first) * C::kRec * 32 + n * Piece4<D, NT>::kPer * 32 + lane;
-#pragma unroll
-        for (int j = 0; j < C::kMT; ++j) q[32 * j] = make_float4(x.acc[j][0], x.acc[j][1], x.acc[j][2], x.acc[j][3]);
-        q[32 * C::kMT] = make_float4(x.m[0], x.m[1], x.l[0], x.l[1]);
-      }
-    }
+    heads[blockIdx.x] = head;
   }
-  if (tid == 0) heads[blockIdx.x] = head;
 }
 
 // Units cut between CTAs.  A warp combines a 16-feature tile of up to
