@@ -44,8 +44,8 @@
 // of 32 keys and 128 features takes a warp some 600, and per SM sub-partition a
 // conversion (F2FP) or byte operation takes 2 cycles, an f16 multiplication 2,
 // an MMA 8, which overlap only in part: 226.6 MB of cache, queries, outputs and
-// tables take 46 us, 4.9 TB/s, 72% of a copy's rate.  Short rows by latency: 8
-// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 9.2 us, of which 3 lie
+// tables take 45 us, 5.0 TB/s, 74% of a copy's rate.  Short rows by latency: 8
+// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 8.6 us, of which 3 lie
 // between the last warp's end and the end of decode_q4_merge.
 #include <math_constants.h>
 
@@ -64,7 +64,7 @@ constexpr int kMaxCtas = 160;  // CTAs the workspace holds pieces for
 constexpr int kUnitCost = 2;   // what a unit costs beside its tiles, in tiles (1 and 4 measure within 0.3 us of it)
 // Warps a CTA uses before work goes to another SM: pieces met in a CTA cost less than those that go through the
 // workspace, but a few warps on every SM convert faster than many on a few.  One row of 2048 keys, 2 K/V heads of
-// 128: 1 warp 9.7 us, 4 9.0, 8 9.6; 8192 keys: 10.3, 10.2, 10.4.
+// 128: 1 warp 9.1 us, 4 8.4, 8 8.8, 12 9.6; 8192 keys: 9.4, 9.4, 9.5, 10.1.
 constexpr int kMinWarps = 4;
 constexpr float kLazy = 8.f;   // the maximum moves when it would grow by more than 2^8 ...
 constexpr float kOff = 7.f;    // ... and P is scaled by 2^7, so P <= 2^15 and f16's smallest step is 2^-31 of a row's largest P
@@ -118,8 +118,7 @@ struct Piece4 {
 };
 
 // TILES 16-feature tiles of 8 rows of a unit, combined from stored pieces with
-// a running maximum; the loads of kBatch pieces are in flight at a time (more
-// in shared memory cost more than they hide).
+// a running maximum.
 template <int D, int TILES>
 struct Combined {
   float acc[TILES][4], m[2], l[2];
@@ -129,32 +128,15 @@ struct Combined {
 #pragma unroll
     for (int i = 0; i < TILES; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   }
-  // pieces first, first + step, ... below count; at(i) is piece i's base, where its fragments' first tile is float4
-  // `frag`, its maxima and sums `stat`
-  template <typename At>
-  __device__ __forceinline__ void add(At at, int first, int step, int count, int frag, int stat, int lane) {
-    constexpr int kBatch = TILES == 1 ? 8 : 1;
-    for (int i = first; i < count; i += kBatch * step) {
-      float4 x[kBatch][TILES], ml[kBatch];
+  // a piece: its first tile at p, its maxima and sums `stat` tiles on
+  __device__ __forceinline__ void add(const float4* p, int stat) {
+    float4 x[TILES];
+    const float4 ml = p[32 * stat];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (i + u * step < count) {
-          const float4* p = at(i + u * step) + lane;
-#pragma unroll
-          for (int j = 0; j < TILES; ++j) x[u][j] = p[32 * (frag + j)];
-          ml[u] = p[32 * stat];
-        }
-      }
-      float top[2] = {m[0], m[1]};
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (i + u * step < count) top[0] = fmaxf(top[0], ml[u].x), top[1] = fmaxf(top[1], ml[u].y);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) scale_to(c, top[c]);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (i + u * step < count) accumulate(ml[u], x[u]);
-    }
+    for (int j = 0; j < TILES; ++j) x[j] = p[32 * j];
+    scale_to(0, fmaxf(m[0], ml.x));
+    scale_to(1, fmaxf(m[1], ml.y));
+    accumulate(ml, x);
   }
   __device__ __forceinline__ void scale_to(int c, float top) {
     const float f = m[c] == -CUDART_INF_F ? 1.f : ex2_approx(m[c] - top);   // zeros so far (or NaN, which is kept)
@@ -308,7 +290,7 @@ __device__ __forceinline__ void row_limits(const DecodeQ4Args& a, int len, int r
 // bf16 values (exact in f16 after scaling); rotated, the f16 value and the f16
 // remainder, each an MMA of its own; or rotated and at most 4 rows, the values
 // in columns 0-3 and the remainders in columns 4-7 of the same MMA, added after
-// it (8 rows of 24k keys on average, 8 K/V heads, 4 queries each: 47 us, 51 with two MMAs).
+// it (8 rows of 8192 keys, 8 K/V heads of 128, 4 query heads each: 24.0 us, 25.9 with two MMAs).
 enum { kPlain = 0, kRotated = 1, kStacked = 2 };
 
 // A unit's query rows as B fragments; rows are scaled by a power of two so that
@@ -597,7 +579,6 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   __shared__ int prefix[C::kThreads];
   __shared__ Unit rec_unit[2 * C::kWarps];   // unit of each stored piece
   __shared__ int rec_kind[2 * C::kWarps];    // kStored, with kFirst / kLast if it has the unit's first / last tile; 0: none
-  __shared__ uint8_t order[C::kWarps][2 * C::kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);   // the same in a warp, told so
   const int g = lane >> 2, t = lane & 3;
   const int upb = a.Hkv * a.nrb;
@@ -950,8 +931,6 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   const int my_P = kind ? rec_unit[lane].P : -1;
   const int prev_P = __shfl_sync(~0u, my_P, earlier ? 31 - __clz(earlier) : lane);
   const unsigned begins = __ballot_sync(~0u, kind && (!earlier || prev_P != my_P));
-  if (kind) order[warp][__popc(earlier)] = (uint8_t)lane;   // the slots taken, in stream order
-  __syncwarp();
   Q4Head* heads = static_cast<Q4Head*>(a.ws);
   float4* pieces = reinterpret_cast<float4*>(heads + kMaxCtas);
   const int unit_of = begins >> lane & 1 ? __popc(begins & ((1u << lane) - 1)) : -1;   // the unit that begins with the lane's slot
@@ -961,11 +940,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     const unsigned later = begins & ~((2u << s0) - 1);
     const unsigned slots = taken & ~((1u << s0) - 1) & (later ? (later & -later) - 1 : ~0u);   // up to the next unit's
     const bool first = __shfl_sync(~0u, kind, s0) & kFirst, last = __shfl_sync(~0u, kind, 31 - __clz(slots)) & kLast;
-    const int rank = __popc(taken & ((1u << s0) - 1));
     Combined<D, C::kMT> x;
     x.clear();
-    x.add([&](int j) -> const float4* { return piece_at<D, NT>(smem, order[warp][rank + j]); }, 0, 1, __popc(slots),
-          n * Piece4<D, NT>::kPer, n * Piece4<D, NT>::kPer + C::kMT, lane);
+    for (unsigned left = slots; left; left &= left - 1)
+      x.add(piece_at<D, NT>(smem, __ffs(left) - 1) + n * Piece4<D, NT>::kPer * 32 + lane, C::kMT);
     if (first && last) {
       const Unit u = rec_unit[s0];
       write_tiles<D, NT>(a, u.b, u.k, u.len, n, 0, x, lane);
@@ -994,7 +972,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
 // 8 or 16 groups of warps share them and meet in shared memory, and the tiles
 // go to several blocks: those of the CTAs from the second on that hold a piece
 // (there are more of them than blocks needed).  One row of 8192 keys, 2 K/V
-// heads of 128: 9.9 us, and 14.7 with one block for a unit.
+// heads of 128: 9.4 us; one block a unit took 4.8 more.
 constexpr int kMergeLog = 4, kMergeWarps = 1 << kMergeLog;
 constexpr int kMergePieces = 4;
 
@@ -1018,9 +996,29 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_q4_merge(const Decode
   const int tile = (block << tiles_log) + tt, n = tile / C::kMT, i = tile % C::kMT;
   Combined<D, 1> x;
   x.clear();
+  constexpr int kBatch = 8;
   if (group < groups)
-    x.add([&](int j) -> const float4* { return pieces + ((long)(h.first + j) * 2 + (j == 0)) * C::kRec * 32; }, group, groups,
-          count, n * kPer + i, n * kPer + C::kMT, lane);
+    for (int j0 = group; j0 < count; j0 += kBatch * groups) {   // up to kBatch pieces' loads in flight
+      float4 y[kBatch], ml[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int j = j0 + u * groups;
+        if (j < count) {
+          const float4* p = pieces + (((long)(h.first + j) * 2 + (j == 0)) * C::kRec + n * kPer) * 32 + lane;
+          y[u] = p[32 * i];
+          ml[u] = p[32 * C::kMT];
+        }
+      }
+      float top[2] = {x.m[0], x.m[1]};
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (j0 + u * groups < count) top[0] = fmaxf(top[0], ml[u].x), top[1] = fmaxf(top[1], ml[u].y);
+      x.scale_to(0, top[0]);
+      x.scale_to(1, top[1]);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (j0 + u * groups < count) x.accumulate(ml[u], &y[u]);
+    }
   if (groups > 1) {
     part[warp][0][lane] = make_float4(x.acc[0][0], x.acc[0][1], x.acc[0][2], x.acc[0][3]);
     part[warp][1][lane] = make_float4(x.m[0], x.m[1], x.l[0], x.l[1]);
@@ -1028,13 +1026,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_q4_merge(const Decode
   }
   if (group > 0) return;
 #pragma unroll 3
-  for (int q = 1; q < groups; ++q) {
-    const float4(*p)[32] = part[(q << tiles_log) + tt];
-    const float4 y = p[0][lane], ml = p[1][lane];
-    x.scale_to(0, fmaxf(x.m[0], ml.x));
-    x.scale_to(1, fmaxf(x.m[1], ml.y));
-    x.accumulate(ml, &y);
-  }
+  for (int q = 1; q < groups; ++q) x.add(&part[(q << tiles_log) + tt][0][lane], 1);
   write_tiles<D, NT>(a, h.b, h.k, h.len, n, i, x, lane);
 }
 
@@ -1066,8 +1058,8 @@ cudaError_t run(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
 
 // Rows go in blocks of 16 (two 8-row tiles, one conversion of the cache for
 // both) unless one tile of 8 holds them all: 8 rows of 8192 keys, 8 K/V heads,
-// blocks of 16 against 8: 16 query rows a head 27.8 us against 34.4 (D = 64:
-// 21.2, 24.3), 8 query rows 27.7 against 23.4 (21.1, 17.5).
+// blocks of 16 against 8: 16 query rows a head 27.1 us against 33.2 (D = 64:
+// 20.3, 23.0), 8 query rows 26.9 against 22.3 (20.3, 16.2).
 static int row_tiles_of(int R) { return R <= 8 ? 1 : 2; }
 
 size_t decode_q4_ws_bytes(int, int Hq, int Hkv, int Tq, int, int D) {
