@@ -101,6 +101,28 @@ def test_decode_q4(gq, case):
     close(o, lse, reference(q, cache, lens, 1 / math.sqrt(D)))
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,D", [(1000, 2, 1, 128), (1300, 3, 3, 64), (700, 12, 1, 128), (2050, 2, 2, 128)])
+def test_decode_q4_more_rows_than_a_block_scans_at_once(gq, B, Hq, Hkv, D):
+    """The rows are counted in several passes; some are empty, two have lengths that are refused."""
+    S, g = 70, torch.Generator().manual_seed(B)
+    lens = torch.randint(0, S + 1, (B,), generator=g, dtype=torch.int32)
+    lens[::7] = 0
+    q, cache = queries(B, Hq, 1, D, 60), cache_of(B, Hkv, S, D, 61)
+    o, lse = run(gq, q, cache, lens, 1 / math.sqrt(D))
+    assert gq.get_device_status() == 0
+    ref = reference(q, cache, lens, 1 / math.sqrt(D))
+    close(o, lse, ref)
+    bad = lens.clone()
+    bad[1], bad[B - 1] = -1, S + 1
+    o2, lse2 = (torch.full_like(t, 7.0) for t in (o, lse))
+    run(gq, q, cache, bad, 1 / math.sqrt(D), o=o2, lse=lse2)
+    assert gq.get_device_status() == 5
+    for x, y in ((o, o2), (lse, lse2)):
+        assert (y[1] == 7).all() and (y[B - 1] == 7).all()
+        y[1], y[B - 1] = x[1], x[B - 1]
+    close(o2, lse2, ref)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Tq", [1, 3])
 def test_decode_q4_rope(gq, D, Tq):
