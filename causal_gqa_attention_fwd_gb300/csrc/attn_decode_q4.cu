@@ -45,7 +45,7 @@
 // conversion (F2FP) or byte operation takes 2 cycles, an f16 multiplication 2,
 // an MMA 8, which overlap only in part: 226.6 MB of cache, queries, outputs and
 // tables take 45 us, 5.0 TB/s, 74% of a copy's rate.  Short rows by latency: 8
-// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 8.6 us, of which 3 lie
+// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 8.4 us, of which 3 lie
 // between the last warp's end and the end of decode_q4_merge.
 #include <math_constants.h>
 
@@ -381,8 +381,9 @@ __device__ __forceinline__ void load_queries(const DecodeQ4Args& a, const Unit& 
 }
 
 // O and LSE of two rows (2t, 2t+1 of the 8 from r0 on) from their sums and
-// a run of O^T's tiles: tile i holds features 2i, 2i+1 of the gD/8.. that a lane group has.
-template <int D, int TILES>
+// a run of O^T's tiles: tile i holds features 2i, 2i+1 of the gD/8.. that a lane group has.  APPROX, in the merge, whose
+// every instruction is waited for: quotient and logarithm to 2 ulp (0.2 us less).
+template <int D, int TILES, bool APPROX>
 __device__ __forceinline__ void write_rows(const DecodeQ4Args& a, int b, int hkv, int r0, const int* lim, int tile0,
                                            const float (*acc)[4], const float* m, const float* lsum, int lane) {
   const int g = lane >> 2, t = lane & 3;
@@ -396,7 +397,7 @@ __device__ __forceinline__ void write_rows(const DecodeQ4Args& a, int b, int hkv
     if (r >= a.R) continue;
     const long row = ((long)b * a.Hq + hkv * a.G) * a.Tq + r;
     const bool empty = lim[c] < 0;      // the row sees no key
-    const float inv = a.v_scale / l;
+    const float inv = APPROX ? __fdividef(a.v_scale, l) : a.v_scale / l;
     if (!GQA_CHECK(row >= 0 && row < (long)a.B * a.Hq * a.Tq, a.status, a.dbg_line)) continue;
     __nv_bfloat16* o = a.o + row * D + g * (D / 8) + 2 * tile0;
     uint32_t w[TILES];
@@ -409,7 +410,7 @@ __device__ __forceinline__ void write_rows(const DecodeQ4Args& a, int b, int hkv
       for (int i = 0; i < TILES / 4; ++i)
         reinterpret_cast<uint4*>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
-    if (g == 0 && tile0 == 0) a.lse[row] = empty ? -CUDART_INF_F : (m[c] - kOff + log2f(l)) * 0.69314718055994531f;
+    if (g == 0 && tile0 == 0) a.lse[row] = empty ? -CUDART_INF_F : (m[c] - kOff + (APPROX ? __log2f(l) : log2f(l))) * 0.69314718055994531f;
   }
 }
 
@@ -419,7 +420,7 @@ __device__ __forceinline__ void write_tiles(const DecodeQ4Args& a, int b, int k,
   const int hkv = k / a.nrb, r0 = (k - hkv * a.nrb) * 8 * NT + n * 8;
   int lim[2];
   row_limits(a, len, r0 + 2 * (lane & 3), lim);
-  write_rows<D, TILES>(a, b, hkv, r0, lim, tile, x.acc, x.m, x.l, lane);
+  write_rows<D, TILES, TILES == 1>(a, b, hkv, r0, lim, tile, x.acc, x.m, x.l, lane);
 }
 
 // Workspace: a header per CTA, then two pieces a CTA (kRec * 32 float4 each): 0 of
@@ -899,7 +900,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
       if (ta == 0 && te == cu.nb) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          write_rows<D, C::kMT>(a, cu.b, cu.k / a.nrb, r0 + 8 * n, lim[n], 0, p.acc[n], p.m[n], p.l[n], lane);
+          write_rows<D, C::kMT, false>(a, cu.b, cu.k / a.nrb, r0 + 8 * n, lim[n], 0, p.acc[n], p.m[n], p.l[n], lane);
       } else {
         const int slot = 2 * warp + (ta == 0);   // a unit begun before the share, or continued after it
         if (slot & 1) {   // the share ends here: no copy is in flight, and every lane has read the last tile
