@@ -38,15 +38,16 @@
 // for another until the end: a unit inside one warp's share is written
 // directly; pieces of a unit cut between warps of a CTA are combined through
 // shared memory, those of a unit cut between CTAs through the workspace by
-// decode_q4_merge.
+// decode_q4_merge.  Few units of short rows go to a cluster of CTAs each
+// instead, whose pieces meet in distributed shared memory (see cluster_of).
 //
 // Bound: long rows by the instructions that turn codes into operands.  A tile
 // of 32 keys and 128 features takes a warp some 600, and per SM sub-partition a
 // conversion (F2FP) or byte operation takes 2 cycles, an f16 multiplication 2,
 // an MMA 8, which overlap only in part: 226.6 MB of cache, queries, outputs and
 // tables take 45 us, 5.0 TB/s, 74% of a copy's rate.  Short rows by latency: 8
-// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 8.4 us, of which 3 lie
-// between the last warp's end and the end of decode_q4_merge.
+// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 7.3 us in clusters (8.4 as a
+// stream, of which 3 lie between the last warp's end and the merge's).
 #include <math_constants.h>
 
 #include <atomic>
@@ -64,7 +65,8 @@ constexpr int kMaxCtas = 160;  // CTAs the workspace holds pieces for
 constexpr int kUnitCost = 2;   // what a unit costs beside its tiles, in tiles (1 and 4 measure within 0.3 us of it)
 // Warps a CTA uses before work goes to another SM: pieces met in a CTA cost less than those that go through the
 // workspace, but a few warps on every SM convert faster than many on a few.  One row of 2048 keys, 2 K/V heads of
-// 128: 1 warp 9.1 us, 4 8.4, 8 8.8, 12 9.6; 8192 keys: 9.4, 9.4, 9.5, 10.1.
+// 128 (as a stream): 1 warp 9.1 us, 4 8.4, 8 8.8, 12 9.6; 8192 keys: 9.4, 9.4, 9.5,
+// 10.1.
 constexpr int kMinWarps = 4;
 constexpr float kLazy = 8.f;   // the maximum moves when it would grow by more than 2^8 ...
 constexpr float kOff = 7.f;    // ... and P is scaled by 2^7, so P <= 2^15 and f16's smallest step is 2^-31 of a row's largest P
@@ -431,8 +433,8 @@ struct Q4Head {
   int pad[3];
 };
 
-// Copies tiles of a share into a warp's ring.
-template <int D, int NT>
+// Copies tiles of a share (CLUSTER: within one unit) into a warp's ring.
+template <int D, int NT, bool CLUSTER>
 struct Loader {
   using C = Q4Cfg<D, NT>;
   static constexpr int kHalf = 16 * D / 2;   // bytes of 16 keys' codes
@@ -560,6 +562,8 @@ struct Loader {
           }
           to_page(a);
         }
+      } else if constexpr (CLUSTER) {
+        more = false;
       } else {
         u.next(a);
         enter(a, 0, lane);
@@ -571,7 +575,68 @@ struct Loader {
 
 constexpr int kStored = 1, kFirst = 2, kLast = 4;
 
-template <int D, int NT, int MODE>
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// A float4 of CTA `rank` of the cluster, at the place that p is in this one's shared memory.
+__device__ __forceinline__ float4 load_of(const float4* p, int rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// Joins the pieces of a cluster's unit: each CTA its own, 8 rows a warp, and then
+// the CTAs and warps share out the unit's 16-feature tiles and read one another's.
+template <int D, int NT>
+__device__ __forceinline__ void join_cluster(const DecodeQ4Args& a, const Unit& u, uint8_t* smem, const int* rec_kind, int warp,
+                                             int lane) {
+  using C = Q4Cfg<D, NT>;
+  constexpr int kPer = Piece4<D, NT>::kPer, kMost = 8;
+  if (u.nb > 1) {          // else nothing, or written already
+    const int kind = lane < 2 * C::kWarps ? rec_kind[lane] : 0;
+    const unsigned slots = __ballot_sync(~0u, kind);
+    float4* own = piece_at<D, NT>(smem, 0) + lane;   // what the CTA has, over warp 0's piece: a lane reads its part before
+    for (int n = warp; n < NT; n += C::kWarps) {
+      Combined<D, C::kMT> x;
+      x.clear();
+      for (unsigned left = slots; left; left &= left - 1)
+        x.add(piece_at<D, NT>(smem, __ffs(left) - 1) + n * kPer * 32 + lane, C::kMT);
+#pragma unroll
+      for (int j = 0; j < C::kMT; ++j) own[(n * kPer + j) * 32] = make_float4(x.acc[j][0], x.acc[j][1], x.acc[j][2], x.acc[j][3]);
+      own[(n * kPer + C::kMT) * 32] = make_float4(x.m[0], x.m[1], x.l[0], x.l[1]);
+    }
+    cluster_barrier();
+    for (int tile = warp * a.cluster + blockIdx.x % a.cluster; tile < NT * C::kMT; tile += C::kWarps * a.cluster) {
+      const int n = tile / C::kMT, i = tile % C::kMT;
+      float4 y[kMost], ml[kMost];
+#pragma unroll
+      for (int r = 0; r < kMost; ++r)
+        if (r < a.cluster) {
+          y[r] = load_of(own + (n * kPer + i) * 32, r);
+          ml[r] = load_of(own + (n * kPer + C::kMT) * 32, r);
+        }
+      Combined<D, 1> x;
+      x.clear();
+      float top[2] = {x.m[0], x.m[1]};
+#pragma unroll
+      for (int r = 0; r < kMost; ++r)
+        if (r < a.cluster) top[0] = fmaxf(top[0], ml[r].x), top[1] = fmaxf(top[1], ml[r].y);
+      x.scale_to(0, top[0]);
+      x.scale_to(1, top[1]);
+#pragma unroll
+      for (int r = 0; r < kMost; ++r)
+        if (r < a.cluster) x.accumulate(ml[r], &y[r]);
+      write_tiles<D, NT>(a, u.b, u.k, u.len, n, i, x, lane);
+    }
+    cluster_barrier();     // no CTA leaves while its pieces are read
+  }
+}
+
+template <int D, int NT, int MODE, bool CLUSTER>
 __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(const DecodeQ4Args a) {
   using C = Q4Cfg<D, NT>;
   constexpr int PARTS = MODE == kRotated ? 2 : 1;
@@ -606,7 +671,21 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
       v0 = sh.begin(gw), v1 = sh.begin(gw + 1);
     }
   };
-  if (a.B > C::kThreads) {
+  if constexpr (CLUSTER) {
+    const int unit = blockIdx.x / a.cluster;
+    cu.b = unit / upb;
+    cu.k = unit - cu.b * upb;
+    cu.nb = row_tiles(a, cu.b, cu.len);
+    if (cu.nb == 0 && cu.k == 0 && tid == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+    // neighbouring shares go to different CTAs, so that few tiles still use all of them
+    const int gw = warp * a.cluster + blockIdx.x - unit * a.cluster;
+    Wn = min(cu.nb, a.cluster * C::kWarps);
+    if (gw < Wn) {
+      const Shares sh(cu.nb, Wn);
+      v0 = sh.begin(gw), v1 = sh.begin(gw + 1);
+    }
+  }
+  if (!CLUSTER && a.B > C::kThreads) {
     int mine = 0;
     for (int b = tid; b < a.B; b += C::kThreads) mine += positions(b);
     mine = __reduce_add_sync(~0u, mine);
@@ -617,7 +696,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     for (int w = 0; w < C::kWarps; ++w) all += sums[w];
     take_share(all);
   }
-  for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
+  for (int b0 = 0; !CLUSTER && b0 < a.B; b0 += C::kThreads) {
     int inc = 0;
     if (b0 + tid < a.B) {
       inc = positions(b0 + tid);
@@ -665,7 +744,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
   int ct = max(v0 - cu.P, 0), te = min(cu.nb, v1 - cu.P);
   if (v0 < v1 && ct < te) {
     const uint32_t ring = smem_u32(smem + warp * C::kRing);
-    Loader<D, NT> ld;
+    Loader<D, NT, CLUSTER> ld;
     ld.u = cu;
     ld.end = v1;
     ld.begin(a, lane);
@@ -913,6 +992,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
           rec_kind[slot] = kStored | (ta == 0 ? kFirst : 0) | (te == cu.nb ? kLast : 0);
         }
       }
+      if constexpr (CLUSTER) break;
       cu.next(a);
       fresh = true;
       ct = ta = 0;
@@ -922,6 +1002,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   __syncthreads();
+  if constexpr (CLUSTER) {
+    join_cluster<D, NT>(a, cu, smem, rec_kind, warp, lane);
+    return;
+  }
 
   // Combine the stored pieces of each unit, in stream order: a warp per 8 rows of a unit (shared out by its feature
   // tiles among more warps, a unit's chain of dependent steps is as long, and there are more of them)
@@ -1031,23 +1115,86 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_q4_merge(const Decode
   write_tiles<D, NT>(a, h.b, h.k, h.len, n, i, x, lane);
 }
 
-template <int D, int NT, int MODE>
-cudaError_t run(const DecodeQ4Args& a, int ctas, cudaStream_t stream) {
-  using C = Q4Cfg<D, NT>;
-  // once per device: the call costs a microsecond
-  static std::atomic<unsigned long long> done{0};
+constexpr int kMaxDevices = 64;
+int device() {
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (!bit || !(done.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_relaxed);
+  return cudaGetDevice(&dev) == cudaSuccess && dev < kMaxDevices ? dev : -1;
+}
+
+// The kernel's shared memory allowed, once per device: the call costs a microsecond.
+template <int D, int NT, int MODE, bool CLUSTER>
+cudaError_t allow_smem(int dev) {
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = 1ull << dev;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, MODE, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Q4Cfg<D, NT>::kSmem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// Clusters of 1 << log CTAs that run at once (a cluster's SMs are of one part of the chip, so fewer than SMs / CTAs).
+template <int D, int NT, int MODE>
+int clusters_at_once(int dev, int log) {
+  static std::atomic<int> known[kMaxDevices][4];   // one more than that; 0: not asked yet
+  int n = known[dev][log].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (allow_smem<D, NT, MODE, true>(dev) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1 << log);
+    cfg.blockDim = dim3(Q4Cfg<D, NT>::kThreads);
+    cfg.dynamicSmemBytes = Q4Cfg<D, NT>::kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1 << log;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, decode_q4_kernel<D, NT, MODE, true>, &cfg) != cudaSuccess || n < 0) n = 0;
+    known[dev][log].store(++n, std::memory_order_relaxed);
   }
+  return n - 1;
+}
+
+// CTAs of a unit's cluster, 0: the units are one stream.  A cluster each saves
+// the scan of the lengths, the second launch and the way through the workspace,
+// 2.5 us, but gives a unit the same share whatever its row's length, and leaves
+// SMs idle: taken where all clusters run at once, a row of S keys is at most 3
+// tiles a warp, and at most 2 more than its part of the stream.  8 K/V heads of
+// 128, 4 queries each, clusters against the stream: 1 row of 1024 keys 6.0 us,
+// 8.4; 4 rows of 2048 8.3, 11.3; 16 of 1024 9.1, 11.4.  2 heads: 1 row of 2048
+// keys 6.7, 8.0; of 4096 8.2, 8.6; of 8192 9.8, 9.3.
+template <int D, int NT, int MODE>
+int cluster_of(const DecodeQ4Args& a, int dev, int ctas) {
+  constexpr int kWarps = Q4Cfg<D, NT>::kWarps;
+  const long units = (long)a.B * a.Hkv * a.nrb, tiles = ((long)a.S + kTK - 1) / kTK;
+  if (units > ctas || tiles > 3 * 8 * kWarps) return 0;
+  for (int log = 3; log >= 0; --log) {
+    if (units << log > ctas || units > clusters_at_once<D, NT, MODE>(dev, log)) continue;
+    const float own = (float)tiles / (float)(kWarps << log), even = (float)(units * tiles) / (float)(kWarps * ctas);
+    return own <= 3.f && own - even <= 2.f ? 1 << log : 0;
+  }
+  return 0;
+}
+
+template <int D, int NT, int MODE, bool CLUSTER>
+cudaError_t run_kernel(const DecodeQ4Args& a, int dev, int ctas, cudaStream_t stream) {
+  cudaError_t e = allow_smem<D, NT, MODE, CLUSTER>(dev);
+  if (e != cudaSuccess) return e;
   prof_begin(kProfDecode, stream);
-  e = launch_programmatic(decode_q4_kernel<D, NT, MODE>, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, a);
+  e = launch_programmatic_clusters(decode_q4_kernel<D, NT, MODE, CLUSTER>, CLUSTER ? a.cluster : 1, dim3(ctas),
+                                   dim3(Q4Cfg<D, NT>::kThreads), Q4Cfg<D, NT>::kSmem, stream, a);
   prof_end(stream);
+  return e;
+}
+
+template <int D, int NT, int MODE>
+cudaError_t run(DecodeQ4Args a, int ctas, cudaStream_t stream) {
+  const int dev = device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  a.cluster = cluster_of<D, NT, MODE>(a, dev, ctas);
+  if (a.cluster) return run_kernel<D, NT, MODE, true>(a, dev, a.B * a.Hkv * a.nrb * a.cluster, stream);
+  cudaError_t e = run_kernel<D, NT, MODE, false>(a, dev, ctas, stream);
   if (e != cudaSuccess) return e;
   prof_begin(kProfDecodeMerge, stream);
   e = launch_programmatic(decode_q4_merge<D, NT>, dim3(ctas), dim3(kMergeWarps * 32), 0, stream, a);

@@ -86,6 +86,7 @@ struct DecodeQ4Args {
   void* ws;
   const float* rope_cs;      // [positions, D] or nullptr
   int B, Hq, Hkv, G, Tq, R, nrb, S, D;
+  int cluster;               // CTAs of a unit, 0: units in one stream
   int page_size, max_pages, num_pages;
   float scale_log2;          // softmax scale * k_scale * log2(e)
   float v_scale;
