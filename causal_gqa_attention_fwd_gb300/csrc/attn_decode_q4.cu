@@ -46,7 +46,7 @@
 // conversion (F2FP) or byte operation takes 2 cycles, an f16 multiplication 2,
 // an MMA 8, which overlap only in part: 226.6 MB of cache, queries, outputs and
 // tables take 45 us, 5.0 TB/s, 74% of a copy's rate.  Short rows by latency: 8
-// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 7.3 us in clusters (8.4 as a
+// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 6.4 us in clusters (8.4 as a
 // stream, of which 3 lie between the last warp's end and the merge's).
 #include <math_constants.h>
 
@@ -68,6 +68,7 @@ constexpr int kUnitCost = 2;   // what a unit costs beside its tiles, in tiles (
 // 128 (as a stream): 1 warp 9.1 us, 4 8.4, 8 8.8, 12 9.6; 8192 keys: 9.4, 9.4, 9.5,
 // 10.1.
 constexpr int kMinWarps = 4;
+constexpr int kMaxCluster = 8; // CTAs of a cluster
 constexpr float kLazy = 8.f;   // the maximum moves when it would grow by more than 2^8 ...
 constexpr float kOff = 7.f;    // ... and P is scaled by 2^7, so P <= 2^15 and f16's smallest step is 2^-31 of a row's largest P
 
@@ -595,7 +596,7 @@ template <int D, int NT>
 __device__ __forceinline__ void join_cluster(const DecodeQ4Args& a, const Unit& u, uint8_t* smem, const int* rec_kind, int warp,
                                              int lane) {
   using C = Q4Cfg<D, NT>;
-  constexpr int kPer = Piece4<D, NT>::kPer, kMost = 8;
+  constexpr int kPer = Piece4<D, NT>::kPer;
   if (u.nb > 1) {          // else nothing, or written already
     const int kind = lane < 2 * C::kWarps ? rec_kind[lane] : 0;
     const unsigned slots = __ballot_sync(~0u, kind);
@@ -612,9 +613,9 @@ __device__ __forceinline__ void join_cluster(const DecodeQ4Args& a, const Unit& 
     cluster_barrier();
     for (int tile = warp * a.cluster + blockIdx.x % a.cluster; tile < NT * C::kMT; tile += C::kWarps * a.cluster) {
       const int n = tile / C::kMT, i = tile % C::kMT;
-      float4 y[kMost], ml[kMost];
+      float4 y[kMaxCluster], ml[kMaxCluster];
 #pragma unroll
-      for (int r = 0; r < kMost; ++r)
+      for (int r = 0; r < kMaxCluster; ++r)
         if (r < a.cluster) {
           y[r] = load_of(own + (n * kPer + i) * 32, r);
           ml[r] = load_of(own + (n * kPer + C::kMT) * 32, r);
@@ -623,12 +624,12 @@ __device__ __forceinline__ void join_cluster(const DecodeQ4Args& a, const Unit& 
       x.clear();
       float top[2] = {x.m[0], x.m[1]};
 #pragma unroll
-      for (int r = 0; r < kMost; ++r)
+      for (int r = 0; r < kMaxCluster; ++r)
         if (r < a.cluster) top[0] = fmaxf(top[0], ml[r].x), top[1] = fmaxf(top[1], ml[r].y);
       x.scale_to(0, top[0]);
       x.scale_to(1, top[1]);
 #pragma unroll
-      for (int r = 0; r < kMost; ++r)
+      for (int r = 0; r < kMaxCluster; ++r)
         if (r < a.cluster) x.accumulate(ml[r], &y[r]);
       write_tiles<D, NT>(a, u.b, u.k, u.len, n, i, x, lane);
     }
@@ -1133,25 +1134,25 @@ cudaError_t allow_smem(int dev) {
   return e;
 }
 
-// Clusters of 1 << log CTAs that run at once (a cluster's SMs are of one part of the chip, so fewer than SMs / CTAs).
+// Clusters of c CTAs that run at once (a cluster's SMs are of one part of the chip, so fewer than SMs / c).
 template <int D, int NT, int MODE>
-int clusters_at_once(int dev, int log) {
-  static std::atomic<int> known[kMaxDevices][4];   // one more than that; 0: not asked yet
-  int n = known[dev][log].load(std::memory_order_relaxed);
+int clusters_at_once(int dev, int c) {
+  static std::atomic<int> known[kMaxDevices][kMaxCluster + 1];   // one more than that; 0: not asked yet
+  int n = known[dev][c].load(std::memory_order_relaxed);
   if (n == 0) {
     if (allow_smem<D, NT, MODE, true>(dev) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1 << log);
+    cfg.gridDim = dim3(c);
     cfg.blockDim = dim3(Q4Cfg<D, NT>::kThreads);
     cfg.dynamicSmemBytes = Q4Cfg<D, NT>::kSmem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 1 << log;
+    attr.val.clusterDim.x = c;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&n, decode_q4_kernel<D, NT, MODE, true>, &cfg) != cudaSuccess || n < 0) n = 0;
-    known[dev][log].store(++n, std::memory_order_relaxed);
+    known[dev][c].store(++n, std::memory_order_relaxed);
   }
   return n - 1;
 }
@@ -1168,11 +1169,11 @@ template <int D, int NT, int MODE>
 int cluster_of(const DecodeQ4Args& a, int dev, int ctas) {
   constexpr int kWarps = Q4Cfg<D, NT>::kWarps;
   const long units = (long)a.B * a.Hkv * a.nrb, tiles = ((long)a.S + kTK - 1) / kTK;
-  if (units > ctas || tiles > 3 * 8 * kWarps) return 0;
-  for (int log = 3; log >= 0; --log) {
-    if (units << log > ctas || units > clusters_at_once<D, NT, MODE>(dev, log)) continue;
-    const float own = (float)tiles / (float)(kWarps << log), even = (float)(units * tiles) / (float)(kWarps * ctas);
-    return own <= 3.f && own - even <= 2.f ? 1 << log : 0;
+  if (units > ctas || tiles > 3 * kMaxCluster * kWarps) return 0;
+  for (int c = kMaxCluster; c > 0; --c) {
+    if (units * c > ctas || units > clusters_at_once<D, NT, MODE>(dev, c)) continue;
+    const float own = (float)tiles / (float)(kWarps * c), even = (float)(units * tiles) / (float)(kWarps * ctas);
+    return own <= 3.f && own - even <= 2.f ? c : 0;
   }
   return 0;
 }

@@ -68,7 +68,7 @@ def test_decode_paged_q4_in_clusters_and_as_a_stream(gq, page, Hq, Tq, rope):
         close(o, lse, ref)
 
 
-@pytest.mark.parametrize("D,S,Hkv", [(128, 2048, 2), (64, 2048, 16), (128, 256, 70), (128, 900, 128), (64, 12288, 1)])
+@pytest.mark.parametrize("D,S,Hkv", [(128, 2048, 2), (64, 2048, 16), (128, 2048, 20), (64, 1500, 25), (128, 700, 40), (128, 256, 70), (128, 900, 128), (64, 12288, 1)])
 def test_decode_q4_cluster_sizes(gq, D, S, Hkv):
     """One row: from a whole cluster for each of few units to a CTA a unit; lengths from one tile to the capacity."""
     for n in (1, 33, S // 2 + 1, S):
