@@ -15,6 +15,7 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/util/accumulate.h>
 
 #include <cmath>
 #include <stdexcept>
@@ -131,6 +132,27 @@ void check(attn_status st, const char* name) {
 
 at::TensorOptions on(const at::Tensor& like, at::ScalarType t) { return like.options().dtype(t).memory_format(c10::nullopt); }
 
+// A contiguous part of `all` from an entry on, not through the dispatcher (five of them took 6 us).
+at::Tensor part(const at::Tensor& all, int64_t entry, at::IntArrayRef sizes) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(entry);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+  return t;
+}
+// bf16 outputs that are missing.  Two small ones (1 MB in all) share an allocation: gathering 64 slots takes the host
+// 4.2 us so, and 4.9 with two; large ones do not, so that either can be freed by itself.
+void allocate(at::Tensor& a, at::IntArrayRef a_sizes, at::Tensor& b, at::IntArrayRef b_sizes, const at::Tensor& like) {
+  const int64_t na = c10::multiply_integers(a_sizes), nb = c10::multiply_integers(b_sizes);
+  if (!a.defined() && !b.defined() && na % 8 == 0 && na + nb <= 1 << 19) {
+    const at::Tensor all = at::empty({na + nb}, on(like, at::kBFloat16));
+    a = part(all, 0, a_sizes);
+    b = part(all, na, b_sizes);
+    return;
+  }
+  if (!a.defined()) a = at::empty(a_sizes, on(like, at::kBFloat16));
+  if (!b.defined()) b = at::empty(b_sizes, on(like, at::kBFloat16));
+}
+
 // (B, T, H, D) of a [total, H, D] or [B, H, T, D] tensor, and its batch, token
 // and head strides in elements; those of single entries are 0.
 struct Tokens {
@@ -214,16 +236,10 @@ PyObject* plan(PyObject* const* a, Py_ssize_t n) {
     missing |= !out[i].defined();
   }
   if (missing) {
-    // one allocation, and parts of it that do not go through the dispatcher (five of them took 6 us)
     const at::Tensor all = at::empty({2 * (int64_t)total + 2 * (int64_t)B + 2}, on(lens, at::kInt));
-    int64_t at_entry = 0;
-    for (int i = 0; i < 5; at_entry += sizes[i++]) {
-      if (out[i].defined()) continue;
-      out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
-      c10::TensorImpl* impl = out[i].unsafeGetTensorImpl();
-      impl->set_storage_offset(at_entry);
-      impl->set_sizes_contiguous(at::IntArrayRef(sizes + i, 1));
-    }
+    int64_t entry = 0;
+    for (int i = 0; i < 5; entry += sizes[i++])
+      if (!out[i].defined()) out[i] = part(all, entry, at::IntArrayRef(sizes + i, 1));
   }
   for (int i = 0; i < 5; ++i) {
     if (out[i].numel() != sizes[i])
@@ -277,7 +293,7 @@ PyObject* rope(PyObject* const* a, Py_ssize_t n) {
     const Tokens u = tokens_of(k, "k");
     if (u.B != t.B || u.T != t.T || u.D != t.D) value_error("k must have q's tokens and head dimension");
     Hkv = u.H;
-    if (!ko.defined()) ko = at::empty(k.sizes(), on(k, k.scalar_type()));
+    allocate(qo, q.sizes(), ko, k.sizes(), q);
     if (ko.sizes() != k.sizes()) value_error("k_out must have k's shape");
     strides_of(k, "k", s + 3);
     strides_of(ko, "k_out", s + 9, true);
@@ -398,10 +414,9 @@ PyObject* gather(PyObject* const* a, Py_ssize_t n) {
   const int tokens = to_int(slots.numel(), "slots");
   at::Tensor out[2] = {optional(a[7], "k"), optional(a[8], "v")};
   const int64_t shape[3] = {tokens, c.H, c.D};
-  for (at::Tensor& t : out) {
-    if (!t.defined()) t = at::empty(at::IntArrayRef(shape, 3), on(slots, at::kBFloat16));
-    if (t.sizes() != at::IntArrayRef(shape, 3)) value_error("k, v must be [tokens, Hkv, D]");
-  }
+  const at::IntArrayRef sizes(shape, 3);
+  allocate(out[0], sizes, out[1], sizes, slots);
+  if (out[0].sizes() != sizes || out[1].sizes() != sizes) value_error("k, v must be [tokens, Hkv, D]");
   const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
   check(g_fn.gather_q4(address_of<const int>(slots, "slots", at::kInt, dev), c.p[0], c.p[1], c.p[2], c.p[3],
                        (float)float_arg(a[5]), (float)float_arg(a[6]), address(out[0], "k", at::kBFloat16, dev),
