@@ -652,7 +652,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
 
   griddep_wait();                            // launched while the kernel before drains
   griddep_launch();                          // the merge waits for this grid's end in any case
-  if (tid < 2 * C::kWarps) rec_kind[tid] = 0;
+  // a warp's own entries, by the thread that sets them: in a cluster no barrier stands between this and the pieces
+  if (lane == 0) rec_kind[2 * warp] = rec_kind[2 * warp + 1] = 0;
   // The positions of all units, and the batch row that holds the share's first:
   // inclusive sums over the rows, kThreads rows at a time (more rows: a pass for the total first).
   int total = 0, Wn = 0, wpc = 1, v0 = 0, v1 = 0, before = 0;

@@ -103,3 +103,23 @@ def test_decode_q4_clusters_report_lengths_and_are_captured(gq):
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
         assert gq.get_device_status() == 0
         close(o, lse, reference(q, cache, lens_of(n), 0.1))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,Tq,rope", [(64, 14, 2, 1, False), (128, 16, 4, 4, False), (128, 4, 1, 1, True), (64, 8, 1, 2, True)])
+def test_decode_q4_clusters_repeat_themselves(gq, D, Hq, Hkv, Tq, rope):
+    """Every piece of every call is joined: 300 replays of four calls over other lengths give the first ones' bits."""
+    B, S = 2, 2048
+    q, cache = queries(B, Hq, Tq, D, 78).cuda(), [c.cuda() for c in cache_of(B, Hkv, S, D, 79)]
+    tab = W.rope_cos_sin_table(S, D).cuda() if rope else None
+    lens = [lens_of(n).cuda() for n in ([S, 1], [33, 700], [1500, 64], [97, 2000])]
+    calls = lambda: [gq.attn_decode_q4_fwd(q, *cache, KS, VS, n, scale=0.1, rope_cos_sin=tab) for n in lens]  # noqa: E731
+    want = calls()
+    for n, (o, lse) in zip(lens, want):
+        close(o, lse, reference(q.cpu(), [c.cpu() for c in cache], n.cpu(), 0.1, tab=None if tab is None else tab.cpu()))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = calls()
+    for _ in range(300):
+        g.replay()
+        assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+    assert gq.get_device_status() == 0
