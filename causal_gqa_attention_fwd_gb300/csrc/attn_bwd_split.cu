@@ -542,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) atomicCAS(a.status, 0, kDevInternal);
+    griddep_wait();
     return;
   }
   const int n_tiles = a.n_items * a.num_seqs * a.Hq;
@@ -937,6 +938,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  // A kernel launched as this one's dependent waits for this grid alone: it
+  // ends after the dK/dV grid, so that dK, dV and the workspace are done with.
+  griddep_wait();
 }
 
 // ==================================================================== launch
@@ -965,8 +969,9 @@ static cudaError_t launch_split(const CUtensorMap& q, const CUtensorMap& k, cons
   // dQ kernel: programmatic dependent launch.  It reads only the inputs and
   // the preprocess's rows (complete once every dK/dV CTA has passed its
   // griddep_wait, which is when that grid lets this one start) and writes
-  // only dQ, so it never waits on the dK/dV grid: its CTAs fill the SMs that
-  // grid leaves idle (its tail; all of a small grid's spare SMs).
+  // only dQ, so its CTAs work beside the dK/dV grid, on the SMs that grid
+  // leaves idle (its tail; all of a small grid's spare SMs), and wait for it
+  // only before they end (every CTA of that grid runs or has run by then).
   // persistent: at most one CTA per SM, each taking tiles until none is left
   static int sms[64] = {};
   if (dev < 64 && sms[dev] == 0) {

@@ -116,6 +116,41 @@ def test_rope_same_as_the_prefill_forward_takes(gq):
     assert float((a.float() - b.float()).norm() / b.float().norm()) < 3 * 2.0 ** -8
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,T,D", [(1, 2, 1, 40, 64), (1, 8, 2, 300, 128), (2, 4, 4, 129, 128), (1, 14, 2, 200, 64)])
+def test_rope_bwd_right_after_attn_bwd(gq, B, Hq, Hkv, T, D):
+    """The backward of rotate-then-attend without a rest between, on small shapes, where the dK/dV kernel is the last to
+    end: the gradients of each call alone, eager (the outputs take the memory of the workspace that was freed) and
+    captured, and a forward behind it."""
+    from causal_gqa_attention_fwd_gb300 import workloads as W
+    x = W.dense_inputs(B, Hq, Hkv, T, D, seed=6)
+    q, k, v, do = (x[m].cuda() for m in ("q", "k", "v", "do"))
+    tab, pos = gq.attn_rope_table(T, D), torch.arange(T, dtype=torch.int32, device="cuda")
+
+    def both(rest):
+        qr, kr = gq.attn_rope(q, k, pos, tab)
+        rest()
+        o, lse = gq.attn_fwd(qr, kr, v)
+        rest()
+        dqr, dkr, dv = gq.attn_bwd(qr, kr, v, o, lse, do)
+        rest()
+        dq, dk = gq.attn_rope_bwd(dqr, dkr, pos, tab)
+        rest()
+        return dqr, dkr, dq, dk, dv, *gq.attn_fwd(q, k, v)
+
+    want = both(torch.cuda.synchronize)
+    for n, g in ((0, 2), (1, 3)):
+        close(want[g], R.rope(want[n].cpu(), pos.cpu(), tab.cpu(), False, -1.0), want[n].cpu(), D)
+    for _ in range(30):
+        assert all(torch.equal(a, b) for a, b in zip(both(lambda: None), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(lambda: None)
+    for _ in range(100):
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert gq.get_device_status() == 0
+
+
 def test_rope_positions_outside_the_table(gq):
     q = torch.randn(4, 2, 64).bfloat16()
     pos = torch.tensor([0, 10, -1, 9], dtype=torch.int32)
