@@ -466,7 +466,7 @@ struct Loader {
     const long page_bytes = (long)a.Hkv * a.page_size * (D / 2);
     const int p0 = __shfl_sync(~0u, entry[0], pidx - pbase);
     ok[0] = ok[1] = (unsigned)p0 < (unsigned)a.num_pages;
-    off[0] = (ok[0] ? p0 : 0) * page_bytes + head + inpg * (D / 2);
+    off[0] = (ok[0] ? p0 : 0) * page_bytes + head + (long)inpg * (D / 2);
     off[1] = off[0] + kHalf;
     if (a.page_size == 16) {
       const int p1 = __shfl_sync(~0u, entry[0], pidx - pbase + 1);

@@ -120,6 +120,7 @@ attn_status decode_q4_check(int B, int Hq, int Hkv, int Tq, int S, int D) {
   if (st != ATTN_OK) return st;
   if (B == 0 || Tq == 0) return ATTN_OK;
   if (Tq > S) return ATTN_ERR_SHAPE;
+  if (S > 0x7fffffff - 32) return ATTN_ERR_SHAPE;   // a row's last 32-key tile ends within 32 bits
   if ((long)B * Hq * Tq > 0x7fffffffL) return ATTN_ERR_SHAPE;
   // the kernel numbers the 32-key tiles (and three more) of all (row, K/V head, block of 8 or 16 query rows) units
   const long blocks = ((long)Hq / Hkv * Tq + 7) / 8;

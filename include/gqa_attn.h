@@ -461,7 +461,8 @@ GQA_ATTN_API attn_status attn_cache_gather_q4(const int* slots, const void* k4, 
  * is rounded to f16 for the P V product (f32 accumulation).
  * workspace: attn_decode_q4_workspace_size() bytes, 256-byte aligned, no
  * initialisation; calls in flight at once need one each.  Errors as
- * attn_decode_fwd; the cache tensors must be 16-byte aligned. */
+ * attn_decode_fwd; the cache tensors must be 16-byte aligned.  S (paged:
+ * max_pages * page_size) is at most 2^31 - 33. */
 GQA_ATTN_API size_t attn_decode_q4_workspace_size(int B, int Hq, int Hkv, int Tq, int S, int D);
 GQA_ATTN_API attn_status attn_decode_q4_fwd(const void* q, const void* k4, const void* k4_sf, const void* v4,
                                             const void* v4_sf, float k_scale, float v_scale, const int* cache_lens,

@@ -116,6 +116,23 @@ def test_decode_q4_refusals(lib):
     assert p(bt=A + 2) == 4 and p(tab=A, n=511) == 2 and p(mp=1 << 26) == 2
 
 
+def test_decode_q4_capacities_near_2_31(lib):
+    """The kernel counts a row's keys in 32-key tiles with 32-bit positions, one tile past the last at most: capacities
+    whose last tile would end past 2^31 - 1 are refused, the ones below are not."""
+    most = 0x7fffffff - 32
+    for D in (64, 128):
+        assert lib.attn_decode_q4_workspace_size(1, 1, 1, 1, most, D) > 0
+        for S in (most + 1, 0x7ffffffe, 0x7fffffff):
+            assert lib.attn_decode_q4_workspace_size(1, 1, 1, 1, S, D) == 0
+            assert lib.attn_decode_q4_fwd(A, A, A, A, A, 0.1, 0.1, A, A, A, A, 1 << 40, 1, 1, 1, 1, S, D, 0.1, None, 0, None) == 2
+
+        def paged(page, max_pages):
+            return lib.attn_decode_paged_q4_fwd(A, A, A, A, A, 0.1, 0.1, A, A, A, A, NULL, 0, 1, 1, 1, 1, page, 1, max_pages, D,
+                                                0.1, None, 0, None)
+        assert paged(16, (1 << 27) - 1) == 2 and paged(16, (1 << 27) - 2) == 2      # 2^31 - 16, 2^31 - 32
+        assert paged(16, (1 << 27) - 3) == 6 and paged(0x7fffff80, 1) == 6          # 2^31 - 48, - 128: only the workspace lacks
+
+
 def test_binding_refuses_cpu_tensors():
     import causal_gqa_attention_fwd_gb300 as g
     x = torch.zeros(2, 2, 64, dtype=torch.bfloat16)

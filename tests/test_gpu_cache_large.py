@@ -92,3 +92,28 @@ def test_append_heads_beyond_4_gib(gq, fmt):
     assert gq.get_device_status() == 0
     for c, w in zip(cache, want):
         assert torch.equal(c[0][:, at.cuda()].transpose(0, 1).cpu(), w)
+
+
+@pytest.mark.parametrize("D,rows", [(128, 2 ** 25), (64, 2 ** 26)])
+def test_q4_one_page_of_a_whole_request(gq, D, rows):
+    """A page of more rows than 2^31 bytes of codes hold, the request's only one, read to its end: all keys zero but the
+    last ones; and the same page as a contiguous cache.  n0 zero keys add exp(0) each to the sum and nothing to O."""
+    page, n, Hq = rows + 384, 300, 4
+    cache = [torch.zeros(2, 1, page, w, dtype=torch.uint8, device="cuda") for w in (D // 2, D // 16) * 2]
+    length = page - 7
+    at = page + length - n                        # in the pool's second page
+    g = torch.Generator().manual_seed(D)
+    k, v = (torch.randn(n, 1, D, generator=g).bfloat16() for _ in range(2))
+    gq.attn_cache_append_q4(k.cuda(), v.cuda(), torch.arange(at, at + n, dtype=torch.int32, device="cuda"), *cache, KS, VS)
+    K, V = (x.transpose(0, 1)[None] for x in quantised(k, v))
+    q, scale, n0 = queries(1, Hq, 1, D, 5), 6.0 / math.sqrt(D), length - n
+    o, lse, spread, weight = R.decode(q, K, V, [n], scale)
+    full = torch.logaddexp(lse, torch.tensor(math.log(n0), dtype=torch.float64))
+    part = (lse - full).exp()[..., None]
+    # spread is sum_j (p_j + 2^-15) |v_j|: its p shrink by `part`; as it is, it bounds that
+    assert float(part.min()) > 0.02 and float(part.max()) < 0.98      # both kinds of keys count
+    ref = (o * part, full, spread, weight)
+    lens = torch.tensor([length], dtype=torch.int32).cuda()
+    close(*gq.attn_decode_paged_q4_fwd(q.cuda(), *cache, KS, VS, torch.tensor([[1]], dtype=torch.int32).cuda(), lens, scale=scale), ref)
+    close(*gq.attn_decode_q4_fwd(q.cuda(), *(c[1:] for c in cache), KS, VS, lens, scale=scale), ref)
+    assert gq.get_device_status() == 0
