@@ -5,7 +5,8 @@ over 4-bit caches.
 All tensors of a call are on one device, which need not be the current one; the
 kernels run on ``stream`` (a torch.cuda.Stream or a handle), or on that device's
 current stream, and so is allocated what the call allocates: an output used on
-another stream afterwards needs Tensor.record_stream, as ever.  Checks, output
+another stream afterwards needs Tensor.record_stream, as ever.  A torch.cuda.Stream
+of another device is refused; a handle is taken for one of the tensors' device.  Checks, output
 allocation and the C calls are native (csrc/cache_binding.cpp): a decode step's
 calls take a few microseconds each.
 """
@@ -41,13 +42,16 @@ def _ext():
     return _mod
 
 
-def _run(stream, f, *args):
-    """f(*args) on `stream`: made the current one, so that what the call allocates belongs to it."""
+def _run(stream, f, *args, device=None):
+    """f(*args) on `stream`: made the current one, so that what the call allocates belongs to it.  device: the call's,
+    where no tensor among args tells it (None: the stream's, or for a handle the current one)."""
     if stream is None:
         return f(*args)
+    device = next((t.device for t in args if isinstance(t, torch.Tensor) and t.is_cuda), device)
     if not isinstance(stream, torch.cuda.Stream):
-        on = next((t.device for t in args if isinstance(t, torch.Tensor) and t.is_cuda), None)
-        stream = torch.cuda.ExternalStream(int(stream), device=on)
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif device is not None and stream.device != device:
+        raise ValueError(f"the stream is one of {stream.device}, the call's tensors are on {device}")
     with torch.cuda.stream(stream):
         return f(*args)
 
@@ -70,11 +74,19 @@ def attn_rope_table(n: int, rotary_dim: int, base: float = 10000.0, factor: floa
     """Rotary table float32 [n, rotary_dim] (cosines, then sines) of positions 0..n-1, frequencies
     base^(-2i/rotary_dim): divided by factor, or with original_positions > 0 only those that make few turns over the
     original context (all below low_turns, none above high_turns, in between blended); entries times mscale."""
+    on = None                                       # out's
+    if out is None:
+        if device is None and isinstance(stream, torch.cuda.Stream):
+            device = stream.device
+        on = torch.device("cuda", device) if isinstance(device, int) else torch.device(device or "cuda")
+        if on.type == "cuda" and on.index is None:
+            on = torch.device("cuda", torch.cuda.current_device())
+
     def make(out):
         if out is None:
-            out = torch.empty(n, rotary_dim, dtype=torch.float32, device="cuda" if device is None else device)
+            out = torch.empty(n, rotary_dim, dtype=torch.float32, device=on)
         return _ext().rope_table(out, n, rotary_dim, base, factor, original_positions, low_turns, high_turns, mscale)
-    return _run(stream, make, out)
+    return _run(stream, make, out, device=on)
 
 
 def attn_rope(q, k, positions, rope_cos_sin, interleaved: bool = False, q_out=None, k_out=None, stream=None):

@@ -166,6 +166,70 @@ def test_native_module_fails_loudly_when_missing(monkeypatch):
         _cache._ext()
 
 
+class OnCuda1(torch.Tensor):
+    is_cuda = True
+    device = torch.device("cuda", 1)
+
+
+class FakeStream:
+    def __init__(self, handle, device=None):
+        self.handle, self.device = handle, device if device is None else torch.device(device)
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """torch.cuda's streams without a GPU: the streams that calls were made on; cuda:0 is the current device."""
+    import contextlib
+    used = []
+
+    @contextlib.contextmanager
+    def use(s):
+        used.append((s.handle, s.device))
+        yield
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", type("FakeExternal", (FakeStream,), {}))
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return used
+
+
+def test_a_call_runs_on_its_stream_of_the_tensors_device(streams):
+    from causal_gqa_attention_fwd_gb300 import _cache
+    x = torch.zeros(2).as_subclass(OnCuda1)
+    dev = torch.device("cuda", 1)
+    assert _cache._run(77, lambda *a: a, None, x) == (None, x)
+    assert _cache._run(FakeStream(5, "cuda:1"), lambda *a: len(a), x) == 1
+    assert streams == [(77, dev), (5, dev)]
+    with pytest.raises(ValueError, match="cuda:0.*cuda:1"):
+        _cache._run(FakeStream(6, "cuda:0"), lambda *a: 1, x)
+    assert len(streams) == 2
+
+
+def test_rope_table_runs_on_the_given_devices_stream(streams, monkeypatch):
+    """Without `out` there is no tensor to tell the device of a handle."""
+    import types
+
+    from causal_gqa_attention_fwd_gb300 import _cache
+    made = []
+    monkeypatch.setattr(torch, "empty", lambda *s, dtype, device: made.append(device) or torch.zeros(*s, dtype=dtype))
+    monkeypatch.setattr(_cache, "_ext", lambda: types.SimpleNamespace(rope_table=lambda out, *a: out))
+    one = torch.device("cuda", 1)
+    for device in (1, "cuda:1", one):
+        _cache.attn_rope_table(4, 16, device=device, stream=77)
+        assert streams.pop() == (77, one) and torch.device(made.pop()) == one
+        _cache.attn_rope_table(4, 16, device=device, stream=FakeStream(5, one))
+        assert streams.pop() == (5, one) and torch.device(made.pop()) == one
+        with pytest.raises(ValueError, match="cuda:0"):
+            _cache.attn_rope_table(4, 16, device=device, stream=FakeStream(5, "cuda:0"))
+    for device in (None, "cuda"):                       # the current device's
+        _cache.attn_rope_table(4, 16, device=device, stream=78)
+        assert streams.pop() == (78, torch.device("cuda", 0)) and str(made.pop()).startswith("cuda")
+    _cache.attn_rope_table(4, 16, stream=FakeStream(5, one))            # no device named: the stream's
+    assert streams.pop() == (5, one) and torch.device(made.pop()) == one
+    _cache.attn_rope_table(4, 16, out=torch.zeros(4, 16).as_subclass(OnCuda1), stream=79)
+    assert streams.pop() == (79, one) and not made and not streams
+
+
 # ------------------------------------------------------------ the references
 def test_reference_quantisation_by_hand():
     """One block whose scale is exactly 1: amax 6; ties go to the even code; the sign is the top bit."""
