@@ -455,10 +455,13 @@ GQA_ATTN_API attn_status attn_cache_gather_q4(const int* slots, const void* k4, 
  * negative position (cache_lens[b] < Tq) sees no key and gets O = 0, LSE =
  * -infinity, so a batch slot without a request is a row of length 0.  A row
  * outside that range is reported (ATTN_ERR_SEQLENS), its outputs unwritten.
- * e2m1 * e4m3 is exact in f16; the query rows (after rotation, if any) are
- * scaled by a power of two per row and carried in f16, value and remainder
- * when rotated, so the scores' only roundings are the f32 accumulation's.  P
- * is rounded to f16 for the P V product (f32 accumulation).
+ * e2m1 * e4m3 is exact in f16; the query rows (after rotation in f32, if any)
+ * are scaled by a power of two per row and carried in f16, value and remainder
+ * when rotated.  A plain query's feature is exact down to 2^-31 of its row's
+ * largest, and below that off by at most 2^-39 of it; a rotated one is off by
+ * at most 2^-22 of itself and 2^-39 of the largest.  Else the scores' only
+ * roundings are the f32 accumulation's.  P is rounded to f16 for the P V
+ * product (f32 accumulation).
  * workspace: attn_decode_q4_workspace_size() bytes, 256-byte aligned, no
  * initialisation; calls in flight at once need one each.  Errors as
  * attn_decode_fwd; the cache tensors must be 16-byte aligned.  S (paged:

@@ -238,6 +238,40 @@ def test_decode_q4_query_magnitudes(gq, std):
     close(o, lse, reference(q, cache, lens, scale))
 
 
+@pytest.mark.parametrize("rope", [False, True])
+@pytest.mark.parametrize("Tq", [1, 3])
+@pytest.mark.parametrize("big", [20, 30, 34])
+def test_decode_q4_one_outlier_feature(gq, big, Tq, rope):
+    """A query feature of 2^big where the keys are 0, beside others of N(0,1): rows are scaled by their largest, so the
+    others lose bits.  In f16 a plain feature is off by at most 2^-39 of the row's largest, M (half of f16's smallest step,
+    2^-25, against 2^14); a rotated one by that, by 2^-22 of itself (two f16 parts), and by the rotation's f32 roundings,
+    3 2^-24 of its pair (|a| + |b|; a table of magnitude 1).  A score is off by delta = scale sum_d |k_d| (that), LSE by
+    delta, a weight by a factor of e^(2 delta), beside the usual bounds."""
+    B, Hq, Hkv, S, D = 2, 6, 2, 333, 64
+    lens = lens_of([333, 129])
+    q, cache = queries(B, Hq, Tq, D, 40), cache_of(B, Hkv, S, D, 41)
+    q[..., 5] = 2.0 ** big
+    cache[0][..., 2] &= 0x0f                       # features 5 and 37, its pair: code 0 (the high half bytes)
+    cache[0][..., 18] &= 0x0f
+    tab = W.rope_cos_sin_table(S, D) if rope else None
+    ref = reference(q, cache, lens, 0.125, tab=tab)
+    ka = R.values(cache[0], cache[1], KS).abs().repeat_interleave(Hq // Hkv, 1)[:, :, None]       # [B, Hq, 1, S, D]
+    x = q.double()
+    M = x.abs().amax(-1, keepdim=True) * (2 if rope else 1)
+    off = 2.0 ** -39 * M
+    if rope:
+        pair = x.abs() + x.abs().roll(D // 2, -1)
+        off = off + (2.0 ** -22 + 3 * 2.0 ** -24) * pair
+    delta = 0.125 * (ka * off[..., None, :]).sum(-1).amax(-1)                                       # [B, Hq, Tq]
+    o, lse = (t.double().cpu() for t in run(gq, q, cache, lens, 0.125, tab=tab))
+    assert gq.get_device_status() == 0
+    ro, rl, spread, weight = ref
+    assert ((o - ro).abs() <= 2.0 ** -8 * ro.abs() + (2.0 ** -10 + torch.expm1(2 * delta)[..., None] * 1.01) * spread).all()
+    assert ((lse - rl).abs() <= delta + 2.0 ** -16 * weight + 2.0 ** -16 + 2.0 ** -22 * rl.abs()).all()
+    if big == 20 and not rope:                     # every bit is kept
+        close(o, lse, ref)
+
+
 def test_decode_q4_large_scores(gq):
     """Scores in the hundreds, either sign: one key takes almost all."""
     B, Hq, Hkv, S, D = 2, 8, 2, 2100, 128
