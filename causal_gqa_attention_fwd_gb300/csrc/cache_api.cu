@@ -132,7 +132,8 @@ attn_status decode_q4(const void* q, const void* k4, const void* ksf, const void
                       float v_scale, const int* block_table, const int* cache_lens, void* o, float* lse, void* ws,
                       size_t ws_bytes, int B, int Hq, int Hkv, int Tq, int S, int D, int page_size, int num_pages,
                       int max_pages, float scale, const float* cs, int n_table, void* stream) {
-  if (!isfinite(scale) || !isfinite(k_scale) || !isfinite(v_scale)) return ATTN_ERR_SHAPE;
+  const float scale_log2 = scale * k_scale * 1.4426950408889634f;
+  if (!isfinite(scale_log2) || !isfinite(scale) || !isfinite(k_scale) || !isfinite(v_scale)) return ATTN_ERR_SHAPE;
   if (!q || !k4 || !ksf || !v4 || !vsf || !cache_lens || !o || !lse) return ATTN_ERR_NULL;
   if (!aligned(q, 16) || !aligned(k4, 16) || !aligned(ksf, 16) || !aligned(v4, 16) || !aligned(vsf, 16) ||
       !aligned(o, 16) || !aligned(lse, 16) || !aligned(cache_lens, 4) || !aligned(block_table, 4))
@@ -168,7 +169,7 @@ attn_status decode_q4(const void* q, const void* k4, const void* ksf, const void
   a.page_size = page_size;
   a.max_pages = max_pages;
   a.num_pages = num_pages;
-  a.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.v_scale = v_scale;
   a.status = gqa::api_status_word();
   a.dbg_line = gqa::api_check_line();
@@ -212,7 +213,7 @@ attn_status attn_rope_table(float* rope_cos_sin, int n, int rotary_dim, double b
                             void* stream) {
   if (n < 0 || rotary_dim < 16 || rotary_dim > 512 || rotary_dim % 16 || original_positions < 0) return ATTN_ERR_SHAPE;
   if (!isfinite(base) || !isfinite(factor) || !isfinite(low_turns) || !isfinite(high_turns) || !isfinite(mscale) ||
-      base <= 1.0 || factor <= 0.0 || low_turns >= high_turns)
+      base <= 1.0 || factor <= 0.0 || low_turns >= high_turns || !isfinite((float)mscale) || !isfinite(1.0 / factor))
     return ATTN_ERR_SHAPE;
   if (n == 0) return ATTN_OK;
   if (!rope_cos_sin) return ATTN_ERR_NULL;

@@ -374,8 +374,9 @@ GQA_ATTN_API attn_status attn_cache_plan(const int* cache_lens, const int* new_l
  * Cosines and sines are multiplied by mscale.  The angle of a position is
  * taken in fixed point (64 bits of a turn from a frequency in double), so that
  * far positions lose little: entries whose angle is below 2^24 are within
- * 2^-22 |mscale| of the exact ones.  rotary_dim: a multiple of 16, at most 512.  base > 1, factor > 0, low_turns <
- * high_turns, all finite. */
+ * 2^-22 |mscale| of the exact ones.  rotary_dim: a multiple of 16, at most
+ * 512.  base > 1, factor > 0, low_turns < high_turns, all finite, and so are
+ * 1 / factor and mscale in float32. */
 GQA_ATTN_API attn_status attn_rope_table(float* rope_cos_sin, int n, int rotary_dim, double base, double factor,
                                          int original_positions, double low_turns, double high_turns, double mscale,
                                          void* stream);
@@ -465,7 +466,8 @@ GQA_ATTN_API attn_status attn_cache_gather_q4(const int* slots, const void* k4, 
  * workspace: attn_decode_q4_workspace_size() bytes, 256-byte aligned, no
  * initialisation; calls in flight at once need one each.  Errors as
  * attn_decode_fwd; the cache tensors must be 16-byte aligned.  S (paged:
- * max_pages * page_size) is at most 2^31 - 33. */
+ * max_pages * page_size) is at most 2^31 - 33; scale * k_scale * log2(e) is
+ * finite in float32. */
 GQA_ATTN_API size_t attn_decode_q4_workspace_size(int B, int Hq, int Hkv, int Tq, int S, int D);
 GQA_ATTN_API attn_status attn_decode_q4_fwd(const void* q, const void* k4, const void* k4_sf, const void* v4,
                                             const void* v4_sf, float k_scale, float v_scale, const int* cache_lens,

@@ -133,6 +133,20 @@ def test_decode_q4_capacities_near_2_31(lib):
         assert paged(16, (1 << 27) - 3) == 6 and paged(0x7fffff80, 1) == 6          # 2^31 - 48, - 128: only the workspace lacks
 
 
+def test_parameters_that_overflow_in_the_kernels_are_refused(lib):
+    """Finite in what the call takes, infinite in what the kernel works with."""
+    def table(factor=1.0, m=1.0):
+        return lib.attn_rope_table(A, 8, 64, 1e4, factor, 0, 1.0, 32.0, m, None)
+    for m in (1e39, -1e39, 3.5e38):                                  # mscale is applied in f32
+        assert table(m=m) == 2
+    assert table(factor=1e-310) == 2                                 # 1 / factor
+    size = (2, 4, 2, 1, 4096, 64)
+    for scale, ks in ((1e30, 1e30), (-1e30, 1e30), (3e38, 1.0), (1.0, 3e38)):       # scale * k_scale * log2(e) is one f32
+        assert lib.attn_decode_q4_fwd(A, A, A, A, A, ks, 0.1, A, A, A, A, 1 << 40, *size, scale, None, 0, None) == 2
+        assert lib.attn_decode_paged_q4_fwd(A, A, A, A, A, ks, 0.1, A, A, A, A, A, 1 << 40, 2, 4, 2, 1, 64, 8, 64, 64, scale,
+                                            None, 0, None) == 2
+
+
 def test_binding_refuses_cpu_tensors():
     import causal_gqa_attention_fwd_gb300 as g
     x = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
