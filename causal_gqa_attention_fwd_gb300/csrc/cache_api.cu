@@ -197,8 +197,13 @@ attn_status attn_cache_plan(const int* cache_lens, const int* new_lens, int* blo
                        cursor_out};
   for (const void* p : all)
     if (!aligned(p, 4)) return ATTN_ERR_ALIGN;
-  // several CTAs read the lengths and the cursor: no output may replace them
-  if ((B > 0 && (lens_out == cache_lens || lens_out == new_lens)) || cursor_out == cursor) return ATTN_ERR_SHAPE;
+  // several CTAs read the inputs while others write: no output may replace an entry of them
+  const struct { const int* p; long n; } in[] = {{cache_lens, B}, {new_lens, B}, {cursor, 1}, {free_pages, num_free},
+                                                 {block_table, (long)B * max_pages}},
+      out[] = {{slots, total_tokens}, {positions, total_tokens}, {cu_seqlens, B + 1L}, {lens_out, B}, {cursor_out, 1}};
+  for (const auto& i : in)
+    for (const auto& o : out)
+      if (i.p && o.p && i.n > 0 && o.n > 0 && i.p < o.p + o.n && o.p < i.p + i.n) return ATTN_ERR_SHAPE;
   const attn_status st = gqa::api_check_arch();
   if (st != ATTN_OK) return st;
   gqa::PlanArgs a{cache_lens, new_lens, free_pages, cursor,    block_table, slots, positions,    cu_seqlens,

@@ -349,7 +349,7 @@ GQA_ATTN_API attn_status attn_decode_paged_fp8_fwd(const void* q, const void* k8
  *   cu_seqlens        [B + 1]  each request's first packed token
  *   lens_out          [B]      cache_lens + new_lens
  *   cursor_out        [1]      index of the first page still free
- * (DEVICE int32; lens_out and cursor_out must not be the inputs' memory.)
+ * (DEVICE int32; none of them may overlap an input or block_table.)
  * A request with a negative length, or whose new length exceeds
  * max_pages * page_size, is refused: it gets no pages, its tokens (none if
  * new_lens[b] < 0) get slot -1 and its length stays (ATTN_ERR_SEQLENS).  So

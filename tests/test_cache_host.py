@@ -34,6 +34,30 @@ def test_plan_refusals(lib):
     assert f(lo=A) == 2 and f(co=A) == 2                                          # in place: several blocks read them
 
 
+def test_plan_outputs_that_overlap_its_inputs(lib):
+    """Every block reads the inputs while others write: an output that shares an entry with one is refused, whole or in
+    part; outputs may lie side by side with them."""
+    sizes = dict(lens=4, new=4, tab=32, free=9, cur=1, slots=5, pos=5, cu=5, lo=4, co=1)
+    at, place = 1 << 20, {}
+    for name, n in sizes.items():       # one after another in memory, no gap
+        place[name] = at
+        at += 4 * n
+
+    def f(**kw):
+        x = dict(place, **kw)
+        return lib.attn_cache_plan(*(x[n] for n in sizes), 4, 16, 8, 9, 5, None)
+    # accepted by the checks: without a GPU the call ends at the device (no device, status 7 or 8)
+    import torch as t
+    if not t.cuda.is_available():
+        assert f() not in (0, 1, 2, 3, 4)
+    for out in ("slots", "pos", "cu", "lo", "co"):
+        for inp in ("lens", "new", "tab", "free", "cur"):
+            first, last = place[inp], place[inp] + 4 * (sizes[inp] - 1)
+            assert f(**{out: first}) == 2 and f(**{out: last}) == 2, (out, inp)
+            if sizes[out] > 1:
+                assert f(**{out: first - 4 * (sizes[out] - 1)}) == 2, (out, inp)
+
+
 def test_rope_table_refusals(lib):
     def f(p=A, n=8, r=64, base=1e4, factor=1.0, orig=0, lo=1.0, hi=32.0, m=1.0):
         return lib.attn_rope_table(p, n, r, base, factor, orig, lo, hi, m, None)
