@@ -61,8 +61,9 @@ def attn_cache_plan(cache_lens, new_lens, block_table, page_size: int, free_page
     """Block table, slots and positions of the tokens new_lens [B] adds to requests of cache_lens [B] keys.
 
     Each request gets the pages it lacks from free_pages, from index cursor (int32 [1], None: 0) on; they are written
-    into block_table [B, max_pages] in place.  total_tokens: length of slots and positions (default: that of slots); the
-    entries past the last new token are -1 and 0.  All tensors int32 on the device
+    into block_table [B, max_pages] in place.  total_tokens: length of slots and positions (default: that of slots), which
+    are packed in request order: request b's from entry cu_seqlens[b] on, none without new tokens; the entries past the last
+    new token are -1 and 0.  All tensors int32 on the device
     -> (slots [total_tokens], positions [total_tokens], cu_seqlens [B+1], lens_out [B], cursor_out [1])."""
     return _run(stream, _ext().plan, cache_lens, new_lens, block_table, page_size, free_pages, cursor, total_tokens, slots,
                 positions, cu_seqlens, lens_out, cursor_out)

@@ -350,6 +350,10 @@ GQA_ATTN_API attn_status attn_decode_paged_fp8_fwd(const void* q, const void* k8
  *   lens_out          [B]      cache_lens + new_lens
  *   cursor_out        [1]      index of the first page still free
  * (DEVICE int32; none of them may overlap an input or block_table.)
+ * Tokens are packed: a request with new_lens[b] = 0 has no entry in slots and
+ * positions.  Where k and v keep a row for every request, idle ones too (a
+ * captured step of one token each), row b's slot is entry cu_seqlens[b] if
+ * cu_seqlens[b + 1] > cu_seqlens[b], else -1; its position likewise.
  * A request with a negative length, or whose new length exceeds
  * max_pages * page_size, is refused: it gets no pages, its tokens (none if
  * new_lens[b] < 0) get slot -1 and its length stays (ATTN_ERR_SEQLENS).  So

@@ -200,6 +200,60 @@ def test_a_captured_step_replayed(gq):
             assert (o[2] == 0).all() and (lse[2] == -math.inf).all()
 
 
+@pytest.mark.parametrize("fmt", ["q4", "fp8", "bf16"])
+def test_a_captured_step_with_idle_rows_anywhere(gq, fmt):
+    """k and v one row a request, idle rows among them: the plan packs its tokens, so a row's slot and position are entry
+    cu_seqlens[b], if the request has a token.  The pattern changes between replays of one captured step."""
+    s = SHAPE
+    Hq, Hkv, D, B = s["Hq"], s["Hkv"], s["D"], 5
+    loop = Loop(gq, fmt, B, 18)
+    g = torch.Generator().manual_seed(19)
+    new = torch.zeros(B, dtype=torch.int32, device="cuda")
+    q = torch.zeros(B, Hq, 1, D, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros(B, Hkv, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def step():
+        slots, pos, cu, lens, cursor = gq.attn_cache_plan(loop.lens, new, loop.table, s["page"], loop.free, loop.cursor, B)
+        first = cu[:-1].clamp(max=B - 1).long()
+        slots = torch.where(cu[1:] > cu[:-1], slots[first], -1)
+        loop.append(k, v, slots, *loop.cache, *loop.scales, positions=pos[first], rope_cos_sin=loop.tab)
+        loop.lens.copy_(lens)
+        loop.cursor.copy_(cursor)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    tab, store = loop.tab.cpu(), [[[] for _ in range(B)] for _ in range(2)]
+    patterns = [[1, 1, 1, 1, 1], [0, 1, 1, 0, 1], [1, 0, 0, 1, 0], [0, 0, 0, 0, 0], [1, 0, 1, 0, 1], [0, 1, 0, 1, 1]]
+    for i in range(36):
+        on = patterns[i % 6]
+        ks, vs = (torch.randn(B, Hkv, D, generator=g).bfloat16() for _ in range(2))
+        k.copy_(ks[:, :, None])
+        v.copy_(vs[:, :, None])
+        new.copy_(torch.tensor(on, dtype=torch.int32))
+        graph.replay()
+        for b in range(B):
+            if on[b]:
+                store[0][b].append(R.rope(ks[b], torch.tensor(len(store[0][b])), tab, False, dtype=torch.float32))
+                store[1][b].append(vs[b].float())
+    assert gq.get_device_status() == 0
+    n = [len(x) for x in store[0]]
+    assert loop.lens.tolist() == n and len(set(n)) > 1
+    qs = torch.randn(B, Hq, 1, D, generator=g).bfloat16()
+    o, lse = loop.attend(qs.cuda(), *loop.cache, *loop.scales, loop.table, loop.lens, scale=0.1, rope_cos_sin=loop.tab)
+    assert gq.get_device_status() == 0
+    for b in range(B):
+        K, V = rows(loop, store, b)
+        ref = R.decode(qs[b:b + 1], K[None], V[None], torch.tensor([n[b]]), 0.1, tab)
+        if fmt == "q4":
+            close(o[b:b + 1], lse[b:b + 1], ref)
+        else:
+            assert float((o[b:b + 1].double().cpu() - ref[0]).norm() / ref[0].norm()) <= 5e-3
+            assert float((lse[b:b + 1].double().cpu() - ref[1]).abs().max()) <= 1e-3
+
+
 def test_on_another_stream_with_a_workspace_of_its_own(gq):
     """The same decode call on a side stream, workspace allocated by the call: the memory is that stream's."""
     B, Hq, Hkv, S, D = 2, 8, 2, 3000, 128
