@@ -74,7 +74,8 @@ def attn_rope_table(n: int, rotary_dim: int, base: float = 10000.0, factor: floa
                     stream=None):
     """Rotary table float32 [n, rotary_dim] (cosines, then sines) of positions 0..n-1, frequencies
     base^(-2i/rotary_dim): divided by factor, or with original_positions > 0 only those that make few turns over the
-    original context (all below low_turns, none above high_turns, in between blended); entries times mscale."""
+    original context (all below low_turns, none above high_turns, in between blended linearly over the turns, not over the
+    pair index as some released models' tables are); entries times mscale."""
     on = None                                       # out's
     if out is None:
         if device is None and isinstance(stream, torch.cuda.Stream):

@@ -375,6 +375,10 @@ GQA_ATTN_API attn_status attn_cache_plan(const int* cache_lens, const int* new_l
  *   otherwise by parts: with t_i = original_positions * theta_i / (2 pi) turns
  *   over the original context and g = clamp((t_i - low_turns) /
  *   (high_turns - low_turns), 0, 1), theta_i g + (theta_i / factor) (1 - g).
+ * (The ramp is over turns.  Where a model's table was made with a ramp over the
+ * pair index, between two bounds found from the turns and rounded to whole
+ * pairs, this one differs for the pairs between the bounds: such a model needs
+ * its own table, which every operator here takes.)
  * Cosines and sines are multiplied by mscale.  The angle of a position is
  * taken in fixed point (64 bits of a turn from a frequency in double), so that
  * far positions lose little; sine and cosine of what is left are f32
