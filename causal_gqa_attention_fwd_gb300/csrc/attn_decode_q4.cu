@@ -41,13 +41,16 @@
 // decode_q4_merge.  Few units of short rows go to a cluster of CTAs each
 // instead, whose pieces meet in distributed shared memory (see cluster_of).
 //
-// Bound: long rows by the instructions that turn codes into operands.  A tile
-// of 32 keys and 128 features takes a warp some 600, and per SM sub-partition a
-// conversion (F2FP) or byte operation takes 2 cycles, an f16 multiplication 2,
-// an MMA 8, which overlap only in part: 226.6 MB of cache, queries, outputs and
-// tables take 45 us, 5.0 TB/s, 74% of a copy's rate.  Short rows by latency: 8
-// rows of 2048 keys of 2 heads of 64, 2.4 MB, take 6.4 us in clusters (8.4 as a
-// stream, of which 3 lie between the last warp's end and the merge's).
+// Bound: long rows by the chain of instructions that turns codes into operands,
+// which three warps a scheduler do not hide.  A tile of 32 keys and 128 features
+// takes a warp some 570, and per SM sub-partition a conversion (F2FP) or byte
+// operation takes 2 cycles, an f16 multiplication 2, an MMA 8, which overlap
+// only in part; no unit is full (issue slots 60%, ALU 47%, tensor 27%).  In a
+// captured graph 226.6 MB of cache, queries, outputs and tables take 45 to 46 us,
+// 5.0 TB/s, 74% of a copy's rate; 8 rows of 8192 keys, 8 heads of 128, 22.4 us,
+// twice their floor, of which 7 to 9 are start, tail and merge.  Short rows by
+// latency: 8 rows of 2048 keys of 2 heads of 64, 2.4 MB, take 6.4 us in clusters
+// (8.4 as a stream, of which 3 lie between the last warp's end and the merge's).
 #include <math_constants.h>
 
 #include <atomic>
@@ -1061,7 +1064,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kThreads, 1) decode_q4_kernel(co
 // kMergePieces pieces (their loads in flight together); with more pieces, 2, 4,
 // 8 or 16 groups of warps share them and meet in shared memory, and the tiles
 // go to several blocks: those of the CTAs from the second on that hold a piece
-// (there are more of them than blocks needed).  One row of 8192 keys, 2 K/V
+// (there are more of them than blocks needed).  Beyond 64 pieces, where there
+// are no more groups to take, a warp has up to 10, in two rounds of loads.  One row of 8192 keys, 2 K/V
 // heads of 128: 9.4 us; one block a unit took 4.8 more.
 constexpr int kMergeLog = 4, kMergeWarps = 1 << kMergeLog;
 constexpr int kMergePieces = 4;

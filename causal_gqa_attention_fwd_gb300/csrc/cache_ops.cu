@@ -15,8 +15,8 @@ namespace {
 // ------------------------------------------------------------- cache plan
 // slot = page * page_size + row of each new token, by integer arithmetic: a scan
 // over the requests, then a search per token.  Bound by the launch and a few
-// dependent loads: 64 requests of one token 4.2 us, 512 with 256k tokens in all
-// (2.2 MB) 6.5 us.
+// dependent loads: in a captured graph 64 requests of one token 4.3 us, 512 with
+// 256k tokens in all (2.2 MB) 6.5 us; called from Python 6.0 and 7.7.
 // One launch and no exchange between CTAs: every CTA scans all B requests
 // (pages needed, new tokens) into shared memory, then fills its share of the
 // tokens and of the block-table rows.  Slots come from the free list directly
@@ -310,8 +310,9 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* out, int n, int 
 }
 
 // ------------------------------------------------------------------ append
-// Bound by instructions (4 bits), or by memory: 8 features are one 16-byte load,
-// but some 100 instructions to scale, round and pack.  A thread takes one part of
+// Bound by memory, or for 4 bits by its latency: 8 features are one 16-byte load
+// and some 100 instructions to scale, round and pack, and each head's loads are
+// waited for before them (issue slots 50%, ALU 42%).  A thread takes one part of
 // a token's row, or two paired ones, of k and of v, in HC heads one after
 // another: what depends on the token alone (its place in the cache) is found
 // once.  A part is 8 features, so that neighbouring threads write neighbouring
@@ -320,10 +321,12 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* out, int n, int 
 // fits 64 registers, and the 8 warps a scheduler that this allows hide more
 // latency than the table's row and the next head's loads kept in registers did
 // (105 of them; 4 bits, 16411 tokens of 8 heads of 128, 64 features rotated:
-// 20.4 us against 18.2, 73% of a copy's rate).  All 128 rotated in halves, 16384
-// tokens: bf16 24.1 us (87%; one part a thread 28.5), E4M3 20.4 (79%; 24.4), 4
-// bits 24 (two parts a thread 23 to 26, but 2.9 against 2.5 for 1000 tokens).  64
-// tokens and their gather: 4.0 us, two launches.  All arithmetic is f32, each
+// 20.4 us against 18.2, 71% of a copy's rate).  All 128 rotated in halves, 16384
+// tokens: bf16 23.1 us (88%; one part a thread 28.5), E4M3 19.8 (78%; 24.4), 4
+// bits 24.4 (54%: the paired features and table rows are loaded twice; two parts
+// a thread 23 to 26, but 2.9 against 2.5 for 1000 tokens).  64 tokens and their
+// gather: 4.1 us, two launches; called from Python 9.5.  Times in captured
+// graphs but for the last.  All arithmetic is f32, each
 // element rounded once to the cache's type.
 __device__ __forceinline__ uint32_t e4m3_of(float x) { return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3); }
 
