@@ -1,8 +1,8 @@
 """The operators of a KV cache under pressure, as cases that can be timed and compared.
 
 Three groups: attention of a batch over a prefix that its rows share and over each row's own cache (the prefix read once
-for all of them), the attention weight each cached key has received (accumulated from a step's queries and log-sum-exps),
-and eviction (a cache cut down to a budget of keys by those weights, in place).  ``run`` computes each either with
+for all of them), the attention weight each cached key has received (accumulated from a step's queries and log-sum-exps;
+the step's own keys start at zero), and eviction (a cache cut down to a budget of keys by those weights, in place).  ``run`` computes each either with
 elementary torch operations (``own`` false) or with the calls of causal_gqa_attention_fwd_gb300 (``own`` true); ``exact``
 computes it in 64 bits.
 
@@ -218,10 +218,15 @@ def _plain_weights(st):
     for b in range(st["B"]):
         s, seen = _scores(st, b)
         p = torch.exp(s - st["lse"][b].reshape(st["Hkv"], -1, 1)).masked_fill(~seen, 0.0).sum(-2)
+        # the step's new keys had no weight before
+        n = st["lens"][b]
+        j = torch.arange(st["S"], device=w.device)
+        old = _row(w, bt, b)
+        p = torch.where(j < n - st["Tq"], old + p, torch.where(j < n, p, old))
         if bt is None:
-            w[b] += p
+            w[b] = p
         else:
-            w[bt[b].long()] += p.unflatten(-1, (-1, page)).transpose(0, 1)
+            w[bt[b].long()] = p.unflatten(-1, (-1, page)).transpose(0, 1)
     return w
 
 
@@ -355,11 +360,12 @@ def exact(case, seed):
                 q = st["q"][b, :, t].double().reshape(Hkv, G, D)
                 s = torch.einsum("hgd,khd->khg", q, K[:seen]) * st["scale"] - st["lse"][b, :, t].double().reshape(Hkv, G)
                 add[:seen] += torch.exp(s).sum(-1)
+            add[:max(n - Tq, 0)] += keys(w, b, n)[:max(n - Tq, 0)]       # what was there: of all but the Tq new keys
             if page:
                 p, r = slots(st["bt"][b], n)
-                w[p, :, r] += add
+                w[p, :, r] = add
             else:
-                w[b, :, :n] += add.t()
+                w[b, :, :n] = add.t()
         return w
     budget, recent, first = case["budget"], case["recent"], case["first"]
     import numpy as np
