@@ -22,6 +22,10 @@ PyTorch CUDA tensors (PyTorch supplies device memory and the stream):
     attn_rope_table(n, rotary_dim, base=10000.0, factor=1.0, ...) -> rope_cos_sin, scaled for long contexts
     attn_cache_append / attn_cache_append_fp8 / attn_cache_append_q4: k and v (k rotated, if asked) into cache slots
     attn_cache_gather_q4(slots, k4, k4_sf, v4, v4_sf, k_scale, v_scale) -> (k, v) bf16
+    attn_decode_prefix_fwd(q, k_prefix, v_prefix, prefix_lens, k_cache, v_cache, cache_lens, scale=None) -> (o, lse):
+        cached attention of rows that share prefixes; attn_decode_paged_prefix_fwd: over one pool of pages
+    attn_cache_weights / attn_cache_weights_fp8 / attn_cache_weights_q4: the attention weight cached keys receive, added up
+    attn_cache_evict(weights, caches, cache_lens, budget, recent=0, first=0, ...) -> (kept, lens_out), caches cut in place
 
 All arithmetic runs in the library's hand-written sm_103a kernels; a call
 raises if the library is not built.
@@ -61,9 +65,16 @@ from ._cache import (  # noqa: F401
     attn_cache_append,
     attn_cache_append_fp8,
     attn_cache_append_q4,
+    attn_cache_evict,
     attn_cache_gather_q4,
     attn_cache_plan,
+    attn_cache_weights,
+    attn_cache_weights_fp8,
+    attn_cache_weights_q4,
+    attn_decode_paged_prefix_fwd,
     attn_decode_paged_q4_fwd,
+    attn_decode_prefix_fwd,
+    attn_decode_prefix_workspace_size,
     attn_decode_q4_fwd,
     attn_decode_q4_workspace_size,
     attn_rope,

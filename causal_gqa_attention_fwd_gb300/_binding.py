@@ -66,11 +66,19 @@ SIGNATURES = {
     "attn_decode_q4_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
     "attn_decode_q4_fwd": (_I, [_P] * 5 + [_F] * 2 + [_P] * 4 + [_Z] + [_I] * 6 + [_F, _P, _I, _P]),
     "attn_decode_paged_q4_fwd": (_I, [_P] * 5 + [_F] * 2 + [_P] * 5 + [_Z] + [_I] * 8 + [_F, _P, _I, _P]),
+    "attn_decode_prefix_workspace_size": (_Z, [_I] * 8),
+    "attn_decode_prefix_fwd": (_I, [_P] * 10 + [_Z] + [_I] * 8 + [_F, _P]),
+    "attn_decode_paged_prefix_fwd": (_I, [_P] * 10 + [_Z] + [_I] * 10 + [_F, _P]),
+    "attn_cache_weights": (_I, [_P] * 6 + [_I] * 8 + [_F, _P]),
+    "attn_cache_weights_fp8": (_I, [_P] * 2 + [_F] + [_P] * 4 + [_I] * 8 + [_F, _P]),
+    "attn_cache_weights_q4": (_I, [_P] * 3 + [_F] + [_P] * 4 + [_I] * 8 + [_F, _P]),
+    "attn_cache_evict": (_I, [_P] * 3 + [_I] + [_P] * 2 + [_I] * 3 + [_P] * 2 + [_I] * 5 + [_P]),
     "attn_decode_paged_fp8_fwd": (_I, [_P, _P, _P, _F, _F] + [_P] * 5 + [_Z] + [_I] * 8 + [_F, _P, _I, _P]),
 }
 
 PROFILE_KINDS = {"attn_fwd": 0, "bwd_pre": 1, "bwd_dkdv": 2, "decode": 4, "decode_merge": 5, "bwd_dq": 6,
-                 "cache_plan": 7, "rope": 8, "rope_table": 9, "cache_append": 10, "cache_gather": 11}
+                 "cache_plan": 7, "rope": 8, "rope_table": 9, "cache_append": 10, "cache_gather": 11,
+                 "prefix": 12, "prefix_merge": 13, "cache_weights": 14, "evict_select": 15, "evict_move": 16}
 
 _lib = None
 

@@ -1,6 +1,7 @@
 """The cache operators of include/gqa_attn.h on PyTorch CUDA tensors: the cache
-plan, rotary positions, appending to and gathering from caches, and attention
-over 4-bit caches.
+plan, rotary positions, appending to and gathering from caches, attention over
+4-bit caches and over a shared prefix, attention weights of cached keys, and
+eviction.
 
 All tensors of a call are on one device, which need not be the current one; the
 kernels run on ``stream`` (a torch.cuda.Stream or a handle), or on that device's
@@ -35,7 +36,7 @@ def _ext():
             raise RuntimeError("the _cache_ext module is missing or was built for another PyTorch: build it with "
                                "causal_gqa_attention_fwd_gb300.build.build(). There is no fallback implementation.") from e
         _mod = _cache_ext
-    names = [n for n in _binding.SIGNATURES if n.startswith(("attn_cache_", "attn_rope")) or "_q4_" in n]
+    names = [n for n in _binding.SIGNATURES if n.startswith(("attn_cache_", "attn_rope")) or "_q4_" in n or "_prefix_" in n]
     _mod.bind({n: ctypes.cast(getattr(handle, n), ctypes.c_void_p).value for n in names}, _binding._check,
               getattr(torch._C, "_cuda_getCurrentRawStream", None))
     _bound = handle
@@ -151,3 +152,61 @@ def attn_decode_paged_q4_fwd(q, k4_pages, k4_sf_pages, v4_pages, v4_sf_pages, k_
         raise TypeError("block_table must be a torch.Tensor")
     return _run(stream, _ext().decode, q, k4_pages, k4_sf_pages, v4_pages, v4_sf_pages, k_scale, v_scale, block_table,
                 cache_lens, scale, o, lse, workspace, rope_cos_sin)
+
+
+def attn_decode_prefix_workspace_size(B, Hq, Hkv, Tq, P, Sp, S, D) -> int:
+    return int(_binding.lib().attn_decode_prefix_workspace_size(B, Hq, Hkv, Tq, P, Sp, S, D))
+
+
+def attn_decode_prefix_fwd(q, k_prefix, v_prefix, prefix_lens, k_cache, v_cache, cache_lens, scale=None, o=None, lse=None,
+                           workspace=None, stream=None):
+    """Cached attention of rows that share prefixes, each prefix read once for all of its rows.  q [B,Hq,Tq,D]; k_prefix,
+    v_prefix [P,Hkv,Sp,D] bf16 with prefix_lens int32 [P] keys in them, prefix p for the B/P rows from p*(B/P) on; k_cache,
+    v_cache [B,Hkv,S,D] the rows' own keys, cache_lens int32 [B] of them (the Tq new ones included).  A query sees its
+    whole prefix and then its own keys as in attn_decode_fwd; queries and keys are rotated beforehand, if at all (an own
+    key's position follows the prefix's).  A query at a negative own position (cache_lens[b] < Tq: a batch slot without
+    a request) gives o = 0, lse = -inf -> (o [B,Hq,Tq,D] bf16, lse [B,Hq,Tq] f32)."""
+    if k_prefix is None:
+        raise TypeError("k_prefix must be a torch.Tensor")
+    return _run(stream, _ext().prefix, q, k_prefix, v_prefix, None, prefix_lens, k_cache, v_cache, None, cache_lens, scale, o,
+                lse, workspace)
+
+
+def attn_decode_paged_prefix_fwd(q, k_pages, v_pages, prefix_table, prefix_lens, block_table, cache_lens, scale=None, o=None,
+                                 lse=None, workspace=None, stream=None):
+    """attn_decode_prefix_fwd over one pool of pages [num_pages,Hkv,page_size,D]: the prefixes through prefix_table
+    [P, max_prefix_pages], the rows' own keys through block_table [B, max_pages] (own position 0 is the first row of a
+    row's first page, wherever its prefix ends)."""
+    return _run(stream, _ext().prefix, q, None, None, prefix_table, prefix_lens, k_pages, v_pages, block_table, cache_lens,
+                scale, o, lse, workspace)
+
+
+def attn_cache_weights(q, k_cache, lse, cache_lens, weights, block_table=None, scale=None, stream=None):
+    """Adds to weights, float32 [pages,Hkv,page_size] beside the keys k_cache [pages,Hkv,page_size,D], the attention
+    weight each cached key has from the queries q [B,Hq,Tq,D]: the sum over the query heads of its K/V head and the Tq
+    positions of exp(scale q.k - lse), with the lse [B,Hq,Tq] of the step's attention (-inf: a query that saw nothing) and
+    the mask of attn_decode_fwd.  The entries of a row's last Tq positions, the step's new keys, are set to that sum
+    whatever their slots held before.  block_table None: contiguous caches [B,Hkv,S,D].  Rows must not share pages -> weights"""
+    return _run(stream, _ext().weights, q, (k_cache,), None, lse, cache_lens, weights, block_table, scale)
+
+
+def attn_cache_weights_fp8(q, k8, k_scale: float, lse, cache_lens, weights, block_table=None, scale=None, stream=None):
+    """attn_cache_weights with E4M3 keys (uint8 codes; key = e4m3(k8) * k_scale)."""
+    return _run(stream, _ext().weights, q, (k8,), float(k_scale), lse, cache_lens, weights, block_table, scale)
+
+
+def attn_cache_weights_q4(q, k4, k4_sf, k_scale: float, lse, cache_lens, weights, block_table=None, scale=None, stream=None):
+    """attn_cache_weights with 4-bit keys (codes and block scales as attn_cache_append_q4 writes them)."""
+    return _run(stream, _ext().weights, q, (k4, k4_sf), float(k_scale), lse, cache_lens, weights, block_table, scale)
+
+
+def attn_cache_evict(weights, caches, cache_lens, budget: int, recent: int = 0, first: int = 0, block_table=None, kept=None,
+                     lens_out=None, stream=None):
+    """Cuts each row of more than budget keys down to budget, in place and for each K/V head by itself: the first `first`
+    and the last `recent` positions stay, and of the others those of the largest weights (of equal ones the lower
+    position).  The kept rows of weights [pages,Hkv,page_size] and of every plane in caches ([pages,Hkv,page_size,width],
+    any type: (k, v), (k8, v8), (k4, k4_sf, v4, v4_sf)) move to positions 0..budget-1 in their order; what lies behind
+    stays as it was, and a row of at most budget keys is not touched.  cache_lens int32 [B]; block_table None: contiguous
+    caches.  Rows must not share pages -> (kept int32 [B,Hkv,budget], the positions kept, -1 behind a shorter row's last;
+    lens_out int32 [B])"""
+    return _run(stream, _ext().evict, weights, tuple(caches), cache_lens, budget, recent, first, block_table, kept, lens_out)

@@ -692,6 +692,7 @@ attn_status decode_common(const void* q, const CUtensorMap& tk, const CUtensorMa
   a.max_pages = max_pages;
   a.num_pages = num_pages;
   a.rope_cs = rope_cos_sin;
+  a.min_len = Tq;
   CUtensorMap tq;
   const uint64_t qdims[2] = {(uint64_t)D, (uint64_t)B * Hq * Tq};
   const uint64_t qstrides[1] = {(uint64_t)D * 2};
@@ -840,6 +841,236 @@ attn_status attn_decode_paged_fp8_fwd(const void* q, const void* k8_pages, const
     return ATTN_ERR_CUDA;
   return decode_common(q, tk, tv, cache_lens, o, lse, workspace, workspace_bytes, B, Hq, Hkv, Tq, (int)S, D, scale,
                        block_table, page_size, max_pages, num_pages, rope_cos_sin, true, k_scale, v_scale, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- attention over a shared prefix
+namespace {
+
+// Work layout of the prefix kernel, as the decode plan a pure function of the
+// sizes.  The width of a team divides the row blocks and is the largest that
+// leaves at most 6% of the CTAs without work (of 152: 1, 2, 4, 8, 19, ... row
+// blocks do).
+struct PrefixPlan {
+  int W, R, Rp, nrt, width, outer, slots;
+  long units;
+};
+
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int Tq, int P, int Sp) {
+  PrefixPlan p{};
+  p.W = B / P;
+  p.R = Hq / Hkv * Tq;
+  p.Rp = p.W * p.R;
+  p.nrt = (p.Rp + gqa::kPrefixRows - 1) / gqa::kPrefixRows;
+  constexpr int kCtas = 152;
+  for (int w = 1; w <= p.nrt && w <= kCtas; ++w)
+    if (p.nrt % w == 0 && kCtas / w * w * 100 >= 94 * kCtas) p.width = w;
+  p.outer = p.nrt / p.width;
+  p.units = (long)P * Hkv * p.nrt;
+  // pieces of a unit: its blocks are one of at least Hkv * outer equally long runs of the stream that at most
+  // kDecodeMaxSlots / width teams share
+  const long blocks = ((long)Sp + 127) / 128, runs = (long)Hkv * p.outer, teams = gqa::kDecodeMaxSlots / p.width;
+  long pieces = (teams + runs - 1) / runs + 1;
+  if (pieces > blocks) pieces = blocks;
+  const bool split = (p.Rp - 1) % gqa::kPrefixRows < 128;      // the last row block is held by both tiles
+  p.slots = (int)(split ? 2 * pieces : pieces);
+  return p;
+}
+
+struct PrefixWs {
+  size_t o, ml, counts, dec_o, dec_ml, dec_counts, bytes;
+};
+
+PrefixWs prefix_ws(const PrefixPlan& p, const DecodePlan& d, int P, int Hkv, int D) {
+  const size_t rows = (size_t)P * Hkv * p.Rp * p.slots, own = (size_t)d.units * d.slots * d.rows_ws;
+  PrefixWs w{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round_up(bytes, 256);
+    return here;
+  };
+  w.o = take(rows * D * 4);
+  w.ml = take(rows * 8);
+  w.counts = take((size_t)p.units * 4);
+  w.dec_o = take(own * D * 4);
+  w.dec_ml = take(own * 8);
+  w.dec_counts = take((size_t)d.units * 4);
+  w.bytes = at;
+  return w;
+}
+
+attn_status prefix_check(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, int D) {
+  if (P < 1 || Sp < 0) return ATTN_ERR_SHAPE;
+  const attn_status st = decode_check(B, Hq, Hkv, Tq, S, D);
+  if (st != ATTN_OK) return st;
+  if (B % P) return ATTN_ERR_SHAPE;
+  if (B == 0 || Tq == 0) return ATTN_OK;
+  const PrefixPlan p = prefix_plan(B, Hq, Hkv, Tq, P, Sp);
+  // block stream and ring indices
+  if (p.units * ((Sp + 127L) / 128) > 0x3fffffffL || (long)P * Hkv > 0x7fffffffL) return ATTN_ERR_SHAPE;
+  return ATTN_OK;
+}
+
+// Everything after the layout-specific checks.
+attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMap& pv, const int* prefix_lens,
+                          const int* prefix_table, int max_prefix_pages, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const int* cache_lens, const int* block_table, int max_pages, int page_size, int num_pages,
+                          void* o, float* lse, void* workspace, int B, int Hq, int Hkv, int Tq, int P, int Sp, int S,
+                          int D, float scale, void* stream) {
+  attn_status st = check_arch();
+  if (st != ATTN_OK) return st;
+  int* status = status_word();
+  const int sms = sm_count();
+  if (!status || sms < 1) return ATTN_ERR_CUDA;
+  const PrefixPlan p = prefix_plan(B, Hq, Hkv, Tq, P, Sp);
+  const DecodePlan d = decode_plan(B, Hq, Hkv, Tq, S);
+  const PrefixWs w = prefix_ws(p, d, P, Hkv, D);
+  char* ws = static_cast<char*>(workspace);
+  const int ctas = sms < gqa::kDecodeMaxSlots ? sms : gqa::kDecodeMaxSlots;   // one a SM, as decode
+  gqa::PrefixArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.prefix_lens = prefix_lens;
+  a.table = prefix_table;
+  a.ws_o = reinterpret_cast<float*>(ws + w.o);
+  a.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.counts = reinterpret_cast<int*>(ws + w.counts);
+  a.status = status;
+  a.dbg_line = gqa::api_check_line();
+  a.P = P;
+  a.W = p.W;
+  a.Hkv = Hkv;
+  a.R = p.R;
+  a.Rp = p.Rp;
+  a.nrt = p.nrt;
+  // a device of fewer SMs than a team has CTAs: teams of one
+  a.width = p.width <= ctas ? p.width : 1;
+  a.outer = p.nrt / a.width;
+  const long blocks = (long)P * Hkv * a.outer * ((Sp + 127L) / 128);
+  a.teams = ctas / a.width;
+  if (a.teams > blocks) a.teams = blocks > 0 ? (int)blocks : 1;
+  a.Sp = Sp;
+  a.slots = p.slots;
+  a.page_size = page_size;
+  a.max_pages = max_prefix_pages;
+  a.num_pages = num_pages;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  gqa::DecodeArgs e{};
+  e.q = a.q;
+  e.cache_lens = cache_lens;
+  e.o = static_cast<__nv_bfloat16*>(o);
+  e.lse = lse;
+  e.ws_o = reinterpret_cast<float*>(ws + w.dec_o);
+  e.ws_ml = reinterpret_cast<float2*>(ws + w.dec_ml);
+  e.counts = reinterpret_cast<int*>(ws + w.dec_counts);
+  e.status = status;
+  e.B = B;
+  e.Hq = Hq;
+  e.Hkv = Hkv;
+  e.G = Hq / Hkv;
+  e.Tq = Tq;
+  e.S = S;
+  e.D = D;
+  e.R = d.R;
+  e.nrb = d.nrb;
+  e.slots = d.slots;
+  e.rows_ws = d.rows_ws;
+  e.ctas = ctas;
+  e.scale_log2 = a.scale_log2;
+  e.v_scale = 1.f;
+  e.block_table = block_table;
+  e.page_size = page_size;
+  e.max_pages = max_pages;
+  e.num_pages = num_pages;
+  CUtensorMap tq;
+  const uint64_t qdims[2] = {(uint64_t)D, (uint64_t)B * Hq * Tq};
+  const uint64_t qstrides[1] = {(uint64_t)D * 2};
+  const uint32_t qbox[2] = {64, (uint32_t)kDecodeRows};
+  if (!gqa::make_tmap(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, qdims, qstrides, qbox, CU_TENSOR_MAP_SWIZZLE_128B))
+    return ATTN_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err = gqa::launch_attn_prefix(pk, pv, a, D, s);
+  if (err == cudaSuccess) err = gqa::launch_attn_decode_parts(tk, tv, tq, e, ctas, s);
+  if (err == cudaSuccess) err = gqa::launch_prefix_merge(a, e, s);
+  return launch_status(err);
+}
+
+attn_status prefix_check_pointers(const void* q, const void* k, const void* v, const int* prefix_lens,
+                                  const int* cache_lens, const void* o, const float* lse, const void* workspace,
+                                  size_t workspace_bytes, int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, int D) {
+  if (!q || !k || !v || !prefix_lens || !cache_lens || !o || !lse) return ATTN_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
+      (reinterpret_cast<uintptr_t>(prefix_lens) & 3u) || (reinterpret_cast<uintptr_t>(cache_lens) & 3u))
+    return ATTN_ERR_ALIGN;
+  const size_t need =
+      prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), decode_plan(B, Hq, Hkv, Tq, S), P, Hkv, D).bytes;
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return ATTN_ERR_WORKSPACE;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_decode_prefix_workspace_size(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, int D) {
+  if (prefix_check(B, Hq, Hkv, Tq, P, Sp, S, D) != ATTN_OK || B == 0 || Tq == 0) return 0;
+  return prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), decode_plan(B, Hq, Hkv, Tq, S), P, Hkv, D).bytes;
+}
+
+attn_status attn_decode_prefix_fwd(const void* q, const void* k_prefix, const void* v_prefix, const int* prefix_lens,
+                                   const void* k_cache, const void* v_cache, const int* cache_lens, void* o, float* lse,
+                                   void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Tq, int P,
+                                   int Sp, int S, int D, float scale, void* stream) {
+  attn_status st = prefix_check(B, Hq, Hkv, Tq, P, Sp, S, D);
+  if (st != ATTN_OK) return st;
+  if (B == 0 || Tq == 0) return ATTN_OK;
+  if (!isfinite(scale * 1.4426950408889634f)) return ATTN_ERR_SHAPE;
+  st = prefix_check_pointers(q, k_cache, v_cache, prefix_lens, cache_lens, o, lse, workspace, workspace_bytes, B, Hq, Hkv,
+                             Tq, P, Sp, S, D);
+  if (st != ATTN_OK) return st;
+  if (Sp > 0 && (!k_prefix || !v_prefix)) return ATTN_ERR_NULL;
+  if (!aligned16(k_prefix) || !aligned16(v_prefix)) return ATTN_ERR_ALIGN;
+  CUtensorMap tk, tv, pk, pv;
+  if (!map_dense(&tk, k_cache, D, S, (long)B * Hkv) || !map_dense(&tv, v_cache, D, S, (long)B * Hkv)) return ATTN_ERR_CUDA;
+  pk = tk;   // Sp = 0: no length is valid but 0, and nothing is loaded through them
+  pv = tv;
+  if (Sp > 0 && (!map_dense(&pk, k_prefix, D, Sp, (long)P * Hkv) || !map_dense(&pv, v_prefix, D, Sp, (long)P * Hkv)))
+    return ATTN_ERR_CUDA;
+  return prefix_common(q, pk, pv, prefix_lens, nullptr, 0, tk, tv, cache_lens, nullptr, 0, 0, 0, o, lse, workspace, B, Hq,
+                       Hkv, Tq, P, Sp, S, D, scale, stream);
+}
+
+attn_status attn_decode_paged_prefix_fwd(const void* q, const void* k_pages, const void* v_pages,
+                                         const int* prefix_table, const int* prefix_lens, const int* block_table,
+                                         const int* cache_lens, void* o, float* lse, void* workspace,
+                                         size_t workspace_bytes, int B, int Hq, int Hkv, int Tq, int P, int page_size,
+                                         int num_pages, int max_prefix_pages, int max_pages, int D, float scale,
+                                         void* stream) {
+  if (page_size < 0 || num_pages < 0 || max_pages < 0 || max_prefix_pages < 0) return ATTN_ERR_SHAPE;
+  const long S = (long)page_size * max_pages, Sp = (long)page_size * max_prefix_pages;
+  if (S > 0x7fffffffL || Sp > 0x7fffffffL) return ATTN_ERR_SHAPE;
+  attn_status st = prefix_check(B, Hq, Hkv, Tq, P, (int)Sp, (int)S, D);
+  if (st != ATTN_OK) return st;
+  if (B == 0 || Tq == 0) return ATTN_OK;
+  if (!decode_page_size_ok(page_size) || num_pages < 1 || (long)num_pages * Hkv > 0x7fffffffL ||
+      (long)B * max_pages > 0x7fffffffL || (long)P * max_prefix_pages > 0x7fffffffL ||
+      !isfinite(scale * 1.4426950408889634f))
+    return ATTN_ERR_SHAPE;
+  st = prefix_check_pointers(q, k_pages, v_pages, prefix_lens, cache_lens, o, lse, workspace, workspace_bytes, B, Hq, Hkv,
+                             Tq, P, (int)Sp, (int)S, D);
+  if (st != ATTN_OK) return st;
+  if (!block_table || (Sp > 0 && !prefix_table)) return ATTN_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(prefix_table) & 3u))
+    return ATTN_ERR_ALIGN;
+  const int box = page_size < 128 ? page_size : 128;
+  CUtensorMap tk, tv;
+  if (!map_dense(&tk, k_pages, D, page_size, (long)num_pages * Hkv, box) ||
+      !map_dense(&tv, v_pages, D, page_size, (long)num_pages * Hkv, box))
+    return ATTN_ERR_CUDA;
+  return prefix_common(q, tk, tv, prefix_lens, Sp > 0 ? prefix_table : block_table, max_prefix_pages, tk, tv, cache_lens,
+                       block_table, max_pages, page_size, num_pages, o, lse, workspace, B, Hq, Hkv, Tq, P, (int)Sp,
+                       (int)S, D, scale, stream);
 }
 
 // ------------------------------------------------- allocation-free backward

@@ -1,0 +1,690 @@
+// attn_prefix.cu -- cached attention of a batch whose rows share a prefix, for
+// sm_103a: the prefix's keys and values are read once for all of its rows.
+//
+// Row b of prefix p holds the prefix's m_p keys and n_b keys of its own; with
+// S_j = scale q k_j the softmax over both is the two softmaxes joined,
+//   M = max(M_p, M_o),  L = L_p 2^(M_p - M) + L_o 2^(M_o - M),
+//   O = (O_p 2^(M_p - M) + O_o 2^(M_o - M)) / L,   LSE = ln 2 (M + log2 L),
+// so the two parts run apart: attn_prefix leaves unnormalised partials
+// (O, M, L) of the prefix, the decode kernel (attn_decode.cu) those of the
+// rows' own caches, and prefix_merge joins them.
+//
+// attn_prefix  The W * G * Tq query rows that meet a (prefix, K/V head) are a
+//   matrix, and both products are GEMM-shaped: tiles of 128 query rows as M,
+//   128 keys as N of the score MMA, on tcgen05 with the accumulators in TMEM
+//   (S_A, S_B, O_A, O_B; P in bf16 over its S), as the prefill kernel has
+//   them.  One CTA holds two tiles.  A unit of more than 128 rows fills both
+//   and each reads every key block; one of at most 128 rows is held by both
+//   tiles, which then take the key blocks in turn, so that one's exponentials
+//   run beside the other's MMAs (two partials a piece).
+//   Persistent CTAs in teams (kernels.h, PrefixArgs) share the key blocks
+//   evenly; a piece is a run of one unit's blocks.
+//   Roles (384 threads): warp 0 TMA producer (K and V blocks, one box a page
+//   where a page is shorter than a block), warp 1 MMA issuer, warps 4-7 and
+//   8-11 softmax of a tile each, thread = row; they also gather the query rows
+//   (a tile's rows lie in runs of G * Tq in memory) and write the partials.
+#include "kernels.h"
+#include "sm103.cuh"
+
+namespace gqa {
+
+namespace {
+
+constexpr int kBM = 128;                   // query rows per tile
+constexpr int kBN = 128;                   // keys per block
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: lazy O rescale
+constexpr int kDevPages = 11;              // ATTN_ERR_PAGES
+
+template <int D>
+struct PreCfg {
+  static constexpr int kTileBytes = kBM * D * 2;
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kBoxBytes = kBM * 128;
+  static constexpr int kStages = D == 128 ? 5 : 10;    // K and V blocks in flight: what shared memory holds
+  static constexpr int kSmemBytes = 2 * kTileBytes + kStages * kTileBytes + 1024;
+  static constexpr uint32_t kIdescQK = idesc_bf16(kBM, kBN, false, false);
+  static constexpr uint32_t kIdescPV = idesc_bf16(kBM, D, false, true);
+  __device__ static constexpr uint32_t col_s(int x) { return (uint32_t)x * 128u; }
+  __device__ static constexpr uint32_t col_o(int x) { return 256u + (uint32_t)x * 128u; }
+  static_assert(kSmemBytes + 1024 <= 232448, "shared memory");
+};
+
+struct __align__(8) PreBarriers {
+  uint64_t q_full[2];
+  uint64_t kv_full[10], kv_empty[10];
+  uint64_t s_full[2];
+  uint64_t p_half[2], p_full[2];   // keys 0-63 of P are in TMEM; all of them
+  uint64_t o_done[2];
+  uint64_t teardown;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ int prefix_blocks(const PrefixArgs& a, int p) {
+  const int m = a.prefix_lens[p];
+  return m > 0 && m <= a.Sp ? (m + kBN - 1) / kBN : 0;
+}
+
+// A piece: blocks [kb, kb + n) of unit (p, hkv, mt).
+struct Piece {
+  int p, hkv, mt;
+  int kb, n;
+  int len;             // keys of the prefix
+  int rows;            // query rows of the unit
+  int split;           // the two tiles take the blocks in turn
+  int slot, npieces;   // in pieces
+};
+
+// Where a CTA's walk over its share stands.  Every role walks it.
+struct Walk {
+  Piece it;
+  long g, g1;          // stream index of the piece's first block; end of the share
+  long C;
+  int T;               // teams with a share
+  int p, nb;           // prefix of the piece, its blocks
+  long Pb;             // stream index of prefix p's first block
+  int inner;
+  bool valid;
+};
+
+__device__ __forceinline__ int team_of(long g, long C, int T) { return (int)(((g + 1) * T - 1) / C); }
+
+__device__ __forceinline__ void walk_piece(const PrefixArgs& a, Walk& w) {
+  const long off = w.g - w.Pb;
+  const int group = (int)(off / w.nb), kb = (int)(off % w.nb);   // (hkv, outer), block
+  Piece& it = w.it;
+  it.p = w.p;
+  it.hkv = group / a.outer;
+  it.mt = group % a.outer * a.width + w.inner;
+  it.kb = kb;
+  it.n = (int)min((long)(w.nb - kb), w.g1 - w.g);
+  it.len = a.prefix_lens[w.p];
+  it.rows = min(kPrefixRows, a.Rp - it.mt * kPrefixRows);
+  it.split = it.rows <= kBM;
+  const long Pg = w.Pb + (long)group * w.nb;
+  const int first = team_of(Pg, w.C, w.T);
+  it.slot = (int)(blockIdx.x / a.width) - first;
+  it.npieces = team_of(Pg + w.nb - 1, w.C, w.T) - first + 1;
+  w.valid = true;
+}
+
+__device__ __forceinline__ void walk_next(const PrefixArgs& a, Walk& w) {
+  w.g += w.it.n;
+  if (w.g >= w.g1) {
+    w.valid = false;
+    return;
+  }
+  const long gpp = (long)a.Hkv * a.outer;
+  while (w.g >= w.Pb + gpp * w.nb) {
+    w.Pb += gpp * w.nb;
+    ++w.p;
+    w.nb = prefix_blocks(a, w.p);
+  }
+  walk_piece(a, w);
+}
+
+// The walk of this CTA's team from its start (one warp).
+__device__ Walk walk_begin(const PrefixArgs& a) {
+  const int lane = threadIdx.x & 31;
+  const long gpp = (long)a.Hkv * a.outer;
+  long C = 0;
+  bool bad = false;
+  for (int p0 = 0; p0 < a.P; p0 += 32) {
+    int n = 0;
+    if (p0 + lane < a.P) {
+      const int m = a.prefix_lens[p0 + lane];
+      bad |= m < 0 || m > a.Sp;
+      n = prefix_blocks(a, p0 + lane);
+    }
+    C += gpp * (long)__reduce_add_sync(0xffffffffu, (unsigned)n);
+  }
+  if (__any_sync(0xffffffffu, bad) && blockIdx.x == 0 && lane == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+  Walk w{};
+  w.C = C;
+  w.T = (int)min((long)a.teams, C);
+  const int team = blockIdx.x / a.width;
+  w.inner = blockIdx.x % a.width;
+  w.valid = false;
+  if (team >= w.T) return w;
+  w.g = (long)team * C / w.T;
+  w.g1 = (long)(team + 1) * C / w.T;
+  long P = 0;
+  for (int p0 = 0; p0 < a.P; p0 += 32) {
+    int n = 0;
+    if (p0 + lane < a.P) n = prefix_blocks(a, p0 + lane);
+    long incl = gpp * n;   // inclusive prefix sum over the 32 prefixes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, P + incl > w.g);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      w.p = p0 + l;
+      w.nb = __shfl_sync(0xffffffffu, n, l);
+      w.Pb = P + __shfl_sync(0xffffffffu, incl - gpp * n, l);
+      break;
+    }
+    P += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  walk_piece(a, w);
+  return w;
+}
+
+}  // namespace
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(384, 1)
+    attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const PrefixArgs a) {
+  using C = PreCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;                          // 2 tiles
+  uint8_t* sRing = smem + 2 * C::kTileBytes;   // kStages tiles: K_0, V_0, K_1, ...
+  __shared__ PreBarriers bars;
+  __shared__ Walk s_walk;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Guard guard{&bars.abort, a.status};
+
+  if (threadIdx.x == 0) {
+    bars.abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.q_full[i], 4);     // one arrive per softmax warp
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_half[i], 4);
+      mbar_init(&bars.p_full[i], 4);
+      mbar_init(&bars.o_done[i], 1);
+    }
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&bars.kv_full[s], 1);
+      mbar_init(&bars.kv_empty[s], 1);
+    }
+    mbar_init(&bars.teardown, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars.tmem_base, 512);
+    tmem_relinquish();
+  }
+  griddep_wait();     // the inputs may come from the previous grid
+  if (warp == 0) {
+    const Walk w0 = walk_begin(a);
+    if (lane == 0) s_walk = w0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  griddep_launch();   // every CTA is past its wait: the decode kernel may read what the grids before wrote
+
+  if (warp == 0) {
+    // ======================================================== TMA producer
+    regs_dec<64>();
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    int stage = 0, fill = 0;
+    int last_fill[C::kStages];
+#pragma unroll
+    for (int i = 0; i < C::kStages; ++i) last_fill[i] = -1;
+    bool ok = true;
+    for (Walk w = s_walk; w.valid && ok; walk_next(a, w)) {
+      for (int j = 0; j < w.it.n && ok; ++j) {
+        const int k0 = (w.it.kb + j) * kBN;
+        // Paged: lane i looks up the block's i-th page; pages without a key of the prefix and invalid entries
+        // (reported) get a coordinate past the tensor, which the TMA fills with zeros.
+        int pg = -1, npc = 1;
+        if constexpr (PAGED) {
+          const int psz = a.page_size;
+          npc = psz >= kBN ? 1 : kBN / psz;
+          const int idx = k0 / psz + lane;
+          bool bad = false;
+          if (lane < npc && idx < (w.it.len + psz - 1) / psz) {
+            const int e = a.table[(long)w.it.p * a.max_pages + idx];
+            if (e >= 0 && e < a.num_pages) pg = e;
+            else bad = true;
+          }
+          if (__any_sync(0xffffffffu, bad) && lane == 0) atomicCAS(a.status, 0, kDevPages);
+        }
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          if (fill >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars.kv_empty[stage], (fill - 1) & 1, guard));
+          if (!ok) break;
+          uint8_t* dst = sRing + stage * C::kTileBytes;
+          uint64_t* bar = &bars.kv_full[stage];
+          const CUtensorMap* tm = kv == 0 ? &tm_k : &tm_v;
+          if (lane == 0) mbar_expect_tx(bar, C::kTileBytes);
+          __syncwarp();
+          if constexpr (PAGED) {
+            const int psz = a.page_size;
+            const int row = psz >= kBN ? k0 % psz : 0;
+            // lane i loads the i-th page's boxes
+            if (lane < npc) {
+              const int z = pg >= 0 ? pg * a.Hkv + w.it.hkv : a.num_pages * a.Hkv;
+#pragma unroll
+              for (int x = 0; x < C::kBoxes; ++x)
+                tma_load_3d(dst + x * C::kBoxBytes + lane * psz * 128, tm, bar, x * 64, row, z);
+            }
+          } else if (lane == 0) {
+#pragma unroll
+            for (int x = 0; x < C::kBoxes; ++x)
+              tma_load_3d(dst + x * C::kBoxBytes, tm, bar, x * 64, k0, w.it.p * a.Hkv + w.it.hkv);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < C::kStages; ++i)
+            if (i == stage) last_fill[i] = fill;
+          if (++stage == C::kStages) {
+            stage = 0;
+            ++fill;
+          }
+        }
+      }
+    }
+    // never leave the CTA with copies in flight
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < C::kStages; ++i)
+        if (last_fill[i] >= 0) mbar_wait_drain(&bars.kv_full[i], (uint32_t)last_fill[i] & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ============================================ MMA issuer (whole warp, one lane issues)
+    regs_dec<64>();
+    const uint32_t sq_addr = smem_u32(sQ), ring_addr = smem_u32(sRing);
+    auto stage_of = [&](int idx) { return idx % C::kStages; };
+    auto wait_kv = [&](int idx) {
+      return (bool)__all_sync(0xffffffffu, mbar_wait(&bars.kv_full[stage_of(idx)], (idx / C::kStages) & 1, guard));
+    };
+    auto issue_qk = [&](int x, int st) {
+      const uint32_t qa = sq_addr + x * C::kTileBytes, ka = ring_addr + st * C::kTileBytes;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kBoxBytes + (kk & 3) * 32;
+          mma_ss(tmem + C::col_s(x), sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), C::kIdescQK,
+                 kk > 0);
+        }
+      }
+      __syncwarp();
+    };
+    // P V over the keys [16 kk0, 16 kk1) of the block (P packed in TMEM over S)
+    auto issue_pv = [&](int x, int st, bool acc, int kk0, int kk1) {
+      const uint32_t va = ring_addr + st * C::kTileBytes;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = kk0; kk < kk1; ++kk)
+          mma_ts(tmem + C::col_o(x), tmem + C::col_s(x) + kk * 8, sdesc_sw128(va + kk * 2048, C::kBoxBytes, 1024),
+                 C::kIdescPV, (acc || kk > 0) ? 1u : 0u);
+      }
+      __syncwarp();
+    };
+    bool ok = true;
+    uint32_t pc[2] = {0, 0};   // P blocks taken from each tile
+    int base = 0, uses = 0;    // ring index of the piece's K_0 (V_j follows K_j); pieces before
+    for (Walk w = s_walk; w.valid && ok; walk_next(a, w), ++uses) {
+      const int n = w.it.n;
+      const bool split = w.it.split;
+      for (int x = 0; x < 2 && ok; ++x) ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full[x], uses & 1, guard));
+      if (!ok) break;
+      // P of tile x for block j, in two halves, so that the first half's P V runs while the softmax forms the second
+      auto pv = [&](int x, int vst, bool acc) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_half[x], pc[x] & 1, guard));
+        if (!ok) return;
+        tc_fence_after();
+        issue_pv(x, vst, acc, 0, kBN / 32);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_full[x], pc[x] & 1, guard));
+        if (!ok) return;
+        tc_fence_after();
+        issue_pv(x, vst, true, kBN / 32, kBN / 16);
+        ++pc[x];
+      };
+      if (split) {
+        // block j belongs to tile j & 1
+        for (int j = 0; j < 2 && j < n && ok; ++j) {
+          ok = wait_kv(base + 2 * j);
+          if (!ok) break;
+          tc_fence_after();
+          issue_qk(j, stage_of(base + 2 * j));
+          tc_commit_warp(&bars.s_full[j]);
+          tc_commit_warp(&bars.kv_empty[stage_of(base + 2 * j)]);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          const int x = j & 1, vi = base + 2 * j + 1, ki = base + 2 * j + 4;
+          ok = wait_kv(vi);
+          if (!ok) break;
+          pv(x, stage_of(vi), j >= 2);
+          if (!ok) break;
+          tc_commit_warp(&bars.kv_empty[stage_of(vi)]);
+          if (j + 2 < n) {
+            ok = wait_kv(ki);
+            if (!ok) break;
+            tc_fence_after();
+            issue_qk(x, stage_of(ki));
+            tc_commit_warp(&bars.s_full[x]);
+            tc_commit_warp(&bars.kv_empty[stage_of(ki)]);
+          } else {
+            tc_commit_warp(&bars.o_done[x]);
+          }
+        }
+        if (ok && n == 1) tc_commit_warp(&bars.o_done[1]);   // a tile without blocks is not a piece ahead either
+      } else {
+        ok = wait_kv(base);
+        if (!ok) break;
+        tc_fence_after();
+        for (int x = 0; x < 2; ++x) {
+          issue_qk(x, stage_of(base));
+          tc_commit_warp(&bars.s_full[x]);
+        }
+        tc_commit_warp(&bars.kv_empty[stage_of(base)]);
+        for (int j = 0; j < n && ok; ++j) {
+          const int vi = base + 2 * j + 1, ki = vi + 1;
+          ok = wait_kv(vi);
+          if (ok && j + 1 < n) ok = wait_kv(ki);
+          if (!ok) break;
+          tc_fence_after();
+          for (int x = 0; x < 2 && ok; ++x) {
+            pv(x, stage_of(vi), j > 0);
+            if (!ok) break;
+            if (j + 1 < n) {
+              issue_qk(x, stage_of(ki));
+              tc_commit_warp(&bars.s_full[x]);
+            } else {
+              tc_commit_warp(&bars.o_done[x]);
+            }
+          }
+          if (!ok) break;
+          tc_commit_warp(&bars.kv_empty[stage_of(vi)]);
+          if (j + 1 < n) tc_commit_warp(&bars.kv_empty[stage_of(ki)]);
+        }
+      }
+      base += 2 * n;
+    }
+    // every issued MMA finishes before TMEM and shared memory are released
+    tc_commit_warp(&bars.teardown);
+    mbar_wait_drain(&bars.teardown, 0);
+  } else if (warp < 4) {
+    regs_dec<64>();                         // idle: registers go to the softmax warpgroups
+  } else {
+    // ============================================================ softmax
+    // Register split (launched 384 x 168 = 64512): 128 * 64 + 256 * 216 = 63488.
+    regs_inc<216>();
+    const int x = (warp - 4) >> 2;          // tile
+    const int r = threadIdx.x & 127;        // row within the tile
+    const int wrow = (warp & 3) * 32;       // first row of the warp
+    const uint32_t lane_base = (uint32_t)wrow << 16;
+    const uint32_t tS = tmem + lane_base + C::col_s(x);
+    const uint32_t tO = tmem + lane_base + C::col_o(x);
+    const float c = a.scale_log2;
+    uint32_t sc = 0, od = 0;                // S blocks and outputs taken so far
+    int base = 0;
+    bool ok = true;
+    for (Walk w = s_walk; w.valid && ok; walk_next(a, w)) {
+      const Piece& it = w.it;
+      const int row0 = it.mt * kPrefixRows + (it.split ? 0 : x * kBM);   // first row of the tile within the unit's head
+      const int rows = min(kBM, it.rows - (it.split ? 0 : x * kBM));
+      const int nx = it.split ? (it.n + 1 - x) / 2 : it.n;               // blocks of this tile
+      // ------------------------------------------------ the tile's query rows
+      // (shared memory is free: the previous piece's MMAs were done before its output was read)
+      {
+        constexpr int kC = D / 8;                 // 16-byte parts of a row
+        constexpr int kPer = 32 / kC;             // rows a warp takes at once
+        const int part = lane % kC;
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kPer) {
+          const int rr = wrow + i + lane / kC;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (rr < rows) {
+            const int gr = row0 + rr, b = it.p * a.W + gr / a.R;
+            const long qr = ((long)b * a.Hkv + it.hkv) * a.R + gr % a.R;
+            v = *reinterpret_cast<const uint4*>(a.q + qr * D + part * 8);
+          }
+          *reinterpret_cast<uint4*>(sQ + x * C::kTileBytes + (part >> 3) * C::kBoxBytes + rr * 128 +
+                                    (((part & 7) ^ (rr & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive_warp(&bars.q_full[x]);
+      }
+      const bool live = wrow < rows;        // a warp without rows only answers the barriers
+      float m_run = -INFINITY;              // running max, log2 units (scale folded in)
+      float l_run = 0.f;
+      for (int i = 0; i < nx; ++i, ++sc) {
+        const int j = it.split ? 2 * i + x : i;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[x], sc & 1, guard));
+        if (!ok) break;
+        tc_fence_after();
+        const int nvis = it.len - (it.kb + j) * kBN;    // visible keys of the block
+        if (nvis < kBN) {
+          // V rows past the prefix may hold anything: zeros, so that 0 * V stays 0 in the MMA
+          const int vi = base + 2 * j + 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.kv_full[vi % C::kStages], (vi / C::kStages) & 1, guard));
+          if (!ok) break;
+          if (r >= nvis) {
+            uint8_t* vs = sRing + (vi % C::kStages) * C::kTileBytes + r * 128;
+#pragma unroll
+            for (int b = 0; b < C::kBoxes; ++b)
+#pragma unroll
+              for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(vs + b * C::kBoxBytes + q * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();         // P V waits for all four warps' P
+        }
+        if (!live) {
+          tc_fence_before();
+          mbar_arrive_warp(&bars.p_half[x]);
+          mbar_arrive_warp(&bars.p_full[x]);
+          continue;
+        }
+        uint32_t s[kBN];
+#pragma unroll
+        for (int q = 0; q < kBN / 32; ++q) tmem_ld_x32(tS + q * 32, s + q * 32);
+        tmem_ld_wait();
+        reg_fence<kBN>(s);
+        float* sf = reinterpret_cast<float*>(s);
+        if (nvis < kBN) {
+#pragma unroll
+          for (int k = 0; k < kBN; ++k)
+            if (k >= nvis) sf[k] = -INFINITY;
+        }
+        float m8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m8[e] = fmaxf(sf[e], sf[e + 8]);
+#pragma unroll
+        for (int k = 16; k < kBN; k += 16)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m8[e] = max3f(m8[e], sf[k + e], sf[k + 8 + e]);
+        const float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        const float mn = mx * c;
+        float alpha = 1.f;
+        bool resc = false;
+        if (i == 0) {
+          m_run = mn;
+        } else if (mn > m_run + kRescaleThreshold) {
+          alpha = ex2_approx(m_run - mn);
+          m_run = mn;
+          resc = true;
+        }
+        const float m_use = m_run == -INFINITY ? 0.f : m_run;
+        // O is rescaled first (the commit of S covered the P V before), then P goes out in two halves
+        if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld_x32(tO + q * 32, o);
+            tmem_ld_wait();
+            reg_fence<32>(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st_x32(tO + q * 32, o);
+          }
+        }
+        const uint64_t c2 = f2(c, c), nm2 = f2(-m_use, -m_use);
+        uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < kBN / 32; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float t0, t1;
+            f2_split(fma2(f2(sf[q * 32 + 2 * k], sf[q * 32 + 2 * k + 1]), c2, nm2), t0, t1);
+            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+            acc[k & 3] = add2(acc[k & 3], f2(p0, p1));
+            pk[k] = pack_bf16x2(p0, p1);   // P rounded to bf16 (2^-9 of each weight), as the prefill's: the MMA's type
+          }
+          tmem_st_x16(tS + q * 16, pk);
+          if (q == kBN / 64 - 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive_warp(&bars.p_half[x]);
+          }
+        }
+        float rs0, rs1;
+        f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), rs0, rs1);
+        l_run = l_run * alpha + (rs0 + rs1);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&bars.p_full[x]);
+      }
+      if (!ok) break;
+      base += 2 * it.n;
+      // ------------------------------------------------------- the partial
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_done[x], od & 1, guard));
+      if (!ok) break;
+      ++od;
+      tc_fence_after();
+      const int slot = it.split ? 2 * it.slot + x : it.slot;
+      const long wr = (((long)it.p * a.Hkv + it.hkv) * a.Rp + row0 + r) * a.slots + slot;
+      const bool mine = r < rows && GQA_CHECK(slot >= 0 && slot < a.slots && row0 + r < a.Rp, a.status, a.dbg_line);
+      if (nx > 0 && live) {
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld_x32(tO + q * 32, o);
+          tmem_ld_wait();
+          reg_fence<32>(o);
+          if (mine) {
+            uint4* dst = reinterpret_cast<uint4*>(a.ws_o + wr * D + q * 32);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        }
+        tc_fence_before();   // O is read before the next piece's P V (after its q_full) writes it
+      }
+      if (mine) a.ws_ml[wr] = make_float2(m_run, l_run);
+      if (it.slot == 0 && x == 0 && r == 0)
+        a.counts[((long)it.p * a.Hkv + it.hkv) * a.nrt + it.mt] = it.split ? 2 * it.npieces : it.npieces;
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// One warp per output row: the maximum over the row's pieces, their weights
+// 2^(M_s - M), and the weighted sum of the partials over the sum of the
+// weighted L.  Pieces of weight 0 (they hold no key the row sees) are skipped.
+template <int D>
+__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs p, const DecodeArgs a) {
+  constexpr int V = D / 32;     // features a lane holds
+  griddep_wait();               // the decode kernel has ended, and it ends after attn_prefix
+  const int lane = threadIdx.x & 31;
+  const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);   // (b * Hq + h) * Tq + t = (b * Hkv + hkv) * R + rr
+  if (row >= (long)a.B * a.Hkv * p.R) return;
+  const int rr = (int)(row % p.R), bh = (int)(row / p.R), hkv = bh % a.Hkv, b = bh / a.Hkv;
+  const int pre = b / p.W, len = a.cache_lens[b], m = p.prefix_lens[pre];
+  if (len < 0 || len > a.S || m < 0 || m > p.Sp) return;        // reported by the kernels before
+  __nv_bfloat16* out = a.o + row * D + lane * V;
+  float acc[V] = {};
+  float M = -INFINITY, L = 0.f;
+  if (len - a.Tq + rr % a.Tq >= 0) {
+    const int gr = b % p.W * p.R + rr;
+    const long hp = (long)pre * a.Hkv + hkv, pbase = (hp * p.Rp + gr) * p.slots;
+    const long u = (long)bh * a.nrb + rr / 16, obase = u * a.slots * a.rows_ws + rr % 16;
+    const int np = m > 0 ? min(max(p.counts[hp * p.nrt + gr / kPrefixRows], 0), p.slots) : 0;
+    const int n = np + min(max(a.counts[u], 0), a.slots);
+    auto ml_of = [&](int s) { return s < np ? p.ws_ml[pbase + s] : a.ws_ml[obase + (long)(s - np) * a.rows_ws]; };
+    float2 ml = lane < n ? ml_of(lane) : make_float2(-INFINITY, 0.f);   // of the first 32 pieces
+    M = ml.x;
+    for (int s = 32 + lane; s < n; s += 32) M = fmaxf(M, ml_of(s).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      if (s0 > 0) ml = s0 + lane < n ? ml_of(s0 + lane) : make_float2(-INFINITY, 0.f);
+      const float wl = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      L = fmaf(ml.y, wl, L);
+      const int k1 = min(32, n - s0);
+#pragma unroll 4
+      for (int k = 0; k < k1; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, wl, k);
+        if (wk == 0.f) continue;
+        const int s = s0 + k;
+        const float* src = (s < np ? p.ws_o + (pbase + s) * D : a.ws_o + (obase + (long)(s - np) * a.rows_ws) * D) + lane * V;
+        if constexpr (V == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          acc[0] = fmaf(v.x, wk, acc[0]);
+          acc[1] = fmaf(v.y, wk, acc[1]);
+          acc[2] = fmaf(v.z, wk, acc[2]);
+          acc[3] = fmaf(v.w, wk, acc[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          acc[0] = fmaf(v.x, wk, acc[0]);
+          acc[1] = fmaf(v.y, wk, acc[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float inv = 1.f / L;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] *= inv;
+  }
+  if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+  } else {
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0], acc[1]);
+  }
+  if (lane == 0) a.lse[row] = (M + __log2f(L)) * 0.69314718055994531f;   // a query without keys: -infinity
+}
+
+template <int D, bool PAGED>
+static cudaError_t launch_prefix_dp(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& a, cudaStream_t stream) {
+  using C = PreCfg<D>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr_set[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(attn_prefix_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set[dev] = true;
+  }
+  prof_begin(kProfPrefix, stream);
+  const cudaError_t e = launch_programmatic(attn_prefix_kernel<D, PAGED>, dim3(a.teams * a.width), dim3(384),
+                                            C::kSmemBytes, stream, k, v, a);
+  prof_end(stream);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& a, int D,
+                               cudaStream_t stream) {
+  if (D == 128)
+    return a.table ? launch_prefix_dp<128, true>(k, v, a, stream) : launch_prefix_dp<128, false>(k, v, a, stream);
+  return a.table ? launch_prefix_dp<64, true>(k, v, a, stream) : launch_prefix_dp<64, false>(k, v, a, stream);
+}
+
+cudaError_t launch_prefix_merge(const PrefixArgs& p, const DecodeArgs& a, cudaStream_t stream) {
+  const long rows = (long)a.B * a.Hkv * p.R;
+  prof_begin(kProfPrefixMerge, stream);
+  const dim3 grid((unsigned)((rows + 7) / 8));
+  const cudaError_t e = a.D == 128 ? launch_programmatic(prefix_merge_kernel<128>, grid, dim3(256), 0, stream, p, a)
+                                   : launch_programmatic(prefix_merge_kernel<64>, grid, dim3(256), 0, stream, p, a);
+  prof_end(stream);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace gqa

@@ -178,9 +178,151 @@ attn_status decode_q4(const void* q, const void* k4, const void* ksf, const void
   return status_of(gqa::launch_decode_q4(a, sms, st_of(stream)));
 }
 
+// What the three entry points share.  Contiguous caches: no block table, page_size = S, num_pages = B.
+attn_status cache_weights(const void* q, const void* k, const void* ksf, float k_scale, const float* lse,
+                          const int* block_table, const int* cache_lens, float* weights, int B, int Hq, int Hkv, int Tq,
+                          int page_size, int num_pages, int max_pages, int D, float scale, void* stream,
+                          gqa::CacheFmt fmt) {
+  if (B < 0 || Tq < 0 || page_size < 0 || num_pages < 0 || max_pages < 0) return ATTN_ERR_SHAPE;
+  attn_status st = gqa::api_check_heads(Hq, Hkv, D);
+  if (st != ATTN_OK) return st;
+  const long S = block_table ? (long)page_size * max_pages : page_size;
+  const float scale_log2 = scale * k_scale * 1.4426950408889634f;
+  if (S > 0x7fffffffL - 512 || (long)page_size * num_pages > 0x7fffffffL || !isfinite(scale_log2) || !isfinite(scale) ||
+      !isfinite(k_scale) || (long)B * Hq * Tq > 0x7fffffffL || (long)B * max_pages > 0x7fffffffL ||
+      (long)B * Hkv > 0x7fffffffL / ((S + 255) / 256 + 1))
+    return ATTN_ERR_SHAPE;
+  if (!block_table && num_pages != B) return ATTN_ERR_SHAPE;
+  if (B == 0 || Tq == 0 || S == 0) return ATTN_OK;
+  if (num_pages < 1) return ATTN_ERR_SHAPE;
+  if (!q || !k || !lse || !cache_lens || !weights || (fmt == gqa::kCacheQ4 && !ksf)) return ATTN_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(ksf, 16) || !aligned(lse, 16) || !aligned(weights, 16) ||
+      !aligned(cache_lens, 4) || !aligned(block_table, 4))
+    return ATTN_ERR_ALIGN;
+  if ((st = gqa::api_check_arch()) != ATTN_OK) return st;
+  gqa::WeightsArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const uint8_t*>(k);
+  a.ksf = static_cast<const uint8_t*>(ksf);
+  a.lse = lse;
+  a.block_table = block_table;
+  a.cache_lens = cache_lens;
+  a.weights = weights;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.Tq = Tq;
+  a.R = Hq / Hkv * Tq;
+  a.S = (int)S;
+  a.D = D;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.scale_log2 = scale_log2;
+  a.status = gqa::api_status_word();
+  const int sms = gqa::api_sm_count();
+  if (!a.status || sms < 1) return ATTN_ERR_CUDA;
+  return status_of(gqa::launch_cache_weights(a, fmt, sms, st_of(stream)));
+}
+
+// Whether [p, p + n) and [q, q + m) (bytes) share one.
+bool overlap(const void* p, long n, const void* q, long m) {
+  const char *a = static_cast<const char*>(p), *b = static_cast<const char*>(q);
+  return a && b && n > 0 && m > 0 && a < b + m && b < a + n;
+}
+
 }  // namespace
 
 extern "C" {
+
+attn_status attn_cache_weights(const void* q, const void* k_cache, const float* lse, const int* block_table,
+                               const int* cache_lens, float* weights, int B, int Hq, int Hkv, int Tq, int page_size,
+                               int num_pages, int max_pages, int D, float scale, void* stream) {
+  return cache_weights(q, k_cache, nullptr, 1.f, lse, block_table, cache_lens, weights, B, Hq, Hkv, Tq, page_size,
+                       num_pages, max_pages, D, scale, stream, gqa::kCacheBf16);
+}
+
+attn_status attn_cache_weights_fp8(const void* q, const void* k8, float k_scale, const float* lse, const int* block_table,
+                                   const int* cache_lens, float* weights, int B, int Hq, int Hkv, int Tq, int page_size,
+                                   int num_pages, int max_pages, int D, float scale, void* stream) {
+  return cache_weights(q, k8, nullptr, k_scale, lse, block_table, cache_lens, weights, B, Hq, Hkv, Tq, page_size,
+                       num_pages, max_pages, D, scale, stream, gqa::kCacheE4m3);
+}
+
+attn_status attn_cache_weights_q4(const void* q, const void* k4, const void* k4_sf, float k_scale, const float* lse,
+                                  const int* block_table, const int* cache_lens, float* weights, int B, int Hq, int Hkv,
+                                  int Tq, int page_size, int num_pages, int max_pages, int D, float scale, void* stream) {
+  return cache_weights(q, k4, k4_sf, k_scale, lse, block_table, cache_lens, weights, B, Hq, Hkv, Tq, page_size, num_pages,
+                       max_pages, D, scale, stream, gqa::kCacheQ4);
+}
+
+attn_status attn_cache_evict(float* weights, void* const* planes, const int* row_bytes, int num_planes,
+                             const int* block_table, const int* cache_lens, int budget, int recent, int first, int* kept,
+                             int* lens_out, int B, int Hkv, int page_size, int num_pages, int max_pages, void* stream) {
+  if (B < 0 || Hkv < 1 || Hkv > 65535 || page_size < 0 || num_pages < 0 || max_pages < 0 || num_planes < 0 ||
+      num_planes > gqa::kEvictPlanes || budget < 1 || recent < 0 || first < 0 || (long)first + recent > budget)
+    return ATTN_ERR_SHAPE;
+  const long S = block_table ? (long)page_size * max_pages : page_size;
+  if (S > 0x7fffffffL - 2048 || (long)page_size * num_pages > 0x7fffffffL || (long)B * Hkv > 0x7fffffffL ||
+      (long)B * max_pages > 0x7fffffffL || budget > 0x7fffffff - 4096)
+    return ATTN_ERR_SHAPE;
+  if (!block_table && num_pages != B) return ATTN_ERR_SHAPE;
+  if (num_planes > 0 && (!planes || !row_bytes)) return ATTN_ERR_NULL;
+  for (int i = 0; i < num_planes; ++i)
+    if (row_bytes[i] < 4 || row_bytes[i] % 4 || row_bytes[i] > 4096) return ATTN_ERR_SHAPE;
+  if (B == 0) return ATTN_OK;
+  if (!cache_lens || !kept || !lens_out) return ATTN_ERR_NULL;
+  const long slots = (long)num_pages * Hkv * page_size;
+  if (slots > 0) {
+    if (!weights) return ATTN_ERR_NULL;
+    for (int i = 0; i < num_planes; ++i)
+      if (!planes[i]) return ATTN_ERR_NULL;
+  }
+  if (!aligned(weights, 16) || !aligned(cache_lens, 4) || !aligned(block_table, 4) || !aligned(kept, 4) ||
+      !aligned(lens_out, 4))
+    return ATTN_ERR_ALIGN;
+  for (int i = 0; i < num_planes; ++i)
+    if (!aligned(planes[i], 16)) return ATTN_ERR_ALIGN;
+  // the lengths and the table are read while rows move and the outputs are written, and no plane may be another's
+  gqa::EvictArgs a{};
+  a.planes[num_planes].p = weights;      // the smallest rows last
+  a.planes[num_planes].row_bytes = 4;
+  for (int i = 0; i < num_planes; ++i) {
+    a.planes[i].p = planes[i];
+    a.planes[i].row_bytes = row_bytes[i];
+  }
+  const struct { const void* p; long n; } io[] = {{cache_lens, 4L * B}, {block_table, 4L * B * max_pages},
+                                                  {kept, 4L * B * Hkv * budget}, {lens_out, 4L * B}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 2; j < 4; ++j)
+      if (i != j && overlap(io[i].p, io[i].n, io[j].p, io[j].n)) return ATTN_ERR_SHAPE;
+    for (int j = 0; j <= num_planes; ++j)
+      if (overlap(io[i].p, io[i].n, a.planes[j].p, slots * a.planes[j].row_bytes)) return ATTN_ERR_SHAPE;
+  }
+  for (int i = 0; i <= num_planes; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(a.planes[i].p, slots * a.planes[i].row_bytes, a.planes[j].p, slots * a.planes[j].row_bytes))
+        return ATTN_ERR_SHAPE;
+  const attn_status st = gqa::api_check_arch();
+  if (st != ATTN_OK) return st;
+  a.weights = weights;
+  a.n_planes = num_planes + 1;
+  a.block_table = block_table;
+  a.cache_lens = cache_lens;
+  a.kept = kept;
+  a.lens_out = lens_out;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.S = (int)S;
+  a.page_size = page_size > 0 ? page_size : 1;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.budget = budget;
+  a.recent = recent;
+  a.first = first;
+  a.status = gqa::api_status_word();
+  if (!a.status) return ATTN_ERR_CUDA;
+  return status_of(gqa::launch_cache_evict(a, st_of(stream)));
+}
 
 attn_status attn_cache_plan(const int* cache_lens, const int* new_lens, int* block_table, const int* free_pages,
                             const int* cursor, int* slots, int* positions, int* cu_seqlens, int* lens_out,

@@ -47,6 +47,13 @@ struct Fns {
   decltype(&attn_decode_q4_workspace_size) decode_ws;
   decltype(&attn_decode_q4_fwd) decode;
   decltype(&attn_decode_paged_q4_fwd) decode_paged;
+  decltype(&attn_cache_weights) weights;
+  decltype(&attn_cache_weights_fp8) weights_fp8;
+  decltype(&attn_cache_weights_q4) weights_q4;
+  decltype(&attn_cache_evict) evict;
+  decltype(&attn_decode_prefix_workspace_size) prefix_ws;
+  decltype(&attn_decode_prefix_fwd) prefix;
+  decltype(&attn_decode_paged_prefix_fwd) prefix_paged;
 } g_fn{};
 PyObject* g_check = nullptr;    // _binding._check(status, name)
 PyObject* g_stream = nullptr;   // the device's current stream's handle
@@ -481,6 +488,176 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   return wrap2(std::move(o), std::move(lse));
 }
 
+// A block table of B rows, or none: its pointer and its width.
+struct Blocks {
+  const int* p = nullptr;
+  int max_pages = 0;
+};
+Blocks blocks_arg(const at::Tensor& t, const char* name, int rows, int dev) {
+  Blocks b;
+  if (!t.defined()) return b;
+  if (t.dim() != 2 || t.size(0) != rows) value_error(std::string(name) + " must be [" + std::to_string(rows) + ", max_pages]");
+  b.p = address_of<const int>(t, name, at::kInt, dev);
+  b.max_pages = dim(t, 1, name);
+  return b;
+}
+
+const int* lens_arg(const at::Tensor& t, const char* name, int n, int dev) {
+  if (t.dim() != 1 || t.size(0) != n) value_error(std::string(name) + " must be [" + std::to_string(n) + "]");
+  return address_of<const int>(t, name, at::kInt, dev);
+}
+
+// (q, keys, k_scale, lse, cache_lens, weights, block_table, scale); keys: a cache of bf16 (k_scale None) or E4M3 keys,
+// or the codes and block scales of 4-bit ones
+PyObject* weights(PyObject* const* a, Py_ssize_t n) {
+  need_args(n, 8);
+  const at::Tensor &q = tensor(a[0], "q"), &lse = tensor(a[3], "lse"), &lens = tensor(a[4], "cache_lens"),
+                   &w = tensor(a[5], "weights");
+  const at::Tensor bt = optional(a[6], "block_table");
+  const int dev = device_of(q, "q");
+  if (q.dim() != 4) value_error("q must be [B, Hq, Tq, D]");
+  const bool q4 = PyTuple_GET_SIZE(a[1]) == 2, bf16 = a[2] == Py_None;
+  const char *kn = bf16 ? "k_cache" : q4 ? "k4" : "k8", *name = bf16 ? "attn_cache_weights" : q4 ? "attn_cache_weights_q4" : "attn_cache_weights_fp8";
+  const at::Tensor& k = tensor(PyTuple_GET_ITEM(a[1], 0), kn);
+  const int B = dim(q, 0, "q"), Hq = dim(q, 1, "q"), Tq = dim(q, 2, "q"), D = dim(q, 3, "q");
+  const int64_t wide = q4 ? D / 2 : D;
+  if (k.dim() != 4 || k.size(3) != wide)
+    value_error(std::string(kn) + " must be [pages, Hkv, page_size, " + std::to_string(wide) + "] matching q");
+  if (!bt.defined() && k.size(0) != B) value_error(std::string(kn) + " must hold a row for each of q's (or come with a block_table)");
+  const void *kp = address(k, kn, bf16 ? at::kBFloat16 : at::kByte, dev), *sf = nullptr;
+  if (q4) {
+    const at::Tensor& x = tensor(PyTuple_GET_ITEM(a[1], 1), "k4_sf");
+    if (x.dim() != 4 || x.sizes().slice(0, 3) != k.sizes().slice(0, 3) || x.size(3) != D / 16)
+      value_error("k4_sf must be [pages, Hkv, page_size, D/16]");
+    sf = address(x, "k4_sf", at::kByte, dev);
+  }
+  if (w.sizes() != k.sizes().slice(0, 3)) value_error("weights must be [pages, Hkv, page_size], an entry for each key");
+  if (lse.sizes() != q.sizes().slice(0, 3)) value_error("lse must be [B, Hq, Tq]");
+  const Blocks blocks = blocks_arg(bt, "block_table", B, dev);
+  if (bt.defined() && blocks.max_pages == 0) {     // no position: its NULL would mean contiguous caches
+    Py_INCREF(a[5]);
+    return a[5];
+  }
+  const void* qp = address(q, "q", at::kBFloat16, dev);
+  const float* lp = address_of<const float>(lse, "lse", at::kFloat, dev);
+  const int* ln = lens_arg(lens, "cache_lens", B, dev);
+  float* wp = address_of<float>(w, "weights", at::kFloat, dev);
+  const int pages = dim(k, 0, kn), H = dim(k, 1, kn), page_size = dim(k, 2, kn);
+  const float scale = a[7] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)float_arg(a[7]);
+  const float ks = bf16 ? 1.f : (float)float_arg(a[2]);
+  const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+  void* st = stream_of(dev);
+  if (bf16)
+    check(g_fn.weights(qp, kp, lp, blocks.p, ln, wp, B, Hq, H, Tq, page_size, pages, blocks.max_pages, D, scale, st), name);
+  else if (q4)
+    check(g_fn.weights_q4(qp, kp, sf, ks, lp, blocks.p, ln, wp, B, Hq, H, Tq, page_size, pages, blocks.max_pages, D, scale, st), name);
+  else
+    check(g_fn.weights_fp8(qp, kp, ks, lp, blocks.p, ln, wp, B, Hq, H, Tq, page_size, pages, blocks.max_pages, D, scale, st), name);
+  Py_INCREF(a[5]);
+  return a[5];
+}
+
+// (weights, caches, cache_lens, budget, recent, first, block_table, kept, lens_out)
+PyObject* evict(PyObject* const* a, Py_ssize_t n) {
+  need_args(n, 9);
+  const at::Tensor &w = tensor(a[0], "weights"), &lens = tensor(a[2], "cache_lens");
+  const at::Tensor bt = optional(a[6], "block_table");
+  const int dev = device_of(w, "weights");
+  if (w.dim() != 3) value_error("weights must be [pages, Hkv, page_size]");
+  if (lens.dim() != 1) value_error("cache_lens must be [B]");
+  const int B = dim(lens, 0, "cache_lens"), pages = dim(w, 0, "weights"), H = dim(w, 1, "weights"), page_size = dim(w, 2, "weights");
+  if (!bt.defined() && pages != B) value_error("weights must hold a row for each length (or come with a block_table)");
+  const int budget = int_arg(a[3], "budget"), recent = int_arg(a[4], "recent"), first = int_arg(a[5], "first");
+  if (budget < 1) value_error("budget must be at least 1");
+  const Py_ssize_t np = PyTuple_GET_SIZE(a[1]);
+  if (np > 8) value_error("caches: at most 8 planes");
+  void* planes[8];
+  int rows[8];
+  for (Py_ssize_t i = 0; i < np; ++i) {
+    const std::string name = "caches[" + std::to_string(i) + "]";
+    const at::Tensor& x = tensor(PyTuple_GET_ITEM(a[1], i), name.c_str());
+    if (x.dim() != 4 || x.sizes().slice(0, 3) != w.sizes()) value_error(name + " must be [pages, Hkv, page_size, width] as weights");
+    planes[i] = address(x, name.c_str(), x.scalar_type(), dev);
+    rows[i] = to_int(x.size(3) * (int64_t)x.element_size(), name.c_str());
+  }
+  const Blocks blocks = blocks_arg(bt, "block_table", B, dev);
+  at::Tensor kept = optional(a[7], "kept"), out = optional(a[8], "lens_out");
+  if (!kept.defined()) kept = at::empty({B, H, budget}, on(w, at::kInt));
+  if (!out.defined()) out = at::empty({B}, on(w, at::kInt));
+  if (kept.dim() != 3 || kept.size(0) != B || kept.size(1) != H || kept.size(2) != budget || out.dim() != 1 || out.size(0) != B)
+    value_error("kept must be [B, Hkv, budget], lens_out [B]");
+  const int* ln = lens_arg(lens, "cache_lens", B, dev);
+  float* wp = address_of<float>(w, "weights", at::kFloat, dev);
+  int *kp = address_of<int>(kept, "kept", at::kInt, dev), *op = address_of<int>(out, "lens_out", at::kInt, dev);
+  if (bt.defined() && blocks.max_pages == 0) value_error("block_table holds no page");
+  const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+  check(g_fn.evict(wp, planes, rows, (int)np, blocks.p, ln, budget, recent, first, kp, op, B, H, page_size, pages,
+                   blocks.max_pages, stream_of(dev)),
+        "attn_cache_evict");
+  return wrap2(std::move(kept), std::move(out));
+}
+
+// (q, k_prefix, v_prefix, prefix_table, prefix_lens, k, v, block_table, cache_lens, scale, o, lse, workspace);
+// k_prefix, v_prefix None: the prefixes are in k, v's pages too, through prefix_table
+PyObject* prefix(PyObject* const* a, Py_ssize_t n) {
+  need_args(n, 13);
+  const at::Tensor &q = tensor(a[0], "q"), &pl = tensor(a[4], "prefix_lens"), &lens = tensor(a[8], "cache_lens");
+  const bool paged = a[1] == Py_None;
+  const char *kn = paged ? "k_pages" : "k_cache", *vn = paged ? "v_pages" : "v_cache";
+  const at::Tensor &k = tensor(a[5], kn), &v = tensor(a[6], vn);
+  const int dev = device_of(q, "q");
+  if (q.dim() != 4) value_error("q must be [B, Hq, Tq, D]");
+  if (pl.dim() != 1) value_error("prefix_lens must be [P]");
+  const int B = dim(q, 0, "q"), Hq = dim(q, 1, "q"), Tq = dim(q, 2, "q"), D = dim(q, 3, "q"), P = dim(pl, 0, "prefix_lens");
+  if (P < 1 || B % P) value_error("the rows must be a multiple of the prefixes: " + std::to_string(B) + " rows, " + std::to_string(P) + " prefixes");
+  if (k.dim() != 4 || k.size(3) != D || v.sizes() != k.sizes() || (!paged && k.size(0) != B))
+    value_error(std::string(kn) + ", " + vn + (paged ? " must be [num_pages, Hkv, page_size, D] matching q" : " must be [B, Hkv, S, D] matching q"));
+  const int N = dim(k, 0, kn), H = dim(k, 1, kn), per = dim(k, 2, kn);
+  int Sp, S = per;
+  Blocks pt, bt;
+  const void *kp = nullptr, *vp = nullptr;
+  if (paged) {
+    pt = blocks_arg(tensor(a[3], "prefix_table"), "prefix_table", P, dev);
+    bt = blocks_arg(tensor(a[7], "block_table"), "block_table", B, dev);
+    Sp = to_int((int64_t)pt.max_pages * per, "prefix_table's positions");
+    S = to_int((int64_t)bt.max_pages * per, "block_table's positions");
+  } else {
+    const at::Tensor &x = tensor(a[1], "k_prefix"), &y = tensor(a[2], "v_prefix");
+    if (x.dim() != 4 || x.size(0) != P || x.size(1) != H || x.size(3) != D || y.sizes() != x.sizes())
+      value_error("k_prefix, v_prefix must be [P, Hkv, Sp, D] matching q and the caches");
+    Sp = dim(x, 2, "k_prefix");
+    kp = address(x, "k_prefix", at::kBFloat16, dev);
+    vp = address(y, "v_prefix", at::kBFloat16, dev);
+  }
+  at::Tensor o = optional(a[10], "o"), lse = optional(a[11], "lse");
+  if (!o.defined()) o = at::empty(q.sizes(), on(q, q.scalar_type()));
+  if (!lse.defined()) lse = at::empty(q.sizes().slice(0, 3), on(q, at::kFloat));
+  if (o.sizes() != q.sizes() || lse.sizes() != q.sizes().slice(0, 3)) value_error("o must be [B, Hq, Tq, D], lse [B, Hq, Tq]");
+  at::Tensor ws = optional(a[12], "workspace");
+  if (!ws.defined()) {
+    const int64_t bytes = (int64_t)g_fn.prefix_ws(B, Hq, H, Tq, P, Sp, S, D);
+    if (bytes > 0) ws = at::empty({bytes}, on(q, at::kByte));
+  }
+  void* wp = ws.defined() ? address(ws, "workspace", at::kByte, dev) : nullptr;
+  const size_t wn = ws.defined() ? (size_t)ws.numel() : 0;
+  const auto bf = at::kBFloat16;
+  const void *qp = address(q, "q", bf, dev), *kc = address(k, kn, bf, dev), *vc = address(v, vn, bf, dev);
+  const int *pn = lens_arg(pl, "prefix_lens", P, dev), *ln = lens_arg(lens, "cache_lens", B, dev);
+  void* op = address(o, "o", bf, dev);
+  float* lp = address_of<float>(lse, "lse", at::kFloat, dev);
+  const float scale = a[9] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)float_arg(a[9]);
+  const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+  void* st = stream_of(dev);
+  if (paged)
+    check(g_fn.prefix_paged(qp, kc, vc, pt.p, pn, bt.p, ln, op, lp, wp, wn, B, Hq, H, Tq, P, per, N, pt.max_pages,
+                            bt.max_pages, D, scale, st),
+          "attn_decode_paged_prefix_fwd");
+  else
+    check(g_fn.prefix(qp, kp, vp, pn, kc, vc, ln, op, lp, wp, wn, B, Hq, H, Tq, P, Sp, S, D, scale, st),
+          "attn_decode_prefix_fwd");
+  return wrap2(std::move(o), std::move(lse));
+}
+
 // (addresses of the C functions by name, _check, current raw stream of a device)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   need_args(n, 3);
@@ -503,6 +680,13 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   BIND(decode_ws, attn_decode_q4_workspace_size);
   BIND(decode, attn_decode_q4_fwd);
   BIND(decode_paged, attn_decode_paged_q4_fwd);
+  BIND(weights, attn_cache_weights);
+  BIND(weights_fp8, attn_cache_weights_fp8);
+  BIND(weights_q4, attn_cache_weights_q4);
+  BIND(evict, attn_cache_evict);
+  BIND(prefix_ws, attn_decode_prefix_workspace_size);
+  BIND(prefix, attn_decode_prefix_fwd);
+  BIND(prefix_paged, attn_decode_paged_prefix_fwd);
 #undef BIND
   PyObject** keep[2] = {&g_check, &g_stream};
   for (int i = 0; i < 2; ++i) {
@@ -528,7 +712,8 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<f>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {METHOD(bind),   METHOD(plan),   METHOD(rope_table), METHOD(rope),
-                           METHOD(append), METHOD(gather), METHOD(decode),     {nullptr, nullptr, 0, nullptr}};
+                           METHOD(append), METHOD(gather), METHOD(decode),     METHOD(weights),
+                           METHOD(evict),  METHOD(prefix), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_cache_ext", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -96,4 +96,39 @@ struct DecodeQ4Args {
 size_t decode_q4_ws_bytes(int B, int Hq, int Hkv, int Tq, int S, int D);
 cudaError_t launch_decode_q4(const DecodeQ4Args& a, int sms, cudaStream_t stream);
 
+// Attention weight of cached keys, added to weights [N, Hkv, P] f32 (contiguous
+// caches: N = B, P = S, no block table).
+struct WeightsArgs {
+  const __nv_bfloat16* q;    // [B, Hkv, R, D], R = G * Tq
+  const uint8_t *k, *ksf;    // keys (any format), 4-bit: their block scales
+  const float* lse;          // [B, Hkv, R]
+  const int* block_table;    // [B, max_pages] or nullptr
+  const int* cache_lens;
+  float* weights;
+  int B, Hkv, Tq, R, S, D, page_size, max_pages, num_pages;
+  float scale_log2;          // softmax scale * k_scale * log2(e)
+  int* status;
+};
+cudaError_t launch_cache_weights(const WeightsArgs& a, CacheFmt fmt, int sms, cudaStream_t stream);
+
+// Eviction.  The planes [N, Hkv, P, row_bytes] of a cache, the weights among them.
+constexpr int kEvictPlanes = 8;
+struct EvictPlane {
+  void* p;
+  int row_bytes;
+  int piece, slice_bytes, slices;   // bytes a thread moves; of a row that a CTA moves; CTAs a row (set by the launch)
+};
+struct EvictArgs {
+  const float* weights;
+  EvictPlane planes[kEvictPlanes + 1];
+  int n_planes;
+  const int* block_table;    // [B, max_pages] or nullptr
+  const int* cache_lens;
+  int *kept, *lens_out;      // [B, Hkv, budget], [B]
+  int B, Hkv, S, page_size, max_pages, num_pages;
+  int budget, recent, first;
+  int* status;
+};
+cudaError_t launch_cache_evict(EvictArgs a, cudaStream_t stream);
+
 }  // namespace gqa

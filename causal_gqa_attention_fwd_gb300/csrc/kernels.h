@@ -126,6 +126,10 @@ struct DecodeArgs {
   // boxes, no swizzle); K's scale is folded into scale_log2, V's applied to O
   int fp8;
   float v_scale;          // 1 for 16-bit caches
+  int min_len;            // shortest valid length: Tq, or 0 (queries at negative positions see no key)
+  // attention over a shared prefix: every unit leaves partials (also one that is not cut) and, in its first piece,
+  // how many; nullptr otherwise
+  int* counts;            // [units]
 };
 
 // k, v: dense maps over the caches ([B*Hkv, S, D], 64 x 128 boxes) or, paged,
@@ -133,6 +137,35 @@ struct DecodeArgs {
 // boxes); q: 2-D map over the query rows ([B*Hq*Tq, D], 64 x 16 boxes).
 cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const DecodeArgs& a,
                                int grid, cudaStream_t stream);
+
+// The partial kernel alone, as a programmatic dependent of the kernel before it in the stream, which must have passed
+// its own griddep_wait when it let dependents start (a.counts set: the merge is launch_prefix_merge's).
+cudaError_t launch_attn_decode_parts(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
+                                     const DecodeArgs& a, int grid, cudaStream_t stream);
+
+// Attention of a batch over prefixes that its rows share: prefix p (p < P) belongs to rows p*W .. p*W + W - 1.  The
+// Rp = W*R query rows (R = G*Tq a batch row) of a (prefix, K/V head) go in nrt blocks of 256; a (prefix, K/V head,
+// block) is a unit.  CTAs work in teams of `width`: a team takes a share of the stream of 128-key blocks of its
+// groups (prefix, K/V head, outer), CTA i of it the unit of row block outer*width + i, so that the CTAs that read the
+// same keys read them at the same time.
+constexpr int kPrefixRows = 256;
+struct PrefixArgs {
+  const __nv_bfloat16* q;   // [B, Hkv, R, D]
+  const int* prefix_lens;   // [P] device
+  const int* table;         // [P, max_pages] device, nullptr for contiguous prefixes
+  float* ws_o;              // [P * Hkv * Rp, slots, D]
+  float2* ws_ml;            // [P * Hkv * Rp, slots] (max in log2 units, sum)
+  int* counts;              // [units] slots in use
+  int* status;
+  int* dbg_line;
+  int P, W, Hkv, R, Rp, nrt, width, outer, teams, Sp, slots;
+  int page_size, max_pages, num_pages;
+  float scale_log2;
+};
+cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& a, int D,
+                               cudaStream_t stream);
+// Joins the prefix's partials with those of the rows' own caches: O and LSE of every row.
+cudaError_t launch_prefix_merge(const PrefixArgs& p, const DecodeArgs& a, cudaStream_t stream);
 
 // Kernel-level timing (opt-in instrumentation, api.cu): event pairs recorded
 // on the launch stream around each kernel.
@@ -149,7 +182,12 @@ enum ProfKind {
   kProfRopeTable = 9,
   kProfAppend = 10,
   kProfGather = 11,
-  kProfKinds = 12
+  kProfPrefix = 12,
+  kProfPrefixMerge = 13,
+  kProfWeights = 14,
+  kProfEvictSelect = 15,
+  kProfEvictMove = 16,
+  kProfKinds = 17
 };
 // Launch with programmatic stream serialization (see griddep_wait in
 // sm103.cuh): the kernel's CTAs may be scheduled, and run their set-up, while

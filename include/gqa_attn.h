@@ -499,6 +499,119 @@ GQA_ATTN_API attn_status attn_decode_paged_q4_fwd(const void* q, const void* k4_
                                                   int D, float scale, const float* rope_cos_sin, int rope_positions,
                                                   void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention of rows that share prefixes (the paged KV-cache management of the
+ * RoseLLM README, section "Inference and serving"; per-row-prefix cached
+ * attention of the microLLM-rocm README, section "Why this project exists"):
+ * one system prompt or document behind a batch, or several samples of each
+ * prompt.  The keys and values of a prefix are read once for all of its rows.
+ *
+ *   prefix p (0 <= p < P) belongs to the W = B / P rows p*W .. p*W + W - 1 and
+ *   holds m_p = prefix_lens[p] keys; row b holds n_b = cache_lens[b] keys of its
+ *   own behind them (the Tq new ones included).  Query t of row b has own
+ *   position n_b - Tq + t; it sees every key of its prefix and the own keys up
+ *   to that position.  A query at a negative own position (n_b < Tq; a batch
+ *   slot without a request has n_b = 0) sees nothing: O = 0, LSE = -infinity.
+ *
+ *   q, o                  bf16 [B, Hq, Tq, D];  lse float32 [B, Hq, Tq]
+ *   k_prefix, v_prefix    bf16 [P, Hkv, Sp, D]   (rows past m_p are not used)
+ *   k_cache, v_cache      bf16 [B, Hkv, S, D]    (rows past n_b are not used)
+ *   prefix_lens           DEVICE int32 [P], 0 <= m_p <= Sp
+ *   cache_lens            DEVICE int32 [B], 0 <= n_b <= S
+ * A length outside its range is reported (ATTN_ERR_SEQLENS); the outputs of the
+ * rows it concerns are left unwritten.  B is a multiple of P; Tq <= S; Sp may
+ * be 0 (k_prefix, v_prefix NULL).  Queries and keys are taken as they are: with
+ * rotary positions, rotated before (attn_rope, attn_cache_append), an own key's
+ * position following the prefix's.  P is rounded to bf16 for the P V product;
+ * everything else is f32.  How a row's keys are cut into pieces follows from
+ * the sizes and the lengths: the same call gives the same bits.
+ * workspace: attn_decode_prefix_workspace_size() bytes, 256-byte aligned, no
+ * initialisation; calls in flight at once need one each. */
+GQA_ATTN_API size_t attn_decode_prefix_workspace_size(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, int D);
+GQA_ATTN_API attn_status attn_decode_prefix_fwd(const void* q, const void* k_prefix, const void* v_prefix,
+                                                const int* prefix_lens, const void* k_cache, const void* v_cache,
+                                                const int* cache_lens, void* o, float* lse, void* workspace,
+                                                size_t workspace_bytes, int B, int Hq, int Hkv, int Tq, int P, int Sp,
+                                                int S, int D, float scale, void* stream);
+
+/* The same over one pool of pages [num_pages, Hkv, page_size, D] (page sizes of
+ * attn_decode_paged_fwd): key j of prefix p is row j % page_size of page
+ * prefix_table[p*max_prefix_pages + j/page_size], own key j of row b that of
+ * page block_table[b*max_pages + j/page_size]; own keys begin with a page of
+ * their own wherever the prefix ends.  An entry outside [0, num_pages) is
+ * reported (ATTN_ERR_PAGES) and its keys read as zeros.  workspace: as above
+ * with Sp = max_prefix_pages * page_size, S = max_pages * page_size. */
+GQA_ATTN_API attn_status attn_decode_paged_prefix_fwd(const void* q, const void* k_pages, const void* v_pages,
+                                                      const int* prefix_table, const int* prefix_lens,
+                                                      const int* block_table, const int* cache_lens, void* o, float* lse,
+                                                      void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
+                                                      int Tq, int P, int page_size, int num_pages, int max_prefix_pages,
+                                                      int max_pages, int D, float scale, void* stream);
+
+/* Attention weight of cached keys (for evicting those that receive little; the
+ * KV-cache management of the RoseLLM README, section "Inference and serving"):
+ *   weights[j] += sum over the Hq/Hkv query heads of j's K/V head and the
+ *   queries t that see j (j <= cache_lens[b] - Tq + t) of
+ *   exp(scale q . k_j - lse)
+ * where the entries of the row's last Tq positions, the step's new keys, are set
+ * to the sum instead (whatever their slots held before), with q bf16
+ * [B, Hq, Tq, D] and the lse float32 [B, Hq, Tq] that the step's
+ * attention returned (-infinity, a query that saw no key: adds nothing).  Behind
+ * a shared prefix that lse counts the prefix's keys too, and so do the weights.
+ *   weights  float32 [num_pages, Hkv, page_size], an entry beside each key
+ *            (slots as above); entries of positions past a row's length stay
+ *   keys     bf16 [num_pages, Hkv, page_size, D], E4M3 codes of the same shape
+ *            (key = e4m3 * k_scale), or 4-bit codes and block scales
+ *   cache_lens DEVICE int32 [B], 0 <= cache_lens[b] <= the capacity: otherwise
+ *            reported (ATTN_ERR_SEQLENS) and the row's weights stay
+ *   block_table DEVICE int32 [B, max_pages], any page size; NULL: contiguous
+ *            caches, num_pages = B, page_size = S, max_pages unused.  An entry
+ *            outside the pool is reported (ATTN_ERR_PAGES), its keys skipped.
+ * No two (row, position) of a call may be the same slot: an entry that two rows
+ * name gets one of their sums.  Scores and sums are f32, in a fixed order; for
+ * E4M3 and 4-bit keys the queries are carried in f16, scaled by a power of two a
+ * row: exact down to 2^-31 of a row's largest feature, below that off by at
+ * most 2^-39 of it. */
+GQA_ATTN_API attn_status attn_cache_weights(const void* q, const void* k_cache, const float* lse, const int* block_table,
+                                            const int* cache_lens, float* weights, int B, int Hq, int Hkv, int Tq,
+                                            int page_size, int num_pages, int max_pages, int D, float scale,
+                                            void* stream);
+GQA_ATTN_API attn_status attn_cache_weights_fp8(const void* q, const void* k8, float k_scale, const float* lse,
+                                                const int* block_table, const int* cache_lens, float* weights, int B,
+                                                int Hq, int Hkv, int Tq, int page_size, int num_pages, int max_pages,
+                                                int D, float scale, void* stream);
+GQA_ATTN_API attn_status attn_cache_weights_q4(const void* q, const void* k4, const void* k4_sf, float k_scale,
+                                               const float* lse, const int* block_table, const int* cache_lens,
+                                               float* weights, int B, int Hq, int Hkv, int Tq, int page_size,
+                                               int num_pages, int max_pages, int D, float scale, void* stream);
+
+/* Eviction: each row of more than `budget` keys is cut down to `budget`, in
+ * place, each K/V head by itself.  Positions below `first` and the last `recent`
+ * ones stay; of the others those with the largest weights do (of equal weights
+ * the lower position; -0 equals 0, a NaN counts as the largest).  The kept
+ * rows of `weights` and of the num_planes <= 8 planes move to positions
+ * 0 .. budget-1 in their order, bit for bit; the entries behind stay as they
+ * were.  A row of at most `budget` keys is not touched.  (Keys that were
+ * rotated keep their rotation; a later key's position is its own, not the row's
+ * new length.  A paged row needs only its first ceil(budget / page_size) pages
+ * afterwards.)
+ *   planes     HOST array of DEVICE pointers, plane i [num_pages, Hkv, page_size]
+ *              rows of row_bytes[i] (HOST; a multiple of 4, at most 4096)
+ *   weights    float32 [num_pages, Hkv, page_size]
+ *   kept       DEVICE int32 [B, Hkv, budget]: the positions kept, ascending; of
+ *              a shorter row all its positions, then -1
+ *   lens_out   DEVICE int32 [B]: min(cache_lens[b], budget)
+ *   block_table, cache_lens as attn_cache_weights; a row whose length is out of
+ *              range is reported, left alone, its kept all -1 and its lens_out its
+ *              cache_lens.  Positions in a page outside the pool are reported
+ *              (ATTN_ERR_PAGES), count as the smallest weight and are not moved.
+ * No two (row, position) may be the same slot; no output may overlap another
+ * buffer of the call (ATTN_ERR_SHAPE).  first + recent <= budget, budget >= 1. */
+GQA_ATTN_API attn_status attn_cache_evict(float* weights, void* const* planes, const int* row_bytes, int num_planes,
+                                          const int* block_table, const int* cache_lens, int budget, int recent,
+                                          int first, int* kept, int* lens_out, int B, int Hkv, int page_size,
+                                          int num_pages, int max_pages, void* stream);
+
 /* Static description of a status code. */
 GQA_ATTN_API const char* attn_status_string(attn_status status);
 
@@ -550,7 +663,8 @@ GQA_ATTN_API attn_status attn_test_inject_timeout(int kernel, int limit_ms);
  * kernel kind (0 forward, 1 backward preprocess, 2 backward dK/dV kernel,
  * 3 unused, 4 decode partial, 5 decode split merge, 6 backward dQ kernel,
  * 7 cache plan, 8 rotary rows, 9 rotary table, 10 cache append, 11 cache
- * gather), the number of launches and their summed device
+ * gather, 12 shared prefix, 13 its merge, 14 attention weights of cached keys,
+ * 15 eviction's selection, 16 its moves), the number of launches and their summed device
  * time in milliseconds since the last attn_profile_reset.  At most 65536
  * launches are recorded between resets.  Off by default. */
 GQA_ATTN_API attn_status attn_profile_enable(int enable);
