@@ -692,7 +692,6 @@ attn_status decode_common(const void* q, const CUtensorMap& tk, const CUtensorMa
   a.max_pages = max_pages;
   a.num_pages = num_pages;
   a.rope_cs = rope_cos_sin;
-  a.min_len = Tq;
   CUtensorMap tq;
   const uint64_t qdims[2] = {(uint64_t)D, (uint64_t)B * Hq * Tq};
   const uint64_t qstrides[1] = {(uint64_t)D * 2};
@@ -878,12 +877,28 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int Tq, int P, int Sp) {
   return p;
 }
 
-struct PrefixWs {
-  size_t o, ml, counts, dec_o, dec_ml, dec_counts, bytes;
+// The rows' own keys: blocks of query rows, and the units that follow.
+struct OwnPlan {
+  int R, nrb, rows_ws;
+  long units;
 };
 
-PrefixWs prefix_ws(const PrefixPlan& p, const DecodePlan& d, int P, int Hkv, int D) {
-  const size_t rows = (size_t)P * Hkv * p.Rp * p.slots, own = (size_t)d.units * d.slots * d.rows_ws;
+OwnPlan own_plan(int B, int Hq, int Hkv, int Tq) {
+  OwnPlan p{};
+  p.R = Hq / Hkv * Tq;
+  const int block = p.R <= 8 ? 8 : 16;
+  p.nrb = (p.R + block - 1) / block;
+  p.rows_ws = p.R < block ? p.R : block;
+  p.units = (long)B * Hkv * p.nrb;
+  return p;
+}
+
+struct PrefixWs {
+  size_t o, ml, counts, own_o, own_ml, own_counts, bytes;
+};
+
+PrefixWs prefix_ws(const PrefixPlan& p, const OwnPlan& d, int P, int Hkv, int D) {
+  const size_t rows = (size_t)P * Hkv * p.Rp * p.slots, own = (size_t)(d.units + gqa::kOwnMaxWarps) * d.rows_ws;
   PrefixWs w{};
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -894,9 +909,9 @@ PrefixWs prefix_ws(const PrefixPlan& p, const DecodePlan& d, int P, int Hkv, int
   w.o = take(rows * D * 4);
   w.ml = take(rows * 8);
   w.counts = take((size_t)p.units * 4);
-  w.dec_o = take(own * D * 4);
-  w.dec_ml = take(own * 8);
-  w.dec_counts = take((size_t)d.units * 4);
+  w.own_o = take(own * D * 4);
+  w.own_ml = take(own * 8);
+  w.own_counts = take((size_t)d.units * 8);
   w.bytes = at;
   return w;
 }
@@ -907,6 +922,8 @@ attn_status prefix_check(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, i
   if (st != ATTN_OK) return st;
   if (B % P) return ATTN_ERR_SHAPE;
   if (B == 0 || Tq == 0) return ATTN_OK;
+  // positions in the stream of the rows' own tiles
+  if (own_plan(B, Hq, Hkv, Tq).units > 0x7fffffffL / (S / 16 + 4L)) return ATTN_ERR_SHAPE;
   const PrefixPlan p = prefix_plan(B, Hq, Hkv, Tq, P, Sp);
   // block stream and ring indices
   if (p.units * ((Sp + 127L) / 128) > 0x3fffffffL || (long)P * Hkv > 0x7fffffffL) return ATTN_ERR_SHAPE;
@@ -925,7 +942,7 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   const int sms = sm_count();
   if (!status || sms < 1) return ATTN_ERR_CUDA;
   const PrefixPlan p = prefix_plan(B, Hq, Hkv, Tq, P, Sp);
-  const DecodePlan d = decode_plan(B, Hq, Hkv, Tq, S);
+  const OwnPlan d = own_plan(B, Hq, Hkv, Tq);
   const PrefixWs w = prefix_ws(p, d, P, Hkv, D);
   char* ws = static_cast<char*>(workspace);
   const int ctas = sms < gqa::kDecodeMaxSlots ? sms : gqa::kDecodeMaxSlots;   // one a SM, as decode
@@ -956,43 +973,31 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   a.max_pages = max_prefix_pages;
   a.num_pages = num_pages;
   a.scale_log2 = scale * 1.4426950408889634f;
-  gqa::DecodeArgs e{};
+  gqa::OwnArgs e{};
   e.q = a.q;
   e.cache_lens = cache_lens;
-  e.o = static_cast<__nv_bfloat16*>(o);
-  e.lse = lse;
-  e.ws_o = reinterpret_cast<float*>(ws + w.dec_o);
-  e.ws_ml = reinterpret_cast<float2*>(ws + w.dec_ml);
-  e.counts = reinterpret_cast<int*>(ws + w.dec_counts);
+  e.block_table = block_table;
+  e.ws_o = reinterpret_cast<float*>(ws + w.own_o);
+  e.ws_ml = reinterpret_cast<float2*>(ws + w.own_ml);
+  e.counts = reinterpret_cast<int2*>(ws + w.own_counts);
   e.status = status;
   e.B = B;
-  e.Hq = Hq;
   e.Hkv = Hkv;
-  e.G = Hq / Hkv;
   e.Tq = Tq;
-  e.S = S;
-  e.D = D;
   e.R = d.R;
   e.nrb = d.nrb;
-  e.slots = d.slots;
   e.rows_ws = d.rows_ws;
-  e.ctas = ctas;
-  e.scale_log2 = a.scale_log2;
-  e.v_scale = 1.f;
-  e.block_table = block_table;
+  e.S = S;
+  e.D = D;
   e.page_size = page_size;
   e.max_pages = max_pages;
   e.num_pages = num_pages;
-  CUtensorMap tq;
-  const uint64_t qdims[2] = {(uint64_t)D, (uint64_t)B * Hq * Tq};
-  const uint64_t qstrides[1] = {(uint64_t)D * 2};
-  const uint32_t qbox[2] = {64, (uint32_t)kDecodeRows};
-  if (!gqa::make_tmap(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, qdims, qstrides, qbox, CU_TENSOR_MAP_SWIZZLE_128B))
-    return ATTN_ERR_CUDA;
+  e.ctas = ctas;
+  e.scale_log2 = a.scale_log2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err = gqa::launch_attn_prefix(pk, pv, a, D, s);
-  if (err == cudaSuccess) err = gqa::launch_attn_decode_parts(tk, tv, tq, e, ctas, s);
-  if (err == cudaSuccess) err = gqa::launch_prefix_merge(a, e, s);
+  if (err == cudaSuccess) err = gqa::launch_attn_own(tk, tv, e, s);
+  if (err == cudaSuccess) err = gqa::launch_prefix_merge(a, e, static_cast<__nv_bfloat16*>(o), lse, s);
   return launch_status(err);
 }
 
@@ -1004,7 +1009,7 @@ attn_status prefix_check_pointers(const void* q, const void* k, const void* v, c
       (reinterpret_cast<uintptr_t>(prefix_lens) & 3u) || (reinterpret_cast<uintptr_t>(cache_lens) & 3u))
     return ATTN_ERR_ALIGN;
   const size_t need =
-      prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), decode_plan(B, Hq, Hkv, Tq, S), P, Hkv, D).bytes;
+      prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), own_plan(B, Hq, Hkv, Tq), P, Hkv, D).bytes;
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return ATTN_ERR_WORKSPACE;
   return ATTN_OK;
 }
@@ -1015,7 +1020,7 @@ extern "C" {
 
 size_t attn_decode_prefix_workspace_size(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, int D) {
   if (prefix_check(B, Hq, Hkv, Tq, P, Sp, S, D) != ATTN_OK || B == 0 || Tq == 0) return 0;
-  return prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), decode_plan(B, Hq, Hkv, Tq, S), P, Hkv, D).bytes;
+  return prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), own_plan(B, Hq, Hkv, Tq), P, Hkv, D).bytes;
 }
 
 attn_status attn_decode_prefix_fwd(const void* q, const void* k_prefix, const void* v_prefix, const int* prefix_lens,
@@ -1032,7 +1037,9 @@ attn_status attn_decode_prefix_fwd(const void* q, const void* k_prefix, const vo
   if (Sp > 0 && (!k_prefix || !v_prefix)) return ATTN_ERR_NULL;
   if (!aligned16(k_prefix) || !aligned16(v_prefix)) return ATTN_ERR_ALIGN;
   CUtensorMap tk, tv, pk, pv;
-  if (!map_dense(&tk, k_cache, D, S, (long)B * Hkv) || !map_dense(&tv, v_cache, D, S, (long)B * Hkv)) return ATTN_ERR_CUDA;
+  const int box = gqa::own_box_rows(D, 0);
+  if (!map_dense(&tk, k_cache, D, S, (long)B * Hkv, box) || !map_dense(&tv, v_cache, D, S, (long)B * Hkv, box))
+    return ATTN_ERR_CUDA;
   pk = tk;   // Sp = 0: no length is valid but 0, and nothing is loaded through them
   pv = tv;
   if (Sp > 0 && (!map_dense(&pk, k_prefix, D, Sp, (long)P * Hkv) || !map_dense(&pv, v_prefix, D, Sp, (long)P * Hkv)))
@@ -1063,12 +1070,14 @@ attn_status attn_decode_paged_prefix_fwd(const void* q, const void* k_pages, con
   if (!block_table || (Sp > 0 && !prefix_table)) return ATTN_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(prefix_table) & 3u))
     return ATTN_ERR_ALIGN;
-  const int box = page_size < 128 ? page_size : 128;
-  CUtensorMap tk, tv;
-  if (!map_dense(&tk, k_pages, D, page_size, (long)num_pages * Hkv, box) ||
+  const int pbox = page_size < 128 ? page_size : 128, box = gqa::own_box_rows(D, page_size);
+  CUtensorMap pk, pv, tk, tv;
+  if (!map_dense(&pk, k_pages, D, page_size, (long)num_pages * Hkv, pbox) ||
+      !map_dense(&pv, v_pages, D, page_size, (long)num_pages * Hkv, pbox) ||
+      !map_dense(&tk, k_pages, D, page_size, (long)num_pages * Hkv, box) ||
       !map_dense(&tv, v_pages, D, page_size, (long)num_pages * Hkv, box))
     return ATTN_ERR_CUDA;
-  return prefix_common(q, tk, tv, prefix_lens, Sp > 0 ? prefix_table : block_table, max_prefix_pages, tk, tv, cache_lens,
+  return prefix_common(q, pk, pv, prefix_lens, Sp > 0 ? prefix_table : block_table, max_prefix_pages, tk, tv, cache_lens,
                        block_table, max_pages, page_size, num_pages, o, lse, workspace, B, Hq, Hkv, Tq, P, (int)Sp,
                        (int)S, D, scale, stream);
 }

@@ -176,7 +176,7 @@ constexpr int kLenCache = 256;  // batch rows whose lengths are kept in shared m
 // `lens` is the shared-memory copy of cache_lens (B <= kLenCache) or cache_lens itself.
 __device__ __forceinline__ int row_chunks(const DecodeArgs& a, const int* lens, int b, int& len) {
   len = lens[b];
-  return (len >= a.min_len && len <= a.S) ? (len + kCK - 1) / kCK : 0;
+  return (len >= a.Tq && len <= a.S) ? (len + kCK - 1) / kCK : 0;
 }
 
 // The CTA's share of the chunk stream.  The stream holds the chunks of every
@@ -589,8 +589,7 @@ __device__ __noinline__ void decode_write_out(const DecodeArgs& a, const Piece& 
   tc_fence_before();
   mbar_arrive_warp(&o_empty[ob]);
   if (guard.aborted() || j >= D) return;
-  const bool whole = it.npieces == 1 && a.counts == nullptr;
-  if (a.counts != nullptr && it.slot == 0 && j == 0) a.counts[it.u] = it.npieces;
+  const bool whole = it.npieces == 1;
   const long pbase = ((long)it.u * a.slots + it.slot) * a.rows_ws;
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
@@ -633,7 +632,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
       if (b0 + lane < a.B) {
         const int len = a.cache_lens[b0 + lane];
         if (a.B <= kLenCache) s_len[b0 + lane] = len;
-        bad |= len < a.min_len || len > a.S;
+        bad |= len < a.Tq || len > a.S;
       }
     }
     if (__any_sync(0xffffffffu, bad) && blockIdx.x == 0 && lane == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
@@ -1143,8 +1142,6 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols<FP8>);
-  // launched beside the prefix kernel, which the merge reads too: this grid does not end before that one has
-  if (a.counts != nullptr) griddep_wait();
 }
 
 // One CTA per output row (b, h, t) of a cut unit (rows of units processed
@@ -1222,28 +1219,22 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const DecodeArgs a) {
 }
 
 template <int D, bool PAGED, bool FP8>
-static cudaError_t set_decode_attr() {
+static cudaError_t launch_decode_dp(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
+                                    const DecodeArgs& a, int grid, cudaStream_t stream) {
   using C = DecCfg<D, FP8>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 64 && attr_set[dev]) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(decode_partial_kernel<D, PAGED, FP8>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  if (e == cudaSuccess && dev < 64) attr_set[dev] = true;
-  return e;
-}
-
-template <int D, bool PAGED, bool FP8>
-static cudaError_t launch_decode_dp(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
-                                    const DecodeArgs& a, int grid, cudaStream_t stream) {
-  using C = DecCfg<D, FP8>;
-  cudaError_t e = set_decode_attr<D, PAGED, FP8>();
-  if (e != cudaSuccess) return e;
+  if (dev < 64 && !attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(decode_partial_kernel<D, PAGED, FP8>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
   prof_begin(kProfDecode, stream);
   decode_partial_kernel<D, PAGED, FP8><<<grid, FP8 ? kThreads8 : kThreads, C::kSmemBytes, stream>>>(k, v, q, a);
   prof_end(stream);
-  e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.slots <= 1) return e;  // no unit can be cut
   // programmatic dependent launch: the merge grid may start while the
   // partial grid drains; it waits (griddepcontrol.wait) before reading
@@ -1279,25 +1270,6 @@ cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const
                                int grid, cudaStream_t stream) {
   if (a.D == 128) return launch_decode_d<128>(k, v, q, a, grid, stream);
   return launch_decode_d<64>(k, v, q, a, grid, stream);
-}
-
-template <int D, bool PAGED>
-static cudaError_t launch_parts(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const DecodeArgs& a,
-                                int grid, cudaStream_t stream) {
-  cudaError_t e = set_decode_attr<D, PAGED, false>();
-  if (e != cudaSuccess) return e;
-  prof_begin(kProfDecode, stream);
-  e = launch_programmatic(decode_partial_kernel<D, PAGED, false>, dim3(grid), dim3(kThreads),
-                          DecCfg<D, false>::kSmemBytes, stream, k, v, q, a);
-  prof_end(stream);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-cudaError_t launch_attn_decode_parts(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
-                                     const DecodeArgs& a, int grid, cudaStream_t stream) {
-  const bool paged = a.block_table != nullptr;
-  if (a.D == 128) return paged ? launch_parts<128, true>(k, v, q, a, grid, stream) : launch_parts<128, false>(k, v, q, a, grid, stream);
-  return paged ? launch_parts<64, true>(k, v, q, a, grid, stream) : launch_parts<64, false>(k, v, q, a, grid, stream);
 }
 
 }  // namespace gqa

@@ -6,8 +6,8 @@
 //   M = max(M_p, M_o),  L = L_p 2^(M_p - M) + L_o 2^(M_o - M),
 //   O = (O_p 2^(M_p - M) + O_o 2^(M_o - M)) / L,   LSE = ln 2 (M + log2 L),
 // so the two parts run apart: attn_prefix leaves unnormalised partials
-// (O, M, L) of the prefix, the decode kernel (attn_decode.cu) those of the
-// rows' own caches, and prefix_merge joins them.
+// (O, M, L) of the prefix, attn_own (attn_own.cu) those of the rows' own caches,
+// and prefix_merge joins them.
 //
 // attn_prefix  The W * G * Tq query rows that meet a (prefix, K/V head) are a
 //   matrix, and both products are GEMM-shaped: tiles of 128 query rows as M,
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
-  griddep_launch();   // every CTA is past its wait: the decode kernel may read what the grids before wrote
+  griddep_launch();   // every CTA is past its wait: attn_own may read what the grids before wrote
 
   if (warp == 0) {
     // ======================================================== TMA producer
@@ -585,44 +585,50 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// One warp per output row: the maximum over the row's pieces, their weights
+// WPR warps per output row: the maximum over the row's pieces, their weights
 // 2^(M_s - M), and the weighted sum of the partials over the sum of the
 // weighted L.  Pieces of weight 0 (they hold no key the row sees) are skipped.
-template <int D>
-__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs p, const DecodeArgs a) {
+// Warp w of a row's takes pieces w, w + WPR, ...
+template <int D, int WPR>
+__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs p, const OwnArgs a, __nv_bfloat16* o, float* lse) {
   constexpr int V = D / 32;     // features a lane holds
-  griddep_wait();               // the decode kernel has ended, and it ends after attn_prefix
-  const int lane = threadIdx.x & 31;
-  const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);   // (b * Hq + h) * Tq + t = (b * Hkv + hkv) * R + rr
-  if (row >= (long)a.B * a.Hkv * p.R) return;
-  const int rr = (int)(row % p.R), bh = (int)(row / p.R), hkv = bh % a.Hkv, b = bh / a.Hkv;
-  const int pre = b / p.W, len = a.cache_lens[b], m = p.prefix_lens[pre];
-  if (len < 0 || len > a.S || m < 0 || m > p.Sp) return;        // reported by the kernels before
-  __nv_bfloat16* out = a.o + row * D + lane * V;
+  __shared__ float s_acc[8][D], s_m[8], s_l[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
+  const long row = (long)blockIdx.x * (8 / WPR) + warp / WPR;   // (b * Hq + h) * Tq + t = (b * Hkv + hkv) * R + rr
+  const bool in = row < (long)a.B * a.Hkv * p.R;
+  const int rr = (int)(row % p.R), bh = (int)(row / p.R), hkv = bh % a.Hkv, b = bh / a.Hkv, pre = b / p.W;
+  griddep_wait();               // the own-keys kernel has ended, and it ends after attn_prefix
+  const int len = in ? a.cache_lens[b] : -1, m = in ? p.prefix_lens[pre] : -1;
+  const bool valid = len >= 0 && len <= a.S && m >= 0 && m <= p.Sp;      // others: reported by the kernels before
   float acc[V] = {};
   float M = -INFINITY, L = 0.f;
-  if (len - a.Tq + rr % a.Tq >= 0) {
+  if (valid && len - a.Tq + rr % a.Tq >= 0) {
+    const int block = p.R <= 8 ? 8 : 16;
     const int gr = b % p.W * p.R + rr;
     const long hp = (long)pre * a.Hkv + hkv, pbase = (hp * p.Rp + gr) * p.slots;
-    const long u = (long)bh * a.nrb + rr / 16, obase = u * a.slots * a.rows_ws + rr % 16;
+    const long u = (long)bh * a.nrb + rr / block;
     const int np = m > 0 ? min(max(p.counts[hp * p.nrt + gr / kPrefixRows], 0), p.slots) : 0;
-    const int n = np + min(max(a.counts[u], 0), a.slots);
+    const int2 own = a.counts[u];
+    const int n = np + min(max(own.y, 0), a.warps);
+    const long obase = (long)own.x * a.rows_ws + rr % block;
     auto ml_of = [&](int s) { return s < np ? p.ws_ml[pbase + s] : a.ws_ml[obase + (long)(s - np) * a.rows_ws]; };
-    float2 ml = lane < n ? ml_of(lane) : make_float2(-INFINITY, 0.f);   // of the first 32 pieces
+    // this warp's pieces are part + WPR * i
+    const int mine = (n - part + WPR - 1) / WPR;
+    float2 ml = lane < mine ? ml_of(part + WPR * lane) : make_float2(-INFINITY, 0.f);   // of the first 32
     M = ml.x;
-    for (int s = 32 + lane; s < n; s += 32) M = fmaxf(M, ml_of(s).x);
+    for (int i = 32 + lane; i < mine; i += 32) M = fmaxf(M, ml_of(part + WPR * i).x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int s0 = 0; s0 < n; s0 += 32) {
-      if (s0 > 0) ml = s0 + lane < n ? ml_of(s0 + lane) : make_float2(-INFINITY, 0.f);
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+      if (i0 > 0) ml = i0 + lane < mine ? ml_of(part + WPR * (i0 + lane)) : make_float2(-INFINITY, 0.f);
       const float wl = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
       L = fmaf(ml.y, wl, L);
-      const int k1 = min(32, n - s0);
+      const int k1 = min(32, mine - i0);
 #pragma unroll 4
       for (int k = 0; k < k1; ++k) {
         const float wk = __shfl_sync(0xffffffffu, wl, k);
         if (wk == 0.f) continue;
-        const int s = s0 + k;
+        const int s = part + WPR * (i0 + k);
         const float* src = (s < np ? p.ws_o + (pbase + s) * D : a.ws_o + (obase + (long)(s - np) * a.rows_ws) * D) + lane * V;
         if constexpr (V == 4) {
           const float4 v = *reinterpret_cast<const float4*>(src);
@@ -638,17 +644,44 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs p, c
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const float inv = 1.f / L;
+    for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+  }
+  if constexpr (WPR > 1) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] *= inv;
+    for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = L;
+    }
+    __syncthreads();
+    if (part > 0) return;
+    float top = M;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) top = fmaxf(top, s_m[warp + w]);
+    if (top > -INFINITY) {
+      L = 0.f;
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) {
+        const float wk = ex2_approx(s_m[warp + w] - top);     // of a warp without pieces: 0, and so are its sums
+        L = fmaf(s_l[warp + w], wk, L);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(s_acc[warp + w][lane * V + k], wk, acc[k]);
+      }
+    }
+    M = top;
   }
+  if (!valid) return;
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;        // 0: a query without keys
+  __nv_bfloat16* out = o + row * D + lane * V;
   if constexpr (V == 4) {
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   } else {
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0], acc[1]);
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
   }
-  if (lane == 0) a.lse[row] = (M + __log2f(L)) * 0.69314718055994531f;   // a query without keys: -infinity
+  if (lane == 0) lse[row] = (M + __log2f(L)) * 0.69314718055994531f;   // a query without keys: -infinity
 }
 
 template <int D, bool PAGED>
@@ -677,12 +710,20 @@ cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const
   return a.table ? launch_prefix_dp<64, true>(k, v, a, stream) : launch_prefix_dp<64, false>(k, v, a, stream);
 }
 
-cudaError_t launch_prefix_merge(const PrefixArgs& p, const DecodeArgs& a, cudaStream_t stream) {
+template <int D>
+static cudaError_t launch_merge_d(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
   const long rows = (long)a.B * a.Hkv * p.R;
+  // few rows have many pieces each, and SMs to spare: four warps a row
+  if (rows <= 8 * 256)
+    return launch_programmatic(prefix_merge_kernel<D, 4>, dim3((unsigned)((rows + 1) / 2)), dim3(256), 0, stream, p, a, o, lse);
+  return launch_programmatic(prefix_merge_kernel<D, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, p, a, o, lse);
+}
+
+cudaError_t launch_prefix_merge(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
+  OwnArgs x = a;
+  x.warps = kOwnMaxWarps;
   prof_begin(kProfPrefixMerge, stream);
-  const dim3 grid((unsigned)((rows + 7) / 8));
-  const cudaError_t e = a.D == 128 ? launch_programmatic(prefix_merge_kernel<128>, grid, dim3(256), 0, stream, p, a)
-                                   : launch_programmatic(prefix_merge_kernel<64>, grid, dim3(256), 0, stream, p, a);
+  const cudaError_t e = a.D == 128 ? launch_merge_d<128>(p, x, o, lse, stream) : launch_merge_d<64>(p, x, o, lse, stream);
   prof_end(stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

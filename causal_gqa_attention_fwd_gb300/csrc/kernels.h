@@ -126,10 +126,6 @@ struct DecodeArgs {
   // boxes, no swizzle); K's scale is folded into scale_log2, V's applied to O
   int fp8;
   float v_scale;          // 1 for 16-bit caches
-  int min_len;            // shortest valid length: Tq, or 0 (queries at negative positions see no key)
-  // attention over a shared prefix: every unit leaves partials (also one that is not cut) and, in its first piece,
-  // how many; nullptr otherwise
-  int* counts;            // [units]
 };
 
 // k, v: dense maps over the caches ([B*Hkv, S, D], 64 x 128 boxes) or, paged,
@@ -137,11 +133,6 @@ struct DecodeArgs {
 // boxes); q: 2-D map over the query rows ([B*Hq*Tq, D], 64 x 16 boxes).
 cudaError_t launch_attn_decode(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const DecodeArgs& a,
                                int grid, cudaStream_t stream);
-
-// The partial kernel alone, as a programmatic dependent of the kernel before it in the stream, which must have passed
-// its own griddep_wait when it let dependents start (a.counts set: the merge is launch_prefix_merge's).
-cudaError_t launch_attn_decode_parts(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
-                                     const DecodeArgs& a, int grid, cudaStream_t stream);
 
 // Attention of a batch over prefixes that its rows share: prefix p (p < P) belongs to rows p*W .. p*W + W - 1.  The
 // Rp = W*R query rows (R = G*Tq a batch row) of a (prefix, K/V head) go in nrt blocks of 256; a (prefix, K/V head,
@@ -164,8 +155,33 @@ struct PrefixArgs {
 };
 cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& a, int D,
                                cudaStream_t stream);
+
+// The rows' own keys: the R = G*Tq query rows of a (batch row, K/V head) go in nrb blocks of 8 (R <= 8) or 16; a (batch
+// row, K/V head, block) is a unit.  Piece i of the stream (attn_own.cu) leaves rows_ws rows at i * rows_ws.
+constexpr int kOwnMaxWarps = 160 * 12;
+struct OwnArgs {
+  const __nv_bfloat16* q;   // [B, Hkv, R, D]
+  const int* cache_lens;    // [B] device
+  const int* block_table;   // [B, max_pages] device, nullptr for contiguous caches
+  float* ws_o;              // [(kOwnMaxWarps + units) * rows_ws, D]
+  float2* ws_ml;            // [(kOwnMaxWarps + units) * rows_ws] (max in log2 units, sum)
+  int2* counts;             // [units] (first piece, pieces)
+  int* status;
+  int B, Hkv, Tq, R, nrb, rows_ws, S, D;
+  int page_size, max_pages, num_pages;
+  int ctas, warps;          // CTAs of the launch, warps in them (set by it)
+  float scale_log2;
+};
+// A programmatic dependent of the prefix kernel, which must have passed its own griddep_wait when it lets dependents
+// start.  k, v: maps over the caches or pages with boxes of 64 features x own_box_rows().
+inline int own_box_rows(int D, int page_size) {   // page_size 0: contiguous
+  const int tile = D == 128 ? 16 : 32;
+  return page_size > 0 && page_size < tile ? page_size : tile;
+}
+cudaError_t launch_attn_own(const CUtensorMap& k, const CUtensorMap& v, const OwnArgs& a, cudaStream_t stream);
+
 // Joins the prefix's partials with those of the rows' own caches: O and LSE of every row.
-cudaError_t launch_prefix_merge(const PrefixArgs& p, const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream);
 
 // Kernel-level timing (opt-in instrumentation, api.cu): event pairs recorded
 // on the launch stream around each kernel.
@@ -187,7 +203,8 @@ enum ProfKind {
   kProfWeights = 14,
   kProfEvictSelect = 15,
   kProfEvictMove = 16,
-  kProfKinds = 17
+  kProfOwn = 17,
+  kProfKinds = 18
 };
 // Launch with programmatic stream serialization (see griddep_wait in
 // sm103.cuh): the kernel's CTAs may be scheduled, and run their set-up, while
