@@ -877,19 +877,24 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int Tq, int P, int Sp) {
   return p;
 }
 
-// The rows' own keys: blocks of query rows, and the units that follow.
+// The stream of units with few query rows: the rows' own keys, and the prefixes where `stream` (few rows share one).
 struct OwnPlan {
-  int R, nrb, rows_ws;
+  int R, block, nrb, nrbp, rows_ws;
+  bool stream;
   long units;
 };
 
-OwnPlan own_plan(int B, int Hq, int Hkv, int Tq) {
+OwnPlan own_plan(int B, int Hq, int Hkv, int Tq, int P, int Sp) {
   OwnPlan p{};
   p.R = Hq / Hkv * Tq;
-  const int block = p.R <= 8 ? 8 : 16;
-  p.nrb = (p.R + block - 1) / block;
-  p.rows_ws = p.R < block ? p.R : block;
-  p.units = (long)B * Hkv * p.nrb;
+  const int Rp = B / P * p.R;
+  p.stream = gqa::prefix_in_stream(Rp, P, Hkv, Sp);
+  const int most = p.stream ? Rp : p.R;
+  p.block = most <= 8 ? 8 : 16;
+  p.nrb = (p.R + p.block - 1) / p.block;
+  p.nrbp = p.stream ? (Rp + p.block - 1) / p.block : 0;
+  p.rows_ws = most < p.block ? most : p.block;
+  p.units = (long)B * Hkv * p.nrb + (long)P * Hkv * p.nrbp;
   return p;
 }
 
@@ -898,7 +903,8 @@ struct PrefixWs {
 };
 
 PrefixWs prefix_ws(const PrefixPlan& p, const OwnPlan& d, int P, int Hkv, int D) {
-  const size_t rows = (size_t)P * Hkv * p.Rp * p.slots, own = (size_t)(d.units + gqa::kOwnMaxWarps) * d.rows_ws;
+  const size_t rows = d.stream ? 0 : (size_t)P * Hkv * p.Rp * p.slots;
+  const size_t own = (size_t)(d.units + gqa::kOwnMaxWarps) * d.rows_ws;
   PrefixWs w{};
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -923,7 +929,7 @@ attn_status prefix_check(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, i
   if (B % P) return ATTN_ERR_SHAPE;
   if (B == 0 || Tq == 0) return ATTN_OK;
   // positions in the stream of the rows' own tiles
-  if (own_plan(B, Hq, Hkv, Tq).units > 0x7fffffffL / (S / 16 + 4L)) return ATTN_ERR_SHAPE;
+  if (own_plan(B, Hq, Hkv, Tq, P, Sp).units > 0x7fffffffL / ((S > Sp ? S : Sp) / 16 + 4L)) return ATTN_ERR_SHAPE;
   const PrefixPlan p = prefix_plan(B, Hq, Hkv, Tq, P, Sp);
   // block stream and ring indices
   if (p.units * ((Sp + 127L) / 128) > 0x3fffffffL || (long)P * Hkv > 0x7fffffffL) return ATTN_ERR_SHAPE;
@@ -932,8 +938,7 @@ attn_status prefix_check(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, i
 
 // Everything after the layout-specific checks.
 attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMap& pv, const int* prefix_lens,
-                          const int* prefix_table, int max_prefix_pages, const CUtensorMap& tk, const CUtensorMap& tv,
-                          const int* cache_lens, const int* block_table, int max_pages, int page_size, int num_pages,
+                          const int* prefix_table, int max_prefix_pages, const gqa::OwnMaps& maps, const int* cache_lens, const int* block_table, int max_pages, int page_size, int num_pages,
                           void* o, float* lse, void* workspace, int B, int Hq, int Hkv, int Tq, int P, int Sp, int S,
                           int D, float scale, void* stream) {
   attn_status st = check_arch();
@@ -942,7 +947,7 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   const int sms = sm_count();
   if (!status || sms < 1) return ATTN_ERR_CUDA;
   const PrefixPlan p = prefix_plan(B, Hq, Hkv, Tq, P, Sp);
-  const OwnPlan d = own_plan(B, Hq, Hkv, Tq);
+  const OwnPlan d = own_plan(B, Hq, Hkv, Tq, P, Sp);
   const PrefixWs w = prefix_ws(p, d, P, Hkv, D);
   char* ws = static_cast<char*>(workspace);
   const int ctas = sms < gqa::kDecodeMaxSlots ? sms : gqa::kDecodeMaxSlots;   // one a SM, as decode
@@ -976,7 +981,9 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   gqa::OwnArgs e{};
   e.q = a.q;
   e.cache_lens = cache_lens;
+  e.prefix_lens = prefix_lens;
   e.block_table = block_table;
+  e.prefix_table = prefix_table;
   e.ws_o = reinterpret_cast<float*>(ws + w.own_o);
   e.ws_ml = reinterpret_cast<float2*>(ws + w.own_ml);
   e.counts = reinterpret_cast<int2*>(ws + w.own_counts);
@@ -985,9 +992,16 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   e.Hkv = Hkv;
   e.Tq = Tq;
   e.R = d.R;
+  e.P = d.stream ? P : 0;
+  e.W = p.W;
   e.nrb = d.nrb;
+  e.nrbp = d.nrbp;
+  e.block = d.block;
   e.rows_ws = d.rows_ws;
   e.S = S;
+  e.Sp = Sp;
+  e.max_prefix_pages = max_prefix_pages;
+  e.beside = !d.stream;
   e.D = D;
   e.page_size = page_size;
   e.max_pages = max_pages;
@@ -995,8 +1009,8 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   e.ctas = ctas;
   e.scale_log2 = a.scale_log2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t err = gqa::launch_attn_prefix(pk, pv, a, D, s);
-  if (err == cudaSuccess) err = gqa::launch_attn_own(tk, tv, e, s);
+  cudaError_t err = d.stream ? cudaSuccess : gqa::launch_attn_prefix(pk, pv, a, D, s);
+  if (err == cudaSuccess) err = gqa::launch_attn_own(maps, e, s);
   if (err == cudaSuccess) err = gqa::launch_prefix_merge(a, e, static_cast<__nv_bfloat16*>(o), lse, s);
   return launch_status(err);
 }
@@ -1009,7 +1023,7 @@ attn_status prefix_check_pointers(const void* q, const void* k, const void* v, c
       (reinterpret_cast<uintptr_t>(prefix_lens) & 3u) || (reinterpret_cast<uintptr_t>(cache_lens) & 3u))
     return ATTN_ERR_ALIGN;
   const size_t need =
-      prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), own_plan(B, Hq, Hkv, Tq), P, Hkv, D).bytes;
+      prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), own_plan(B, Hq, Hkv, Tq, P, Sp), P, Hkv, D).bytes;
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return ATTN_ERR_WORKSPACE;
   return ATTN_OK;
 }
@@ -1020,7 +1034,7 @@ extern "C" {
 
 size_t attn_decode_prefix_workspace_size(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, int D) {
   if (prefix_check(B, Hq, Hkv, Tq, P, Sp, S, D) != ATTN_OK || B == 0 || Tq == 0) return 0;
-  return prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), own_plan(B, Hq, Hkv, Tq), P, Hkv, D).bytes;
+  return prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), own_plan(B, Hq, Hkv, Tq, P, Sp), P, Hkv, D).bytes;
 }
 
 attn_status attn_decode_prefix_fwd(const void* q, const void* k_prefix, const void* v_prefix, const int* prefix_lens,
@@ -1036,16 +1050,19 @@ attn_status attn_decode_prefix_fwd(const void* q, const void* k_prefix, const vo
   if (st != ATTN_OK) return st;
   if (Sp > 0 && (!k_prefix || !v_prefix)) return ATTN_ERR_NULL;
   if (!aligned16(k_prefix) || !aligned16(v_prefix)) return ATTN_ERR_ALIGN;
-  CUtensorMap tk, tv, pk, pv;
+  gqa::OwnMaps m;
   const int box = gqa::own_box_rows(D, 0);
-  if (!map_dense(&tk, k_cache, D, S, (long)B * Hkv, box) || !map_dense(&tv, v_cache, D, S, (long)B * Hkv, box))
+  if (!map_dense(&m.k, k_cache, D, S, (long)B * Hkv, box) || !map_dense(&m.v, v_cache, D, S, (long)B * Hkv, box))
     return ATTN_ERR_CUDA;
-  pk = tk;   // Sp = 0: no length is valid but 0, and nothing is loaded through them
-  pv = tv;
-  if (Sp > 0 && (!map_dense(&pk, k_prefix, D, Sp, (long)P * Hkv) || !map_dense(&pv, v_prefix, D, Sp, (long)P * Hkv)))
+  m.pk = m.k;   // Sp = 0: no length is valid but 0, and nothing is loaded through them
+  m.pv = m.v;
+  CUtensorMap pk = m.k, pv = m.v;
+  if (Sp > 0 && (!map_dense(&pk, k_prefix, D, Sp, (long)P * Hkv) || !map_dense(&pv, v_prefix, D, Sp, (long)P * Hkv) ||
+                 !map_dense(&m.pk, k_prefix, D, Sp, (long)P * Hkv, box) ||
+                 !map_dense(&m.pv, v_prefix, D, Sp, (long)P * Hkv, box)))
     return ATTN_ERR_CUDA;
-  return prefix_common(q, pk, pv, prefix_lens, nullptr, 0, tk, tv, cache_lens, nullptr, 0, 0, 0, o, lse, workspace, B, Hq,
-                       Hkv, Tq, P, Sp, S, D, scale, stream);
+  return prefix_common(q, pk, pv, prefix_lens, nullptr, 0, m, cache_lens, nullptr, 0, 0, 0, o, lse, workspace, B, Hq, Hkv,
+                       Tq, P, Sp, S, D, scale, stream);
 }
 
 attn_status attn_decode_paged_prefix_fwd(const void* q, const void* k_pages, const void* v_pages,
@@ -1071,13 +1088,16 @@ attn_status attn_decode_paged_prefix_fwd(const void* q, const void* k_pages, con
   if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(prefix_table) & 3u))
     return ATTN_ERR_ALIGN;
   const int pbox = page_size < 128 ? page_size : 128, box = gqa::own_box_rows(D, page_size);
-  CUtensorMap pk, pv, tk, tv;
+  CUtensorMap pk, pv;
+  gqa::OwnMaps m;
   if (!map_dense(&pk, k_pages, D, page_size, (long)num_pages * Hkv, pbox) ||
       !map_dense(&pv, v_pages, D, page_size, (long)num_pages * Hkv, pbox) ||
-      !map_dense(&tk, k_pages, D, page_size, (long)num_pages * Hkv, box) ||
-      !map_dense(&tv, v_pages, D, page_size, (long)num_pages * Hkv, box))
+      !map_dense(&m.k, k_pages, D, page_size, (long)num_pages * Hkv, box) ||
+      !map_dense(&m.v, v_pages, D, page_size, (long)num_pages * Hkv, box))
     return ATTN_ERR_CUDA;
-  return prefix_common(q, pk, pv, prefix_lens, Sp > 0 ? prefix_table : block_table, max_prefix_pages, tk, tv, cache_lens,
+  m.pk = m.k;
+  m.pv = m.v;
+  return prefix_common(q, pk, pv, prefix_lens, Sp > 0 ? prefix_table : block_table, max_prefix_pages, m, cache_lens,
                        block_table, max_pages, page_size, num_pages, o, lse, workspace, B, Hq, Hkv, Tq, P, (int)Sp,
                        (int)S, D, scale, stream);
 }

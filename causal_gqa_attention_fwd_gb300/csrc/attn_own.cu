@@ -1,6 +1,6 @@
-// attn_own.cu -- the rows' own keys in attention over a shared prefix, for
-// sm_103a: unnormalised partials (O, M, L) of cached attention over short,
-// ragged bf16 caches.
+// attn_own.cu -- the rows' own keys in attention over a shared prefix, and the
+// prefix itself where few rows share it, for sm_103a: unnormalised partials
+// (O, M, L) of cached attention of few query rows over ragged bf16 caches.
 //
 // A few query rows (G * Tq of a (batch row, K/V head)) meet each key once: the
 // stream of keys and values bounds it, and with rows of a few hundred keys what
@@ -63,19 +63,22 @@ __device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, uint32_t b
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A unit in the stream, and the warp's run of its tiles.
+// The stream's rows are the prefixes it holds (a.P of them, query rows of all their batch rows), then the batch rows.
+// A unit in it, and the warp's run of the unit's tiles.
 struct Run {
-  int b, k;          // batch row; unit within it (K/V head, row block)
+  int i, k;          // row of the stream; unit within it (K/V head, row block)
   int len, nb;       // the row's keys, tiles
   int P;             // stream position of the unit's first tile
   int t, te;         // tiles [t, te)
 };
 
 template <int KT>
-__device__ __forceinline__ int row_tiles(const OwnArgs& a, int b, int& len) {
-  len = a.cache_lens[b];
-  return len > 0 && len <= a.S ? (len + KT - 1) / KT : 0;
+__device__ __forceinline__ int row_tiles(const OwnArgs& a, int i, int& len) {
+  len = i < a.P ? a.prefix_lens[i] : a.cache_lens[i - a.P];
+  return len > 0 && len <= (i < a.P ? a.Sp : a.S) ? (len + KT - 1) / KT : 0;
 }
+
+__device__ __forceinline__ int blocks_of(const OwnArgs& a, int i) { return i < a.P ? a.nrbp : a.nrb; }
 
 // The next unit's run; te <= t: the share is done.
 template <int KT>
@@ -84,11 +87,11 @@ __device__ __forceinline__ void next_run(const OwnArgs& a, Run& u, int end) {
   u.t = 0;
   u.te = 0;
   if (u.P >= end) return;
-  if (++u.k == a.Hkv * a.nrb) {
+  if (++u.k == a.Hkv * blocks_of(a, u.i)) {
     u.k = 0;
     do {
-      ++u.b;
-      u.nb = row_tiles<KT>(a, u.b, u.len);
+      ++u.i;
+      u.nb = row_tiles<KT>(a, u.i, u.len);
     } while (u.nb == 0);
   }
   u.te = min(u.nb, end - u.P);
@@ -98,7 +101,8 @@ __device__ __forceinline__ void next_run(const OwnArgs& a, Run& u, int end) {
 
 template <int D, bool PAGED, int NT>
 __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
-    attn_own_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const OwnArgs a) {
+    attn_own_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_pk, const __grid_constant__ CUtensorMap tm_pv, const OwnArgs a) {
   using C = OwnCfg<D, NT>;
   constexpr int KT = C::KT, NB = D / 64, kSteps = D / 16, kMT = D / 16;
   extern __shared__ uint8_t smem_raw[];
@@ -106,9 +110,9 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
   __shared__ uint64_t s_full[C::kWarps][C::kStages];
   __shared__ int s_sum[C::kWarps], s_pre[C::kThreads], s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0), g = lane >> 2, tig = lane & 3;
-  const int upb = a.Hkv * a.nrb;
   Guard guard{&s_abort, a.status};
-  // Launched beside the prefix kernel, past whose own wait this grid starts: what the grids before wrote is there.
+  // Beside the prefix kernel, past whose own wait this grid starts, what the grids before wrote is there.
+  if (!a.beside) griddep_wait();
   griddep_launch();
   if (tid == 0) s_abort = 0;
   if (lane == 0) {
@@ -119,21 +123,21 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
   }
 
   // ------------------------------------------------ the warp's share: inclusive sums of the rows' stream positions
-  auto positions = [&](int b) {
+  const int rows = a.P + a.B;
+  auto positions = [&](int i) {
     int len;
-    const int nb = row_tiles<KT>(a, b, len);
-    if (len < 0 || len > a.S) atomicCAS(a.status, 0, kDevBadSeqlens);
-    return nb ? nb + kUnitCost : 0;
+    const int nb = row_tiles<KT>(a, i, len);
+    if (nb == 0 && len != 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+    return nb ? (nb + kUnitCost) * (a.Hkv * blocks_of(a, i)) : 0;
   };
   long total = 0;
-  if (a.B > C::kThreads) {     // more rows than threads: a pass for the total first
+  if (rows > C::kThreads) {     // more rows than threads: a pass for the total first
     int mine = 0;
-    for (int b = tid; b < a.B; b += C::kThreads) mine += positions(b);
+    for (int i = tid; i < rows; i += C::kThreads) mine += positions(i);
     mine = __reduce_add_sync(~0u, mine);
     if (lane == 0) s_sum[warp] = mine;
     __syncthreads();
     for (int w = 0; w < C::kWarps; ++w) total += s_sum[w];
-    total *= upb;
   }
   int Wn = 0, v0 = 0, v1 = 0, before = 0;
   const int gw = warp * gridDim.x + blockIdx.x;     // neighbouring shares go to different SMs
@@ -144,10 +148,10 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
       v1 = (int)((gw + 1) * total / Wn);
     }
   };
-  if (a.B > C::kThreads) take_share();
+  if (rows > C::kThreads) take_share();
   Run u{-1, 0, 0, 0, 0, 0, 0};
-  for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
-    int inc = b0 + tid < a.B ? positions(b0 + tid) : 0;
+  for (int i0 = 0; i0 < rows; i0 += C::kThreads) {
+    int inc = i0 + tid < rows ? positions(i0 + tid) : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int x = __shfl_up_sync(~0u, inc, d);
@@ -163,21 +167,21 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
     }
     s_pre[tid] = inc;
     __syncthreads();
-    if (a.B <= C::kThreads) {
-      total = (long)all * upb;
+    if (rows <= C::kThreads) {
+      total = all;
       take_share();
     }
-    if (v0 < v1 && u.b < 0 && v0 < (before + all) * upb) {
-      const int x = v0 - before * upb;      // the first row whose inclusive sum times upb is above
-      int lo = 0, hi = min(C::kThreads, a.B - b0) - 1;
+    if (v0 < v1 && u.i < 0 && v0 < before + all) {
+      const int x = v0 - before;      // the first row whose inclusive sum is above
+      int lo = 0, hi = min(C::kThreads, rows - i0) - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (s_pre[mid] * upb > x) hi = mid;
+        if (s_pre[mid] > x) hi = mid;
         else lo = mid + 1;
       }
-      u.b = b0 + lo;
-      u.nb = row_tiles<KT>(a, u.b, u.len);
-      const int P = (before + (lo ? s_pre[lo - 1] : 0)) * upb;
+      u.i = i0 + lo;
+      u.nb = row_tiles<KT>(a, u.i, u.len);
+      const int P = before + (lo ? s_pre[lo - 1] : 0);
       u.k = (v0 - P) / (u.nb + kUnitCost);
       u.P = P + u.k * (u.nb + kUnitCost) + kUnitCost;
       u.t = max(v0 - u.P, 0);
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
     before += all;
   }
 
-  if (u.b >= 0 && u.t < u.te) {
+  if (u.i >= 0 && u.t < u.te) {
     const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
     uint8_t* ring_p = smem + warp * (C::kStages * C::kStage);
     // ---------------------------------------------------------- loads
@@ -194,7 +198,8 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
     int page0 = -1, ids = -1, loaded = 0;      // paged: lane i holds the id of the row's page page0 + i
     auto issue = [&]() {
       if (ld.t >= ld.te) return;
-      const int st = loaded % C::kStages, k0 = ld.t * KT, hkv = ld.k / a.nrb;
+      const bool pre = ld.i < a.P;
+      const int st = loaded % C::kStages, k0 = ld.t * KT, row = pre ? ld.i : ld.i - a.P, hkv = ld.k / blocks_of(a, ld.i);
       uint8_t* dst = ring_p + st * C::kStage;
       uint64_t* bar = &s_full[warp][st];
       if constexpr (PAGED) {
@@ -204,7 +209,8 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
           page0 = k0 / psz;
           ids = -1;
           if (page0 + lane < used) {
-            const int e = a.block_table[(long)ld.b * a.max_pages + page0 + lane];
+            const int e = pre ? a.prefix_table[(long)row * a.max_prefix_pages + page0 + lane]
+                              : a.block_table[(long)row * a.max_pages + page0 + lane];
             if (e >= 0 && e < a.num_pages) ids = e;
             else atomicCAS(a.status, 0, kDevPages);
           }
@@ -224,10 +230,11 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
         }
       } else if (lane == 0) {
         mbar_expect_tx(bar, C::kStage);
+        const CUtensorMap *mk = pre ? &tm_pk : &tm_k, *mv = pre ? &tm_pv : &tm_v;
 #pragma unroll
         for (int x = 0; x < NB; ++x) {
-          tma_load_3d(dst + x * (KT * 128), &tm_k, bar, x * 64, k0, ld.b * a.Hkv + hkv);
-          tma_load_3d(dst + 4096 + x * (KT * 128), &tm_v, bar, x * 64, k0, ld.b * a.Hkv + hkv);
+          tma_load_3d(dst + x * (KT * 128), mk, bar, x * 64, k0, row * a.Hkv + hkv);
+          tma_load_3d(dst + 4096 + x * (KT * 128), mv, bar, x * 64, k0, row * a.Hkv + hkv);
         }
       }
       ++loaded;
@@ -240,15 +247,16 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
 
     // query fragments of a unit: rows 8 n + g of its block, features 16 s + 2 tig (+1, +8, +9)
     auto load_q = [&](const Run& r, uint32_t (*q)[NT][2]) {
-      const int hkv = r.k / a.nrb, r0 = r.k % a.nrb * (8 * NT);
+      const int nrb = blocks_of(a, r.i), hkv = r.k / nrb, r0 = r.k % nrb * (8 * NT);
+      const int b0 = r.i < a.P ? r.i * a.W : r.i - a.P, n_rows = r.i < a.P ? a.W * a.R : a.R;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int row = r0 + 8 * n + g;
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + (((long)r.b * a.Hkv + hkv) * a.R + row) * D) + tig;
+        const int row = r0 + 8 * n + g, b = b0 + row / a.R;
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + (((long)b * a.Hkv + hkv) * a.R + row % a.R) * D) + tig;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          q[s][n][0] = row < a.R ? __ldg(p + 8 * s) : 0u;
-          q[s][n][1] = row < a.R ? __ldg(p + 8 * s + 4) : 0u;
+          q[s][n][0] = row < n_rows ? __ldg(p + 8 * s) : 0u;
+          q[s][n][1] = row < n_rows ? __ldg(p + 8 * s + 4) : 0u;
         }
       }
     };
@@ -273,16 +281,17 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
         for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
       float mx[NT][2], l[NT][2];
       int lim[NT][2];                        // last key the row sees
-      const int r0 = u.k % a.nrb * (8 * NT);
+      const bool pre = u.i < a.P;
+      const int r0 = u.k % blocks_of(a, u.i) * (8 * NT), n_rows = pre ? a.W * a.R : a.R;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           mx[n][i] = -INFINITY;
           l[n][i] = 0.f;
-          lim[n][i] = u.len - a.Tq + (r0 + 8 * n + 2 * tig + i) % a.Tq;
+          lim[n][i] = pre ? u.len - 1 : u.len - a.Tq + (r0 + 8 * n + 2 * tig + i) % a.Tq;
         }
-      const int all_see = u.len - a.Tq;      // keys up to here are seen by every row
+      const int all_see = pre ? u.len - 1 : u.len - a.Tq;      // keys up to here are seen by every row
       for (int t = u.t; t < u.te; ++t) {
         const int st = done % C::kStages;
         ok = __all_sync(~0u, mbar_wait(&s_full[warp][st], (done / C::kStages) & 1, guard));
@@ -374,7 +383,7 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
       }
       if (!ok) break;
       // ------------------------------------------------------- the piece
-      const int unit = u.b * upb + u.k;
+      const int unit = (pre ? u.i * a.nrbp : a.P * a.nrbp + (u.i - a.P) * a.nrb) * a.Hkv + u.k;
       const long base = ((long)gw + unit) * a.rows_ws;
       if (u.t == 0 && lane == 0) {
         const int last = (int)((((long)u.P + u.nb) * Wn - 1) / total);     // the warp of the unit's last tile
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
           sum += __shfl_xor_sync(~0u, sum, 8);
           sum += __shfl_xor_sync(~0u, sum, 16);
           const int row = 8 * n + 2 * tig + i;
-          if (row < a.rows_ws && r0 + row < a.R) {
+          if (row < a.rows_ws && r0 + row < n_rows) {
             if (g == 0) a.ws_ml[base + row] = make_float2(mx[n][i], sum);
             float* o = a.ws_o + (base + row) * D + g;
 #pragma unroll
@@ -407,11 +416,11 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
     __syncwarp();
   }
   // the merge reads the prefix kernel's partials too: this grid does not end before that one has
-  griddep_wait();
+  if (a.beside) griddep_wait();
 }
 
 template <int D, bool PAGED, int NT>
-static cudaError_t launch_own_n(const CUtensorMap& k, const CUtensorMap& v, const OwnArgs& a, cudaStream_t stream) {
+static cudaError_t launch_own_n(const OwnMaps& m, const OwnArgs& a, cudaStream_t stream) {
   using C = OwnCfg<D, NT>;
   static bool attr_set[64] = {};
   int dev = 0;
@@ -426,20 +435,20 @@ static cudaError_t launch_own_n(const CUtensorMap& k, const CUtensorMap& v, cons
   x.warps = a.ctas * C::kWarps;
   prof_begin(kProfOwn, stream);
   const cudaError_t e = launch_programmatic(attn_own_kernel<D, PAGED, NT>, dim3(a.ctas), dim3(C::kThreads), C::kSmemBytes,
-                                            stream, k, v, x);
+                                            stream, m.k, m.v, m.pk, m.pv, x);
   prof_end(stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D>
-static cudaError_t launch_own_d(const CUtensorMap& k, const CUtensorMap& v, const OwnArgs& a, cudaStream_t stream) {
+static cudaError_t launch_own_d(const OwnMaps& m, const OwnArgs& a, cudaStream_t stream) {
   const bool paged = a.block_table != nullptr;
-  if (a.R <= 8) return paged ? launch_own_n<D, true, 1>(k, v, a, stream) : launch_own_n<D, false, 1>(k, v, a, stream);
-  return paged ? launch_own_n<D, true, 2>(k, v, a, stream) : launch_own_n<D, false, 2>(k, v, a, stream);
+  if (a.block == 8) return paged ? launch_own_n<D, true, 1>(m, a, stream) : launch_own_n<D, false, 1>(m, a, stream);
+  return paged ? launch_own_n<D, true, 2>(m, a, stream) : launch_own_n<D, false, 2>(m, a, stream);
 }
 
-cudaError_t launch_attn_own(const CUtensorMap& k, const CUtensorMap& v, const OwnArgs& a, cudaStream_t stream) {
-  return a.D == 128 ? launch_own_d<128>(k, v, a, stream) : launch_own_d<64>(k, v, a, stream);
+cudaError_t launch_attn_own(const OwnMaps& m, const OwnArgs& a, cudaStream_t stream) {
+  return a.D == 128 ? launch_own_d<128>(m, a, stream) : launch_own_d<64>(m, a, stream);
 }
 
 }  // namespace gqa

@@ -603,15 +603,30 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs p, c
   float acc[V] = {};
   float M = -INFINITY, L = 0.f;
   if (valid && len - a.Tq + rr % a.Tq >= 0) {
-    const int block = p.R <= 8 ? 8 : 16;
     const int gr = b % p.W * p.R + rr;
-    const long hp = (long)pre * a.Hkv + hkv, pbase = (hp * p.Rp + gr) * p.slots;
-    const long u = (long)bh * a.nrb + rr / block;
-    const int np = m > 0 ? min(max(p.counts[hp * p.nrt + gr / kPrefixRows], 0), p.slots) : 0;
-    const int2 own = a.counts[u];
+    const long hp = (long)pre * a.Hkv + hkv;
+    // the prefix's pieces: attn_prefix's, or pieces of the stream
+    const float* po;
+    const float2* pml;
+    int np = 0, pstep;
+    if (a.P == 0) {
+      pstep = 1;
+      const long at = (hp * p.Rp + gr) * p.slots;
+      po = p.ws_o + at * D;
+      pml = p.ws_ml + at;
+      if (m > 0) np = min(max(p.counts[hp * p.nrt + gr / kPrefixRows], 0), p.slots);
+    } else {
+      pstep = a.rows_ws;
+      const int2 c = m > 0 ? a.counts[hp * a.nrbp + gr / a.block] : make_int2(0, 0);
+      const long at = (long)c.x * a.rows_ws + gr % a.block;
+      po = a.ws_o + at * D;
+      pml = a.ws_ml + at;
+      np = min(max(c.y, 0), a.warps);
+    }
+    const int2 own = a.counts[(long)a.P * a.Hkv * a.nrbp + (long)bh * a.nrb + rr / a.block];
     const int n = np + min(max(own.y, 0), a.warps);
-    const long obase = (long)own.x * a.rows_ws + rr % block;
-    auto ml_of = [&](int s) { return s < np ? p.ws_ml[pbase + s] : a.ws_ml[obase + (long)(s - np) * a.rows_ws]; };
+    const long obase = (long)own.x * a.rows_ws + rr % a.block;
+    auto ml_of = [&](int s) { return s < np ? pml[(long)s * pstep] : a.ws_ml[obase + (long)(s - np) * a.rows_ws]; };
     // this warp's pieces are part + WPR * i
     const int mine = (n - part + WPR - 1) / WPR;
     float2 ml = lane < mine ? ml_of(part + WPR * lane) : make_float2(-INFINITY, 0.f);   // of the first 32
@@ -629,7 +644,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs p, c
         const float wk = __shfl_sync(0xffffffffu, wl, k);
         if (wk == 0.f) continue;
         const int s = part + WPR * (i0 + k);
-        const float* src = (s < np ? p.ws_o + (pbase + s) * D : a.ws_o + (obase + (long)(s - np) * a.rows_ws) * D) + lane * V;
+        const float* src = (s < np ? po + (long)s * pstep * D : a.ws_o + (obase + (long)(s - np) * a.rows_ws) * D) + lane * V;
         if constexpr (V == 4) {
           const float4 v = *reinterpret_cast<const float4*>(src);
           acc[0] = fmaf(v.x, wk, acc[0]);

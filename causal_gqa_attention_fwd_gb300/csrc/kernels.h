@@ -6,6 +6,9 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#ifndef GQA_STREAM_ROWS
+#define GQA_STREAM_ROWS 16
+#endif
 namespace gqa {
 
 // Forward.  Dense layout: Q,O [B,Hq,T,D], K,V [B,Hkv,T,D], LSE [B,Hq,T]
@@ -156,29 +159,37 @@ struct PrefixArgs {
 cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& a, int D,
                                cudaStream_t stream);
 
-// The rows' own keys: the R = G*Tq query rows of a (batch row, K/V head) go in nrb blocks of 8 (R <= 8) or 16; a (batch
-// row, K/V head, block) is a unit.  Piece i of the stream (attn_own.cu) leaves rows_ws rows at i * rows_ws.
+// Few query rows a key: the rows' own keys, R = G*Tq query rows a (batch row, K/V head), and, where few rows share a
+// prefix (P > 0), the prefixes, W*R query rows a (prefix, K/V head).  They go in nrb (nrbp) blocks of `block` rows; a
+// (row or prefix, K/V head, block) is a unit, the prefixes' units first.  Piece i of the stream (attn_own.cu) leaves
+// rows_ws rows at i * rows_ws.
 constexpr int kOwnMaxWarps = 160 * 12;
 struct OwnArgs {
   const __nv_bfloat16* q;   // [B, Hkv, R, D]
-  const int* cache_lens;    // [B] device
-  const int* block_table;   // [B, max_pages] device, nullptr for contiguous caches
+  const int *cache_lens, *prefix_lens;     // [B], [P] device
+  const int *block_table, *prefix_table;   // [B, max_pages], [P, max_prefix_pages] device, nullptr for contiguous caches
   float* ws_o;              // [(kOwnMaxWarps + units) * rows_ws, D]
   float2* ws_ml;            // [(kOwnMaxWarps + units) * rows_ws] (max in log2 units, sum)
   int2* counts;             // [units] (first piece, pieces)
   int* status;
-  int B, Hkv, Tq, R, nrb, rows_ws, S, D;
-  int page_size, max_pages, num_pages;
+  int B, P, W, Hkv, Tq, R, nrb, nrbp, block, rows_ws, S, Sp, D;
+  int page_size, max_pages, max_prefix_pages, num_pages;
   int ctas, warps;          // CTAs of the launch, warps in them (set by it)
+  int beside;               // launched as the prefix kernel's programmatic dependent, which passed its own griddep_wait
+                            // when it let dependents start, and runs beside it
   float scale_log2;
 };
-// A programmatic dependent of the prefix kernel, which must have passed its own griddep_wait when it lets dependents
-// start.  k, v: maps over the caches or pages with boxes of 64 features x own_box_rows().
+// Maps over the caches or pages with boxes of 64 features x own_box_rows(); pk, pv: of contiguous prefixes.
+struct OwnMaps {
+  CUtensorMap k, v, pk, pv;
+};
+// Whether prefixes of Sp keys, Rp query rows each, go into the stream.
+inline bool prefix_in_stream(int Rp, int P, int Hkv, int Sp) { return Rp <= GQA_STREAM_ROWS; }
 inline int own_box_rows(int D, int page_size) {   // page_size 0: contiguous
   const int tile = D == 128 ? 16 : 32;
   return page_size > 0 && page_size < tile ? page_size : tile;
 }
-cudaError_t launch_attn_own(const CUtensorMap& k, const CUtensorMap& v, const OwnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_own(const OwnMaps& m, const OwnArgs& a, cudaStream_t stream);
 
 // Joins the prefix's partials with those of the rows' own caches: O and LSE of every row.
 cudaError_t launch_prefix_merge(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream);

@@ -66,6 +66,8 @@ def test_workspace_covers_every_cut(lib):
         outer = nrt // width
         own = lib.attn_decode_prefix_workspace_size(B, Hkv * G, Hkv, Tq, P, 0, 128, 64)
         size = lib.attn_decode_prefix_workspace_size(B, Hkv * G, Hkv, Tq, P, Sp, 128, 64)
+        if size == own:         # few rows: the prefix's pieces are the stream's, which needs no slots
+            continue
         slots = (size - own) // (P * Hkv * Rp * (64 * 4 + 8))                   # rounded sections: at most one too few
         ctas = r.choice([152, 148, 132])
         nb = [-(-m // 128) for m in (r.choice([0, Sp, r.randint(0, Sp)]) for _ in range(P))]
