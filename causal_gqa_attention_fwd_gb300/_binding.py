@@ -78,7 +78,7 @@ SIGNATURES = {
 
 PROFILE_KINDS = {"attn_fwd": 0, "bwd_pre": 1, "bwd_dkdv": 2, "decode": 4, "decode_merge": 5, "bwd_dq": 6,
                  "cache_plan": 7, "rope": 8, "rope_table": 9, "cache_append": 10, "cache_gather": 11,
-                 "prefix": 12, "prefix_merge": 13, "cache_weights": 14, "evict_select": 15, "evict_move": 16, "own_keys": 17}
+                 "prefix": 12, "prefix_merge": 13, "cache_weights": 14, "cache_evict": 15, "own_keys": 16}
 
 _lib = None
 

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(384, 1)
   __shared__ PreBarriers bars;
   __shared__ Walk s_walk;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // the same in a warp, told so
   Guard guard{&bars.abort, a.status};
 
   if (threadIdx.x == 0) {

@@ -13,12 +13,12 @@
 //   the row's largest feature.  One lane group adds up a key's weight in a
 //   fixed order: the same call gives the same bits.
 //
-// evict_select   one CTA a (row, K/V head): the budget-th largest weight by
-//   radix selection over the weights' bits, then the kept positions in order.
-// evict_move     the kept rows of every plane to the front.  Row i comes from
-//   position src_i >= i, and src grows, so going up in chunks a chunk's rows
-//   are read before any is overwritten; planes and column slices of a row are
-//   independent of each other and go to CTAs of their own.
+// evict  a cluster of CTAs a (row, K/V head): each keeps a run of the weights in
+//   shared memory; the budget-th largest by radix selection over the weights'
+//   bits (11, 11, 10, histograms added up through distributed shared memory),
+//   then the kept positions in order, then the rows of every plane to the front.
+//   Row i comes from position src_i >= i, and src grows, so going up in chunks a
+//   chunk's rows are read before any is overwritten.
 #include <cuda_fp16.h>
 
 #include "cache_ops.h"
@@ -249,196 +249,396 @@ cudaError_t launch_cache_weights(const WeightsArgs& a, CacheFmt fmt, int sms, cu
 
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kEvThreads = 512;      // two CTAs an SM at 64 registers
+constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kBins = 2048;          // of a pass over 11 bits (the last: 10)
+constexpr int kMoveRows = 6;         // rows a thread has parts of on the way between reading and writing
+constexpr int kPlaceBytes = kMoveRows * kEvThreads * 16;
+constexpr int kKeyBytes = 80 << 10;  // weights a CTA keeps in shared memory; a longer share is read again each pass
+constexpr int kAlone = 8192;         // positions up to which each CTA selects by itself (weights and list in 64 KB)
 
-// Whole numbers in the weights' order: NaN above all, -0 = 0.
+// Whole numbers in the weights' order: NaN above all, -0 = 0; 0 is below all of them.
 __device__ __forceinline__ uint32_t order_of(float w) {
   if (w != w) return 0xffffffffu;
   const uint32_t u = __float_as_uint(w + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ int s_hist[256];
-  __shared__ int s_gt[32], s_eq[32];
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+__device__ __forceinline__ int4 peer_int4(const void* p, int rank) {
+  int4 v;
+  asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+               "ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [a];\n\t}"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem_u32(p)), "r"(rank)
+               : "memory");
+  return v;
+}
+
+// Where position j of (row b, head h) is: the number of its slot row in a plane, -1 in a page outside the pool.
+struct Slots {
+  const int* table;      // of row b, nullptr: contiguous
+  int num_pages, page_size, b;
+  unsigned mul, shift;   // j / page_size = umulhi(j, mul) >> shift, page_size > 1
+  long heads, h;
+  __device__ __forceinline__ long operator()(int j) const {
+    int page = b, r = j;
+    if (table) {
+      const int i = page_size == 1 ? j : (int)(__umulhi((unsigned)j, mul) >> shift);
+      r = j - i * page_size;
+      page = table[i];
+      if (page < 0 || page >= num_pages) return -1;
+    }
+    return ((long)page * heads + h) * page_size + r;
+  }
+};
+
+// A thread's part of every row that it moves: 16, 8 or 4 bytes of one plane, by way of its place in shared memory.
+struct Part {
+  uint8_t* base;      // of the plane, at the part
+  int row_bytes, size;
+  __device__ __forceinline__ void load(uint32_t to, long slot) const {
+    const uint8_t* p = base + slot * row_bytes;
+    if (size == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+    else if (size == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(p) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p) : "memory");
+  }
+  __device__ __forceinline__ void store(const uint4* from, long slot) const {
+    uint8_t* p = base + slot * row_bytes;
+    if (size == 16) *reinterpret_cast<uint4*>(p) = *from;
+    else if (size == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(from);
+    else *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(from);
+  }
+};
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Moves the rows list[d] -> d, d in [first, budget), of every plane.  A thread has one part of a row (a row's parts of all
+// planes lie on neighbouring threads), kMoveRows of them on the way at a time.  Row d may be written once whatever is kept
+// of position d has been read, that is all rows i with list[i] <= d.  So the rows go in phases [c0, c1): if list[c0] lies
+// further behind c0 than the threads' places reach, all rows up to position list[c0] are free to go one by one, for every
+// source in front of that position belongs to an earlier phase; otherwise as many as there are places are read before any
+// is written.
+__device__ __forceinline__ void move_rows(const EvictArgs& a, const Slots& slot_of, const int* list, uint4* places, int rank,
+                                          int ranks) {
+  // the first row that moves: list[d] - d never falls
+  int d_lo = a.first, d_hi = a.budget;
+  while (d_lo < d_hi) {
+    const int mid = (d_lo + d_hi) >> 1;
+    if (list[mid] > mid) d_hi = mid;
+    else d_lo = mid + 1;
+  }
+  for (int p0 = 0; p0 < a.parts; p0 += kEvThreads) {     // more parts than threads: some of each row's at a time
+    const int ppr = min(a.parts - p0, kEvThreads), rpi = kEvThreads / ppr, sub = threadIdx.x / ppr;
+    Part part{nullptr, 0, 0};
+    int q = p0 + threadIdx.x % ppr;
+    for (int i = 0; i < a.n_planes; ++i) {
+      const EvictPlane& pl = a.planes[i];
+      const int size = pl.row_bytes % 16 == 0 ? 16 : pl.row_bytes % 8 == 0 ? 8 : 4, n = pl.row_bytes / size;
+      if (q >= 0 && q < n) part = Part{static_cast<uint8_t*>(pl.p) + q * size, pl.row_bytes, size};
+      q -= n;
+    }
+    const int step = ranks * rpi, hold = step * kMoveRows;
+    uint4* mine = places + threadIdx.x;                  // place u: kEvThreads further on
+    auto source = [&](int d, int c1) { return sub < rpi && d < c1 ? list[d] : -1; };
+    auto read = [&](int u, int src) {
+      const long s = src >= 0 ? slot_of(src) : -1;
+      if (s >= 0) part.load(smem_u32(mine + u * kEvThreads), s);
+      copies_commit();
+      return s >= 0;
+    };
+    auto write = [&](int u, int d) {
+      const long t = slot_of(d);
+      if (t >= 0) part.store(mine + u * kEvThreads, t);
+    };
+    for (int c0 = d_lo; c0 < a.budget;) {
+      const int free_to = min(list[c0], a.budget);
+      const bool held = free_to < c0 + hold && free_to < a.budget;
+      const int c1 = held ? min(c0 + hold, a.budget) : free_to;
+      int d = c0 + rank * rpi + sub, src[kMoveRows];
+      unsigned go = 0;
+#pragma unroll
+      for (int u = 0; u < kMoveRows; ++u) src[u] = source(d + u * step, c1);
+#pragma unroll
+      for (int u = 0; u < kMoveRows; ++u) go |= (unsigned)read(u, src[u]) << u;
+      if (held) {
+        copies_wait<0>();
+        cluster_sync();
+#pragma unroll
+        for (int u = 0; u < kMoveRows; ++u)
+          if (go >> u & 1u) write(u, d + u * step);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kMoveRows; ++u) src[u] = source(d + hold + u * step, c1);
+        while (go) {
+          unsigned next = 0;
+#pragma unroll
+          for (int u = 0; u < kMoveRows; ++u) {
+            copies_wait<kMoveRows - 1>();                 // the oldest has landed
+            if (go >> u & 1u) write(u, d + u * step);
+            next |= (unsigned)read(u, src[u]) << u;
+            src[u] = source(d + 2 * hold + u * step, c1);
+          }
+          d += hold;
+          go = next;
+        }
+        copies_wait<0>();
+        if (c1 < a.budget) cluster_sync();   // the phase's rows are read before later ones are written over them
+      }
+      c0 = c1;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictArgs a) {
+  extern __shared__ __align__(16) uint32_t s_keys[];   // order_of this CTA's share of the weights
+  __shared__ __align__(16) int s_hist[3][kBins];
+  __shared__ __align__(16) int s_coarse[3][kEvWarps];  // sums over 128 bins
+  __shared__ int s_gt[kEvWarps], s_eq[kEvWarps];
+  __shared__ __align__(16) int s_tot[4];               // the CTA's keys above the threshold, and equal to it
   __shared__ uint32_t s_pre;
-  __shared__ int s_need;
+  __shared__ int s_need, s_all;
+  const int ranks = a.cluster, rank = blockIdx.x % ranks, unit = blockIdx.x / ranks, b = unit / a.Hkv, h = unit % a.Hkv;
+  // the warp's number told to be the same in all lanes: votes and shuffles under conditions on it take 100 ns each otherwise
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   griddep_wait();
   griddep_launch();
-  const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n = a.cache_lens[b];
-  int* kept = a.kept + (long)blockIdx.x * a.budget;
+  const int n = __shfl_sync(~0u, a.cache_lens[b], 0);
+  int* kept = a.kept + (long)unit * a.budget;
   const bool valid = n >= 0 && n <= a.S;
-  if (h == 0 && tid == 0) {
+  if (h == 0 && rank == 0 && tid == 0) {
     if (!valid) atomicCAS(a.status, 0, kDevBadSeqlens);
     a.lens_out[b] = valid ? min(n, a.budget) : n;
   }
-  if (!valid || n <= a.budget) {
-    for (int i = tid; i < a.budget; i += kSelThreads) kept[i] = valid && i < n ? i : -1;
+  if (!valid || n <= a.budget) {                        // the same in the whole cluster
+    for (int i = rank * kEvThreads + tid; i < a.budget; i += ranks * kEvThreads) kept[i] = valid && i < n ? i : -1;
     return;
   }
-  // n > budget >= first + recent: of the positions [lo, hi) the `need` largest are kept
-  const int lo = a.first, hi = n - a.recent;
+  // n > budget >= first + recent: of the positions [first, n - recent) the `need` largest are kept.  Each CTA selects
+  // among all of them by itself, or (a.shared_select) the cluster together, a CTA a run, so that the runs follow one
+  // another in the list.
+  const int sr = a.shared_select ? rank : 0, srs = a.shared_select ? ranks : 1;
+  const int m = n - a.recent - a.first, run = (m + srs - 1) / srs;
+  const int lo = a.first + min(sr * run, m), hi = a.first + min((sr + 1) * run, m);
   int need = a.budget - a.first - a.recent;
+  const bool cached = run * 4 <= a.key_bytes;
+  // shared memory: the weights, in whose place rows are on the way later; the list
+  int* list = a.shared_select ? kept : reinterpret_cast<int*>(s_keys) + max(a.key_bytes, kPlaceBytes) / 4;
   bool bad = false;
-  auto key = [&](int j) {
-    const int page = page_of(a.block_table, a.max_pages, a.num_pages, b, j / a.page_size);
-    bad |= page < 0;
-    return page < 0 ? 0u : order_of(a.weights[((long)page * a.Hkv + h) * a.page_size + j % a.page_size]);
+  const Slots slot_of{a.block_table ? a.block_table + (long)b * a.max_pages : nullptr, a.num_pages, a.page_size, b,
+                      a.div_mul, a.div_shift, a.Hkv, h};
+  auto load_key = [&](int j) {
+    const long s = slot_of(j);
+    bad |= s < 0;
+    return s < 0 ? 0u : order_of(a.weights[s]);
   };
-  uint32_t pre = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) s_hist[tid] = 0;
+  auto key = [&](int j) { return cached ? s_keys[j - lo] : load_key(j); };
+  uint32_t thr = 0xffffffffu, mask = 0xffffffffu;       // kept: (key & mask) > thr, and the first `need` equal to it
+  if (need > 0) {
+    for (int i = tid; i < 3 * kBins / 4; i += kEvThreads) reinterpret_cast<int4*>(&s_hist[0][0])[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      const uint32_t k = key(j);
-      if ((k & above) == pre) atomicAdd(&s_hist[(k >> shift) & 255u], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // bins 8 lane .. 8 lane + 7; the bin where the count from the top reaches `need`
-      int c[8], t = 0;
+    thr = mask = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t bins = pass == 2 ? 1023u : 2047u;
+      int* hist = s_hist[pass];
+      if (pass == 0 && cached) {
+        for (int j0 = lo + tid; j0 < hi; j0 += 8 * kEvThreads) {
+          uint32_t k[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t += c[i] = s_hist[8 * lane + i];
-      int above_lane = t;     // keys in bins of this and higher lanes
+          for (int u = 0; u < 8; ++u) k[u] = j0 + u * kEvThreads < hi ? load_key(j0 + u * kEvThreads) : 0u;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_down_sync(0xffffffffu, above_lane, o);
-        if (lane + o < 32) above_lane += y;
-      }
-      int from = above_lane - t;
-#pragma unroll
-      for (int i = 7; i >= 0; --i) {
-        if (from < need && need <= from + c[i]) {
-          s_pre = pre | (uint32_t)(8 * lane + i) << shift;
-          s_need = need - from;
+          for (int u = 0; u < 8; ++u)
+            if (j0 + u * kEvThreads < hi) {
+              s_keys[j0 + u * kEvThreads - lo] = k[u];
+              atomicAdd(&hist[k[u] >> shift], 1);
+            }
         }
-        from += c[i];
+      } else if (cached) {
+#pragma unroll 8
+        for (int i = tid; i < hi - lo; i += kEvThreads) {
+          const uint32_t k = s_keys[i];
+          if ((k & mask) == thr) atomicAdd(&hist[(k >> shift) & bins], 1);
+        }
+      } else {
+        for (int j = lo + tid; j < hi; j += kEvThreads) {
+          const uint32_t k = load_key(j);
+          if ((k & mask) == thr) atomicAdd(&hist[(k >> shift) & bins], 1);
+        }
       }
-      if (need == 0 && lane == 0) {
-        s_pre = 0xffffffffu;
-        s_need = 0;
+      __syncthreads();
+      const int4 own = *reinterpret_cast<const int4*>(&hist[4 * tid]);
+      const int sum = __reduce_add_sync(0xffffffffu, own.x + own.y + own.z + own.w);
+      if (lane == 0) s_coarse[pass][warp] = sum;
+      if (srs > 1) cluster_sync();
+      else __syncthreads();
+      if (warp == 0) {
+        // Of 16 x 128 bins, from above until `need` keys are reached: the sums of 128, then the bins of one of them.
+        // Lane 4 r + k has rank r's sums 4 k .. 4 k + 3, then all ranks' together.
+        int4 c = make_int4(0, 0, 0, 0);
+        if (lane / 4 < srs) c = srs > 1 ? peer_int4(&s_coarse[pass][4 * (lane & 3)], lane / 4)
+                                        : *reinterpret_cast<const int4*>(&s_coarse[pass][4 * (lane & 3)]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          c.x += __shfl_xor_sync(0xffffffffu, c.x, o);
+          c.y += __shfl_xor_sync(0xffffffffu, c.y, o);
+          c.z += __shfl_xor_sync(0xffffffffu, c.z, o);
+          c.w += __shfl_xor_sync(0xffffffffu, c.w, o);
+        }
+        const int t = c.x + c.y + c.z + c.w;
+        int from = 0;
+#pragma unroll
+        for (int k = 1; k < 4; ++k) {
+          const int y = __shfl_sync(0xffffffffu, t, k);
+          if (k > (lane & 3)) from += y;
+        }
+        int hit = -1, base = 0;
+        const int cc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          if (from < need && need <= from + cc[i]) hit = 4 * (lane & 3) + i, base = from;
+          from += cc[i];
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, hit >= 0)) - 1;
+        hit = __shfl_sync(0xffffffffu, hit, src);
+        base = __shfl_sync(0xffffffffu, base, src);
+        const int* fine = &hist[128 * hit + 4 * lane];
+        int4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          v[r] = r >= srs ? make_int4(0, 0, 0, 0) : srs > 1 ? peer_int4(fine, r) : *reinterpret_cast<const int4*>(fine);
+        int f[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < 8; ++r) f[0] += v[r].x, f[1] += v[r].y, f[2] += v[r].z, f[3] += v[r].w;
+        const int mine = f[0] + f[1] + f[2] + f[3];
+        int above = mine;                               // keys in bins of this and higher lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_down_sync(0xffffffffu, above, o);
+          if (lane + o < 32) above += y;
+        }
+        from = base + above - mine;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          if (from < need && need <= from + f[i]) {
+            s_pre = thr | (uint32_t)(128 * hit + 4 * lane + i) << shift;
+            s_need = need - from;
+            s_all = need - from == f[i];
+          }
+          from += f[i];
+        }
       }
+      __syncthreads();
+      thr = s_pre;
+      need = s_need;
+      mask |= bins << shift;
+      if (s_all) break;                                 // the whole bin is kept: its keys need no order
+      __syncthreads();
     }
-    __syncthreads();
-    pre = s_pre;
-    need = s_need;
-    if (need == 0) break;
   }
-  // kept: keys above `pre`, and the first `need` equal to it.  A warp takes a run of positions: count, then write.
-  const bool none = a.budget == a.first + a.recent;
-  const int run = ((hi - lo + 31) / 32 + 31) & ~31, w0 = lo + warp * run, w1 = min(w0 + run, hi);
+  // Count, then write: a warp takes a run of the CTA's.
+  const bool any = a.budget > a.first + a.recent;
+  const int wrun = ((hi - lo + kEvWarps - 1) / kEvWarps + 31) & ~31;
+  const int w0 = min(lo + warp * wrun, hi), w1 = min(w0 + wrun, hi);
   int gt = 0, eq = 0;
-  for (int j0 = w0; j0 < w1; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t k = j < w1 ? key(j) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, j < w1 && !none && k > pre));
-    eq += __popc(__ballot_sync(0xffffffffu, j < w1 && !none && k == pre));
+  if (any) {
+#pragma unroll 4
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+      const int j = j0 + lane;
+      const uint32_t k = j < w1 ? key(j) & mask : 0u;
+      gt += j < w1 && k > thr;
+      eq += j < w1 && k == thr;
+    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
   }
   if (lane == 0) {
     s_gt[warp] = gt;
     s_eq[warp] = eq;
   }
   __syncthreads();
-  gt = eq = 0;
-  for (int i = 0; i < warp; ++i) {
-    gt += s_gt[i];
-    eq += s_eq[i];
+  if (srs > 1) {
+    if (warp == 0) {
+      const int g = __reduce_add_sync(0xffffffffu, lane < kEvWarps ? s_gt[lane] : 0);
+      const int e = __reduce_add_sync(0xffffffffu, lane < kEvWarps ? s_eq[lane] : 0);
+      if (lane == 0) s_tot[0] = g, s_tot[1] = e;
+    }
+    cluster_sync();
   }
-  for (int j0 = w0; j0 < w1; j0 += 32) {
+  // what lies before this warp's run: lane r adds up rank r's, lane 8 + i warp i's
+  gt = eq = 0;
+  if (lane < sr) {
+    const int4 v = peer_int4(s_tot, lane);
+    gt = v.x, eq = v.y;
+  } else if (lane >= 8 && lane - 8 < warp) {
+    gt = s_gt[lane - 8], eq = s_eq[lane - 8];
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  for (int j0 = w0; j0 < w1 && any; j0 += 32) {
     const int j = j0 + lane;
-    const uint32_t k = j < w1 ? key(j) : 0u;
-    const unsigned bg = __ballot_sync(0xffffffffu, j < w1 && !none && k > pre);
-    const unsigned be = __ballot_sync(0xffffffffu, j < w1 && !none && k == pre);
+    const uint32_t k = j < w1 ? key(j) & mask : 0u;
+    const unsigned bg = __ballot_sync(0xffffffffu, j < w1 && k > thr), be = __ballot_sync(0xffffffffu, j < w1 && k == thr);
     const unsigned below = (1u << lane) - 1u;
     const int g = gt + __popc(bg & below), e = eq + __popc(be & below);
-    if ((bg >> lane & 1u) || ((be >> lane & 1u) && e < need)) kept[a.first + g + min(e, need)] = j;
+    if ((bg >> lane & 1u) || ((be >> lane & 1u) && e < need)) list[a.first + g + min(e, need)] = j;
     gt += __popc(bg);
     eq += __popc(be);
   }
-  for (int i = tid; i < a.first; i += kSelThreads) kept[i] = i;
-  for (int i = tid; i < a.recent; i += kSelThreads) kept[a.budget - a.recent + i] = n - a.recent + i;
+  for (int i = sr * kEvThreads + tid; i < a.first; i += srs * kEvThreads) list[i] = i;
+  for (int i = sr * kEvThreads + tid; i < a.recent; i += srs * kEvThreads) list[a.budget - a.recent + i] = n - a.recent + i;
   if (bad) atomicCAS(a.status, 0, kDevBadPage);
-}
-
-constexpr int kMoveThreads = 256, kMoveRows = 4;   // rows a thread moves a piece of at once
-
-template <typename V>
-__device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictPlane& pl, int slice, int b, int h) {
-  const int tpr = pl.slice_bytes / (int)sizeof(V), rpi = kMoveThreads / tpr;
-  const int sub = threadIdx.x / tpr;
-  const bool active = sub < rpi;
-  const long col = (long)slice * pl.slice_bytes + (threadIdx.x % tpr) * (long)sizeof(V);
-  const int* kept = a.kept + ((long)b * a.Hkv + h) * a.budget;
-  uint8_t* base = static_cast<uint8_t*>(pl.p) + col;
-  auto at = [&](int j) -> V* {
-    const int page = page_of(a.block_table, a.max_pages, a.num_pages, b, j / a.page_size);
-    return page < 0 ? nullptr
-                    : reinterpret_cast<V*>(base + (((long)page * a.Hkv + h) * a.page_size + j % a.page_size) * pl.row_bytes);
-  };
-  for (int c0 = a.first; c0 < a.budget; c0 += rpi * kMoveRows) {
-    V v[kMoveRows];
-    bool go[kMoveRows];
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int d = c0 + u * rpi + sub;
-      go[u] = false;
-      if (active && d < a.budget) {
-        const int src = kept[d];
-        const V* s = src > d ? at(src) : nullptr;
-        if (s) {
-          v[u] = *s;
-          go[u] = true;
-        }
-      }
-    }
-    __syncthreads();      // the chunk's rows are read before any of them is overwritten
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      if (!go[u]) continue;
-      V* d = at(c0 + u * rpi + sub);
-      if (d) *d = v[u];
-    }
-  }
-}
-
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
-  griddep_wait();
-  griddep_launch();
-  const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
-  const int n = a.cache_lens[b];
-  if (n <= a.budget || n > a.S) return;
-  int slice = blockIdx.y, i = 0;
-  while (slice >= a.planes[i].slices) slice -= a.planes[i++].slices;
-  const EvictPlane& pl = a.planes[i];
-  if (pl.piece == 16) move_rows<uint4>(a, pl, slice, b, h);
-  else if (pl.piece == 8) move_rows<uint2>(a, pl, slice, b, h);
-  else move_rows<uint32_t>(a, pl, slice, b, h);
+  // the list is written, and every weight is read (and every peer's shared memory), before rows move
+  cluster_sync();
+  if (!a.shared_select)
+    for (int i = rank * kEvThreads + tid; i < a.budget; i += ranks * kEvThreads) kept[i] = list[i];
+  move_rows(a, slot_of, list, reinterpret_cast<uint4*>(s_keys), rank, ranks);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_evict(EvictArgs a, cudaStream_t stream) {
-  int slices = 0;
-  for (int i = 0; i < a.n_planes; ++i) {
-    EvictPlane& p = a.planes[i];
-    p.piece = p.row_bytes % 16 == 0 ? 16 : p.row_bytes % 8 == 0 ? 8 : 4;
-    const int pieces = p.row_bytes / p.piece;
-    int t = 1;                                   // pieces of a row that a CTA moves: at most 8
-    for (int d = 1; d <= 8; ++d)
-      if (pieces % d == 0) t = d;
-    p.slice_bytes = t * p.piece;
-    p.slices = pieces / t;
-    slices += p.slices;
+  const long units = (long)a.B * a.Hkv;
+  // a cluster a unit, as large as leaves all CTAs resident (two an SM) and 256 positions a CTA
+  a.cluster = 8;
+  while (a.cluster > 1 && (units * a.cluster > 304 || a.S < 256L * a.cluster)) a.cluster /= 2;
+  a.shared_select = a.cluster > 1 && a.S > kAlone;
+  const long run = a.shared_select ? ((long)a.S + a.cluster - 1) / a.cluster : a.S;
+  a.key_bytes = run * 4 <= kKeyBytes ? (int)(run * 4 + 15) / 16 * 16 : 0;
+  int smem = a.key_bytes > kPlaceBytes ? a.key_bytes : kPlaceBytes;
+  if (!a.shared_select) {      // the list beside the weights; rows too long for that: one CTA, the list in memory
+    if (a.S <= kAlone) smem += (a.budget < a.S ? a.budget : a.S) * 4;
+    else a.shared_select = 1;
   }
-  const dim3 grid((unsigned)(a.B * a.Hkv));
-  prof_begin(kProfEvictSelect, stream);
-  cudaError_t e = launch_programmatic(evict_select_kernel, grid, dim3(kSelThreads), 0, stream, a);
-  prof_end(stream);
-  if (e != cudaSuccess) return e;
-  prof_begin(kProfEvictMove, stream);
-  e = launch_programmatic(evict_move_kernel, dim3(grid.x, (unsigned)slices), dim3(kMoveThreads), 0, stream, a);
+  // j / page_size for 0 <= j < 2^31 by a multiplication: with s = ceil(log2 p) and m = ceil(2^(31+s) / p) < 2^32 the error
+  // m p - 2^(31+s) is below p <= 2^s, so floor(j m / 2^(31+s)) is exact; umulhi takes 32 of the bits
+  a.div_shift = 0;
+  while ((1L << a.div_shift) < a.page_size) ++a.div_shift;
+  a.div_mul = a.page_size > 1 ? (unsigned)(((1ULL << (31 + a.div_shift)) + a.page_size - 1) / a.page_size) : 0;
+  a.div_shift -= a.page_size > 1;
+  a.parts = 0;
+  for (int i = 0; i < a.n_planes; ++i) {
+    const int rb = a.planes[i].row_bytes;
+    a.parts += rb / (rb % 16 == 0 ? 16 : rb % 8 == 0 ? 8 : 4);
+  }
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyBytes + 8192);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set[dev] = true;
+  }
+  prof_begin(kProfEvict, stream);
+  const cudaError_t e = launch_programmatic_clusters(evict_kernel, a.cluster, dim3((unsigned)(units * a.cluster)),
+                                                     dim3(kEvThreads), (size_t)smem, stream, a);
   prof_end(stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -116,7 +116,6 @@ constexpr int kEvictPlanes = 8;
 struct EvictPlane {
   void* p;
   int row_bytes;
-  int piece, slice_bytes, slices;   // bytes a thread moves; of a row that a CTA moves; CTAs a row (set by the launch)
 };
 struct EvictArgs {
   const float* weights;
@@ -127,6 +126,10 @@ struct EvictArgs {
   int *kept, *lens_out;      // [B, Hkv, budget], [B]
   int B, Hkv, S, page_size, max_pages, num_pages;
   int budget, recent, first;
+  // set by the launch: CTAs of a unit; shared memory for a CTA's weights, 0: they do not fit; threads' parts of a row
+  int cluster, key_bytes, parts;
+  unsigned div_mul, div_shift;   // division by page_size
+  int shared_select;         // the cluster selects together and the list is `kept`; otherwise each CTA does, into its own
   int* status;
 };
 cudaError_t launch_cache_evict(EvictArgs a, cudaStream_t stream);

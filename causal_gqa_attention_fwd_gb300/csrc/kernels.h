@@ -212,10 +212,9 @@ enum ProfKind {
   kProfPrefix = 12,
   kProfPrefixMerge = 13,
   kProfWeights = 14,
-  kProfEvictSelect = 15,
-  kProfEvictMove = 16,
-  kProfOwn = 17,
-  kProfKinds = 18
+  kProfEvict = 15,
+  kProfOwn = 16,
+  kProfKinds = 17
 };
 // Launch with programmatic stream serialization (see griddep_wait in
 // sm103.cuh): the kernel's CTAs may be scheduled, and run their set-up, while

@@ -664,7 +664,7 @@ GQA_ATTN_API attn_status attn_test_inject_timeout(int kernel, int limit_ms);
  * 3 unused, 4 decode partial, 5 decode split merge, 6 backward dQ kernel,
  * 7 cache plan, 8 rotary rows, 9 rotary table, 10 cache append, 11 cache
  * gather, 12 shared prefix, 13 its merge, 14 attention weights of cached keys,
- * 15 eviction's selection, 16 its moves, 17 a shared prefix's own keys), the number of launches and their summed device
+ * 15 eviction, 16 a shared prefix's own keys), the number of launches and their summed device
  * time in milliseconds since the last attn_profile_reset.  At most 65536
  * launches are recorded between resets.  Off by default. */
 GQA_ATTN_API attn_status attn_profile_enable(int enable);
