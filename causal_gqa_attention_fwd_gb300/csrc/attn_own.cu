@@ -20,6 +20,7 @@
 // warps + units entries whatever the lengths are.
 #include "kernels.h"
 #include "sm103.cuh"
+#include "stream.cuh"
 
 namespace gqa {
 
@@ -122,7 +123,6 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
 
-  // ------------------------------------------------ the warp's share: inclusive sums of the rows' stream positions
   const int rows = a.P + a.B;
   auto positions = [&](int i) {
     int len;
@@ -130,64 +130,16 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
     if (nb == 0 && len != 0) atomicCAS(a.status, 0, kDevBadSeqlens);
     return nb ? (nb + kUnitCost) * (a.Hkv * blocks_of(a, i)) : 0;
   };
-  long total = 0;
-  if (rows > C::kThreads) {     // more rows than threads: a pass for the total first
-    int mine = 0;
-    for (int i = tid; i < rows; i += C::kThreads) mine += positions(i);
-    mine = __reduce_add_sync(~0u, mine);
-    if (lane == 0) s_sum[warp] = mine;
-    __syncthreads();
-    for (int w = 0; w < C::kWarps; ++w) total += s_sum[w];
-  }
-  int Wn = 0, v0 = 0, v1 = 0, before = 0;
   const int gw = warp * gridDim.x + blockIdx.x;     // neighbouring shares go to different SMs
-  auto take_share = [&]() {
-    Wn = (int)min((long)a.warps, (total + kMinShare - 1) / kMinShare);
-    if (gw < Wn) {
-      v0 = (int)(gw * total / Wn);
-      v1 = (int)((gw + 1) * total / Wn);
-    }
-  };
-  if (rows > C::kThreads) take_share();
-  Run u{-1, 0, 0, 0, 0, 0, 0};
-  for (int i0 = 0; i0 < rows; i0 += C::kThreads) {
-    int inc = i0 + tid < rows ? positions(i0 + tid) : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(~0u, inc, d);
-      if (lane >= d) inc += x;
-    }
-    __syncthreads();     // the sums before are read
-    if (lane == 31) s_sum[warp] = inc;
-    __syncthreads();
-    int all = 0;
-    for (int w = 0; w < C::kWarps; ++w) {
-      if (w < warp) inc += s_sum[w];
-      all += s_sum[w];
-    }
-    s_pre[tid] = inc;
-    __syncthreads();
-    if (rows <= C::kThreads) {
-      total = all;
-      take_share();
-    }
-    if (v0 < v1 && u.i < 0 && v0 < before + all) {
-      const int x = v0 - before;      // the first row whose inclusive sum is above
-      int lo = 0, hi = min(C::kThreads, rows - i0) - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s_pre[mid] > x) hi = mid;
-        else lo = mid + 1;
-      }
-      u.i = i0 + lo;
-      u.nb = row_tiles<KT>(a, u.i, u.len);
-      const int P = before + (lo ? s_pre[lo - 1] : 0);
-      u.k = (v0 - P) / (u.nb + kUnitCost);
-      u.P = P + u.k * (u.nb + kUnitCost) + kUnitCost;
-      u.t = max(v0 - u.P, 0);
-      u.te = min(u.nb, v1 - u.P);
-    }
-    before += all;
+  const StreamShare sh = stream_share<C::kThreads>(rows, gw, a.warps, kMinShare, s_sum, s_pre, positions);
+  Run u{sh.row, 0, 0, 0, 0, 0, 0};
+  const int v1 = sh.v1;
+  if (u.i >= 0) {
+    u.nb = row_tiles<KT>(a, u.i, u.len);
+    u.k = (sh.v0 - sh.at) / (u.nb + kUnitCost);
+    u.P = sh.at + u.k * (u.nb + kUnitCost) + kUnitCost;
+    u.t = max(sh.v0 - u.P, 0);
+    u.te = min(u.nb, v1 - u.P);
   }
 
   if (u.i >= 0 && u.t < u.te) {
@@ -386,8 +338,7 @@ __global__ void __launch_bounds__(OwnCfg<D, NT>::kThreads, 1)
       const int unit = (pre ? u.i * a.nrbp : a.P * a.nrbp + (u.i - a.P) * a.nrb) * a.Hkv + u.k;
       const long base = ((long)gw + unit) * a.rows_ws;
       if (u.t == 0 && lane == 0) {
-        const int last = (int)((((long)u.P + u.nb) * Wn - 1) / total);     // the warp of the unit's last tile
-        a.counts[unit] = make_int2(gw + unit, last - gw + 1);
+        a.counts[unit] = make_int2(gw + unit, sh.owner(u.P + u.nb - 1) - gw + 1);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)

@@ -25,6 +25,7 @@
 #include "fp4.cuh"
 #include "kernels.h"
 #include "sm103.cuh"
+#include "stream.cuh"
 
 namespace gqa {
 
@@ -58,33 +59,12 @@ struct KeyPart {
   __device__ static int feature(int s, int tig) { return E * (tig + 4 * (4 * s / E)) + 4 * s % E; }
 };
 
+// A lane's share of one key row.
 template <int D, CacheFmt F>
 struct KeyRow {
   using P = KeyPart<D, F>;
   uint32_t w[P::kWords];
   uint32_t sf;      // 4-bit: the block scales of the lane's features
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < P::kWords; ++i) w[i] = 0;
-    sf = 0;
-  }
-  __device__ __forceinline__ void load(const WeightsArgs& a, long row, int tig) {
-    const uint8_t* p = a.k + row * P::kRowBytes;
-#pragma unroll
-    for (int i = 0; i < P::kParts; ++i) {
-      if constexpr (P::kBytes == 16) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + (tig + 4 * i) * 16));
-        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-      } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + tig * 8));
-        w[0] = v.x, w[1] = v.y;
-      }
-    }
-    if constexpr (F == kCacheQ4) {
-      if constexpr (D == 128) sf = __ldg(reinterpret_cast<const uint16_t*>(a.ksf + row * 8) + tig);
-      else sf = __ldg(a.ksf + row * 4 + tig);
-    }
-  }
   // The 16-bit pairs (features 4 s, +1) and (+2, +3) of step s.
   __device__ __forceinline__ void step(int s, uint32_t& lo, uint32_t& hi) const {
     if constexpr (F == kCacheBf16) {
@@ -103,24 +83,257 @@ struct KeyRow {
   }
 };
 
-// The page of position j of batch row b, -1 where the table names none.
-__device__ __forceinline__ int page_of(const int* table, int max_pages, int num_pages, int b, int page) {
-  if (!table) return b;
-  const int e = table[(long)b * max_pages + page];
-  return e >= 0 && e < num_pages ? e : -1;
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
 }
 
+// A tile of 32 keys on its way: a lane copies the parts that it uses itself (rows 8 m + g), so that nothing has to be
+// exchanged and any number of tiles can be under way without registers.
 template <int D, CacheFmt F>
-__global__ void __launch_bounds__(32 * kWWarps) cache_weights_kernel(const WeightsArgs a) {
+struct KeyStage {
+  using P = KeyPart<D, F>;
+  struct Lane { uint8_t b[P::kBytes]; };
+  static constexpr int kParts = 4 * P::kParts * 32 * P::kBytes;
+  static constexpr int kSf = F == kCacheQ4 ? 4 * 32 * 4 : 0;
+  static constexpr int kBytes = kParts + kSf + 32 * 4 + 32 * 8;   // parts, scales, weights, their slots
+
+  // Keys 32 t .. of a row of len keys; returns whether a page was bad.
+  __device__ static bool issue(const WeightsArgs& a, uint8_t* st, const Slots& slot_of, int t, int len, int lane) {
+    const int g = lane >> 2, tig = lane & 3;
+    bool bad = false;
+    long mine = -1;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int j = 32 * t + 8 * m + g;
+      const long slot = j < len ? slot_of(j) : -1;
+      bad |= j < len && slot < 0;
+      if (m == tig) mine = slot;
+      if (slot < 0) continue;      // what stands there is scored, and its weight neither written nor kept
+      const uint8_t* p = a.k + slot * P::kRowBytes + tig * P::kBytes;
+#pragma unroll
+      for (int i = 0; i < P::kParts; ++i)
+        copy_async<P::kBytes>(smem_u32(st + ((m * P::kParts + i) * 32 + lane) * P::kBytes), p + 4 * i * P::kBytes);
+      if constexpr (F == kCacheQ4)      // D = 128: 2 of the 4 bytes
+        copy_async<4>(smem_u32(st + kParts + (m * 32 + lane) * 4), a.ksf + slot * (D / 16) + (D == 128 ? tig / 2 * 4 : 0));
+    }
+    if (mine >= 0) copy_async<4>(smem_u32(st + kParts + kSf + lane * 4), a.weights + mine);
+    *reinterpret_cast<long*>(st + kParts + kSf + 128 + lane * 8) = mine;
+    return bad;
+  }
+  __device__ static void row(const uint8_t* st, int m, int lane, KeyRow<D, F>& k) {
+#pragma unroll
+    for (int i = 0; i < P::kParts; ++i) {
+      const uint8_t* p = st + ((m * P::kParts + i) * 32 + lane) * P::kBytes;
+      if constexpr (P::kBytes == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        k.w[4 * i] = v.x, k.w[4 * i + 1] = v.y, k.w[4 * i + 2] = v.z, k.w[4 * i + 3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        k.w[0] = v.x, k.w[1] = v.y;
+      }
+    }
+    if constexpr (F == kCacheQ4) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(st + kParts + (m * 32 + lane) * 4);
+      k.sf = w >> (D == 128 ? (lane & 1) * 16 : (lane & 3) * 8);
+    }
+  }
+  __device__ static float weight(const uint8_t* st, int lane) { return *reinterpret_cast<const float*>(st + kParts + kSf + lane * 4); }
+  __device__ static long slot(const uint8_t* st, int lane) { return *reinterpret_cast<const long*>(st + kParts + kSf + 128 + lane * 8); }
+};
+
+// The lane's share of query row `row` (-1: none) in fragments q[s] of step s; f16: scaled by 2^e, which it returns.
+template <int D, CacheFmt F>
+__device__ __forceinline__ int query_fragments(const WeightsArgs& a, long row, int tig, uint2* q) {
   using P = KeyPart<D, F>;
   constexpr int kSteps = D / 16;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s)
+    q[s] = row >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.q + row * D + P::feature(s, tig))) : make_uint2(0, 0);
+  int e = 0;
+  if constexpr (F != kCacheBf16) {
+    float mx = 0.f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const float2 x = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&q[s].x));
+      const float2 y = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&q[s].y));
+      mx = fmaxf(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))), mx);
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    if (mx > 0.f && mx < INFINITY) e = 14 - ilogbf(mx);     // the largest feature goes to [2^14, 2^15)
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const float2 x = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&q[s].x));
+      const float2 y = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&q[s].y));
+      q[s].x = pack_f16x2(ldexpf(x.x, e), ldexpf(x.y, e));
+      q[s].y = pack_f16x2(ldexpf(y.x, e), ldexpf(y.y, e));
+    }
+  }
+  return e;
+}
+
+// Score factor and -lse of a query row, in log2 units; factor NaN: no query.
+__device__ __forceinline__ float2 row_constants(const WeightsArgs& a, long row, int e) {
+  const float lse = row >= 0 ? __ldg(a.lse + row) : -INFINITY;
+  return lse == -INFINITY ? make_float2(NAN, 0.f) : make_float2(ldexpf(a.scale_log2, -e), -lse * 1.4426950408889634f);
+}
+
+// ------------------------------------------------ at most 8 NT query rows a key: one stream of tiles over all warps
+template <int D, CacheFmt F>
+struct NarrowCfg {
+  static constexpr int kWarps = F == kCacheQ4 ? 16 : 12;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kFit = (216 << 10) / (kWarps * KeyStage<D, F>::kBytes);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr int kSmemBytes = kWarps * kStages * KeyStage<D, F>::kBytes;
+  static_assert(kStages >= 2, "two tiles on the way");
+};
+
+template <int D, CacheFmt F, int NT>
+__global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_kernel(const WeightsArgs a) {
+  using C = NarrowCfg<D, F>;
+  using St = KeyStage<D, F>;
+  constexpr int kSteps = D / 16;
   constexpr bool f16 = F != kCacheBf16;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int s_sum[C::kWarps], s_pre[C::kThreads];
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31, g = lane >> 2, tig = lane & 3;
+  griddep_wait();
+  griddep_launch();
+  auto tiles_of = [&](int b, int& len) {
+    len = a.cache_lens[b];
+    return len > 0 && len <= a.S ? (len + 31) / 32 : 0;
+  };
+  auto positions = [&](int b) {
+    int len;
+    const int nb = tiles_of(b, len);
+    if (nb == 0 && len != 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+    return nb * a.Hkv;
+  };
+  const int gw = warp * gridDim.x + blockIdx.x;
+  const StreamShare sh = stream_share<C::kThreads>(a.B, gw, gridDim.x * C::kWarps, 1, s_sum, s_pre, positions);
+  int left = sh.v1 - sh.v0;
+  if (sh.row < 0 || left <= 0) return;
+  // where the loads and the scores stand: tile t of (row b, head h)
+  struct At {
+    int b, h, len, nb, t;
+  };
+  At ld{sh.row, 0, 0, 0, 0};
+  ld.nb = tiles_of(ld.b, ld.len);
+  ld.h = (sh.v0 - sh.at) / ld.nb;
+  ld.t = (sh.v0 - sh.at) % ld.nb;
+  auto next = [&](At& x) {
+    if (++x.t < x.nb) return;
+    x.t = 0;
+    if (++x.h < a.Hkv) return;
+    x.h = 0;
+    do x.nb = tiles_of(++x.b, x.len);
+    while (x.nb == 0);
+  };
+  uint8_t* ring = smem + warp * (C::kStages * St::kBytes);
+  int to_load = left;
+  bool bad = false;
+  auto issue = [&](int st) {
+    if (to_load > 0) {
+      const Slots slot_of{a.block_table ? a.block_table + (long)ld.b * a.max_pages : nullptr, a.num_pages, ld.b, a.page,
+                          a.Hkv, ld.h};
+      bad |= St::issue(a, ring + st * St::kBytes, slot_of, ld.t, ld.len, lane);
+      if (--to_load > 0) next(ld);
+    }
+    copies_commit();
+  };
+  At at = ld;
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+  uint2 q[NT][kSteps];
+  float2 c[NT][2];      // of rows 8 n + 2 tig + i
+  int lim[NT][2];
+  bool fresh = true;
+  for (int st = 0; left > 0; --left, st = st + 1 == C::kStages ? 0 : st + 1) {
+    issue(st == 0 ? C::kStages - 1 : st - 1);
+    if (fresh) {
+      const long row0 = ((long)at.b * a.Hkv + at.h) * a.R;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int e = query_fragments<D, F>(a, 8 * n + g < a.R ? row0 + 8 * n + g : -1, tig, q[n]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * n + 2 * tig + i;
+          const int er = __shfl_sync(~0u, e, 4 * (2 * tig + i));
+          c[n][i] = row_constants(a, r < a.R ? row0 + r : -1, er);
+          lim[n][i] = at.len - a.Tq + r % a.Tq;
+        }
+      }
+      fresh = false;
+    }
+    copies_wait<C::kStages - 1>();
+    const uint8_t* sp = ring + st * St::kBytes;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      KeyRow<D, F> k0, k1;      // keys 16 m + g and 16 m + 8 + g
+      St::row(sp, 2 * m, lane, k0);
+      St::row(sp, 2 * m + 1, lane, k1);
+      float acc[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint32_t f[4];
+        k0.step(s, f[0], f[2]);
+        k1.step(s, f[1], f[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_16816(acc[n], f, q[n][s].x, q[n][s].y, f16);
+      }
+      const int j = 32 * at.t + 16 * m + g;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool query = !(c[n][i].x != c[n][i].x);
+          const float p0 = ex2_approx(fmaf(acc[n][i], c[n][i].x, c[n][i].y));
+          const float p1 = ex2_approx(fmaf(acc[n][2 + i], c[n][i].x, c[n][i].y));
+          sum[2 * m] += query && j <= lim[n][i] ? p0 : 0.f;
+          sum[2 * m + 1] += query && j + 8 <= lim[n][i] ? p1 : 0.f;
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      sum[m] += __shfl_xor_sync(~0u, sum[m], 1);
+      sum[m] += __shfl_xor_sync(~0u, sum[m], 2);
+    }
+    const float mine = tig == 0 ? sum[0] : tig == 1 ? sum[1] : tig == 2 ? sum[2] : sum[3];
+    const long slot = St::slot(sp, lane);
+    // the step's new keys had no weight before
+    if (slot >= 0) a.weights[slot] = mine + (32 * at.t + 8 * tig + g < at.len - a.Tq ? St::weight(sp, lane) : 0.f);
+    if (left > 1) {
+      fresh = at.t + 1 == at.nb;
+      next(at);
+    }
+  }
+  copies_wait<0>();
+  if (bad) atomicCAS(a.status, 0, kDevBadPage);
+}
+
+// ------------------------------------------------ more query rows (a window of a prompt): a CTA a chunk of keys
+// Each warp holds the fragments of 32 keys in registers and takes the query rows, kWRows at a time, from shared memory.
+template <int D, CacheFmt F>
+__global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const WeightsArgs a) {
+  using St = KeyStage<D, F>;
+  constexpr int kSteps = D / 16;
+  constexpr bool f16 = F != kCacheBf16;
+  extern __shared__ __align__(16) uint8_t smem[];   // a stage a warp
   __shared__ uint2 s_q[kWRows / 8][kSteps][32];     // query fragments, by lane
-  __shared__ float2 s_c[kWRows];                    // score factor and -lse, in log2 units; factor NaN: no query
+  __shared__ float2 s_c[kWRows];
   __shared__ int s_t[kWRows];                       // query position of the row
   griddep_wait();
   griddep_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   const int bh = (int)(blockIdx.x % (unsigned)(a.B * a.Hkv)), b = bh / a.Hkv, hkv = bh % a.Hkv;
   const int c0 = (int)(blockIdx.x / (unsigned)(a.B * a.Hkv)) * kWKeys;
   const int len = a.cache_lens[b];
@@ -129,68 +342,41 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_kernel(const Weigh
     return;
   }
   if (c0 >= len) return;
-  // the lane's four keys: 8 m + g of the warp's 32, m = 0..3
   const int k0 = c0 + warp * 32;
-  KeyRow<D, F> kr[4];
-  bool bad = false;
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const int j = k0 + 8 * m + g;
-    kr[m].zero();
-    if (j < len) {
-      const int page = page_of(a.block_table, a.max_pages, a.num_pages, b, j / a.page_size);
-      bad |= page < 0;
-      if (page >= 0) kr[m].load(a, ((long)page * a.Hkv + hkv) * a.page_size + j % a.page_size, tig);
-    }
-  }
-  if (bad) atomicCAS(a.status, 0, kDevBadPage);
-  // the key whose weight this lane writes
-  const int jw = k0 + 8 * tig + g;
-  float* wp = nullptr;
-  float w = 0.f;
-  if (jw < len) {
-    const int page = page_of(a.block_table, a.max_pages, a.num_pages, b, jw / a.page_size);
-    if (page >= 0) {
-      wp = a.weights + ((long)page * a.Hkv + hkv) * a.page_size + jw % a.page_size;
-      w = jw < len - a.Tq ? *wp : 0.f;     // the step's new keys had no weight before
-    }
-  }
+  uint8_t* sp = smem + warp * St::kBytes;
+  const Slots slot_of{a.block_table ? a.block_table + (long)b * a.max_pages : nullptr, a.num_pages, b, a.page, a.Hkv, hkv};
+  if (St::issue(a, sp, slot_of, k0 / 32, len, lane)) atomicCAS(a.status, 0, kDevBadPage);
+  copies_commit();
+  uint32_t f[2][kSteps][4];
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   for (int r0 = 0; r0 < a.R; r0 += kWRows) {
     const int nt = min(kWRows, (a.R - r0 + 7) & ~7) / 8;
     if (r0) __syncthreads();
-    // query rows r0 .. into fragments, a warp a row
-    for (int r = warp; r < 8 * nt; r += kWWarps) {
-      const bool real = r0 + r < a.R;
-      const long qrow = (long)bh * a.R + r0 + r;
-      int e = 0;
-      if (real && f16) {
-        float mx = 0.f;
+    for (int t = warp; t < nt; t += kWWarps) {      // eight query rows a warp
+      const long row0 = (long)bh * a.R + r0;
+      const int r = 8 * t + g;
+      uint2 q[kSteps];
+      const long row = r0 + r < a.R ? row0 + r : -1;
+      const int e = query_fragments<D, F>(a, row, tig, q);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) mx = fmaxf(mx, fabsf(__bfloat162float(a.q[qrow * D + i * 32 + lane])));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (mx > 0.f && mx < INFINITY) e = 15 - ilogbf(mx) - 1;     // the largest feature goes to [2^14, 2^15)
-      }
-      for (int i = lane; i < kSteps * 4; i += 32) {
-        const int s = i / 4, t = i % 4;
-        uint2 v = make_uint2(0, 0);
-        if (real) {
-          v = *reinterpret_cast<const uint2*>(a.q + qrow * D + P::feature(s, t));
-          if constexpr (f16) {
-            const float2 x = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v.x));
-            const float2 y = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v.y));
-            v.x = pack_f16x2(ldexpf(x.x, e), ldexpf(x.y, e));
-            v.y = pack_f16x2(ldexpf(y.x, e), ldexpf(y.y, e));
-          }
-        }
-        s_q[r / 8][s][r % 8 * 4 + t] = v;
-      }
-      if (lane == 0) {
-        const float lse = real ? a.lse[qrow] : -INFINITY;
-        s_c[r] = lse == -INFINITY ? make_float2(NAN, 0.f)
-                                  : make_float2(ldexpf(a.scale_log2, -e), -lse * 1.4426950408889634f);
+      for (int s = 0; s < kSteps; ++s) s_q[t][s][lane] = q[s];
+      if (tig == 0) {
+        s_c[r] = row_constants(a, row, e);
         s_t[r] = (r0 + r) % a.Tq;
+      }
+    }
+    if (r0 == 0) {
+      copies_wait<0>();
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        KeyRow<D, F> x, y;
+        St::row(sp, 2 * m, lane, x);
+        St::row(sp, 2 * m + 1, lane, y);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          x.step(s, f[m][s][0], f[m][s][2]);
+          y.step(s, f[m][s][1], f[m][s][3]);
+        }
       }
     }
     __syncthreads();
@@ -199,13 +385,8 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_kernel(const Weigh
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const uint2 q = s_q[t][s][lane];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t f[4];
-          kr[2 * m].step(s, f[0], f[2]);
-          kr[2 * m + 1].step(s, f[1], f[3]);
-          mma_16816(acc[m], f, q.x, q.y, f16);
-        }
+        mma_16816(acc[0], f[0][s], q.x, q.y, f16);
+        mma_16816(acc[1], f[1][s], q.x, q.y, f16);
       }
       // acc[m][0, 1]: key 16 m + g, rows 2 tig, 2 tig + 1; [2, 3]: key 16 m + 8 + g
 #pragma unroll
@@ -228,21 +409,46 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_kernel(const Weigh
     sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], 2);
   }
   const float mine = tig == 0 ? sum[0] : tig == 1 ? sum[1] : tig == 2 ? sum[2] : sum[3];
-  if (wp) *wp = w + mine;
+  const long slot = St::slot(sp, lane);
+  // the step's new keys had no weight before
+  if (slot >= 0) a.weights[slot] = mine + (k0 + 8 * tig + g < len - a.Tq ? St::weight(sp, lane) : 0.f);
+}
+
+template <auto KERNEL>
+cudaError_t launch_weights(dim3 grid, int threads, int smem, const WeightsArgs& a, cudaStream_t stream) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set[dev] = true;
+  }
+  return launch_programmatic(KERNEL, grid, dim3(threads), (size_t)smem, stream, a);
+}
+
+template <int D, CacheFmt F>
+cudaError_t launch_weights_df(const WeightsArgs& a, int sms, cudaStream_t stream) {
+  using C = NarrowCfg<D, F>;
+  if (a.R <= 8) return launch_weights<cache_weights_kernel<D, F, 1>>(dim3(sms), C::kThreads, C::kSmemBytes, a, stream);
+  if (a.R <= 16) return launch_weights<cache_weights_kernel<D, F, 2>>(dim3(sms), C::kThreads, C::kSmemBytes, a, stream);
+  const dim3 grid((unsigned)((long)a.B * a.Hkv * ((a.S + (long)kWKeys - 1) / kWKeys)));
+  return launch_weights<cache_weights_wide_kernel<D, F>>(grid, 32 * kWWarps, kWWarps * KeyStage<D, F>::kBytes, a, stream);
+}
+
+template <CacheFmt F>
+cudaError_t launch_weights_f(const WeightsArgs& a, int sms, cudaStream_t stream) {
+  return a.D == 128 ? launch_weights_df<128, F>(a, sms, stream) : launch_weights_df<64, F>(a, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_weights(const WeightsArgs& a, CacheFmt fmt, int sms, cudaStream_t stream) {
-  (void)sms;
-  const dim3 grid((unsigned)((long)a.B * a.Hkv * ((a.S + (long)kWKeys - 1) / kWKeys))), block(32 * kWWarps);
+cudaError_t launch_cache_weights(WeightsArgs a, CacheFmt fmt, int sms, cudaStream_t stream) {
+  a.page = FastDiv::of(a.page_size);
   prof_begin(kProfWeights, stream);
-  cudaError_t e;
-#define GQA_WEIGHTS(F)                                                                              \
-  (a.D == 128 ? launch_programmatic(cache_weights_kernel<128, F>, grid, block, 0, stream, a)        \
-              : launch_programmatic(cache_weights_kernel<64, F>, grid, block, 0, stream, a))
-  e = fmt == kCacheBf16 ? GQA_WEIGHTS(kCacheBf16) : fmt == kCacheE4m3 ? GQA_WEIGHTS(kCacheE4m3) : GQA_WEIGHTS(kCacheQ4);
-#undef GQA_WEIGHTS
+  const cudaError_t e = fmt == kCacheBf16   ? launch_weights_f<kCacheBf16>(a, sms, stream)
+                        : fmt == kCacheE4m3 ? launch_weights_f<kCacheE4m3>(a, sms, stream)
+                                            : launch_weights_f<kCacheQ4>(a, sms, stream);
   prof_end(stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -280,33 +486,15 @@ __device__ __forceinline__ int4 peer_int4(const void* p, int rank) {
   return v;
 }
 
-// Where position j of (row b, head h) is: the number of its slot row in a plane, -1 in a page outside the pool.
-struct Slots {
-  const int* table;      // of row b, nullptr: contiguous
-  int num_pages, page_size, b;
-  unsigned mul, shift;   // j / page_size = umulhi(j, mul) >> shift, page_size > 1
-  long heads, h;
-  __device__ __forceinline__ long operator()(int j) const {
-    int page = b, r = j;
-    if (table) {
-      const int i = page_size == 1 ? j : (int)(__umulhi((unsigned)j, mul) >> shift);
-      r = j - i * page_size;
-      page = table[i];
-      if (page < 0 || page >= num_pages) return -1;
-    }
-    return ((long)page * heads + h) * page_size + r;
-  }
-};
-
 // A thread's part of every row that it moves: 16, 8 or 4 bytes of one plane, by way of its place in shared memory.
 struct Part {
   uint8_t* base;      // of the plane, at the part
   int row_bytes, size;
   __device__ __forceinline__ void load(uint32_t to, long slot) const {
     const uint8_t* p = base + slot * row_bytes;
-    if (size == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
-    else if (size == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(p) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p) : "memory");
+    if (size == 16) copy_async<16>(to, p);
+    else if (size == 8) copy_async<8>(to, p);
+    else copy_async<4>(to, p);
   }
   __device__ __forceinline__ void store(const uint4* from, long slot) const {
     uint8_t* p = base + slot * row_bytes;
@@ -315,10 +503,6 @@ struct Part {
     else *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(from);
   }
 };
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // Moves the rows list[d] -> d, d in [first, budget), of every plane.  A thread has one part of a row (a row's parts of all
 // planes lie on neighbouring threads), kMoveRows of them on the way at a time.  Row d may be written once whatever is kept
 // of position d has been read, that is all rows i with list[i] <= d.  So the rows go in phases [c0, c1): if list[c0] lies
@@ -431,8 +615,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictArgs a)
   // shared memory: the weights, in whose place rows are on the way later; the list
   int* list = a.shared_select ? kept : reinterpret_cast<int*>(s_keys) + max(a.key_bytes, kPlaceBytes) / 4;
   bool bad = false;
-  const Slots slot_of{a.block_table ? a.block_table + (long)b * a.max_pages : nullptr, a.num_pages, a.page_size, b,
-                      a.div_mul, a.div_shift, a.Hkv, h};
+  const Slots slot_of{a.block_table ? a.block_table + (long)b * a.max_pages : nullptr, a.num_pages, b, a.page, a.Hkv, h};
   auto load_key = [&](int j) {
     const long s = slot_of(j);
     bad |= s < 0;
@@ -605,6 +788,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictArgs a)
 }  // namespace
 
 cudaError_t launch_cache_evict(EvictArgs a, cudaStream_t stream) {
+  a.page = FastDiv::of(a.page_size);
   const long units = (long)a.B * a.Hkv;
   // a cluster a unit, as large as leaves all CTAs resident (two an SM) and 256 positions a CTA
   a.cluster = 8;
@@ -617,12 +801,6 @@ cudaError_t launch_cache_evict(EvictArgs a, cudaStream_t stream) {
     if (a.S <= kAlone) smem += (a.budget < a.S ? a.budget : a.S) * 4;
     else a.shared_select = 1;
   }
-  // j / page_size for 0 <= j < 2^31 by a multiplication: with s = ceil(log2 p) and m = ceil(2^(31+s) / p) < 2^32 the error
-  // m p - 2^(31+s) is below p <= 2^s, so floor(j m / 2^(31+s)) is exact; umulhi takes 32 of the bits
-  a.div_shift = 0;
-  while ((1L << a.div_shift) < a.page_size) ++a.div_shift;
-  a.div_mul = a.page_size > 1 ? (unsigned)(((1ULL << (31 + a.div_shift)) + a.page_size - 1) / a.page_size) : 0;
-  a.div_shift -= a.page_size > 1;
   a.parts = 0;
   for (int i = 0; i < a.n_planes; ++i) {
     const int rb = a.planes[i].row_bytes;

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "stream.cuh"
+
 namespace gqa {
 
 struct PlanArgs {
@@ -107,9 +109,10 @@ struct WeightsArgs {
   float* weights;
   int B, Hkv, Tq, R, S, D, page_size, max_pages, num_pages;
   float scale_log2;          // softmax scale * k_scale * log2(e)
+  FastDiv page;              // page_size (set by the launch)
   int* status;
 };
-cudaError_t launch_cache_weights(const WeightsArgs& a, CacheFmt fmt, int sms, cudaStream_t stream);
+cudaError_t launch_cache_weights(WeightsArgs a, CacheFmt fmt, int sms, cudaStream_t stream);
 
 // Eviction.  The planes [N, Hkv, P, row_bytes] of a cache, the weights among them.
 constexpr int kEvictPlanes = 8;
@@ -128,7 +131,7 @@ struct EvictArgs {
   int budget, recent, first;
   // set by the launch: CTAs of a unit; shared memory for a CTA's weights, 0: they do not fit; threads' parts of a row
   int cluster, key_bytes, parts;
-  unsigned div_mul, div_shift;   // division by page_size
+  FastDiv page;              // page_size
   int shared_select;         // the cluster selects together and the list is `kept`; otherwise each CTA does, into its own
   int* status;
 };
