@@ -433,17 +433,21 @@ __global__ void __launch_bounds__(384, 1)
         constexpr int kC = D / 8;                 // 16-byte parts of a row
         constexpr int kPer = 32 / kC;             // rows a warp takes at once
         const int part = lane % kC;
-#pragma unroll 4
-        for (int i = 0; i < 32; i += kPer) {
-          const int rr = wrow + i + lane / kC;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (rr < rows) {
-            const int gr = row0 + rr, b = it.p * a.W + gr / a.R;
-            const long qr = ((long)b * a.Hkv + it.hkv) * a.R + gr % a.R;
-            v = *reinterpret_cast<const uint4*>(a.q + qr * D + part * 8);
-          }
+        // the row's place within its batch row moves on by kPer a step: one division
+        int gr = row0 + wrow + lane / kC, b = it.p * a.W + gr / a.R, in = gr % a.R;
+        uint4 v[kC];
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          const bool real = wrow + i * kPer + lane / kC < rows;
+          const long qr = ((long)b * a.Hkv + it.hkv) * a.R + in;
+          v[i] = real ? __ldg(reinterpret_cast<const uint4*>(a.q + qr * D + part * 8)) : make_uint4(0, 0, 0, 0);
+          for (in += kPer; in >= a.R; in -= a.R) ++b;
+        }
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          const int rr = wrow + i * kPer + lane / kC;
           *reinterpret_cast<uint4*>(sQ + x * C::kTileBytes + (part >> 3) * C::kBoxBytes + rr * 128 +
-                                    (((part & 7) ^ (rr & 7)) << 4)) = v;
+                                    (((part & 7) ^ (rr & 7)) << 4)) = v[i];
         }
         fence_proxy_async_smem();
         mbar_arrive_warp(&bars.q_full[x]);
@@ -558,16 +562,27 @@ __global__ void __launch_bounds__(384, 1)
       const long wr = (((long)it.p * a.Hkv + it.hkv) * a.Rp + row0 + r) * a.slots + slot;
       const bool mine = r < rows && GQA_CHECK(slot >= 0 && slot < a.slots && row0 + r < a.Rp, a.status, a.dbg_line);
       if (nx > 0 && live) {
+        // by way of this warp's rows of the query tile (free: the piece's MMAs are done), 32 features at a time, so that
+        // a row's 128 bytes go out together
+        const long wr0 = wr - (long)lane * a.slots;      // of the warp's first row
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
           tmem_ld_x32(tO + q * 32, o);
           tmem_ld_wait();
           reg_fence<32>(o);
-          if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(a.ws_o + wr * D + q * 32);
+          const uint32_t buf = smem_u32(sQ + x * C::kTileBytes + (q & (C::kBoxes - 1)) * C::kBoxBytes + wrow * 128);
+          if (C::kBoxes == 1) __syncwarp();              // the buffer before is read
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 8; ++k)
+            st_shared_v4(buf + lane * 128 + ((k ^ (lane & 7)) << 4), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = 4 * k + (lane >> 3);
+            const uint4 v = ld_shared_v4(buf + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+            if (wrow + rr < rows && GQA_CHECK(slot >= 0 && slot < a.slots && row0 + wrow + rr < a.Rp, a.status, a.dbg_line))
+              *reinterpret_cast<uint4*>(a.ws_o + (wr0 + (long)rr * a.slots) * D + q * 32 + (lane & 7) * 4) = v;
           }
         }
         tc_fence_before();   // O is read before the next piece's P V (after its q_full) writes it
