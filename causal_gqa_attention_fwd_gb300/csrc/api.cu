@@ -884,11 +884,11 @@ struct OwnPlan {
   long units;
 };
 
-OwnPlan own_plan(int B, int Hq, int Hkv, int Tq, int P, int Sp) {
+OwnPlan own_plan(int B, int Hq, int Hkv, int Tq, int P, int Sp, int D) {
   OwnPlan p{};
   p.R = Hq / Hkv * Tq;
   const int Rp = B / P * p.R;
-  p.stream = gqa::prefix_in_stream(Rp, P, Hkv, Sp);
+  p.stream = gqa::prefix_in_stream(Rp, P, Hkv, Sp, D);
   const int most = p.stream ? Rp : p.R;
   p.block = most <= 8 ? 8 : 16;
   p.nrb = (p.R + p.block - 1) / p.block;
@@ -929,7 +929,7 @@ attn_status prefix_check(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, i
   if (B % P) return ATTN_ERR_SHAPE;
   if (B == 0 || Tq == 0) return ATTN_OK;
   // positions in the stream of the rows' own tiles
-  if (own_plan(B, Hq, Hkv, Tq, P, Sp).units > 0x7fffffffL / ((S > Sp ? S : Sp) / 16 + 4L)) return ATTN_ERR_SHAPE;
+  if (own_plan(B, Hq, Hkv, Tq, P, Sp, D).units > 0x7fffffffL / ((S > Sp ? S : Sp) / 16 + 4L)) return ATTN_ERR_SHAPE;
   const PrefixPlan p = prefix_plan(B, Hq, Hkv, Tq, P, Sp);
   // block stream and ring indices
   if (p.units * ((Sp + 127L) / 128) > 0x3fffffffL || (long)P * Hkv > 0x7fffffffL) return ATTN_ERR_SHAPE;
@@ -947,7 +947,7 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   const int sms = sm_count();
   if (!status || sms < 1) return ATTN_ERR_CUDA;
   const PrefixPlan p = prefix_plan(B, Hq, Hkv, Tq, P, Sp);
-  const OwnPlan d = own_plan(B, Hq, Hkv, Tq, P, Sp);
+  const OwnPlan d = own_plan(B, Hq, Hkv, Tq, P, Sp, D);
   const PrefixWs w = prefix_ws(p, d, P, Hkv, D);
   char* ws = static_cast<char*>(workspace);
   const int ctas = sms < gqa::kDecodeMaxSlots ? sms : gqa::kDecodeMaxSlots;   // one a SM, as decode
@@ -1023,7 +1023,7 @@ attn_status prefix_check_pointers(const void* q, const void* k, const void* v, c
       (reinterpret_cast<uintptr_t>(prefix_lens) & 3u) || (reinterpret_cast<uintptr_t>(cache_lens) & 3u))
     return ATTN_ERR_ALIGN;
   const size_t need =
-      prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), own_plan(B, Hq, Hkv, Tq, P, Sp), P, Hkv, D).bytes;
+      prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), own_plan(B, Hq, Hkv, Tq, P, Sp, D), P, Hkv, D).bytes;
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return ATTN_ERR_WORKSPACE;
   return ATTN_OK;
 }
@@ -1034,7 +1034,7 @@ extern "C" {
 
 size_t attn_decode_prefix_workspace_size(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, int D) {
   if (prefix_check(B, Hq, Hkv, Tq, P, Sp, S, D) != ATTN_OK || B == 0 || Tq == 0) return 0;
-  return prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), own_plan(B, Hq, Hkv, Tq, P, Sp), P, Hkv, D).bytes;
+  return prefix_ws(prefix_plan(B, Hq, Hkv, Tq, P, Sp), own_plan(B, Hq, Hkv, Tq, P, Sp, D), P, Hkv, D).bytes;
 }
 
 attn_status attn_decode_prefix_fwd(const void* q, const void* k_prefix, const void* v_prefix, const int* prefix_lens,

@@ -294,34 +294,10 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp == 1) {
     // ============================================ MMA issuer (whole warp, one lane issues)
     regs_dec<64>();
+    // One loop for both kinds of unit and both tiles: a CTA sees few blocks, and code that runs for the first time costs
+    // 0.5 us for every 50 instructions (a loop for each kind with both tiles unrolled: 20 us at 8192 keys and 100 at 32768
+    // where this takes 15 and 87; the products rolled too: 17 and 112).
     const uint32_t sq_addr = smem_u32(sQ), ring_addr = smem_u32(sRing);
-    auto stage_of = [&](int idx) { return idx % C::kStages; };
-    auto wait_kv = [&](int idx) {
-      return (bool)__all_sync(0xffffffffu, mbar_wait(&bars.kv_full[stage_of(idx)], (idx / C::kStages) & 1, guard));
-    };
-    auto issue_qk = [&](int x, int st) {
-      const uint32_t qa = sq_addr + x * C::kTileBytes, ka = ring_addr + st * C::kTileBytes;
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::kBoxBytes + (kk & 3) * 32;
-          mma_ss(tmem + C::col_s(x), sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), C::kIdescQK,
-                 kk > 0);
-        }
-      }
-      __syncwarp();
-    };
-    // P V over the keys [16 kk0, 16 kk1) of the block (P packed in TMEM over S)
-    auto issue_pv = [&](int x, int st, bool acc, int kk0, int kk1) {
-      const uint32_t va = ring_addr + st * C::kTileBytes;
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = kk0; kk < kk1; ++kk)
-          mma_ts(tmem + C::col_o(x), tmem + C::col_s(x) + kk * 8, sdesc_sw128(va + kk * 2048, C::kBoxBytes, 1024),
-                 C::kIdescPV, (acc || kk > 0) ? 1u : 0u);
-      }
-      __syncwarp();
-    };
     bool ok = true;
     uint32_t pc[2] = {0, 0};   // P blocks taken from each tile
     int base = 0, uses = 0;    // ring index of the piece's K_0 (V_j follows K_j); pieces before
@@ -329,76 +305,59 @@ __global__ void __launch_bounds__(384, 1)
       const int n = w.it.n;
       const bool split = w.it.split;
       for (int x = 0; x < 2 && ok; ++x) ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full[x], uses & 1, guard));
-      if (!ok) break;
-      // P of tile x for block j, in two halves, so that the first half's P V runs while the softmax forms the second
-      auto pv = [&](int x, int vst, bool acc) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_half[x], pc[x] & 1, guard));
-        if (!ok) return;
-        tc_fence_after();
-        issue_pv(x, vst, acc, 0, kBN / 32);
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_full[x], pc[x] & 1, guard));
-        if (!ok) return;
-        tc_fence_after();
-        issue_pv(x, vst, true, kBN / 32, kBN / 16);
-        ++pc[x];
-      };
-      if (split) {
-        // block j belongs to tile j & 1
-        for (int j = 0; j < 2 && j < n && ok; ++j) {
-          ok = wait_kv(base + 2 * j);
+      // Step t is tile t & 1's: P V of its block j, then the scores of its next one.  Tiles that read every block:
+      // j = t / 2 - 1 and j + 1; tiles that take them in turn: j = t - 2 and j + 2.
+      const int steps = split ? n + 2 : 2 * n + 2;
+#pragma unroll 1
+      for (int t = 0; t < steps && ok; ++t) {
+        const int x = t & 1, nj = split ? t : t >> 1, j = split ? t - 2 : (t >> 1) - 1;
+        const bool last_reader = split || x == 1;
+        if (j >= 0) {
+          const int vi = base + 2 * j + 1, st = vi % C::kStages;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.kv_full[st], (vi / C::kStages) & 1, guard));
           if (!ok) break;
-          tc_fence_after();
-          issue_qk(j, stage_of(base + 2 * j));
-          tc_commit_warp(&bars.s_full[j]);
-          tc_commit_warp(&bars.kv_empty[stage_of(base + 2 * j)]);
-        }
-        for (int j = 0; j < n && ok; ++j) {
-          const int x = j & 1, vi = base + 2 * j + 1, ki = base + 2 * j + 4;
-          ok = wait_kv(vi);
-          if (!ok) break;
-          pv(x, stage_of(vi), j >= 2);
-          if (!ok) break;
-          tc_commit_warp(&bars.kv_empty[stage_of(vi)]);
-          if (j + 2 < n) {
-            ok = wait_kv(ki);
+          const uint64_t vd = sdesc_sw128(ring_addr + st * C::kTileBytes, C::kBoxBytes, 1024);
+          const uint32_t par = (x ? pc[1] : pc[0]) & 1;
+          const bool acc = j >= (split ? 2 : 1);
+          // P comes in two halves, so that the first half's P V runs while the softmax forms the second
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            ok = __all_sync(0xffffffffu, mbar_wait(half ? &bars.p_full[x] : &bars.p_half[x], par, guard));
             if (!ok) break;
             tc_fence_after();
-            issue_qk(x, stage_of(ki));
-            tc_commit_warp(&bars.s_full[x]);
-            tc_commit_warp(&bars.kv_empty[stage_of(ki)]);
-          } else {
-            tc_commit_warp(&bars.o_done[x]);
+            if (elect_one()) {
+              const uint64_t hd = sdesc_add(vd, half * (kBN / 32) * 2048);
+              const uint32_t p = tmem + C::col_s(x) + half * (kBN / 4);
+#pragma unroll
+              for (int kk = 0; kk < kBN / 32; ++kk)
+                mma_ts(tmem + C::col_o(x), p + kk * 8, sdesc_add(hd, kk * 2048), C::kIdescPV, acc || half || kk > 0);
+            }
+            __syncwarp();
           }
+          if (!ok) break;
+          if (x) ++pc[1];
+          else ++pc[0];
+          if (last_reader) tc_commit_warp(&bars.kv_empty[st]);
         }
-        if (ok && n == 1) tc_commit_warp(&bars.o_done[1]);   // a tile without blocks is not a piece ahead either
-      } else {
-        ok = wait_kv(base);
-        if (!ok) break;
-        tc_fence_after();
-        for (int x = 0; x < 2; ++x) {
-          issue_qk(x, stage_of(base));
-          tc_commit_warp(&bars.s_full[x]);
-        }
-        tc_commit_warp(&bars.kv_empty[stage_of(base)]);
-        for (int j = 0; j < n && ok; ++j) {
-          const int vi = base + 2 * j + 1, ki = vi + 1;
-          ok = wait_kv(vi);
-          if (ok && j + 1 < n) ok = wait_kv(ki);
+        if (nj < n) {
+          const int ki = base + 2 * nj, st = ki % C::kStages;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.kv_full[st], (ki / C::kStages) & 1, guard));
           if (!ok) break;
           tc_fence_after();
-          for (int x = 0; x < 2 && ok; ++x) {
-            pv(x, stage_of(vi), j > 0);
-            if (!ok) break;
-            if (j + 1 < n) {
-              issue_qk(x, stage_of(ki));
-              tc_commit_warp(&bars.s_full[x]);
-            } else {
-              tc_commit_warp(&bars.o_done[x]);
+          const uint64_t qd = sdesc_sw128(sq_addr + x * C::kTileBytes, 16, 1024);
+          const uint64_t kd = sdesc_sw128(ring_addr + st * C::kTileBytes, 16, 1024);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C::kBoxBytes + (kk & 3) * 32;
+              mma_ss(tmem + C::col_s(x), sdesc_add(qd, off), sdesc_add(kd, off), C::kIdescQK, kk > 0);
             }
           }
-          if (!ok) break;
-          tc_commit_warp(&bars.kv_empty[stage_of(vi)]);
-          if (j + 1 < n) tc_commit_warp(&bars.kv_empty[stage_of(ki)]);
+          __syncwarp();
+          tc_commit_warp(&bars.s_full[x]);
+          if (last_reader) tc_commit_warp(&bars.kv_empty[st]);
+        } else if (j >= 0 || n == 1) {
+          tc_commit_warp(&bars.o_done[x]);     // also of a tile without blocks, which is not a piece ahead either
         }
       }
       base += 2 * n;
@@ -600,30 +559,33 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// WPR warps per output row: the maximum over the row's pieces, their weights
-// 2^(M_s - M), and the weighted sum of the partials over the sum of the
-// weighted L.  Pieces of weight 0 (they hold no key the row sees) are skipped.
-// Warp w of a row's takes pieces w, w + WPR, ...
-template <int D, int WPR>
-__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs p, const OwnArgs a, __nv_bfloat16* o, float* lse) {
+// WPR warps per output row, warp w with the row's pieces w, w + WPR, ...: the weights 2^(M_s - M) under a running
+// maximum M, and the weighted sums of the partials and of their L.  What a row costs is a chain of loads (lengths; which
+// pieces; their statistics and partials, kAt pieces at a time).
+template <int D, int WPR, int kAt>
+__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) prefix_merge_kernel(const PrefixArgs p, const OwnArgs a, __nv_bfloat16* o, float* lse) {
   constexpr int V = D / 32;     // features a lane holds
-  __shared__ float s_acc[8][D], s_m[8], s_l[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
-  const long row = (long)blockIdx.x * (8 / WPR) + warp / WPR;   // (b * Hq + h) * Tq + t = (b * Hkv + hkv) * R + rr
+  constexpr int kW = WPR > 8 ? WPR : 8;
+  __shared__ float s_acc[WPR > 1 ? kW : 1][D], s_m[kW], s_l[kW];
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), part = warp % WPR;
+  const long row = (long)blockIdx.x * (kW / WPR) + warp / WPR;   // (b * Hq + h) * Tq + t = (b * Hkv + hkv) * R + rr
   const bool in = row < (long)a.B * a.Hkv * p.R;
   const int rr = (int)(row % p.R), bh = (int)(row / p.R), hkv = bh % a.Hkv, b = bh / a.Hkv, pre = b / p.W;
-  griddep_wait();               // the own-keys kernel has ended, and it ends after attn_prefix
+  const int gr = b % p.W * p.R + rr;
+  const long hp = (long)pre * a.Hkv + hkv;
+  // the lengths are older than the kernels whose partials are waited for
   const int len = in ? a.cache_lens[b] : -1, m = in ? p.prefix_lens[pre] : -1;
   const bool valid = len >= 0 && len <= a.S && m >= 0 && m <= p.Sp;      // others: reported by the kernels before
+  const bool query = valid && len - a.Tq + rr % a.Tq >= 0;
+  griddep_wait();               // the own-keys kernel has ended, and it ends after attn_prefix
   float acc[V] = {};
   float M = -INFINITY, L = 0.f;
-  if (valid && len - a.Tq + rr % a.Tq >= 0) {
-    const int gr = b % p.W * p.R + rr;
-    const long hp = (long)pre * a.Hkv + hkv;
+  if (query) {
     // the prefix's pieces: attn_prefix's, or pieces of the stream
     const float* po;
     const float2* pml;
     int np = 0, pstep;
+    const int2 own = a.counts[(long)a.P * a.Hkv * a.nrbp + (long)bh * a.nrb + rr / a.block];
     if (a.P == 0) {
       pstep = 1;
       const long at = (hp * p.Rp + gr) * p.slots;
@@ -638,43 +600,46 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs p, c
       pml = a.ws_ml + at;
       np = min(max(c.y, 0), a.warps);
     }
-    const int2 own = a.counts[(long)a.P * a.Hkv * a.nrbp + (long)bh * a.nrb + rr / a.block];
     const int n = np + min(max(own.y, 0), a.warps);
     const long obase = (long)own.x * a.rows_ws + rr % a.block;
-    auto ml_of = [&](int s) { return s < np ? pml[(long)s * pstep] : a.ws_ml[obase + (long)(s - np) * a.rows_ws]; };
-    // this warp's pieces are part + WPR * i
-    const int mine = (n - part + WPR - 1) / WPR;
-    float2 ml = lane < mine ? ml_of(part + WPR * lane) : make_float2(-INFINITY, 0.f);   // of the first 32
-    M = ml.x;
-    for (int i = 32 + lane; i < mine; i += 32) M = fmaxf(M, ml_of(part + WPR * i).x);
+    for (int s0 = part; s0 < n; s0 += WPR * kAt) {
+      float2 ml[kAt];
+      float v[kAt][V];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    for (int i0 = 0; i0 < mine; i0 += 32) {
-      if (i0 > 0) ml = i0 + lane < mine ? ml_of(part + WPR * (i0 + lane)) : make_float2(-INFINITY, 0.f);
-      const float wl = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-      L = fmaf(ml.y, wl, L);
-      const int k1 = min(32, mine - i0);
-#pragma unroll 4
-      for (int k = 0; k < k1; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, wl, k);
-        if (wk == 0.f) continue;
-        const int s = part + WPR * (i0 + k);
-        const float* src = (s < np ? po + (long)s * pstep * D : a.ws_o + (obase + (long)(s - np) * a.rows_ws) * D) + lane * V;
+      for (int k = 0; k < kAt; ++k) {
+        const int s = s0 + WPR * k;
+        const long at = s < np ? (long)s * pstep : obase + (long)(s - np) * a.rows_ws;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (s >= n) continue;
+        ml[k] = (s < np ? pml : a.ws_ml)[at];
+        const float* src = (s < np ? po : a.ws_o) + at * D + lane * V;
         if constexpr (V == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          acc[0] = fmaf(v.x, wk, acc[0]);
-          acc[1] = fmaf(v.y, wk, acc[1]);
-          acc[2] = fmaf(v.z, wk, acc[2]);
-          acc[3] = fmaf(v.w, wk, acc[3]);
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
         } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          acc[0] = fmaf(v.x, wk, acc[0]);
-          acc[1] = fmaf(v.y, wk, acc[1]);
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          v[k][0] = x.x, v[k][1] = x.y;
         }
       }
-    }
+      float top = M;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+      for (int k = 0; k < kAt; ++k) top = fmaxf(top, ml[k].x);
+      if (top == -INFINITY) continue;
+      const float scale = ex2_approx(M - top);
+      M = top;
+      L *= scale;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] *= scale;
+#pragma unroll
+      for (int k = 0; k < kAt; ++k) {
+        // a piece of weight 0 holds no key that the row sees, and its partial may be anything
+        const float w = ex2_approx(ml[k].x - top);
+        const bool any = ml[k].x > -INFINITY || ml[k].x != ml[k].x;
+        L = fmaf(ml[k].y, w, L);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = any ? fmaf(v[k][e], w, acc[e]) : acc[e];
+      }
+    }
   }
   if constexpr (WPR > 1) {
 #pragma unroll
@@ -703,7 +668,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs p, c
     M = top;
   }
   if (!valid) return;
-  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;        // 0: a query without keys
+  const float inv = query ? 1.f / L : 0.f;
   __nv_bfloat16* out = o + row * D + lane * V;
   if constexpr (V == 4) {
     *reinterpret_cast<uint2*>(out) =
@@ -711,7 +676,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs p, c
   } else {
     *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
   }
-  if (lane == 0) lse[row] = (M + __log2f(L)) * 0.69314718055994531f;   // a query without keys: -infinity
+  if (lane == 0) lse[row] = query ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int D, bool PAGED>
@@ -743,10 +708,21 @@ cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const
 template <int D>
 static cudaError_t launch_merge_d(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
   const long rows = (long)a.B * a.Hkv * p.R;
-  // few rows have many pieces each, and SMs to spare: four warps a row
-  if (rows <= 8 * 256)
-    return launch_programmatic(prefix_merge_kernel<D, 4>, dim3((unsigned)((rows + 1) / 2)), dim3(256), 0, stream, p, a, o, lse);
-  return launch_programmatic(prefix_merge_kernel<D, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, p, a, o, lse);
+  // about as many pieces as a row has, if all its keys are there: the prefix's by its CTAs or warps, its own by warps
+  const long units = (long)a.B * a.Hkv * a.nrb + (long)a.P * a.Hkv * a.nrbp;
+  long n = 2 + kOwnMaxWarps / units;
+  if (a.P > 0) n *= 2;
+  else n += (1 + p.teams / ((long)p.P * p.Hkv * p.outer)) * (p.Rp <= kPrefixRows / 2 ? 2 : 1);
+  auto go = [&](auto kernel, int wpr) {
+    const int w = wpr > 8 ? wpr : 8;
+    return launch_programmatic(kernel, dim3((unsigned)((rows * wpr + w - 1) / w)), dim3(32 * w), 0, stream, p, a, o, lse);
+  };
+  // measured (us with the launch): 8192 rows of 7 pieces, 1 warp 9 where 4 take 18; 2048 rows of 21, 4 warps by fours 8,
+  // by eights 12; 28 rows of 480, 16 warps 5, 8 warps 9
+  if (n > 160) return go(prefix_merge_kernel<D, 16, 8>, 16);
+  if (n > 40 || (n > 10 && rows <= 512)) return go(prefix_merge_kernel<D, 8, 8>, 8);
+  if (n > 10) return go(prefix_merge_kernel<D, 4, 4>, 4);
+  return go(prefix_merge_kernel<D, 1, 8>, 1);
 }
 
 cudaError_t launch_prefix_merge(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
