@@ -92,45 +92,48 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
   else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
 }
 
-// A tile of 32 keys on its way: a lane copies the parts that it uses itself (rows 8 m + g), so that nothing has to be
-// exchanged and any number of tiles can be under way without registers.
+// A tile of 32 keys on its way into shared memory, by bulk copies of the rows that lie side by side (a page's), with their
+// block scales, weights and slots: any number of tiles can be under way without registers, and a warp spends some tens of
+// instructions on one.  Rows of 128 or 256 bytes are read back two lanes a bank, which the time does not show.
 template <int D, CacheFmt F>
 struct KeyStage {
   using P = KeyPart<D, F>;
-  struct Lane { uint8_t b[P::kBytes]; };
-  static constexpr int kParts = 4 * P::kParts * 32 * P::kBytes;
-  static constexpr int kSf = F == kCacheQ4 ? 4 * 32 * 4 : 0;
-  static constexpr int kBytes = kParts + kSf + 32 * 4 + 32 * 8;   // parts, scales, weights, their slots
+  static constexpr int kKeys = 32 * P::kRowBytes;
+  static constexpr int kSfRow = F == kCacheQ4 ? D / 16 : 0;
+  static constexpr int kWeights = kKeys + 32 * kSfRow, kSlots = kWeights + 32 * 4;
+  static constexpr int kBytes = kSlots + 32 * 8;
 
-  // Keys 32 t .. of a row of len keys; returns whether a page was bad.
-  __device__ static bool issue(const WeightsArgs& a, uint8_t* st, const Slots& slot_of, int t, int len, int lane) {
-    const int g = lane >> 2, tig = lane & 3;
-    bool bad = false;
-    long mine = -1;
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int j = 32 * t + 8 * m + g;
-      const long slot = j < len ? slot_of(j) : -1;
-      bad |= j < len && slot < 0;
-      if (m == tig) mine = slot;
-      if (slot < 0) continue;      // what stands there is scored, and its weight neither written nor kept
-      const uint8_t* p = a.k + slot * P::kRowBytes + tig * P::kBytes;
-#pragma unroll
-      for (int i = 0; i < P::kParts; ++i)
-        copy_async<P::kBytes>(smem_u32(st + ((m * P::kParts + i) * 32 + lane) * P::kBytes), p + 4 * i * P::kBytes);
-      if constexpr (F == kCacheQ4)      // D = 128: 2 of the 4 bytes
-        copy_async<4>(smem_u32(st + kParts + (m * 32 + lane) * 4), a.ksf + slot * (D / 16) + (D == 128 ? tig / 2 * 4 : 0));
+  // Keys 32 t .. of a row of len keys: the copies complete on `bar` (one phase) and as one group of this lane's own.
+  // Returns whether a page was bad.
+  __device__ static bool issue(const WeightsArgs& a, uint8_t* st, uint64_t* bar, const Slots& slot_of, int t, int len, int lane) {
+    const int j = 32 * t + lane, ps = a.page.d;
+    const long slot = j < len ? slot_of(j) : -1;
+    const int in_page = slot_of.table ? j - slot_of.page(j) * ps : lane;      // 0: another page begins
+    const int run = slot_of.table ? min(ps - in_page, 32 - lane) : 32;
+    const int bytes = slot >= 0 && (lane == 0 || in_page == 0) ? min(run, len - j) * P::kRowBytes : 0;
+    const int all = __reduce_add_sync(~0u, bytes);
+    if (lane == 0) mbar_expect_tx(bar, all);
+    __syncwarp();
+    if (bytes)
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       smem_u32(st + lane * P::kRowBytes)),
+                   "l"(a.k + slot * P::kRowBytes), "r"(bytes), "r"(smem_u32(bar))
+                   : "memory");
+    if (slot >= 0) {
+      if constexpr (F == kCacheQ4) copy_async<kSfRow>(smem_u32(st + kKeys + lane * kSfRow), a.ksf + slot * kSfRow);
+      copy_async<4>(smem_u32(st + kWeights + lane * 4), a.weights + slot);
     }
-    if (mine >= 0) copy_async<4>(smem_u32(st + kParts + kSf + lane * 4), a.weights + mine);
-    *reinterpret_cast<long*>(st + kParts + kSf + 128 + lane * 8) = mine;
-    return bad;
+    *reinterpret_cast<long*>(st + kSlots + lane * 8) = slot;
+    copies_commit();
+    return j < len && slot < 0;
   }
-  __device__ static void row(const uint8_t* st, int m, int lane, KeyRow<D, F>& k) {
+  // Row `row` of the tile (8 m + g), the lane's share of it.
+  __device__ static void row(const uint8_t* st, int row, int tig, KeyRow<D, F>& k) {
+    const uint8_t* p = st + row * P::kRowBytes + tig * P::kBytes;
 #pragma unroll
     for (int i = 0; i < P::kParts; ++i) {
-      const uint8_t* p = st + ((m * P::kParts + i) * 32 + lane) * P::kBytes;
       if constexpr (P::kBytes == 16) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i * P::kBytes);
         k.w[4 * i] = v.x, k.w[4 * i + 1] = v.y, k.w[4 * i + 2] = v.z, k.w[4 * i + 3] = v.w;
       } else {
         const uint2 v = *reinterpret_cast<const uint2*>(p);
@@ -138,12 +141,13 @@ struct KeyStage {
       }
     }
     if constexpr (F == kCacheQ4) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(st + kParts + (m * 32 + lane) * 4);
-      k.sf = w >> (D == 128 ? (lane & 1) * 16 : (lane & 3) * 8);
+      const uint8_t* f = st + kKeys + row * kSfRow;
+      if constexpr (D == 128) k.sf = *reinterpret_cast<const uint16_t*>(f + 2 * tig);
+      else k.sf = f[tig];
     }
   }
-  __device__ static float weight(const uint8_t* st, int lane) { return *reinterpret_cast<const float*>(st + kParts + kSf + lane * 4); }
-  __device__ static long slot(const uint8_t* st, int lane) { return *reinterpret_cast<const long*>(st + kParts + kSf + 128 + lane * 8); }
+  __device__ static float weight(const uint8_t* st, int row) { return *reinterpret_cast<const float*>(st + kWeights + row * 4); }
+  __device__ static long slot(const uint8_t* st, int row) { return *reinterpret_cast<const long*>(st + kSlots + row * 8); }
 };
 
 // The lane's share of query row `row` (-1: none) in fragments q[s] of step s; f16: scaled by 2^e, which it returns.
@@ -200,9 +204,16 @@ __global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_ke
   using St = KeyStage<D, F>;
   constexpr int kSteps = D / 16;
   constexpr bool f16 = F != kCacheBf16;
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_sum[C::kWarps], s_pre[C::kThreads];
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_sum[C::kWarps], s_pre[C::kThreads], s_abort;
+  __shared__ uint64_t s_full[C::kWarps][C::kStages];
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31, g = lane >> 2, tig = lane & 3;
+  if (tid == 0) s_abort = 0;
+  if (lane == 0) {
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&s_full[warp][i], 1);
+    fence_barrier_init();
+  }
+  const Guard guard{&s_abort, a.status};
   griddep_wait();
   griddep_launch();
   auto tiles_of = [&](int b, int& len) {
@@ -237,15 +248,16 @@ __global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_ke
   };
   uint8_t* ring = smem + warp * (C::kStages * St::kBytes);
   int to_load = left;
-  bool bad = false;
+  bool bad = false, ok = true;
   auto issue = [&](int st) {
     if (to_load > 0) {
       const Slots slot_of{a.block_table ? a.block_table + (long)ld.b * a.max_pages : nullptr, a.num_pages, ld.b, a.page,
                           a.Hkv, ld.h};
-      bad |= St::issue(a, ring + st * St::kBytes, slot_of, ld.t, ld.len, lane);
+      bad |= St::issue(a, ring + st * St::kBytes, &s_full[warp][st], slot_of, ld.t, ld.len, lane);
       if (--to_load > 0) next(ld);
+    } else {
+      copies_commit();
     }
-    copies_commit();
   };
   At at = ld;
 #pragma unroll
@@ -254,7 +266,10 @@ __global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_ke
   float2 c[NT][2];      // of rows 8 n + 2 tig + i
   int lim[NT][2];
   bool fresh = true;
-  for (int st = 0; left > 0; --left, st = st + 1 == C::kStages ? 0 : st + 1) {
+  uint32_t phase = 0;
+  int st = 0;
+  for (; left > 0; --left) {
+    __syncwarp();        // the stage before is read
     issue(st == 0 ? C::kStages - 1 : st - 1);
     if (fresh) {
       const long row0 = ((long)at.b * a.Hkv + at.h) * a.R;
@@ -272,13 +287,16 @@ __global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_ke
       fresh = false;
     }
     copies_wait<C::kStages - 1>();
+    ok = __all_sync(~0u, mbar_wait(&s_full[warp][st], phase, guard));
+    if (!ok) break;
+    __syncwarp();        // the other lanes' copies have landed too
     const uint8_t* sp = ring + st * St::kBytes;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       KeyRow<D, F> k0, k1;      // keys 16 m + g and 16 m + 8 + g
-      St::row(sp, 2 * m, lane, k0);
-      St::row(sp, 2 * m + 1, lane, k1);
+      St::row(sp, 16 * m + g, tig, k0);
+      St::row(sp, 16 * m + 8 + g, tig, k1);
       float acc[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
@@ -308,15 +326,27 @@ __global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_ke
       sum[m] += __shfl_xor_sync(~0u, sum[m], 2);
     }
     const float mine = tig == 0 ? sum[0] : tig == 1 ? sum[1] : tig == 2 ? sum[2] : sum[3];
-    const long slot = St::slot(sp, lane);
+    const int r = 8 * tig + g;
+    const long slot = St::slot(sp, r);
     // the step's new keys had no weight before
-    if (slot >= 0) a.weights[slot] = mine + (32 * at.t + 8 * tig + g < at.len - a.Tq ? St::weight(sp, lane) : 0.f);
+    if (slot >= 0) a.weights[slot] = mine + (32 * at.t + r < at.len - a.Tq ? St::weight(sp, r) : 0.f);
     if (left > 1) {
       fresh = at.t + 1 == at.nb;
       next(at);
     }
+    if (++st == C::kStages) {
+      st = 0;
+      phase ^= 1;
+    }
   }
+  // never leave with copies in flight (after a wait that gave up)
   copies_wait<0>();
+  if (lane == 0)
+    for (int i = left - to_load; i > 0; --i) {
+      mbar_wait_drain(&s_full[warp][st], phase);
+      if (++st == C::kStages) st = 0, phase ^= 1;
+    }
+  __syncwarp();
   if (bad) atomicCAS(a.status, 0, kDevBadPage);
 }
 
@@ -327,7 +357,9 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
   using St = KeyStage<D, F>;
   constexpr int kSteps = D / 16;
   constexpr bool f16 = F != kCacheBf16;
-  extern __shared__ __align__(16) uint8_t smem[];   // a stage a warp
+  extern __shared__ __align__(128) uint8_t smem[];  // a stage a warp
+  __shared__ uint64_t s_full[kWWarps];
+  __shared__ int s_abort;
   __shared__ uint2 s_q[kWRows / 8][kSteps][32];     // query fragments, by lane
   __shared__ float2 s_c[kWRows];
   __shared__ int s_t[kWRows];                       // query position of the row
@@ -342,11 +374,18 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
     return;
   }
   if (c0 >= len) return;
+  if (threadIdx.x == 0) s_abort = 0;
+  if (lane == 0) {
+    mbar_init(&s_full[warp], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const Guard guard{&s_abort, a.status};
   const int k0 = c0 + warp * 32;
   uint8_t* sp = smem + warp * St::kBytes;
   const Slots slot_of{a.block_table ? a.block_table + (long)b * a.max_pages : nullptr, a.num_pages, b, a.page, a.Hkv, hkv};
-  if (St::issue(a, sp, slot_of, k0 / 32, len, lane)) atomicCAS(a.status, 0, kDevBadPage);
-  copies_commit();
+  if (St::issue(a, sp, &s_full[warp], slot_of, k0 / 32, len, lane)) atomicCAS(a.status, 0, kDevBadPage);
+  bool ok = true;
   uint32_t f[2][kSteps][4];
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   for (int r0 = 0; r0 < a.R; r0 += kWRows) {
@@ -367,11 +406,12 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
     }
     if (r0 == 0) {
       copies_wait<0>();
+      ok = __all_sync(~0u, mbar_wait(&s_full[warp], 0, guard));      // and, as a barrier, the other lanes' copies
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         KeyRow<D, F> x, y;
-        St::row(sp, 2 * m, lane, x);
-        St::row(sp, 2 * m + 1, lane, y);
+        St::row(sp, 16 * m + g, tig, x);
+        St::row(sp, 16 * m + 8 + g, tig, y);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           x.step(s, f[m][s][0], f[m][s][2]);
@@ -409,9 +449,11 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
     sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], 2);
   }
   const float mine = tig == 0 ? sum[0] : tig == 1 ? sum[1] : tig == 2 ? sum[2] : sum[3];
-  const long slot = St::slot(sp, lane);
+  const int r = 8 * tig + g;
+  const long slot = St::slot(sp, r);
   // the step's new keys had no weight before
-  if (slot >= 0) a.weights[slot] = mine + (k0 + 8 * tig + g < len - a.Tq ? St::weight(sp, lane) : 0.f);
+  if (ok && slot >= 0) a.weights[slot] = mine + (k0 + r < len - a.Tq ? St::weight(sp, r) : 0.f);
+  if (!ok) mbar_wait_drain(&s_full[warp], 0);        // never leave with copies in flight
 }
 
 template <auto KERNEL>
