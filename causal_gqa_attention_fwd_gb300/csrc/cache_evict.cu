@@ -65,20 +65,23 @@ struct KeyRow {
   using P = KeyPart<D, F>;
   uint32_t w[P::kWords];
   uint32_t sf;      // 4-bit: the block scales of the lane's features
-  // The 16-bit pairs (features 4 s, +1) and (+2, +3) of step s.
-  __device__ __forceinline__ void step(int s, uint32_t& lo, uint32_t& hi) const {
+  // The 16-bit pairs of steps 2 s (r[0], r[1]: its features 0, 1 and 2, 3) and 2 s + 1 (r[2], r[3]).
+  __device__ __forceinline__ void steps(int s, uint32_t* r) const {
     if constexpr (F == kCacheBf16) {
-      lo = w[2 * s];
-      hi = w[2 * s + 1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = w[4 * s + i];
     } else if constexpr (F == kCacheE4m3) {
-      lo = e4m3x2_to_f16(w[s] & 0xffffu);
-      hi = e4m3x2_to_f16(w[s] >> 16);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        r[2 * i] = e4m3x2_to_f16(w[2 * s + i] & 0xffffu);
+        r[2 * i + 1] = e4m3x2_to_f16(w[2 * s + i] >> 16);
+      }
     } else {
-      uint32_t h[4];      // 8 codes: steps 2 s', 2 s' + 1; the unused half is dropped by the compiler
-      e2m1x8_to_f16(w[s / 2], h);
-      const uint32_t byte = (sf >> (s / 4 * 8)) & 0xffu, two = e4m3x2_to_f16(byte | byte << 8);
-      lo = hmul2_u(h[2 * (s & 1)], two);
-      hi = hmul2_u(h[2 * (s & 1) + 1], two);
+      const uint32_t both = e4m3x2_to_f16(sf);      // of features 0-15 and (D = 128) 16-31
+      const uint32_t two = __byte_perm(both, both, s / 2 ? 0x3232 : 0x1010);
+      e2m1x8_to_f16(w[s], r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = hmul2_u(r[i], two);
     }
   }
 };
@@ -103,13 +106,20 @@ struct KeyStage {
   static constexpr int kWeights = kKeys + 32 * kSfRow, kSlots = kWeights + 32 * 4;
   static constexpr int kBytes = kSlots + 32 * 8;
 
-  // Keys 32 t .. of a row of len keys: the copies complete on `bar` (one phase) and as one group of this lane's own.
-  // Returns whether a page was bad.
-  __device__ static bool issue(const WeightsArgs& a, uint8_t* st, uint64_t* bar, const Slots& slot_of, int t, int len, int lane) {
+  // The block table's entry for this lane's key (row b itself in a contiguous cache): looked up a tile ahead, for what it
+  // takes to come is time that the warp stands still.
+  __device__ static int page_of(const WeightsArgs& a, int b, int t, int len, int lane) {
+    const int j = 32 * t + lane;
+    return a.block_table && j < len ? a.block_table[(long)b * a.max_pages + a.page(j)] : b;
+  }
+  // Keys 32 t .. of head h of a row of len keys: the copies complete on `bar` (one phase) and as one group of this lane's
+  // own.  Returns whether a page was bad.
+  __device__ static bool issue(const WeightsArgs& a, uint8_t* st, uint64_t* bar, int page, int h, int t, int len, int lane) {
     const int j = 32 * t + lane, ps = a.page.d;
-    const long slot = j < len ? slot_of(j) : -1;
-    const int in_page = slot_of.table ? j - slot_of.page(j) * ps : lane;      // 0: another page begins
-    const int run = slot_of.table ? min(ps - in_page, 32 - lane) : 32;
+    const int in_page = a.block_table ? j - a.page(j) * ps : j;               // 0: another page begins
+    const int run = a.block_table ? min(ps - in_page, 32 - lane) : 32;
+    const bool there = j < len && page >= 0 && page < a.num_pages;
+    const long slot = there ? ((long)page * a.Hkv + h) * ps + in_page : -1;
     const int bytes = slot >= 0 && (lane == 0 || in_page == 0) ? min(run, len - j) * P::kRowBytes : 0;
     const int all = __reduce_add_sync(~0u, bytes);
     if (lane == 0) mbar_expect_tx(bar, all);
@@ -181,16 +191,21 @@ __device__ __forceinline__ int query_fragments(const WeightsArgs& a, long row, i
   return e;
 }
 
-// Score factor and -lse of a query row, in log2 units; factor NaN: no query.
-__device__ __forceinline__ float2 row_constants(const WeightsArgs& a, long row, int e) {
+// Score factor and -lse of a query row, in log2 units, and the last key that it sees (none: no key, nor does a query
+// that the caller's attention found to see none).
+struct RowConstants {
+  float c, l;
+  int lim;
+};
+__device__ __forceinline__ RowConstants row_constants(const WeightsArgs& a, long row, int e, int lim) {
   const float lse = row >= 0 ? __ldg(a.lse + row) : -INFINITY;
-  return lse == -INFINITY ? make_float2(NAN, 0.f) : make_float2(ldexpf(a.scale_log2, -e), -lse * 1.4426950408889634f);
+  return {ldexpf(a.scale_log2, -e), -lse * 1.4426950408889634f, lse == -INFINITY ? -1 : lim};
 }
 
 // ------------------------------------------------ at most 8 NT query rows a key: one stream of tiles over all warps
-template <int D, CacheFmt F>
+template <int D, CacheFmt F, int NT>
 struct NarrowCfg {
-  static constexpr int kWarps = F == kCacheQ4 ? 16 : 12;
+  static constexpr int kWarps = F == kCacheQ4 ? (NT == 1 ? 20 : 16) : 12;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kFit = (216 << 10) / (kWarps * KeyStage<D, F>::kBytes);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -199,8 +214,8 @@ struct NarrowCfg {
 };
 
 template <int D, CacheFmt F, int NT>
-__global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_kernel(const WeightsArgs a) {
-  using C = NarrowCfg<D, F>;
+__global__ void __launch_bounds__(NarrowCfg<D, F, NT>::kThreads, 1) cache_weights_kernel(const WeightsArgs a) {
+  using C = NarrowCfg<D, F, NT>;
   using St = KeyStage<D, F>;
   constexpr int kSteps = D / 16;
   constexpr bool f16 = F != kCacheBf16;
@@ -247,14 +262,15 @@ __global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_ke
     while (x.nb == 0);
   };
   uint8_t* ring = smem + warp * (C::kStages * St::kBytes);
-  int to_load = left;
+  int to_load = left, page = St::page_of(a, ld.b, ld.t, ld.len, lane);
   bool bad = false, ok = true;
   auto issue = [&](int st) {
     if (to_load > 0) {
-      const Slots slot_of{a.block_table ? a.block_table + (long)ld.b * a.max_pages : nullptr, a.num_pages, ld.b, a.page,
-                          a.Hkv, ld.h};
-      bad |= St::issue(a, ring + st * St::kBytes, &s_full[warp][st], slot_of, ld.t, ld.len, lane);
-      if (--to_load > 0) next(ld);
+      bad |= St::issue(a, ring + st * St::kBytes, &s_full[warp][st], page, ld.h, ld.t, ld.len, lane);
+      if (--to_load > 0) {
+        next(ld);
+        page = St::page_of(a, ld.b, ld.t, ld.len, lane);
+      }
     } else {
       copies_commit();
     }
@@ -263,8 +279,7 @@ __global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_ke
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) issue(i);
   uint2 q[NT][kSteps];
-  float2 c[NT][2];      // of rows 8 n + 2 tig + i
-  int lim[NT][2];
+  RowConstants c[NT][2];      // of rows 8 n + 2 tig + i
   bool fresh = true;
   uint32_t phase = 0;
   int st = 0;
@@ -280,8 +295,7 @@ __global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_ke
         for (int i = 0; i < 2; ++i) {
           const int r = 8 * n + 2 * tig + i;
           const int er = __shfl_sync(~0u, e, 4 * (2 * tig + i));
-          c[n][i] = row_constants(a, r < a.R ? row0 + r : -1, er);
-          lim[n][i] = at.len - a.Tq + r % a.Tq;
+          c[n][i] = row_constants(a, r < a.R ? row0 + r : -1, er, at.len - a.Tq + r % a.Tq);
         }
       }
       fresh = false;
@@ -301,23 +315,26 @@ __global__ void __launch_bounds__(NarrowCfg<D, F>::kThreads, 1) cache_weights_ke
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        uint32_t f[4];
-        k0.step(s, f[0], f[2]);
-        k1.step(s, f[1], f[3]);
+      for (int s = 0; s < kSteps / 2; ++s) {
+        uint32_t f0[4], f1[4];
+        k0.steps(s, f0);
+        k1.steps(s, f1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_16816(acc[n], f, q[n][s].x, q[n][s].y, f16);
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t f[4] = {f0[2 * i], f1[2 * i], f0[2 * i + 1], f1[2 * i + 1]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_16816(acc[n], f, q[n][2 * s + i].x, q[n][2 * s + i].y, f16);
+        }
       }
       const int j = 32 * at.t + 16 * m + g;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const bool query = !(c[n][i].x != c[n][i].x);
-          const float p0 = ex2_approx(fmaf(acc[n][i], c[n][i].x, c[n][i].y));
-          const float p1 = ex2_approx(fmaf(acc[n][2 + i], c[n][i].x, c[n][i].y));
-          sum[2 * m] += query && j <= lim[n][i] ? p0 : 0.f;
-          sum[2 * m + 1] += query && j + 8 <= lim[n][i] ? p1 : 0.f;
+          const float p0 = ex2_approx(fmaf(acc[n][i], c[n][i].c, c[n][i].l));
+          const float p1 = ex2_approx(fmaf(acc[n][2 + i], c[n][i].c, c[n][i].l));
+          if (j <= c[n][i].lim) sum[2 * m] += p0;
+          if (j + 8 <= c[n][i].lim) sum[2 * m + 1] += p1;
         }
     }
 #pragma unroll
@@ -361,8 +378,7 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
   __shared__ uint64_t s_full[kWWarps];
   __shared__ int s_abort;
   __shared__ uint2 s_q[kWRows / 8][kSteps][32];     // query fragments, by lane
-  __shared__ float2 s_c[kWRows];
-  __shared__ int s_t[kWRows];                       // query position of the row
+  __shared__ RowConstants s_c[kWRows];
   griddep_wait();
   griddep_launch();
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
@@ -383,8 +399,8 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
   const Guard guard{&s_abort, a.status};
   const int k0 = c0 + warp * 32;
   uint8_t* sp = smem + warp * St::kBytes;
-  const Slots slot_of{a.block_table ? a.block_table + (long)b * a.max_pages : nullptr, a.num_pages, b, a.page, a.Hkv, hkv};
-  if (St::issue(a, sp, &s_full[warp], slot_of, k0 / 32, len, lane)) atomicCAS(a.status, 0, kDevBadPage);
+  if (St::issue(a, sp, &s_full[warp], St::page_of(a, b, k0 / 32, len, lane), hkv, k0 / 32, len, lane))
+    atomicCAS(a.status, 0, kDevBadPage);
   bool ok = true;
   uint32_t f[2][kSteps][4];
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -400,8 +416,7 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) s_q[t][s][lane] = q[s];
       if (tig == 0) {
-        s_c[r] = row_constants(a, row, e);
-        s_t[r] = (r0 + r) % a.Tq;
+        s_c[r] = row_constants(a, row, e, len - a.Tq + (r0 + r) % a.Tq);
       }
     }
     if (r0 == 0) {
@@ -413,9 +428,14 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
         St::row(sp, 16 * m + g, tig, x);
         St::row(sp, 16 * m + 8 + g, tig, y);
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          x.step(s, f[m][s][0], f[m][s][2]);
-          y.step(s, f[m][s][1], f[m][s][3]);
+        for (int s = 0; s < kSteps / 2; ++s) {
+          uint32_t f0[4], f1[4];
+          x.steps(s, f0);
+          y.steps(s, f1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            f[m][2 * s + i][0] = f0[2 * i], f[m][2 * s + i][1] = f1[2 * i], f[m][2 * s + i][2] = f0[2 * i + 1],
+                            f[m][2 * s + i][3] = f1[2 * i + 1];
         }
       }
     }
@@ -432,13 +452,11 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 8 * t + 2 * tig + i;
-        const float2 c = s_c[r];
-        const bool query = !(c.x != c.x);
-        const int lim = len - a.Tq + s_t[r] - k0;      // last key the row sees
+        const RowConstants c = s_c[r];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const float p = ex2_approx(fmaf(acc[m / 2][2 * (m & 1) + i], c.x, c.y));
-          sum[m] += query && 8 * m + g <= lim ? p : 0.f;
+          const float p = ex2_approx(fmaf(acc[m / 2][2 * (m & 1) + i], c.c, c.l));
+          if (k0 + 8 * m + g <= c.lim) sum[m] += p;
         }
       }
     }
@@ -471,9 +489,10 @@ cudaError_t launch_weights(dim3 grid, int threads, int smem, const WeightsArgs& 
 
 template <int D, CacheFmt F>
 cudaError_t launch_weights_df(const WeightsArgs& a, int sms, cudaStream_t stream) {
-  using C = NarrowCfg<D, F>;
-  if (a.R <= 8) return launch_weights<cache_weights_kernel<D, F, 1>>(dim3(sms), C::kThreads, C::kSmemBytes, a, stream);
-  if (a.R <= 16) return launch_weights<cache_weights_kernel<D, F, 2>>(dim3(sms), C::kThreads, C::kSmemBytes, a, stream);
+  using C1 = NarrowCfg<D, F, 1>;
+  using C2 = NarrowCfg<D, F, 2>;
+  if (a.R <= 8) return launch_weights<cache_weights_kernel<D, F, 1>>(dim3(sms), C1::kThreads, C1::kSmemBytes, a, stream);
+  if (a.R <= 16) return launch_weights<cache_weights_kernel<D, F, 2>>(dim3(sms), C2::kThreads, C2::kSmemBytes, a, stream);
   const dim3 grid((unsigned)((long)a.B * a.Hkv * ((a.S + (long)kWKeys - 1) / kWKeys)));
   return launch_weights<cache_weights_wide_kernel<D, F>>(grid, 32 * kWWarps, kWWarps * KeyStage<D, F>::kBytes, a, stream);
 }
