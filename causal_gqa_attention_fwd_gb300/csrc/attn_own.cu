@@ -27,7 +27,7 @@ namespace gqa {
 namespace {
 
 constexpr int kUnitCost = 2;        // tiles that a unit counts more than it has
-constexpr int kMinShare = 4;        // least tiles (so counted) a warp takes
+constexpr int kMinShare = 2;        // least tiles (so counted) a warp takes
 constexpr float kRescale = 8.0f;    // log2 units: the maximum in use moves when a score exceeds it by more
 constexpr int kDevPages = 11;       // ATTN_ERR_PAGES
 
