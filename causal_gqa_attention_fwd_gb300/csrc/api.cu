@@ -848,9 +848,8 @@ attn_status attn_decode_paged_fp8_fwd(const void* q, const void* k8_pages, const
 namespace {
 
 // Work layout of the prefix kernel, as the decode plan a pure function of the
-// sizes.  The width of a team divides the row blocks and is the largest that
-// leaves at most 6% of the CTAs without work (of 152: 1, 2, 4, 8, 19, ... row
-// blocks do).
+// sizes.  The width of a team divides the row blocks and is the largest up to a
+// quarter of the CTAs that leaves at most 6% of them without work.
 struct PrefixPlan {
   int W, R, Rp, nrt, width, outer, slots;
   long units;
@@ -863,7 +862,7 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int Tq, int P, int Sp) {
   p.Rp = p.W * p.R;
   p.nrt = (p.Rp + gqa::kPrefixRows - 1) / gqa::kPrefixRows;
   constexpr int kCtas = 152;
-  for (int w = 1; w <= p.nrt && w <= kCtas; ++w)
+  for (int w = 1; w <= p.nrt && w <= kCtas / 4; ++w)
     if (p.nrt % w == 0 && kCtas / w * w * 100 >= 94 * kCtas) p.width = w;
   p.outer = p.nrt / p.width;
   p.units = (long)P * Hkv * p.nrt;
@@ -951,6 +950,7 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   const PrefixWs w = prefix_ws(p, d, P, Hkv, D);
   char* ws = static_cast<char*>(workspace);
   const int ctas = sms < gqa::kDecodeMaxSlots ? sms : gqa::kDecodeMaxSlots;   // one a SM, as decode
+  if (ctas < 2) return ATTN_ERR_ARCH;
   gqa::PrefixArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.prefix_lens = prefix_lens;
@@ -966,12 +966,10 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   a.R = p.R;
   a.Rp = p.Rp;
   a.nrt = p.nrt;
-  // a device of fewer SMs than a team has CTAs: teams of one
-  a.width = p.width <= ctas ? p.width : 1;
+  // a device with fewer SMs than two teams have CTAs: teams of one
+  a.width = 2 * p.width <= ctas ? p.width : 1;
   a.outer = p.nrt / a.width;
-  const long blocks = (long)P * Hkv * a.outer * ((Sp + 127L) / 128);
-  a.teams = ctas / a.width;
-  if (a.teams > blocks) a.teams = blocks > 0 ? (int)blocks : 1;
+  a.ctas = ctas;
   a.Sp = Sp;
   a.slots = p.slots;
   a.page_size = page_size;
@@ -1001,7 +999,6 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   e.S = S;
   e.Sp = Sp;
   e.max_prefix_pages = max_prefix_pages;
-  e.beside = !d.stream;
   e.D = D;
   e.page_size = page_size;
   e.max_pages = max_pages;
@@ -1009,8 +1006,7 @@ attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMa
   e.ctas = ctas;
   e.scale_log2 = a.scale_log2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t err = d.stream ? cudaSuccess : gqa::launch_attn_prefix(pk, pv, a, D, s);
-  if (err == cudaSuccess) err = gqa::launch_attn_own(maps, e, s);
+  cudaError_t err = d.stream ? gqa::launch_attn_own(maps, e, s) : gqa::launch_attn_prefix(pk, pv, a, maps, e, s);
   if (err == cudaSuccess) err = gqa::launch_prefix_merge(a, e, static_cast<__nv_bfloat16*>(o), lse, s);
   return launch_status(err);
 }

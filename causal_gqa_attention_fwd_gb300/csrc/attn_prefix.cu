@@ -23,8 +23,7 @@
 //   where a page is shorter than a block), warp 1 MMA issuer, warps 4-7 and
 //   8-11 softmax of a tile each, thread = row; they also gather the query rows
 //   (a tile's rows lie in runs of G * Tq in memory) and write the partials.
-#include "kernels.h"
-#include "sm103.cuh"
+#include "own_keys.cuh"
 
 namespace gqa {
 
@@ -33,7 +32,6 @@ namespace {
 constexpr int kBM = 128;                   // query rows per tile
 constexpr int kBN = 128;                   // keys per block
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: lazy O rescale
-constexpr int kDevPages = 11;              // ATTN_ERR_PAGES
 
 template <int D>
 struct PreCfg {
@@ -83,7 +81,7 @@ struct Walk {
   int T;               // teams with a share
   int p, nb;           // prefix of the piece, its blocks
   long Pb;             // stream index of prefix p's first block
-  int inner;
+  int team, inner;
   bool valid;
 };
 
@@ -103,7 +101,7 @@ __device__ __forceinline__ void walk_piece(const PrefixArgs& a, Walk& w) {
   it.split = it.rows <= kBM;
   const long Pg = w.Pb + (long)group * w.nb;
   const int first = team_of(Pg, w.C, w.T);
-  it.slot = (int)(blockIdx.x / a.width) - first;
+  it.slot = w.team - first;
   it.npieces = team_of(Pg + w.nb - 1, w.C, w.T) - first + 1;
   w.valid = true;
 }
@@ -123,27 +121,19 @@ __device__ __forceinline__ void walk_next(const PrefixArgs& a, Walk& w) {
   walk_piece(a, w);
 }
 
-// The walk of this CTA's team from its start (one warp).
-__device__ Walk walk_begin(const PrefixArgs& a) {
+// The walk of CTA `cta` of `ctas` from its start (one warp).
+__device__ Walk walk_begin(const PrefixArgs& a, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
   const long gpp = (long)a.Hkv * a.outer;
   long C = 0;
-  bool bad = false;
-  for (int p0 = 0; p0 < a.P; p0 += 32) {
-    int n = 0;
-    if (p0 + lane < a.P) {
-      const int m = a.prefix_lens[p0 + lane];
-      bad |= m < 0 || m > a.Sp;
-      n = prefix_blocks(a, p0 + lane);
-    }
-    C += gpp * (long)__reduce_add_sync(0xffffffffu, (unsigned)n);
-  }
-  if (__any_sync(0xffffffffu, bad) && blockIdx.x == 0 && lane == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+  for (int p0 = 0; p0 < a.P; p0 += 32)
+    C += gpp * (long)__reduce_add_sync(0xffffffffu, p0 + lane < a.P ? (unsigned)prefix_blocks(a, p0 + lane) : 0u);
   Walk w{};
   w.C = C;
-  w.T = (int)min((long)a.teams, C);
-  const int team = blockIdx.x / a.width;
-  w.inner = blockIdx.x % a.width;
+  w.T = (int)min((long)(ctas / a.width), C);
+  const int team = cta / a.width;
+  w.team = team;
+  w.inner = cta % a.width;
   w.valid = false;
   if (team >= w.T) return w;
   w.g = (long)team * C / w.T;
@@ -174,10 +164,59 @@ __device__ Walk walk_begin(const PrefixArgs& a) {
 
 }  // namespace
 
-template <int D, bool PAGED>
+// How many of the grid's G CTAs take the rows' own keys, the others the prefixes: so that both end at the same time, by
+// what they were measured to take.  An SM by itself streams kOwnTile ns a 8 KB tile, all of them together kOwnTileAll;
+// two tiles of 128 query rows take kPair ns a block of 128 keys, one kSplit.  All threads call this.
+constexpr float kOwnStart = 6000.f, kOwnTile = 95.f, kOwnTileAll = 1.25f;
+constexpr float kPreStart = 8000.f, kPair = 1550.f, kSplit = 950.f;
+
+template <int KT>
+__device__ int own_ctas(const PrefixArgs& p, const OwnArgs& a, int G, int* s_red) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int tiles = 0, blocks = 0;
+  for (int b = tid; b < a.B; b += 384) {
+    int len;
+    const int nb = row_tiles<KT>(a, b, len);
+    if (nb == 0 && len != 0 && blockIdx.x == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+    tiles += nb;
+  }
+  for (int i = tid; i < p.P; i += 384) {
+    const int m = p.prefix_lens[i];
+    if ((m < 0 || m > p.Sp) && blockIdx.x == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+    blocks += prefix_blocks(p, i);
+  }
+  tiles = __reduce_add_sync(~0u, tiles);
+  blocks = __reduce_add_sync(~0u, blocks);
+  if (lane == 0) s_red[warp] = tiles, s_red[12 + warp] = blocks;
+  __syncthreads();
+  tiles = blocks = 0;
+#pragma unroll
+  for (int w = 0; w < 12; ++w) tiles += s_red[w], blocks += s_red[12 + w];
+  if (tiles == 0) return 0;
+  if (blocks == 0) return G;
+  const float own = (float)tiles * (a.Hkv * a.nrb);
+  const int last = p.Rp - (p.nrt - 1) * kPrefixRows;     // rows of the last unit
+  const float pre = (float)blocks * (p.Hkv * p.outer) * (p.nrt == 1 && last <= kBM ? kSplit : kPair);
+  unsigned best = ~0u;
+  if (tid >= 1 && tid <= G - p.width) {
+    const float t_own = kOwnStart + fmaxf(own * kOwnTile / tid, own * kOwnTileAll);
+    const float t_pre = kPreStart + pre / ((G - tid) / p.width);
+    best = (unsigned)fminf(fmaxf(t_own, t_pre), 1.6e7f) << 8 | tid;
+  }
+  best = __reduce_min_sync(~0u, best);
+  __syncthreads();
+  if (lane == 0) s_red[warp] = (int)best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 12; ++w) best = min(best, (unsigned)s_red[w]);
+  return best & 255u;
+}
+
+template <int D, bool PAGED, int NT>
 __global__ void __launch_bounds__(384, 1)
     attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const PrefixArgs a) {
+                       const __grid_constant__ CUtensorMap tm_ok, const __grid_constant__ CUtensorMap tm_ov,
+                       const PrefixArgs a, const OwnArgs own) {
   using C = PreCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -185,12 +224,27 @@ __global__ void __launch_bounds__(384, 1)
   uint8_t* sRing = smem + 2 * C::kTileBytes;   // kStages tiles: K_0, V_0, K_1, ...
   __shared__ PreBarriers bars;
   __shared__ Walk s_walk;
+  __shared__ int s_red[24];
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // the same in a warp, told so
   Guard guard{&bars.abort, a.status};
+  if (threadIdx.x == 0) bars.abort = 0;
+  griddep_wait();
+  griddep_launch();
+
+  // ------------------------------------------------ this CTA's part: own keys (spread evenly over the grid) or prefixes
+  const int G = gridDim.x, X = __shfl_sync(~0u, own_ctas<OwnCfg<D, NT>::KT>(a, own, G, s_red), 0);
+  const int before = blockIdx.x * X / G;       // own-key CTAs of lower number
+  if ((blockIdx.x + 1) * X / G > before) {
+    using O = OwnCfg<D, NT>;
+    auto& shared = *reinterpret_cast<OwnShared<D, NT, 384>*>(smem + O::kWarps * O::kStages * O::kStage);   // behind the rings
+    const int gw = warp < O::kWarps ? warp * X + before : kOwnIdle;
+    own_keys<D, PAGED, NT, 384>(smem, shared, tm_ok, tm_ov, tm_ok, tm_ov, own, gw, X * O::kWarps, guard);
+    return;
+  }
+  const int cta = blockIdx.x - before, ctas = G - X;
 
   if (threadIdx.x == 0) {
-    bars.abort = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 4);     // one arrive per softmax warp
       mbar_init(&bars.s_full[i], 1);
@@ -209,16 +263,14 @@ __global__ void __launch_bounds__(384, 1)
     tmem_alloc(&bars.tmem_base, 512);
     tmem_relinquish();
   }
-  griddep_wait();     // the inputs may come from the previous grid
   if (warp == 0) {
-    const Walk w0 = walk_begin(a);
+    const Walk w0 = walk_begin(a, cta, ctas);
     if (lane == 0) s_walk = w0;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
-  griddep_launch();   // every CTA is past its wait: attn_own may read what the grids before wrote
 
   if (warp == 0) {
     // ======================================================== TMA producer
@@ -577,7 +629,7 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) prefix_merge_kernel(
   const int len = in ? a.cache_lens[b] : -1, m = in ? p.prefix_lens[pre] : -1;
   const bool valid = len >= 0 && len <= a.S && m >= 0 && m <= p.Sp;      // others: reported by the kernels before
   const bool query = valid && len - a.Tq + rr % a.Tq >= 0;
-  griddep_wait();               // the own-keys kernel has ended, and it ends after attn_prefix
+  griddep_wait();               // the kernel that leaves the pieces has ended
   float acc[V] = {};
   float M = -INFINITY, L = 0.f;
   if (query) {
@@ -598,9 +650,9 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) prefix_merge_kernel(
       const long at = (long)c.x * a.rows_ws + gr % a.block;
       po = a.ws_o + at * D;
       pml = a.ws_ml + at;
-      np = min(max(c.y, 0), a.warps);
+      np = min(max(c.y, 0), kOwnMaxWarps);
     }
-    const int n = np + min(max(own.y, 0), a.warps);
+    const int n = np + min(max(own.y, 0), kOwnMaxWarps);
     const long obase = (long)own.x * a.rows_ws + rr % a.block;
     for (int s0 = part; s0 < n; s0 += WPR * kAt) {
       float2 ml[kAt];
@@ -679,30 +731,39 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) prefix_merge_kernel(
   if (lane == 0) lse[row] = query ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
-template <int D, bool PAGED>
-static cudaError_t launch_prefix_dp(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& a, cudaStream_t stream) {
-  using C = PreCfg<D>;
+template <int D, bool PAGED, int NT>
+static cudaError_t launch_prefix_dp(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& p, const OwnMaps& m,
+                                    const OwnArgs& a, cudaStream_t stream) {
+  constexpr int kOwn = OwnCfg<D, NT>::kSmemBytes + (int)sizeof(OwnShared<D, NT, 384>);
+  constexpr int kSmem = PreCfg<D>::kSmemBytes > kOwn ? PreCfg<D>::kSmemBytes : kOwn;
+  static_assert(kSmem + 1024 <= 232448, "shared memory");
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !attr_set[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(attn_prefix_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        cudaFuncSetAttribute(attn_prefix_kernel<D, PAGED, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set[dev] = true;
   }
   prof_begin(kProfPrefix, stream);
-  const cudaError_t e = launch_programmatic(attn_prefix_kernel<D, PAGED>, dim3(a.teams * a.width), dim3(384),
-                                            C::kSmemBytes, stream, k, v, a);
+  const cudaError_t e = launch_programmatic(attn_prefix_kernel<D, PAGED, NT>, dim3(p.ctas), dim3(384), kSmem, stream, k, v,
+                                            m.k, m.v, p, a);
   prof_end(stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& a, int D,
-                               cudaStream_t stream) {
-  if (D == 128)
-    return a.table ? launch_prefix_dp<128, true>(k, v, a, stream) : launch_prefix_dp<128, false>(k, v, a, stream);
-  return a.table ? launch_prefix_dp<64, true>(k, v, a, stream) : launch_prefix_dp<64, false>(k, v, a, stream);
+template <int D>
+static cudaError_t launch_prefix_d(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& p, const OwnMaps& m,
+                                   const OwnArgs& a, cudaStream_t stream) {
+  if (a.block == 8)
+    return p.table ? launch_prefix_dp<D, true, 1>(k, v, p, m, a, stream) : launch_prefix_dp<D, false, 1>(k, v, p, m, a, stream);
+  return p.table ? launch_prefix_dp<D, true, 2>(k, v, p, m, a, stream) : launch_prefix_dp<D, false, 2>(k, v, p, m, a, stream);
+}
+
+cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& p, const OwnMaps& m,
+                               const OwnArgs& a, cudaStream_t stream) {
+  return a.D == 128 ? launch_prefix_d<128>(k, v, p, m, a, stream) : launch_prefix_d<64>(k, v, p, m, a, stream);
 }
 
 template <int D>
@@ -712,7 +773,7 @@ static cudaError_t launch_merge_d(const PrefixArgs& p, const OwnArgs& a, __nv_bf
   const long units = (long)a.B * a.Hkv * a.nrb + (long)a.P * a.Hkv * a.nrbp;
   long n = 2 + kOwnMaxWarps / units;
   if (a.P > 0) n *= 2;
-  else n += (1 + p.teams / ((long)p.P * p.Hkv * p.outer)) * (p.Rp <= kPrefixRows / 2 ? 2 : 1);
+  else n += (1 + p.ctas / p.width / ((long)p.P * p.Hkv * p.outer)) * (p.Rp <= kPrefixRows / 2 ? 2 : 1);
   auto go = [&](auto kernel, int wpr) {
     const int w = wpr > 8 ? wpr : 8;
     return launch_programmatic(kernel, dim3((unsigned)((rows * wpr + w - 1) / w)), dim3(32 * w), 0, stream, p, a, o, lse);
@@ -726,10 +787,8 @@ static cudaError_t launch_merge_d(const PrefixArgs& p, const OwnArgs& a, __nv_bf
 }
 
 cudaError_t launch_prefix_merge(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
-  OwnArgs x = a;
-  x.warps = kOwnMaxWarps;
   prof_begin(kProfPrefixMerge, stream);
-  const cudaError_t e = a.D == 128 ? launch_merge_d<128>(p, x, o, lse, stream) : launch_merge_d<64>(p, x, o, lse, stream);
+  const cudaError_t e = a.D == 128 ? launch_merge_d<128>(p, a, o, lse, stream) : launch_merge_d<64>(p, a, o, lse, stream);
   prof_end(stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -149,12 +149,10 @@ struct PrefixArgs {
   int* counts;              // [units] slots in use
   int* status;
   int* dbg_line;
-  int P, W, Hkv, R, Rp, nrt, width, outer, teams, Sp, slots;
+  int P, W, Hkv, R, Rp, nrt, width, outer, ctas, Sp, slots;
   int page_size, max_pages, num_pages;
   float scale_log2;
 };
-cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& a, int D,
-                               cudaStream_t stream);
 
 // Few query rows a key: the rows' own keys, R = G*Tq query rows a (batch row, K/V head), and, where few rows share a
 // prefix (P > 0), the prefixes, W*R query rows a (prefix, K/V head).  They go in nrb (nrbp) blocks of `block` rows; a
@@ -171,9 +169,7 @@ struct OwnArgs {
   int* status;
   int B, P, W, Hkv, Tq, R, nrb, nrbp, block, rows_ws, S, Sp, D;
   int page_size, max_pages, max_prefix_pages, num_pages;
-  int ctas, warps;          // CTAs of the launch, warps in them (set by it)
-  int beside;               // launched as the prefix kernel's programmatic dependent, which passed its own griddep_wait
-                            // when it let dependents start, and runs beside it
+  int ctas;                 // CTAs of the launch
   float scale_log2;
 };
 // Maps over the caches or pages with boxes of 64 features x own_box_rows(); pk, pv: of contiguous prefixes.
@@ -192,7 +188,12 @@ inline int own_box_rows(int D, int page_size) {   // page_size 0: contiguous
   const int tile = D == 128 ? 16 : 32;
   return page_size > 0 && page_size < tile ? page_size : tile;
 }
+// Both as one stream (a.P > 0).
 cudaError_t launch_attn_own(const OwnMaps& m, const OwnArgs& a, cudaStream_t stream);
+// The prefixes by large tiles (maps k, v with boxes of 128 rows), and beside them, on SMs of its own, the stream of the
+// rows' own keys (a.P = 0).
+cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const PrefixArgs& p, const OwnMaps& m,
+                               const OwnArgs& a, cudaStream_t stream);
 
 // Joins the prefix's partials with those of the rows' own caches: O and LSE of every row.
 cudaError_t launch_prefix_merge(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream);

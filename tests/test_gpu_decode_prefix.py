@@ -88,22 +88,48 @@ CASES = [
 ]
 
 
+def tile_capacity(B, P, Hq, Hkv, Tq, D):
+    """The least prefix capacity (in steps of 1024) that sends prefixes of more than 16 query rows to the kernel of large
+    tiles: it counts what the stream would read again, not how long the prefixes are."""
+    again = -(-(B // P * Hq // Hkv * Tq) // 16) - 1
+    return ((65 << 20) // (again * P * Hkv * D * 4) // 1024 + 1) * 1024 if again else None
+
+
+def ran(gq, f):
+    """f(), and which kernels it launched."""
+    gq.profile_enable(True)
+    gq.profile_reset()
+    out = f()
+    torch.cuda.synchronize()
+    names = {k for k, (n, _) in gq.profile_read().items() if n}
+    gq.profile_enable(False)
+    return out, names
+
+
+@pytest.mark.parametrize("tiles", [False, True])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: f"B{c[0]}P{c[1]}H{c[2]}-{c[3]}T{c[4]}D{c[5]}p{c[6]}m{max(c[7])}")
-def test_against_the_definition(gq, case):
+def test_against_the_definition(gq, case, tiles):
+    """Both ways a prefix goes: in the stream of tiles beside the rows' own keys, and through the kernel of large tiles."""
     B, P, Hq, Hkv, Tq, D, page, plens, lens = case
-    f, args, ref = make(*case, seed=1)
+    Sp = tile_capacity(B, P, Hq, Hkv, Tq, D) if tiles else None
+    if tiles and Sp is None:
+        pytest.skip("at most 16 query rows a key: always in the stream")
+    f, args, ref = make(*case, seed=1, Sp=Sp)
     scale = 1 / math.sqrt(D)
-    got = getattr(gq, f)(*args, scale=scale)
+    got, names = ran(gq, lambda: getattr(gq, f)(*args, scale=scale))
+    assert names == ({"prefix", "prefix_merge"} if tiles else {"own_keys", "prefix_merge"})
     assert gq.get_device_status() == 0
     check(got, R.prefix(*ref, scale), D)
     again = getattr(gq, f)(*args, scale=scale)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
+@pytest.mark.parametrize("Hq", [8, 64])
 @pytest.mark.parametrize("page", [0, 16])
-@pytest.mark.parametrize("Tq,lens", [(1, [0, 5, 0, 1]), (4, [0, 1, 3, 4]), (3, [2, 2, 0, 0])])
-def test_queries_at_negative_positions_see_nothing(gq, page, Tq, lens):
-    f, args, ref = make(4, 2, 8, 2, Tq, 128, page, [130, 0], lens, seed=2)
+@pytest.mark.parametrize("Tq,lens", [(1, [0, 5, 0, 1]), (4, [0, 1, 3, 4]), (3, [2, 2, 0, 0]), (2, [0, 0, 0, 0])])
+def test_queries_at_negative_positions_see_nothing(gq, page, Tq, lens, Hq):
+    f, args, ref = make(4, 2, Hq, 2, Tq, 128, page, [130, 0], lens, seed=2,
+                        Sp=tile_capacity(4, 2, Hq, 2, Tq, 128) if Hq == 64 else None)
     got = getattr(gq, f)(*args, scale=0.1)
     assert gq.get_device_status() == 0
     check(got, R.prefix(*ref, 0.1), 128)
@@ -117,11 +143,13 @@ def test_capacities_beyond_the_lengths_and_default_scale(gq):
         check(got, R.prefix(*ref, 1 / 8), 64)
 
 
-def test_large_scores_and_growing_maxima(gq):
+@pytest.mark.parametrize("tiles", [False, True])
+def test_large_scores_and_growing_maxima(gq, tiles):
     """Scores of tens, rising along the prefix, so that the running maximum moves in every block."""
-    f, args, ref = make(9, 1, 8, 2, 1, 128, 0, [900], [1 + 20 * i for i in range(9)], seed=4, qs=6.0)
-    k = args[1]
-    ramp = torch.linspace(0.1, 3.0, k.shape[2], device="cuda")
+    f, args, ref = make(9, 1, 8, 2, 1, 128, 0, [900], [1 + 20 * i for i in range(9)], seed=4, qs=6.0,
+                        Sp=tile_capacity(9, 1, 8, 2, 1, 128) if tiles else None)
+    k = args[1][:, :, :900]
+    ramp = torch.linspace(0.1, 3.0, 900, device="cuda")
     k.copy_((k.float() * ramp[None, None, :, None]).bfloat16())
     pre = [(k[0].cpu().double(), ref[1][0][1])]
     got = getattr(gq, f)(*args, scale=0.2)
@@ -148,8 +176,10 @@ def test_agrees_with_the_decode_over_the_joined_cache(gq):
     check((o, lse), want, D)
 
 
-def test_bad_lengths_and_pages_are_reported(gq):
-    f, args, ref = make(4, 2, 4, 2, 1, 64, 16, [40, 33], [3, 4, 5, 6], seed=7, junk=0.0)
+@pytest.mark.parametrize("Hq", [4, 128])
+def test_bad_lengths_and_pages_are_reported(gq, Hq):
+    f, args, ref = make(4, 2, Hq, 2, 1, 64, 16, [40, 33], [3, 4, 5, 6], seed=7, junk=0.0,
+                        Sp=tile_capacity(4, 2, Hq, 2, 1, 64) if Hq == 128 else None)
     for i, bad, rows in ((4, 1 << 20, [0, 1]), (4, -1, [0, 1]), (6, -2, [0]), (6, 1 << 20, [0])):
         a = list(args)
         a[i] = a[i].clone()
@@ -170,11 +200,23 @@ def test_bad_lengths_and_pages_are_reported(gq):
     assert gq.get_device_status() == 0
 
 
-def test_many_prefixes_of_one_row_each(gq):
+@pytest.mark.parametrize("Hq", [2, 24])
+def test_many_prefixes_of_one_row_each(gq, Hq):
     """More prefixes than a scan of 32 holds, lengths from none to several blocks."""
     P = 70
     plens = [(37 * i) % 400 for i in range(P)]
-    f, args, ref = make(P, P, 2, 1, 1, 64, 0, plens, [1 + i % 50 for i in range(P)], seed=8)
+    f, args, ref = make(P, P, Hq, 1, 1, 64, 0, plens, [1 + i % 50 for i in range(P)], seed=8,
+                        Sp=tile_capacity(P, P, Hq, 1, 1, 64) if Hq == 24 else None)
+    got = getattr(gq, f)(*args, scale=0.125)
+    assert gq.get_device_status() == 0
+    check(got, R.prefix(*ref, 0.125), 64)
+
+
+@pytest.mark.parametrize("Hq", [4, 40])
+def test_more_rows_than_a_block_scans_at_once(gq, Hq):
+    B = 500
+    f, args, ref = make(B, 4, Hq, 1, 1, 64, 16, [5, 0, 300, 129], [(7 * i) % 40 for i in range(B)], seed=12,
+                        Sp=tile_capacity(B, 4, Hq, 1, 1, 64) if Hq == 40 else None)
     got = getattr(gq, f)(*args, scale=0.125)
     assert gq.get_device_status() == 0
     check(got, R.prefix(*ref, 0.125), 64)
@@ -194,9 +236,11 @@ def test_workspace_and_streams(gq):
         gq.attn_decode_prefix_fwd(*args, workspace=ws[:n - 256])
 
 
-def test_replayed_with_other_lengths(gq):
+@pytest.mark.parametrize("tiles", [False, True])
+def test_replayed_with_other_lengths(gq, tiles):
     """A captured call reads the lengths on the device: replayed after they changed, it gives the eager call's bits."""
-    f, args, ref = make(8, 1, 8, 2, 1, 128, 64, [900], [50 + 9 * i for i in range(8)], seed=10, junk=0.0)
+    f, args, ref = make(8, 1, 8, 2, 1, 128, 64, [900], [50 + 9 * i for i in range(8)], seed=10, junk=0.0,
+                        Sp=tile_capacity(8, 1, 8, 2, 1, 128) if tiles else None)
     o, lse = torch.empty_like(args[0]), torch.empty(args[0].shape[:3], device="cuda")
     getattr(gq, f)(*args, o=o, lse=lse)
     g = torch.cuda.CUDAGraph()
