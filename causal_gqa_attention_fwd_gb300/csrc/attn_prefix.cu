@@ -76,33 +76,28 @@ struct Piece {
 // Where a CTA's walk over its share stands.  Every role walks it.
 struct Walk {
   Piece it;
-  long g, g1;          // stream index of the piece's first block; end of the share
-  long C;
-  int T;               // teams with a share
+  EvenSplit split;     // of the stream between the teams with a share
+  int g, g1;           // stream position of the piece's first block; end of the share
   int p, nb;           // prefix of the piece, its blocks
-  long Pb;             // stream index of prefix p's first block
+  int Pb;              // stream position of prefix p's first block
   int team, inner;
   bool valid;
 };
 
-__device__ __forceinline__ int team_of(long g, long C, int T) { return (int)(((g + 1) * T - 1) / C); }
-
 __device__ __forceinline__ void walk_piece(const PrefixArgs& a, Walk& w) {
-  const long off = w.g - w.Pb;
-  const int group = (int)(off / w.nb), kb = (int)(off % w.nb);   // (hkv, outer), block
+  const int off = w.g - w.Pb, group = off / w.nb, kb = off - group * w.nb;   // (hkv, outer), block
   Piece& it = w.it;
   it.p = w.p;
   it.hkv = group / a.outer;
-  it.mt = group % a.outer * a.width + w.inner;
+  it.mt = (group - it.hkv * a.outer) * a.width + w.inner;
   it.kb = kb;
-  it.n = (int)min((long)(w.nb - kb), w.g1 - w.g);
+  it.n = min(w.nb - kb, w.g1 - w.g);
   it.len = a.prefix_lens[w.p];
   it.rows = min(kPrefixRows, a.Rp - it.mt * kPrefixRows);
   it.split = it.rows <= kBM;
-  const long Pg = w.Pb + (long)group * w.nb;
-  const int first = team_of(Pg, w.C, w.T);
+  const int Pg = w.Pb + group * w.nb, first = w.split.owner(Pg);
   it.slot = w.team - first;
-  it.npieces = team_of(Pg + w.nb - 1, w.C, w.T) - first + 1;
+  it.npieces = w.split.owner(Pg + w.nb - 1) - first + 1;
   w.valid = true;
 }
 
@@ -112,7 +107,7 @@ __device__ __forceinline__ void walk_next(const PrefixArgs& a, Walk& w) {
     w.valid = false;
     return;
   }
-  const long gpp = (long)a.Hkv * a.outer;
+  const int gpp = a.Hkv * a.outer;
   while (w.g >= w.Pb + gpp * w.nb) {
     w.Pb += gpp * w.nb;
     ++w.p;
@@ -121,31 +116,24 @@ __device__ __forceinline__ void walk_next(const PrefixArgs& a, Walk& w) {
   walk_piece(a, w);
 }
 
-// The walk of CTA `cta` of `ctas` from its start (one warp).
-__device__ Walk walk_begin(const PrefixArgs& a, int cta, int ctas) {
-  const int lane = threadIdx.x & 31;
-  const long gpp = (long)a.Hkv * a.outer;
-  long C = 0;
-  for (int p0 = 0; p0 < a.P; p0 += 32)
-    C += gpp * (long)__reduce_add_sync(0xffffffffu, p0 + lane < a.P ? (unsigned)prefix_blocks(a, p0 + lane) : 0u);
+// The walk of CTA `cta` of `ctas` from its start (one warp); total: blocks of all groups.
+__device__ Walk walk_begin(const PrefixArgs& a, int cta, int ctas, int total) {
+  const int lane = threadIdx.x & 31, gpp = a.Hkv * a.outer;
   Walk w{};
-  w.C = C;
-  w.T = (int)min((long)(ctas / a.width), C);
-  const int team = cta / a.width;
-  w.team = team;
-  w.inner = cta % a.width;
+  w.split = EvenSplit::of(total, min(ctas / a.width, total));
+  w.team = cta / a.width;
+  w.inner = cta - w.team * a.width;
   w.valid = false;
-  if (team >= w.T) return w;
-  w.g = (long)team * C / w.T;
-  w.g1 = (long)(team + 1) * C / w.T;
-  long P = 0;
+  if (w.team >= w.split.parts) return w;
+  w.g = w.split.begin(w.team);
+  w.g1 = w.split.begin(w.team + 1);
+  int P = 0;
   for (int p0 = 0; p0 < a.P; p0 += 32) {
-    int n = 0;
-    if (p0 + lane < a.P) n = prefix_blocks(a, p0 + lane);
-    long incl = gpp * n;   // inclusive prefix sum over the 32 prefixes
+    const int n = p0 + lane < a.P ? prefix_blocks(a, p0 + lane) : 0;
+    int incl = gpp * n;   // inclusive sums over the 32 prefixes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long y = __shfl_up_sync(0xffffffffu, incl, o);
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, P + incl > w.g);
@@ -165,13 +153,24 @@ __device__ Walk walk_begin(const PrefixArgs& a, int cta, int ctas) {
 }  // namespace
 
 // How many of the grid's G CTAs take the rows' own keys, the others the prefixes: so that both end at the same time, by
-// what they were measured to take.  An SM by itself streams kOwnTile ns a 8 KB tile, all of them together kOwnTileAll;
-// two tiles of 128 query rows take kPair ns a block of 128 keys, one kSplit.  All threads call this.
-constexpr float kOwnStart = 6000.f, kOwnTile = 95.f, kOwnTileAll = 1.25f;
-constexpr float kPreStart = 8000.f, kPair = 1550.f, kSplit = 950.f;
+// what they were measured to take (ns).
+//   Two tiles of query rows a CTA: the MMAs bound a prefix, kPair a block of 128 keys.  Beside it an SM streams own keys
+//   at kOwnTile a tile of 8 KB, all SMs together at kOwnTileAll; a prefix starts slowly beside a stream that fills the
+//   memory's queues.
+//   One tile of rows, held by both: the memory bounds both parts, and an SM gets its share of it: kByte a byte.
+// 64 rows over 8192 keys and 32768 own ones, CTAs of own keys 64 / 72 / 80 / 88 / 96: 43.5, 42.6, 42.5, 43.4, 45.8 us;
+// 256 rows over 32768, 32 / 34 / 36 / 40: 141, 134, 131, 133.
+constexpr float kOwnStart = 6000.f, kOwnTile = 102.f, kOwnTileAll = 1.25f;
+constexpr float kPreStart = 18000.f, kPair = 1350.f, kByte = 1.f / 41.f;
+constexpr float kPiece = 5000.f;      // a second piece: its queries, the first one's drain and partial
+
+struct Parts {
+  int own;         // CTAs of the rows' own keys
+  int blocks;      // key blocks of all prefixes' groups
+};
 
 template <int KT>
-__device__ int own_ctas(const PrefixArgs& p, const OwnArgs& a, int G, int* s_red) {
+__device__ Parts share_out(const PrefixArgs& p, const OwnArgs& a, int G, int* s_red) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int tiles = 0, blocks = 0;
   for (int b = tid; b < a.B; b += 384) {
@@ -192,15 +191,23 @@ __device__ int own_ctas(const PrefixArgs& p, const OwnArgs& a, int G, int* s_red
   tiles = blocks = 0;
 #pragma unroll
   for (int w = 0; w < 12; ++w) tiles += s_red[w], blocks += s_red[12 + w];
-  if (tiles == 0) return 0;
-  if (blocks == 0) return G;
+  const int runs = p.Hkv * p.outer;
+  blocks *= runs;
+  if (tiles == 0) return {0, blocks};
+  if (blocks == 0) return {G, 0};
   const float own = (float)tiles * (a.Hkv * a.nrb);
   const int last = p.Rp - (p.nrt - 1) * kPrefixRows;     // rows of the last unit
-  const float pre = (float)blocks * (p.Hkv * p.outer) * (p.nrt == 1 && last <= kBM ? kSplit : kPair);
+  const bool split = p.nrt == 1 && last <= kBM;
+  const float tile = split ? 8192 * kByte : kOwnTile, block = split ? 4 * kBN * a.D * kByte : kPair;
+  const float start = split ? kOwnStart : kPreStart;
   unsigned best = ~0u;
   if (tid >= 1 && tid <= G - p.width) {
-    const float t_own = kOwnStart + fmaxf(own * kOwnTile / tid, own * kOwnTileAll);
-    const float t_pre = kPreStart + pre / ((G - tid) / p.width);
+    const int teams = (G - tid) / p.width;
+    const float t_own = kOwnStart + fmaxf(own * tile / tid, own * kOwnTileAll);
+    // one prefix: no CTA crosses from a unit to the next if the teams are a multiple of its groups, or the reverse
+    const bool whole = p.P == 1 && (teams % runs == 0 || runs % teams == 0);
+    const int most = (blocks + teams - 1) / teams;
+    const float t_pre = start + most * block + (whole ? 0.f : kPiece * (1 + most * runs * p.P / blocks));
     best = (unsigned)fminf(fmaxf(t_own, t_pre), 1.6e7f) << 8 | tid;
   }
   best = __reduce_min_sync(~0u, best);
@@ -209,7 +216,7 @@ __device__ int own_ctas(const PrefixArgs& p, const OwnArgs& a, int G, int* s_red
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 12; ++w) best = min(best, (unsigned)s_red[w]);
-  return best & 255u;
+  return {(int)(best & 255u), blocks};
 }
 
 template <int D, bool PAGED, int NT>
@@ -233,7 +240,8 @@ __global__ void __launch_bounds__(384, 1)
   griddep_launch();
 
   // ------------------------------------------------ this CTA's part: own keys (spread evenly over the grid) or prefixes
-  const int G = gridDim.x, X = __shfl_sync(~0u, own_ctas<OwnCfg<D, NT>::KT>(a, own, G, s_red), 0);
+  const Parts parts = share_out<OwnCfg<D, NT>::KT>(a, own, gridDim.x, s_red);
+  const int G = gridDim.x, X = __shfl_sync(~0u, parts.own, 0);
   const int before = blockIdx.x * X / G;       // own-key CTAs of lower number
   if ((blockIdx.x + 1) * X / G > before) {
     using O = OwnCfg<D, NT>;
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(384, 1)
     tmem_relinquish();
   }
   if (warp == 0) {
-    const Walk w0 = walk_begin(a, cta, ctas);
+    const Walk w0 = walk_begin(a, cta, ctas, parts.blocks);
     if (lane == 0) s_walk = w0;
   }
   tc_fence_before();

@@ -519,10 +519,10 @@ namespace {
 constexpr int kEvThreads = 512;      // two CTAs an SM at 64 registers
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kBins = 2048;          // of a pass over 11 bits (the last: 10)
-constexpr int kMoveRows = 6;         // rows a thread has parts of on the way between reading and writing
-constexpr int kPlaceBytes = kMoveRows * kEvThreads * 16;
+constexpr int kPlaceBytes = 4096;    // of rows that a warp has on the way between reading and writing
+constexpr int kPlaces = kEvWarps * kPlaceBytes;
 constexpr int kKeyBytes = 80 << 10;  // weights a CTA keeps in shared memory; a longer share is read again each pass
-constexpr int kAlone = 8192;         // positions up to which each CTA selects by itself (weights and list in 64 KB)
+constexpr int kAlone = 8192;         // positions up to which each CTA selects by itself
 
 // Whole numbers in the weights' order: NaN above all, -0 = 0; 0 is below all of them.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -547,31 +547,69 @@ __device__ __forceinline__ int4 peer_int4(const void* p, int rank) {
   return v;
 }
 
-// A thread's part of every row that it moves: 16, 8 or 4 bytes of one plane, by way of its place in shared memory.
-struct Part {
-  uint8_t* base;      // of the plane, at the part
-  int row_bytes, size;
-  __device__ __forceinline__ void load(uint32_t to, long slot) const {
-    const uint8_t* p = base + slot * row_bytes;
-    if (size == 16) copy_async<16>(to, p);
-    else if (size == 8) copy_async<8>(to, p);
-    else copy_async<4>(to, p);
+// A run of `cnt` rows, list[d0 + i] -> d0 + i, of one plane, by one warp through its place in shared memory.  Lane i finds
+// where row i comes from and goes to; the warp then moves the rows' parts side by side.
+struct Task {
+  uint8_t* base;
+  int row_bytes, size, parts, cnt;
+  long from, to;      // slots of row `lane`; -1: it stays, or is in a page outside the pool
+  __device__ __forceinline__ void find(const EvictPlane& pl, const Slots& slot_of, const int* list, int d0, int rows, int lane) {
+    base = static_cast<uint8_t*>(pl.p);
+    row_bytes = pl.row_bytes;
+    size = pl.size;
+    parts = pl.parts;
+    cnt = rows;
+    const int src = lane < cnt ? list[d0 + lane] : -1;
+    from = to = -1;
+    if (src > d0 + lane) {
+      from = slot_of(src);
+      to = from >= 0 ? slot_of(d0 + lane) : -1;
+      if (to < 0) from = -1;
+    }
   }
-  __device__ __forceinline__ void store(const uint4* from, long slot) const {
-    uint8_t* p = base + slot * row_bytes;
-    if (size == 16) *reinterpret_cast<uint4*>(p) = *from;
-    else if (size == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(from);
-    else *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(from);
+  // f(byte in the run, address of that part of its row), for all parts of rows whose slot is not -1
+  template <class F>
+  __device__ __forceinline__ void each(long slot, int lane, F f) const {
+    const int n = min(parts, 32), rpw = 32 / n;           // rows at once
+    const int sub = lane / n, part = lane - sub * n;
+    for (int r0 = 0; r0 < cnt; r0 += rpw) {
+      const int r = r0 + sub;
+      const long s = __shfl_sync(~0u, slot, r & 31);
+      if (sub < rpw && r < cnt && s >= 0)
+        for (int p = part; p < parts; p += 32) f(r * row_bytes + p * size, base + s * row_bytes + p * size);
+    }
+  }
+  __device__ __forceinline__ void read(uint8_t* place, int lane) const {
+    each(from, lane, [&](int at, const uint8_t* p) {
+      const uint32_t to_smem = smem_u32(place + at);
+      if (size == 16) copy_async<16>(to_smem, p);
+      else if (size == 8) copy_async<8>(to_smem, p);
+      else copy_async<4>(to_smem, p);
+    });
+    copies_commit();
+    copies_wait<0>();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void write(const uint8_t* place, int lane) const {
+    each(to, lane, [&](int at, uint8_t* p) {
+      if (size == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(place + at);
+      else if (size == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(place + at);
+      else *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(place + at);
+    });
+    __syncwarp();         // the place is free again
   }
 };
-// Moves the rows list[d] -> d, d in [first, budget), of every plane.  A thread has one part of a row (a row's parts of all
-// planes lie on neighbouring threads), kMoveRows of them on the way at a time.  Row d may be written once whatever is kept
-// of position d has been read, that is all rows i with list[i] <= d.  So the rows go in phases [c0, c1): if list[c0] lies
-// further behind c0 than the threads' places reach, all rows up to position list[c0] are free to go one by one, for every
-// source in front of that position belongs to an earlier phase; otherwise as many as there are places are read before any
-// is written.
-__device__ __forceinline__ void move_rows(const EvictArgs& a, const Slots& slot_of, const int* list, uint4* places, int rank,
+
+// Moves the rows list[d] -> d, d in [first, budget), of every plane, runs of rows by the cluster's warps.  Row d may be
+// written once whatever is kept of position d has been read, that is all rows i with list[i] <= d.  So the rows go in
+// phases [c0, c1): if list[c0] lies `hold` rows or more behind c0, all rows up to position list[c0] are free to go one
+// run after another, for every source in front of that position belongs to an earlier phase; otherwise as many as the
+// warps' places hold are read before any is written.
+__device__ __forceinline__ void move_rows(const EvictArgs& a, const Slots& slot_of, const int* list, uint8_t* places, int rank,
                                           int ranks) {
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
+  uint8_t* place = places + warp * kPlaceBytes;
+  const int me = warp * ranks + rank, all = kEvWarps * ranks;
   // the first row that moves: list[d] - d never falls
   int d_lo = a.first, d_hi = a.budget;
   while (d_lo < d_hi) {
@@ -579,65 +617,31 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const Slots& slot_
     if (list[mid] > mid) d_hi = mid;
     else d_lo = mid + 1;
   }
-  for (int p0 = 0; p0 < a.parts; p0 += kEvThreads) {     // more parts than threads: some of each row's at a time
-    const int ppr = min(a.parts - p0, kEvThreads), rpi = kEvThreads / ppr, sub = threadIdx.x / ppr;
-    Part part{nullptr, 0, 0};
-    int q = p0 + threadIdx.x % ppr;
-    for (int i = 0; i < a.n_planes; ++i) {
-      const EvictPlane& pl = a.planes[i];
-      const int size = pl.row_bytes % 16 == 0 ? 16 : pl.row_bytes % 8 == 0 ? 8 : 4, n = pl.row_bytes / size;
-      if (q >= 0 && q < n) part = Part{static_cast<uint8_t*>(pl.p) + q * size, pl.row_bytes, size};
-      q -= n;
-    }
-    const int step = ranks * rpi, hold = step * kMoveRows;
-    uint4* mine = places + threadIdx.x;                  // place u: kEvThreads further on
-    auto source = [&](int d, int c1) { return sub < rpi && d < c1 ? list[d] : -1; };
-    auto read = [&](int u, int src) {
-      const long s = src >= 0 ? slot_of(src) : -1;
-      if (s >= 0) part.load(smem_u32(mine + u * kEvThreads), s);
-      copies_commit();
-      return s >= 0;
-    };
-    auto write = [&](int u, int d) {
-      const long t = slot_of(d);
-      if (t >= 0) part.store(mine + u * kEvThreads, t);
-    };
-    for (int c0 = d_lo; c0 < a.budget;) {
-      const int free_to = min(list[c0], a.budget);
-      const bool held = free_to < c0 + hold && free_to < a.budget;
-      const int c1 = held ? min(c0 + hold, a.budget) : free_to;
-      int d = c0 + rank * rpi + sub, src[kMoveRows];
-      unsigned go = 0;
-#pragma unroll
-      for (int u = 0; u < kMoveRows; ++u) src[u] = source(d + u * step, c1);
-#pragma unroll
-      for (int u = 0; u < kMoveRows; ++u) go |= (unsigned)read(u, src[u]) << u;
-      if (held) {
-        copies_wait<0>();
-        cluster_sync();
-#pragma unroll
-        for (int u = 0; u < kMoveRows; ++u)
-          if (go >> u & 1u) write(u, d + u * step);
-      } else {
-#pragma unroll
-        for (int u = 0; u < kMoveRows; ++u) src[u] = source(d + hold + u * step, c1);
-        while (go) {
-          unsigned next = 0;
-#pragma unroll
-          for (int u = 0; u < kMoveRows; ++u) {
-            copies_wait<kMoveRows - 1>();                 // the oldest has landed
-            if (go >> u & 1u) write(u, d + u * step);
-            next |= (unsigned)read(u, src[u]) << u;
-            src[u] = source(d + 2 * hold + u * step, c1);
-          }
-          d += hold;
-          go = next;
-        }
-        copies_wait<0>();
-        if (c1 < a.budget) cluster_sync();   // the phase's rows are read before later ones are written over them
+  for (int c0 = d_lo; c0 < a.budget;) {
+    const int free_to = min(list[c0], a.budget);
+    const bool held = free_to < c0 + a.hold && free_to < a.budget;
+    const int c1 = held ? min(c0 + a.hold, a.budget) : free_to;
+    for (int k = me;; k += all) {          // held: no warp has more than one run
+      int i = 0, t = k, runs = 0;
+      for (; i < a.n_planes; ++i) {
+        runs = (c1 - c0 + a.planes[i].run - 1) / a.planes[i].run;
+        if (t < runs) break;
+        t -= runs;
       }
-      c0 = c1;
+      const bool mine = i < a.n_planes;
+      if (!mine && !held) break;
+      Task task;
+      if (mine) {
+        const int d0 = c0 + t * a.planes[i].run;
+        task.find(a.planes[i], slot_of, list, d0, min(a.planes[i].run, c1 - d0), lane);
+        task.read(place, lane);
+      }
+      if (held) cluster_sync();
+      if (mine) task.write(place, lane);
+      if (held) break;
     }
+    if (!held && c1 < a.budget) cluster_sync();       // the phase's rows are read before later ones are written over them
+    c0 = c1;
   }
 }
 
@@ -674,7 +678,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictArgs a)
   int need = a.budget - a.first - a.recent;
   const bool cached = run * 4 <= a.key_bytes;
   // shared memory: the weights, in whose place rows are on the way later; the list
-  int* list = a.shared_select ? kept : reinterpret_cast<int*>(s_keys) + max(a.key_bytes, kPlaceBytes) / 4;
+  int* list = a.shared_select ? kept : reinterpret_cast<int*>(s_keys) + max(a.key_bytes, kPlaces) / 4;
   bool bad = false;
   const Slots slot_of{a.block_table ? a.block_table + (long)b * a.max_pages : nullptr, a.num_pages, b, a.page, a.Hkv, h};
   auto load_key = [&](int j) {
@@ -792,17 +796,22 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictArgs a)
   const int wrun = ((hi - lo + kEvWarps - 1) / kEvWarps + 31) & ~31;
   const int w0 = min(lo + warp * wrun, hi), w1 = min(w0 + wrun, hi);
   int gt = 0, eq = 0;
-  if (any) {
+  if (any && cached) {
 #pragma unroll 4
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-      const int j = j0 + lane;
-      const uint32_t k = j < w1 ? key(j) & mask : 0u;
-      gt += j < w1 && k > thr;
-      eq += j < w1 && k == thr;
+    for (int j = w0 + lane; j < w1; j += 32) {
+      const uint32_t k = s_keys[j - lo] & mask;
+      gt += k > thr;
+      eq += k == thr;
     }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
+  } else if (any) {
+    for (int j = w0 + lane; j < w1; j += 32) {
+      const uint32_t k = load_key(j) & mask;
+      gt += k > thr;
+      eq += k == thr;
+    }
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     s_gt[warp] = gt;
     s_eq[warp] = eq;
@@ -843,7 +852,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictArgs a)
   cluster_sync();
   if (!a.shared_select)
     for (int i = rank * kEvThreads + tid; i < a.budget; i += ranks * kEvThreads) kept[i] = list[i];
-  move_rows(a, slot_of, list, reinterpret_cast<uint4*>(s_keys), rank, ranks);
+  move_rows(a, slot_of, list, reinterpret_cast<uint8_t*>(s_keys), rank, ranks);
 }
 
 }  // namespace
@@ -857,21 +866,31 @@ cudaError_t launch_cache_evict(EvictArgs a, cudaStream_t stream) {
   a.shared_select = a.cluster > 1 && a.S > kAlone;
   const long run = a.shared_select ? ((long)a.S + a.cluster - 1) / a.cluster : a.S;
   a.key_bytes = run * 4 <= kKeyBytes ? (int)(run * 4 + 15) / 16 * 16 : 0;
-  int smem = a.key_bytes > kPlaceBytes ? a.key_bytes : kPlaceBytes;
+  int smem = a.key_bytes > kPlaces ? a.key_bytes : kPlaces;
   if (!a.shared_select) {      // the list beside the weights; rows too long for that: one CTA, the list in memory
     if (a.S <= kAlone) smem += (a.budget < a.S ? a.budget : a.S) * 4;
     else a.shared_select = 1;
   }
-  a.parts = 0;
+  // runs of rows that fill a warp's place, 32 at most; as many rows as the cluster's warps hold with a run each
   for (int i = 0; i < a.n_planes; ++i) {
-    const int rb = a.planes[i].row_bytes;
-    a.parts += rb / (rb % 16 == 0 ? 16 : rb % 8 == 0 ? 8 : 4);
+    EvictPlane& p = a.planes[i];
+    p.size = p.row_bytes % 16 == 0 ? 16 : p.row_bytes % 8 == 0 ? 8 : 4;
+    p.parts = p.row_bytes / p.size;
+    p.run = kPlaceBytes / p.row_bytes < 32 ? kPlaceBytes / p.row_bytes : 32;
   }
+  auto runs = [&](int rows) {
+    int n = 0;
+    for (int i = 0; i < a.n_planes; ++i) n += (rows + a.planes[i].run - 1) / a.planes[i].run;
+    return n;
+  };
+  a.hold = 1;
+  for (int step = 1 << 12; step > 0; step /= 2)
+    if (runs(a.hold + step) <= kEvWarps * a.cluster) a.hold += step;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyBytes + 8192);
+    const cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlaces + 4 * kAlone);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set[dev] = true;
   }

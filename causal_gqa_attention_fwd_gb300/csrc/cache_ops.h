@@ -119,6 +119,7 @@ constexpr int kEvictPlanes = 8;
 struct EvictPlane {
   void* p;
   int row_bytes;
+  int size, parts, run;      // bytes a lane moves, such parts of a row, rows a warp moves at once (set by the launch)
 };
 struct EvictArgs {
   const float* weights;
@@ -129,8 +130,8 @@ struct EvictArgs {
   int *kept, *lens_out;      // [B, Hkv, budget], [B]
   int B, Hkv, S, page_size, max_pages, num_pages;
   int budget, recent, first;
-  // set by the launch: CTAs of a unit; shared memory for a CTA's weights, 0: they do not fit; threads' parts of a row
-  int cluster, key_bytes, parts;
+  // set by the launch: CTAs of a unit; shared memory for a CTA's weights, 0: they do not fit; rows the cluster holds at once
+  int cluster, key_bytes, hold;
   FastDiv page;              // page_size
   int shared_select;         // the cluster selects together and the list is `kept`; otherwise each CTA does, into its own
   int* status;

@@ -178,11 +178,11 @@ struct OwnMaps {
 };
 // Whether prefixes of Sp keys, Rp query rows each, go into the stream: it reads them again for every 16 rows, from L2,
 // where attn_prefix needs some microseconds for its pipeline of large tiles.  Measured (us, stream / attn_prefix; 8 heads
-// of 128): 2048 keys, 32 rows 10.8 / 15.9, 128 rows 18.4 / 21.8, 256 rows 29.4 / 26.3; 8192 keys, 16 rows 14.1 / 17.3, 32
-// rows 17.7 / 18.3, 64 rows 24.4 / 22.1; 8 prefixes of 2048, 32 rows 31.9 / 37.6, 64 rows 37.5 / 34.3; heads of 64, 2 of
-// them, 32768 keys, 56 rows 17.6 / 17.2: about 64 MB read again is where they meet.
+// of 128): 2048 keys, 32 rows 12 / 16, 128 rows 18 / 20; 8192 keys, 16 rows 15 / 17, 48 rows 23 / 18; 8 prefixes of 2048,
+// 32 rows 28 / 32, 48 rows 36 / 30; heads of 64, 2 of them, 32768 keys, 56 rows 18 / 17: about 48 MB read again is where
+// they meet.
 inline bool prefix_in_stream(int Rp, int P, int Hkv, int Sp, int D) {
-  return ((long)(Rp + 15) / 16 - 1) * P * Hkv * Sp * D * 4 <= 64L << 20;
+  return ((long)(Rp + 15) / 16 - 1) * P * Hkv * Sp * D * 4 <= 48L << 20;
 }
 inline int own_box_rows(int D, int page_size) {   // page_size 0: contiguous
   const int tile = D == 128 ? 16 : 32;

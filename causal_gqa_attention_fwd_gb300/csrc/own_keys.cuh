@@ -343,7 +343,7 @@ __device__ __forceinline__ void own_keys(uint8_t* smem, OwnShared<D, NT, THREADS
     const int unit = (pre ? u.i * a.nrbp : a.P * a.nrbp + (u.i - a.P) * a.nrb) * a.Hkv + u.k;
     const long base = ((long)gw + unit) * a.rows_ws;
     if (u.t == 0 && lane == 0) {
-      a.counts[unit] = make_int2(gw + unit, sh.owner(u.P + u.nb - 1) - gw + 1);
+      a.counts[unit] = make_int2(gw + unit, sh.split.owner(u.P + u.nb - 1) - gw + 1);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)

@@ -42,27 +42,45 @@ struct Slots {
   }
 };
 
-// Positions [v0, v1) are warp gw's of `warps` (those in use); `row` holds v0 and begins at position `at`.  v1 <= v0: none.
+// `total` positions in `parts` runs, run i from floor(i total / parts) on, so that the runs of equal parts of the whole
+// end with them.  32-bit divisions only (a 64-bit one takes as long as a load): with total = q parts + r that is
+// i q + floor(i r / parts), parts < 2^15.
+struct EvenSplit {
+  int total, parts, q, r;
+  __device__ __forceinline__ static EvenSplit of(int total, int parts) {
+    EvenSplit e{total, parts, 0, 0};
+    if (parts > 0) e.q = total / parts, e.r = total - e.q * parts;
+    return e;
+  }
+  __device__ __forceinline__ int begin(int i) const { return i * q + (int)((unsigned)(i * r) / (unsigned)parts); }
+  // The run that has position x: an estimate, off by one at most, then exactly.
+  __device__ __forceinline__ int owner(int x) const {
+    int i = min(parts - 1, (int)((float)x / (float)total * (float)parts));
+    while (begin(i) > x) --i;
+    while (begin(i + 1) <= x) ++i;
+    return i;
+  }
+};
+
+// Positions [v0, v1) are warp gw's; `row` holds v0 and begins at position `at`.  v1 <= v0: none.
 struct StreamShare {
-  long total;
-  int warps, v0, v1, row, at;
-  // the warp that has position x
-  __device__ __forceinline__ int owner(int x) const { return (int)((((long)x + 1) * warps - 1) / total); }
+  EvenSplit split;      // between the warps in use
+  int v0, v1, row, at;
 };
 
 // All threads of a block of THREADS call this; s_sum [THREADS / 32], s_pre [THREADS] in shared memory.  A warp takes at
-// least min_share positions, if there are fewer than `warps` times that.  total < 2^31.
+// least min_share positions, if there are fewer than `warps` times that.  The total is below 2^31 - 2^12.
 template <int THREADS, class Positions>
 __device__ __forceinline__ StreamShare stream_share(int rows, int gw, int warps, int min_share, int* s_sum, int* s_pre,
                                                     Positions positions) {
   constexpr int kWarps = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
-  StreamShare sh{0, 0, 0, 0, -1, 0};
-  auto take = [&]() {
-    sh.warps = (int)min((long)warps, (sh.total + min_share - 1) / min_share);
-    if (gw < sh.warps) {
-      sh.v0 = (int)(gw * sh.total / sh.warps);
-      sh.v1 = (int)((gw + 1) * sh.total / sh.warps);
+  StreamShare sh{{}, 0, 0, -1, 0};
+  auto take = [&](int total) {
+    sh.split = EvenSplit::of(total, min(warps, (total + min_share - 1) / min_share));
+    if (gw < sh.split.parts) {
+      sh.v0 = sh.split.begin(gw);
+      sh.v1 = sh.split.begin(gw + 1);
     }
   };
   if (rows > THREADS) {     // a pass for the total first
@@ -71,9 +89,10 @@ __device__ __forceinline__ StreamShare stream_share(int rows, int gw, int warps,
     mine = __reduce_add_sync(~0u, mine);
     if (lane == 0) s_sum[warp] = mine;
     __syncthreads();
+    int total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sh.total += s_sum[w];
-    take();
+    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+    take(total);
   }
   int before = 0;
   for (int i0 = 0; i0 < rows; i0 += THREADS) {
@@ -95,10 +114,7 @@ __device__ __forceinline__ StreamShare stream_share(int rows, int gw, int warps,
     }
     s_pre[tid] = inc;
     __syncthreads();
-    if (rows <= THREADS) {
-      sh.total = all;
-      take();
-    }
+    if (rows <= THREADS) take(all);
     if (sh.v0 < sh.v1 && sh.row < 0 && sh.v0 < before + all) {
       const int x = sh.v0 - before;      // the first row whose inclusive sum is above
       int lo = 0, hi = min(THREADS, rows - i0) - 1;
