@@ -160,7 +160,8 @@ __device__ Walk walk_begin(const PrefixArgs& a, int cta, int ctas, int total) {
 //   One tile of rows, held by both: the memory bounds both parts, and an SM gets its share of it: kByte a byte.
 // 64 rows over 8192 keys and 32768 own ones, CTAs of own keys 64 / 72 / 80 / 88 / 96: 43.5, 42.6, 42.5, 43.4, 45.8 us;
 // 256 rows over 32768, 32 / 34 / 36 / 40: 141, 134, 131, 133.
-constexpr float kOwnStart = 6000.f, kOwnTile = 102.f, kOwnTileAll = 1.25f;
+constexpr float kOwnStart = 6000.f, kOwnTile = 94.f, kOwnTileAll = 1.25f;
+constexpr float kOwnUnit = 2000.f;    // a unit, of one of a CTA's warps: its queries and its output
 constexpr float kPreStart = 18000.f, kPair = 1350.f, kByte = 1.f / 41.f;
 constexpr float kPiece = 5000.f;      // a second piece: its queries, the first one's drain and partial
 
@@ -169,15 +170,16 @@ struct Parts {
   int blocks;      // key blocks of all prefixes' groups
 };
 
-template <int KT>
+template <int KT, int WARPS>
 __device__ Parts share_out(const PrefixArgs& p, const OwnArgs& a, int G, int* s_red) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int tiles = 0, blocks = 0;
+  int tiles = 0, blocks = 0, rows = 0;
   for (int b = tid; b < a.B; b += 384) {
     int len;
     const int nb = row_tiles<KT>(a, b, len);
     if (nb == 0 && len != 0 && blockIdx.x == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
     tiles += nb;
+    rows += nb > 0;
   }
   for (int i = tid; i < p.P; i += 384) {
     const int m = p.prefix_lens[i];
@@ -186,24 +188,25 @@ __device__ Parts share_out(const PrefixArgs& p, const OwnArgs& a, int G, int* s_
   }
   tiles = __reduce_add_sync(~0u, tiles);
   blocks = __reduce_add_sync(~0u, blocks);
-  if (lane == 0) s_red[warp] = tiles, s_red[12 + warp] = blocks;
+  rows = __reduce_add_sync(~0u, rows);
+  if (lane == 0) s_red[warp] = tiles, s_red[12 + warp] = blocks, s_red[24 + warp] = rows;
   __syncthreads();
-  tiles = blocks = 0;
+  tiles = blocks = rows = 0;
 #pragma unroll
-  for (int w = 0; w < 12; ++w) tiles += s_red[w], blocks += s_red[12 + w];
+  for (int w = 0; w < 12; ++w) tiles += s_red[w], blocks += s_red[12 + w], rows += s_red[24 + w];
   const int runs = p.Hkv * p.outer;
   blocks *= runs;
   if (tiles == 0) return {0, blocks};
   if (blocks == 0) return {G, 0};
-  const float own = (float)tiles * (a.Hkv * a.nrb);
   const int last = p.Rp - (p.nrt - 1) * kPrefixRows;     // rows of the last unit
   const bool split = p.nrt == 1 && last <= kBM;
   const float tile = split ? 8192 * kByte : kOwnTile, block = split ? 4 * kBN * a.D * kByte : kPair;
   const float start = split ? kOwnStart : kPreStart;
+  const float own = (tiles * tile + rows * (kOwnUnit / WARPS)) * (a.Hkv * a.nrb), all = tiles * kOwnTileAll * (a.Hkv * a.nrb);
   unsigned best = ~0u;
   if (tid >= 1 && tid <= G - p.width) {
     const int teams = (G - tid) / p.width;
-    const float t_own = kOwnStart + fmaxf(own * tile / tid, own * kOwnTileAll);
+    const float t_own = kOwnStart + fmaxf(own / tid, all);
     // one prefix: no CTA crosses from a unit to the next if the teams are a multiple of its groups, or the reverse
     const bool whole = p.P == 1 && (teams % runs == 0 || runs % teams == 0);
     const int most = (blocks + teams - 1) / teams;
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(384, 1)
   uint8_t* sRing = smem + 2 * C::kTileBytes;   // kStages tiles: K_0, V_0, K_1, ...
   __shared__ PreBarriers bars;
   __shared__ Walk s_walk;
-  __shared__ int s_red[24];
+  __shared__ int s_red[36];
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // the same in a warp, told so
   Guard guard{&bars.abort, a.status};
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(384, 1)
   griddep_launch();
 
   // ------------------------------------------------ this CTA's part: own keys (spread evenly over the grid) or prefixes
-  const Parts parts = share_out<OwnCfg<D, NT>::KT>(a, own, gridDim.x, s_red);
+  const Parts parts = share_out<OwnCfg<D, NT>::KT, OwnCfg<D, NT>::kWarps>(a, own, gridDim.x, s_red);
   const int G = gridDim.x, X = __shfl_sync(~0u, parts.own, 0);
   const int before = blockIdx.x * X / G;       // own-key CTAs of lower number
   if ((blockIdx.x + 1) * X / G > before) {
