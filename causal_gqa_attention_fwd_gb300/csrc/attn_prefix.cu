@@ -440,7 +440,9 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_base = (uint32_t)wrow << 16;
     const uint32_t tS = tmem + lane_base + C::col_s(x);
     const uint32_t tO = tmem + lane_base + C::col_o(x);
-    const float c = a.scale_log2;
+    // a negative scale is its absolute value on negated queries; one of 0 the least that keeps a masked score's -infinity
+    const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const float c = fmaxf(fabsf(a.scale_log2), 1e-37f);
     uint32_t sc = 0, od = 0;                // S blocks and outputs taken so far
     int base = 0;
     bool ok = true;
@@ -463,6 +465,7 @@ __global__ void __launch_bounds__(384, 1)
           const bool real = wrow + i * kPer + lane / kC < rows;
           const long qr = ((long)b * a.Hkv + it.hkv) * a.R + in;
           v[i] = real ? __ldg(reinterpret_cast<const uint4*>(a.q + qr * D + part * 8)) : make_uint4(0, 0, 0, 0);
+          v[i].x ^= sign, v[i].y ^= sign, v[i].z ^= sign, v[i].w ^= sign;
           for (in += kPer; in >= a.R; in -= a.R) ++b;
         }
 #pragma unroll

@@ -156,6 +156,35 @@ def test_large_scores_and_growing_maxima(gq, tiles):
     check(got, R.prefix(ref[0], pre, ref[2], ref[3], 0.2), 128)
 
 
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("scale", [0.0, -0.11, 1e-30, 2.5])
+def test_scales(gq, tiles, scale):
+    f, args, ref = make(9, 1, 8, 2, 1, 128, 0, [300], [1 + 20 * i for i in range(9)], seed=14,
+                        Sp=tile_capacity(9, 1, 8, 2, 1, 128) if tiles else None)
+    got = getattr(gq, f)(*args, scale=scale)
+    assert gq.get_device_status() == 0
+    check(got, R.prefix(*ref, scale), 128)
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+def test_a_prefix_that_is_not_finite(gq, tiles):
+    """An infinite value and a NaN key of one prefix: its own rows are what the definition makes of them, others are whole."""
+    B, P, Hq = 8, 2, 16
+    f, args, ref = make(B, P, Hq, 2, 1, 64, 16, [200, 150], [3 + i for i in range(B)], seed=15, junk=0.0,
+                        Sp=tile_capacity(B, P, Hq, 2, 1, 64) if tiles else None)
+    page = int(args[3][0, 4])                       # keys 64..79 of prefix 0
+    args[2][page, 1, 3, 7] = math.inf
+    o, lse = getattr(gq, f)(*args, scale=0.125)
+    assert gq.get_device_status() == 0
+    want = R.prefix(*ref, 0.125)
+    o[:4, 8:, :, 7] = want[0][:4, 8:, :, 7].bfloat16().cuda()          # infinity, where the definition says so
+    check((o, lse), want, 64)
+    args[1][page, 0, 9] = math.nan
+    o, lse = getattr(gq, f)(*args, scale=0.125)
+    assert bool(torch.isnan(o[:4, :8]).all()) and bool(torch.isnan(lse[:4, :8]).all())
+    check((o[4:], lse[4:]), [x[4:] for x in want], 64)
+
+
 def test_no_prefix_at_all(gq):
     f, args, ref = make(3, 1, 4, 2, 1, 64, 0, [0], [9, 200, 1], seed=5)
     empty = torch.empty(1, 2, 0, 64, dtype=torch.bfloat16, device="cuda")
