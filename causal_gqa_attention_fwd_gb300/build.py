@@ -26,7 +26,8 @@ EXT_SOURCE = os.path.join(CSRC, "cache_binding.cpp")
 
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_split.cu", "attn_decode.cu",
            "cache_api.cu", "cache_ops.cu", "attn_decode_q4.cu", "attn_prefix.cu", "attn_own.cu", "cache_evict.cu"]
-HEADERS = ["sm103.cuh", "kernels.h", "tmap.h", "rope.h", "bwd_common.cuh", "api_util.h", "cache_ops.h", "fp4.cuh", "stream.cuh", "own_keys.cuh"]
+HEADERS = ["sm103.cuh", "kernels.h", "tmap.h", "rope.h", "bwd_common.cuh", "api_util.h", "cache_ops.h", "fp4.cuh",
+           "stream.cuh", "own_keys.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

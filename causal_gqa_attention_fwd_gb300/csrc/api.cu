@@ -923,6 +923,10 @@ PrefixWs prefix_ws(const PrefixPlan& p, const OwnPlan& d, int P, int Hkv, int D)
 
 attn_status prefix_check(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, int D) {
   if (P < 1 || Sp < 0) return ATTN_ERR_SHAPE;
+  // sizes up to which the plans count in 32 bits
+  if (B > 0 && Tq > 0 && Hq > 0 &&
+      ((long)B * Hq > 0x3fffffffL / Tq || S > 0x7fffffff - 512 || Sp > 0x7fffffff - 512))
+    return ATTN_ERR_SHAPE;
   const attn_status st = decode_check(B, Hq, Hkv, Tq, S, D);
   if (st != ATTN_OK) return st;
   if (B % P) return ATTN_ERR_SHAPE;
@@ -937,7 +941,8 @@ attn_status prefix_check(int B, int Hq, int Hkv, int Tq, int P, int Sp, int S, i
 
 // Everything after the layout-specific checks.
 attn_status prefix_common(const void* q, const CUtensorMap& pk, const CUtensorMap& pv, const int* prefix_lens,
-                          const int* prefix_table, int max_prefix_pages, const gqa::OwnMaps& maps, const int* cache_lens, const int* block_table, int max_pages, int page_size, int num_pages,
+                          const int* prefix_table, int max_prefix_pages, const gqa::OwnMaps& maps,
+                          const int* cache_lens, const int* block_table, int max_pages, int page_size, int num_pages,
                           void* o, float* lse, void* workspace, int B, int Hq, int Hkv, int Tq, int P, int Sp, int S,
                           int D, float scale, void* stream) {
   attn_status st = check_arch();

@@ -189,7 +189,7 @@ attn_status cache_weights(const void* q, const void* k, const void* ksf, float k
   const long S = block_table ? (long)page_size * max_pages : page_size;
   const float scale_log2 = scale * k_scale * 1.4426950408889634f;
   if (S > 0x7fffffffL - 512 || (long)page_size * num_pages > 0x7fffffffL || !isfinite(scale_log2) || !isfinite(scale) ||
-      !isfinite(k_scale) || (long)B * Hq * Tq > 0x7fffffffL || (long)B * max_pages > 0x7fffffffL ||
+      !isfinite(k_scale) || (Tq > 0 && (long)B * Hq > 0x3fffffffL / Tq) || (long)B * max_pages > 0x7fffffffL ||
       (long)B * Hkv > 0x7fffffffL / ((S + 31) / 32 + 1))
     return ATTN_ERR_SHAPE;
   if (!block_table && num_pages != B) return ATTN_ERR_SHAPE;

@@ -39,6 +39,21 @@ def test_prefix_refusals(lib):
     assert lib.attn_decode_prefix_workspace_size(4, 8, 2, 1, 3, 256, 64, 128) == 0
 
 
+def test_sizes_beyond_the_plans_are_refused(lib):
+    """Sizes up to the largest integer, in every argument: a workspace that memory could hold, or a refusal."""
+    import itertools
+    top = 0x7fffffff
+    vals = [1, 8, 255, 65535, 1 << 20, 1 << 30, top - 300, top - 255, top - 16, top]
+    for B, Tq, Sp, S in itertools.product(vals, repeat=4):
+        for P in (1, B):
+            for Hq, Hkv in ((1, 1), (64, 8)):
+                assert lib.attn_decode_prefix_workspace_size(B, Hq, Hkv, Tq, P, Sp, S, 64) < 1 << 44
+    assert lib.attn_decode_prefix_workspace_size(1, 1, 1, top, 1, 0, top, 64) == 0
+    w = [A] * 6
+    assert lib.attn_cache_weights(*w, 1, 1, 1, top, top, 1, 1, 64, 0.1, None) == 2
+    assert lib.attn_cache_weights(*w, top, 64, 64, top, 1, 1, 1, 64, 0.1, None) == 2
+
+
 def test_paged_prefix_refusals(lib):
     def f(q=A, k=A, v=A, pt=A, pl=A, bt=A, ln=A, o=A, lse=A, ws=A, wsb=1 << 40, B=4, Hq=8, Hkv=2, Tq=1, P=2, ps=16, n=9, mpp=4,
           mp=4, D=128, scale=0.1):
