@@ -5,11 +5,14 @@
 // S_j = scale q k_j the softmax over both is the two softmaxes joined,
 //   M = max(M_p, M_o),  L = L_p 2^(M_p - M) + L_o 2^(M_o - M),
 //   O = (O_p 2^(M_p - M) + O_o 2^(M_o - M)) / L,   LSE = ln 2 (M + log2 L),
-// so the two parts run apart: attn_prefix leaves unnormalised partials
-// (O, M, L) of the prefix, attn_own (attn_own.cu) those of the rows' own caches,
-// and prefix_merge joins them.
+// so the two parts run apart, in one launch: some CTAs of attn_prefix leave
+// unnormalised partials (O, M, L) of the prefixes, the others those of the rows'
+// own caches (own_keys.cuh), and prefix_merge joins them.  (Where few rows share
+// a prefix attn_own.cu takes both parts as one stream instead.)
 //
-// attn_prefix  The W * G * Tq query rows that meet a (prefix, K/V head) are a
+// attn_prefix  Which CTAs take the own keys is settled on the device, by the
+//   lengths (share_out).  To a prefix: the W * G * Tq query rows that meet a
+//   (prefix, K/V head) are a
 //   matrix, and both products are GEMM-shaped: tiles of 128 query rows as M,
 //   128 keys as N of the score MMA, on tcgen05 with the accumulators in TMEM
 //   (S_A, S_B, O_A, O_B; P in bf16 over its S), as the prefill kernel has
@@ -23,6 +26,11 @@
 //   where a page is shorter than a block), warp 1 MMA issuer, warps 4-7 and
 //   8-11 softmax of a tile each, thread = row; they also gather the query rows
 //   (a tile's rows lie in runs of G * Tq in memory) and write the partials.
+//   Bound: many rows, the MMAs (a pair of tiles' two products take 1.1 us a
+//   block of 128 keys at the rate of a large library product, 1.35 here);
+//   few rows, the stream of keys and values.  64 rows over 8192 keys and ~32000
+//   own ones 43 us (25 at the copy rate), 256 rows over 32768 keys and ~70000
+//   own ones 131 us (74).
 #include "own_keys.cuh"
 
 namespace gqa {
@@ -560,7 +568,7 @@ __global__ void __launch_bounds__(384, 1)
             f2_split(fma2(f2(sf[q * 32 + 2 * k], sf[q * 32 + 2 * k + 1]), c2, nm2), t0, t1);
             const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
             acc[k & 3] = add2(acc[k & 3], f2(p0, p1));
-            pk[k] = pack_bf16x2(p0, p1);   // P rounded to bf16 (2^-9 of each weight), as the prefill's: the MMA's type
+            pk[k] = pack_bf16x2(p0, p1);   // rounded to bf16 (2^-8 of each weight): the type of V, for the MMA
           }
           tmem_st_x16(tS + q * 16, pk);
           if (q == kBN / 64 - 1) {
@@ -629,7 +637,8 @@ __global__ void __launch_bounds__(384, 1)
 // maximum M, and the weighted sums of the partials and of their L.  What a row costs is a chain of loads (lengths; which
 // pieces; their statistics and partials, kAt pieces at a time).
 template <int D, int WPR, int kAt>
-__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) prefix_merge_kernel(const PrefixArgs p, const OwnArgs a, __nv_bfloat16* o, float* lse) {
+__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256)
+    prefix_merge_kernel(const PrefixArgs p, const OwnArgs a, __nv_bfloat16* o, float* lse) {
   constexpr int V = D / 32;     // features a lane holds
   constexpr int kW = WPR > 8 ? WPR : 8;
   __shared__ float s_acc[WPR > 1 ? kW : 1][D], s_m[kW], s_l[kW];
@@ -651,6 +660,11 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) prefix_merge_kernel(
     const float* po;
     const float2* pml;
     int np = 0, pstep;
+    // a kernel that gave up (reported) has not written all of its counts
+    const unsigned entries = kOwnMaxWarps + a.Hkv * (a.B * a.nrb + a.P * a.nrbp);
+    auto pieces = [&](int2 c) {
+      return (unsigned)c.x < entries && (unsigned)c.y <= (unsigned)kOwnMaxWarps && (unsigned)(c.x + c.y) <= entries ? c.y : 0;
+    };
     const int2 own = a.counts[(long)a.P * a.Hkv * a.nrbp + (long)bh * a.nrb + rr / a.block];
     if (a.P == 0) {
       pstep = 1;
@@ -664,9 +678,9 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) prefix_merge_kernel(
       const long at = (long)c.x * a.rows_ws + gr % a.block;
       po = a.ws_o + at * D;
       pml = a.ws_ml + at;
-      np = min(max(c.y, 0), kOwnMaxWarps);
+      np = pieces(c);
     }
-    const int n = np + min(max(own.y, 0), kOwnMaxWarps);
+    const int n = np + pieces(own);
     const long obase = (long)own.x * a.rows_ws + rr % a.block;
     for (int s0 = part; s0 < n; s0 += WPR * kAt) {
       float2 ml[kAt];

@@ -2,9 +2,9 @@
 // a cache down to the keys that received most, for sm_103a.
 //
 // cache_weights  w_j += sum over a step's queries that see key j of
-//   exp(scale q . k_j - lse), from w_j = 0 for its Tq new keys: K is read once (memory bounds it for few
-//   queries), the scores are warp-level MMAs with 16 keys as M and 8 query rows
-//   as N.  A dot product does not care for the order of its terms, so a lane
+//   exp(scale q . k_j - lse), from w_j = 0 for its Tq new keys: K is read once
+//   (memory bounds it for few queries), the scores are warp-level MMAs with 16
+//   keys as M and 8 query rows as N.  A dot product does not care for the order of its terms, so a lane
 //   takes whole 16-byte parts of a key row as its share of the k index and
 //   needs neither shared memory nor shuffles to bring them into place; the
 //   query fragments follow the same order.  E4M3 and 4-bit codes are widened to
@@ -13,12 +13,19 @@
 //   the row's largest feature.  One lane group adds up a key's weight in a
 //   fixed order: the same call gives the same bits.
 //
+//   Many keys: 32 of them a tile, all in one stream that the grid's warps share
+//   (cache_weights_kernel); 8 long rows of 8 heads of 128, 61 us at the copy
+//   rate: bf16 keys 67 us; 4-bit ones (18) 32, bound by the instructions that
+//   widen them.
+//
 // evict  a cluster of CTAs a (row, K/V head): each keeps a run of the weights in
-//   shared memory; the budget-th largest by radix selection over the weights'
-//   bits (11, 11, 10, histograms added up through distributed shared memory),
-//   then the kept positions in order, then the rows of every plane to the front.
-//   Row i comes from position src_i >= i, and src grows, so going up in chunks a
-//   chunk's rows are read before any is overwritten.
+//   shared memory (short rows: each all of them, and no exchange); the budget-th
+//   largest by radix selection over the weights' bits (11, 11, 10, histograms
+//   added up through distributed shared memory), then the kept positions in
+//   order, then the rows of every plane to the front.
+//   Row i comes from position src_i >= i, and src grows, so going up in phases a
+//   phase's rows are read before any is overwritten.
+//   Bound: the chain of passes and barriers (some 10 us), then the moves.
 #include <cuda_fp16.h>
 
 #include "cache_ops.h"
@@ -203,6 +210,7 @@ __device__ __forceinline__ RowConstants row_constants(const WeightsArgs& a, long
 }
 
 // ------------------------------------------------ at most 8 NT query rows a key: one stream of tiles over all warps
+// Warps: what registers leave; 4-bit keys, whose instructions bound it, with more of them (20 and 16; 12, 16, 24: slower).
 template <int D, CacheFmt F, int NT>
 struct NarrowCfg {
   static constexpr int kWarps = F == kCacheQ4 ? (NT == 1 ? 20 : 16) : 12;
@@ -367,7 +375,7 @@ __global__ void __launch_bounds__(NarrowCfg<D, F, NT>::kThreads, 1) cache_weight
   if (bad) atomicCAS(a.status, 0, kDevBadPage);
 }
 
-// ------------------------------------------------ more query rows (a window of a prompt): a CTA a chunk of keys
+// ------------------------------------------------ more query rows (a window of a prompt), or few keys: a CTA a chunk of keys
 // Each warp holds the fragments of 32 keys in registers and takes the query rows, kWRows at a time, from shared memory.
 template <int D, CacheFmt F>
 __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const WeightsArgs a) {
@@ -491,9 +499,15 @@ template <int D, CacheFmt F>
 cudaError_t launch_weights_df(const WeightsArgs& a, int sms, cudaStream_t stream) {
   using C1 = NarrowCfg<D, F, 1>;
   using C2 = NarrowCfg<D, F, 2>;
-  if (a.R <= 8) return launch_weights<cache_weights_kernel<D, F, 1>>(dim3(sms), C1::kThreads, C1::kSmemBytes, a, stream);
-  if (a.R <= 16) return launch_weights<cache_weights_kernel<D, F, 2>>(dim3(sms), C2::kThreads, C2::kSmemBytes, a, stream);
-  const dim3 grid((unsigned)((long)a.B * a.Hkv * ((a.S + (long)kWKeys - 1) / kWKeys)));
+  // The stream is for many keys: where a CTA a chunk of the capacity are resident together (two an SM, heads of 64 three),
+  // they have no shares to work out.  us, CTAs / stream, 8 rows: bf16 keys of 128, 32768: 3.4 / 4.1, 65536: 4.3 / 5.4,
+  // 98304: 7.0 / 6.5; keys of 64, 98304: 4.1 / 5.0, 131072: 5.9 / 5.6; E4M3 of 128, 65536: 4.1 / 5.5, 131072: 6.8 / 6.7;
+  // 4-bit of 128, 65536: 3.8 / 6.0, 131072: 6.3 / 7.3, 262144: 11.2 / 9.4.
+  const long ctas = (long)a.B * a.Hkv * ((a.S + (long)kWKeys - 1) / kWKeys);
+  if (a.R <= 16 && ctas > (D == 128 ? 2L : 3L) * sms)
+    return a.R <= 8 ? launch_weights<cache_weights_kernel<D, F, 1>>(dim3(sms), C1::kThreads, C1::kSmemBytes, a, stream)
+                    : launch_weights<cache_weights_kernel<D, F, 2>>(dim3(sms), C2::kThreads, C2::kSmemBytes, a, stream);
+  const dim3 grid((unsigned)ctas);
   return launch_weights<cache_weights_wide_kernel<D, F>>(grid, 32 * kWWarps, kWWarps * KeyStage<D, F>::kBytes, a, stream);
 }
 
@@ -522,7 +536,9 @@ constexpr int kBins = 2048;          // of a pass over 11 bits (the last: 10)
 constexpr int kPlaceBytes = 4096;    // of rows that a warp has on the way between reading and writing
 constexpr int kPlaces = kEvWarps * kPlaceBytes;
 constexpr int kKeyBytes = 80 << 10;  // weights a CTA keeps in shared memory; a longer share is read again each pass
-constexpr int kAlone = 8192;         // positions up to which each CTA selects by itself
+// Positions up to which each CTA of a cluster selects by itself, without the cluster's barriers (us, alone / together,
+// 16 units: 2048 positions 11.8 / 12.7, 4096: 20.6 / 18.0, 8192: 29.8 / 25.0).
+constexpr int kAlone = 2048;
 
 // Whole numbers in the weights' order: NaN above all, -0 = 0; 0 is below all of them.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -553,7 +569,8 @@ struct Task {
   uint8_t* base;
   int row_bytes, size, parts, cnt;
   long from, to;      // slots of row `lane`; -1: it stays, or is in a page outside the pool
-  __device__ __forceinline__ void find(const EvictPlane& pl, const Slots& slot_of, const int* list, int d0, int rows, int lane) {
+  __device__ __forceinline__ void find(const EvictPlane& pl, const Slots& slot_of, const int* list, int d0, int rows, int S,
+                                       int lane) {
     base = static_cast<uint8_t*>(pl.p);
     row_bytes = pl.row_bytes;
     size = pl.size;
@@ -561,7 +578,7 @@ struct Task {
     cnt = rows;
     const int src = lane < cnt ? list[d0 + lane] : -1;
     from = to = -1;
-    if (src > d0 + lane) {
+    if (src > d0 + lane && src < S) {
       from = slot_of(src);
       to = from >= 0 ? slot_of(d0 + lane) : -1;
       if (to < 0) from = -1;
@@ -633,7 +650,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const Slots& slot_
       Task task;
       if (mine) {
         const int d0 = c0 + t * a.planes[i].run;
-        task.find(a.planes[i], slot_of, list, d0, min(a.planes[i].run, c1 - d0), lane);
+        task.find(a.planes[i], slot_of, list, d0, min(a.planes[i].run, c1 - d0), a.S, lane);
         task.read(place, lane);
       }
       if (held) cluster_sync();
@@ -841,7 +858,9 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictArgs a)
     const unsigned bg = __ballot_sync(0xffffffffu, j < w1 && k > thr), be = __ballot_sync(0xffffffffu, j < w1 && k == thr);
     const unsigned below = (1u << lane) - 1u;
     const int g = gt + __popc(bg & below), e = eq + __popc(be & below);
-    if ((bg >> lane & 1u) || ((be >> lane & 1u) && e < need)) list[a.first + g + min(e, need)] = j;
+    // (in bounds whatever happens: weights read again each pass may be another row's too, against the contract)
+    const int at = a.first + g + min(e, need);
+    if (((bg >> lane & 1u) || ((be >> lane & 1u) && e < need)) && at < a.budget) list[at] = j;
     gt += __popc(bg);
     eq += __popc(be);
   }

@@ -523,7 +523,9 @@ GQA_ATTN_API attn_status attn_decode_paged_q4_fwd(const void* q, const void* k4_
  * be 0 (k_prefix, v_prefix NULL).  Queries and keys are taken as they are: with
  * rotary positions, rotated before (attn_rope, attn_cache_append), an own key's
  * position following the prefix's.  P is rounded to bf16 for the P V product;
- * everything else is f32.  How a row's keys are cut into pieces follows from
+ * everything else is f32.  Rows of a cache that no query of a (row, K/V head)
+ * sees may hold anything; a V that is infinite or NaN at an own position that
+ * one of the Tq queries sees may make NaN of the others too.  How a row's keys are cut into pieces follows from
  * the sizes and the lengths: the same call gives the same bits.
  * workspace: attn_decode_prefix_workspace_size() bytes, 256-byte aligned, no
  * initialisation; calls in flight at once need one each. */

@@ -107,6 +107,18 @@ def test_every_byte(gq, case, kind):
     check(got, reference(planes, w, table, lens, budget, recent, first))
 
 
+@pytest.mark.parametrize("kind", ["heavy", "ties", "signs"])
+@pytest.mark.parametrize("S", [255, 2048, 2049, 9000])          # one CTA; CTAs that select alone, and together
+@pytest.mark.parametrize("budget", [0.5, 0.97])
+def test_capacities(gq, S, kind, budget):
+    lens = [S, S - 1, S * 2 // 3]
+    planes, w, table = make("bf16", 3, 2, 64, 0, lens, 6, kind)
+    k = int(S * budget)
+    got = run(gq, planes, w, table, lens, k, 11, 5)
+    assert gq.get_device_status() == 0
+    check(got, reference(planes, w, table, lens, k, 11, 5))
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "q4", "none", "odd"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("page", [0, 16])

@@ -27,9 +27,10 @@ def test_debug_prefix(dbg, case, tiles):  # noqa: F811
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "q4"])
-def test_debug_weights(dbg, fmt):  # noqa: F811
+@pytest.mark.parametrize("stream", [False, True])
+def test_debug_weights(dbg, fmt, stream):  # noqa: F811
     case = (3, 12, 4, 5, 64, 7, [0, 33, 100])
-    planes, keys, q, table, w = W.make(fmt, *case, seed=2)
+    planes, keys, q, table, w = W.make(fmt, *case, seed=2, S=W.stream_capacity(3, 4) if stream else None)
     lse = W.lse_of(q, keys, table, case[6], 0.125)
     out = W.call(dbg, fmt, planes, q, lse, case[6], w.cuda(), table, 0.125)
     no_check_fired(dbg)

@@ -120,6 +120,43 @@ def test_against_the_definition(gq, case, fmt):
     assert torch.equal(out[0].nan_to_num(-1), out[1].nan_to_num(-1))         # the same bits again
 
 
+def stream_capacity(B, Hkv):
+    """A capacity whose chunks of 256 positions are more than the CTAs that any GPU of this kind holds at once: few query
+    rows then go by the stream of tiles whatever the lengths are."""
+    return 256 * (3 * 160 // (B * Hkv) + 1)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "q4"])
+@pytest.mark.parametrize("case", [c for c in CASES if c[1] // c[2] * c[3] <= 16] + [(3, 8, 4, 8, 128, 0, [3000, 7, 0])],
+                         ids=lambda c: f"B{c[0]}H{c[1]}-{c[2]}T{c[3]}D{c[4]}p{c[5]}n{max(c[6])}")
+def test_few_rows_of_a_large_capacity(gq, case, fmt):
+    B, Hq, Hkv, Tq, D, page, lens = case
+    planes, keys, q, table, w = make(fmt, *case, seed=7, S=stream_capacity(B, Hkv))
+    scale = 1 / math.sqrt(D)
+    lse = lse_of(q, keys, table, lens, scale)
+    out = [w.cuda(), w.cuda()]
+    for o in out:
+        call(gq, fmt, planes, q, lse, lens, o, table, scale)
+    assert gq.get_device_status() == 0
+    check(out[0], w, q, keys, lse, table, lens, scale)
+    assert torch.equal(out[0].nan_to_num(-1), out[1].nan_to_num(-1))
+
+
+def test_a_large_capacity_reports_too(gq):
+    case = (3, 4, 2, 1, 64, 16, [20, 40, 33])
+    planes, keys, q, table, w = make("bf16", *case, seed=8, S=stream_capacity(3, 2))
+    lse = lse_of(q, keys, table, case[6], 0.125)
+    for bad in (-1, 1 << 30):
+        out = call(gq, "bf16", planes, q, lse, [20, bad, 33], w.cuda(), table, 0.125)
+        assert gq.get_device_status() == 5
+        check(out, w, q, keys, lse, table, [20, 0, 33], 0.125)
+    t = table.clone()
+    t[1, 1] = planes[0].shape[0]
+    out = call(gq, "bf16", planes, q, lse, case[6], w.cuda(), t, 0.125)
+    assert gq.get_device_status() == 11
+    assert torch.equal(out[int(table[1, 1])].cpu().nan_to_num(-1), w[int(table[1, 1])].nan_to_num(-1))
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "q4"])
 @pytest.mark.parametrize("qs", [1e-30, 1e-3, 30.0, 1e30])
 def test_queries_of_any_size(gq, fmt, qs):
