@@ -13,6 +13,7 @@
 //   the row's largest feature.  One lane group adds up a key's weight in a
 //   fixed order: the same call gives the same bits.
 //
+//   A long window of queries is GEMM-shaped: tcgen05 (cache_weights_window).
 //   Many keys: 32 of them a tile, all in one stream that the grid's warps share
 //   (cache_weights_kernel); 8 long rows of 8 heads of 128, 61 us at the copy
 //   rate: bf16 keys 67 us; 4-bit ones (18) 32, bound by the instructions that
@@ -482,6 +483,257 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
   if (!ok) mbar_wait_drain(&s_full[warp], 0);        // never leave with copies in flight
 }
 
+// ------------------------------------------------ a long window: S^T = K Q^T on tcgen05
+// A CTA a chunk of 256 keys, in shared memory as two tiles of 128 (M); the query rows (N) go by 64, and while a block's
+// weights are formed the next one's products run.  A thread has one key's scores and adds its weights up by itself.
+// Bound: instructions beside the exponentials; for 8- and 4-bit keys the query rows' conversion to f16, which every CTA
+// does for itself.  512 rows over 2^20 keys: bf16 of 128 221 us, of 64 174 (3.1e12 exponentials a second), E4M3 of 128 340.
+template <int D>
+struct WindowCfg {
+  static constexpr int kRows = 64, kKeys = 256;
+  static constexpr int kBoxes = D / 64;             // of 64 features, 128 bytes a row
+  static constexpr int kKeyBox = 128 * 128, kRowBox = kRows * 128;
+  static constexpr int kSmemBytes = kBoxes * (2 * kKeyBox + 2 * kRowBox) + 1024;
+};
+
+// Part c (16 bytes) of row r of a tile whose boxes are `box` bytes apart, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_at(uint32_t tile, int box, int r, int c) {
+  return tile + (c >> 3) * box + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+template <int D, CacheFmt F>
+__global__ void __launch_bounds__(WindowCfg<D>::kKeys, 2) cache_weights_window_kernel(const WeightsArgs a) {
+  using C = WindowCfg<D>;
+  using P = KeyPart<D, F>;
+  constexpr int kParts = D / 8, kAt = C::kRows * kParts / C::kKeys;
+  extern __shared__ uint8_t smem_raw[];
+  // RowConstants of the block before, this and the next: c, l side by side (bf16 keys: c is the same for all)
+  constexpr int kEach = F == kCacheBf16 ? 1 : 2;
+  __shared__ __align__(16) float s_c[3][C::kRows * kEach];
+  __shared__ int s_lim[3][C::kRows], s_whole[3][2];      // s_whole: 32 rows that see all of the chunk's keys
+  __shared__ uint64_t s_done[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31, x = warp >> 2;
+  const int bh = (int)(blockIdx.x % (unsigned)(a.B * a.Hkv)), b = bh / a.Hkv, hkv = bh % a.Hkv;
+  const int c0 = (int)(blockIdx.x / (unsigned)(a.B * a.Hkv)) * C::kKeys;
+  griddep_wait();
+  const int len = a.cache_lens[b];
+  if (len < 0 || len > a.S) {
+    if (c0 == 0 && tid == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+    return;
+  }
+  if (c0 >= len) return;
+  const uint32_t s_k = (smem_u32(smem_raw) + 1023) & ~1023u, s_q = s_k + 2 * C::kBoxes * C::kKeyBox;
+  const uint32_t tile = s_k + x * C::kBoxes * C::kKeyBox;
+  if (tid == 0) {
+    s_abort = 0;
+    mbar_init(&s_done[0], 1);
+    mbar_init(&s_done[1], 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s_tmem, 4 * C::kRows);
+    tmem_relinquish();
+  }
+  const Guard guard{&s_abort, a.status};
+  // ---------------------------------------------------------- query rows, D / 8 lanes each; on their way a block ahead
+  uint4 q[kAt];
+  float lse = -INFINITY;                                 // of row tid
+  auto load_q = [&](int r0) {
+    const int rows = min(C::kRows, a.R - r0);
+    const long row0 = (long)bh * a.R + r0;
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) {
+      const int at = tid + i * C::kKeys;
+      q[i] = at < rows * kParts ? __ldg(reinterpret_cast<const uint4*>(a.q + row0 * D) + at) : make_uint4(0, 0, 0, 0);
+    }
+    lse = tid < rows ? __ldg(a.lse + row0 + tid) : -INFINITY;
+  };
+  auto store_q = [&](int blk) {
+    const int r0 = blk * C::kRows, buf = blk & 1, cbuf = blk % 3;
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) {
+      const int at = tid + i * C::kKeys, r = at / kParts, c = at % kParts;
+      uint4 v = q[i];
+      int e = 0;
+      if constexpr (F != kCacheBf16) {
+        float f[8];
+        bf16x8_to_f32(v, f);
+        float mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(f[k]));
+#pragma unroll
+        for (int o = 1; o < kParts; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+        if (mx > 0.f && mx < INFINITY) e = 14 - ilogbf(mx);     // the largest feature goes to [2^14, 2^15)
+        // 2^e in two factors, each a normal number; what the first makes subnormal is below f16's least by far
+        const float e0 = __int_as_float((127 + (e >> 1)) << 23), e1 = __int_as_float((127 + e - (e >> 1)) << 23);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = f[k] * e0 * e1;
+        v = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
+      }
+      st_shared_v4(tile_at(s_q + buf * C::kBoxes * C::kRowBox, C::kRowBox, r, c), v.x, v.y, v.z, v.w);
+      if (kEach == 2 && c == 0) s_c[cbuf][2 * r] = ldexpf(a.scale_log2, -e);
+    }
+    if (tid < C::kRows) {
+      s_c[cbuf][kEach * tid + kEach - 1] = -lse * 1.4426950408889634f;
+      s_lim[cbuf][tid] = lse == -INFINITY ? -1 : len - a.Tq + (r0 + tid) % a.Tq;
+      const bool all = __all_sync(~0u, c0 + C::kKeys - 1 <= len - a.Tq && lse > -INFINITY && r0 + tid < a.R);
+      if (lane == 0) s_whole[cbuf][warp] = all;
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+  };
+  // warp 0: both tiles' scores of the block in buffer `buf`
+  auto issue = [&](int buf) {
+    constexpr uint32_t kIdesc = F == kCacheBf16 ? idesc_bf16(128, C::kRows, false, false) : idesc_f16(128, C::kRows, false, false);
+    tc_fence_after();
+    const uint64_t kd = sdesc_sw128(s_k, 16, 1024), qd = sdesc_sw128(s_q + buf * C::kBoxes * C::kRowBox, 16, 1024);
+    if (elect_one()) {
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          mma_ss(s_tmem + (2 * buf + t) * C::kRows, sdesc_add(kd, (t * C::kBoxes + (s >> 2)) * C::kKeyBox + (s & 3) * 32),
+                 sdesc_add(qd, (s >> 2) * C::kRowBox + (s & 3) * 32), kIdesc, s > 0);
+    }
+    __syncwarp();
+    tc_commit_warp(&s_done[buf]);
+  };
+  load_q(0);
+  // ---------------------------------------------------------- keys: thread = key, then lanes side by side along its row
+  const int j = c0 + tid;
+  long slot = -1;
+  if (j < len) {
+    const int i = a.block_table ? a.page(j) : 0, page = a.block_table ? a.block_table[(long)b * a.max_pages + i] : b;
+    if (page >= 0 && page < a.num_pages) slot = ((long)page * a.Hkv + hkv) * a.page.d + (j - i * a.page.d);
+    else atomicCAS(a.status, 0, kDevBadPage);
+  }
+  {
+    constexpr int kLanes = P::kRowBytes / 16, kPer = 32 / kLanes, kSteps = 32 / kPer;
+    const int part = lane % kLanes, row0 = lane / kLanes, r0 = (warp & 3) * 32;
+    if constexpr (F == kCacheBf16) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = i * kPer + row0;
+        const long s = __shfl_sync(~0u, slot, r);
+        if (s >= 0) copy_async<16>(tile_at(tile, C::kKeyBox, r0 + r, part), a.k + s * P::kRowBytes + part * 16);
+      }
+      copies_commit();
+      store_q(0);
+      copies_wait<0>();
+      fence_proxy_async_smem();
+    } else {
+      uint4 v[kSteps];
+      uint32_t sf[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const long s = __shfl_sync(~0u, slot, i * kPer + row0);
+        v[i] = make_uint4(0, 0, 0, 0);
+        sf[i] = 0;
+        if (s >= 0) {
+          v[i] = __ldg(reinterpret_cast<const uint4*>(a.k + s * P::kRowBytes + part * 16));
+          if constexpr (F == kCacheQ4) sf[i] = __ldg(reinterpret_cast<const uint16_t*>(a.ksf + s * (D / 16) + part * 2));
+        }
+      }
+      store_q(0);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = r0 + i * kPer + row0;
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        if constexpr (F == kCacheE4m3) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            st_shared_v4(tile_at(tile, C::kKeyBox, r, 2 * part + c), e4m3x2_to_f16(w[2 * c] & 0xffffu),
+                         e4m3x2_to_f16(w[2 * c] >> 16), e4m3x2_to_f16(w[2 * c + 1] & 0xffffu), e4m3x2_to_f16(w[2 * c + 1] >> 16));
+        } else {
+          const uint32_t both = e4m3x2_to_f16(sf[i]);      // the scales of 16 features each
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t f[4];
+            const uint32_t two = __byte_perm(both, both, c / 2 ? 0x3232 : 0x1010);
+            e2m1x8_to_f16(w[c], f);
+            st_shared_v4(tile_at(tile, C::kKeyBox, r, 4 * part + c), hmul2_u(f[0], two), hmul2_u(f[1], two),
+                         hmul2_u(f[2], two), hmul2_u(f[3], two));
+          }
+        }
+      }
+      fence_proxy_async_smem();
+    }
+  }
+  // the step's new keys had no weight before
+  const float old = slot >= 0 && j < len - a.Tq ? a.weights[slot] : 0.f;
+  __syncthreads();
+  griddep_launch();      // not before this CTA has its TMEM: the next kernel's CTAs may take theirs before they wait
+  if (warp == 0) issue(0);
+  if (C::kRows < a.R) load_q(C::kRows);
+  const uint32_t mine = s_tmem + ((uint32_t)(warp & 3) * 32 << 16) + x * C::kRows;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  bool ok = true;
+  const int blocks = (a.R + C::kRows - 1) / C::kRows;
+  int issued = 1;
+  for (int i = 0; i < blocks; ++i) {
+    const int buf = i & 1;
+    if (i + 1 < blocks) {
+      // its rows' place is free: this warp has waited for block i - 1's products
+      store_q(i + 1);
+      ok = __syncthreads_and(ok);      // and all warps have read block i - 1's scores
+      if (!ok) break;
+      if (warp == 0) issue(buf ^ 1);
+      ++issued;
+      if (i + 2 < blocks) load_q((i + 2) * C::kRows);
+    }
+    ok = __all_sync(~0u, mbar_wait(&s_done[buf], (i >> 1) & 1, guard));
+    if (ok) {
+      tc_fence_after();
+      const float* cs = s_c[i % 3];
+#pragma unroll 1
+      for (int n0 = 0; n0 < C::kRows; n0 += 32) {
+        uint32_t s[32];
+        tmem_ld_x32(mine + 2 * buf * C::kRows + n0, s);
+        tmem_ld_wait();
+        reg_fence<32>(s);
+        if (s_whole[i % 3][n0 / 32]) {
+          // a shared-memory word serves 32 lanes at once, but a 16-byte one takes four times as long as a 4-byte one: 16 a
+          // row (c, l, the last key seen) would take longer than the exponentials
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            float c[4], l[4];
+            if constexpr (kEach == 1) {
+              const float4 v = *reinterpret_cast<const float4*>(cs + n0 + k);
+              c[0] = c[1] = c[2] = c[3] = a.scale_log2;
+              l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
+            } else {
+              const float4 v = *reinterpret_cast<const float4*>(cs + 2 * (n0 + k)), w = *reinterpret_cast<const float4*>(cs + 2 * (n0 + k) + 4);
+              c[0] = v.x, c[1] = v.z, c[2] = w.x, c[3] = w.z;
+              l[0] = v.y, l[1] = v.w, l[2] = w.y, l[3] = w.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += ex2_approx(fmaf(__uint_as_float(s[k + e]), c[e], l[e]));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float c = kEach == 1 ? a.scale_log2 : cs[2 * (n0 + k)], l = cs[kEach * (n0 + k) + kEach - 1];
+            const float p = ex2_approx(fmaf(__uint_as_float(s[k]), c, l));
+            if (j <= s_lim[i % 3][n0 + k]) sum[k & 3] += p;
+          }
+        }
+      }
+    }
+  }
+  if (ok && slot >= 0) a.weights[slot] = (sum[0] + sum[1]) + (sum[2] + sum[3]) + old;
+  // never leave with MMAs in flight (after a wait that gave up): the last block's, and the one's before
+  if (!ok)
+    for (int i = max(issued - 2, 0); i < issued; ++i) mbar_wait_drain(&s_done[i & 1], (i >> 1) & 1);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(s_tmem, 4 * C::kRows);
+  }
+}
+
 template <auto KERNEL>
 cudaError_t launch_weights(dim3 grid, int threads, int smem, const WeightsArgs& a, cudaStream_t stream) {
   static bool attr_set[64] = {};
@@ -508,6 +760,12 @@ cudaError_t launch_weights_df(const WeightsArgs& a, int sms, cudaStream_t stream
     return a.R <= 8 ? launch_weights<cache_weights_kernel<D, F, 1>>(dim3(sms), C1::kThreads, C1::kSmemBytes, a, stream)
                     : launch_weights<cache_weights_kernel<D, F, 2>>(dim3(sms), C2::kThreads, C2::kSmemBytes, a, stream);
   const dim3 grid((unsigned)ctas);
+  // Warp MMAs keep up with few rows only, but need no tiles in shared memory.  us, this / those: bf16 keys of 128, 131072
+  // of them: 32 rows 9.0 / 9.9, 64: 9.1 / 13.8, 128: 12.6 / 22.9, 512: 34 / 75; 2^20, 512 rows: 221 / 490; keys of 64,
+  // 2^20: 48 rows 50 / 45, 64: 50 / 51, 128: 69 / 82.  E4M3 of 128, 262144: 64 rows 21 / 21, 96: 31 / 29, 128: 31 / 34,
+  // 512: 93 / 119; 4-bit: 96 rows 31 / 32, 512: 93 / 130.
+  if (a.R > (F != kCacheBf16 ? 96 : D == 128 ? 32 : 48))
+    return launch_weights<cache_weights_window_kernel<D, F>>(grid, WindowCfg<D>::kKeys, WindowCfg<D>::kSmemBytes, a, stream);
   return launch_weights<cache_weights_wide_kernel<D, F>>(grid, 32 * kWWarps, kWWarps * KeyStage<D, F>::kBytes, a, stream);
 }
 

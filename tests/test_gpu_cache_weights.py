@@ -120,6 +120,59 @@ def test_against_the_definition(gq, case, fmt):
     assert torch.equal(out[0].nan_to_num(-1), out[1].nan_to_num(-1))         # the same bits again
 
 
+LONG = [
+    # windows of many query rows: whole and partial blocks of 64 rows, chunks of 256 keys that all rows see and others
+    (2, 8, 2, 9, 128, 0, [700, 257]),                     # 36 rows
+    (2, 14, 2, 14, 64, 16, [513, 256]),                   # 98
+    (3, 8, 2, 32, 128, 64, [1023, 31, 0]),                # 128; rows shorter than the window
+    (1, 8, 1, 25, 64, 7, [300]),                          # 200
+    (2, 16, 2, 40, 128, 16, [40, 900]),                   # 320
+    (1, 32, 4, 67, 64, 0, [1500]),                        # 536
+]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "q4"])
+@pytest.mark.parametrize("case", LONG, ids=lambda c: f"B{c[0]}H{c[1]}-{c[2]}T{c[3]}D{c[4]}p{c[5]}n{max(c[6])}")
+def test_long_windows(gq, case, fmt):
+    B, Hq, Hkv, Tq, D, page, lens = case
+    planes, keys, q, table, w = make(fmt, *case, seed=9)
+    scale = -1 / math.sqrt(D) if B == 1 else 1 / math.sqrt(D)
+    lse = lse_of(q, keys, table, lens, scale)
+    lse[0, 1] = -math.inf                                                    # a head that the caller leaves out
+    out = [w.cuda(), w.cuda()]
+    for o in out:
+        call(gq, fmt, planes, q, lse, lens, o, table, scale)
+    assert gq.get_device_status() == 0
+    check(out[0], w, q, keys, lse, table, lens, scale)
+    assert torch.equal(out[0].nan_to_num(-1), out[1].nan_to_num(-1))
+
+
+@pytest.mark.parametrize("qs", [1e-30, 30.0, 1e30])
+def test_long_window_of_any_size(gq, qs):
+    case = (2, 8, 2, 30, 128, 0, [400, 255])
+    for fmt in ("bf16", "fp8", "q4"):
+        planes, keys, q, table, w = make(fmt, *case, seed=10, qs=qs)
+        scale = 0.05 / qs if qs > 1 else 0.05
+        lse = lse_of(q, keys, table, case[6], scale)
+        out = call(gq, fmt, planes, q, lse, case[6], w.cuda(), table, scale)
+        check(out, w, q, keys, lse, table, case[6], scale)
+
+
+def test_long_window_reports(gq):
+    case = (3, 8, 2, 30, 64, 16, [320, 140, 333])
+    planes, keys, q, table, w = make("bf16", *case, seed=11)
+    lse = lse_of(q, keys, table, case[6], 0.125)
+    for bad in (-1, 1000):
+        out = call(gq, "bf16", planes, q, lse, [320, bad, 333], w.cuda(), table, 0.125)
+        assert gq.get_device_status() == 5
+        check(out, w, q, keys, lse, table, [320, 0, 333], 0.125)
+    t = table.clone()
+    t[1, 1] = -1
+    out = call(gq, "bf16", planes, q, lse, case[6], w.cuda(), t, 0.125)
+    assert gq.get_device_status() == 11
+    assert torch.equal(out[int(table[1, 1])].cpu().nan_to_num(-1), w[int(table[1, 1])].nan_to_num(-1))
+
+
 def stream_capacity(B, Hkv):
     """A capacity whose chunks of 256 positions are more than the CTAs that any GPU of this kind holds at once: few query
     rows then go by the stream of tiles whatever the lengths are."""
