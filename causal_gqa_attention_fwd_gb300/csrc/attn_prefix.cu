@@ -802,16 +802,14 @@ static cudaError_t launch_merge_d(const PrefixArgs& p, const OwnArgs& a, __nv_bf
   long n = 2 + kOwnMaxWarps / units;
   if (a.P > 0) n *= 2;
   else n += (1 + p.ctas / p.width / ((long)p.P * p.Hkv * p.outer)) * (p.Rp <= kPrefixRows / 2 ? 2 : 1);
-  auto go = [&](auto kernel, int wpr) {
-    const int w = wpr > 8 ? wpr : 8;
-    return launch_programmatic(kernel, dim3((unsigned)((rows * wpr + w - 1) / w)), dim3(32 * w), 0, stream, p, a, o, lse);
-  };
+  auto blocks = [&](int per_block) { return dim3((unsigned)((rows + per_block - 1) / per_block)); };
   // measured (us with the launch): 8192 rows of 7 pieces, 1 warp 9 where 4 take 18; 2048 rows of 21, 4 warps by fours 8,
   // by eights 12; 28 rows of 480, 16 warps 5, 8 warps 9
-  if (n > 160) return go(prefix_merge_kernel<D, 16, 8>, 16);
-  if (n > 40 || (n > 10 && rows <= 512)) return go(prefix_merge_kernel<D, 8, 8>, 8);
-  if (n > 10) return go(prefix_merge_kernel<D, 4, 4>, 4);
-  return go(prefix_merge_kernel<D, 1, 8>, 1);
+  if (n > 160) return launch_programmatic(prefix_merge_kernel<D, 16, 8>, blocks(1), dim3(512), 0, stream, p, a, o, lse);
+  if (n > 40 || (n > 10 && rows <= 512))
+    return launch_programmatic(prefix_merge_kernel<D, 8, 8>, blocks(1), dim3(256), 0, stream, p, a, o, lse);
+  if (n > 10) return launch_programmatic(prefix_merge_kernel<D, 4, 4>, blocks(2), dim3(256), 0, stream, p, a, o, lse);
+  return launch_programmatic(prefix_merge_kernel<D, 1, 8>, blocks(8), dim3(256), 0, stream, p, a, o, lse);
 }
 
 cudaError_t launch_prefix_merge(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {

@@ -734,39 +734,53 @@ __global__ void __launch_bounds__(WindowCfg<D>::kKeys, 2) cache_weights_window_k
   }
 }
 
+// Once a device.
 template <auto KERNEL>
-cudaError_t launch_weights(dim3 grid, int threads, int smem, const WeightsArgs& a, cudaStream_t stream) {
+cudaError_t allow_smem(int bytes) {
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev >= 64 || !attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr_set[dev] = true;
-  }
-  return launch_programmatic(KERNEL, grid, dim3(threads), (size_t)smem, stream, a);
+  if (dev < 64 && attr_set[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) attr_set[dev] = true;
+  return e;
+}
+
+template <int D, CacheFmt F, int NT>
+cudaError_t launch_narrow(const WeightsArgs& a, int sms, cudaStream_t stream) {
+  using C = NarrowCfg<D, F, NT>;
+  const cudaError_t e = allow_smem<cache_weights_kernel<D, F, NT>>(C::kSmemBytes);
+  return e != cudaSuccess ? e
+                          : launch_programmatic(cache_weights_kernel<D, F, NT>, dim3(sms), dim3(C::kThreads),
+                                                (size_t)C::kSmemBytes, stream, a);
 }
 
 template <int D, CacheFmt F>
 cudaError_t launch_weights_df(const WeightsArgs& a, int sms, cudaStream_t stream) {
-  using C1 = NarrowCfg<D, F, 1>;
-  using C2 = NarrowCfg<D, F, 2>;
   // The stream is for many keys: where a CTA a chunk of the capacity are resident together (two an SM, heads of 64 three),
   // they have no shares to work out.  us, CTAs / stream, 8 rows: bf16 keys of 128, 32768: 3.4 / 4.1, 65536: 4.3 / 5.4,
   // 98304: 7.0 / 6.5; keys of 64, 98304: 4.1 / 5.0, 131072: 5.9 / 5.6; E4M3 of 128, 65536: 4.1 / 5.5, 131072: 6.8 / 6.7;
   // 4-bit of 128, 65536: 3.8 / 6.0, 131072: 6.3 / 7.3, 262144: 11.2 / 9.4.
   const long ctas = (long)a.B * a.Hkv * ((a.S + (long)kWKeys - 1) / kWKeys);
   if (a.R <= 16 && ctas > (D == 128 ? 2L : 3L) * sms)
-    return a.R <= 8 ? launch_weights<cache_weights_kernel<D, F, 1>>(dim3(sms), C1::kThreads, C1::kSmemBytes, a, stream)
-                    : launch_weights<cache_weights_kernel<D, F, 2>>(dim3(sms), C2::kThreads, C2::kSmemBytes, a, stream);
+    return a.R <= 8 ? launch_narrow<D, F, 1>(a, sms, stream) : launch_narrow<D, F, 2>(a, sms, stream);
   const dim3 grid((unsigned)ctas);
   // Warp MMAs keep up with few rows only, but need no tiles in shared memory.  us, this / those: bf16 keys of 128, 131072
   // of them: 32 rows 9.0 / 9.9, 64: 9.1 / 13.8, 128: 12.6 / 22.9, 512: 34 / 75; 2^20, 512 rows: 221 / 490; keys of 64,
   // 2^20: 48 rows 50 / 45, 64: 50 / 51, 128: 69 / 82.  E4M3 of 128, 262144: 64 rows 21 / 21, 96: 31 / 29, 128: 31 / 34,
   // 512: 93 / 119; 4-bit: 96 rows 31 / 32, 512: 93 / 130.
-  if (a.R > (F != kCacheBf16 ? 96 : D == 128 ? 32 : 48))
-    return launch_weights<cache_weights_window_kernel<D, F>>(grid, WindowCfg<D>::kKeys, WindowCfg<D>::kSmemBytes, a, stream);
-  return launch_weights<cache_weights_wide_kernel<D, F>>(grid, 32 * kWWarps, kWWarps * KeyStage<D, F>::kBytes, a, stream);
+  if (a.R > (F != kCacheBf16 ? 96 : D == 128 ? 32 : 48)) {
+    using C = WindowCfg<D>;
+    const cudaError_t e = allow_smem<cache_weights_window_kernel<D, F>>(C::kSmemBytes);
+    return e != cudaSuccess ? e
+                            : launch_programmatic(cache_weights_window_kernel<D, F>, grid, dim3(C::kKeys),
+                                                  (size_t)C::kSmemBytes, stream, a);
+  }
+  constexpr int kSmem = kWWarps * KeyStage<D, F>::kBytes;
+  const cudaError_t e = allow_smem<cache_weights_wide_kernel<D, F>>(kSmem);
+  return e != cudaSuccess ? e
+                          : launch_programmatic(cache_weights_wide_kernel<D, F>, grid, dim3(32 * kWWarps), (size_t)kSmem,
+                                                stream, a);
 }
 
 template <CacheFmt F>
