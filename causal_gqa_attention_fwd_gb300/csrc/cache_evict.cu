@@ -42,6 +42,7 @@ namespace {
 constexpr int kWWarps = 8;
 constexpr int kWKeys = 32 * kWWarps;   // keys a CTA takes at once
 constexpr int kWRows = 64;             // query rows in shared memory at once
+constexpr int kScanRows = 128;
 
 __device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1, bool f16) {
   if (f16)
@@ -376,6 +377,52 @@ __global__ void __launch_bounds__(NarrowCfg<D, F, NT>::kThreads, 1) cache_weight
   if (bad) atomicCAS(a.status, 0, kDevBadPage);
 }
 
+// The chunk of kWKeys keys that this CTA takes: from key c0 on of head hkv of row b.
+struct Chunk {
+  int b, hkv, c0, len;
+};
+
+// All warps together.  a.scan: the chunks that hold keys, one CTA after another, found by a scan of the lengths in each
+// warp, so that none of the CTAs that start together is one that its row has no keys for.  For grids that do not fit at
+// once (5 rows of 301-7001 keys, 16 queries, 560 CTAs: 7.3 us, otherwise 8.9; where all have keys it costs 2-5%) and up to
+// kScanRows rows.  Otherwise a CTA has its place in the capacity.
+__device__ __forceinline__ bool find_chunk(const WeightsArgs& a, Chunk& c) {
+  const int lane = threadIdx.x & 31, at = (int)blockIdx.x;
+  if (!a.scan) {
+    const int bh = at % (a.B * a.Hkv);
+    c.b = bh / a.Hkv, c.hkv = bh % a.Hkv, c.c0 = at / (a.B * a.Hkv) * kWKeys;
+    c.len = a.cache_lens[c.b];
+    if (c.len >= 0 && c.len <= a.S) return c.c0 < c.len;
+    if (c.c0 == 0 && threadIdx.x == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+    return false;
+  }
+  int before = 0;
+  bool found = false;
+  for (int b0 = 0; b0 < a.B && (!found || at == 0); b0 += 32) {
+    int len = b0 + lane < a.B ? a.cache_lens[b0 + lane] : 0;
+    if (len < 0 || len > a.S) {
+      if (at == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
+      len = 0;
+    }
+    const int n = (len + kWKeys - 1) / kWKeys * a.Hkv;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned hit = __ballot_sync(~0u, before + incl > at);
+    if (hit && !found) {
+      const int l = __ffs(hit) - 1, k = at - before - __shfl_sync(~0u, incl - n, l);
+      found = true;
+      c.b = b0 + l, c.hkv = k % a.Hkv, c.c0 = k / a.Hkv * kWKeys;
+      c.len = __shfl_sync(~0u, len, l);
+    }
+    before += __shfl_sync(~0u, incl, 31);
+  }
+  return found;
+}
+
 // ------------------------------------------------ more query rows (a window of a prompt), or few keys: a CTA a chunk of keys
 // Each warp holds the fragments of 32 keys in registers and takes the query rows, kWRows at a time, from shared memory.
 template <int D, CacheFmt F>
@@ -391,14 +438,9 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
   griddep_wait();
   griddep_launch();
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  const int bh = (int)(blockIdx.x % (unsigned)(a.B * a.Hkv)), b = bh / a.Hkv, hkv = bh % a.Hkv;
-  const int c0 = (int)(blockIdx.x / (unsigned)(a.B * a.Hkv)) * kWKeys;
-  const int len = a.cache_lens[b];
-  if (len < 0 || len > a.S) {
-    if (c0 == 0 && threadIdx.x == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
-    return;
-  }
-  if (c0 >= len) return;
+  Chunk chunk;
+  if (!find_chunk(a, chunk)) return;
+  const int b = chunk.b, hkv = chunk.hkv, c0 = chunk.c0, len = chunk.len, bh = b * a.Hkv + hkv;
   if (threadIdx.x == 0) s_abort = 0;
   if (lane == 0) {
     mbar_init(&s_full[warp], 1);
@@ -490,7 +532,7 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
 // does for itself.  512 rows over 2^20 keys: bf16 of 128 221 us, of 64 174 (3.1e12 exponentials a second), E4M3 of 128 340.
 template <int D>
 struct WindowCfg {
-  static constexpr int kRows = 64, kKeys = 256;
+  static constexpr int kRows = 64, kKeys = kWKeys;
   static constexpr int kBoxes = D / 64;             // of 64 features, 128 bytes a row
   static constexpr int kKeyBox = 128 * 128, kRowBox = kRows * 128;
   static constexpr int kSmemBytes = kBoxes * (2 * kKeyBox + 2 * kRowBox) + 1024;
@@ -515,15 +557,10 @@ __global__ void __launch_bounds__(WindowCfg<D>::kKeys, 2) cache_weights_window_k
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31, x = warp >> 2;
-  const int bh = (int)(blockIdx.x % (unsigned)(a.B * a.Hkv)), b = bh / a.Hkv, hkv = bh % a.Hkv;
-  const int c0 = (int)(blockIdx.x / (unsigned)(a.B * a.Hkv)) * C::kKeys;
   griddep_wait();
-  const int len = a.cache_lens[b];
-  if (len < 0 || len > a.S) {
-    if (c0 == 0 && tid == 0) atomicCAS(a.status, 0, kDevBadSeqlens);
-    return;
-  }
-  if (c0 >= len) return;
+  Chunk chunk;
+  if (!find_chunk(a, chunk)) return;
+  const int b = chunk.b, hkv = chunk.hkv, c0 = chunk.c0, len = chunk.len, bh = b * a.Hkv + hkv;
   const uint32_t s_k = (smem_u32(smem_raw) + 1023) & ~1023u, s_q = s_k + 2 * C::kBoxes * C::kKeyBox;
   const uint32_t tile = s_k + x * C::kBoxes * C::kKeyBox;
   if (tid == 0) {
@@ -756,15 +793,17 @@ cudaError_t launch_narrow(const WeightsArgs& a, int sms, cudaStream_t stream) {
 }
 
 template <int D, CacheFmt F>
-cudaError_t launch_weights_df(const WeightsArgs& a, int sms, cudaStream_t stream) {
+cudaError_t launch_weights_df(WeightsArgs a, int sms, cudaStream_t stream) {
   // The stream is for many keys: where a CTA a chunk of the capacity are resident together (two an SM, heads of 64 three),
   // they have no shares to work out.  us, CTAs / stream, 8 rows: bf16 keys of 128, 32768: 3.4 / 4.1, 65536: 4.3 / 5.4,
   // 98304: 7.0 / 6.5; keys of 64, 98304: 4.1 / 5.0, 131072: 5.9 / 5.6; E4M3 of 128, 65536: 4.1 / 5.5, 131072: 6.8 / 6.7;
   // 4-bit of 128, 65536: 3.8 / 6.0, 131072: 6.3 / 7.3, 262144: 11.2 / 9.4.
   const long ctas = (long)a.B * a.Hkv * ((a.S + (long)kWKeys - 1) / kWKeys);
-  if (a.R <= 16 && ctas > (D == 128 ? 2L : 3L) * sms)
+  const bool at_once = ctas <= (D == 128 ? 2L : 3L) * sms;
+  if (a.R <= 16 && !at_once)
     return a.R <= 8 ? launch_narrow<D, F, 1>(a, sms, stream) : launch_narrow<D, F, 2>(a, sms, stream);
   const dim3 grid((unsigned)ctas);
+  a.scan = a.B <= kScanRows && !at_once;
   // Warp MMAs keep up with few rows only, but need no tiles in shared memory.  us, this / those: bf16 keys of 128, 131072
   // of them: 32 rows 9.0 / 9.9, 64: 9.1 / 13.8, 128: 12.6 / 22.9, 512: 34 / 75; 2^20, 512 rows: 221 / 490; keys of 64,
   // 2^20: 48 rows 50 / 45, 64: 50 / 51, 128: 69 / 82.  E4M3 of 128, 262144: 64 rows 21 / 21, 96: 31 / 29, 128: 31 / 34,

@@ -110,6 +110,7 @@ struct WeightsArgs {
   int B, Hkv, Tq, R, S, D, page_size, max_pages, num_pages;
   float scale_log2;          // softmax scale * k_scale * log2(e)
   FastDiv page;              // page_size (set by the launch)
+  int scan;                  // CTAs look for their keys by the lengths (set by the launch)
   int* status;
 };
 cudaError_t launch_cache_weights(WeightsArgs a, CacheFmt fmt, int sms, cudaStream_t stream);

@@ -147,6 +147,29 @@ def test_long_windows(gq, case, fmt):
     assert torch.equal(out[0].nan_to_num(-1), out[1].nan_to_num(-1))
 
 
+@pytest.mark.parametrize("B,Tq", [(3, 5), (3, 33), (40, 5), (70, 9), (130, 5)])
+def test_ragged_rows_of_a_large_capacity(gq, B, Tq):
+    """More chunks of the capacity than CTAs at once: CTAs find their keys by the lengths (up to 128 rows), also behind
+    rows without keys, or by their place."""
+    S = stream_capacity(B, 2)
+    g = torch.Generator().manual_seed(B + Tq)
+    lens = torch.randint(0, min(S, 600), (B,), generator=g).tolist()
+    lens[0] = 0
+    lens[B // 2] = min(S, 700)
+    case = (B, 8, 2, Tq, 64, 64, lens)
+    planes, keys, q, table, w = make("bf16", *case, seed=12, S=S)
+    lse = lse_of(q, keys, table, lens, 0.125)
+    out = call(gq, "bf16", planes, q, lse, lens, w.cuda(), table, 0.125)
+    assert gq.get_device_status() == 0
+    check(out, w, q, keys, lse, table, lens, 0.125)
+    bad = list(lens)
+    bad[B - 1] = -5
+    out = call(gq, "bf16", planes, q, lse, bad, w.cuda(), table, 0.125)
+    assert gq.get_device_status() == 5
+    bad[B - 1] = 0
+    check(out, w, q, keys, lse, table, bad, 0.125)
+
+
 @pytest.mark.parametrize("qs", [1e-30, 30.0, 1e30])
 def test_long_window_of_any_size(gq, qs):
     case = (2, 8, 2, 30, 128, 0, [400, 255])
