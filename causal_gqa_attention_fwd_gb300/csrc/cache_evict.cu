@@ -941,9 +941,11 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const Slots& slot_
   // the first row that moves: list[d] - d never falls
   int d_lo = a.first, d_hi = a.budget;
   while (d_lo < d_hi) {
-    const int mid = (d_lo + d_hi) >> 1;
-    if (list[mid] > mid) d_hi = mid;
-    else d_lo = mid + 1;
+    const int step = (d_hi - d_lo + 31) / 32, d = d_lo + lane * step;
+    const unsigned in = __ballot_sync(~0u, d < d_hi), moves = __ballot_sync(~0u, d < d_hi && list[d] > d);
+    const int i = moves ? __ffs(moves) - 1 : __popc(in);     // the first of the lanes whose row moves
+    if (moves) d_hi = d_lo + i * step;
+    d_lo = i ? d_lo + (i - 1) * step + 1 : d_hi;
   }
   for (int c0 = d_lo; c0 < a.budget;) {
     const int free_to = min(list[c0], a.budget);
