@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kBM = 128;                   // query rows per tile
 constexpr int kBN = 128;                   // keys per block
+constexpr int kCh = 64;                    // scores of a row in registers at once
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: lazy O rescale
 
 template <int D>
@@ -71,6 +72,19 @@ __device__ __forceinline__ int prefix_blocks(const PrefixArgs& a, int p) {
   return m > 0 && m <= a.Sp ? (m + kBN - 1) / kBN : 0;
 }
 
+// Scores kCh q .. of a row, -infinity from column nvis on.
+__device__ __forceinline__ void load_scores(uint32_t tS, int q, int nvis, uint32_t* s) {
+#pragma unroll
+  for (int k = 0; k < kCh / 32; ++k) tmem_ld_x32(tS + q * kCh + k * 32, s + k * 32);
+  tmem_ld_wait();
+  reg_fence<kCh>(s);
+  if (nvis < kBN) {
+#pragma unroll
+    for (int k = 0; k < kCh; ++k)
+      if (q * kCh + k >= nvis) s[k] = 0xff800000u;
+  }
+}
+
 // A piece: blocks [kb, kb + n) of unit (p, hkv, mt).
 struct Piece {
   int p, hkv, mt;
@@ -78,7 +92,6 @@ struct Piece {
   int len;             // keys of the prefix
   int rows;            // query rows of the unit
   int split;           // the two tiles take the blocks in turn
-  int slot, npieces;   // in pieces
 };
 
 // Where a CTA's walk over its share stands.  Every role walks it.
@@ -103,9 +116,6 @@ __device__ __forceinline__ void walk_piece(const PrefixArgs& a, Walk& w) {
   it.len = a.prefix_lens[w.p];
   it.rows = min(kPrefixRows, a.Rp - it.mt * kPrefixRows);
   it.split = it.rows <= kBM;
-  const int Pg = w.Pb + group * w.nb, first = w.split.owner(Pg);
-  it.slot = w.team - first;
-  it.npieces = w.split.owner(Pg + w.nb - 1) - first + 1;
   w.valid = true;
 }
 
@@ -459,6 +469,7 @@ __global__ void __launch_bounds__(384, 1)
       const int row0 = it.mt * kPrefixRows + (it.split ? 0 : x * kBM);   // first row of the tile within the unit's head
       const int rows = min(kBM, it.rows - (it.split ? 0 : x * kBM));
       const int nx = it.split ? (it.n + 1 - x) / 2 : it.n;               // blocks of this tile
+      int piece, pieces;
       // ------------------------------------------------ the tile's query rows
       // (shared memory is free: the previous piece's MMAs were done before its output was read)
       {
@@ -473,12 +484,16 @@ __global__ void __launch_bounds__(384, 1)
           const bool real = wrow + i * kPer + lane / kC < rows;
           const long qr = ((long)b * a.Hkv + it.hkv) * a.R + in;
           v[i] = real ? __ldg(reinterpret_cast<const uint4*>(a.q + qr * D + part * 8)) : make_uint4(0, 0, 0, 0);
-          v[i].x ^= sign, v[i].y ^= sign, v[i].z ^= sign, v[i].w ^= sign;
           for (in += kPer; in >= a.R; in -= a.R) ++b;
         }
+        // while they are on their way: which of the unit's pieces this is
+        const int Pg = w.g - it.kb, first = w.split.owner(Pg);
+        piece = w.team - first;
+        pieces = w.split.owner(Pg + w.nb - 1) - first + 1;
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
           const int rr = wrow + i * kPer + lane / kC;
+          v[i].x ^= sign, v[i].y ^= sign, v[i].z ^= sign, v[i].w ^= sign;
           *reinterpret_cast<uint4*>(sQ + x * C::kTileBytes + (part >> 3) * C::kBoxBytes + rr * 128 +
                                     (((part & 7) ^ (rr & 7)) << 4)) = v[i];
         }
@@ -514,25 +529,21 @@ __global__ void __launch_bounds__(384, 1)
           mbar_arrive_warp(&bars.p_full[x]);
           continue;
         }
-        uint32_t s[kBN];
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < kBN / kCh; ++q) {
+          uint32_t s[kCh];
+          load_scores(tS, q, nvis, s);
+          const float* sf = reinterpret_cast<const float*>(s);
+          float m8[8];
 #pragma unroll
-        for (int q = 0; q < kBN / 32; ++q) tmem_ld_x32(tS + q * 32, s + q * 32);
-        tmem_ld_wait();
-        reg_fence<kBN>(s);
-        float* sf = reinterpret_cast<float*>(s);
-        if (nvis < kBN) {
+          for (int e = 0; e < 8; ++e) m8[e] = fmaxf(sf[e], sf[e + 8]);
 #pragma unroll
-          for (int k = 0; k < kBN; ++k)
-            if (k >= nvis) sf[k] = -INFINITY;
+          for (int k = 16; k < kCh; k += 16)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m8[e] = max3f(m8[e], sf[k + e], sf[k + 8 + e]);
+          mx = max3f(mx, max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), m8[6]), m8[7]);
         }
-        float m8[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m8[e] = fmaxf(sf[e], sf[e + 8]);
-#pragma unroll
-        for (int k = 16; k < kBN; k += 16)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m8[e] = max3f(m8[e], sf[k + e], sf[k + 8 + e]);
-        const float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
         const float mn = mx * c;
         float alpha = 1.f;
         bool resc = false;
@@ -559,19 +570,25 @@ __global__ void __launch_bounds__(384, 1)
         }
         const uint64_t c2 = f2(c, c), nm2 = f2(-m_use, -m_use);
         uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll 1
+        for (int h = 0; h < kBN / kCh; ++h) {
+          uint32_t s[kCh];
+          load_scores(tS, h, nvis, s);
+          const float* sf = reinterpret_cast<const float*>(s);
 #pragma unroll
-        for (int q = 0; q < kBN / 32; ++q) {
-          uint32_t pk[16];
+          for (int q = 0; q < kCh / 32; ++q) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float t0, t1;
-            f2_split(fma2(f2(sf[q * 32 + 2 * k], sf[q * 32 + 2 * k + 1]), c2, nm2), t0, t1);
-            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-            acc[k & 3] = add2(acc[k & 3], f2(p0, p1));
-            pk[k] = pack_bf16x2(p0, p1);   // rounded to bf16 (2^-8 of each weight): the type of V, for the MMA
+            for (int k = 0; k < 16; ++k) {
+              float t0, t1;
+              f2_split(fma2(f2(sf[q * 32 + 2 * k], sf[q * 32 + 2 * k + 1]), c2, nm2), t0, t1);
+              const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+              acc[k & 3] = add2(acc[k & 3], f2(p0, p1));
+              pk[k] = pack_bf16x2(p0, p1);   // rounded to bf16 (2^-8 of each weight): the type of V, for the MMA
+            }
+            tmem_st_x16(tS + h * (kCh / 2) + q * 16, pk);
           }
-          tmem_st_x16(tS + q * 16, pk);
-          if (q == kBN / 64 - 1) {
+          if (h == kBN / kCh / 2 - 1) {
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive_warp(&bars.p_half[x]);
@@ -591,7 +608,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) break;
       ++od;
       tc_fence_after();
-      const int slot = it.split ? 2 * it.slot + x : it.slot;
+      const int slot = it.split ? 2 * piece + x : piece;
       const long wr = (((long)it.p * a.Hkv + it.hkv) * a.Rp + row0 + r) * a.slots + slot;
       const bool mine = r < rows && GQA_CHECK(slot >= 0 && slot < a.slots && row0 + r < a.Rp, a.status, a.dbg_line);
       if (nx > 0 && live) {
@@ -621,8 +638,8 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_before();   // O is read before the next piece's P V (after its q_full) writes it
       }
       if (mine) a.ws_ml[wr] = make_float2(m_run, l_run);
-      if (it.slot == 0 && x == 0 && r == 0)
-        a.counts[((long)it.p * a.Hkv + it.hkv) * a.nrt + it.mt] = it.split ? 2 * it.npieces : it.npieces;
+      if (piece == 0 && x == 0 && r == 0)
+        a.counts[((long)it.p * a.Hkv + it.hkv) * a.nrt + it.mt] = it.split ? 2 * pieces : pieces;
     }
   }
 
