@@ -29,8 +29,8 @@
 //   Bound: many rows, the MMAs (a pair of tiles' two products take 1.1 us a
 //   block of 128 keys at the rate of a large library product, 1.35 here);
 //   few rows, the stream of keys and values.  64 rows over 8192 keys and ~32000
-//   own ones 43 us (25 at the copy rate), 256 rows over 32768 keys and ~70000
-//   own ones 131 us (74).
+//   own ones 41 us (25 at the copy rate), 256 rows over 32768 keys and ~70000
+//   own ones 130 us (74).
 #include "own_keys.cuh"
 
 namespace gqa {
@@ -173,14 +173,13 @@ __device__ Walk walk_begin(const PrefixArgs& a, int cta, int ctas, int total) {
 // How many of the grid's G CTAs take the rows' own keys, the others the prefixes: so that both end at the same time, by
 // what they were measured to take (ns).
 //   Two tiles of query rows a CTA: the MMAs bound a prefix, kPair a block of 128 keys.  Beside it an SM streams own keys
-//   at kOwnTile a tile of 8 KB, all SMs together at kOwnTileAll; a prefix starts slowly beside a stream that fills the
-//   memory's queues.
+//   at kOwnTile a tile of 8 KB, all SMs together at kOwnTileAll.
 //   One tile of rows, held by both: the memory bounds both parts, and an SM gets its share of it: kByte a byte.
-// 64 rows over 8192 keys and 32768 own ones, CTAs of own keys 64 / 72 / 80 / 88 / 96: 43.5, 42.6, 42.5, 43.4, 45.8 us;
-// 256 rows over 32768, 32 / 34 / 36 / 40: 141, 134, 131, 133.
+// 64 rows over 8192 keys and 32768 own ones, CTAs of own keys 64 / 72 / 80 / 88 / 96: 43.4, 42.5, 42.0, 41.6, 44.5 us;
+// 256 rows over 32768, 32 / 34 / 36 / 38: 132.3, 130.0, 129.9, 132.4.
 constexpr float kOwnStart = 6000.f, kOwnTile = 94.f, kOwnTileAll = 1.25f;
 constexpr float kOwnUnit = 2000.f;    // a unit, of one of a CTA's warps: its queries and its output
-constexpr float kPreStart = 18000.f, kPair = 1350.f, kByte = 1.f / 41.f;
+constexpr float kPreStart = 10000.f, kPair = 1350.f, kByte = 1.f / 41.f;
 constexpr float kPiece = 5000.f;      // a second piece: its queries, the first one's drain and partial
 
 struct Parts {
@@ -814,18 +813,27 @@ cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const
 template <int D>
 static cudaError_t launch_merge_d(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
   const long rows = (long)a.B * a.Hkv * p.R;
-  // about as many pieces as a row has, if all its keys are there: the prefix's by its CTAs or warps, its own by warps
-  const long units = (long)a.B * a.Hkv * a.nrb + (long)a.P * a.Hkv * a.nrbp;
-  long n = 2 + kOwnMaxWarps / units;
-  if (a.P > 0) n *= 2;
-  else n += (1 + p.ctas / p.width / ((long)p.P * p.Hkv * p.outer)) * (p.Rp <= kPrefixRows / 2 ? 2 : 1);
+  // about as many pieces as a row has, if all its keys are there
+  constexpr int KT = OwnCfg<D, 1>::KT;
+  auto tiles = [](int keys) { return (keys + KT - 1) / KT + kUnitCost; };
+  const long total = (long)a.B * a.Hkv * a.nrb * tiles(a.S) + (long)a.P * a.Hkv * a.nrbp * tiles(a.Sp);
+  const long share = total / kOwnMaxWarps > kMinShare ? total / kOwnMaxWarps : kMinShare;
+  long n = tiles(a.S) / share;
+  if (a.P > 0) {
+    n += tiles(a.Sp) / share;
+  } else {
+    const long per = 1 + p.ctas / p.width / ((long)p.P * p.Hkv * p.outer), most = (p.Sp + kBN - 1) / kBN;
+    n += (per < most ? per : most) * (p.Rp <= kPrefixRows / 2 ? 2 : 1);
+  }
   auto blocks = [&](int per_block) { return dim3((unsigned)((rows + per_block - 1) / per_block)); };
-  // measured (us with the launch): 8192 rows of 7 pieces, 1 warp 9 where 4 take 18; 2048 rows of 21, 4 warps by fours 8,
-  // by eights 12; 28 rows of 480, 16 warps 5, 8 warps 9
-  if (n > 160) return launch_programmatic(prefix_merge_kernel<D, 16, 8>, blocks(1), dim3(512), 0, stream, p, a, o, lse);
-  if (n > 40 || (n > 10 && rows <= 512))
+  // Warps a row, as many as leave the blocks in about a wave.  Whole calls, us, 16 / 8 / 4 / 1 warps: 32 rows of 70 pieces
+  // 8.0 / 8.9 / 9.0 / 18.6, 128 rows 9.6 / 10.4 / 10.4 / 21.3, 112 rows of 40 (heads of 64) 10.1 / 9.3 / 9.2 / 13.6,
+  // 256 rows 13.8 / 11.9 / 11.9 / 23.0, 512 rows 21.0 / 15.9 / 15.9 / 19.3, 1024 rows of 20 31 / 23 / 17.1 / 18.8, 896 rows
+  // of 40 (heads of 64) 22.9 / 17.6 / 20.7 / 19.0 and 1024 of 23 - / 19.4 / 15.7 / -, 2048 rows 49 / 31 / 18.9 / 18.1, 8192 rows of 7 245 / 195 / 142 / 132.
+  if (rows <= 128 && n > 64) return launch_programmatic(prefix_merge_kernel<D, 16, 8>, blocks(1), dim3(512), 0, stream, p, a, o, lse);
+  if (rows <= 512 || (D == 64 && rows <= 1024 && n > 40))
     return launch_programmatic(prefix_merge_kernel<D, 8, 8>, blocks(1), dim3(256), 0, stream, p, a, o, lse);
-  if (n > 10) return launch_programmatic(prefix_merge_kernel<D, 4, 4>, blocks(2), dim3(256), 0, stream, p, a, o, lse);
+  if (rows <= 1536) return launch_programmatic(prefix_merge_kernel<D, 4, 4>, blocks(2), dim3(256), 0, stream, p, a, o, lse);
   return launch_programmatic(prefix_merge_kernel<D, 1, 8>, blocks(8), dim3(256), 0, stream, p, a, o, lse);
 }
 

@@ -178,11 +178,12 @@ struct OwnMaps {
 };
 // Whether prefixes of Sp keys, Rp query rows each, go into the stream: it reads them again for every 16 rows, from L2,
 // where attn_prefix needs some microseconds for its pipeline of large tiles.  Measured (us, stream / attn_prefix; 8 heads
-// of 128): 2048 keys, 32 rows 12 / 16, 128 rows 18 / 20; 8192 keys, 16 rows 15 / 17, 48 rows 23 / 18; 8 prefixes of 2048,
-// 32 rows 28 / 32, 48 rows 36 / 30; heads of 64, 2 of them, 32768 keys, 56 rows 18 / 17: about 48 MB read again is where
-// they meet.
+// of 128): 2048 keys, 96 rows 16.4 / 15.9, 128 rows 17.6 / 16.9; 8192 keys, 16 rows 13.7 / 13.7, 32 rows 17.7 / 14.9, 48
+// rows 22.0 / 17.4; 3001 keys, 4 heads, 80 rows 15.0 / 16.4; 8 prefixes of 2048, 24 rows 28.5 / 27.8, 48 rows 37.5 / 29.5;
+// 8 heads of 64, 32 rows 20.7 / 22.0, 48 rows 25.9 / 25.1; 2 heads, 32768 keys, 56 rows 18.3 / 17.1: about 24 MB read again
+// is where they meet.
 inline bool prefix_in_stream(int Rp, int P, int Hkv, int Sp, int D) {
-  return ((long)(Rp + 15) / 16 - 1) * P * Hkv * Sp * D * 4 <= 48L << 20;
+  return ((long)(Rp + 15) / 16 - 1) * P * Hkv * Sp * D * 4 <= 24L << 20;
 }
 inline int own_box_rows(int D, int page_size) {   // page_size 0: contiguous
   const int tile = D == 128 ? 16 : 32;
