@@ -181,9 +181,13 @@ struct OwnMaps {
 // of 128): 2048 keys, 96 rows 16.4 / 15.9, 128 rows 17.6 / 16.9; 8192 keys, 16 rows 13.7 / 13.7, 32 rows 17.7 / 14.9, 48
 // rows 22.0 / 17.4; 3001 keys, 4 heads, 80 rows 15.0 / 16.4; 8 prefixes of 2048, 24 rows 28.5 / 27.8, 48 rows 37.5 / 29.5;
 // 8 heads of 64, 32 rows 20.7 / 22.0, 48 rows 25.9 / 25.1; 2 heads, 32768 keys, 56 rows 18.3 / 17.1: about 24 MB read again
-// is where they meet.
+// is where they meet; about 96 MB where the units are nearly as many as the CTAs or more, each of which then pays for one
+// unit's queries and partials after the other (5 prefixes, 8 heads of 64, 520 rows, 120 units: 128 keys, 41 MB, 34 / 45,
+// 384, 124 MB, 42 / 44, 768 56 / 48; 16 prefixes, 8 heads of 128, 32 rows, 128 units: 384 keys, 48 MB, 22.4 / 23.6, 1536,
+// 192 MB, 38 / 37; 32 units, 256 rows, 384 keys, 96 MB: 35 / 30).
 inline bool prefix_in_stream(int Rp, int P, int Hkv, int Sp, int D) {
-  return ((long)(Rp + 15) / 16 - 1) * P * Hkv * Sp * D * 4 <= 24L << 20;
+  const long again = ((long)(Rp + 15) / 16 - 1) * P * Hkv * Sp * D * 4;
+  return again <= ((long)P * Hkv * ((Rp + kPrefixRows - 1) / kPrefixRows) < 96 ? 24L << 20 : 96L << 20);
 }
 inline int own_box_rows(int D, int page_size) {   // page_size 0: contiguous
   const int tile = D == 128 ? 16 : 32;

@@ -79,7 +79,7 @@ def test_workspace_covers_every_cut(lib):
         nrt = -(-Rp // 256)
         width = max(w for w in range(1, min(nrt, 38) + 1) if nrt % w == 0 and 152 // w * w * 100 >= 94 * 152)
         outer = nrt // width
-        if (-(-Rp // 16) - 1) * P * Hkv * Sp * 64 * 4 <= 24 << 20:
+        if (-(-Rp // 16) - 1) * P * Hkv * Sp * 64 * 4 <= (24 if P * Hkv * -(-Rp // 256) < 96 else 96) << 20:
             continue                # few rows: the prefix's pieces are the stream's, which needs no slots
         size = lib.attn_decode_prefix_workspace_size(B, Hkv * G, Hkv, Tq, P, Sp, 128, 64)
         R, block = G * Tq, 8 if G * Tq <= 8 else 16

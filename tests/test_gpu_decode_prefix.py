@@ -92,7 +92,7 @@ def tile_capacity(B, P, Hq, Hkv, Tq, D):
     """The least prefix capacity (in steps of 1024) that sends prefixes of more than 16 query rows to the kernel of large
     tiles: it counts what the stream would read again, not how long the prefixes are."""
     again = -(-(B // P * Hq // Hkv * Tq) // 16) - 1
-    return ((49 << 20) // (again * P * Hkv * D * 4) // 1024 + 1) * 1024 if again else None
+    return ((97 << 20) // (again * P * Hkv * D * 4) // 1024 + 1) * 1024 if again else None
 
 
 def ran(gq, f):
