@@ -11,12 +11,11 @@
 // a prefix attn_own.cu takes both parts as one stream instead.)
 //
 // attn_prefix  Which CTAs take the own keys is settled on the device, by the
-//   lengths (share_out).  To a prefix: the W * G * Tq query rows that meet a
-//   (prefix, K/V head) are a
-//   matrix, and both products are GEMM-shaped: tiles of 128 query rows as M,
-//   128 keys as N of the score MMA, on tcgen05 with the accumulators in TMEM
-//   (S_A, S_B, O_A, O_B; P in bf16 over its S), as the prefill kernel has
-//   them.  One CTA holds two tiles.  A unit of more than 128 rows fills both
+//   lengths (share_out).  The W * G * Tq query rows that meet a (prefix, K/V
+//   head) are a matrix, and both products are GEMM-shaped: tiles of 128 query
+//   rows as M, 128 keys as N of the score MMA, on tcgen05 with the accumulators
+//   in TMEM (S_A, S_B, O_A, O_B; P in bf16 over its S), as the prefill kernel
+//   has them.  One CTA holds two tiles.  A unit of more than 128 rows fills both
 //   and each reads every key block; one of at most 128 rows is held by both
 //   tiles, which then take the key blocks in turn, so that one's exponentials
 //   run beside the other's MMAs (two partials a piece).
@@ -26,9 +25,11 @@
 //   where a page is shorter than a block), warp 1 MMA issuer, warps 4-7 and
 //   8-11 softmax of a tile each, thread = row; they also gather the query rows
 //   (a tile's rows lie in runs of G * Tq in memory) and write the partials.
-//   Bound: many rows, the MMAs (a pair of tiles' two products take 1.1 us a
-//   block of 128 keys at the rate of a large library product, 1.35 here);
-//   few rows, the stream of keys and values.  64 rows over 8192 keys and ~32000
+//   Bound: many rows, the MMAs (a pair of tiles' two products are 1.35 us a
+//   block of 128 keys at the rate of a large library product); few rows, the
+//   stream of keys and values.  A CTA's start takes some 10 us beside the own
+//   keys' loads, much of it code that it meets for the first time: the softmax
+//   takes 64 scores at a time rather than 128 for that.  64 rows over 8192 keys and ~32000
 //   own ones 41 us (25 at the copy rate), 256 rows over 32768 keys and ~70000
 //   own ones 130 us (74).
 #include "own_keys.cuh"
@@ -829,8 +830,10 @@ static cudaError_t launch_merge_d(const PrefixArgs& p, const OwnArgs& a, __nv_bf
   // Warps a row, as many as leave the blocks in about a wave.  Whole calls, us, 16 / 8 / 4 / 1 warps: 32 rows of 70 pieces
   // 8.0 / 8.9 / 9.0 / 18.6, 128 rows 9.6 / 10.4 / 10.4 / 21.3, 112 rows of 40 (heads of 64) 10.1 / 9.3 / 9.2 / 13.6,
   // 256 rows 13.8 / 11.9 / 11.9 / 23.0, 512 rows 21.0 / 15.9 / 15.9 / 19.3, 1024 rows of 20 31 / 23 / 17.1 / 18.8, 896 rows
-  // of 40 (heads of 64) 22.9 / 17.6 / 20.7 / 19.0 and 1024 of 23 - / 19.4 / 15.7 / -, 2048 rows 49 / 31 / 18.9 / 18.1, 8192 rows of 7 245 / 195 / 142 / 132.
-  if (rows <= 128 && n > 64) return launch_programmatic(prefix_merge_kernel<D, 16, 8>, blocks(1), dim3(512), 0, stream, p, a, o, lse);
+  // of 40 (heads of 64) 22.9 / 17.6 / 20.7 / 19.0 and 1024 of 23 - / 19.4 / 15.7 / -, 2048 rows 49 / 31 / 18.9
+  // / 18.1, 8192 rows of 7 245 / 195 / 142 / 132.
+  if (rows <= 128 && n > 64)
+    return launch_programmatic(prefix_merge_kernel<D, 16, 8>, blocks(1), dim3(512), 0, stream, p, a, o, lse);
   if (rows <= 512 || (D == 64 && rows <= 1024 && n > 40))
     return launch_programmatic(prefix_merge_kernel<D, 8, 8>, blocks(1), dim3(256), 0, stream, p, a, o, lse);
   if (rows <= 1536) return launch_programmatic(prefix_merge_kernel<D, 4, 4>, blocks(2), dim3(256), 0, stream, p, a, o, lse);

@@ -517,13 +517,15 @@ PyObject* weights(PyObject* const* a, Py_ssize_t n) {
   const int dev = device_of(q, "q");
   if (q.dim() != 4) value_error("q must be [B, Hq, Tq, D]");
   const bool q4 = PyTuple_GET_SIZE(a[1]) == 2, bf16 = a[2] == Py_None;
-  const char *kn = bf16 ? "k_cache" : q4 ? "k4" : "k8", *name = bf16 ? "attn_cache_weights" : q4 ? "attn_cache_weights_q4" : "attn_cache_weights_fp8";
+  const char* kn = bf16 ? "k_cache" : q4 ? "k4" : "k8";
+  const char* name = bf16 ? "attn_cache_weights" : q4 ? "attn_cache_weights_q4" : "attn_cache_weights_fp8";
   const at::Tensor& k = tensor(PyTuple_GET_ITEM(a[1], 0), kn);
   const int B = dim(q, 0, "q"), Hq = dim(q, 1, "q"), Tq = dim(q, 2, "q"), D = dim(q, 3, "q");
   const int64_t wide = q4 ? D / 2 : D;
   if (k.dim() != 4 || k.size(3) != wide)
     value_error(std::string(kn) + " must be [pages, Hkv, page_size, " + std::to_string(wide) + "] matching q");
-  if (!bt.defined() && k.size(0) != B) value_error(std::string(kn) + " must hold a row for each of q's (or come with a block_table)");
+  if (!bt.defined() && k.size(0) != B)
+    value_error(std::string(kn) + " must hold a row for each of q's (or come with a block_table)");
   const void *kp = address(k, kn, bf16 ? at::kBFloat16 : at::kByte, dev), *sf = nullptr;
   if (q4) {
     const at::Tensor& x = tensor(PyTuple_GET_ITEM(a[1], 1), "k4_sf");
@@ -550,9 +552,13 @@ PyObject* weights(PyObject* const* a, Py_ssize_t n) {
   if (bf16)
     check(g_fn.weights(qp, kp, lp, blocks.p, ln, wp, B, Hq, H, Tq, page_size, pages, blocks.max_pages, D, scale, st), name);
   else if (q4)
-    check(g_fn.weights_q4(qp, kp, sf, ks, lp, blocks.p, ln, wp, B, Hq, H, Tq, page_size, pages, blocks.max_pages, D, scale, st), name);
+    check(g_fn.weights_q4(qp, kp, sf, ks, lp, blocks.p, ln, wp, B, Hq, H, Tq, page_size, pages, blocks.max_pages, D, scale,
+                          st),
+          name);
   else
-    check(g_fn.weights_fp8(qp, kp, ks, lp, blocks.p, ln, wp, B, Hq, H, Tq, page_size, pages, blocks.max_pages, D, scale, st), name);
+    check(g_fn.weights_fp8(qp, kp, ks, lp, blocks.p, ln, wp, B, Hq, H, Tq, page_size, pages, blocks.max_pages, D, scale,
+                           st),
+          name);
   Py_INCREF(a[5]);
   return a[5];
 }
@@ -565,7 +571,8 @@ PyObject* evict(PyObject* const* a, Py_ssize_t n) {
   const int dev = device_of(w, "weights");
   if (w.dim() != 3) value_error("weights must be [pages, Hkv, page_size]");
   if (lens.dim() != 1) value_error("cache_lens must be [B]");
-  const int B = dim(lens, 0, "cache_lens"), pages = dim(w, 0, "weights"), H = dim(w, 1, "weights"), page_size = dim(w, 2, "weights");
+  const int B = dim(lens, 0, "cache_lens"), pages = dim(w, 0, "weights"), H = dim(w, 1, "weights");
+  const int page_size = dim(w, 2, "weights");
   if (!bt.defined() && pages != B) value_error("weights must hold a row for each length (or come with a block_table)");
   const int budget = int_arg(a[3], "budget"), recent = int_arg(a[4], "recent"), first = int_arg(a[5], "first");
   if (budget < 1) value_error("budget must be at least 1");
@@ -576,7 +583,8 @@ PyObject* evict(PyObject* const* a, Py_ssize_t n) {
   for (Py_ssize_t i = 0; i < np; ++i) {
     const std::string name = "caches[" + std::to_string(i) + "]";
     const at::Tensor& x = tensor(PyTuple_GET_ITEM(a[1], i), name.c_str());
-    if (x.dim() != 4 || x.sizes().slice(0, 3) != w.sizes()) value_error(name + " must be [pages, Hkv, page_size, width] as weights");
+    if (x.dim() != 4 || x.sizes().slice(0, 3) != w.sizes())
+      value_error(name + " must be [pages, Hkv, page_size, width] as weights");
     planes[i] = address(x, name.c_str(), x.scalar_type(), dev);
     rows[i] = to_int(x.size(3) * (int64_t)x.element_size(), name.c_str());
   }
@@ -609,9 +617,12 @@ PyObject* prefix(PyObject* const* a, Py_ssize_t n) {
   if (q.dim() != 4) value_error("q must be [B, Hq, Tq, D]");
   if (pl.dim() != 1) value_error("prefix_lens must be [P]");
   const int B = dim(q, 0, "q"), Hq = dim(q, 1, "q"), Tq = dim(q, 2, "q"), D = dim(q, 3, "q"), P = dim(pl, 0, "prefix_lens");
-  if (P < 1 || B % P) value_error("the rows must be a multiple of the prefixes: " + std::to_string(B) + " rows, " + std::to_string(P) + " prefixes");
+  if (P < 1 || B % P)
+    value_error("the rows must be a multiple of the prefixes: " + std::to_string(B) + " rows, " + std::to_string(P) +
+                " prefixes");
   if (k.dim() != 4 || k.size(3) != D || v.sizes() != k.sizes() || (!paged && k.size(0) != B))
-    value_error(std::string(kn) + ", " + vn + (paged ? " must be [num_pages, Hkv, page_size, D] matching q" : " must be [B, Hkv, S, D] matching q"));
+    value_error(std::string(kn) + ", " + vn +
+                (paged ? " must be [num_pages, Hkv, page_size, D] matching q" : " must be [B, Hkv, S, D] matching q"));
   const int N = dim(k, 0, kn), H = dim(k, 1, kn), per = dim(k, 2, kn);
   int Sp, S = per;
   Blocks pt, bt;

@@ -623,7 +623,8 @@ __global__ void __launch_bounds__(WindowCfg<D>::kKeys, 2) cache_weights_window_k
   };
   // warp 0: both tiles' scores of the block in buffer `buf`
   auto issue = [&](int buf) {
-    constexpr uint32_t kIdesc = F == kCacheBf16 ? idesc_bf16(128, C::kRows, false, false) : idesc_f16(128, C::kRows, false, false);
+    constexpr uint32_t kIdesc =
+        F == kCacheBf16 ? idesc_bf16(128, C::kRows, false, false) : idesc_f16(128, C::kRows, false, false);
     tc_fence_after();
     const uint64_t kd = sdesc_sw128(s_k, 16, 1024), qd = sdesc_sw128(s_q + buf * C::kBoxes * C::kRowBox, 16, 1024);
     if (elect_one()) {
@@ -741,7 +742,8 @@ __global__ void __launch_bounds__(WindowCfg<D>::kKeys, 2) cache_weights_window_k
               c[0] = c[1] = c[2] = c[3] = a.scale_log2;
               l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
             } else {
-              const float4 v = *reinterpret_cast<const float4*>(cs + 2 * (n0 + k)), w = *reinterpret_cast<const float4*>(cs + 2 * (n0 + k) + 4);
+              const float4 v = *reinterpret_cast<const float4*>(cs + 2 * (n0 + k));
+              const float4 w = *reinterpret_cast<const float4*>(cs + 2 * (n0 + k) + 4);
               c[0] = v.x, c[1] = v.z, c[2] = w.x, c[3] = w.z;
               l[0] = v.y, l[1] = v.w, l[2] = w.y, l[3] = w.w;
             }
