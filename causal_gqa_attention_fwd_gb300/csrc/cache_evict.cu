@@ -852,6 +852,9 @@ constexpr int kKeyBytes = 80 << 10;  // weights a CTA keeps in shared memory; a 
 // Positions up to which each CTA of a cluster selects by itself, without the cluster's barriers (us, alone / together,
 // 16 units: 2048 positions 11.8 / 12.7, 4096: 20.6 / 18.0, 8192: 29.8 / 25.0).
 constexpr int kAlone = 2048;
+// The most that a launch asks for: a share of the weights, or places and (CTAs that select alone) a list behind them.
+constexpr int kEvMaxSmem = kKeyBytes > kPlaces + 4 * kAlone ? kKeyBytes : kPlaces + 4 * kAlone;
+static_assert(4 * kAlone <= kPlaces && kKeyBytes % 16 == 0, "the list lies behind the places");
 
 // Whole numbers in the weights' order: NaN above all, -0 = 0; 0 is below all of them.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -1224,7 +1227,7 @@ cudaError_t launch_cache_evict(EvictArgs a, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlaces + 4 * kAlone);
+    const cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvMaxSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set[dev] = true;
   }

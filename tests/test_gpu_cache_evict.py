@@ -137,6 +137,19 @@ def test_long_row(gq):
     check(run(gq, planes, w, table, lens, 70000, 0, 0), reference(planes, w, table, lens, 70000, 0, 0))
 
 
+@pytest.mark.parametrize("share", [18432, 18433, 20480, 20481])
+@pytest.mark.parametrize("units,ctas", [(160, 1), (80, 2), (40, 4), (32, 8)])
+def test_shares_up_to_what_shared_memory_holds(gq, units, ctas, share):
+    """Capacities around the most that a CTA's part of a row takes in shared memory (18432 and 20480 positions), for each
+    number of CTAs a row gets; most rows are short, for the capacity alone settles how the call is launched."""
+    S = ctas * share
+    lens = [S, S - 5] + [(i * 7) % 300 for i in range(units - 2)]
+    planes, w, table = make("none", units, 1, 64, 0, lens, 8, "ties", S=S)
+    got = run(gq, planes, w, table, lens, 257, 31, 4)
+    assert gq.get_device_status() == 0
+    check(got, reference(planes, w, table, lens, 257, 31, 4))
+
+
 def test_budget_beyond_the_capacity(gq):
     lens = [20, 3]
     planes, w, table = make("bf16", 2, 2, 64, 0, lens, 4, "heavy")
