@@ -721,8 +721,10 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256)
       float top = M;
 #pragma unroll
       for (int k = 0; k < kAt; ++k) top = fmaxf(top, ml[k].x);
-      if (top == -INFINITY) continue;
-      const float scale = ex2_approx(M - top);
+      // No finite maximum yet: the weights are 0 (2^-inf, not of -inf - -inf).  An L is then 0, of a piece that the row sees
+      // nothing of, or NaN, of one whose scores are NaN: those have no part in a maximum, but their L counts.
+      const float use = top == -INFINITY ? 0.f : top;
+      const float scale = ex2_approx(M - use);
       M = top;
       L *= scale;
 #pragma unroll
@@ -730,7 +732,7 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256)
 #pragma unroll
       for (int k = 0; k < kAt; ++k) {
         // a piece of weight 0 holds no key that the row sees, and its partial may be anything
-        const float w = ex2_approx(ml[k].x - top);
+        const float w = ex2_approx(ml[k].x - use);
         const bool any = ml[k].x > -INFINITY || ml[k].x != ml[k].x;
         L = fmaf(ml[k].y, w, L);
 #pragma unroll
@@ -750,17 +752,16 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256)
     float top = M;
 #pragma unroll
     for (int w = 1; w < WPR; ++w) top = fmaxf(top, s_m[warp + w]);
-    if (top > -INFINITY) {
-      L = 0.f;
+    const float use = top == -INFINITY ? 0.f : top;
+    L = 0.f;
 #pragma unroll
-      for (int k = 0; k < V; ++k) acc[k] = 0.f;
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) {
-        const float wk = ex2_approx(s_m[warp + w] - top);     // of a warp without pieces: 0, and so are its sums
-        L = fmaf(s_l[warp + w], wk, L);
+    for (int w = 0; w < WPR; ++w) {
+      const float wk = ex2_approx(s_m[warp + w] - use);     // of a warp without pieces: 0, and so are its sums
+      L = fmaf(s_l[warp + w], wk, L);
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = fmaf(s_acc[warp + w][lane * V + k], wk, acc[k]);
-      }
+      for (int k = 0; k < V; ++k) acc[k] = fmaf(s_acc[warp + w][lane * V + k], wk, acc[k]);
     }
     M = top;
   }

@@ -185,6 +185,60 @@ def test_a_prefix_that_is_not_finite(gq, tiles):
     check((o[4:], lse[4:]), [x[4:] for x in want], 64)
 
 
+def check_with_nan(got, ref, D):
+    """As check, but where the definition gives a log-sum-exp of NaN both outputs are NaN; returns those queries."""
+    lost = torch.isnan(ref[1])
+    o, lse = (x.cpu().double() for x in got)
+    assert torch.equal(torch.isnan(lse), lost) and torch.equal(torch.isnan(o).all(-1), lost)
+    whole = lambda x: x.masked_fill(lost.reshape(lost.shape + (1,) * (x.dim() - 3)), 0.0)  # noqa: E731
+    check((whole(o), whole(lse)), [whole(x) for x in ref], D)
+    return lost
+
+
+NAN_CASES = [
+    # as CASES, and warps a row that join its pieces: 8, 16, 8 (heads of 64), 4, 1
+    (2, 1, 8, 2, 1, 128, 0, [64], [1, 1]),
+    (12, 1, 8, 1, 1, 128, 0, [9000], [1, 2, 17, 40, 1, 1, 1, 3, 16, 1, 700, 1]),
+    (40, 2, 24, 1, 1, 64, 0, [500, 64], [1 + i % 33 for i in range(40)]),
+    (20, 1, 16, 2, 3, 128, 0, [64], [3 + i % 20 for i in range(20)]),
+    (60, 1, 32, 2, 1, 64, 0, [130], [1 + i % 3 for i in range(60)]),
+]
+
+
+@pytest.mark.parametrize("what", ["a row's newest key", "a row's keys", "a prefix", "a query"])
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("case", NAN_CASES, ids=lambda c: f"B{c[0]}H{c[2]}-{c[3]}T{c[4]}D{c[5]}m{max(c[7])}")
+def test_nan_scores_reach_the_outputs(gq, case, tiles, what):
+    """A NaN score makes NaN of the output and of the log-sum-exp of the queries that see it, however the row's keys are cut
+    into pieces (a piece of nothing but NaN scores has no maximum), and of no other."""
+    B, P, Hq, Hkv, Tq, D, page, plens, lens = case
+    Sp = tile_capacity(B, P, Hq, Hkv, Tq, D) if tiles else None
+    if tiles and Sp is None:
+        pytest.skip("at most 16 query rows a key: always in the stream")
+    f, args, (q, pre, own, lens) = make(*case, seed=21, Sp=Sp)
+    for b in (0,) if what == "a prefix" else (0, B // 2):
+        h = (b + 1) % Hkv
+        if what == "a query":
+            q[b, h * (Hq // Hkv), 0] = math.nan
+            args[0][b, h * (Hq // Hkv), 0] = math.nan
+        elif what == "a prefix":
+            pre[0][0][h] = math.nan
+            args[1][0, h] = math.nan
+        else:
+            j = lens[b] - 1 if what == "a row's newest key" else 0
+            own[b][0][h, j:] = math.nan
+            args[4][b, h, j:] = math.nan
+    o, lse = getattr(gq, f)(*args, scale=0.1)
+    assert gq.get_device_status() == 0
+    lost = check_with_nan((o, lse), R.prefix(q, pre, own, lens, 0.1), D)
+    assert bool(lost.any()) and (what == "a prefix" or not bool(lost.all()))
+    # a NaN log-sum-exp is not the -infinity of a query that saw nothing: the keys' weights are NaN too
+    w = torch.zeros(args[4].shape[:3], device="cuda")
+    gq.attn_cache_weights(args[0], args[4], lse, args[6], w, scale=0.1)
+    if what == "a query":
+        assert bool(torch.isnan(w[0, 1 % Hkv, :lens[0] - Tq + 1]).all())
+
+
 def test_no_prefix_at_all(gq):
     f, args, ref = make(3, 1, 4, 2, 1, 64, 0, [0], [9, 200, 1], seed=5)
     empty = torch.empty(1, 2, 0, 64, dtype=torch.bfloat16, device="cuda")
