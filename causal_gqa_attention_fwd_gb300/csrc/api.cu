@@ -103,7 +103,12 @@ bool map_packed(CUtensorMap* m, const void* base, int D, int H, int total, int b
   return gqa::make_tmap(m, base, dtype, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-attn_status launch_status(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+// The runtime keeps an error until it is asked for: what one call has returned is not left for the next launch to find.
+attn_status launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return ATTN_OK;
+  cudaGetLastError();
+  return ATTN_ERR_CUDA;
+}
 
 // Failure-path test (attn_test_inject_timeout): one armed injection, consumed
 // by the next launch of the named kernel (1 forward, 2 backward dK/dV,
@@ -391,7 +396,7 @@ attn_status attn_fwd_rope(const void* q, const void* k, const void* v, void* o, 
   rr.status = status;
   const cudaError_t e =
       gqa::launch_rope_qk_f16(q, k, wq, wk, rr, D, rope_cos_sin, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+  if (e != cudaSuccess) return launch_status(e);
   return fwd_common(wq, wk, v, o, lse, nullptr, B, T, 0, 0, Hq, Hkv, D, causal, scale, stream, false, true);
 }
 
@@ -432,7 +437,7 @@ attn_status attn_varlen_fwd_rope(const void* q, const void* k, const void* v, vo
   rr.status = status;
   const cudaError_t e =
       gqa::launch_rope_qk_f16(q, k, wq, wk, rr, D, rope_cos_sin, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+  if (e != cudaSuccess) return launch_status(e);
   return fwd_common(wq, wk, v, o, lse, cu_seqlens, num_seqs, 0, total_tokens, max_seqlen, Hq, Hkv, D, causal,
                     scale, stream, true, true);
 }
@@ -1183,14 +1188,15 @@ const char* attn_status_string(attn_status s) {
 
 attn_status attn_get_check_line(void* stream, int* out, int clear) {
   if (!out) return ATTN_ERR_NULL;
+  cudaError_t e;
   int* w = check_line_word();
   if (!w) return ATTN_ERR_CUDA;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+  if ((e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream))) != cudaSuccess) return launch_status(e);
   int v = 0;
-  if (cudaMemcpy(&v, w, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;
+  if ((e = cudaMemcpy(&v, w, sizeof(int), cudaMemcpyDeviceToHost)) != cudaSuccess) return launch_status(e);
   if (clear && v != 0) {
     const int zero = 0;
-    if (cudaMemcpy(w, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return ATTN_ERR_CUDA;
+    if ((e = cudaMemcpy(w, &zero, sizeof(int), cudaMemcpyHostToDevice)) != cudaSuccess) return launch_status(e);
   }
   *out = v;
   return ATTN_OK;
@@ -1206,15 +1212,16 @@ int attn_is_debug_build(void) {
 
 attn_status attn_get_device_status(void* stream, int* out, int clear) {
   if (!out) return ATTN_ERR_NULL;
+  cudaError_t e;
   int* w = status_word();
   if (!w) return ATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaStreamSynchronize(s) != cudaSuccess) return ATTN_ERR_CUDA;
+  if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return launch_status(e);
   int v = 0;
-  if (cudaMemcpy(&v, w, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;
+  if ((e = cudaMemcpy(&v, w, sizeof(int), cudaMemcpyDeviceToHost)) != cudaSuccess) return launch_status(e);
   if (clear && v != 0) {
     const int zero = 0;
-    if (cudaMemcpy(w, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return ATTN_ERR_CUDA;
+    if ((e = cudaMemcpy(w, &zero, sizeof(int), cudaMemcpyHostToDevice)) != cudaSuccess) return launch_status(e);
   }
   *out = v;
   return ATTN_OK;

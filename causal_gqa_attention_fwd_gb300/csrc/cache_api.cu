@@ -12,7 +12,12 @@ namespace {
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 cudaStream_t st_of(void* stream) { return static_cast<cudaStream_t>(stream); }
-attn_status status_of(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+// (as launch_status in api.cu: an error that was returned is not left for the next launch to find)
+attn_status status_of(cudaError_t e) {
+  if (e == cudaSuccess) return ATTN_OK;
+  cudaGetLastError();
+  return ATTN_ERR_CUDA;
+}
 
 // A token view: strides not negative and multiples of 8 elements, so that every
 // row of a 16-byte aligned tensor is 16-byte aligned.

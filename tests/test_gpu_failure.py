@@ -73,3 +73,54 @@ def test_production_kernel_wait_expires_and_next_call_is_clean(kernel, name):
     assert g.get_device_status() == 0
     for a, b in zip(again, ref):
         assert torch.equal(a, b), name
+
+
+REFUSED = """
+import sys
+import torch
+import causal_gqa_attention_fwd_gb300 as g
+q = torch.randn(1, 2, 130, 64, device="cuda").to(torch.bfloat16)
+w, c = torch.rand(1, 2, 130, device="cuda"), torch.randn(1, 2, 130, 64, device="cuda").to(torch.bfloat16)
+n = torch.full((1,), 130, dtype=torch.int32, device="cuda")
+x = dict(o=torch.empty_like(q), lse=torch.empty(1, 2, 130, device="cuda"))
+kept, out = torch.empty(1, 2, 64, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+calls = {"attn_fwd": lambda: g.attn_fwd(q, c, c, **x),
+         "attn_cache_evict": lambda: g.attn_cache_evict(w, (c,), n, 64, kept=kept, lens_out=out)}
+for f in calls.values():
+    f()
+assert g.get_device_status() == 0
+for name, f in calls.items():
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        graph.capture_begin()
+        try:
+            torch.cuda.synchronize()            # not allowed while capturing: the capture is void from here on
+            sys.exit("the capture stands")
+        except RuntimeError:
+            pass
+        try:
+            f()
+            sys.exit(name + " was not refused")
+        except g.AttnError as e:
+            assert "CUDA" in str(e), e
+        try:
+            graph.capture_end()
+        except RuntimeError:
+            pass
+    torch.cuda.synchronize()
+    f()                                         # raises if it is told of the launch before
+    torch.cuda.synchronize()
+    assert g.get_device_status() == 0
+print("ok")
+"""
+
+
+def test_a_refused_launch_is_not_the_next_calls_error():
+    """A launch that the runtime refuses (here: into a capture that is void) raises in its own call alone.  In a process of
+    its own, for what a void capture leaves in the allocator."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", REFUSED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr[-2000:]
