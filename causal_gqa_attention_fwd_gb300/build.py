@@ -27,7 +27,7 @@ EXT_SOURCE = os.path.join(CSRC, "cache_binding.cpp")
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_split.cu", "attn_decode.cu",
            "cache_api.cu", "cache_ops.cu", "attn_decode_q4.cu", "attn_prefix.cu", "attn_own.cu", "cache_evict.cu"]
 HEADERS = ["sm103.cuh", "kernels.h", "tmap.h", "rope.h", "bwd_common.cuh", "api_util.h", "cache_ops.h", "fp4.cuh",
-           "stream.cuh", "own_keys.cuh"]
+           "stream.cuh", "own_keys.cuh", "share_out.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

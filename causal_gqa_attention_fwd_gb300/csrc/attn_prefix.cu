@@ -33,6 +33,7 @@
 //   own ones 41 us (25 at the copy rate), 256 rows over 32768 keys and ~70000
 //   own ones 130 us (74).
 #include "own_keys.cuh"
+#include "share_out.h"
 
 namespace gqa {
 
@@ -171,20 +172,9 @@ __device__ Walk walk_begin(const PrefixArgs& a, int cta, int ctas, int total) {
 
 }  // namespace
 
-// How many of the grid's G CTAs take the rows' own keys, the others the prefixes: so that both end at the same time, by
-// what they were measured to take (ns).
-//   Two tiles of query rows a CTA: the MMAs bound a prefix, kPair a block of 128 keys.  Beside it an SM streams own keys
-//   at kOwnTile a tile of 8 KB, all SMs together at kOwnTileAll.
-//   One tile of rows, held by both: the memory bounds both parts, and an SM gets its share of it: kByte a byte.
-// 64 rows over 8192 keys and 32768 own ones, CTAs of own keys 64 / 72 / 80 / 88 / 96: 43.4, 42.5, 42.0, 41.6, 44.5 us;
-// 256 rows over 32768, 32 / 34 / 36 / 38: 132.3, 130.0, 129.9, 132.4.
-constexpr float kOwnStart = 6000.f, kOwnTile = 94.f, kOwnTileAll = 1.25f;
-constexpr float kOwnUnit = 2000.f;    // a unit, of one of a CTA's warps: its queries and its output
-constexpr float kPreStart = 10000.f, kPair = 1350.f, kByte = 1.f / 41.f;
-constexpr float kPiece = 5000.f;      // a second piece: its queries, the first one's drain and partial
-
+// What the lengths make of the grid's G CTAs (share_out.h).
 struct Parts {
-  int own;         // CTAs of the rows' own keys
+  int own;         // CTAs of the rows' own keys, the others take the prefixes
   int blocks;      // key blocks of all prefixes' groups
 };
 
@@ -216,21 +206,10 @@ __device__ Parts share_out(const PrefixArgs& p, const OwnArgs& a, int G, int* s_
   blocks *= runs;
   if (tiles == 0) return {0, blocks};
   if (blocks == 0) return {G, 0};
-  const int last = p.Rp - (p.nrt - 1) * kPrefixRows;     // rows of the last unit
-  const bool split = p.nrt == 1 && last <= kBM;
-  const float tile = split ? 8192 * kByte : kOwnTile, block = split ? 4 * kBN * a.D * kByte : kPair;
-  const float start = split ? kOwnStart : kPreStart;
-  const float own = (tiles * tile + rows * (kOwnUnit / WARPS)) * (a.Hkv * a.nrb), all = tiles * kOwnTileAll * (a.Hkv * a.nrb);
+  // (a single unit of at most a tile's rows: `split`)
+  const ShareWork work{G, p.width, runs, p.P, blocks, p.nrt == 1 && p.Rp <= kBM, a.Hkv * a.nrb, tiles, rows, WARPS, a.D};
   unsigned best = ~0u;
-  if (tid >= 1 && tid <= G - p.width) {
-    const int teams = (G - tid) / p.width;
-    const float t_own = kOwnStart + fmaxf(own / tid, all);
-    // one prefix: no CTA crosses from a unit to the next if the teams are a multiple of its groups, or the reverse
-    const bool whole = p.P == 1 && (teams % runs == 0 || runs % teams == 0);
-    const int most = (blocks + teams - 1) / teams;
-    const float t_pre = start + most * block + (whole ? 0.f : kPiece * (1 + most * runs * p.P / blocks));
-    best = (unsigned)fminf(fmaxf(t_own, t_pre), 1.6e7f) << 8 | tid;
-  }
+  if (tid >= 1 && tid <= G - p.width) best = share_rank(share_time(work, tid), tid);
   best = __reduce_min_sync(~0u, best);
   __syncthreads();
   if (lane == 0) s_red[warp] = (int)best;
