@@ -614,6 +614,7 @@ __global__ void __launch_bounds__(384, 1)
               *reinterpret_cast<uint4*>(a.ws_o + (wr0 + (long)rr * a.slots) * D + q * 32 + (lane & 7) * 4) = v;
           }
         }
+        __syncwarp();        // all lanes have read before the next piece's queries go into these rows
         tc_fence_before();   // O is read before the next piece's P V (after its q_full) writes it
       }
       if (mine) a.ws_ml[wr] = make_float2(m_run, l_run);
