@@ -197,8 +197,9 @@ attn_status cache_weights(const void* q, const void* k, const void* ksf, float k
       !isfinite(k_scale) || (Tq > 0 && (long)B * Hq > 0x3fffffffL / Tq) || (long)B * max_pages > 0x7fffffffL ||
       (long)B * Hkv > 0x7fffffffL / ((S + 31) / 32 + 1))
     return ATTN_ERR_SHAPE;
+  if (B == 0) return ATTN_OK;      // (a block table without rows may be NULL)
   if (!block_table && num_pages != B) return ATTN_ERR_SHAPE;
-  if (B == 0 || Tq == 0 || S == 0) return ATTN_OK;
+  if (Tq == 0 || S == 0) return ATTN_OK;
   if (num_pages < 1) return ATTN_ERR_SHAPE;
   if (!q || !k || !lse || !cache_lens || !weights || (fmt == gqa::kCacheQ4 && !ksf)) return ATTN_ERR_NULL;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(ksf, 16) || !aligned(lse, 16) || !aligned(weights, 16) ||
@@ -270,7 +271,7 @@ attn_status attn_cache_evict(float* weights, void* const* planes, const int* row
   if (S > 0x7fffffffL - 2048 || (long)page_size * num_pages > 0x7fffffffL || (long)B * Hkv > 0x7fffffffL ||
       (long)B * max_pages > 0x7fffffffL || budget > 0x7fffffff - 4096)
     return ATTN_ERR_SHAPE;
-  if (!block_table && num_pages != B) return ATTN_ERR_SHAPE;
+  if (B > 0 && !block_table && num_pages != B) return ATTN_ERR_SHAPE;      // (one without rows may be NULL)
   if (num_planes > 0 && (!planes || !row_bytes)) return ATTN_ERR_NULL;
   for (int i = 0; i < num_planes; ++i)
     if (row_bytes[i] < 4 || row_bytes[i] % 4 || row_bytes[i] > 4096) return ATTN_ERR_SHAPE;

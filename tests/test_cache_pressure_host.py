@@ -173,3 +173,16 @@ def test_evict_reference():
     assert R.evict(w, 9, 4, 1, 1) == [0, 2, 4, 8]      # NaN above all, then the first of the threes
     assert R.evict(w, 9, 9, 0, 0) == list(range(9)) and R.evict(w[:3], 3, 5, 5, 0) == [0, 1, 2]
     assert R.evict(w, 9, 3, 3, 0) == [6, 7, 8] and R.evict(w, 9, 2, 0, 2) == [0, 1]
+
+
+def test_an_empty_batch_over_pages(lib):
+    """A block table without rows is NULL for most allocators; that is no contiguous cache of another batch."""
+    one = (ctypes.c_void_p * 1)(A << 12)
+    wide = (ctypes.c_int * 1)(128)
+    sizes = (0, 4, 2, 1, 16, 9, 4, 64, 0.1, None)
+    for table in (NULL, A):
+        assert lib.attn_cache_weights(A, A, A, table, NULL, A, *sizes) == 0
+        assert lib.attn_cache_weights_fp8(A, A, 1.0, A, table, NULL, A, *sizes) == 0
+        assert lib.attn_cache_weights_q4(A, A, A, 1.0, A, table, NULL, A, *sizes) == 0
+        assert lib.attn_cache_evict(A, one, wide, 1, table, NULL, 8, 2, 1, NULL, NULL, 0, 2, 16, 9, 4, None) == 0
+        assert lib.attn_cache_evict(A, one, wide, 1, table, NULL, 8, 8, 1, NULL, NULL, 0, 2, 16, 9, 4, None) == 2

@@ -141,3 +141,27 @@ def test_two_streams_at_once(gq):
         torch.cuda.synchronize()
         for x, y in zip(got, want):
             assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_a_step_without_requests(gq, page):
+    """An empty batch, over a pool of pages or contiguous: every call returns its empty outputs and touches nothing."""
+    Hkv, D = 2, 64
+    n, per = (9, page) if page else (0, 32)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    q, lse, lens = torch.zeros(0, 4, 1, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(0, 4, 1, device="cuda"), i32(0)
+    bt = i32(0, 4) if page else None
+    k, w = torch.randn(n, Hkv, per, D, device="cuda").bfloat16(), torch.rand(n, Hkv, per, device="cuda")
+    k8, k4, sf = (torch.zeros(n, Hkv, per, x, dtype=torch.uint8, device="cuda") for x in (D, D // 2, D // 16))
+    if page:
+        o, out = gq.attn_decode_paged_prefix_fwd(q, k, k, i32(1, 2), i32(1), bt, lens)
+    else:
+        o, out = gq.attn_decode_prefix_fwd(q, *[torch.zeros(1, Hkv, 8, D, dtype=torch.bfloat16, device="cuda")] * 2, i32(1), k, k, lens)
+    assert o.shape == q.shape and out.shape == lse.shape
+    before = k.clone(), w.clone()
+    assert gq.attn_cache_weights(q, k, lse, lens, w, block_table=bt) is w
+    assert gq.attn_cache_weights_fp8(q, k8, 0.1, lse, lens, w, block_table=bt) is w
+    assert gq.attn_cache_weights_q4(q, k4, sf, 0.1, lse, lens, w, block_table=bt) is w
+    kept, lens_out = gq.attn_cache_evict(w, (k,), lens, 8, recent=2, block_table=bt)
+    assert kept.shape == (0, Hkv, 8) and lens_out.shape == (0,)
+    assert torch.equal(before[0], k) and torch.equal(before[1], w) and gq.get_device_status() == 0
