@@ -64,7 +64,8 @@ def attn_cache_plan(cache_lens, new_lens, block_table, page_size: int, free_page
     Each request gets the pages it lacks from free_pages, from index cursor (int32 [1], None: 0) on; they are written
     into block_table [B, max_pages] in place.  total_tokens: length of slots and positions (default: that of slots), which
     are packed in request order: request b's from entry cu_seqlens[b] on, none without new tokens; the entries past the last
-    new token are -1 and 0.  All tensors int32 on the device
+    new token are -1 and 0.  Positions count the row's keys: behind a shared prefix, and in a row that attn_cache_evict has
+    cut, a token's rotary position is another, which the caller keeps.  All tensors int32 on the device
     -> (slots [total_tokens], positions [total_tokens], cu_seqlens [B+1], lens_out [B], cursor_out [1])."""
     return _run(stream, _ext().plan, cache_lens, new_lens, block_table, page_size, free_pages, cursor, total_tokens, slots,
                 positions, cu_seqlens, lens_out, cursor_out)
@@ -207,6 +208,7 @@ def attn_cache_evict(weights, caches, cache_lens, budget: int, recent: int = 0, 
     position).  The kept rows of weights [pages,Hkv,page_size] and of every plane in caches ([pages,Hkv,page_size,width],
     any type: (k, v), (k8, v8), (k4, k4_sf, v4, v4_sf)) move to positions 0..budget-1 in their order; what lies behind
     stays as it was, and a row of at most budget keys is not touched.  cache_lens int32 [B]; block_table None: contiguous
-    caches.  Rows must not share pages -> (kept int32 [B,Hkv,budget], the positions kept, -1 behind a shorter row's last;
+    caches.  Rows must not share pages.  Rotated keys keep their rotation: a later token goes on at the position it has in the
+    text, not at the row's new length -> (kept int32 [B,Hkv,budget], the positions kept, -1 behind a shorter row's last;
     lens_out int32 [B])"""
     return _run(stream, _ext().evict, weights, tuple(caches), cache_lens, budget, recent, first, block_table, kept, lens_out)

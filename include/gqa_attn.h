@@ -354,6 +354,11 @@ GQA_ATTN_API attn_status attn_decode_paged_fp8_fwd(const void* q, const void* k8
  * positions.  Where k and v keep a row for every request, idle ones too (a
  * captured step of one token each), row b's slot is entry cu_seqlens[b] if
  * cu_seqlens[b + 1] > cu_seqlens[b], else -1; its position likewise.
+ * Positions count the row's keys: cache_lens[b] and on.  They are those of the
+ * text only where the row holds its whole text.  Behind a shared prefix of m keys
+ * they are m further on, and in a row that was cut (attn_cache_evict) further by
+ * the keys it lost: there the program keeps each row's next position and takes
+ * the slots alone from here.
  * A request with a negative length, or whose new length exceeds
  * max_pages * page_size, is refused: it gets no pages, its tokens (none if
  * new_lens[b] < 0) get slot -1 and its length stays (ATTN_ERR_SEQLENS).  So
@@ -594,9 +599,10 @@ GQA_ATTN_API attn_status attn_cache_weights_q4(const void* q, const void* k4, co
  * rows of `weights` and of the num_planes <= 8 planes move to positions
  * 0 .. budget-1 in their order, bit for bit; the entries behind stay as they
  * were.  A row of at most `budget` keys is not touched.  (Keys that were
- * rotated keep their rotation; a later key's position is its own, not the row's
- * new length.  A paged row needs only its first ceil(budget / page_size) pages
- * afterwards.)
+ * rotated keep their rotation, so a later token's rotary position is the one it
+ * has in the text, not the row's new length, which is what attn_cache_plan gives:
+ * the program keeps it.  A paged row needs only its first
+ * ceil(budget / page_size) pages afterwards.)
  *   planes     HOST array of DEVICE pointers, plane i [num_pages, Hkv, page_size]
  *              rows of row_bytes[i] (HOST; a multiple of 4, at most 4096)
  *   weights    float32 [num_pages, Hkv, page_size]
