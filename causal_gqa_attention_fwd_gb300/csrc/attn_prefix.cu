@@ -795,7 +795,7 @@ cudaError_t launch_attn_prefix(const CUtensorMap& k, const CUtensorMap& v, const
 template <int D>
 static cudaError_t launch_merge_d(const PrefixArgs& p, const OwnArgs& a, __nv_bfloat16* o, float* lse, cudaStream_t stream) {
   const long rows = (long)a.B * a.Hkv * p.R;
-  // about as many pieces as a row has, if all its keys are there
+  // about as many pieces as a row has, if all its keys are there (a host knows the capacities alone)
   constexpr int KT = OwnCfg<D, 1>::KT;
   auto tiles = [](int keys) { return (keys + KT - 1) / KT + kUnitCost; };
   const long total = (long)a.B * a.Hkv * a.nrb * tiles(a.S) + (long)a.P * a.Hkv * a.nrbp * tiles(a.Sp);
@@ -812,7 +812,10 @@ static cudaError_t launch_merge_d(const PrefixArgs& p, const OwnArgs& a, __nv_bf
   // 8.0 / 8.9 / 9.0 / 18.6, 128 rows 9.6 / 10.4 / 10.4 / 21.3, 112 rows of 40 (heads of 64) 10.1 / 9.3 / 9.2 / 13.6,
   // 256 rows 13.8 / 11.9 / 11.9 / 23.0, 512 rows 21.0 / 15.9 / 15.9 / 19.3, 1024 rows of 20 31 / 23 / 17.1 / 18.8, 896 rows
   // of 40 (heads of 64) 22.9 / 17.6 / 20.7 / 19.0 and 1024 of 23 - / 19.4 / 15.7 / -, 2048 rows 49 / 31 / 18.9
-  // / 18.1, 8192 rows of 7 245 / 195 / 142 / 132.
+  // / 18.1, 8192 rows of 7 245 / 195 / 142 / 132.  Heads of 64, 8 warps / 4 for up to 1024 rows where n is above 40: 640
+  // rows (32 / 8 heads) over 4096 and 8192 keys 16.6 / 18.5, 17.7 / 19.6; 768 (8 / 2) over 8192 20.4 / 26.4; 896 (14 / 2)
+  // 19.8 / 22.4; 1024 (8 / 1) 20.7 / 22.2, (32 / 8) 21.7 / 21.3; where the table is far wider than the prefix (2048 keys of
+  // 65536) n tells nothing: 15.5 / 17.1, 18.0 / 20.2, 18.1 / 18.2, 19.0 / 18.2, 17.9 / 15.8.
   if (rows <= 128 && n > 64)
     return launch_programmatic(prefix_merge_kernel<D, 16, 8>, blocks(1), dim3(512), 0, stream, p, a, o, lse);
   if (rows <= 512 || (D == 64 && rows <= 1024 && n > 40))

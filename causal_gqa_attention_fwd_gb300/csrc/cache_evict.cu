@@ -16,8 +16,8 @@
 //   A long window of queries is GEMM-shaped: tcgen05 (cache_weights_window).
 //   Many keys: 32 of them a tile, all in one stream that the grid's warps share
 //   (cache_weights_kernel); 8 long rows of 8 heads of 128, 61 us at the copy
-//   rate: bf16 keys 67 us; 4-bit ones (18) 32, bound by the instructions that
-//   widen them.
+//   rate: bf16 keys 67 us; 4-bit ones (18) 32: the chain that widens a tile's keys
+//   and multiplies them (issue slots 63% active, no unit full).
 //
 // evict  a cluster of CTAs a (row, K/V head): each keeps a run of the weights in
 //   shared memory (short rows: each all of them, and no exchange); the budget-th
@@ -212,7 +212,7 @@ __device__ __forceinline__ RowConstants row_constants(const WeightsArgs& a, long
 }
 
 // ------------------------------------------------ at most 8 NT query rows a key: one stream of tiles over all warps
-// Warps: what registers leave; 4-bit keys, whose instructions bound it, with more of them (20 and 16; 12, 16, 24: slower).
+// Warps: what registers leave; 4-bit keys, with a longer chain a tile, more of them (20 and 16; 12, 16, 24: slower).
 template <int D, CacheFmt F, int NT>
 struct NarrowCfg {
   static constexpr int kWarps = F == kCacheQ4 ? (NT == 1 ? 20 : 16) : 12;
@@ -528,8 +528,8 @@ __global__ void __launch_bounds__(32 * kWWarps) cache_weights_wide_kernel(const 
 // ------------------------------------------------ a long window: S^T = K Q^T on tcgen05
 // A CTA a chunk of 256 keys, in shared memory as two tiles of 128 (M); the query rows (N) go by 64, and while a block's
 // weights are formed the next one's products run.  A thread has one key's scores and adds its weights up by itself.
-// Bound: instructions beside the exponentials; for 8- and 4-bit keys the query rows' conversion to f16, which every CTA
-// does for itself.  512 rows over 2^20 keys: bf16 of 128 221 us, of 64 174 (3.1e12 exponentials a second), E4M3 of 128 340.
+// Bound: latency of a block's chain (128 rows: issue slots 45% active, XU and tensor pipe 26% each); for 8- and 4-bit keys
+// also the query rows' conversion to f16, which every CTA does for itself.  512 rows over 2^20 keys: bf16 of 128 221 us, of 64 174 (3.1e12 exponentials a second), E4M3 of 128 340.
 template <int D>
 struct WindowCfg {
   static constexpr int kRows = 64, kKeys = kWKeys;
@@ -799,7 +799,8 @@ cudaError_t launch_weights_df(WeightsArgs a, int sms, cudaStream_t stream) {
   // The stream is for many keys: where a CTA a chunk of the capacity are resident together (two an SM, heads of 64 three),
   // they have no shares to work out.  us, CTAs / stream, 8 rows: bf16 keys of 128, 32768: 3.4 / 4.1, 65536: 4.3 / 5.4,
   // 98304: 7.0 / 6.5; keys of 64, 98304: 4.1 / 5.0, 131072: 5.9 / 5.6; E4M3 of 128, 65536: 4.1 / 5.5, 131072: 6.8 / 6.7;
-  // 4-bit of 128, 65536: 3.8 / 6.0, 131072: 6.3 / 7.3, 262144: 11.2 / 9.4.
+  // 4-bit of 128, 65536: 3.8 / 6.0, 131072: 6.3 / 7.3, 262144: 11.2 / 9.4.  (Lengths equal to the capacity, which is what
+  // a host knows: 8 rows of 2048 keys, 2 heads of 64, tables of 2048 / 8192 / 131072 positions: 3.0 / 3.5 / 3.6.)
   const long ctas = (long)a.B * a.Hkv * ((a.S + (long)kWKeys - 1) / kWKeys);
   const bool at_once = ctas <= (D == 128 ? 2L : 3L) * sms;
   if (a.R <= 16 && !at_once)

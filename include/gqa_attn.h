@@ -530,7 +530,9 @@ GQA_ATTN_API attn_status attn_decode_paged_q4_fwd(const void* q, const void* k4_
  * position following the prefix's.  P is rounded to bf16 for the P V product;
  * everything else is f32.  Rows of a cache that no query of a (row, K/V head)
  * sees may hold anything; a V that is infinite or NaN at an own position that
- * one of the Tq queries sees may make NaN of the others too.  How a row's keys are cut into pieces follows from
+ * one of the Tq queries sees may make NaN of the others too.  A NaN score makes
+ * NaN of O and LSE of the query that has it (LSE is -infinity only where a query
+ * sees nothing, or scores of -infinity alone).  How a row's keys are cut into pieces follows from
  * the sizes and the lengths: the same call gives the same bits.
  * workspace: attn_decode_prefix_workspace_size() bytes, 256-byte aligned, no
  * initialisation; calls in flight at once need one each. */
@@ -563,7 +565,8 @@ GQA_ATTN_API attn_status attn_decode_paged_prefix_fwd(const void* q, const void*
  * where the entries of the row's last Tq positions, the step's new keys, are set
  * to the sum instead (whatever their slots held before), with q bf16
  * [B, Hq, Tq, D] and the lse float32 [B, Hq, Tq] that the step's
- * attention returned (-infinity, a query that saw no key: adds nothing).  Behind
+ * attention returned (-infinity, a query that saw no key: adds nothing; NaN:
+ * makes NaN of what it sees).  Behind
  * a shared prefix that lse counts the prefix's keys too, and so do the weights.
  *   weights  float32 [num_pages, Hkv, page_size], an entry beside each key
  *            (slots as above); entries of positions past a row's length stay
