@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(384, 1)
           npc = psz >= kBN ? 1 : kBN / psz;
           const int idx = k0 / psz + lane;
           bool bad = false;
-          if (lane < npc && idx < (w.it.len + psz - 1) / psz) {
+          if (lane < npc && idx <= (w.it.len - 1) / psz) {
             const int e = a.table[(long)w.it.p * a.max_pages + idx];
             if (e >= 0 && e < a.num_pages) pg = e;
             else bad = true;

@@ -160,7 +160,7 @@ __device__ __forceinline__ void own_keys(uint8_t* smem, OwnShared<D, NT, THREADS
     uint8_t* dst = ring_p + st * C::kStage;
     uint64_t* bar = &full[st];
     if constexpr (PAGED) {
-      const int psz = a.page_size, used = (ld.len + psz - 1) / psz;
+      const int psz = a.page_size, used = (ld.len - 1) / psz + 1;      // (len + psz may pass 32 bits)
       const int box = min(KT, psz), n = KT / box;
       if (page0 < 0 || (k0 + KT - 1) / psz >= page0 + 32) {
         page0 = k0 / psz;
