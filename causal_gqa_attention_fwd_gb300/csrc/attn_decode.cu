@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(FP8 ? kThreads8 : kThreads, 1)
         const int psz = a.page_size;
         npc = psz >= kCK ? 1 : kCK / psz;
         const int idx = k0 / psz + lane;
-        const int used = (it.len + psz - 1) / psz;
+        const int used = (it.len - 1) / psz + 1;       // (len + psz may pass 32 bits)
         int pg = -1;
         bool bad = false;
         if (lane < npc && idx < used) {
