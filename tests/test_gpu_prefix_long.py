@@ -19,8 +19,10 @@ def gq():
 @pytest.mark.parametrize("Hq,what", [(1, "own"), (1, "prefix"), (32, "prefix")], ids=["own", "stream", "tiles"])
 def test_rows_that_end_within_a_page_of_2_31_positions(gq, Hq, what):
     """A row of 130055 pages of 16512 positions, less than a page from 2^31, and all of them the same page of the pool: its
-    attention is that over the one page, with a log-sum-exp larger by ln 130055.  Sums go on for up to 2^17 additions a
-    thread (products: the tensor cores' steps), off by 2^-23 of the sum each: 2^-6, and 2^-8 for the weights' rounding."""
+    attention is that over the one page, with a log-sum-exp larger by ln 130055.  In the stream a warp of 152 * 12 takes 2^31
+    / 1824 keys, in tensor-core steps and additions of 16 keys: 73585 < 2^17 of them, off by 2^-23 of the sum each, 2^-6.  With
+    large tiles a tile of 302 takes 2^31 / 302: 55556 < 2^17 additions of 128 keys a thread, but 444443 < 2^19 tensor-core
+    steps, 2^-4, for O.  The weights' rounding adds 2^-8."""
     page, times = 16512, 130055
     n = page * times
     assert n < 2 ** 31 - 512 < n + page
@@ -41,6 +43,6 @@ def test_rows_that_end_within_a_page_of_2_31_positions(gq, Hq, what):
     lse = torch.logsumexp(s, -1) + math.log(times)
     o = torch.softmax(s, -1) @ V[0].double()
     size = torch.softmax(s, -1) @ V[0].double().abs()
-    tol = 2.0 ** -6 + 2.0 ** -8 + more * 2.0 ** -20
-    assert float((got[1][0, :, 0].cpu().double() - lse).abs().max()) <= 2 * tol
-    assert bool(((got[0][0, :, 0].cpu().double() - o).abs() <= (2 * tol + 2.0 ** -8) * size).all())
+    assert float((got[1][0, :, 0].cpu().double() - lse).abs().max()) <= 2 * 2.0 ** -6 + more * 2.0 ** -20
+    tol = (2.0 ** -4 if Hq == 32 else 2.0 ** -6) + 2 * 2.0 ** -6 + 2 * 2.0 ** -8 + more * 2.0 ** -20
+    assert bool(((got[0][0, :, 0].cpu().double() - o).abs() <= tol * size).all())
